@@ -46,6 +46,12 @@ def _declare(lib):
     lib.attn_bwd_ex.argtypes = ([c_void_p] * 9 + [c_int] * 7 + [c_float, c_int, c_int, c_int, c_void_p, c_int,
                                                                   c_void_p, c_void_p, c_int, c_void_p, c_size_t,
                                                                   c_void_p])
+    lib.attn_fwd_sinks.restype = c_int
+    lib.attn_fwd_sinks.argtypes = ([c_void_p] * 5 + [c_int] * 7 + [c_float, c_int, c_int, c_int, c_int, c_void_p,
+                                                                     c_void_p, c_void_p])
+    lib.attn_bwd_sinks.restype = c_int
+    lib.attn_bwd_sinks.argtypes = ([c_void_p] * 9 + [c_int] * 7 + [c_float, c_int, c_int, c_int, c_int, c_void_p,
+                                                                     c_void_p, c_int, c_void_p, c_size_t, c_void_p])
     lib.attn_fwd_varlen.restype = c_int
     lib.attn_fwd_varlen.argtypes = [c_void_p] * 5 + [c_int] * 7 + [c_float, c_int, c_void_p, c_void_p, c_void_p]
     lib.attn_bwd_workspace_size.restype = c_size_t
@@ -178,6 +184,22 @@ def attn_bwd_ex(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, sc
                               _ptr(cu_seqlens_k), int(deterministic), _ptr(workspace), ws_bytes, _stream(stream))
 
 
+def attn_fwd_sinks(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left, window_right, sinks,
+                   cu_seqlens_q=None, cu_seqlens_k=None, stream=None) -> int:
+    return load().attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, Lq, Lk, d, d_v, scale,
+                                 int(causal), int(window_left), int(window_right), int(sinks), _ptr(cu_seqlens_q),
+                                 _ptr(cu_seqlens_k), _stream(stream))
+
+
+def attn_bwd_sinks(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left,
+                   window_right, sinks, cu_seqlens_q, cu_seqlens_k, deterministic, workspace, ws_bytes,
+                   stream=None) -> int:
+    return load().attn_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+                                 _ptr(dv), B, H, Hkv, Lq, Lk, d, d_v, scale, int(causal), int(window_left),
+                                 int(window_right), int(sinks), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                 int(deterministic), _ptr(workspace), ws_bytes, _stream(stream))
+
+
 def attn_bwd_workspace_size(B, H, Lq, Lk, d, causal, deterministic) -> int:
     return load().attn_bwd_workspace_size(B, H, Lq, Lk, d, int(causal), int(deterministic))
 
@@ -260,6 +282,11 @@ def _mask_heads(block_mask, H, Lq, Lk):
     return 1 if len(shape) == 2 else shape[0]
 
 
+def _no_block_mask(block_mask):
+    if block_mask is not None:
+        raise ValueError("sinks are not combined with a block mask")
+
+
 def _check_tensors(*ts):
     for t in ts:
         if t is None:
@@ -269,12 +296,14 @@ def _check_tensors(*ts):
 
 
 def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, out=None, lse=None,
-            stream=None, cu_seqlens_k=None, window=(-1, -1), block_mask=None):
+            stream=None, cu_seqlens_k=None, window=(-1, -1), block_mask=None, sinks=0):
     """O, LSE for bf16 q, k, v ([B, L, H, d], or [T, H, d] with int32 cu_seqlens).
     v (and O) may have a head dim of their own (d = 192 with 128); k and v may
     have fewer heads than q (grouped heads: query head h reads h // (H // Hkv)).
     cu_seqlens_k: key offsets of a varlen batch whose key lengths differ.
     window: (left, right) bounds of a local window, -1 for an open side.
+    sinks: the first keys of each sequence that stay visible left of the window
+    (not with a block mask).
     block_mask: uint8 CUDA tensor [Hm, ceil(Lq/128), ceil(Lk/128)] (Hm 1 or H;
     2-D means Hm = 1), dense problems only; zero drops a 128 x 128 block."""
     _check_tensors(q, k, v, cu_seqlens, cu_seqlens_k)
@@ -285,7 +314,11 @@ def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, 
         out = torch.empty(q.shape[:-1] + (dv,), dtype=q.dtype, device=q.device)
     if lse is None:
         lse = torch.empty((B, H, Lq) if cu_seqlens is None else (H, Lq), dtype=torch.float32, device=q.device)
-    if tuple(window) != (-1, -1) or block_mask is not None:
+    if sinks:
+        _no_block_mask(block_mask)
+        _check(attn_fwd_sinks(q, k, v, out, lse, B, H, Hkv, Lq, Lk, d, dv, scale, causal, window[0], window[1], sinks,
+                              cu_seqlens, cu_seqlens_k, stream))
+    elif tuple(window) != (-1, -1) or block_mask is not None:
         mh = _mask_heads(block_mask, H, Lq, Lk)
         _check_tensors(block_mask)
         _check(attn_fwd_ex(q, k, v, out, lse, B, H, Hkv, Lq, Lk, d, dv, scale, causal, window[0], window[1],
@@ -304,10 +337,10 @@ def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, 
 
 def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu_seqlens=None,
              deterministic: bool = False, workspace=None, dq=None, dk=None, dv=None, stream=None,
-             cu_seqlens_k=None, window=(-1, -1), block_mask=None):
+             cu_seqlens_k=None, window=(-1, -1), block_mask=None, sinks=0):
     """dQ, dK, dV (bf16) for the loss sum(O * dO); k and v may have fewer heads
     than q (grouped heads), dK and dV then have theirs; v (dO, dV) may have a head
-    dim of its own (d = 192 with 128). cu_seqlens_k, window and block_mask as in forward()."""
+    dim of its own (d = 192 with 128). cu_seqlens_k, window, block_mask and sinks as in forward()."""
     _check_tensors(q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_k)
     B, H, Lq, Lk, d, Hkv = _dims(q, k, cu_seqlens)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
@@ -319,7 +352,11 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     ws_bytes = workspace.numel() * workspace.element_size()
-    if d_v != d or tuple(window) != (-1, -1) or block_mask is not None:
+    if sinks:
+        _no_block_mask(block_mask)
+        _check(attn_bwd_sinks(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window[0],
+                              window[1], sinks, cu_seqlens, cu_seqlens_k, deterministic, workspace, ws_bytes, stream))
+    elif d_v != d or tuple(window) != (-1, -1) or block_mask is not None:
         mh = _mask_heads(block_mask, H, Lq, Lk)
         _check_tensors(block_mask)
         _check(attn_bwd_ex(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window[0],

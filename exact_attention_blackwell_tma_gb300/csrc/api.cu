@@ -171,15 +171,17 @@ int check_block_mask(const unsigned char* mask, int heads, int H, const int* cu)
     return ATTN_OK;
 }
 
-int check_window(int wl, int wr) {
+int check_window(int wl, int wr, int sinks) {
     if (wl < -1 || wr < -1) return fail(ATTN_ERR_ARG, "window bounds must be >= 0, or -1 for none (%d, %d)", wl, wr);
+    if (sinks < 0) return fail(ATTN_ERR_ARG, "sinks must be >= 0 (%d)", sinks);
     return ATTN_OK;
 }
 
 // causal != 0 sets the right bound to 0 (whatever window_right says)
 void set_mask(Geometry* g, int causal, int wl, int wr) {
-    g->win_left = wl;
-    g->win_right = causal ? 0 : wr;
+    // (bounds past the sequence change nothing; clamped so the index arithmetic cannot overflow)
+    g->win_left = wl < g->Lk ? wl : g->Lk;
+    g->win_right = causal ? 0 : (wr < g->Lq ? wr : g->Lq);
     g->causal = g->win_right >= 0 ? 1 : 0;
 }
 
@@ -205,14 +207,14 @@ namespace {
 // The forward behind every entry point: dense (cu_seqlens null), varlen with
 // one offset array (cu_seqlens_k == cu_seqlens) or with key offsets of their own.
 int fwd_entry(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv, int Lq,
-              int Lk, int d, int dv, float scale, int causal, int window_left, int window_right,
+              int Lk, int d, int dv, float scale, int causal, int window_left, int window_right, int sinks,
               const unsigned char* block_mask, int mask_heads, const int* cu_seqlens, const int* cu_seqlens_k,
               cudaStream_t stream) {
     int rc = check_common(B, H, Lq, Lk, d, scale, cu_seqlens, cu_seqlens_k);
     if (rc) return rc;
     rc = check_block_mask(block_mask, mask_heads, H, cu_seqlens);
     if (rc) return rc;
-    rc = check_window(window_left, window_right);
+    rc = check_window(window_left, window_right, sinks);
     if (rc) return rc;
     rc = check_heads(H, Hkv);
     if (rc) return rc;
@@ -243,6 +245,7 @@ int fwd_entry(const void* q, const void* k, const void* v, void* o, float* lse, 
     p.dv = dv;
     p.mask.ptr = block_mask;
     p.mask.heads = mask_heads;
+    p.mask.sinks = window_left < 0 ? 0 : (sinks < Lk ? sinks : Lk);   // (no left bound: nothing to keep visible)
     p.lse = lse;
     // d <= 128: a work tile is two 128-row Q tiles; wider heads: one
     const bool wide = d > 128;
@@ -275,7 +278,7 @@ int fwd_entry(const void* q, const void* k, const void* v, void* o, float* lse, 
 extern "C" int attn_fwd_gqa(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
                             int Hkv, int Lq, int Lk, int d, int dv, float scale, int causal,
                             const int* cu_seqlens, cudaStream_t stream) {
-    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, dv, scale, causal, -1, -1, nullptr, 1, cu_seqlens,
+    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, dv, scale, causal, -1, -1, 0, nullptr, 1, cu_seqlens,
                      cu_seqlens, stream);
 }
 
@@ -284,15 +287,24 @@ extern "C" int attn_fwd_ex(const void* q, const void* k, const void* v, void* o,
                            int window_right, const unsigned char* block_mask, int mask_heads,
                            const int* cu_seqlens_q, const int* cu_seqlens_k, cudaStream_t stream) {
     if (cu_seqlens_k && !cu_seqlens_q) return fail(ATTN_ERR_ARG, "attn_fwd_ex: key offsets without query offsets");
-    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left, window_right,
+    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left, window_right, 0,
                      block_mask, mask_heads, cu_seqlens_q, cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q, stream);
+}
+
+extern "C" int attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
+                              int Lq, int Lk, int d, int d_v, float scale, int causal, int window_left,
+                              int window_right, int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                              cudaStream_t stream) {
+    if (cu_seqlens_k && !cu_seqlens_q) return fail(ATTN_ERR_ARG, "attn_fwd_sinks: key offsets without query offsets");
+    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left, window_right, sinks,
+                     nullptr, 1, cu_seqlens_q, cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q, stream);
 }
 
 extern "C" int attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
                                int Hkv, int Tq, int Tk, int d, int dv, float scale, int causal,
                                const int* cu_seqlens_q, const int* cu_seqlens_k, cudaStream_t stream) {
     if (!cu_seqlens_q || !cu_seqlens_k) return fail(ATTN_ERR_ARG, "attn_fwd_varlen: null offsets");
-    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Tq, Tk, d, dv, scale, causal, -1, -1, nullptr, 1, cu_seqlens_q,
+    return fwd_entry(q, k, v, o, lse, B, H, Hkv, Tq, Tk, d, dv, scale, causal, -1, -1, 0, nullptr, 1, cu_seqlens_q,
                      cu_seqlens_k, stream);
 }
 
@@ -358,14 +370,14 @@ namespace {
 // The backward behind every entry point (cu_seqlens_k as in fwd_entry).
 int bwd_entry(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
               void* dq, void* dk, void* dv, int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, float scale,
-              int causal, int window_left, int window_right, const unsigned char* block_mask, int mask_heads,
-              const int* cu_seqlens, const int* cu_seqlens_k, int deterministic, void* workspace, size_t ws_bytes,
-              cudaStream_t stream) {
+              int causal, int window_left, int window_right, int sinks, const unsigned char* block_mask,
+              int mask_heads, const int* cu_seqlens, const int* cu_seqlens_k, int deterministic, void* workspace,
+              size_t ws_bytes, cudaStream_t stream) {
     int rc = check_common(B, H, Lq, Lk, d, scale, cu_seqlens, cu_seqlens_k);
     if (rc) return rc;
     rc = check_block_mask(block_mask, mask_heads, H, cu_seqlens);
     if (rc) return rc;
-    rc = check_window(window_left, window_right);
+    rc = check_window(window_left, window_right, sinks);
     if (rc) return rc;
     rc = check_heads(H, Hkv);
     if (rc) return rc;
@@ -405,6 +417,7 @@ int bwd_entry(const void* q, const void* k, const void* v, const void* o, const 
     p.g.scale_log2 = scale * kLog2e;
     p.mask.ptr = block_mask;
     p.mask.heads = mask_heads;
+    p.mask.sinks = window_left < 0 ? 0 : (sinks < Lk ? sinks : Lk);   // (no left bound: nothing to keep visible)
     p.o = static_cast<const __nv_bfloat16*>(o);
     p.dout = static_cast<const __nv_bfloat16*>(dout);
     p.lse = lse;
@@ -458,7 +471,7 @@ extern "C" int attn_bwd_gqa(const void* q, const void* k, const void* v, const v
                             const void* dout, void* dq, void* dk, void* dv, int B, int H, int Hkv, int Lq, int Lk,
                             int d, float scale, int causal, const int* cu_seqlens, int deterministic,
                             void* workspace, size_t ws_bytes, cudaStream_t stream) {
-    return bwd_entry(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d, scale, causal, -1, -1, nullptr, 1,
+    return bwd_entry(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d, scale, causal, -1, -1, 0, nullptr, 1,
                      cu_seqlens, cu_seqlens, deterministic, workspace, ws_bytes, stream);
 }
 
@@ -470,7 +483,18 @@ extern "C" int attn_bwd_ex(const void* q, const void* k, const void* v, const vo
                            cudaStream_t stream) {
     if (cu_seqlens_k && !cu_seqlens_q) return fail(ATTN_ERR_ARG, "attn_bwd_ex: key offsets without query offsets");
     return bwd_entry(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left,
-                     window_right, block_mask, mask_heads, cu_seqlens_q, cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q,
+                     window_right, 0, block_mask, mask_heads, cu_seqlens_q, cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q,
+                     deterministic, workspace, ws_bytes, stream);
+}
+
+extern "C" int attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                              const void* dout, void* dq, void* dk, void* dv, int B, int H, int Hkv, int Lq, int Lk,
+                              int d, int d_v, float scale, int causal, int window_left, int window_right, int sinks,
+                              const int* cu_seqlens_q, const int* cu_seqlens_k, int deterministic, void* workspace,
+                              size_t ws_bytes, cudaStream_t stream) {
+    if (cu_seqlens_k && !cu_seqlens_q) return fail(ATTN_ERR_ARG, "attn_bwd_sinks: key offsets without query offsets");
+    return bwd_entry(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left,
+                     window_right, sinks, nullptr, 1, cu_seqlens_q, cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q,
                      deterministic, workspace, ws_bytes, stream);
 }
 
@@ -480,7 +504,7 @@ extern "C" int attn_bwd_varlen(const void* q, const void* k, const void* v, cons
                                const int* cu_seqlens_k, int deterministic, void* workspace, size_t ws_bytes,
                                cudaStream_t stream) {
     if (!cu_seqlens_q || !cu_seqlens_k) return fail(ATTN_ERR_ARG, "attn_bwd_varlen: null offsets");
-    return bwd_entry(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Tq, Tk, d, d, scale, causal, -1, -1, nullptr, 1,
+    return bwd_entry(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Tq, Tk, d, d, scale, causal, -1, -1, 0, nullptr, 1,
                      cu_seqlens_q, cu_seqlens_k, deterministic, workspace, ws_bytes, stream);
 }
 

@@ -183,8 +183,8 @@ __device__ __forceinline__ WideBwdTile wide_bwd_tile(int t, const BwdParams& p, 
     // none: the tile writes zero dK/dV rows). No mask or the causal one: all
     // blocks, or those from the one holding row n*kBN - (lk - lq) on.
     if constexpr (kBand) {
-        band_query_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right), f.n * kBN, f.n * kBN + kBN - 1, kBM,
-                          &f.m_begin, &f.m_end);
+        band_query_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks), f.n * kBN,
+                          f.n * kBN + kBN - 1, kBM, &f.m_begin, &f.m_end);
     } else {
         f.m_end = (f.lq + kBM - 1) / kBM;
         f.m_begin = 0;
@@ -589,7 +589,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             // query q is allowed for this key iff q_lo <= q < q_hi (the mask band)
             int q_lo, q_hi;
             if constexpr (kBand) {
-                const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right);
+                const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks);
                 q_lo = key_ok ? band_query_lo(mb, key) : 0;
                 q_hi = key_ok ? band_query_hi(mb, key) : 0;   // (key_ok false: lo = 64 below)
             } else {

@@ -30,15 +30,21 @@ __host__ __device__ __forceinline__ long dq_semaphore(const BwdParams& p, const 
 // The number of key blocks that go before block f.n at query block m of head
 // h. Order: from the highest key block down with a right mask bound (shortest
 // tiles first, so no tile waits at its first dQ write), else ascending. The key
-// blocks that see query block m form one range [n_lo, n_hi) (the mask band);
-// with a block mask only the kept ones count.
+// blocks that see query block m form one range [n_lo, n_hi) (the mask band),
+// with sinks also the blocks [0, n_sink) before it; with a block mask only the
+// kept ones count.
 template <bool kBand, bool kSparse, class Tile>
 __host__ __device__ __forceinline__ int dq_turn(const BwdParams& p, const Tile& f, int h, int m) {
     const Geometry& g = p.g;
     int n_lo, n_hi;
-    band_key_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right), m * 128, m * 128 + 127, 128, &n_lo, &n_hi);
+    const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right, kBand ? p.mask.sinks : 0);
+    band_key_blocks(mb, m * 128, m * 128 + 127, 128, &n_lo, &n_hi);
     const bool spt = g.causal != 0;
     int before = spt ? n_hi - 1 - f.n : f.n - (kBand ? n_lo : 0);
+    if (kBand && mb.sinks > 0) {   // the gap between the sinks and the window has no turns
+        const int n_sink = band_sink_blocks(mb, 128, n_lo), gap = n_lo - n_sink;
+        before += spt ? (f.n < n_sink ? -gap : 0) : (f.n < n_sink ? n_lo : n_sink);
+    }
     if (kSparse && f.mcol) {
         const unsigned char* row =
             p.mask.ptr + ((p.mask.heads == 1 ? 0 : (long)h) * mask_rows(g) + m) * mask_cols(g);

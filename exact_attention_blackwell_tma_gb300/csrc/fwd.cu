@@ -131,16 +131,26 @@ struct FwdTile {
     const unsigned char* mrow0;
     const unsigned char* mrow1;
     int kb_end;
+    // sinks: the stream starts with key blocks 0 .. n_sink - 1 (sinks left of the
+    // window, for both Q tiles: kv_start1 = 0) and goes on at kv_first
+    int n_sink;
 };
+
+// The key block that follows kb in a tile's stream (no block mask).
+template <bool kSinks>
+__device__ __forceinline__ int next_block(const FwdTile& f, int kb) {
+    return kSinks && kb + 1 == f.n_sink ? f.kv_first : kb + 1;
+}
 
 // kGeneral: the mask has a left bound (a local window) or a block mask.
 // Without either every row's keys start at key 0 and every block in range is
 // visited, so the kernels instantiated with kGeneral = false keep the stream
 // start, Q tile 1's first block and the rows' lower column bound at the
 // constant 0 and contain no mask scans (fewer live registers in the softmax
-// loop). kSparse (with kGeneral only): a block mask is given. lane: the
-// calling warp's lane (the block-mask scans are warp-wide).
-template <bool kGeneral, bool kSparse>
+// loop). kSparse (with kGeneral only): a block mask is given. kSinks (with
+// kGeneral, without kSparse): the window has sinks. lane: the calling warp's
+// lane (the block-mask scans are warp-wide).
+template <bool kGeneral, bool kSparse, bool kSinks>
 __device__ __forceinline__ FwdTile fwd_tile(int t, const FwdParams& p, const VarlenMap& vm, bool varlen, int lane) {
     const Geometry& g = p.g;
     Tile ti = varlen ? sched_varlen(vm, t, g.B, g.H, kRowsPerTile, p.head_section, g.causal != 0, false)
@@ -189,10 +199,19 @@ __device__ __forceinline__ FwdTile fwd_tile(int t, const FwdParams& p, const Var
             f.kv_start1 = 0;
         }
     }
+    f.n_sink = 0;
+    if constexpr (kSinks) {
+        if (f.n_kv > 0) {
+            f.n_sink = band_sink_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks), kBN, f.kv_first);
+            f.n_kv += f.n_sink;
+            if (f.n_kv0 > 0) f.n_kv0 += f.n_sink;
+            f.kv_start1 = 0;   // tile 1 masks the block at the window's left edge that only tile 0 sees
+        }
+    }
     return f;
 }
 
-template <int HD, bool kGeneral, bool kSparse, int kPoly>
+template <int HD, bool kGeneral, bool kSparse, int kPoly, bool kSinks = false>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -255,7 +274,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         uint32_t kv_cnt = 0, it = 0, q_issued = 0;
         bool ok = true;
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const FwdTile f = fwd_tile<kGeneral, kSparse>(t, p, vm, varlen, lane);
+            const FwdTile f = fwd_tile<kGeneral, kSparse, kSinks>(t, p, vm, varlen, lane);
             if (f.n_kv == 0) continue;
             ok = warp_wait(bar(Lay::kQEmpty), (it & 1u) ^ 1u, w, lane);
             if (!ok) break;
@@ -270,6 +289,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             ++q_issued;
             const bool sparse = kSparse && f.mrow0 != nullptr;
             int kb = kGeneral ? f.kv_first : 0;   // key block of stream block j
+            if (kSinks && f.n_sink > 0) kb = 0;
             if (sparse) kb = sparse_next(f.mrow0, f.mrow1, kb, f.kb_end, lane);
             for (int j = 0; j < f.n_kv && ok; ++j) {
                 // K and V of a block complete on the K slot's barrier (one wait for both)
@@ -288,7 +308,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     __syncwarp();
                     ++kv_cnt;
                 }
-                if constexpr (kGeneral) kb = sparse ? sparse_next(f.mrow0, f.mrow1, kb + 1, f.kb_end, lane) : kb + 1;
+                if constexpr (kGeneral) kb = sparse ? sparse_next(f.mrow0, f.mrow1, kb + 1, f.kb_end, lane) : next_block<kSinks>(f, kb);
             }
             ++it;
         }
@@ -363,7 +383,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             // scheduler (this order measured 6-8% slower than the d = 128 order that way,
             // 18-21% faster converged); commits stay on lane 0.
             for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-                const FwdTile f = fwd_tile<kGeneral, kSparse>(t, p, vm, varlen, lane);
+                const FwdTile f = fwd_tile<kGeneral, kSparse, kSinks>(t, p, vm, varlen, lane);
                 if (f.n_kv == 0) continue;
                 const int n0 = f.n_kv0, s1 = kGeneral ? f.kv_start1 : 0;   // Q tile 0: [0, n0), Q tile 1: [s1, n_kv)
                 ok = warp_wait(bar(Lay::kQFull), it & 1u, w, lane);
@@ -456,7 +476,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         uint32_t kv_cnt = 0, it = 0, pc0 = 0, pc1 = 0;
         bool ok = true;
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const FwdTile f = fwd_tile<kGeneral, kSparse>(t, p, vm, varlen, lane);
+            const FwdTile f = fwd_tile<kGeneral, kSparse, kSinks>(t, p, vm, varlen, lane);
             if (f.n_kv == 0) continue;
             const int n0 = f.n_kv0, s1 = kGeneral ? f.kv_start1 : 0;   // Q tile 0: [0, n0), Q tile 1: [s1, n_kv)
             ok = warp_wait(bar(Lay::kQFull), it & 1u, w, lane);
@@ -556,7 +576,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         bool ok = true;
         uint32_t rr[32];
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const FwdTile f = fwd_tile<kGeneral, kSparse>(t, p, vm, varlen, lane);
+            const FwdTile f = fwd_tile<kGeneral, kSparse, kSinks>(t, p, vm, varlen, lane);
             const int r = f.mp * kRowsPerTile + tq * kBM + row_in_tile;   // row inside the sequence
             const bool valid = r < f.lq;
             const long prow = (long)f.q_row0 + tq * kBM + row_in_tile;   // packed row
@@ -575,10 +595,12 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right);
             const int col_lo = kGeneral ? band_key_lo(mb, r) : 0, col_limit = band_key_hi(mb, r);   // keys [col_lo, col_limit)
+            const int sinks = kSinks ? p.mask.sinks : 0;   // and keys [0, sinks) below col_limit
             // block-sparse: this Q tile's mask row (null: its row block is past the mask, no row is stored)
             const bool sparse = kSparse && f.mrow0 != nullptr;
             const unsigned char* mrow = tq ? f.mrow1 : f.mrow0;
             int kb = (kGeneral ? f.kv_first : 0) + jb;   // key block of stream block j
+            if (kSinks && f.n_sink > 0) kb = 0;          // (jb = 0)
             if (sparse) kb = sparse_next(f.mrow0, f.mrow1, f.kv_first, f.kb_end, lane);
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = jb; j < nkv; ++j) {
@@ -604,9 +626,10 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 if (dropped || c0 + kBN > col_limit || c0 < col_lo) {
 #pragma unroll
                     for (int c = 0; c < kBN; ++c)
-                        if (dropped || c0 + c >= col_limit || c0 + c < col_lo) s[c] = -INFINITY;
+                        if (dropped || c0 + c >= col_limit || (c0 + c < col_lo && (!kSinks || c0 + c >= sinks)))
+                            s[c] = -INFINITY;
                 }
-                if constexpr (kGeneral) kb = sparse ? sparse_next(f.mrow0, f.mrow1, kb + 1, f.kb_end, lane) : kb + 1;
+                if constexpr (kGeneral) kb = sparse ? sparse_next(f.mrow0, f.mrow1, kb + 1, f.kb_end, lane) : next_block<kSinks>(f, kb);
                 float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
                 for (int c = 4; c < kBN; c += 4) {
@@ -691,12 +714,13 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     }
 }
 
-// The kernel for a problem: the general one for a left window bound or a block
-// mask (MUFU only), else the plain one with the requested exp2 emulation.
+// The kernel for a problem: the general ones for a left window bound (with or
+// without sinks) or a block mask (MUFU only), else the plain one with the
+// requested exp2 emulation.
 template <int HD>
 auto fwd_kernel_for(const FwdParams& p, int poly_every) {
     if (p.mask.ptr) return fwd_kernel<HD, true, true, 0>;
-    if (p.g.win_left >= 0) return fwd_kernel<HD, true, false, 0>;
+    if (p.g.win_left >= 0) return p.mask.sinks > 0 ? fwd_kernel<HD, true, false, 0, true> : fwd_kernel<HD, true, false, 0>;
     return poly_every == 8 ? fwd_kernel<HD, false, false, 8>
                            : (poly_every == 4 ? fwd_kernel<HD, false, false, 4> : fwd_kernel<HD, false, false, 0>);
 }

@@ -68,10 +68,18 @@ struct WideTile {
     // that the tile's mask row keeps
     const unsigned char* mrow;
     int kb_end;
+    int n_sink;   // sinks: the tile first visits key blocks 0 .. n_sink - 1, then kv_first and on
 };
 
-// kSparse: a block mask may be given (the kernels without one contain no mask scans)
-template <bool kSparse>
+// The key block that follows kb in a tile's walk (no block mask).
+template <bool kSinks>
+__device__ __forceinline__ int next_block(const WideTile& f, int kb) {
+    return kSinks && kb + 1 == f.n_sink ? f.kv_first : kb + 1;
+}
+
+// kSparse: a block mask may be given (the kernels without one contain no mask
+// scans); kSinks (without kSparse): the window has sinks
+template <bool kSparse, bool kSinks>
 __device__ __forceinline__ WideTile wide_tile(int t, const FwdParams& p, const VarlenMap& vm, bool varlen, int lane) {
     const Geometry& g = p.g;
     Tile ti = varlen ? sched_varlen(vm, t, g.B, g.H, kBM, p.head_section, g.causal != 0, false)
@@ -107,10 +115,17 @@ __device__ __forceinline__ WideTile wide_tile(int t, const FwdParams& p, const V
             f.n_kv = f.n_kv > 0 ? sparse_count(f.mrow, nullptr, jlo, jhi, lane) : 0;
         }
     }
+    f.n_sink = 0;
+    if constexpr (kSinks) {
+        if (f.n_kv > 0) {
+            f.n_sink = band_sink_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks), kBN, jlo);
+            f.n_kv += f.n_sink;
+        }
+    }
     return f;
 }
 
-template <int HD, int DV, bool kSparse>
+template <int HD, int DV, bool kSparse, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -185,7 +200,7 @@ fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
         };
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideTile f = wide_tile<kSparse>(t, p, vm, varlen, lane);
+            const WideTile f = wide_tile<kSparse, kSinks>(t, p, vm, varlen, lane);
             if (f.n_kv == 0) continue;
             ok = warp_wait(bar(Lay::kQEmpty), (it & 1u) ^ 1u, w, lane);
             if (!ok) break;
@@ -200,19 +215,20 @@ fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             // V cursors walk the tile's key blocks (block-sparse: the kept ones)
             const bool sparse = kSparse && f.mrow != nullptr;
             auto kept = [&](int kb) { return sparse ? sparse_next(f.mrow, nullptr, kb, f.kb_end, lane) : kb; };
-            int kb_k = kept(f.kv_first), kb_v = kb_k;
+            auto following = [&](int kb) { return kSinks ? next_block<kSinks>(f, kb) : kept(kb + 1); };
+            int kb_k = kSinks && f.n_sink > 0 ? 0 : kept(f.kv_first), kb_v = kb_k;
             ok = load_kv(f, 0, kb_k);
-            kb_k = kept(kb_k + 1);
+            kb_k = following(kb_k);
             if (ok && f.n_kv >= 2) {
                 ok = load_kv(f, 0, kb_k);
-                kb_k = kept(kb_k + 1);
+                kb_k = following(kb_k);
             }
             for (int j = 0; j < f.n_kv && ok; ++j) {
                 ok = load_kv(f, 1, kb_v);
-                kb_v = kept(kb_v + 1);
+                kb_v = following(kb_v);
                 if (ok && j + 2 < f.n_kv) {
                     ok = load_kv(f, 0, kb_k);
-                    kb_k = kept(kb_k + 1);
+                    kb_k = following(kb_k);
                 }
             }
             ++it;
@@ -254,7 +270,7 @@ fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             tc_commit(bar(Lay::kKVEmpty + slot));
         };
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideTile f = wide_tile<kSparse>(t, p, vm, varlen, lane);
+            const WideTile f = wide_tile<kSparse, kSinks>(t, p, vm, varlen, lane);
             if (f.n_kv == 0) continue;
             ok = warp_wait(bar(Lay::kQFull), it & 1u, w, lane);
             if (!ok) break;
@@ -326,7 +342,7 @@ fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         uint32_t rr[32];
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideTile f = wide_tile<kSparse>(t, p, vm, varlen, lane);
+            const WideTile f = wide_tile<kSparse, kSinks>(t, p, vm, varlen, lane);
             const int r = f.m * kBM + row_in_tile;
             const bool valid = r < f.lq;
             const long prow = (long)f.q_row0 + row_in_tile;
@@ -345,6 +361,8 @@ fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int col_lo = band_key_lo(mb, r), col_limit = band_key_hi(mb, r);   // keys [col_lo, col_limit)
             const bool sparse = kSparse && f.mrow != nullptr;
             int kb = sparse ? sparse_next(f.mrow, nullptr, f.kv_first, f.kb_end, lane) : f.kv_first;
+            if (kSinks && f.n_sink > 0) kb = 0;
+            const int sinks = kSinks ? p.mask.sinks : 0;   // keys [0, sinks) below col_limit are seen too
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < f.n_kv; ++j) {
                 const int buf = j & 1;
@@ -361,11 +379,11 @@ fwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int i = 0; i < kBN; ++i) s[i] = u2f(r128[i]);
                 }
                 const int c0 = kb * kBN;
-                kb = sparse ? sparse_next(f.mrow, nullptr, kb + 1, f.kb_end, lane) : kb + 1;
+                kb = sparse ? sparse_next(f.mrow, nullptr, kb + 1, f.kb_end, lane) : next_block<kSinks>(f, kb);
                 if (c0 + kBN > col_limit || c0 < col_lo) {
 #pragma unroll
                     for (int c = 0; c < kBN; ++c)
-                        if (c0 + c >= col_limit || c0 + c < col_lo) s[c] = -INFINITY;
+                        if (c0 + c >= col_limit || (c0 + c < col_lo && (!kSinks || c0 + c >= sinks))) s[c] = -INFINITY;
                 }
                 float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
@@ -456,7 +474,9 @@ template <int HD, int DV>
 cudaError_t launch_fwd_wide_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const FwdParams& p, int num_sms, cudaStream_t stream) {
     using Lay = WideLayout<HD, DV>;
-    auto kern = p.mask.ptr ? fwd_wide_kernel<HD, DV, true> : fwd_wide_kernel<HD, DV, false>;
+    auto kern = p.mask.ptr ? fwd_wide_kernel<HD, DV, true, false>
+                           : (p.g.win_left >= 0 && p.mask.sinks > 0 ? fwd_wide_kernel<HD, DV, false, true>
+                                                                    : fwd_wide_kernel<HD, DV, false, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int grid = p.g.cu_seqlens ? num_sms : min(p.n_tiles, num_sms);

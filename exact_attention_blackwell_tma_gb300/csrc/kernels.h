@@ -30,10 +30,13 @@ struct Geometry {
 
 // A block mask (dense problems): bytes [heads][ceil(Lq/128)][ceil(Lk/128)],
 // heads 1 (shared) or H; a zero byte drops that 128 x 128 block (mask.cuh).
-// ptr null: none.
+// ptr null: none. Or, without one, the sinks of a local window: the first
+// `sinks` keys stay visible left of it (mask.cuh; the field sits here because
+// it fills the padding that FwdParams has room for).
 struct BlockMask {
     const unsigned char* ptr;
     int heads;
+    int sinks;
 };
 __host__ __device__ inline int mask_rows(const Geometry& g) { return (g.Lq + 127) / 128; }
 __host__ __device__ inline int mask_cols(const Geometry& g) { return (g.Lk + 127) / 128; }

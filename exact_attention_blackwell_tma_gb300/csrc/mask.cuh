@@ -8,6 +8,11 @@
 // one of the primitives its kernels compose with varlen and scheduling; the
 // band is the plainest one beyond the causal mask and contains it.
 //
+// Sinks: with a left bound (wl >= 0) the first `sinks` keys of the sequence
+// stay visible left of the window (key j < sinks still obeys the right bound).
+// They never give a key to a row whose window is empty: wl >= 0 keeps a row's
+// window non-empty unless its right bound lies before key 0.
+//
 // The functions are also compiled for the host, where tests/sched_host.cu
 // checks them against a brute-force scan of the mask.
 #pragma once
@@ -16,13 +21,14 @@ struct MaskBand {
     int delta;   // lk - lq
     int wl, wr;  // -1: no bound
     int lq, lk;
+    int sinks;   // keys [0, sinks) stay visible left of the window
 };
 
-__host__ __device__ __forceinline__ MaskBand mask_band(int lq, int lk, int wl, int wr) {
-    return MaskBand{lk - lq, wl, wr, lq, lk};
+__host__ __device__ __forceinline__ MaskBand mask_band(int lq, int lk, int wl, int wr, int sinks = 0) {
+    return MaskBand{lk - lq, wl, wr, lq, lk, wl >= 0 ? sinks : 0};
 }
 
-// Keys [lo, hi) that row r sees (hi <= lo: none).
+// Keys [lo, hi) of row r's window (hi <= lo: none; sinks left of lo are not counted).
 __host__ __device__ __forceinline__ int band_key_lo(const MaskBand& m, int r) {
     const int lo = m.wl >= 0 ? r + m.delta - m.wl : 0;
     return lo > 0 ? lo : 0;
@@ -49,13 +55,19 @@ __host__ __device__ __forceinline__ bool band_key_blocks(const MaskBand& m, int 
     return true;
 }
 
+// Blocks [0, *) of `bn` keys left of window block jlo that hold sinks.
+__host__ __device__ __forceinline__ int band_sink_blocks(const MaskBand& m, int bn, int jlo) {
+    const int n = (m.sinks + bn - 1) / bn;
+    return n < jlo ? n : jlo;
+}
+
 // Query rows [lo, hi) that see key j.
 __host__ __device__ __forceinline__ int band_query_lo(const MaskBand& m, int j) {
     const int lo = m.wr >= 0 ? j - m.delta - m.wr : 0;
     return lo > 0 ? lo : 0;
 }
 __host__ __device__ __forceinline__ int band_query_hi(const MaskBand& m, int j) {
-    const int hi = m.wl >= 0 ? j - m.delta + m.wl + 1 : m.lq;
+    const int hi = m.wl >= 0 && j >= m.sinks ? j - m.delta + m.wl + 1 : m.lq;
     return hi < m.lq ? hi : m.lq;
 }
 
@@ -67,7 +79,8 @@ __host__ __device__ __forceinline__ bool band_query_blocks(const MaskBand& m, in
     if (k0 < 0) k0 = 0;
     *mlo = *mhi = 0;
     if (k0 > k1) return false;
-    const int lo = band_query_lo(m, k0), hi = band_query_hi(m, k1);
+    // a block holding a sink is seen to the last row (by its first key already)
+    const int lo = band_query_lo(m, k0), hi = band_query_hi(m, k0 < m.sinks ? k0 : k1);
     if (hi <= lo) return false;
     *mlo = lo / bm;
     *mhi = (hi + bm - 1) / bm;

@@ -42,6 +42,11 @@
  *          with no key left gets O = 0, LSE = -inf. The causal mask is the
  *          band (-1, 0). (FlashAttention-4 paper, Section 4: masking
  *          strategies compose with varlen and scheduling.)
+ *   sinks (attn_fwd_sinks, attn_bwd_sinks): with a left bound, the first
+ *          `sinks` keys of every sequence stay visible left of the window
+ *          (keys j < sinks drop the left bound and keep the right one; the
+ *          band plus the attention sinks of long streams). Without a left
+ *          bound they change nothing. They are not combined with a block mask.
  *   block mask (attn_fwd_ex, attn_bwd_ex; dense problems only): a DEVICE
  *          byte array [mask_heads][ceil(Lq/128)][ceil(Lk/128)], mask_heads 1
  *          (one mask for every head) or H (query head h uses its own); a zero
@@ -196,6 +201,27 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
                 int window_left, int window_right, const unsigned char* block_mask, int mask_heads,
                 const int* cu_seqlens_q, const int* cu_seqlens_k, int deterministic,
                 void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The general forward and backward with sinks (see "sinks" above; sinks >= 0,
+ * at most Lk of them count; 0 gives attn_fwd_ex and attn_bwd_ex without a
+ * block mask). Grouped heads, the head-dim pairs, dense and packed problems
+ * as there. A work tile visits the key blocks that hold sinks and then the
+ * blocks of its rows' window; in the backward a block that holds a sink visits
+ * every query row from its diagonal on. Key and value rows of every visited
+ * 128-key block must be finite, as for the other masks. workspace:
+ * attn_bwd_ex_workspace_size(...) bytes.
+ */
+int attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                   int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, float scale, int causal,
+                   int window_left, int window_right, int sinks,
+                   const int* cu_seqlens_q, const int* cu_seqlens_k, cudaStream_t stream);
+int attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                   const void* dout, void* dq, void* dk, void* dv,
+                   int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, float scale, int causal,
+                   int window_left, int window_right, int sinks,
+                   const int* cu_seqlens_q, const int* cu_seqlens_k, int deterministic,
+                   void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Workspace for attn_bwd_gqa: as attn_bwd_workspace_size, plus fp32 slots
