@@ -24,6 +24,12 @@ c_int, c_float, c_size_t, c_void_p = ctypes.c_int, ctypes.c_float, ctypes.c_size
 ATTN_OK, ATTN_ERR_ARG, ATTN_ERR_ALIGN, ATTN_ERR_LAUNCH, ATTN_ERR_WORKSPACE, ATTN_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
 
 
+class _Kv4Struct(ctypes.Structure):
+    """attn_kv4_cache of include/attn.h."""
+    _fields_ = [("k_codes", c_void_p), ("k_params", c_void_p), ("v_codes", c_void_p), ("v_params", c_void_p),
+                ("n_pages", c_int), ("Hkv", c_int), ("d", c_int), ("d_v", c_int)]
+
+
 class AttnError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"attn error {code}: {msg}")
@@ -69,6 +75,21 @@ def _declare(lib):
                                                                       c_void_p, c_size_t, c_void_p])
     lib.attn_bwd_noalloc.restype = c_int
     lib.attn_bwd_noalloc.argtypes = [c_void_p] * 9 + [c_int] * 5 + [c_float, c_int, c_void_p, c_int, c_void_p]
+    kv4, i64 = ctypes.POINTER(_Kv4Struct), ctypes.c_longlong
+    lib.attn_kv4_append.restype = c_int
+    lib.attn_kv4_append.argtypes = [c_void_p, c_void_p, i64, i64, kv4, c_void_p, c_int, c_void_p, c_void_p, c_int,
+                                    c_int, c_void_p]
+    lib.attn_kv4_read.restype = c_int
+    lib.attn_kv4_read.argtypes = [c_void_p, c_void_p, kv4, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p]
+    lib.attn_kv4_fwd_workspace_size.restype = c_size_t
+    lib.attn_kv4_fwd_workspace_size.argtypes = [c_int] * 9
+    lib.attn_kv4_fwd.restype = c_int
+    lib.attn_kv4_fwd.argtypes = ([c_void_p, i64, kv4, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p]
+                                 + [c_int] * 3 + [c_float] + [c_int] * 4
+                                 + [c_void_p, i64, c_float, c_void_p, c_size_t, c_void_p])
+    lib.attn_kv4_evict.restype = c_int
+    lib.attn_kv4_evict.argtypes = ([kv4, c_void_p, c_int, c_void_p, c_void_p, i64, c_void_p] + [c_int] * 5
+                                   + [c_void_p] * 3 + [i64, c_void_p])
     lib.attn_set_backward_cta_pairs.restype = c_int
     lib.attn_set_backward_cta_pairs.argtypes = [c_int]
     lib.attn_set_exp2_emulation.restype = c_int
@@ -239,6 +260,37 @@ def attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, B, H, Lq, Lk, d, scale, 
                                    int(deterministic), _stream(stream))
 
 
+def attn_kv4_append(k, v, k_stride, v_stride, cache, page_table, table_width, cache_lens, cu_seqlens, B, L,
+                    stream=None) -> int:
+    return load().attn_kv4_append(_ptr(k), _ptr(v), k_stride, v_stride, cache, _ptr(page_table), table_width,
+                                  _ptr(cache_lens), _ptr(cu_seqlens), B, L, _stream(stream))
+
+
+def attn_kv4_read(k, v, cache, page_table, table_width, cache_lens, cu_seqlens, B, L, stream=None) -> int:
+    return load().attn_kv4_read(_ptr(k), _ptr(v), cache, _ptr(page_table), table_width, _ptr(cache_lens),
+                                _ptr(cu_seqlens), B, L, _stream(stream))
+
+
+def attn_kv4_fwd_workspace_size(B, H, Hkv, L, packed, table_width, d, d_v, key_weights) -> int:
+    return load().attn_kv4_fwd_workspace_size(B, H, Hkv, L, int(packed), table_width, d, d_v, int(key_weights))
+
+
+def attn_kv4_fwd(q, q_stride, cache, page_table, table_width, cache_lens, cu_seqlens, o, lse, B, H, L, scale, causal,
+                 window_left, window_right, sinks, key_weights, weight_stride, weight_decay, workspace, ws_bytes,
+                 stream=None) -> int:
+    return load().attn_kv4_fwd(_ptr(q), q_stride, cache, _ptr(page_table), table_width, _ptr(cache_lens),
+                               _ptr(cu_seqlens), _ptr(o), _ptr(lse), B, H, L, scale, int(causal), int(window_left),
+                               int(window_right), int(sinks), _ptr(key_weights), weight_stride, weight_decay,
+                               _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def attn_kv4_evict(cache, page_table, table_width, cache_lens, key_weights, weight_stride, new_table, new_width, B,
+                   budget, sinks, recent, new_lens, kept, new_key_weights, new_weight_stride, stream=None) -> int:
+    return load().attn_kv4_evict(cache, _ptr(page_table), table_width, _ptr(cache_lens), _ptr(key_weights),
+                                 weight_stride, _ptr(new_table), new_width, B, budget, sinks, recent, _ptr(new_lens),
+                                 _ptr(kept), _ptr(new_key_weights), new_weight_stride, _stream(stream))
+
+
 def attn_set_backward_cta_pairs(enable) -> int:
     """Backward main kernel on CTA pairs (2-CTA tensor cores) where it applies;
     returns the previous setting."""
@@ -376,3 +428,184 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
 
 def check_status(stream=None):
     _check(attn_check_status(stream))
+
+
+# ---------------------------------------------------------------- the 4-bit key/value cache
+
+KV4_PAGE, KV4_GROUP = 64, 64   # tokens of a page; channels that share a scale and a minimum
+
+
+class Kv4Cache:
+    """The four tensors of a 4-bit cache (layout: include/attn.h, attn_kv4_cache):
+    k_codes uint8 [pages, Hkv, d // 64, 64, 32], k_params bf16 [pages, Hkv, d // 64, 64, 2],
+    v_codes and v_params the same with v's head dim."""
+
+    __slots__ = ("k_codes", "k_params", "v_codes", "v_params", "n_pages", "Hkv", "d", "dv", "_struct")
+
+    def __init__(self, k_codes, k_params, v_codes, v_params):
+        for codes, params in ((k_codes, k_params), (v_codes, v_params)):
+            pages, heads, groups = k_codes.shape[0], k_codes.shape[1], codes.shape[2]
+            if (codes.dtype != torch.uint8 or tuple(codes.shape) != (pages, heads, groups, KV4_PAGE, KV4_GROUP // 2)
+                    or params.dtype != torch.bfloat16
+                    or tuple(params.shape) != (pages, heads, groups, KV4_PAGE, 2)):
+                raise ValueError(f"a 4-bit cache needs uint8 codes [pages, heads, groups, {KV4_PAGE}, {KV4_GROUP // 2}] "
+                                 f"and bf16 params [pages, heads, groups, {KV4_PAGE}, 2], got {codes.dtype} "
+                                 f"{tuple(codes.shape)} and {params.dtype} {tuple(params.shape)}")
+        _check_tensors(k_codes, k_params, v_codes, v_params)
+        self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
+        self.n_pages, self.Hkv = k_codes.shape[0], k_codes.shape[1]
+        self.d, self.dv = k_codes.shape[2] * KV4_GROUP, v_codes.shape[2] * KV4_GROUP
+        self._struct = _Kv4Struct(k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
+                                  self.n_pages, self.Hkv, self.d, self.dv)
+
+    @classmethod
+    def empty(cls, n_pages, Hkv, d, dv=None, device="cuda"):
+        """A cache of n_pages zeroed pages."""
+        dv = d if dv is None else dv
+
+        def codes(width):
+            return torch.zeros((n_pages, Hkv, width // KV4_GROUP, KV4_PAGE, KV4_GROUP // 2), dtype=torch.uint8,
+                               device=device)
+
+        def params(width):
+            return torch.zeros((n_pages, Hkv, width // KV4_GROUP, KV4_PAGE, 2), dtype=torch.bfloat16, device=device)
+        return cls(codes(d), params(d), codes(dv), params(dv))
+
+
+def _kv4_ints(cache, B, **tensors):
+    """int32 contiguous tensors on the cache's device, which is the current one."""
+    device = cache.k_codes.device
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+        rows = B + 1 if name.startswith("cu_") else B
+        if t.shape[0] != rows or t.dim() != (2 if name.endswith("table") else 1):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows} rows")
+
+
+def _kv4_rows(x, heads, width, B, cu_seqlens, name, device):
+    """Rows of [T, heads, width] (packed) or [B, L, heads, width] (dense): (L, elements between rows).
+    Heads and channels are contiguous; rows may lie further apart (a slice of a fused projection)."""
+    dims = 3 if cu_seqlens is not None else 4
+    if (x.dim() != dims or tuple(x.shape[-2:]) != (heads, width) or x.dtype != torch.bfloat16 or x.device != device
+            or (dims == 4 and x.shape[0] != B)):
+        lead = "T" if dims == 3 else f"{B}, L"
+        raise ValueError(f"{name} must be a bf16 tensor [{lead}, {heads}, {width}] on {device}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    L = x.shape[-3]
+    if x.numel() == 0:
+        return L, heads * width
+    row = x.stride(-3) if L > 1 else (x.stride(0) if dims == 4 and B > 1 else heads * width)
+    if (x.stride(-1) != 1 or (heads > 1 and x.stride(-2) != width)
+            or (dims == 4 and B > 1 and x.stride(0) != L * row)):
+        raise ValueError(f"{name}: heads and channels must be contiguous and rows evenly spaced, strides {x.stride()}")
+    return L, row
+
+
+def _kv4_out(t, shape, dtype, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+    return t
+
+
+class _On:
+    """Allocations inside belong to the stream that the call runs on."""
+
+    def __init__(self, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        self.context = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+
+
+def kv4_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=None):
+    """Quantise new keys and values (bf16 [T, Hkv, d] with int32 cu_seqlens, or [B, L, Hkv, d]) into the pages of
+    their sequences. cache_lens (int32 [B]) counts the new tokens already: sequence b's n rows become its tokens
+    cache_lens[b] - n .. cache_lens[b] - 1. Rows of k and v may be strided (a slice of a fused projection)."""
+    B, device = cache_lens.shape[0], cache.k_codes.device
+    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, cu_seqlens=cu_seqlens)
+    L, k_stride = _kv4_rows(k, cache.Hkv, cache.d, B, cu_seqlens, "k", device)
+    Lv, v_stride = _kv4_rows(v, cache.Hkv, cache.dv, B, cu_seqlens, "v", device)
+    if L != Lv:
+        raise ValueError(f"k has {L} rows, v {Lv}")
+    _check(attn_kv4_append(k, v, k_stride, v_stride, cache._struct, page_table, page_table.shape[1], cache_lens,
+                           cu_seqlens, B, L, stream))
+
+
+def kv4_read(cache, page_table, cache_lens, rows, cu_seqlens=None, k=None, v=None, stream=None):
+    """K, V in bf16 as the cache stands for them: the last rows of every sequence, packed ([rows, Hkv, d], rows =
+    cu_seqlens[-1]) or dense (rows per sequence; [B, rows, Hkv, d], zero before a sequence's first token)."""
+    B, device = cache_lens.shape[0], cache.k_codes.device
+    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, cu_seqlens=cu_seqlens)
+    lead = (rows,) if cu_seqlens is not None else (B, rows)
+    with _On(stream):
+        k = _kv4_out(k, lead + (cache.Hkv, cache.d), torch.bfloat16, device, "k")
+        v = _kv4_out(v, lead + (cache.Hkv, cache.dv), torch.bfloat16, device, "v")
+    _check(attn_kv4_read(k, v, cache._struct, page_table, page_table.shape[1], cache_lens, cu_seqlens, B, rows, stream))
+    return k, v
+
+
+def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: float | None = None, cu_seqlens=None,
+                window=(-1, -1), sinks: int = 0, key_weights=None, weight_decay: float = 1.0, out=None, lse=None,
+                workspace=None, stream=None):
+    """O, LSE of new tokens q (bf16 [T, H, d] with cu_seqlens, or [B, L, H, d]) over their sequence's cache, to which
+    their keys have been appended. window and sinks as in forward(). key_weights (fp32 [B, Hkv, >= longest cache]):
+    updated in place to weight_decay * key_weights + the attention weight each key got from the call's rows."""
+    B, device = cache_lens.shape[0], cache.k_codes.device
+    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, cu_seqlens=cu_seqlens)
+    H = q.shape[-2]
+    L, q_stride = _kv4_rows(q, H, cache.d, B, cu_seqlens, "q", device)
+    if H % cache.Hkv != 0 or H == 0:
+        raise ValueError(f"{H} query heads over {cache.Hkv} key/value heads")
+    if key_weights is not None and (key_weights.dtype != torch.float32 or key_weights.device != device
+                                    or not key_weights.is_contiguous() or key_weights.dim() != 3
+                                    or tuple(key_weights.shape[:2]) != (B, cache.Hkv)):
+        raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on {device}")
+    scale = 1.0 / math.sqrt(cache.d) if scale is None else scale
+    width, packed = page_table.shape[1], cu_seqlens is not None
+    need = attn_kv4_fwd_workspace_size(B, H, cache.Hkv, L, packed, width, cache.d, cache.dv, key_weights is not None)
+    with _On(stream):
+        out = _kv4_out(out, q.shape[:-1] + (cache.dv,), torch.bfloat16, device, "out")
+        lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, device, "lse")
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _check(attn_kv4_fwd(q, q_stride, cache._struct, page_table, width, cache_lens, cu_seqlens, out, lse, B, H, L, scale,
+                        causal, window[0], window[1], sinks, key_weights,
+                        0 if key_weights is None else key_weights.shape[2], weight_decay, workspace,
+                        workspace.numel() * workspace.element_size(), stream))
+    return out, lse
+
+
+def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int, sinks: int = 0, recent: int = 0,
+              new_lens=None, kept=None, new_key_weights=None, stream=None):
+    """Keep, of every sequence longer than budget and for each key/value head, the first `sinks` keys, the last
+    `recent` and those between with the largest key_weights, in the pages of new_table (pages of the same cache that
+    are not in page_table). Returns new_lens int32 [B], kept int32 [B, Hkv, budget] (old token of each new one, -1 past
+    the new length) and the kept key weights fp32 [B, Hkv, budget] (or as wide as new_key_weights is)."""
+    B, device = cache_lens.shape[0], cache.k_codes.device
+    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, new_table=new_table)
+    if (key_weights.dtype != torch.float32 or key_weights.device != device or not key_weights.is_contiguous()
+            or key_weights.dim() != 3 or tuple(key_weights.shape[:2]) != (B, cache.Hkv)):
+        raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on {device}")
+    columns = budget if new_key_weights is None else new_key_weights.shape[-1]
+    with _On(stream):
+        new_lens = _kv4_out(new_lens, (B,), torch.int32, device, "new_lens")
+        kept = _kv4_out(kept, (B, cache.Hkv, budget), torch.int32, device, "kept")
+        new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, device, "new_key_weights")
+    _check(attn_kv4_evict(cache._struct, page_table, page_table.shape[1], cache_lens, key_weights, key_weights.shape[2],
+                          new_table, new_table.shape[1], B, budget, sinks, recent, new_lens, kept, new_key_weights,
+                          columns, stream))
+    return new_lens, kept, new_key_weights

@@ -14,6 +14,7 @@
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
+#include "kv4.h"
 #include "ptx.cuh"
 #include "sched.cuh"
 
@@ -571,6 +572,202 @@ extern "C" int attn_bwd_noalloc(const void* q, const void* k, const void* v, con
                     scratch, (size_t)ATTN_NOALLOC_SCRATCH_BYTES, stream);
 }
 
+// ---------------------------------------------------------------- the 4-bit key/value cache
+namespace {
+
+int check_kv4(const attn_kv4_cache* c, int B, int L, const int* table, int width, const int* lens, const int* cu,
+              Kv4Cache* cache, Kv4Batch* batch) {
+    if (!c) return fail(ATTN_ERR_ARG, "kv4: null cache");
+    if (B < 0 || L < 0 || c->Hkv < 1 || c->Hkv > 65535 || c->n_pages < 1 || width < 1)
+        return fail(ATTN_ERR_ARG, "kv4: bad sizes B=%d L=%d Hkv=%d pages=%d table width=%d", B, L, c->Hkv, c->n_pages,
+                    width);
+    if (B > kKv4MaxBatch) return fail(ATTN_ERR_ARG, "kv4: B must be in [0, %d]", kKv4MaxBatch);
+    if (c->d != 64 && c->d != 128 && c->d != 192 && c->d != 256)
+        return fail(ATTN_ERR_ARG, "head dim %d not supported (64, 128, 192, 256)", c->d);
+    if (c->d_v != c->d && !(c->d == 192 && c->d_v == 128))
+        return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (d_v = d, or d = 192 with d_v = 128)", c->d,
+                    c->d_v);
+    if ((long)width * kPage >= (1L << 31)) return fail(ATTN_ERR_ARG, "kv4: table width %d too large", width);
+    const long total = cu ? (long)L : (long)B * L;
+    if (total >= (1L << 31)) return fail(ATTN_ERR_ARG, "too many rows");
+    if (B > 0 && (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params || !table || !lens))
+        return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(c->k_codes) || !aligned16(c->k_params) || !aligned16(c->v_codes) || !aligned16(c->v_params))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    *cache = Kv4Cache{static_cast<unsigned char*>(c->k_codes), static_cast<unsigned*>(c->k_params),
+                      static_cast<unsigned char*>(c->v_codes), static_cast<unsigned*>(c->v_params),
+                      c->n_pages, c->Hkv, c->d, c->d_v};
+    *batch = Kv4Batch{table, lens, cu, B, width, L, (int)total};
+    return ATTN_OK;
+}
+
+int check_stride(const char* what, long long stride, long long least) {
+    if (stride < least || stride % 8 != 0)
+        return fail(ATTN_ERR_ARG, "%s stride %lld must be a multiple of 8 of at least %lld elements", what, stride, least);
+    return ATTN_OK;
+}
+
+struct Kv4Workspace {
+    size_t ml, part, scores, total;
+};
+Kv4Workspace kv4_layout(int B, int H, int Hkv, long total, int width, int d, int dv, bool weights) {
+    const int nr = kv4_row_tiles(H / Hkv, B, (int)total, d, dv);
+    Kv4Workspace w{};
+    w.ml = align256(kv4_prefix_bytes());
+    w.part = w.ml + align256(kv4_ml_bytes(nr));
+    w.scores = w.part + align256(kv4_part_bytes(nr, dv));
+    w.total = w.scores + (weights ? align256((size_t)total * H * width * kPage * sizeof(float)) : 0);
+    return w;
+}
+
+}  // namespace
+
+extern "C" int attn_kv4_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                               const attn_kv4_cache* cache, const int* page_table, int table_width,
+                               const int* cache_lens, const int* cu_seqlens, int B, int L, cudaStream_t stream) {
+    Kv4Cache c;
+    Kv4Batch s;
+    int rc = check_kv4(cache, B, L, page_table, table_width, cache_lens, cu_seqlens, &c, &s);
+    if (rc) return rc;
+    if (B == 0 || s.total == 0) return ok();
+    if (!k || !v) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if ((rc = check_stride("k", k_stride, (long long)c.Hkv * c.d))) return rc;
+    if ((rc = check_stride("v", v_stride, (long long)c.Hkv * c.dv))) return rc;
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    const cudaError_t e = launch_kv4_append(c, s, static_cast<const __nv_bfloat16*>(k),
+                                            static_cast<const __nv_bfloat16*>(v), (long)k_stride, (long)v_stride,
+                                            di.status, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 append launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int attn_kv4_read(void* k, void* v, const attn_kv4_cache* cache, const int* page_table, int table_width,
+                             const int* cache_lens, const int* cu_seqlens, int B, int L, cudaStream_t stream) {
+    Kv4Cache c;
+    Kv4Batch s;
+    int rc = check_kv4(cache, B, L, page_table, table_width, cache_lens, cu_seqlens, &c, &s);
+    if (rc) return rc;
+    if (B == 0 || s.total == 0) return ok();
+    if (!k || !v) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    const cudaError_t e = launch_kv4_read(c, s, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v),
+                                          di.status, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 read launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" size_t attn_kv4_fwd_workspace_size(int B, int H, int Hkv, int L, int packed, int table_width, int d, int d_v,
+                                              int key_weights) {
+    if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || table_width < 1 || d <= 0 || d_v <= 0) return 0;
+    const long total = packed ? (long)L : (long)B * L;
+    if (total >= (1L << 31)) return 0;
+    return kv4_layout(B, H, Hkv, total, table_width, d, d_v, key_weights != 0).total;
+}
+
+extern "C" int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_cache* cache, const int* page_table,
+                            int table_width, const int* cache_lens, const int* cu_seqlens, void* o, float* lse, int B,
+                            int H, int L, float scale, int causal, int window_left, int window_right, int sinks,
+                            float* key_weights, long long weight_stride, float weight_decay, void* workspace,
+                            size_t ws_bytes, cudaStream_t stream) {
+    Kv4FwdParams p{};
+    int rc = check_kv4(cache, B, L, page_table, table_width, cache_lens, cu_seqlens, &p.c, &p.s);
+    if (rc) return rc;
+    if ((rc = check_heads(H, p.c.Hkv))) return rc;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_ARG, "scale must be finite and > 0");
+    if ((rc = check_window(window_left, window_right, sinks))) return rc;
+    if (key_weights && (weight_stride < 1 || !(weight_decay >= 0.f && weight_decay <= 1.f)))
+        return fail(ATTN_ERR_ARG, "key weights need a row length >= 1 and a decay in [0, 1]");
+    if (B == 0 || (p.s.total == 0 && !key_weights)) return ok();
+    const int group = H / p.c.Hkv;
+    const int nr = kv4_row_tiles(group, B, p.s.total, p.c.d, p.c.dv);
+    // the work list counts pages of row blocks in an int
+    const double units = ((double)p.s.total * group / (8 * nr) + B) * table_width * p.c.Hkv;
+    if (units >= 2.0e9) return fail(ATTN_ERR_ARG, "kv4: too many (row block, page) pairs");
+    if (p.s.total > 0 && (!q || !o || !lse)) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(key_weights))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if ((rc = check_stride("q", q_stride, (long long)H * p.c.d))) return rc;
+    const Kv4Workspace wl = kv4_layout(B, H, p.c.Hkv, p.s.total, table_width, p.c.d, p.c.dv, key_weights != nullptr);
+    if (!workspace || ws_bytes < wl.total)
+        return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total, ws_bytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    char* ws = static_cast<char*>(workspace);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.q_stride = (long)q_stride;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.key_weights = key_weights;
+    p.weight_stride = (long)weight_stride;
+    p.weight_decay = weight_decay;
+    p.H = H;
+    p.group = group;
+    // (bounds past any cache change nothing; clamped so the index arithmetic cannot overflow)
+    const int most = table_width * kPage > p.s.total ? table_width * kPage : p.s.total;
+    p.win_left = window_left < most ? window_left : most;
+    p.win_right = causal ? 0 : (window_right < most ? window_right : most);
+    p.sinks = window_left < 0 ? 0 : (sinks < most ? sinks : most);
+    p.scale_log2 = scale * kLog2e;
+    p.prefix = reinterpret_cast<int*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + wl.ml);
+    p.part_o = reinterpret_cast<float*>(ws + wl.part);
+    p.scores = key_weights ? reinterpret_cast<float*>(ws + wl.scores) : nullptr;
+    p.status = di.status;
+    p.wait_budget_ns = wait_budget_ns();
+    const cudaError_t e = launch_kv4_fwd(p, di.sms, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 forward launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int attn_kv4_evict(const attn_kv4_cache* cache, const int* page_table, int table_width, const int* cache_lens,
+                              const float* key_weights, long long weight_stride, const int* new_table, int new_width,
+                              int B, int budget, int sinks, int recent, int* new_lens, int* kept,
+                              float* new_key_weights, long long new_weight_stride, cudaStream_t stream) {
+    Kv4EvictParams p{};
+    Kv4Batch s;
+    int rc = check_kv4(cache, B, 0, page_table, table_width, cache_lens, nullptr, &p.c, &s);
+    if (rc) return rc;
+    if (budget < 1 || sinks < 0 || recent < 0 || (long)sinks + recent > budget)
+        return fail(ATTN_ERR_ARG, "kv4 evict: budget %d must hold the %d sinks and %d recent keys", budget, sinks, recent);
+    if (new_width < 1 || (long)new_width * kPage < budget)
+        return fail(ATTN_ERR_ARG, "kv4 evict: a new table of %d pages does not hold %d keys", new_width, budget);
+    if (weight_stride < 1 || new_weight_stride < budget)
+        return fail(ATTN_ERR_ARG, "kv4 evict: weight rows of %lld and %lld (at least the budget)", weight_stride,
+                    new_weight_stride);
+    if (B == 0) return ok();
+    if (!key_weights || !new_table || !new_lens || !kept || !new_key_weights)
+        return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (new_table == page_table || new_key_weights == key_weights || new_lens == cache_lens)
+        return fail(ATTN_ERR_ARG, "kv4 evict: the kept keys go to new pages, lengths and weights, not in place");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    p.table = page_table;
+    p.lens = cache_lens;
+    p.weights = key_weights;
+    p.new_table = new_table;
+    p.new_lens = new_lens;
+    p.kept = kept;
+    p.new_weights = new_key_weights;
+    p.weight_stride = (long)weight_stride;
+    p.new_stride = (long)new_weight_stride;
+    p.B = B;
+    p.width = table_width;
+    p.new_width = new_width;
+    p.budget = budget;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.status = di.status;
+    const cudaError_t e = launch_kv4_evict(p, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 evict launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
 extern "C" int attn_set_backward_cta_pairs(int enable) { return g_bwd_pairs.exchange(enable ? 1 : 0); }
 
 extern "C" int attn_set_exp2_emulation(int d, int every) {
@@ -593,6 +790,8 @@ extern "C" int attn_check_status(cudaStream_t stream) {
         cudaMemcpyToSymbol(g_attn_status, &zero, sizeof(int));
         if (st == kStatusMisaligned)
             return fail(ATTN_ERR_LAUNCH, "dynamic shared memory was not 1024-byte aligned");
+        if (st == kStatusBadPage)
+            return fail(ATTN_ERR_ARG, "4-bit cache: a page id, a cache length or a row offset was out of range");
         return fail(ATTN_ERR_TIMEOUT, "a kernel gave up waiting (status %d)", st);
     }
     return ok();

@@ -1,0 +1,786 @@
+// Attention of a few new tokens per sequence over the 4-bit key/value cache.
+//
+// Mathematics. A code c of key j, channel group g stands for a_jg c + b_jg, so
+//   s_ij = scale * sum_g ( a_jg <q_ig, c_jg> + b_jg sum(q_ig) )
+//   O_i  = sum_j p_ij v_j,   v_j = a'_jg c'_jg + b'_jg:
+// the products run on the 4-bit codes themselves and the parameters enter as one
+// factor per (key, group) in fp32 (scores) or fold into P (values); nothing is
+// dequantised element by element.
+//
+// What bounds it: the cache is read once (4.5 bits per element) by 152 SMs at
+// HBM speed, about 45 bytes per ns and SM, i.e. 80 codes per ns to turn into
+// MMA operands. So the layout of the products is chosen for cheap operands and
+// small row counts: keys (channels for PV) take the M side and the query rows
+// the N side of mma.sync m16n8k16,
+//   S^T[key, row] = codes[key, ch] q^T[ch, row],
+//   O^T[ch, row] += codes^T[ch, key] P^T[key, row],
+// which pads rows to 8 instead of 16 (64 or 128 for a tcgen05 tile, whose
+// operands would also have to pass through shared memory again as 16-bit
+// values: more shared-memory traffic than the cache itself). A code becomes an
+// fp16 operand by one AND: the bits 0-3 (4-7) of a half are the subnormal
+// c 2^-24 (c 2^-20), which the tensor cores take exactly; the powers of two go
+// into q and the epilogue. Two codes per AND, one shift per eight.
+//
+// P^T: the accumulator tile of S^T (row = key) is transposed in registers by
+// movmatrix; before that p is multiplied by a'_jg. That product is rounded to
+// fp16 (11 bits), scaled by a power of two per group that follows the largest
+// a' seen, so that p a' keeps full precision 2^-19 below it. Scores, statistics
+// and accumulators are fp32; q is rounded to fp16 after scaling its row to
+// 2^14 .. 2^15, which keeps all 8 bits of every bf16 element down to 2^-28 of
+// the row's largest.
+//
+// Work: a unit is one page of one (sequence, key/value head, row block); all
+// units form one list, cut into equal ranges for the CTAs (long and short
+// caches balance, one long cache uses every SM). A row block that lies in one
+// CTA's range is finished there; others leave (max, sum, O) in the workspace
+// for the combining kernel. Within a CTA, warp 4 loads pages through a ring of
+// stages by bulk copies and each of warps 0-3 takes 16 of the 64 tokens with
+// softmax statistics of its own, so nothing but the ring synchronises; the four
+// are merged at the end of a row block.
+#include <cuda_fp16.h>
+
+#include "kv4.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4;                        // compute warps
+constexpr int kKv4Threads = 32 * (kWarps + 1);   // and the loader
+constexpr float kKv4Tau = 8.f;                   // a row's max moves when it grows by more (log2 units)
+constexpr float kWTarget = 32.f;                 // the largest a' of a group is scaled to [16, 32)
+constexpr float kWMost = 128.f;                  // ... and rescaled past this: p a' <= 2^8 * 2^7 in fp16
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void lds64(uint32_t a, uint32_t& x, uint32_t& y) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// Every lane waits for the phase itself, so that each sees the data it guards.
+__device__ __forceinline__ bool lanes_wait(uint32_t bar, uint32_t parity, const WaitCtx& w) {
+    return __all_sync(kFullMask, mbar_wait(bar, parity, w));
+}
+// 2^e for an unbiased exponent in the normal range
+__device__ __forceinline__ float pow2(int e) {
+    return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
+}
+
+template <int D, int DV, int NR>
+struct Kv4Layout {
+    static constexpr int kRows = 8 * NR;
+    static constexpr int kKC = D * kPage / 2, kVC = DV * kPage / 2;                          // codes of a page and head
+    static constexpr int kKP = D / kKv4Group * kPage * 4, kVP = DV / kKv4Group * kPage * 4;   // parameters
+    static constexpr int kStage = kKC + kVC + kKP + kVP;
+    static constexpr int kMerge = kWarps * kRows * DV * 4;   // the four warps' O rows
+    // two CTAs per SM at least, each with 4 stages (18 - 74 KB in flight)
+    static constexpr int kStages = 4;
+    static constexpr int kMergeOff = kStages * kStage;
+    static constexpr int kMlOff = kMergeOff + kMerge;             // (max, sum) per warp and row
+    static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
+    static constexpr int kFlagOff = kBarOff + 2 * kStages * 8;    // per stage: the page is valid
+    static constexpr int kAbortOff = kFlagOff + kStages * 4;
+    static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
+    static constexpr int kSmem = kPrefixOff + (kKv4MaxBatch + 1) * 4;
+    static constexpr int kRegCtas = NR * DV <= 64 ? 4 : (NR * DV <= 128 ? 3 : (NR * DV <= 256 ? 2 : 1));
+    static constexpr int kSmemCtas = 227 * 1024 / (kSmem + 1024);
+    static constexpr int kCtas = kRegCtas < kSmemCtas ? kRegCtas : kSmemCtas;
+    static_assert(kCtas >= 1, "shared memory budget");
+};
+
+// A sequence's work: pages 0 .. n_sink - 1, then first .. (the window), `pages` in
+// all, for each of `blocks` row blocks of each key/value head.
+struct SeqWork {
+    Kv4Seq s;
+    int rows, blocks, first, n_sink, pages;
+};
+__device__ __forceinline__ SeqWork seq_work(const Kv4FwdParams& p, int b, int rows_per_block) {
+    SeqWork w;
+    w.s = kv4_seq(p.s, b);
+    w.rows = w.s.nq * p.group;
+    w.blocks = (w.rows + rows_per_block - 1) / rows_per_block;
+    const MaskBand m = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
+    int hi;
+    if (band_key_blocks(m, 0, w.s.nq - 1, kPage, &w.first, &hi)) {
+        w.n_sink = band_sink_blocks(m, kPage, w.first);
+        w.pages = w.n_sink + hi - w.first;
+    } else {
+        w.n_sink = w.pages = 0;
+    }
+    return w;
+}
+__device__ __forceinline__ int page_of(const SeqWork& w, int i) { return i < w.n_sink ? i : w.first + i - w.n_sink; }
+
+// The units of all sequences as a prefix sum in shared memory (every thread of
+// the CTA calls); returns the units of one CTA.
+template <int kThreads>
+__device__ __forceinline__ int build_prefix(const Kv4FwdParams& p, int* prefix, int rows_per_block, int ctas) {
+    for (int b = threadIdx.x; b < p.s.B; b += kThreads) {
+        const SeqWork w = seq_work(p, b, rows_per_block);
+        if (w.s.bad && blockIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusBadPage);
+        prefix[b + 1] = p.c.Hkv * w.blocks * w.pages;
+    }
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int carry = 0;
+        for (int b0 = 0; b0 < p.s.B; b0 += 32) {
+            const int b = b0 + threadIdx.x;
+            int x = b < p.s.B ? prefix[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFullMask, x, o);
+                if ((int)threadIdx.x >= o) x += y;
+            }
+            if (b < p.s.B) prefix[b + 1] = carry + x;
+            carry += __shfl_sync(kFullMask, x, 31);
+        }
+    }
+    __syncthreads();
+    return (prefix[p.s.B] + ctas - 1) / ctas;
+}
+
+// Unit u: sequence, head, row block and page index within the row block.
+struct Unit {
+    int b, h, rb, i;
+};
+__device__ __forceinline__ Unit unit_at(const Kv4FwdParams& p, const int* prefix, int u, int rows_per_block, SeqWork* w) {
+    int lo = 0, hi = p.s.B - 1;   // the last b with prefix[b] <= u (and units of its own)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    *w = seq_work(p, lo, rows_per_block);
+    Unit r;
+    r.b = lo;
+    const int rem = u - prefix[lo], per_head = w->blocks * w->pages;
+    r.h = rem / per_head;
+    const int x = rem - r.h * per_head;
+    r.rb = x / w->pages;
+    r.i = x - r.rb * w->pages;
+    return r;
+}
+
+template <int D, int DV, int NR>
+__global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_fwd_kernel(const Kv4FwdParams p) {
+    using Lay = Kv4Layout<D, DV, NR>;
+    constexpr int GK = D / kKv4Group, GV = DV / kKv4Group, S = Lay::kStages, kRows = Lay::kRows;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* prefix = reinterpret_cast<int*>(smem + Lay::kPrefixOff);
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + Lay::kFlagOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbortOff);
+    auto full = [&](uint32_t s) { return base + Lay::kBarOff + 8u * s; };
+    auto empty = [&](uint32_t s) { return base + Lay::kBarOff + 8u * (S + s); };
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kWarps);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    const int per = build_prefix<kKv4Threads>(p, prefix, kRows, gridDim.x);   // (ends with __syncthreads)
+    const int total = prefix[p.s.B];
+    if (blockIdx.x == 0) {   // for the kernels that follow
+        for (int i = tid; i <= p.s.B; i += kKv4Threads) p.prefix[i] = prefix[i];
+        if (tid == 0) p.prefix[kKv4MaxBatch + 1] = per;
+    }
+    const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
+    const WaitCtx wc{abort_flag, p.status, p.wait_budget_ns};
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ loader
+        uint32_t cnt = 0;
+        bool ok = true;
+        for (int v0 = u0; v0 < u1 && ok; v0 += 32) {
+            const int u = v0 + lane;
+            int page = -1, h = 0;
+            if (u < u1) {   // each lane looks one unit's page up
+                SeqWork w;
+                const Unit t = unit_at(p, prefix, u, kRows, &w);
+                h = t.h;
+                page = p.s.table[(long)t.b * p.s.width + page_of(w, t.i)];
+                if (page < 0 || page >= p.c.n_pages) {
+                    page = -1;
+                    atomicCAS(p.status, kStatusOk, kStatusBadPage);
+                }
+            }
+            for (int i = 0; i < 32 && v0 + i < u1; ++i, ++cnt) {
+                const int pg = __shfl_sync(kFullMask, page, i), hh = __shfl_sync(kFullMask, h, i);
+                const uint32_t s = cnt % S;
+                ok = lanes_wait(empty(s), ((cnt / S) & 1u) ^ 1u, wc);
+                if (!ok) break;
+                if (lane == 0) {
+                    flags[s] = pg >= 0;
+                    if (pg >= 0) {
+                        const uint32_t dst = base + s * Lay::kStage;
+                        const long ph = (long)pg * p.c.Hkv + hh;
+                        mbar_expect_tx(full(s), Lay::kStage);
+                        bulk_load(dst, p.c.k_codes + ph * Lay::kKC, Lay::kKC, full(s));
+                        bulk_load(dst + Lay::kKC, p.c.v_codes + ph * Lay::kVC, Lay::kVC, full(s));
+                        bulk_load(dst + Lay::kKC + Lay::kVC, p.c.k_params + ph * (Lay::kKP / 4), Lay::kKP, full(s));
+                        bulk_load(dst + Lay::kKC + Lay::kVC + Lay::kKP, p.c.v_params + ph * (Lay::kVP / 4), Lay::kVP,
+                                  full(s));
+                    } else {
+                        mbar_arrive(full(s));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0)   // issued copies land before the CTA can exit
+            for (uint32_t i = 0; i < (uint32_t)S && i < cnt; ++i) {
+                const uint32_t n = cnt - 1 - i;
+                drain_wait(full(n % S), (n / S) & 1u, p.wait_budget_ns);
+            }
+        return;
+    }
+
+    // ---------------------------------------------------------------- compute warps
+    const int g8 = lane >> 2, t4 = lane & 3;
+    // S^T row r of this warp's 16 keys is token t + 4 e + 8 h (r = 2 t + e + 8 h): then the
+    // V words of a lane (rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of P^T) lie 4 tokens apart
+    // and a warp's 32-bit loads hit 32 banks.
+    const int tok0 = warp * 16 + (g8 >> 1) + 4 * (g8 & 1);   // this lane's keys: tok0 and tok0 + 8
+    float acc[GV * 4][NR][4];
+    uint32_t qf[NR][GK][8];
+    float qsum[NR][2][GK], qscale[NR][2], m_run[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
+    int klo[NR][2], khi[NR][2];
+    float* merge = reinterpret_cast<float*>(smem + Lay::kMergeOff);
+    float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
+    uint32_t cnt = 0;
+    Unit t{0, 0, 0, 0};
+    SeqWork w;
+    int full_lo = 0, full_hi = 0, item0 = 0;   // keys every row sees; the row block's first unit
+    bool fresh = true, ok = true;
+    for (int u = u0; u < u1; ++u) {
+        if (fresh) {
+            // ------------------------------------------------ the row block's queries
+            t = unit_at(p, prefix, u, kRows, &w);
+            item0 = u - t.i;
+            const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
+            full_lo = 0;
+            full_hi = w.s.lk;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const int r = t.rb * kRows + n * 8 + g8;   // this lane loads row r's channels 16 t4 .. of each group
+                const bool live = r < w.rows;
+                uint4 raw[GK][2];
+                const __nv_bfloat16* src = p.q + (long)(w.s.q0 + (live ? r / p.group : 0)) * p.q_stride +
+                                           (long)(t.h * p.group + (live ? r % p.group : 0)) * D + 16 * t4;
+                float top = 0.f;
+#pragma unroll
+                for (int g = 0; g < GK; ++g)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        raw[g][x] = live ? *reinterpret_cast<const uint4*>(src + g * kKv4Group + 8 * x) : make_uint4(0, 0, 0, 0);
+                        const uint32_t ws[4] = {raw[g][x].x, raw[g][x].y, raw[g][x].z, raw[g][x].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(ws[i])), fabsf(hi_bf16(ws[i]))));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+                // the row times 2^e has its largest element in [2^14, 2^15)
+                // (both powers stay in the float range)
+                const int e = top > 0.f && top < INFINITY ? min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 126) : 0;
+                const float f = pow2(e);
+                float part[GK];
+#pragma unroll
+                for (int g = 0; g < GK; ++g) {
+                    part[g] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t ws[4] = {raw[g][x].x, raw[g][x].y, raw[g][x].z, raw[g][x].w};
+                        float c[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            c[2 * i] = lo_bf16(ws[i]);
+                            c[2 * i + 1] = hi_bf16(ws[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) part[g] += c[i];
+                        // word x holds channels 8 x .. 8 x + 7; step 2 x takes (0, 4) and (1, 5), step 2 x + 1 (2, 6) and (3, 7);
+                        // odd nibbles read 16 times too large
+                        qf[n][g][4 * x + 0] = pack_f16x2(c[0] * f, c[4] * f);
+                        qf[n][g][4 * x + 1] = pack_f16x2(c[1] * f * 0.0625f, c[5] * f * 0.0625f);
+                        qf[n][g][4 * x + 2] = pack_f16x2(c[2] * f, c[6] * f);
+                        qf[n][g][4 * x + 3] = pack_f16x2(c[3] * f * 0.0625f, c[7] * f * 0.0625f);
+                    }
+                    part[g] += __shfl_xor_sync(kFullMask, part[g], 1);
+                    part[g] += __shfl_xor_sync(kFullMask, part[g], 2);
+                }
+                // accumulator columns 2 t4, 2 t4 + 1 are rows 8 n + 2 t4 (+ 1): their statistics live in lanes 4 (2 t4 (+ 1))
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int from = 4 * (2 * t4 + c);
+                    const int ec = __shfl_sync(kFullMask, e, from);
+                    qscale[n][c] = p.scale_log2 * pow2(24 - ec);
+#pragma unroll
+                    for (int g = 0; g < GK; ++g) qsum[n][c][g] = p.scale_log2 * __shfl_sync(kFullMask, part[g], from);
+                    const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
+                    const int i = row / p.group;
+                    klo[n][c] = row < w.rows ? band_key_lo(mb, i) : 0;
+                    khi[n][c] = row < w.rows ? band_key_hi(mb, i) : 0;
+                    m_run[n][c] = -INFINITY;
+                    l_run[n][c] = 0.f;
+#pragma unroll
+                    for (int g = 0; g < GV; ++g) zb[n][c][g] = 0.f;
+                }
+            }
+            {   // keys that the block's first and last rows (hence all) see
+                const int r0 = t.rb * kRows, r1 = min(w.rows, r0 + kRows) - 1;
+                full_lo = band_key_lo(mb, r1 / p.group);
+                full_hi = band_key_hi(mb, r0 / p.group);
+            }
+#pragma unroll
+            for (int g = 0; g < GV; ++g) wsc[g] = INFINITY;
+#pragma unroll
+            for (int j = 0; j < GV * 4; ++j)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[j][n][x] = 0.f;
+            fresh = false;
+        }
+        // ---------------------------------------------------- one page
+        const uint32_t s = cnt % S;
+        // (after a wait that ran out the pages count as invalid: the warp goes on to the
+        // barriers that the other warps wait at)
+        if (ok) ok = lanes_wait(full(s), (cnt / S) & 1u, wc);
+        ++cnt;
+        const uint32_t st = base + s * Lay::kStage;
+        const bool valid = ok && flags[s] != 0;
+        const int page = page_of(w, t.i), key0 = page * kPage;
+        const bool whole = valid && key0 >= full_lo && key0 + kPage <= full_hi;
+        float sc[NR][4];   // scores: [key tok0, tok0 + 8][row 2 t4, 2 t4 + 1] at 2 * key + row
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[n][x] = 0.f;
+        if (valid) {
+#pragma unroll
+            for (int g = 0; g < GK; ++g) {
+                const uint32_t row = st + g * (kPage * 32) + tok0 * 32 + 8 * t4;
+                uint32_t wa[2], wb[2];
+                lds64(row, wa[0], wa[1]);
+                lds64(row + 8 * 32, wb[0], wb[1]);
+                const uint32_t par = st + Lay::kKC + Lay::kVC + g * (kPage * 4) + tok0 * 4;
+                const uint32_t pa = lds32(par), pb = lds32(par + 32);
+                float d[NR][4];
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) d[n][x] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t xa = (k & 1) ? wa[k >> 1] >> 8 : wa[k >> 1], xb = (k & 1) ? wb[k >> 1] >> 8 : wb[k >> 1];
+                    const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma_f16(d[n], a0, a1, a2, a3, qf[n][g][2 * k], qf[n][g][2 * k + 1]);
+                }
+                const float aa = lo_bf16(pa), ba = hi_bf16(pa), ab = lo_bf16(pb), bb = hi_bf16(pb);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        sc[n][c] = fmaf(d[n][c] * qscale[n][c], aa, fmaf(qsum[n][c][g], ba, sc[n][c]));
+                        sc[n][2 + c] = fmaf(d[n][2 + c] * qscale[n][c], ab, fmaf(qsum[n][c][g], bb, sc[n][2 + c]));
+                    }
+            }
+        }
+        if (!whole) {
+            const int ja = key0 + tok0, jb = ja + 8;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int hi = valid ? khi[n][c] : 0;
+                    if (!(ja < hi && (ja >= klo[n][c] || ja < p.sinks))) sc[n][c] = -INFINITY;
+                    if (!(jb < hi && (jb >= klo[n][c] || jb < p.sinks))) sc[n][2 + c] = -INFINITY;
+                }
+        }
+        if (p.scores) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
+                    if (row < w.rows) {
+                        float* dst = p.scores + ((long)(w.s.q0 + row / p.group) * p.H + t.h * p.group + row % p.group) *
+                                                    ((long)p.s.width * kPage) + key0 + tok0;
+                        dst[0] = sc[n][c];
+                        dst[8] = sc[n][2 + c];
+                    }
+                }
+        }
+        // ---------------------------------------------------- running maximum
+        bool grow = false;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) grow |= fmaxf(sc[n][c], sc[n][2 + c]) > m_run[n][c] + kKv4Tau;
+        if (__any_sync(kFullMask, grow)) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float al[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(sc[n][c], sc[n][2 + c]);
+                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
+                    const float m_new = fmaxf(m_run[n][c], mx);
+                    al[c] = m_new == -INFINITY ? 1.f : ex2_mufu(m_run[n][c] - m_new);
+                    m_run[n][c] = m_new;
+                    l_run[n][c] *= al[c];
+#pragma unroll
+                    for (int g = 0; g < GV; ++g) zb[n][c][g] *= al[c];
+                }
+#pragma unroll
+                for (int j = 0; j < GV * 4; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[j][n][x] *= al[x & 1];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float m = m_run[n][c] == -INFINITY ? 0.f : m_run[n][c];
+                sc[n][c] = ex2_mufu(sc[n][c] - m);
+                sc[n][2 + c] = ex2_mufu(sc[n][2 + c] - m);
+                l_run[n][c] += sc[n][c] + sc[n][2 + c];
+            }
+        // ---------------------------------------------------- values
+        if (valid) {
+#pragma unroll
+            for (int g = 0; g < GV; ++g) {
+                const uint32_t par = st + Lay::kKC + Lay::kVC + Lay::kKP + g * (kPage * 4) + tok0 * 4;
+                const uint32_t pa = lds32(par), pb = lds32(par + 32);
+                const float va = lo_bf16(pa), ba = hi_bf16(pa), vb = lo_bf16(pb), bb = hi_bf16(pb);
+                bool big = !(fabsf(va) * wsc[g] <= kWMost) || !(fabsf(vb) * wsc[g] <= kWMost);
+                if (!whole) {   // keys that no row sees do not count (their parameters may hold anything)
+                    bool sa = false, sb = false;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            sa |= sc[n][c] > 0.f;
+                            sb |= sc[n][2 + c] > 0.f;
+                        }
+                    big = (sa && !(fabsf(va) * wsc[g] <= kWMost)) || (sb && !(fabsf(vb) * wsc[g] <= kWMost)) ||
+                          wsc[g] == INFINITY;
+                }
+                if (__any_sync(kFullMask, big)) {
+                    // a new power of two for the group; infinities and NaN do not set it
+                    bool sa = whole, sb = whole;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            sa |= sc[n][c] > 0.f;
+                            sb |= sc[n][2 + c] > 0.f;
+                        }
+                    float top = fmaxf(sa && fabsf(va) < INFINITY ? fabsf(va) : 0.f, sb && fabsf(vb) < INFINITY ? fabsf(vb) : 0.f);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+                    const bool first = wsc[g] == INFINITY;
+                    const float now = top > 0.f ? kWTarget * pow2(127 - (int)(__float_as_uint(top) >> 23) - 1) : INFINITY;
+                    if (first || now < wsc[g]) {
+                        const float f = first ? 1.f : now / wsc[g];
+                        wsc[g] = now;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) acc[4 * g + j][n][x] *= f;
+                    }
+                }
+                const float ws = wsc[g] == INFINITY ? 1.f : wsc[g];
+                const float fa = va * ws, fb = vb * ws;
+                uint32_t b0[NR], b1[NR];
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    float x[4] = {sc[n][0] * fa, sc[n][1] * fa, sc[n][2] * fb, sc[n][3] * fb};
+                    float z[4] = {sc[n][0] * ba, sc[n][1] * ba, sc[n][2] * bb, sc[n][3] * bb};
+                    if (!whole) {   // p = 0 times an infinity or a NaN of a masked key stays 0
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(sc[n][i] != 0.f)) x[i] = z[i] = 0.f;
+                    }
+                    zb[n][0][g] += z[0] + z[2];
+                    zb[n][1][g] += z[1] + z[3];
+                    b0[n] = transpose8x8(pack_f16x2(x[0], x[1]));
+                    b1[n] = transpose8x8(pack_f16x2(x[2], x[3]));
+                }
+                const uint32_t row = st + Lay::kKC + g * (kPage * 32) + (warp * 16 + t4) * 32 + 4 * g8;
+                const uint32_t w0 = lds32(row), w1 = lds32(row + 4 * 32), w2 = lds32(row + 8 * 32), w3 = lds32(row + 12 * 32);
+                // channels 8 g8 + 2 j (accumulator rows g8) and + 1 (rows g8 + 8, 16 times too large) of the group
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t sel = j < 2 ? 0x5410u : 0x7632u;
+                    uint32_t xa = __byte_perm(w0, w1, sel), xb = __byte_perm(w2, w3, sel);
+                    if (j & 1) {
+                        xa >>= 8;
+                        xb >>= 8;
+                    }
+                    const uint32_t a0 = xa & 0x000f000fu, a1 = xa & 0x00f000f0u, a2 = xb & 0x000f000fu, a3 = xb & 0x00f000f0u;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma_f16(acc[4 * g + j][n], a0, a1, a2, a3, b0[n], b1[n]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(s));
+        ++t.i;
+        if (t.i < w.pages && u + 1 < u1) continue;
+        // ---------------------------------------------------- the row block ends here (or this CTA's share of it)
+        const bool ends = t.i == w.pages, starts = item0 >= u0;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[n][c];
+                l += __shfl_xor_sync(kFullMask, l, 4);
+                l += __shfl_xor_sync(kFullMask, l, 8);
+                l += __shfl_xor_sync(kFullMask, l, 16);
+                const int row = n * 8 + 2 * t4 + c;
+                if (g8 == 0) ml[warp * kRows + row] = make_float2(m_run[n][c], l);
+#pragma unroll
+                for (int g = 0; g < GV; ++g) {
+                    float z = zb[n][c][g];
+                    z += __shfl_xor_sync(kFullMask, z, 4);
+                    z += __shfl_xor_sync(kFullMask, z, 8);
+                    z += __shfl_xor_sync(kFullMask, z, 16);
+                    const float inv = wsc[g] == INFINITY ? 1.f : 1.f / wsc[g];   // (a power of two)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 o = make_float2(fmaf(acc[4 * g + j][n][c], inv * 16777216.f, z),
+                                                     fmaf(acc[4 * g + j][n][2 + c], inv * 1048576.f, z));
+                        *reinterpret_cast<float2*>(merge + ((long)warp * kRows + row) * DV + g * kKv4Group + 8 * g8 + 2 * j) = o;
+                    }
+                }
+            }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        {
+            const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+            for (int i = tid; i < kRows * (DV / 4); i += 32 * kWarps) {
+                const int row = i / (DV / 4), c4 = i % (DV / 4);
+                const int r = t.rb * kRows + row;
+                float m = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * kRows + row].x);
+                float l = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) {
+                    const float2 v = ml[x * kRows + row];
+                    const float f = v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m);
+                    l += v.y * f;
+                    if (f != 0.f) {
+                        const float4 y = *reinterpret_cast<const float4*>(merge + ((long)x * kRows + row) * DV + 4 * c4);
+                        o.x = fmaf(f, y.x, o.x);
+                        o.y = fmaf(f, y.y, o.y);
+                        o.z = fmaf(f, y.z, o.z);
+                        o.w = fmaf(f, y.w, o.w);
+                    }
+                }
+                if (starts && ends) {
+                    if (r >= w.rows) continue;
+                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (NaN stays)
+                    const long tok = w.s.q0 + r / p.group;
+                    const int head = t.h * p.group + r % p.group;
+                    uint2 out;
+                    out.x = pack_bf16x2(o.x * inv, o.y * inv);
+                    out.y = pack_bf16x2(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2*>(p.o + (tok * p.H + head) * DV + 4 * c4) = out;
+                    if (c4 == 0) {
+                        float* dst = p.s.cu ? p.lse + (long)head * p.s.total + tok
+                                            : p.lse + ((long)t.b * p.H + head) * p.s.rows + r / p.group;
+                        *dst = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    }
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + ((long)slot * kRows + row) * DV + 4 * c4) = o;
+                    if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)slot * kRows + row) * 2) = make_float2(m, l);
+                }
+            }
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        fresh = true;
+    }
+}
+
+// One warp per (token, head) whose row block several CTAs shared: their partial
+// rows in CTA order (the same sum on every run). Rows that no key reaches get
+// O = 0, LSE = -inf here.
+__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4FwdParams p, int rows_per_block) {
+    const int lane = threadIdx.x & 31;
+    const long row = ((long)blockIdx.x * blockDim.x + threadIdx.x) / 32;
+    if (row >= (long)p.s.total * p.H) return;
+    const int tok = (int)(row / p.H), head = (int)(row % p.H);
+    const int b = kv4_seq_of_row(p.s, tok);
+    if (b < 0) return;
+    const SeqWork w = seq_work(p, b, rows_per_block);
+    if (w.s.bad) return;
+    const int i = tok - w.s.q0, r = i * p.group + head % p.group, h = head / p.group;
+    const int per = p.prefix[kKv4MaxBatch + 1];
+    const int dv = p.c.dv;
+    float* lse = p.s.cu ? p.lse + (long)head * p.s.total + tok : p.lse + ((long)b * p.H + head) * p.s.rows + i;
+    __nv_bfloat16* out = p.o + ((long)tok * p.H + head) * dv;
+    if (w.pages == 0) {
+        for (int c = lane * 4; c < dv; c += 128) *reinterpret_cast<uint2*>(out + c) = make_uint2(0, 0);
+        if (lane == 0) *lse = -INFINITY;
+        return;
+    }
+    const int u = p.prefix[b] + (h * w.blocks + r / rows_per_block) * w.pages;
+    const int c0 = u / per, c1 = (u + w.pages - 1) / per;
+    if (c0 == c1) return;   // finished by its CTA
+    const int in_block = r % rows_per_block;
+    auto slot_row = [&](int c) { return (long)(2 * c + (c == c0 ? 1 : 0)) * rows_per_block + in_block; };
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[2 * slot_row(c)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+    float l = 0.f;
+    float4 o[2] = {};
+    for (int b0 = c0; b0 <= c1; b0 += 32) {
+        const int c = b0 + lane;
+        float f = 0.f;
+        if (c <= c1) {
+            const float2 v = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot_row(c));
+            f = v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m);
+            l += v.y * f;
+        }
+        for (int k = 0; k < 32 && b0 + k <= c1; ++k) {
+            const float fk = __shfl_sync(kFullMask, f, k);
+            if (fk == 0.f) continue;
+            const float* src = p.part_o + slot_row(b0 + k) * dv;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int col = x * 128 + lane * 4;
+                if (col < dv) {
+                    const float4 y = *reinterpret_cast<const float4*>(src + col);
+                    o[x].x = fmaf(fk, y.x, o[x].x);
+                    o[x].y = fmaf(fk, y.y, o[x].y);
+                    o[x].z = fmaf(fk, y.z, o[x].z);
+                    o[x].w = fmaf(fk, y.w, o[x].w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFullMask, l, x);
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int col = x * 128 + lane * 4;
+        if (col < dv)
+            *reinterpret_cast<uint2*>(out + col) =
+                make_uint2(pack_bf16x2(o[x].x * inv, o[x].y * inv), pack_bf16x2(o[x].z * inv, o[x].w * inv));
+    }
+    if (lane == 0) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// key_weights[b][h][j] = decay * key_weights + sum over the rows of the group of
+// exp(s - LSE), one thread per key, rows in order. Scores of pages that no row
+// block visited were not written and count as nothing.
+constexpr int kWeightThreads = 128;
+__global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4FwdParams p, int rows_per_block) {
+    const int b = blockIdx.z, h = blockIdx.y;
+    const SeqWork w = seq_work(p, b, rows_per_block);
+    const int j = blockIdx.x * kWeightThreads + threadIdx.x;
+    if (j == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
+    if (w.s.bad || j >= w.s.lk || j >= p.weight_stride) return;
+    const int page = j / kPage;
+    float sum = 0.f;
+    const bool seen = w.pages > 0 && (page < w.n_sink || (page >= w.first && page < w.first + w.pages - w.n_sink));
+    if (seen) {
+        const long row_len = (long)p.s.width * kPage;
+        for (int i = 0; i < w.s.nq; ++i)
+            for (int x = 0; x < p.group; ++x) {
+                const long tok = w.s.q0 + i;
+                const int head = h * p.group + x;
+                const float lse = p.s.cu ? p.lse[(long)head * p.s.total + tok] : p.lse[((long)b * p.H + head) * p.s.rows + i];
+                const float s = p.scores[(tok * p.H + head) * row_len + j];
+                if (s != -INFINITY) sum += ex2_mufu(s - lse * kLog2e);
+            }
+    }
+    float* dst = p.key_weights + ((long)b * p.c.Hkv + h) * p.weight_stride + j;
+    *dst = p.weight_decay == 0.f ? sum : fmaf(p.weight_decay, *dst, sum);
+}
+
+template <int D, int DV, int NR>
+cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
+    using Lay = Kv4Layout<D, DV, NR>;
+    auto kern = kv4_fwd_kernel<D, DV, NR>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
+    if (e != cudaSuccess) return e;
+    int grid = num_sms * Lay::kCtas;
+    if (grid > kKv4MaxCtas) grid = kKv4MaxCtas;
+    kern<<<grid, kKv4Threads, Lay::kSmem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long rows = (long)p.s.total * p.H;
+    if (rows > 0) {
+        kv4_combine_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p, Lay::kRows);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || !p.key_weights) return e;
+    const dim3 wg((p.s.width * kPage + kWeightThreads - 1) / kWeightThreads, p.c.Hkv, p.s.B);
+    kv4_weights_kernel<<<wg, kWeightThreads, 0, stream>>>(p, Lay::kRows);
+    return cudaGetLastError();
+}
+
+template <int D, int DV>
+cudaError_t launch_dims(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
+    switch (kv4_row_tiles(p.group, p.s.B, p.s.total, D, DV)) {
+        case 1: return launch_one<D, DV, 1>(p, num_sms, stream);
+        case 2: return launch_one<D, DV, 2>(p, num_sms, stream);
+        default:
+            if constexpr (D <= 128 && DV <= 128) return launch_one<D, DV, 4>(p, num_sms, stream);
+            return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
+    const int d = p.c.d, dv = p.c.dv;
+    if (d == 64 && dv == 64) return launch_dims<64, 64>(p, num_sms, stream);
+    if (d == 128 && dv == 128) return launch_dims<128, 128>(p, num_sms, stream);
+    if (d == 192 && dv == 192) return launch_dims<192, 192>(p, num_sms, stream);
+    if (d == 192 && dv == 128) return launch_dims<192, 128>(p, num_sms, stream);
+    if (d == 256 && dv == 256) return launch_dims<256, 256>(p, num_sms, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

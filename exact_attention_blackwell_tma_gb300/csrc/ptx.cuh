@@ -20,6 +20,7 @@ enum : int {
     kStatusOk = 0,
     kStatusWaitTimeout = 1,
     kStatusMisaligned = 2,    // dynamic shared memory not 1024-byte aligned
+    kStatusBadPage = 3,       // a page id, length or offset of a 4-bit cache call is out of range
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {

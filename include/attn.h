@@ -293,6 +293,111 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
                      const int* cu_seqlens, int deterministic, cudaStream_t stream);
 
 /*
+ * A paged key/value cache held in 4 bits, for serving: append new keys and
+ * values to it, attend to it, read it back, evict from it.
+ *
+ * Pages of 64 tokens. Within one page and key/value head the channels (d of K,
+ * d_v of V) form groups of 64; per token a group has 32 bytes of codes (channel
+ * 2i in the low half of byte i, 2i + 1 in the high half) and two bf16
+ * parameters, scale and minimum. A code c stands for scale * c + minimum.
+ *   k_codes  bytes [n_pages, Hkv, d / 64, 64, 32]    v_codes  [.., d_v / 64, ..]
+ *   k_params bf16  [n_pages, Hkv, d / 64, 64, 2]     v_params [.., d_v / 64, ..]
+ * (4.5 bits per element). Head dims as in attn_fwd_ex (d_v = d, or 192 with
+ * 128). All calls take B <= 1024 sequences with
+ *   page_table  int32 [B, table_width]: the page of tokens 64 p .. 64 p + 63;
+ *               entries past a sequence's last page are not read;
+ *   cache_lens  int32 [B]: cached tokens per sequence, the call's new tokens
+ *               included, at most 64 * table_width;
+ *   rows        packed (cu_seqlens: int32 [B + 1] row offsets, L = the packed row
+ *               count) or dense (cu_seqlens NULL, L rows per sequence). The n rows
+ *               of a sequence are the last n tokens of its cache: row t is token
+ *               cache_lens[b] - n + t. Rows past the last sequence are left as
+ *               they are. A sequence may have no rows.
+ * All on the device; pages may be shared by sequences as long as no call
+ * writes them. A page id, length or offset out of range touches no memory
+ * outside the cache: the keys of such a page do not count, and
+ * attn_check_status reports ATTN_ERR_ARG. Calls are asynchronous, allocate
+ * nothing and can be captured into a CUDA graph.
+ */
+typedef struct attn_kv4_cache {
+    void* k_codes;
+    void* k_params;
+    void* v_codes;
+    void* v_params;
+    int n_pages, Hkv, d, d_v;
+} attn_kv4_cache;
+
+/*
+ * Quantise the rows of k and v (bf16 [rows, Hkv, d] and [rows, Hkv, d_v], with
+ * k_stride and v_stride elements between rows, multiples of 8) into the cache.
+ * Per group of 64 channels: minimum = min x, scale = bf16((max x - min x) / 15),
+ * code = round((x - minimum) / scale) clamped to 0 .. 15, ties to even, decided
+ * exactly (0 where scale is 0). A group that holds a NaN or an infinity, or
+ * whose spread exceeds the fp32 range, reads back as NaN.
+ */
+int attn_kv4_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                    const attn_kv4_cache* cache, const int* page_table, int table_width, const int* cache_lens,
+                    const int* cu_seqlens, int B, int L, cudaStream_t stream);
+
+/*
+ * The inverse: write the values that the last rows of every sequence's cache
+ * stand for, in bf16, to k [rows, Hkv, d] and v [rows, Hkv, d_v] (for instance
+ * the whole cache, to run attn_fwd_ex over a long chunk). A dense row before a
+ * sequence's first token (L > cache_lens[b]) is written as zero.
+ */
+int attn_kv4_read(void* k, void* v, const attn_kv4_cache* cache, const int* page_table, int table_width,
+                  const int* cache_lens, const int* cu_seqlens, int B, int L, cudaStream_t stream);
+
+/*
+ * Attention of the rows of q (bf16 [rows, H, d], q_stride elements between
+ * rows, a multiple of 8) over their sequence's cache, new tokens included:
+ * o (bf16 [rows, H, d_v]) and lse (fp32 [B, H, L] dense, [H, L] packed) as
+ * defined at the top for keys and values with the values their codes stand
+ * for. Masks as in attn_fwd_sinks, aligned at the end of the cache; a row that
+ * sees no key gets O = 0, LSE = -inf. Meant for one to a few dozen rows of a
+ * group per sequence (decode, speculative tokens, short chunks): the cache is
+ * read once per 8, 16 or 32 (query, head of the group) rows. For long chunks
+ * use attn_kv4_read and attn_fwd_ex.
+ * key_weights (fp32 [B, Hkv, weight_stride], or NULL): for every cached key
+ *   key_weights = weight_decay * key_weights + sum over the call's rows and the
+ *   group's query heads of exp(s - LSE)
+ * (weight_decay in [0, 1]; 1 accumulates, 0 ignores the old contents). Entries
+ * past a sequence's length are left as they are; weight_stride must cover the
+ * longest cache. Sums are taken in a fixed order: results repeat bit for bit.
+ * workspace: attn_kv4_fwd_workspace_size(...) bytes, 256-byte aligned, used by
+ * one call at a time (calls or captured graphs that may overlap need one each);
+ * its contents need not be initialised.
+ */
+size_t attn_kv4_fwd_workspace_size(int B, int H, int Hkv, int L, int packed, int table_width, int d, int d_v,
+                                   int key_weights);
+int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_cache* cache, const int* page_table,
+                 int table_width, const int* cache_lens, const int* cu_seqlens, void* o, float* lse,
+                 int B, int H, int L, float scale, int causal, int window_left, int window_right, int sinks,
+                 float* key_weights, long long weight_stride, float weight_decay,
+                 void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Eviction by accumulated attention weight. Of each sequence longer than
+ * `budget`, every key/value head keeps its first `sinks` keys, its last `recent`
+ * keys and, of those between, the ones with the largest key_weights (fp32 [B,
+ * Hkv, weight_stride]; equal weights: the earlier key; NaN counts as the
+ * smallest), `budget` in all; shorter sequences keep every key. The kept keys
+ * and values move, in their order and bit for bit, to the pages of new_table
+ * (int32 [B, new_width], pages of the same cache that hold nothing of page_table;
+ * pages are per sequence, so each head has its own tokens in them). Written:
+ *   new_lens int32 [B], kept int32 [B, Hkv, budget] (the old token of each new
+ *   one, -1 past the new length), new_key_weights fp32 [B, Hkv,
+ *   new_weight_stride] (the kept weights, 0 past the new length;
+ *   new_weight_stride >= budget).
+ * Nothing is updated in place: page_table, cache_lens and key_weights stay as
+ * they are, so pages shared with other sequences are safe to evict from.
+ */
+int attn_kv4_evict(const attn_kv4_cache* cache, const int* page_table, int table_width, const int* cache_lens,
+                   const float* key_weights, long long weight_stride, const int* new_table, int new_width,
+                   int B, int budget, int sinks, int recent, int* new_lens, int* kept,
+                   float* new_key_weights, long long new_weight_stride, cudaStream_t stream);
+
+/*
  * Partial emulation of the forward's exponentials (FlashAttention-4 paper,
  * Section 3.1.3, "partial emulation"; FA4 blog, "关键实现技术"): for head dim d
  * (64 or 128), `every` = 8 or 4 computes one score-column pair in every 8 or 4
