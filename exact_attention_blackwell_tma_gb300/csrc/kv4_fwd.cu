@@ -96,28 +96,28 @@ struct Kv4Layout {
     static constexpr int kRows = 8 * NR;
     static constexpr int kKC = D * kPage / 2, kVC = DV * kPage / 2;                          // codes of a page and head
     static constexpr int kKP = D / kKv4Group * kPage * 4, kVP = DV / kKv4Group * kPage * 4;   // parameters
-    static constexpr int kStage = kKC + kVC + kKP + kVP;
+    static constexpr int kPageBytes = kKC + kVC + kKP + kVP;
+    static constexpr int kStage = 2 * kPageBytes;
     static constexpr int kMerge = kWarps * kRows * DV * 4;   // the four warps' O rows
-    // two CTAs per SM at least, each with 4 stages (18 - 74 KB in flight)
-    static constexpr int kStages = 4;
+    static constexpr int kStages = D + DV <= 256 ? 3 : 2;
     static constexpr int kMergeOff = kStages * kStage;
     static constexpr int kMlOff = kMergeOff + kMerge;             // (max, sum) per warp and row
     static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
-    static constexpr int kFlagOff = kBarOff + 2 * kStages * 8;    // per stage: the page is valid
-    static constexpr int kAbortOff = kFlagOff + kStages * 4;
+    static constexpr int kFlagOff = kBarOff + 2 * kStages * 8;    // per stage and page: 0 out of range, 1 loaded
+    static constexpr int kAbortOff = kFlagOff + kStages * 8;
     static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
-    static constexpr int kSmem = kPrefixOff + (kKv4MaxBatch + 1) * 4;
+    static constexpr int smem(int B) { return kPrefixOff + (B + 1) * 4; }
     static constexpr int kRegCtas = NR * DV <= 64 ? 4 : (NR * DV <= 128 ? 3 : (NR * DV <= 256 ? 2 : 1));
-    static constexpr int kSmemCtas = 227 * 1024 / (kSmem + 1024);
+    static constexpr int kSmemCtas = 227 * 1024 / (smem(64) + 1024);   // (with up to 64 sequences)
     static constexpr int kCtas = kRegCtas < kSmemCtas ? kRegCtas : kSmemCtas;
-    static_assert(kCtas >= 1, "shared memory budget");
+    static_assert(kCtas >= 1 && smem(kKv4MaxBatch) <= 227 * 1024, "shared memory budget");
 };
 
 // A sequence's work: pages 0 .. n_sink - 1, then first .. (the window), `pages` in
-// all, for each of `blocks` row blocks of each key/value head.
+// all, in units of two for each of `blocks` row blocks of each key/value head.
 struct SeqWork {
     Kv4Seq s;
-    int rows, blocks, first, n_sink, pages;
+    int rows, blocks, first, n_sink, pages, units;
 };
 __device__ __forceinline__ SeqWork seq_work(const Kv4FwdParams& p, int b, int rows_per_block) {
     SeqWork w;
@@ -132,6 +132,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4FwdParams& p, int b, int ro
     } else {
         w.n_sink = w.pages = 0;
     }
+    w.units = (w.pages + 1) / 2;
     return w;
 }
 __device__ __forceinline__ int page_of(const SeqWork& w, int i) { return i < w.n_sink ? i : w.first + i - w.n_sink; }
@@ -143,7 +144,7 @@ __device__ __forceinline__ int build_prefix(const Kv4FwdParams& p, int* prefix, 
     for (int b = threadIdx.x; b < p.s.B; b += kThreads) {
         const SeqWork w = seq_work(p, b, rows_per_block);
         if (w.s.bad && blockIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusBadPage);
-        prefix[b + 1] = p.c.Hkv * w.blocks * w.pages;
+        prefix[b + 1] = p.c.Hkv * w.blocks * w.units;
     }
     if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
@@ -165,7 +166,7 @@ __device__ __forceinline__ int build_prefix(const Kv4FwdParams& p, int* prefix, 
     return (prefix[p.s.B] + ctas - 1) / ctas;
 }
 
-// Unit u: sequence, head, row block and page index within the row block.
+// Unit u: sequence, head, row block and unit index within the row block.
 struct Unit {
     int b, h, rb, i;
 };
@@ -179,11 +180,11 @@ __device__ __forceinline__ Unit unit_at(const Kv4FwdParams& p, const int* prefix
     *w = seq_work(p, lo, rows_per_block);
     Unit r;
     r.b = lo;
-    const int rem = u - prefix[lo], per_head = w->blocks * w->pages;
+    const int rem = u - prefix[lo], per_head = w->blocks * w->units;
     r.h = rem / per_head;
     const int x = rem - r.h * per_head;
-    r.rb = x / w->pages;
-    r.i = x - r.rb * w->pages;
+    r.rb = x / w->units;
+    r.i = x - r.rb * w->units;
     return r;
 }
 
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbortOff);
     auto full = [&](uint32_t s) { return base + Lay::kBarOff + 8u * s; };
     auto empty = [&](uint32_t s) { return base + Lay::kBarOff + 8u * (S + s); };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the finishing kernel waits for this grid's end)
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     }
     const int per = build_prefix<kKv4Threads>(p, prefix, kRows, gridDim.x);   // (ends with __syncthreads)
     const int total = prefix[p.s.B];
-    if (blockIdx.x == 0) {   // for the kernels that follow
+    if (blockIdx.x == 0) {   // for the kernel that follows
         for (int i = tid; i <= p.s.B; i += kKv4Threads) p.prefix[i] = prefix[i];
         if (tid == 0) p.prefix[kKv4MaxBatch + 1] = per;
     }
@@ -220,37 +222,44 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         // ------------------------------------------------------------ loader
         uint32_t cnt = 0;
         bool ok = true;
-        for (int v0 = u0; v0 < u1 && ok; v0 += 32) {
-            const int u = v0 + lane;
-            int page = -1, h = 0;
-            if (u < u1) {   // each lane looks one unit's page up
+        for (int v0 = u0; v0 < u1 && ok; v0 += 16) {
+            const int u = v0 + (lane >> 1);
+            int page = -2, h = 0;   // -2: no such page, -1: out of range
+            if (u < u1) {   // each lane looks up one page of a unit
                 SeqWork w;
                 const Unit t = unit_at(p, prefix, u, kRows, &w);
                 h = t.h;
-                page = p.s.table[(long)t.b * p.s.width + page_of(w, t.i)];
-                if (page < 0 || page >= p.c.n_pages) {
-                    page = -1;
-                    atomicCAS(p.status, kStatusOk, kStatusBadPage);
+                const int i = 2 * t.i + (lane & 1);
+                if (i < w.pages) {
+                    page = p.s.table[(long)t.b * p.s.width + page_of(w, i)];
+                    if (page < 0 || page >= p.c.n_pages) {
+                        page = -1;
+                        atomicCAS(p.status, kStatusOk, kStatusBadPage);
+                    }
                 }
             }
-            for (int i = 0; i < 32 && v0 + i < u1; ++i, ++cnt) {
-                const int pg = __shfl_sync(kFullMask, page, i), hh = __shfl_sync(kFullMask, h, i);
+            for (int i = 0; i < 16 && v0 + i < u1; ++i, ++cnt) {
+                const int pg0 = __shfl_sync(kFullMask, page, 2 * i), pg1 = __shfl_sync(kFullMask, page, 2 * i + 1);
+                const int hh = __shfl_sync(kFullMask, h, 2 * i);
                 const uint32_t s = cnt % S;
                 ok = lanes_wait(empty(s), ((cnt / S) & 1u) ^ 1u, wc);
                 if (!ok) break;
                 if (lane == 0) {
-                    flags[s] = pg >= 0;
-                    if (pg >= 0) {
-                        const uint32_t dst = base + s * Lay::kStage;
+                    flags[2 * s] = pg0 >= 0;
+                    flags[2 * s + 1] = pg1 >= 0;
+                    const uint32_t bytes = (pg0 >= 0 ? Lay::kPageBytes : 0) + (pg1 >= 0 ? Lay::kPageBytes : 0);
+                    if (bytes) mbar_expect_tx(full(s), bytes);
+                    else mbar_arrive(full(s));
+                    for (int x = 0; x < 2; ++x) {
+                        const int pg = x ? pg1 : pg0;
+                        if (pg < 0) continue;
+                        const uint32_t dst = base + s * Lay::kStage + x * Lay::kPageBytes;
                         const long ph = (long)pg * p.c.Hkv + hh;
-                        mbar_expect_tx(full(s), Lay::kStage);
                         bulk_load(dst, p.c.k_codes + ph * Lay::kKC, Lay::kKC, full(s));
-                        bulk_load(dst + Lay::kKC, p.c.v_codes + ph * Lay::kVC, Lay::kVC, full(s));
                         bulk_load(dst + Lay::kKC + Lay::kVC, p.c.k_params + ph * (Lay::kKP / 4), Lay::kKP, full(s));
+                        bulk_load(dst + Lay::kKC, p.c.v_codes + ph * Lay::kVC, Lay::kVC, full(s));
                         bulk_load(dst + Lay::kKC + Lay::kVC + Lay::kKP, p.c.v_params + ph * (Lay::kVP / 4), Lay::kVP,
                                   full(s));
-                    } else {
-                        mbar_arrive(full(s));
                     }
                 }
                 __syncwarp();
@@ -266,20 +275,22 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 
     // ---------------------------------------------------------------- compute warps
     const int g8 = lane >> 2, t4 = lane & 3;
-    // S^T row r of this warp's 16 keys is token t + 4 e + 8 h (r = 2 t + e + 8 h): then the
-    // V words of a lane (rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of P^T) lie 4 tokens apart
-    // and a warp's 32-bit loads hit 32 banks.
-    const int tok0 = warp * 16 + (g8 >> 1) + 4 * (g8 & 1);   // this lane's keys: tok0 and tok0 + 8
+    // This warp's 32 tokens of the unit's page warp / 2, in two chunks of 16. S^T row r of a
+    // chunk is token t + 4 e + 8 h (r = 2 t + e + 8 h): then the V words of a lane (rows 2 t,
+    // 2 t + 1, 2 t + 8, 2 t + 9 of P^T) lie 4 tokens apart and a warp's 32-bit loads hit 32 banks.
+    const int tok_w = (warp & 1) * 32, tok0 = tok_w + (g8 >> 1) + 4 * (g8 & 1);   // keys tok0, + 8 (chunk 0), + 16, + 24
     float acc[GV * 4][NR][4];
     uint32_t qf[NR][GK][8];
-    float qsum[NR][2][GK], qscale[NR][2], m_run[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
+    float qsum[NR][2][GK], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV], qs = 0.f;
     int klo[NR][2], khi[NR][2];
     float* merge = reinterpret_cast<float*>(smem + Lay::kMergeOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
-    uint32_t cnt = 0;
+    uint32_t slot = 0, phase = 0;
     Unit t{0, 0, 0, 0};
     SeqWork w;
     int full_lo = 0, full_hi = 0, item0 = 0;   // keys every row sees; the row block's first unit
+    float* score_at = nullptr;                 // the scores of row 2 t4, key tok0 of the cache
+    const long row_len = (long)p.s.width * kPage;
     bool fresh = true, ok = true;
     for (int u = u0; u < u1; ++u) {
         if (fresh) {
@@ -287,38 +298,39 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             t = unit_at(p, prefix, u, kRows, &w);
             item0 = u - t.i;
             const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
-            full_lo = 0;
-            full_hi = w.s.lk;
+            uint4 raw[NR][GK][2];
+            float top = 0.f;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const int r = t.rb * kRows + n * 8 + g8;   // this lane loads row r's channels 16 t4 .. of each group
                 const bool live = r < w.rows;
-                uint4 raw[GK][2];
                 const __nv_bfloat16* src = p.q + (long)(w.s.q0 + (live ? r / p.group : 0)) * p.q_stride +
                                            (long)(t.h * p.group + (live ? r % p.group : 0)) * D + 16 * t4;
-                float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < GK; ++g)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        raw[g][x] = live ? *reinterpret_cast<const uint4*>(src + g * kKv4Group + 8 * x) : make_uint4(0, 0, 0, 0);
-                        const uint32_t ws[4] = {raw[g][x].x, raw[g][x].y, raw[g][x].z, raw[g][x].w};
+                        raw[n][g][x] = live ? *reinterpret_cast<const uint4*>(src + g * kKv4Group + 8 * x) : make_uint4(0, 0, 0, 0);
+                        const uint32_t ws[4] = {raw[n][g][x].x, raw[n][g][x].y, raw[n][g][x].z, raw[n][g][x].w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(ws[i])), fabsf(hi_bf16(ws[i]))));
                     }
-                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-                // the row times 2^e has its largest element in [2^14, 2^15)
-                // (both powers stay in the float range)
-                const int e = top > 0.f && top < INFINITY ? min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 126) : 0;
-                const float f = pow2(e);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            // the block's rows times 2^e have their largest element in [2^14, 2^15) (both powers stay in the float range)
+            const int e = top > 0.f && top < INFINITY ? min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 126) : 0;
+            const float f = pow2(e);
+            qs = p.scale_log2 * pow2(24 - e);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
                 float part[GK];
 #pragma unroll
                 for (int g = 0; g < GK; ++g) {
                     part[g] = 0.f;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint32_t ws[4] = {raw[g][x].x, raw[g][x].y, raw[g][x].z, raw[g][x].w};
+                        const uint32_t ws[4] = {raw[n][g][x].x, raw[n][g][x].y, raw[n][g][x].z, raw[n][g][x].w};
                         float c[8];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -337,20 +349,18 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     part[g] += __shfl_xor_sync(kFullMask, part[g], 1);
                     part[g] += __shfl_xor_sync(kFullMask, part[g], 2);
                 }
-                // accumulator columns 2 t4, 2 t4 + 1 are rows 8 n + 2 t4 (+ 1): their statistics live in lanes 4 (2 t4 (+ 1))
+                // accumulator columns 2 t4, 2 t4 + 1 are rows 8 n + 2 t4 (+ 1): their sums live in lanes 4 (2 t4 (+ 1))
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int from = 4 * (2 * t4 + c);
-                    const int ec = __shfl_sync(kFullMask, e, from);
-                    qscale[n][c] = p.scale_log2 * pow2(24 - ec);
 #pragma unroll
-                    for (int g = 0; g < GK; ++g) qsum[n][c][g] = p.scale_log2 * __shfl_sync(kFullMask, part[g], from);
+                    for (int g = 0; g < GK; ++g)
+                        qsum[n][c][g] = p.scale_log2 * __shfl_sync(kFullMask, part[g], 4 * (2 * t4 + c));
                     const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
                     const int i = row / p.group;
                     klo[n][c] = row < w.rows ? band_key_lo(mb, i) : 0;
                     khi[n][c] = row < w.rows ? band_key_hi(mb, i) : 0;
                     m_run[n][c] = -INFINITY;
-                    l_run[n][c] = 0.f;
+                    mu[n][c] = l_run[n][c] = 0.f;
 #pragma unroll
                     for (int g = 0; g < GV; ++g) zb[n][c][g] = 0.f;
                 }
@@ -360,6 +370,8 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 full_lo = band_key_lo(mb, r1 / p.group);
                 full_hi = band_key_hi(mb, r0 / p.group);
             }
+            if (p.scores)
+                score_at = p.scores + ((long)t.h * p.s.total * p.group + (long)w.s.q0 * p.group + t.rb * kRows + 2 * t4) * row_len + tok0;
 #pragma unroll
             for (int g = 0; g < GV; ++g) wsc[g] = INFINITY;
 #pragma unroll
@@ -370,201 +382,229 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     for (int x = 0; x < 4; ++x) acc[j][n][x] = 0.f;
             fresh = false;
         }
-        // ---------------------------------------------------- one page
-        const uint32_t s = cnt % S;
-        // (after a wait that ran out the pages count as invalid: the warp goes on to the
+        // ---------------------------------------------------- one unit: this warp's page of it
+        // (after a wait that ran out the pages count as out of range: the warp goes on to the
         // barriers that the other warps wait at)
-        if (ok) ok = lanes_wait(full(s), (cnt / S) & 1u, wc);
-        ++cnt;
-        const uint32_t st = base + s * Lay::kStage;
-        const bool valid = ok && flags[s] != 0;
-        const int page = page_of(w, t.i), key0 = page * kPage;
-        const bool whole = valid && key0 >= full_lo && key0 + kPage <= full_hi;
-        float sc[NR][4];   // scores: [key tok0, tok0 + 8][row 2 t4, 2 t4 + 1] at 2 * key + row
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) sc[n][x] = 0.f;
+        if (ok) ok = lanes_wait(full(slot), phase, wc);
+        const int pi = 2 * t.i + (warp >> 1);
+        const uint32_t st = base + slot * Lay::kStage + (warp >> 1) * Lay::kPageBytes;
+        const bool valid = ok && flags[2 * slot + (warp >> 1)] != 0;
+        const int key0 = page_of(w, pi) * kPage;
         if (valid) {
+            const bool whole = key0 >= full_lo && key0 + kPage <= full_hi;
+            float sc[2][NR][4];   // s - mu: per chunk [key g8, g8 + 8][row 2 t4, 2 t4 + 1] at 2 * key + row
 #pragma unroll
             for (int g = 0; g < GK; ++g) {
-                const uint32_t row = st + g * (kPage * 32) + tok0 * 32 + 8 * t4;
-                uint32_t wa[2], wb[2];
-                lds64(row, wa[0], wa[1]);
-                lds64(row + 8 * 32, wb[0], wb[1]);
-                const uint32_t par = st + Lay::kKC + Lay::kVC + g * (kPage * 4) + tok0 * 4;
-                const uint32_t pa = lds32(par), pb = lds32(par + 32);
-                float d[NR][4];
+#pragma unroll
+                for (int ck = 0; ck < 2; ++ck) {
+                    const uint32_t row = st + g * (kPage * 32) + (tok0 + 16 * ck) * 32 + 8 * t4;
+                    uint32_t wa[2], wb[2];
+                    lds64(row, wa[0], wa[1]);
+                    lds64(row + 8 * 32, wb[0], wb[1]);
+                    const uint32_t par = st + Lay::kKC + Lay::kVC + g * (kPage * 4) + (tok0 + 16 * ck) * 4;
+                    const uint32_t pa = lds32(par), pb = lds32(par + 32);
+                    float d[NR][4];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) d[n][x] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t xa = (k & 1) ? wa[k >> 1] >> 8 : wa[k >> 1], xb = (k & 1) ? wb[k >> 1] >> 8 : wb[k >> 1];
+                        const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma_f16(d[n], a0, a1, a2, a3, qf[n][g][2 * k], qf[n][g][2 * k + 1]);
+                    }
+                    const float aa = lo_bf16(pa) * qs, ba = hi_bf16(pa), ab = lo_bf16(pb) * qs, bb = hi_bf16(pb);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            sc[ck][n][c] = fmaf(d[n][c], aa, fmaf(qsum[n][c][g], ba, g ? sc[ck][n][c] : -mu[n][c]));
+                            sc[ck][n][2 + c] = fmaf(d[n][2 + c], ab, fmaf(qsum[n][c][g], bb, g ? sc[ck][n][2 + c] : -mu[n][c]));
+                        }
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int ck = 0; ck < 2; ++ck)
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int j = key0 + tok0 + 16 * ck + 8 * (x >> 1);
+                            if (!(j < khi[n][x & 1] && (j >= klo[n][x & 1] || j < p.sinks))) sc[ck][n][x] = -INFINITY;
+                        }
+            }
+            if (p.scores) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) d[n][x] = 0.f;
+                    for (int c = 0; c < 2; ++c)
+                        if (t.rb * kRows + n * 8 + 2 * t4 + c < w.rows) {
+                            float* dst = score_at + (n * 8 + c) * row_len + key0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t xa = (k & 1) ? wa[k >> 1] >> 8 : wa[k >> 1], xb = (k & 1) ? wb[k >> 1] >> 8 : wb[k >> 1];
-                    const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) mma_f16(d[n], a0, a1, a2, a3, qf[n][g][2 * k], qf[n][g][2 * k + 1]);
-                }
-                const float aa = lo_bf16(pa), ba = hi_bf16(pa), ab = lo_bf16(pb), bb = hi_bf16(pb);
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        sc[n][c] = fmaf(d[n][c] * qscale[n][c], aa, fmaf(qsum[n][c][g], ba, sc[n][c]));
-                        sc[n][2 + c] = fmaf(d[n][2 + c] * qscale[n][c], ab, fmaf(qsum[n][c][g], bb, sc[n][2 + c]));
-                    }
+                            for (int ck = 0; ck < 2; ++ck) {
+                                dst[16 * ck] = sc[ck][n][c] + mu[n][c];
+                                dst[16 * ck + 8] = sc[ck][n][2 + c] + mu[n][c];
+                            }
+                        }
             }
-        }
-        if (!whole) {
-            const int ja = key0 + tok0, jb = ja + 8;
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int hi = valid ? khi[n][c] : 0;
-                    if (!(ja < hi && (ja >= klo[n][c] || ja < p.sinks))) sc[n][c] = -INFINITY;
-                    if (!(jb < hi && (jb >= klo[n][c] || jb < p.sinks))) sc[n][2 + c] = -INFINITY;
-                }
-        }
-        if (p.scores) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
-                    if (row < w.rows) {
-                        float* dst = p.scores + ((long)(w.s.q0 + row / p.group) * p.H + t.h * p.group + row % p.group) *
-                                                    ((long)p.s.width * kPage) + key0 + tok0;
-                        dst[0] = sc[n][c];
-                        dst[8] = sc[n][2 + c];
-                    }
-                }
-        }
-        // ---------------------------------------------------- running maximum
-        bool grow = false;
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) grow |= fmaxf(sc[n][c], sc[n][2 + c]) > m_run[n][c] + kKv4Tau;
-        if (__any_sync(kFullMask, grow)) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                float al[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(sc[n][c], sc[n][2 + c]);
-                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
-                    const float m_new = fmaxf(m_run[n][c], mx);
-                    al[c] = m_new == -INFINITY ? 1.f : ex2_mufu(m_run[n][c] - m_new);
-                    m_run[n][c] = m_new;
-                    l_run[n][c] *= al[c];
-#pragma unroll
-                    for (int g = 0; g < GV; ++g) zb[n][c][g] *= al[c];
-                }
-#pragma unroll
-                for (int j = 0; j < GV * 4; ++j)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[j][n][x] *= al[x & 1];
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float m = m_run[n][c] == -INFINITY ? 0.f : m_run[n][c];
-                sc[n][c] = ex2_mufu(sc[n][c] - m);
-                sc[n][2 + c] = ex2_mufu(sc[n][2 + c] - m);
-                l_run[n][c] += sc[n][c] + sc[n][2 + c];
-            }
-        // ---------------------------------------------------- values
-        if (valid) {
+            // ------------------------------------------------ V's parameters; does a maximum or a scale have to move?
+            uint32_t vp[2][GV][2];
+            bool move = false;
 #pragma unroll
             for (int g = 0; g < GV; ++g) {
-                const uint32_t par = st + Lay::kKC + Lay::kVC + Lay::kKP + g * (kPage * 4) + tok0 * 4;
-                const uint32_t pa = lds32(par), pb = lds32(par + 32);
-                const float va = lo_bf16(pa), ba = hi_bf16(pa), vb = lo_bf16(pb), bb = hi_bf16(pb);
-                bool big = !(fabsf(va) * wsc[g] <= kWMost) || !(fabsf(vb) * wsc[g] <= kWMost);
-                if (!whole) {   // keys that no row sees do not count (their parameters may hold anything)
-                    bool sa = false, sb = false;
+                float top = 0.f;
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
+                for (int ck = 0; ck < 2; ++ck)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            sa |= sc[n][c] > 0.f;
-                            sb |= sc[n][2 + c] > 0.f;
+                    for (int x = 0; x < 2; ++x) {
+                        vp[ck][g][x] = lds32(st + Lay::kKC + Lay::kVC + Lay::kKP + g * (kPage * 4) + (tok0 + 16 * ck + 8 * x) * 4);
+                        if (!whole) {   // a key that none of this lane's rows sees: its parameters may hold anything
+                            bool seen = false;
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) seen |= sc[ck][n][2 * x] != -INFINITY || sc[ck][n][2 * x + 1] != -INFINITY;
+                            if (!seen) vp[ck][g][x] = 0u;
                         }
-                    big = (sa && !(fabsf(va) * wsc[g] <= kWMost)) || (sb && !(fabsf(vb) * wsc[g] <= kWMost)) ||
-                          wsc[g] == INFINITY;
+                        top = fmaxf(top, fabsf(lo_bf16(vp[ck][g][x])));
+                    }
+                move |= !(top * wsc[g] <= kWMost);
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
+                    move |= mx > (m_run[n][c] == -INFINITY ? -INFINITY : kKv4Tau);
                 }
-                if (__any_sync(kFullMask, big)) {
-                    // a new power of two for the group; infinities and NaN do not set it
-                    bool sa = whole, sb = whole;
+            if (__any_sync(kFullMask, move)) {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
+                for (int n = 0; n < NR; ++n) {
+                    float al[2];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            sa |= sc[n][c] > 0.f;
-                            sb |= sc[n][2 + c] > 0.f;
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
+                        const float m_new = fmaxf(m_run[n][c], mx + mu[n][c]);
+                        al[c] = m_new == -INFINITY ? 1.f : ex2_mufu(m_run[n][c] - m_new);
+                        const float mu_new = m_new == -INFINITY ? 0.f : m_new;
+#pragma unroll
+                        for (int ck = 0; ck < 2; ++ck) {
+                            sc[ck][n][c] += mu[n][c] - mu_new;
+                            sc[ck][n][2 + c] += mu[n][c] - mu_new;
                         }
-                    float top = fmaxf(sa && fabsf(va) < INFINITY ? fabsf(va) : 0.f, sb && fabsf(vb) < INFINITY ? fabsf(vb) : 0.f);
+                        m_run[n][c] = m_new;
+                        mu[n][c] = mu_new;
+                        l_run[n][c] *= al[c];
+#pragma unroll
+                        for (int g = 0; g < GV; ++g) zb[n][c][g] *= al[c];
+                    }
+#pragma unroll
+                    for (int j = 0; j < GV * 4; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) acc[j][n][x] *= al[x & 1];
+                }
+#pragma unroll
+                for (int g = 0; g < GV; ++g) {
+                    // a new power of two for the group's a'; infinities and NaN do not set it
+                    float top = 0.f;
+#pragma unroll
+                    for (int ck = 0; ck < 2; ++ck)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float v = fabsf(lo_bf16(vp[ck][g][x]));
+                            top = fmaxf(top, v < INFINITY ? v : 0.f);
+                        }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-                    const bool first = wsc[g] == INFINITY;
-                    const float now = top > 0.f ? kWTarget * pow2(127 - (int)(__float_as_uint(top) >> 23) - 1) : INFINITY;
-                    if (first || now < wsc[g]) {
-                        const float f = first ? 1.f : now / wsc[g];
+                    if (!(top * wsc[g] <= kWMost) && top > 0.f) {
+                        const float now = kWTarget * pow2(127 - (int)(__float_as_uint(top) >> 23) - 1);
+                        const float r = wsc[g] == INFINITY ? 1.f : now / wsc[g];
                         wsc[g] = now;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int n = 0; n < NR; ++n)
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) acc[4 * g + j][n][x] *= f;
+                                for (int x = 0; x < 4; ++x) acc[4 * g + j][n][x] *= r;
                     }
-                }
-                const float ws = wsc[g] == INFINITY ? 1.f : wsc[g];
-                const float fa = va * ws, fb = vb * ws;
-                uint32_t b0[NR], b1[NR];
-#pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float x[4] = {sc[n][0] * fa, sc[n][1] * fa, sc[n][2] * fb, sc[n][3] * fb};
-                    float z[4] = {sc[n][0] * ba, sc[n][1] * ba, sc[n][2] * bb, sc[n][3] * bb};
-                    if (!whole) {   // p = 0 times an infinity or a NaN of a masked key stays 0
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!(sc[n][i] != 0.f)) x[i] = z[i] = 0.f;
-                    }
-                    zb[n][0][g] += z[0] + z[2];
-                    zb[n][1][g] += z[1] + z[3];
-                    b0[n] = transpose8x8(pack_f16x2(x[0], x[1]));
-                    b1[n] = transpose8x8(pack_f16x2(x[2], x[3]));
-                }
-                const uint32_t row = st + Lay::kKC + g * (kPage * 32) + (warp * 16 + t4) * 32 + 4 * g8;
-                const uint32_t w0 = lds32(row), w1 = lds32(row + 4 * 32), w2 = lds32(row + 8 * 32), w3 = lds32(row + 12 * 32);
-                // channels 8 g8 + 2 j (accumulator rows g8) and + 1 (rows g8 + 8, 16 times too large) of the group
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t sel = j < 2 ? 0x5410u : 0x7632u;
-                    uint32_t xa = __byte_perm(w0, w1, sel), xb = __byte_perm(w2, w3, sel);
-                    if (j & 1) {
-                        xa >>= 8;
-                        xb >>= 8;
-                    }
-                    const uint32_t a0 = xa & 0x000f000fu, a1 = xa & 0x00f000f0u, a2 = xb & 0x000f000fu, a3 = xb & 0x00f000f0u;
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) mma_f16(acc[4 * g + j][n], a0, a1, a2, a3, b0[n], b1[n]);
                 }
             }
+#pragma unroll
+            for (int ck = 0; ck < 2; ++ck)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        sc[ck][n][x] = ex2_mufu(sc[ck][n][x]);
+                        l_run[n][x & 1] += sc[ck][n][x];
+                    }
+            // ------------------------------------------------ values
+#pragma unroll
+            for (int g = 0; g < GV; ++g) {
+                const float ws = wsc[g] == INFINITY ? 1.f : wsc[g];
+#pragma unroll
+                for (int ck = 0; ck < 2; ++ck) {
+                    const float fa = lo_bf16(vp[ck][g][0]) * ws, fb = lo_bf16(vp[ck][g][1]) * ws;
+                    const float ba = hi_bf16(vp[ck][g][0]), bb = hi_bf16(vp[ck][g][1]);
+                    uint32_t b0[NR], b1[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const float* s4 = sc[ck][n];
+                        float x[4] = {s4[0] * fa, s4[1] * fa, s4[2] * fb, s4[3] * fb};
+                        if (whole) {
+                            zb[n][0][g] = fmaf(s4[0], ba, fmaf(s4[2], bb, zb[n][0][g]));
+                            zb[n][1][g] = fmaf(s4[1], ba, fmaf(s4[3], bb, zb[n][1][g]));
+                        } else {   // p = 0 times an infinity or a NaN of a masked key stays 0
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const bool zero = s4[i] == 0.f;
+                                x[i] = zero ? 0.f : x[i];
+                                zb[n][i & 1][g] += zero ? 0.f : s4[i] * (i < 2 ? ba : bb);
+                            }
+                        }
+                        b0[n] = transpose8x8(pack_f16x2(x[0], x[1]));
+                        b1[n] = transpose8x8(pack_f16x2(x[2], x[3]));
+                    }
+                    const uint32_t row = st + Lay::kKC + g * (kPage * 32) + (tok_w + 16 * ck + t4) * 32 + 4 * g8;
+                    const uint32_t w0 = lds32(row), w1 = lds32(row + 4 * 32), w2 = lds32(row + 8 * 32), w3 = lds32(row + 12 * 32);
+                    // channels 8 g8 + 2 j (accumulator rows g8) and + 1 (rows g8 + 8, 16 times too large) of the group
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t sel = j < 2 ? 0x5410u : 0x7632u;
+                        uint32_t xa = __byte_perm(w0, w1, sel), xb = __byte_perm(w2, w3, sel);
+                        if (j & 1) {
+                            xa >>= 8;
+                            xb >>= 8;
+                        }
+                        const uint32_t a0 = xa & 0x000f000fu, a1 = xa & 0x00f000f0u, a2 = xb & 0x000f000fu, a3 = xb & 0x00f000f0u;
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma_f16(acc[4 * g + j][n], a0, a1, a2, a3, b0[n], b1[n]);
+                    }
+                }
+            }
+        } else if (p.scores && pi < w.pages) {   // no key of a page that is out of range counts
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (t.rb * kRows + n * 8 + 2 * t4 + c < w.rows)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) score_at[(n * 8 + c) * row_len + key0 + 8 * x] = -INFINITY;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty(s));
+        if (lane == 0) mbar_arrive(empty(slot));
+        if (++slot == S) {
+            slot = 0;
+            phase ^= 1u;
+        }
         ++t.i;
-        if (t.i < w.pages && u + 1 < u1) continue;
+        if (t.i < w.units && u + 1 < u1) continue;
         // ---------------------------------------------------- the row block ends here (or this CTA's share of it)
-        const bool ends = t.i == w.pages, starts = item0 >= u0;
+        const bool ends = t.i == w.units, starts = item0 >= u0;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -592,10 +632,11 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             }
         asm volatile("bar.sync 1, 128;" ::: "memory");
         {
-            const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+            const int part = 2 * blockIdx.x + (starts ? 1 : 0);
             for (int i = tid; i < kRows * (DV / 4); i += 32 * kWarps) {
                 const int row = i / (DV / 4), c4 = i % (DV / 4);
                 const int r = t.rb * kRows + row;
+                if (r >= w.rows) continue;
                 float m = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * kRows + row].x);
@@ -615,7 +656,6 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     }
                 }
                 if (starts && ends) {
-                    if (r >= w.rows) continue;
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (NaN stays)
                     const long tok = w.s.q0 + r / p.group;
                     const int head = t.h * p.group + r % p.group;
@@ -629,8 +669,8 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                         *dst = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                     }
                 } else {
-                    *reinterpret_cast<float4*>(p.part_o + ((long)slot * kRows + row) * DV + 4 * c4) = o;
-                    if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)slot * kRows + row) * 2) = make_float2(m, l);
+                    *reinterpret_cast<float4*>(p.part_o + ((long)part * kRows + row) * DV + 4 * c4) = o;
+                    if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)part * kRows + row) * 2) = make_float2(m, l);
                 }
             }
         }
@@ -639,125 +679,174 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     }
 }
 
-// One warp per (token, head) whose row block several CTAs shared: their partial
-// rows in CTA order (the same sum on every run). Rows that no key reaches get
-// O = 0, LSE = -inf here.
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4FwdParams p, int rows_per_block) {
-    const int lane = threadIdx.x & 31;
-    const long row = ((long)blockIdx.x * blockDim.x + threadIdx.x) / 32;
-    if (row >= (long)p.s.total * p.H) return;
-    const int tok = (int)(row / p.H), head = (int)(row % p.H);
-    const int b = kv4_seq_of_row(p.s, tok);
-    if (b < 0) return;
-    const SeqWork w = seq_work(p, b, rows_per_block);
-    if (w.s.bad) return;
-    const int i = tok - w.s.q0, r = i * p.group + head % p.group, h = head / p.group;
+// ---------------------------------------------------------------- finish
+// Row r of head h of a sequence: which CTAs had a share of its row block.
+struct Shares {
+    int c0, c1, in_block, rows_per_block;   // c0 == c1: finished by its CTA
+    __device__ __forceinline__ long at(int c) const { return (long)(2 * c + (c == c0 ? 1 : 0)) * rows_per_block + in_block; }
+};
+__device__ __forceinline__ Shares shares_of(const Kv4FwdParams& p, const SeqWork& w, int b, int h, int r, int rows_per_block) {
     const int per = p.prefix[kKv4MaxBatch + 1];
-    const int dv = p.c.dv;
-    float* lse = p.s.cu ? p.lse + (long)head * p.s.total + tok : p.lse + ((long)b * p.H + head) * p.s.rows + i;
-    __nv_bfloat16* out = p.o + ((long)tok * p.H + head) * dv;
-    if (w.pages == 0) {
-        for (int c = lane * 4; c < dv; c += 128) *reinterpret_cast<uint2*>(out + c) = make_uint2(0, 0);
-        if (lane == 0) *lse = -INFINITY;
-        return;
-    }
-    const int u = p.prefix[b] + (h * w.blocks + r / rows_per_block) * w.pages;
-    const int c0 = u / per, c1 = (u + w.pages - 1) / per;
-    if (c0 == c1) return;   // finished by its CTA
-    const int in_block = r % rows_per_block;
-    auto slot_row = [&](int c) { return (long)(2 * c + (c == c0 ? 1 : 0)) * rows_per_block + in_block; };
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[2 * slot_row(c)]);
+    const int u = p.prefix[b] + (h * w.blocks + r / rows_per_block) * w.units;
+    return Shares{u / per, (u + w.units - 1) / per, r % rows_per_block, rows_per_block};
+}
+// (max, sum) of all shares of a row: every lane of the warp calls and gets both.
+__device__ __forceinline__ float2 join_ml(const Kv4FwdParams& p, const Shares& s, int lane) {
+    float m = -INFINITY, l = 0.f;
+    for (int c = s.c0 + lane; c <= s.c1; c += 32) m = fmaxf(m, p.part_ml[2 * s.at(c)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-    float l = 0.f;
-    float4 o[2] = {};
-    for (int b0 = c0; b0 <= c1; b0 += 32) {
-        const int c = b0 + lane;
-        float f = 0.f;
-        if (c <= c1) {
-            const float2 v = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot_row(c));
-            f = v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m);
-            l += v.y * f;
-        }
-        for (int k = 0; k < 32 && b0 + k <= c1; ++k) {
-            const float fk = __shfl_sync(kFullMask, f, k);
-            if (fk == 0.f) continue;
-            const float* src = p.part_o + slot_row(b0 + k) * dv;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int col = x * 128 + lane * 4;
-                if (col < dv) {
-                    const float4 y = *reinterpret_cast<const float4*>(src + col);
-                    o[x].x = fmaf(fk, y.x, o[x].x);
-                    o[x].y = fmaf(fk, y.y, o[x].y);
-                    o[x].z = fmaf(fk, y.z, o[x].z);
-                    o[x].w = fmaf(fk, y.w, o[x].w);
-                }
-            }
-        }
+    for (int c = s.c0 + lane; c <= s.c1; c += 32) {
+        const float2 v = *reinterpret_cast<const float2*>(p.part_ml + 2 * s.at(c));
+        l += v.y * (v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m));
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFullMask, l, x);
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int col = x * 128 + lane * 4;
-        if (col < dv)
-            *reinterpret_cast<uint2*>(out + col) =
-                make_uint2(pack_bf16x2(o[x].x * inv, o[x].y * inv), pack_bf16x2(o[x].z * inv, o[x].w * inv));
-    }
-    if (lane == 0) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFullMask, l, o);
+    return make_float2(m, l);
+}
+__device__ __forceinline__ long lse_at(const Kv4FwdParams& p, const SeqWork& w, int b, int i, int head) {
+    return p.s.cu ? (long)head * p.s.total + w.s.q0 + i : ((long)b * p.H + head) * p.s.rows + i;
 }
 
-// key_weights[b][h][j] = decay * key_weights + sum over the rows of the group of
-// exp(s - LSE), one thread per key, rows in order. Scores of pages that no row
-// block visited were not written and count as nothing.
-constexpr int kWeightThreads = 128;
-__global__ void __launch_bounds__(kWeightThreads) kv4_weights_kernel(const Kv4FwdParams p, int rows_per_block) {
-    const int b = blockIdx.z, h = blockIdx.y;
-    const SeqWork w = seq_work(p, b, rows_per_block);
-    const int j = blockIdx.x * kWeightThreads + threadIdx.x;
-    if (j == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
-    if (w.s.bad || j >= w.s.lk || j >= p.weight_stride) return;
-    const int page = j / kPage;
-    float sum = 0.f;
-    const bool seen = w.pages > 0 && (page < w.n_sink || (page >= w.first && page < w.first + w.pages - w.n_sink));
-    if (seen) {
-        const long row_len = (long)p.s.width * kPage;
-        for (int i = 0; i < w.s.nq; ++i)
-            for (int x = 0; x < p.group; ++x) {
-                const long tok = w.s.q0 + i;
-                const int head = h * p.group + x;
-                const float lse = p.s.cu ? p.lse[(long)head * p.s.total + tok] : p.lse[((long)b * p.H + head) * p.s.rows + i];
-                const float s = p.scores[(tok * p.H + head) * row_len + j];
-                if (s != -INFINITY) sum += ex2_mufu(s - lse * kLog2e);
+constexpr int kFinishThreads = 128;
+constexpr int kFinishKeys = 4 * kFinishThreads;   // keys of a weights block
+constexpr int kFinishRows = 64;                   // rows whose LSE it holds at a time
+
+// Blocks [0, row_blocks): one warp per (token, head) whose row block several CTAs
+// shared joins their partial rows in CTA order (the same sum on every run); rows
+// that no key reaches get O = 0, LSE = -inf. The other blocks update key weights:
+//   key_weights[b][h][j] = decay * key_weights + sum over rows of exp(s - LSE),
+// four keys per thread, rows in order. Scores of pages that no row block visited
+// were not written and count as nothing. Launched while the attention kernel
+// runs (programmatic dependent launch); what it left is read after the wait.
+__global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4FwdParams p, int rows_per_block,
+                                                                    int row_blocks, int key_blocks) {
+    __shared__ float lse2[kFinishRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x < row_blocks) {
+        const long row = (long)blockIdx.x * (kFinishThreads / 32) + warp;
+        const bool live = row < (long)p.s.total * p.H;
+        const int tok = live ? (int)(row / p.H) : 0, head = live ? (int)(row % p.H) : 0;
+        const int b = live ? kv4_seq_of_row(p.s, tok) : -1;
+        const SeqWork w = seq_work(p, b < 0 ? 0 : b, rows_per_block);
+        const int i = tok - w.s.q0, dv = p.c.dv;
+        __nv_bfloat16* out = p.o + ((long)tok * p.H + head) * dv;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // (every thread: the next kernel counts on it)
+        if (b < 0 || w.s.bad) return;
+        float* lse = p.lse + lse_at(p, w, b, i, head);
+        if (w.pages == 0) {
+            for (int c = lane * 4; c < dv; c += 128) *reinterpret_cast<uint2*>(out + c) = make_uint2(0, 0);
+            if (lane == 0) *lse = -INFINITY;
+            return;
+        }
+        const Shares s = shares_of(p, w, b, head / p.group, i * p.group + head % p.group, rows_per_block);
+        if (s.c0 == s.c1) return;
+        const float2 ml = join_ml(p, s, lane);
+        float4 o[2] = {};
+        for (int c = s.c0; c <= s.c1; c += 8) {   // eight shares' loads in flight
+            float f[8];
+            float4 y[8][2];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool in = c + k <= s.c1;
+                const long at = s.at(in ? c + k : s.c1);
+                const float mk = p.part_ml[2 * at];
+                f[k] = !in || mk == -INFINITY ? 0.f : ex2_mufu(mk - ml.x);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (x * 128 + lane * 4 < dv) y[k][x] = *reinterpret_cast<const float4*>(p.part_o + at * dv + x * 128 + lane * 4);
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (f[k] != 0.f)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        o[x].x = fmaf(f[k], y[k][x].x, o[x].x);
+                        o[x].y = fmaf(f[k], y[k][x].y, o[x].y);
+                        o[x].z = fmaf(f[k], y[k][x].z, o[x].z);
+                        o[x].w = fmaf(f[k], y[k][x].w, o[x].w);
+                    }
+        }
+        const float inv = ml.y > 0.f ? 1.f / ml.y : (ml.y == 0.f ? 0.f : ml.y);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int col = x * 128 + lane * 4;
+            if (col < dv)
+                *reinterpret_cast<uint2*>(out + col) =
+                    make_uint2(pack_bf16x2(o[x].x * inv, o[x].y * inv), pack_bf16x2(o[x].z * inv, o[x].w * inv));
+        }
+        if (lane == 0) *lse = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+        return;
+    }
+    const int id = blockIdx.x - row_blocks;
+    const int bh = id / key_blocks, b = bh / p.c.Hkv, h = bh % p.c.Hkv;
+    const SeqWork w = seq_work(p, b, rows_per_block);
+    const int j = (id % key_blocks) * kFinishKeys + 4 * threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (j == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
+    const int keys = (int)min((long)w.s.lk, p.weight_stride);
+    if (w.s.bad || (id % key_blocks) * kFinishKeys >= keys) return;
+    const int page = j / kPage;
+    const bool seen = j < keys && (page < w.n_sink || (page >= w.first && page < w.first + w.pages - w.n_sink));
+    float sum[4] = {};
+    const long row_len = (long)p.s.width * kPage;
+    const float* src = p.scores + ((long)h * p.s.total * p.group + (long)w.s.q0 * p.group) * row_len + j;
+    for (int r0 = 0; r0 < w.rows && w.pages > 0; r0 += kFinishRows) {
+        const int nr = min(kFinishRows, w.rows - r0);
+        __syncthreads();
+        for (int r = warp; r < nr; r += kFinishThreads / 32) {
+            const Shares s = shares_of(p, w, b, h, r0 + r, rows_per_block);
+            float v;
+            if (s.c0 == s.c1) {
+                v = p.lse[lse_at(p, w, b, (r0 + r) / p.group, h * p.group + (r0 + r) % p.group)] * kLog2e;
+            } else {
+                const float2 ml = join_ml(p, s, lane);
+                v = ml.y == 0.f ? -INFINITY : ml.x + log2f(ml.y);
+            }
+            if (lane == 0) lse2[r] = v;
+        }
+        __syncthreads();
+        if (!seen) continue;
+#pragma unroll 4
+        for (int r = 0; r < nr; ++r) {
+            const float4 s = __ldcs(reinterpret_cast<const float4*>(src + (r0 + r) * row_len));
+            const float e = lse2[r];
+            sum[0] += s.x == -INFINITY ? 0.f : ex2_mufu(s.x - e);
+            sum[1] += s.y == -INFINITY ? 0.f : ex2_mufu(s.y - e);
+            sum[2] += s.z == -INFINITY ? 0.f : ex2_mufu(s.z - e);
+            sum[3] += s.w == -INFINITY ? 0.f : ex2_mufu(s.w - e);
+        }
     }
     float* dst = p.key_weights + ((long)b * p.c.Hkv + h) * p.weight_stride + j;
-    *dst = p.weight_decay == 0.f ? sum : fmaf(p.weight_decay, *dst, sum);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        if (j + x < keys) dst[x] = p.weight_decay == 0.f ? sum[x] : fmaf(p.weight_decay, dst[x], sum[x]);
 }
 
 template <int D, int DV, int NR>
 cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
     using Lay = Kv4Layout<D, DV, NR>;
     auto kern = kv4_fwd_kernel<D, DV, NR>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
+    const int smem = Lay::smem(p.s.B);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int grid = num_sms * Lay::kCtas;
     if (grid > kKv4MaxCtas) grid = kKv4MaxCtas;
-    kern<<<grid, kKv4Threads, Lay::kSmem, stream>>>(p);
+    kern<<<grid, kKv4Threads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long rows = (long)p.s.total * p.H;
-    if (rows > 0) {
-        kv4_combine_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p, Lay::kRows);
-        e = cudaGetLastError();
-    }
-    if (e != cudaSuccess || !p.key_weights) return e;
-    const dim3 wg((p.s.width * kPage + kWeightThreads - 1) / kWeightThreads, p.c.Hkv, p.s.B);
-    kv4_weights_kernel<<<wg, kWeightThreads, 0, stream>>>(p, Lay::kRows);
-    return cudaGetLastError();
+    const int row_blocks = (int)(((long)p.s.total * p.H + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
+    const int key_blocks = p.key_weights ? (p.s.width * kPage + kFinishKeys - 1) / kFinishKeys : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(row_blocks + (long)key_blocks * p.c.Hkv * p.s.B));
+    cfg.blockDim = dim3(kFinishThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_finish_kernel, p, Lay::kRows, row_blocks, key_blocks);
 }
 
 template <int D, int DV>
