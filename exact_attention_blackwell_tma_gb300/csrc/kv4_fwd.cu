@@ -29,14 +29,16 @@
 // 2^14 .. 2^15, which keeps all 8 bits of every bf16 element down to 2^-28 of
 // the row's largest.
 //
-// Work: a unit is one page of one (sequence, key/value head, row block); all
+// Work: a unit is two pages of one (sequence, key/value head, row block); all
 // units form one list, cut into equal ranges for the CTAs (long and short
 // caches balance, one long cache uses every SM). A row block that lies in one
 // CTA's range is finished there; others leave (max, sum, O) in the workspace
-// for the combining kernel. Within a CTA, warp 4 loads pages through a ring of
-// stages by bulk copies and each of warps 0-3 takes 16 of the 64 tokens with
-// softmax statistics of its own, so nothing but the ring synchronises; the four
-// are merged at the end of a row block.
+// for the finishing kernel. Within a CTA each of four warps takes 32 of a unit's
+// 128 tokens, with softmax statistics and a ring of bulk copies of its own (one
+// lane per copy), so that nothing synchronises the warps until they add their
+// rows up at the end of a row block.
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "kv4.h"
@@ -45,8 +47,8 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;                        // compute warps
-constexpr int kKv4Threads = 32 * (kWarps + 1);   // and the loader
+constexpr int kWarps = 4;
+constexpr int kKv4Threads = 32 * kWarps;
 constexpr float kKv4Tau = 8.f;                   // a row's max moves when it grows by more (log2 units)
 constexpr float kWTarget = 32.f;                 // the largest a' of a group is scaled to [16, 32)
 constexpr float kWMost = 128.f;                  // ... and rescaled past this: p a' <= 2^8 * 2^7 in fp16
@@ -66,6 +68,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t r;
@@ -93,21 +100,21 @@ __device__ __forceinline__ float pow2(int e) {
 
 template <int D, int DV, int NR>
 struct Kv4Layout {
-    static constexpr int kRows = 8 * NR;
-    static constexpr int kKC = D * kPage / 2, kVC = DV * kPage / 2;                          // codes of a page and head
-    static constexpr int kKP = D / kKv4Group * kPage * 4, kVP = DV / kKv4Group * kPage * 4;   // parameters
-    static constexpr int kPageBytes = kKC + kVC + kKP + kVP;
-    static constexpr int kStage = 2 * kPageBytes;
-    static constexpr int kMerge = kWarps * kRows * DV * 4;   // the four warps' O rows
-    static constexpr int kStages = D + DV <= 256 ? 3 : 2;
-    static constexpr int kMergeOff = kStages * kStage;
-    static constexpr int kMlOff = kMergeOff + kMerge;             // (max, sum) per warp and row
+    static constexpr int kRows = 8 * NR, GK = D / kKv4Group, GV = DV / kKv4Group;
+    // a slot: 32 tokens of a page and head, group by group: K codes, V codes, K and V parameters
+    static constexpr int kCodes = 32 * 32, kParams = 32 * 4;   // of one group
+    static constexpr int kVOff = GK * kCodes, kKpOff = kVOff + GV * kCodes, kVpOff = kKpOff + GK * kParams,
+                         kSlot = kVpOff + GV * kParams;
+    static constexpr int kSlots = D + DV <= 128 ? 3 : 2;          // per warp
+    static constexpr int kQOff = kWarps * kSlots * kSlot;         // q fragments [NR][GK][2][32 lanes] x 16 bytes
+    static constexpr int kSumOff = kQOff + NR * GK * 1024;        // O rows of the block, summed warp by warp
+    static constexpr int kMlOff = kSumOff + kRows * DV * 4;       // (max, sum) per warp and row
     static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
-    static constexpr int kFlagOff = kBarOff + 2 * kStages * 8;    // per stage and page: 0 out of range, 1 loaded
-    static constexpr int kAbortOff = kFlagOff + kStages * 8;
+    static constexpr int kAbortOff = kBarOff + kWarps * kSlots * 8;
     static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
     static constexpr int smem(int B) { return kPrefixOff + (B + 1) * 4; }
-    static constexpr int kRegCtas = NR * DV <= 64 ? 4 : (NR * DV <= 128 ? 3 : (NR * DV <= 256 ? 2 : 1));
+    // accumulators take NR * DV / 4 registers of a thread
+    static constexpr int kRegCtas = NR * DV <= 128 ? 4 : (NR * DV <= 256 && DV < 256 ? 3 : 2);
     static constexpr int kSmemCtas = 227 * 1024 / (smem(64) + 1024);   // (with up to 64 sequences)
     static constexpr int kCtas = kRegCtas < kSmemCtas ? kRegCtas : kSmemCtas;
     static_assert(kCtas >= 1 && smem(kKv4MaxBatch) <= 227 * 1024, "shared memory budget");
@@ -188,24 +195,20 @@ __device__ __forceinline__ Unit unit_at(const Kv4FwdParams& p, const int* prefix
     return r;
 }
 
-template <int D, int DV, int NR>
+// kScores: key weights are wanted, the scores go to the workspace.
+template <int D, int DV, int NR, bool kScores>
 __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_fwd_kernel(const Kv4FwdParams p) {
     using Lay = Kv4Layout<D, DV, NR>;
-    constexpr int GK = D / kKv4Group, GV = DV / kKv4Group, S = Lay::kStages, kRows = Lay::kRows;
+    constexpr int GK = Lay::GK, GV = Lay::GV, S = Lay::kSlots, kRows = Lay::kRows;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int* prefix = reinterpret_cast<int*>(smem + Lay::kPrefixOff);
-    volatile int* flags = reinterpret_cast<volatile int*>(smem + Lay::kFlagOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbortOff);
-    auto full = [&](uint32_t s) { return base + Lay::kBarOff + 8u * s; };
-    auto empty = [&](uint32_t s) { return base + Lay::kBarOff + 8u * (S + s); };
+    const uint32_t ring = base + warp * S * Lay::kSlot, bars = base + Lay::kBarOff + warp * S * 8;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the finishing kernel waits for this grid's end)
     if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), kWarps);
-        }
+        for (int s = 0; s < kWarps * S; ++s) mbar_init(base + Lay::kBarOff + 8 * s, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -218,99 +221,83 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
     const WaitCtx wc{abort_flag, p.status, p.wait_budget_ns};
 
-    if (warp == kWarps) {
-        // ------------------------------------------------------------ loader
-        uint32_t cnt = 0;
-        bool ok = true;
-        for (int v0 = u0; v0 < u1 && ok; v0 += 16) {
-            const int u = v0 + (lane >> 1);
-            int page = -2, h = 0;   // -2: no such page, -1: out of range
-            if (u < u1) {   // each lane looks up one page of a unit
-                SeqWork w;
-                const Unit t = unit_at(p, prefix, u, kRows, &w);
-                h = t.h;
-                const int i = 2 * t.i + (lane & 1);
-                if (i < w.pages) {
-                    page = p.s.table[(long)t.b * p.s.width + page_of(w, i)];
-                    if (page < 0 || page >= p.c.n_pages) {
-                        page = -1;
-                        atomicCAS(p.status, kStatusOk, kStatusBadPage);
-                    }
-                }
-            }
-            for (int i = 0; i < 16 && v0 + i < u1; ++i, ++cnt) {
-                const int pg0 = __shfl_sync(kFullMask, page, 2 * i), pg1 = __shfl_sync(kFullMask, page, 2 * i + 1);
-                const int hh = __shfl_sync(kFullMask, h, 2 * i);
-                const uint32_t s = cnt % S;
-                ok = lanes_wait(empty(s), ((cnt / S) & 1u) ^ 1u, wc);
-                if (!ok) break;
-                if (lane == 0) {
-                    flags[2 * s] = pg0 >= 0;
-                    flags[2 * s + 1] = pg1 >= 0;
-                    const uint32_t bytes = (pg0 >= 0 ? Lay::kPageBytes : 0) + (pg1 >= 0 ? Lay::kPageBytes : 0);
-                    if (bytes) mbar_expect_tx(full(s), bytes);
-                    else mbar_arrive(full(s));
-                    for (int x = 0; x < 2; ++x) {
-                        const int pg = x ? pg1 : pg0;
-                        if (pg < 0) continue;
-                        const uint32_t dst = base + s * Lay::kStage + x * Lay::kPageBytes;
-                        const long ph = (long)pg * p.c.Hkv + hh;
-                        bulk_load(dst, p.c.k_codes + ph * Lay::kKC, Lay::kKC, full(s));
-                        bulk_load(dst + Lay::kKC + Lay::kVC, p.c.k_params + ph * (Lay::kKP / 4), Lay::kKP, full(s));
-                        bulk_load(dst + Lay::kKC, p.c.v_codes + ph * Lay::kVC, Lay::kVC, full(s));
-                        bulk_load(dst + Lay::kKC + Lay::kVC + Lay::kKP, p.c.v_params + ph * (Lay::kVP / 4), Lay::kVP,
-                                  full(s));
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        if (lane == 0)   // issued copies land before the CTA can exit
-            for (uint32_t i = 0; i < (uint32_t)S && i < cnt; ++i) {
-                const uint32_t n = cnt - 1 - i;
-                drain_wait(full(n % S), (n / S) & 1u, p.wait_budget_ns);
-            }
-        return;
-    }
-
-    // ---------------------------------------------------------------- compute warps
     const int g8 = lane >> 2, t4 = lane & 3;
-    // This warp's 32 tokens of the unit's page warp / 2, in two chunks of 16. S^T row r of a
-    // chunk is token t + 4 e + 8 h (r = 2 t + e + 8 h): then the V words of a lane (rows 2 t,
-    // 2 t + 1, 2 t + 8, 2 t + 9 of P^T) lie 4 tokens apart and a warp's 32-bit loads hit 32 banks.
-    const int tok_w = (warp & 1) * 32, tok0 = tok_w + (g8 >> 1) + 4 * (g8 & 1);   // keys tok0, + 8 (chunk 0), + 16, + 24
+    // This warp's 32 tokens of a unit (half warp % 2 of page warp / 2), in two chunks of 16. S^T
+    // row r of a chunk is token t + 4 e + 8 h (r = 2 t + e + 8 h): then the V words of a lane (rows
+    // 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of P^T) lie 4 tokens apart and a warp's 32-bit loads hit 32 banks.
+    const int half = warp & 1, tok0 = (g8 >> 1) + 4 * (g8 & 1);   // keys tok0, + 8 (chunk 0), + 16, + 24
     float acc[GV * 4][NR][4];
-    uint32_t qf[NR][GK][8];
-    float qsum[NR][2][GK], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV], qs = 0.f;
+    float qsum[NR][2][GK], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
     int klo[NR][2], khi[NR][2];
-    float* merge = reinterpret_cast<float*>(smem + Lay::kMergeOff);
+    float* sums = reinterpret_cast<float*>(smem + Lay::kSumOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
-    uint32_t slot = 0, phase = 0;
-    Unit t{0, 0, 0, 0};
-    SeqWork w;
-    int full_lo = 0, full_hi = 0, item0 = 0;   // keys every row sees; the row block's first unit
-    float* score_at = nullptr;                 // the scores of row 2 t4, key tok0 of the cache
+    uint32_t got = 0, sent = 0, live = 0;   // slots waited for and issued so far; bit n % 32: the page of issue n is in range
     const long row_len = (long)p.s.width * kPage;
-    bool fresh = true, ok = true;
-    for (int u = u0; u < u1; ++u) {
-        if (fresh) {
-            // ------------------------------------------------ the row block's queries
-            t = unit_at(p, prefix, u, kRows, &w);
-            item0 = u - t.i;
-            const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
+    bool ok = true;
+    for (int u = u0; u < u1;) {
+        // ------------------------------------------------ a row block (this CTA's share of it): units i0 .. i1 - 1
+        SeqWork w;
+        const Unit t = unit_at(p, prefix, u, kRows, &w);
+        const int i0 = t.i, i1 = min(w.units, i0 + u1 - u);
+        u += i1 - i0;
+        // this warp's pages: index 2 i + warp / 2; each lane holds one of the next 32 ids
+        const int* table = p.s.table + (long)t.b * p.s.width;
+        auto page_id = [&](int i) {
+            const int x = 2 * i + (warp >> 1);
+            if (i >= i1 || x >= w.pages) return -2;   // no such page
+            const int id = table[page_of(w, x)];
+            if (id >= 0 && id < p.c.n_pages) return id;
+            atomicCAS(p.status, kStatusOk, kStatusBadPage);
+            return -1;
+        };
+        int ids = page_id(i0 + lane), ids_next = -2;
+        // copy `lane` of a slot: the codes of a group, or its parameters
+        const bool cp_params = lane >= GK + GV, cp_v = (cp_params ? lane - GK - GV : lane) >= GK;
+        const int cp_g = (cp_params ? lane - GK - GV : lane) - (cp_v ? GK : 0);
+        const uint8_t* cp_src = cp_params ? reinterpret_cast<const uint8_t*>(cp_v ? p.c.v_params : p.c.k_params)
+                                          : (cp_v ? p.c.v_codes : p.c.k_codes);
+        const uint32_t cp_bytes = cp_params ? Lay::kParams : Lay::kCodes;
+        const uint32_t cp_dst = cp_params ? (cp_v ? Lay::kVpOff : Lay::kKpOff) + cp_g * Lay::kParams
+                                          : (cp_v ? Lay::kVOff : 0) + cp_g * Lay::kCodes;
+        auto issue = [&](int i) {   // the loads of unit i into the next slot (i - i0 = 0, 1, 2, ...)
+            const int n = i - i0;
+            if ((n & 31) == 16) ids_next = page_id(i + 16 + lane);
+            if ((n & 31) == 0 && n > 0) ids = ids_next;
+            const int id = __shfl_sync(kFullMask, ids, n & 31);
+            const uint32_t s = sent % S;
+            live = (live & ~(1u << (sent & 31))) | ((id >= 0 ? 1u : 0u) << (sent & 31));
+            ++sent;
+            if (id >= 0) {
+                if (lane == 0) mbar_expect_tx(bars + 8 * s, Lay::kSlot);
+                __syncwarp();
+                if (lane < 2 * (GK + GV)) {
+                    const long at = ((long)id * p.c.Hkv + t.h) * (cp_v ? GV : GK) + cp_g;   // group of the cache
+                    bulk_load(ring + s * Lay::kSlot + cp_dst, cp_src + (at * 2 + half) * cp_bytes, cp_bytes, bars + 8 * s);
+                }
+            } else if (lane == 0) {
+                mbar_arrive(bars + 8 * s);
+            }
+            __syncwarp();
+        };
+        if (ok)
+            for (int i = i0; i < i1 && i < i0 + S; ++i) issue(i);
+        // ------------------------------------------------ its queries
+        const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
+        float qs;
+        {
             uint4 raw[NR][GK][2];
             float top = 0.f;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const int r = t.rb * kRows + n * 8 + g8;   // this lane loads row r's channels 16 t4 .. of each group
-                const bool live = r < w.rows;
-                const __nv_bfloat16* src = p.q + (long)(w.s.q0 + (live ? r / p.group : 0)) * p.q_stride +
-                                           (long)(t.h * p.group + (live ? r % p.group : 0)) * D + 16 * t4;
+                const bool in = r < w.rows;
+                const __nv_bfloat16* src = p.q + (long)(w.s.q0 + (in ? r / p.group : 0)) * p.q_stride +
+                                           (long)(t.h * p.group + (in ? r % p.group : 0)) * D + 16 * t4;
 #pragma unroll
                 for (int g = 0; g < GK; ++g)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        raw[n][g][x] = live ? *reinterpret_cast<const uint4*>(src + g * kKv4Group + 8 * x) : make_uint4(0, 0, 0, 0);
+                        raw[n][g][x] = in ? *reinterpret_cast<const uint4*>(src + g * kKv4Group + 8 * x) : make_uint4(0, 0, 0, 0);
                         const uint32_t ws[4] = {raw[n][g][x].x, raw[n][g][x].y, raw[n][g][x].z, raw[n][g][x].w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(ws[i])), fabsf(hi_bf16(ws[i]))));
@@ -341,10 +328,10 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                         for (int i = 0; i < 8; ++i) part[g] += c[i];
                         // word x holds channels 8 x .. 8 x + 7; step 2 x takes (0, 4) and (1, 5), step 2 x + 1 (2, 6) and (3, 7);
                         // odd nibbles read 16 times too large
-                        qf[n][g][4 * x + 0] = pack_f16x2(c[0] * f, c[4] * f);
-                        qf[n][g][4 * x + 1] = pack_f16x2(c[1] * f * 0.0625f, c[5] * f * 0.0625f);
-                        qf[n][g][4 * x + 2] = pack_f16x2(c[2] * f, c[6] * f);
-                        qf[n][g][4 * x + 3] = pack_f16x2(c[3] * f * 0.0625f, c[7] * f * 0.0625f);
+                        if (warp == n % kWarps)   // one warp writes the fragments that all read
+                            *reinterpret_cast<uint4*>(smem + Lay::kQOff + (((n * GK + g) * 2 + x) * 32 + lane) * 16) =
+                                make_uint4(pack_f16x2(c[0] * f, c[4] * f), pack_f16x2(c[1] * f * 0.0625f, c[5] * f * 0.0625f),
+                                           pack_f16x2(c[2] * f, c[6] * f), pack_f16x2(c[3] * f * 0.0625f, c[7] * f * 0.0625f));
                     }
                     part[g] += __shfl_xor_sync(kFullMask, part[g], 1);
                     part[g] += __shfl_xor_sync(kFullMask, part[g], 2);
@@ -365,43 +352,48 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     for (int g = 0; g < GV; ++g) zb[n][c][g] = 0.f;
                 }
             }
-            {   // keys that the block's first and last rows (hence all) see
-                const int r0 = t.rb * kRows, r1 = min(w.rows, r0 + kRows) - 1;
-                full_lo = band_key_lo(mb, r1 / p.group);
-                full_hi = band_key_hi(mb, r0 / p.group);
-            }
-            if (p.scores)
-                score_at = p.scores + ((long)t.h * p.s.total * p.group + (long)w.s.q0 * p.group + t.rb * kRows + 2 * t4) * row_len + tok0;
-#pragma unroll
-            for (int g = 0; g < GV; ++g) wsc[g] = INFINITY;
-#pragma unroll
-            for (int j = 0; j < GV * 4; ++j)
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[j][n][x] = 0.f;
-            fresh = false;
         }
-        // ---------------------------------------------------- one unit: this warp's page of it
-        // (after a wait that ran out the pages count as out of range: the warp goes on to the
-        // barriers that the other warps wait at)
-        if (ok) ok = lanes_wait(full(slot), phase, wc);
-        const int pi = 2 * t.i + (warp >> 1);
-        const uint32_t st = base + slot * Lay::kStage + (warp >> 1) * Lay::kPageBytes;
-        const bool valid = ok && flags[2 * slot + (warp >> 1)] != 0;
-        const int key0 = page_of(w, pi) * kPage;
-        if (valid) {
-            const bool whole = key0 >= full_lo && key0 + kPage <= full_hi;
+        // keys that the block's first and last rows (hence all) see
+        const int full_lo = band_key_lo(mb, (min(w.rows, t.rb * kRows + kRows) - 1) / p.group);
+        const int full_hi = band_key_hi(mb, t.rb * kRows / p.group);
+        float* score_at = nullptr;   // the scores of row 2 t4, token tok0 of a half page
+        uint32_t rows_in = 0;        // bit 2 n + c: row 8 n + 2 t4 + c exists
+        if constexpr (kScores) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                for (int c = 0; c < 2; ++c) rows_in |= (t.rb * kRows + n * 8 + 2 * t4 + c < w.rows ? 1u : 0u) << (2 * n + c);
+            score_at = p.scores + ((long)t.h * p.s.total * p.group + (long)w.s.q0 * p.group + t.rb * kRows + 2 * t4) * row_len + tok0;
+        }
+#pragma unroll
+        for (int g = 0; g < GV; ++g) wsc[g] = INFINITY;
+#pragma unroll
+        for (int j = 0; j < GV * 4; ++j)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[j][n][x] = 0.f;
+        __syncthreads();   // the q fragments are in place
+        const uint32_t qfrag = base + Lay::kQOff + lane * 16;
+
+        // One half page of 32 keys from slot `st`, its first key key0. kWhole: every row sees all of
+        // them (the common case, kept free of masks and branches).
+        auto half_page = [&](auto whole_tag, const uint32_t st, const int key0) {
+            constexpr bool kWhole = decltype(whole_tag)::value;
             float sc[2][NR][4];   // s - mu: per chunk [key g8, g8 + 8][row 2 t4, 2 t4 + 1] at 2 * key + row
 #pragma unroll
             for (int g = 0; g < GK; ++g) {
+                uint4 qf[NR][2];
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) qf[n][x] = lds128(qfrag + ((n * GK + g) * 2 + x) * 512);
 #pragma unroll
                 for (int ck = 0; ck < 2; ++ck) {
-                    const uint32_t row = st + g * (kPage * 32) + (tok0 + 16 * ck) * 32 + 8 * t4;
+                    const uint32_t row = st + g * Lay::kCodes + (tok0 + 16 * ck) * 32 + 8 * t4;
                     uint32_t wa[2], wb[2];
                     lds64(row, wa[0], wa[1]);
                     lds64(row + 8 * 32, wb[0], wb[1]);
-                    const uint32_t par = st + Lay::kKC + Lay::kVC + g * (kPage * 4) + (tok0 + 16 * ck) * 4;
+                    const uint32_t par = st + Lay::kKpOff + g * Lay::kParams + (tok0 + 16 * ck) * 4;
                     const uint32_t pa = lds32(par), pb = lds32(par + 32);
                     float d[NR][4];
 #pragma unroll
@@ -413,7 +405,10 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                         const uint32_t xa = (k & 1) ? wa[k >> 1] >> 8 : wa[k >> 1], xb = (k & 1) ? wb[k >> 1] >> 8 : wb[k >> 1];
                         const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) mma_f16(d[n], a0, a1, a2, a3, qf[n][g][2 * k], qf[n][g][2 * k + 1]);
+                        for (int n = 0; n < NR; ++n) {
+                            const uint4 q4 = qf[n][k >> 1];
+                            mma_f16(d[n], a0, a1, a2, a3, (k & 1) ? q4.z : q4.x, (k & 1) ? q4.w : q4.y);
+                        }
                     }
                     const float aa = lo_bf16(pa) * qs, ba = hi_bf16(pa), ab = lo_bf16(pb) * qs, bb = hi_bf16(pb);
 #pragma unroll
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                         }
                 }
             }
-            if (!whole) {
+            if constexpr (!kWhole) {
 #pragma unroll
                 for (int ck = 0; ck < 2; ++ck)
 #pragma unroll
@@ -436,21 +431,23 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                             if (!(j < khi[n][x & 1] && (j >= klo[n][x & 1] || j < p.sinks))) sc[ck][n][x] = -INFINITY;
                         }
             }
-            if (p.scores) {
+            if constexpr (kScores) {
+                float* dst = score_at + key0;
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        if (t.rb * kRows + n * 8 + 2 * t4 + c < w.rows) {
-                            float* dst = score_at + (n * 8 + c) * row_len + key0;
+                    for (int c = 0; c < 2; ++c) {
+                        if ((rows_in >> (2 * n + c)) & 1u) {
 #pragma unroll
                             for (int ck = 0; ck < 2; ++ck) {
                                 dst[16 * ck] = sc[ck][n][c] + mu[n][c];
                                 dst[16 * ck + 8] = sc[ck][n][2 + c] + mu[n][c];
                             }
                         }
+                        dst += c ? 7 * row_len : row_len;
+                    }
             }
-            // ------------------------------------------------ V's parameters; does a maximum or a scale have to move?
+            // ---------------------------------------- V's parameters; does a maximum or a scale have to move?
             uint32_t vp[2][GV][2];
             bool move = false;
 #pragma unroll
@@ -460,8 +457,8 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 for (int ck = 0; ck < 2; ++ck)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        vp[ck][g][x] = lds32(st + Lay::kKC + Lay::kVC + Lay::kKP + g * (kPage * 4) + (tok0 + 16 * ck + 8 * x) * 4);
-                        if (!whole) {   // a key that none of this lane's rows sees: its parameters may hold anything
+                        vp[ck][g][x] = lds32(st + Lay::kVpOff + g * Lay::kParams + (tok0 + 16 * ck + 8 * x) * 4);
+                        if constexpr (!kWhole) {   // a key that none of this lane's rows sees: its parameters may hold anything
                             bool seen = false;
 #pragma unroll
                             for (int n = 0; n < NR; ++n) seen |= sc[ck][n][2 * x] != -INFINITY || sc[ck][n][2 * x + 1] != -INFINITY;
@@ -542,7 +539,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                         sc[ck][n][x] = ex2_mufu(sc[ck][n][x]);
                         l_run[n][x & 1] += sc[ck][n][x];
                     }
-            // ------------------------------------------------ values
+            // ---------------------------------------- values
 #pragma unroll
             for (int g = 0; g < GV; ++g) {
                 const float ws = wsc[g] == INFINITY ? 1.f : wsc[g];
@@ -555,21 +552,21 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     for (int n = 0; n < NR; ++n) {
                         const float* s4 = sc[ck][n];
                         float x[4] = {s4[0] * fa, s4[1] * fa, s4[2] * fb, s4[3] * fb};
-                        if (whole) {
+                        if constexpr (kWhole) {
                             zb[n][0][g] = fmaf(s4[0], ba, fmaf(s4[2], bb, zb[n][0][g]));
                             zb[n][1][g] = fmaf(s4[1], ba, fmaf(s4[3], bb, zb[n][1][g]));
                         } else {   // p = 0 times an infinity or a NaN of a masked key stays 0
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const bool zero = s4[i] == 0.f;
-                                x[i] = zero ? 0.f : x[i];
-                                zb[n][i & 1][g] += zero ? 0.f : s4[i] * (i < 2 ? ba : bb);
+                            for (int y = 0; y < 4; ++y) {
+                                const bool zero = s4[y] == 0.f;
+                                x[y] = zero ? 0.f : x[y];
+                                zb[n][y & 1][g] += zero ? 0.f : s4[y] * (y < 2 ? ba : bb);
                             }
                         }
                         b0[n] = transpose8x8(pack_f16x2(x[0], x[1]));
                         b1[n] = transpose8x8(pack_f16x2(x[2], x[3]));
                     }
-                    const uint32_t row = st + Lay::kKC + g * (kPage * 32) + (tok_w + 16 * ck + t4) * 32 + 4 * g8;
+                    const uint32_t row = st + Lay::kVOff + g * Lay::kCodes + (16 * ck + t4) * 32 + 4 * g8;
                     const uint32_t w0 = lds32(row), w1 = lds32(row + 4 * 32), w2 = lds32(row + 8 * 32), w3 = lds32(row + 12 * 32);
                     // channels 8 g8 + 2 j (accumulator rows g8) and + 1 (rows g8 + 8, 16 times too large) of the group
 #pragma unroll
@@ -586,25 +583,33 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     }
                 }
             }
-        } else if (p.scores && pi < w.pages) {   // no key of a page that is out of range counts
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (t.rb * kRows + n * 8 + 2 * t4 + c < w.rows)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) score_at[(n * 8 + c) * row_len + key0 + 8 * x] = -INFINITY;
+        };
+
+        for (int i = i0; i < i1; ++i) {
+            // -------------------------------------------- this warp's half page of unit i
+            // (after a wait that ran out no more is loaded or counted, and the warp goes on to the
+            // barriers that the other warps wait at)
+            const uint32_t s = got % S;
+            if (ok) ok = lanes_wait(bars + 8 * s, (got / S) & 1u, wc);
+            const bool valid = ok && ((live >> (got & 31)) & 1u);
+            if (ok) ++got;
+            const int key0 = page_of(w, 2 * i + (warp >> 1)) * kPage + 32 * half;
+            if (valid) {
+                if (key0 >= full_lo && key0 + 32 <= full_hi) half_page(std::true_type{}, ring + s * Lay::kSlot, key0);
+                else half_page(std::false_type{}, ring + s * Lay::kSlot, key0);
+            } else if (kScores && 2 * i + (warp >> 1) < w.pages) {   // no key of a page that is out of range counts
+                float* dst = score_at + key0;
+                for (int n = 0; n < 2 * NR; ++n) {
+                    if ((rows_in >> n) & 1u)
+                        for (int x = 0; x < 4; ++x) dst[8 * x] = -INFINITY;
+                    dst += n & 1 ? 7 * row_len : row_len;
+                }
+            }
+            __syncwarp();   // every lane has read the slot
+            if (ok && i + S < i1) issue(i + S);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(slot));
-        if (++slot == S) {
-            slot = 0;
-            phase ^= 1u;
-        }
-        ++t.i;
-        if (t.i < w.units && u + 1 < u1) continue;
-        // ---------------------------------------------------- the row block ends here (or this CTA's share of it)
-        const bool ends = t.i == w.units, starts = item0 >= u0;
+        // ------------------------------------------------ the four warps' rows become one
+        const bool ends = i1 == w.units, starts = i0 == 0;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -613,70 +618,80 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 l += __shfl_xor_sync(kFullMask, l, 4);
                 l += __shfl_xor_sync(kFullMask, l, 8);
                 l += __shfl_xor_sync(kFullMask, l, 16);
-                const int row = n * 8 + 2 * t4 + c;
-                if (g8 == 0) ml[warp * kRows + row] = make_float2(m_run[n][c], l);
-#pragma unroll
-                for (int g = 0; g < GV; ++g) {
-                    float z = zb[n][c][g];
-                    z += __shfl_xor_sync(kFullMask, z, 4);
-                    z += __shfl_xor_sync(kFullMask, z, 8);
-                    z += __shfl_xor_sync(kFullMask, z, 16);
-                    const float inv = wsc[g] == INFINITY ? 1.f : 1.f / wsc[g];   // (a power of two)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 o = make_float2(fmaf(acc[4 * g + j][n][c], inv * 16777216.f, z),
-                                                     fmaf(acc[4 * g + j][n][2 + c], inv * 1048576.f, z));
-                        *reinterpret_cast<float2*>(merge + ((long)warp * kRows + row) * DV + g * kKv4Group + 8 * g8 + 2 * j) = o;
-                    }
-                }
+                if (g8 == 0) ml[warp * kRows + n * 8 + 2 * t4 + c] = make_float2(m_run[n][c], l);
             }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        {
-            const int part = 2 * blockIdx.x + (starts ? 1 : 0);
-            for (int i = tid; i < kRows * (DV / 4); i += 32 * kWarps) {
-                const int row = i / (DV / 4), c4 = i % (DV / 4);
-                const int r = t.rb * kRows + row;
-                if (r >= w.rows) continue;
+        __syncthreads();
+        float f[NR][2];   // this warp's rows relative to the common maximum
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
                 float m = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * kRows + row].x);
-                float l = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * kRows + n * 8 + 2 * t4 + c].x);
+                f[n][c] = m_run[n][c] == -INFINITY ? 0.f : ex2_mufu(m_run[n][c] - m);
+            }
+        for (int x = 0; x < kWarps; ++x) {   // in warp order: the same sum on every run
+            if (warp == x) {
 #pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float2 v = ml[x * kRows + row];
-                    const float f = v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m);
-                    l += v.y * f;
-                    if (f != 0.f) {
-                        const float4 y = *reinterpret_cast<const float4*>(merge + ((long)x * kRows + row) * DV + 4 * c4);
-                        o.x = fmaf(f, y.x, o.x);
-                        o.y = fmaf(f, y.y, o.y);
-                        o.z = fmaf(f, y.z, o.z);
-                        o.w = fmaf(f, y.w, o.w);
-                    }
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int g = 0; g < GV; ++g) {
+                            float z = zb[n][c][g];
+                            z += __shfl_xor_sync(kFullMask, z, 4);
+                            z += __shfl_xor_sync(kFullMask, z, 8);
+                            z += __shfl_xor_sync(kFullMask, z, 16);
+                            const float inv = wsc[g] == INFINITY ? 1.f : 1.f / wsc[g];   // (a power of two)
+                            float2* at = reinterpret_cast<float2*>(sums + (n * 8 + 2 * t4 + c) * DV + g * kKv4Group + 8 * g8);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float2 o = x ? at[j] : make_float2(0.f, 0.f);
+                                if (f[n][c] != 0.f) {
+                                    o.x = fmaf(f[n][c], fmaf(acc[4 * g + j][n][c], inv * 16777216.f, z), o.x);
+                                    o.y = fmaf(f[n][c], fmaf(acc[4 * g + j][n][2 + c], inv * 1048576.f, z), o.y);
+                                }
+                                at[j] = o;
+                            }
+                        }
+            }
+            __syncthreads();
+        }
+        const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+        for (int x = tid; x < kRows * (DV / 4); x += kKv4Threads) {
+            const int row = x / (DV / 4), c4 = x % (DV / 4);
+            const int r = t.rb * kRows + row;
+            if (r >= w.rows) continue;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) m = fmaxf(m, ml[y * kRows + row].x);
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) {
+                const float2 v = ml[y * kRows + row];
+                l += v.y * (v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m));
+            }
+            const float4 o = *reinterpret_cast<const float4*>(sums + row * DV + 4 * c4);
+            if (starts && ends) {
+                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (NaN stays)
+                const long tok = w.s.q0 + r / p.group;
+                const int head = t.h * p.group + r % p.group;
+                *reinterpret_cast<uint2*>(p.o + (tok * p.H + head) * DV + 4 * c4) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (c4 == 0) {
+                    float* dst = p.s.cu ? p.lse + (long)head * p.s.total + tok
+                                        : p.lse + ((long)t.b * p.H + head) * p.s.rows + r / p.group;
+                    *dst = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
-                if (starts && ends) {
-                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (NaN stays)
-                    const long tok = w.s.q0 + r / p.group;
-                    const int head = t.h * p.group + r % p.group;
-                    uint2 out;
-                    out.x = pack_bf16x2(o.x * inv, o.y * inv);
-                    out.y = pack_bf16x2(o.z * inv, o.w * inv);
-                    *reinterpret_cast<uint2*>(p.o + (tok * p.H + head) * DV + 4 * c4) = out;
-                    if (c4 == 0) {
-                        float* dst = p.s.cu ? p.lse + (long)head * p.s.total + tok
-                                            : p.lse + ((long)t.b * p.H + head) * p.s.rows + r / p.group;
-                        *dst = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-                    }
-                } else {
-                    *reinterpret_cast<float4*>(p.part_o + ((long)part * kRows + row) * DV + 4 * c4) = o;
-                    if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)part * kRows + row) * 2) = make_float2(m, l);
-                }
+            } else {
+                *reinterpret_cast<float4*>(p.part_o + ((long)part * kRows + row) * DV + 4 * c4) = o;
+                if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)part * kRows + row) * 2) = make_float2(m, l);
             }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        fresh = true;
+        __syncthreads();
     }
+    if (!ok && lane == 0)   // issued copies land before the CTA can exit
+        for (uint32_t n = got; n < sent; ++n) drain_wait(bars + 8 * (n % S), (n / S) & 1u, p.wait_budget_ns);
 }
 
 // ---------------------------------------------------------------- finish
@@ -826,7 +841,7 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4Fwd
 template <int D, int DV, int NR>
 cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
     using Lay = Kv4Layout<D, DV, NR>;
-    auto kern = kv4_fwd_kernel<D, DV, NR>;
+    auto kern = p.key_weights ? kv4_fwd_kernel<D, DV, NR, true> : kv4_fwd_kernel<D, DV, NR, false>;
     const int smem = Lay::smem(p.s.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
