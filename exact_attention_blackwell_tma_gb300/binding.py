@@ -6,7 +6,9 @@ library has not been built, ``load()`` raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -110,6 +112,8 @@ def library_path() -> str:
 def load():
     """Load libattn.so (built by ``build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -147,8 +151,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the handle of torch.cuda.current_stream() without building the Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -443,18 +447,19 @@ class Kv4Cache:
     __slots__ = ("k_codes", "k_params", "v_codes", "v_params", "n_pages", "Hkv", "d", "dv", "_struct")
 
     def __init__(self, k_codes, k_params, v_codes, v_params):
-        for codes, params in ((k_codes, k_params), (v_codes, v_params)):
-            pages, heads, groups = k_codes.shape[0], k_codes.shape[1], codes.shape[2]
-            if (codes.dtype != torch.uint8 or tuple(codes.shape) != (pages, heads, groups, KV4_PAGE, KV4_GROUP // 2)
-                    or params.dtype != torch.bfloat16
-                    or tuple(params.shape) != (pages, heads, groups, KV4_PAGE, 2)):
+        pages, heads, groups = k_codes.shape[:3]
+        v_groups = v_codes.shape[2] if v_codes.dim() == 5 else 0
+        rows, dtype, device = (KV4_PAGE, KV4_GROUP // 2), (torch.uint8, torch.bfloat16), k_codes.get_device()
+        for codes, params, g in ((k_codes, k_params, groups), (v_codes, v_params, v_groups)):
+            if (codes.shape != (pages, heads, g) + rows or params.shape != (pages, heads, g, KV4_PAGE, 2)
+                    or (codes.dtype, params.dtype) != dtype or codes.get_device() != device
+                    or params.get_device() != device):
                 raise ValueError(f"a 4-bit cache needs uint8 codes [pages, heads, groups, {KV4_PAGE}, {KV4_GROUP // 2}] "
-                                 f"and bf16 params [pages, heads, groups, {KV4_PAGE}, 2], got {codes.dtype} "
+                                 f"and bf16 params [pages, heads, groups, {KV4_PAGE}, 2] on one device, got {codes.dtype} "
                                  f"{tuple(codes.shape)} and {params.dtype} {tuple(params.shape)}")
         _check_tensors(k_codes, k_params, v_codes, v_params)
         self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
-        self.n_pages, self.Hkv = k_codes.shape[0], k_codes.shape[1]
-        self.d, self.dv = k_codes.shape[2] * KV4_GROUP, v_codes.shape[2] * KV4_GROUP
+        self.n_pages, self.Hkv, self.d, self.dv = pages, heads, groups * KV4_GROUP, v_groups * KV4_GROUP
         self._struct = _Kv4Struct(k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
                                   self.n_pages, self.Hkv, self.d, self.dv)
 
@@ -472,73 +477,72 @@ class Kv4Cache:
         return cls(codes(d), params(d), codes(dv), params(dv))
 
 
-def _kv4_ints(cache, B, **tensors):
-    """int32 contiguous tensors on the cache's device, which is the current one."""
-    device = cache.k_codes.device
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is None:
+def _kv4_ints(cache, page_table, cache_lens, cu_seqlens, new_table=None):
+    """Checks the int32 tensors of a call, which live on the cache's device, the current one; returns (B, device index)."""
+    device = cache.k_codes.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the cache is on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    B = cache_lens.shape[0] if cache_lens.dim() == 1 else -1
+    for name, t, shape in (("cache_lens", cache_lens, 0), ("page_table", page_table, 2), ("cu_seqlens", cu_seqlens, 1),
+                           ("new_table", new_table, 2)):
+        if t is None and shape and name != "page_table":
             continue
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-        rows = B + 1 if name.startswith("cu_") else B
-        if t.shape[0] != rows or t.dim() != (2 if name.endswith("table") else 1):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows} rows")
+        if t.dtype != torch.int32 or t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on cuda:{device}")
+        if t.dim() != max(shape, 1) or t.shape[0] != (B + 1 if shape == 1 else B):
+            raise ValueError(f"{name} has shape {tuple(t.shape)} for {B} sequences")
+    return B, device
 
 
-def _kv4_rows(x, heads, width, B, cu_seqlens, name, device):
+def _kv4_rows(x, heads, width, B, packed, name, device):
     """Rows of [T, heads, width] (packed) or [B, L, heads, width] (dense): (L, elements between rows).
     Heads and channels are contiguous; rows may lie further apart (a slice of a fused projection)."""
-    dims = 3 if cu_seqlens is not None else 4
-    if (x.dim() != dims or tuple(x.shape[-2:]) != (heads, width) or x.dtype != torch.bfloat16 or x.device != device
-            or (dims == 4 and x.shape[0] != B)):
-        lead = "T" if dims == 3 else f"{B}, L"
-        raise ValueError(f"{name} must be a bf16 tensor [{lead}, {heads}, {width}] on {device}, got {x.dtype} "
-                         f"{tuple(x.shape)} on {x.device}")
-    L = x.shape[-3]
-    if x.numel() == 0:
+    shape, stride = x.shape, x.stride()
+    if (len(shape) != (3 if packed else 4) or shape[-2] != heads or shape[-1] != width or x.dtype != torch.bfloat16
+            or x.get_device() != device or (not packed and shape[0] != B)):
+        lead = "T" if packed else f"{B}, L"
+        raise ValueError(f"{name} must be a bf16 tensor [{lead}, {heads}, {width}] on cuda:{device}, got {x.dtype} "
+                         f"{tuple(shape)} on {x.device}")
+    L = shape[-3]
+    if L == 0 or (not packed and B == 0):
         return L, heads * width
-    row = x.stride(-3) if L > 1 else (x.stride(0) if dims == 4 and B > 1 else heads * width)
-    if (x.stride(-1) != 1 or (heads > 1 and x.stride(-2) != width)
-            or (dims == 4 and B > 1 and x.stride(0) != L * row)):
-        raise ValueError(f"{name}: heads and channels must be contiguous and rows evenly spaced, strides {x.stride()}")
+    row = stride[-3] if L > 1 else (stride[0] if not packed and B > 1 else heads * width)
+    if stride[-1] != 1 or (heads > 1 and stride[-2] != width) or (not packed and B > 1 and stride[0] != L * row):
+        raise ValueError(f"{name}: heads and channels must be contiguous and rows evenly spaced, strides {stride}")
     return L, row
+
+
+def _kv4_weights(key_weights, B, cache, device):
+    if (key_weights.dtype != torch.float32 or key_weights.get_device() != device or not key_weights.is_contiguous()
+            or key_weights.dim() != 3 or key_weights.shape[0] != B or key_weights.shape[1] != cache.Hkv):
+        raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on cuda:{device}")
 
 
 def _kv4_out(t, shape, dtype, device, name):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
     return t
 
 
-class _On:
+_kv4_workspace = functools.lru_cache(maxsize=4096)(attn_kv4_fwd_workspace_size)   # a function of the sizes alone
+
+
+def _on(stream):
     """Allocations inside belong to the stream that the call runs on."""
-
-    def __init__(self, stream):
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        self.context = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.context is not None:
-            self.context.__enter__()
-
-    def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def kv4_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=None):
     """Quantise new keys and values (bf16 [T, Hkv, d] with int32 cu_seqlens, or [B, L, Hkv, d]) into the pages of
     their sequences. cache_lens (int32 [B]) counts the new tokens already: sequence b's n rows become its tokens
     cache_lens[b] - n .. cache_lens[b] - 1. Rows of k and v may be strided (a slice of a fused projection)."""
-    B, device = cache_lens.shape[0], cache.k_codes.device
-    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, cu_seqlens=cu_seqlens)
-    L, k_stride = _kv4_rows(k, cache.Hkv, cache.d, B, cu_seqlens, "k", device)
-    Lv, v_stride = _kv4_rows(v, cache.Hkv, cache.dv, B, cu_seqlens, "v", device)
+    B, device = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    L, k_stride = _kv4_rows(k, cache.Hkv, cache.d, B, cu_seqlens is not None, "k", device)
+    Lv, v_stride = _kv4_rows(v, cache.Hkv, cache.dv, B, cu_seqlens is not None, "v", device)
     if L != Lv:
         raise ValueError(f"k has {L} rows, v {Lv}")
     _check(attn_kv4_append(k, v, k_stride, v_stride, cache._struct, page_table, page_table.shape[1], cache_lens,
@@ -548,10 +552,10 @@ def kv4_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=None
 def kv4_read(cache, page_table, cache_lens, rows, cu_seqlens=None, k=None, v=None, stream=None):
     """K, V in bf16 as the cache stands for them: the last rows of every sequence, packed ([rows, Hkv, d], rows =
     cu_seqlens[-1]) or dense (rows per sequence; [B, rows, Hkv, d], zero before a sequence's first token)."""
-    B, device = cache_lens.shape[0], cache.k_codes.device
-    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, cu_seqlens=cu_seqlens)
+    B, _ = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    device = cache.k_codes.device
     lead = (rows,) if cu_seqlens is not None else (B, rows)
-    with _On(stream):
+    with _on(stream):
         k = _kv4_out(k, lead + (cache.Hkv, cache.d), torch.bfloat16, device, "k")
         v = _kv4_out(v, lead + (cache.Hkv, cache.dv), torch.bfloat16, device, "v")
     _check(attn_kv4_read(k, v, cache._struct, page_table, page_table.shape[1], cache_lens, cu_seqlens, B, rows, stream))
@@ -564,20 +568,17 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     """O, LSE of new tokens q (bf16 [T, H, d] with cu_seqlens, or [B, L, H, d]) over their sequence's cache, to which
     their keys have been appended. window and sinks as in forward(). key_weights (fp32 [B, Hkv, >= longest cache]):
     updated in place to weight_decay * key_weights + the attention weight each key got from the call's rows."""
-    B, device = cache_lens.shape[0], cache.k_codes.device
-    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, cu_seqlens=cu_seqlens)
-    H = q.shape[-2]
-    L, q_stride = _kv4_rows(q, H, cache.d, B, cu_seqlens, "q", device)
+    B, index = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    H, packed, device = q.shape[-2], cu_seqlens is not None, cache.k_codes.device
+    L, q_stride = _kv4_rows(q, H, cache.d, B, packed, "q", index)
     if H % cache.Hkv != 0 or H == 0:
         raise ValueError(f"{H} query heads over {cache.Hkv} key/value heads")
-    if key_weights is not None and (key_weights.dtype != torch.float32 or key_weights.device != device
-                                    or not key_weights.is_contiguous() or key_weights.dim() != 3
-                                    or tuple(key_weights.shape[:2]) != (B, cache.Hkv)):
-        raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on {device}")
+    if key_weights is not None:
+        _kv4_weights(key_weights, B, cache, index)
     scale = 1.0 / math.sqrt(cache.d) if scale is None else scale
-    width, packed = page_table.shape[1], cu_seqlens is not None
-    need = attn_kv4_fwd_workspace_size(B, H, cache.Hkv, L, packed, width, cache.d, cache.dv, key_weights is not None)
-    with _On(stream):
+    width = page_table.shape[1]
+    need = _kv4_workspace(B, H, cache.Hkv, L, packed, width, cache.d, cache.dv, key_weights is not None)
+    with _on(stream):
         out = _kv4_out(out, q.shape[:-1] + (cache.dv,), torch.bfloat16, device, "out")
         lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, device, "lse")
         if workspace is None:
@@ -595,13 +596,11 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
     `recent` and those between with the largest key_weights, in the pages of new_table (pages of the same cache that
     are not in page_table). Returns new_lens int32 [B], kept int32 [B, Hkv, budget] (old token of each new one, -1 past
     the new length) and the kept key weights fp32 [B, Hkv, budget] (or as wide as new_key_weights is)."""
-    B, device = cache_lens.shape[0], cache.k_codes.device
-    _kv4_ints(cache, B, page_table=page_table, cache_lens=cache_lens, new_table=new_table)
-    if (key_weights.dtype != torch.float32 or key_weights.device != device or not key_weights.is_contiguous()
-            or key_weights.dim() != 3 or tuple(key_weights.shape[:2]) != (B, cache.Hkv)):
-        raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on {device}")
+    B, index = _kv4_ints(cache, page_table, cache_lens, None, new_table)
+    device = cache.k_codes.device
+    _kv4_weights(key_weights, B, cache, index)
     columns = budget if new_key_weights is None else new_key_weights.shape[-1]
-    with _On(stream):
+    with _on(stream):
         new_lens = _kv4_out(new_lens, (B,), torch.int32, device, "new_lens")
         kept = _kv4_out(kept, (B, cache.Hkv, budget), torch.int32, device, "kept")
         new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, device, "new_key_weights")

@@ -1,5 +1,7 @@
 // The 4-bit key/value cache: append (quantise), read (dequantise) and evict.
 // All three are bound by memory: each value is touched once.
+#include <type_traits>
+
 #include "kv4.h"
 #include "ptx.cuh"
 
@@ -54,106 +56,142 @@ __device__ __forceinline__ uint32_t code_of(float x, float lo, float s, float in
     return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);   // (NaN gives 0)
 }
 
-// Eight lanes quantise one group of 64 channels of one token and head: 16 bytes
-// of bf16 in and 4 bytes of codes out per lane, the group's extremes by three
-// shuffles.
+// Where a packed row lives: its page and slot, or page -1: nowhere (out of
+// range, reported), -2: no such row (past the last sequence), -3: before the
+// sequence's first token (a padded dense batch).
+struct RowPlace {
+    int page, slot;
+};
+__device__ __forceinline__ RowPlace place_of(const Kv4Cache& c, const Kv4Batch& s, int t, int* status) {
+    RowPlace r{-2, 0};
+    if (t >= s.total) return r;
+    const int b = kv4_seq_of_row(s, t);
+    if (b < 0) return r;
+    const Kv4Seq q = kv4_seq(s, b);
+    const int slot = q.lk - q.nq + t - q.q0;
+    r.page = -1;
+    if (!q.bad && slot < 0) r.page = -3;
+    if (!q.bad && slot >= 0) {
+        r.slot = slot % kPage;
+        r.page = s.table[(long)b * s.width + slot / kPage];
+        if (r.page < 0 || r.page >= c.n_pages) r.page = -1;
+    }
+    if (r.page == -1) bad_page(status);
+    return r;
+}
+
+// A warp takes `rows` (1 to 4) consecutive rows, whose places its first lanes
+// look up together, and walks their groups of 64 channels four at a time, eight
+// lanes per group: 16 bytes of bf16 and 4 bytes of codes per lane, the extremes
+// by three shuffles. GK, GV: groups of a head.
+template <int GK, int GV>
 __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4Cache c, Kv4Batch s, const __nv_bfloat16* k,
                                                          const __nv_bfloat16* v, long k_stride, long v_stride,
-                                                         int* status) {
-    const int gk = c.d / kKv4Group, gv = c.dv / kKv4Group, per_head = gk + gv;
-    const long chunks = (long)s.total * c.Hkv * per_head;
-    const long step = (long)gridDim.x * blockDim.x / 8;
-    const int l8 = threadIdx.x & 7;
-    for (long i0 = ((long)blockIdx.x * blockDim.x + threadIdx.x) / 8; i0 - (threadIdx.x & 31) / 8 < chunks; i0 += step) {
-        const bool live = i0 < chunks;   // (the warp's four groups stay together for the shuffles)
-        const long i = live ? i0 : 0;
-        const int t = (int)(i / (c.Hkv * per_head));
-        const int rem = (int)(i - (long)t * c.Hkv * per_head);
-        const int h = rem / per_head, gi = rem - h * per_head;
-        const bool is_v = gi >= gk;
-        const int g = is_v ? gi - gk : gi, groups = is_v ? gv : gk;
-        const int width = groups * kKv4Group;
-        const __nv_bfloat16* src = (is_v ? v + t * v_stride : k + t * k_stride) + h * width + g * kKv4Group + l8 * 8;
-        const uint4 raw = *reinterpret_cast<const uint4*>(src);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        float x[8];
+                                                         int rows, int* status) {
+    const int lane = threadIdx.x & 31, l8 = lane & 7;
+    const int t0 = (blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * rows;
+    RowPlace mine{-2, 0};
+    if (lane < rows) {
+        mine = place_of(c, s, t0 + lane, status);
+        if (mine.page == -3) bad_page(status);   // more new rows than the cache holds tokens
+    }
+    const int chunks = c.Hkv * (GK + GV);
+    for (int x = 0; x < rows; ++x) {
+        const int page = __shfl_sync(kFullMask, mine.page, x), slot = __shfl_sync(kFullMask, mine.slot, x);
+        if (page < 0) continue;
+        const long t = t0 + x;
+        for (int c0 = 0; c0 < chunks; c0 += 8) {   // two groups per lane octet: their loads go out together
+            uint4 raw[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-        float lo = x[0], hi = x[0];
+            for (int y = 0; y < 2; ++y) {
+                const int ch = min(c0 + 4 * y + (lane >> 3), chunks - 1);
+                const int h = ch / (GK + GV), gi = ch - h * (GK + GV);
+                raw[y] = __ldg(reinterpret_cast<const uint4*>(
+                    (gi >= GK ? v + t * v_stride + (h * GV + gi - GK) * kKv4Group : k + t * k_stride + (h * GK + gi) * kKv4Group) +
+                    l8 * 8));
+            }
 #pragma unroll
-        for (int j = 1; j < 8; ++j) {
-            lo = min_nan(lo, x[j]);
-            hi = max_nan(hi, x[j]);
-        }
+            for (int y = 0; y < 2; ++y) {
+                const int ch = c0 + 4 * y + (lane >> 3);
+                const uint32_t w[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
+                float f[8];
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(kFullMask, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(kFullMask, hi, o));
-        }
-        if (!live) continue;
-        const float sc = scale_of(lo, hi);
-        const float inv = sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
-        uint32_t codes = 0;
-        if (sc > 0.f) {
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] = __uint_as_float(w[j] << 16);
+                    f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                }
+                float lo = f[0], hi = f[0];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) codes |= code_of(x[j], lo, sc, inv) << (4 * j);
+                for (int j = 1; j < 8; ++j) {
+                    lo = min_nan(lo, f[j]);
+                    hi = max_nan(hi, f[j]);
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    lo = min_nan(lo, __shfl_xor_sync(kFullMask, lo, o));
+                    hi = max_nan(hi, __shfl_xor_sync(kFullMask, hi, o));
+                }
+                if (ch >= chunks) continue;
+                const float sc = scale_of(lo, hi);
+                uint32_t codes = 0;
+                if (sc > 0.f) {
+                    const float inv = __fdiv_rn(1.f, sc);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) codes |= code_of(f[j], lo, sc, inv) << (4 * j);
+                }
+                const int h = ch / (GK + GV), gi = ch - h * (GK + GV);
+                const bool is_v = gi >= GK;
+                const long row = (is_v ? (((long)page * c.Hkv + h) * GV + gi - GK) : (((long)page * c.Hkv + h) * GK + gi)) * kPage + slot;
+                reinterpret_cast<uint32_t*>(is_v ? c.v_codes : c.k_codes)[row * 8 + l8] = codes;
+                if (l8 == 0)
+                    (is_v ? c.v_params : c.k_params)[row] = (__float_as_uint(sc) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+            }
         }
-        const int b = kv4_seq_of_row(s, t);
-        if (b < 0) continue;
-        const Kv4Seq q = kv4_seq(s, b);
-        const int slot = q.lk - q.nq + t - q.q0;
-        int page = -1;
-        if (!q.bad && slot >= 0) page = s.table[(long)b * s.width + slot / kPage];
-        if (page < 0 || page >= c.n_pages) {
-            bad_page(status);
-            continue;
-        }
-        const long row = (((long)page * c.Hkv + h) * groups + g) * kPage + slot % kPage;
-        reinterpret_cast<uint32_t*>(is_v ? c.v_codes : c.k_codes)[row * 8 + l8] = codes;
-        if (l8 == 0)
-            (is_v ? c.v_params : c.k_params)[row] = (__float_as_uint(sc) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
     }
 }
 
-// Eight lanes restore one group: 4 bytes of codes in, 16 bytes of bf16 out.
+// The inverse on the same walk: 4 bytes of codes in, 16 bytes of bf16 out per lane.
+template <int GK, int GV>
 __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Cache c, Kv4Batch s, __nv_bfloat16* k, __nv_bfloat16* v,
-                                                       int* status) {
-    const int gk = c.d / kKv4Group, gv = c.dv / kKv4Group, per_head = gk + gv;
-    const long chunks = (long)s.total * c.Hkv * per_head;
-    const long step = (long)gridDim.x * blockDim.x / 8;
-    const int l8 = threadIdx.x & 7;
-    for (long i = ((long)blockIdx.x * blockDim.x + threadIdx.x) / 8; i < chunks; i += step) {
-        const int t = (int)(i / (c.Hkv * per_head));
-        const int rem = (int)(i - (long)t * c.Hkv * per_head);
-        const int h = rem / per_head, gi = rem - h * per_head;
-        const bool is_v = gi >= gk;
-        const int g = is_v ? gi - gk : gi, groups = is_v ? gv : gk;
-        const int b = kv4_seq_of_row(s, t);
-        if (b < 0) continue;
-        const Kv4Seq q = kv4_seq(s, b);
-        const int slot = q.lk - q.nq + t - q.q0;
-        uint4 out = make_uint4(0, 0, 0, 0);
-        int page = -1;
-        if (!q.bad && slot >= 0) page = s.table[(long)b * s.width + slot / kPage];
-        if (page >= 0 && page < c.n_pages) {
-            const long row = (((long)page * c.Hkv + h) * groups + g) * kPage + slot % kPage;
-            const uint32_t w = reinterpret_cast<const uint32_t*>(is_v ? c.v_codes : c.k_codes)[row * 8 + l8];
-            const uint32_t p = (is_v ? c.v_params : c.k_params)[row];
-            const float sc = __uint_as_float(p << 16), lo = __uint_as_float(p & 0xffff0000u);
-            uint32_t r[4];
+                                                       int rows, int* status) {
+    const int lane = threadIdx.x & 31, l8 = lane & 7;
+    const int t0 = (blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * rows;
+    RowPlace mine{-2, 0};
+    if (lane < rows) mine = place_of(c, s, t0 + lane, status);
+    const int chunks = c.Hkv * (GK + GV);
+    for (int x = 0; x < rows; ++x) {
+        const int page = __shfl_sync(kFullMask, mine.page, x), slot = __shfl_sync(kFullMask, mine.slot, x);
+        if (page == -2) continue;
+        const long t = t0 + x;
+        for (int c0 = 0; c0 < chunks; c0 += 16) {   // four groups per lane octet: their loads go out together
+            uint32_t w[4], p[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                r[j] = pack_bf16x2(fmaf((float)((w >> (8 * j)) & 15u), sc, lo),
-                                   fmaf((float)((w >> (8 * j + 4)) & 15u), sc, lo));
-            out = make_uint4(r[0], r[1], r[2], r[3]);
-        } else if (q.bad || slot >= 0) {
-            bad_page(status);
-        }   // (a row before the cache's first token reads as zero)
-        __nv_bfloat16* dst = (is_v ? v : k) + ((long)t * c.Hkv + h) * (groups * kKv4Group) + g * kKv4Group + l8 * 8;
-        *reinterpret_cast<uint4*>(dst) = out;
+            for (int y = 0; y < 4; ++y) {
+                const int ch = c0 + 4 * y + (lane >> 3);
+                const int h = ch / (GK + GV), gi = ch - h * (GK + GV);
+                const bool is_v = gi >= GK;
+                const long row = (is_v ? (((long)page * c.Hkv + h) * GV + gi - GK) : (((long)page * c.Hkv + h) * GK + gi)) * kPage + slot;
+                w[y] = p[y] = 0;   // (a row that lies nowhere reads as zero)
+                if (page >= 0 && ch < chunks) {
+                    w[y] = __ldg(reinterpret_cast<const uint32_t*>(is_v ? c.v_codes : c.k_codes) + row * 8 + l8);
+                    p[y] = __ldg((is_v ? c.v_params : c.k_params) + row);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int ch = c0 + 4 * y + (lane >> 3);
+                if (ch >= chunks) continue;
+                const int h = ch / (GK + GV), gi = ch - h * (GK + GV);
+                const float sc = __uint_as_float(p[y] << 16), lo = __uint_as_float(p[y] & 0xffff0000u);
+                uint32_t r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    r[j] = pack_bf16x2(fmaf((float)((w[y] >> (8 * j)) & 15u), sc, lo),
+                                       fmaf((float)((w[y] >> (8 * j + 4)) & 15u), sc, lo));
+                __nv_bfloat16* dst = gi >= GK ? v + ((t * c.Hkv + h) * GV + gi - GK) * kKv4Group : k + ((t * c.Hkv + h) * GK + gi) * kKv4Group;
+                __stcs(reinterpret_cast<uint4*>(dst + l8 * 8), make_uint4(r[0], r[1], r[2], r[3]));
+            }
+        }
     }
 }
 
@@ -165,17 +203,22 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024, kSelBins = 2048;
+constexpr int kSelKeys = 49152;   // keys of a row that stay in shared memory; those behind are read again
 
-// One CTA per (sequence, head): the slots it keeps, ascending. The need-th
-// largest key of the middle is found by four rounds of 8-bit histograms (radix
-// select); then one ordered pass writes the kept slots, equal weights in slot
-// order.
-__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams p) {
-    __shared__ int hist[256];
-    __shared__ int warp_sum[kSelThreads / 32];
+// One CTA per (sequence, head): the slots it keeps, ascending. The weights are
+// read once into shared memory; the need-th largest key of the middle is found
+// digit by digit (11, 11 and 10 bits, a histogram each); then one ordered pass
+// writes the kept slots. Of the keys equal to the threshold the first `need`
+// stay, so a slot's place is (slots kept above the threshold before it) +
+// min(threshold slots before it, need): one scan of two counts.
+__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams p, int cap) {
+    extern __shared__ uint32_t keys[];   // cap of them
+    __shared__ int hist[kSelBins];
+    __shared__ int2 warp_sum[kSelThreads / 32];
     __shared__ uint32_t s_prefix;
     __shared__ int s_need;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x % p.c.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int n = p.lens[b];
@@ -191,149 +234,229 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams 
     if (h == 0 && tid == 0) p.new_lens[b] = m;
     const bool all = n <= p.budget;
     const int lo = all ? n : p.sinks, hi = all ? n : n - p.recent;   // the middle [lo, hi)
-    if (tid == 0) {
-        s_prefix = 0;
-        s_need = all ? 0 : m - p.sinks - p.recent;
-    }
-    __syncthreads();
+    const bool some = !all && m > p.sinks + p.recent;                // some of the middle stay
     uint32_t prefix = 0;
-    int need = s_need;
-    // (need == 0: no key of the middle stays)
-    for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-            const uint32_t key = weight_key(w[j]);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {   // from the largest digit down, the one that holds the need-th key
-            int cnt[8], sum = 0;
+    int need = some ? m - p.sinks - p.recent : 0;
+    if (some) {
+        auto key_at = [&](int j) { return j < cap ? keys[j] : weight_key(__ldg(w + j)); };
+        constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += cnt[i] = hist[255 - (lane * 8 + i)];
-            int before = sum;
+        for (int d = 0; d < 3; ++d) {
+            for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+            const uint32_t mask = d == 0 ? 0u : 0xffffffffu << kShift[d - 1], digit = (1u << kBits[d]) - 1;
+#pragma unroll 4
+            for (int j = lo + tid; j < hi; j += kSelThreads) {
+                uint32_t key;
+                if (d == 0) {
+                    key = weight_key(__ldg(w + j));
+                    if (j < cap) keys[j] = key;
+                } else {
+                    key = key_at(j);
+                }
+                if ((key & mask) == prefix) atomicAdd(&hist[(key >> kShift[d]) & digit], 1);
+            }
+            __syncthreads();
+            // the digit that holds the need-th key, counted from the largest: two bins per thread
+            const int bins = 1 << kBits[d], top = bins - 1 - 2 * tid;
+            const int c0 = 2 * tid < bins ? hist[top] : 0, c1 = 2 * tid < bins ? hist[top - 1] : 0;
+            int before = c0 + c1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(kFullMask, before, o);
                 if (lane >= o) before += x;
             }
-            before -= sum;
-            for (int i = 0; i < 8; ++i) {
-                if (before < need && need <= before + cnt[i]) {
-                    s_prefix = prefix | (uint32_t)(255 - (lane * 8 + i)) << shift;
-                    s_need = need - before;
-                }
-                before += cnt[i];
+            if (lane == 31) warp_sum[warp].x = before;
+            before -= c0 + c1;
+            __syncthreads();
+            for (int i = 0; i < warp; ++i) before += warp_sum[i].x;
+            if (before < need && need <= before + c0) {
+                s_prefix = prefix | (uint32_t)top << kShift[d];
+                s_need = need - before;
+            } else if (before + c0 < need && need <= before + c0 + c1) {
+                s_prefix = prefix | (uint32_t)(top - 1) << kShift[d];
+                s_need = need - before - c0;
+            }
+            __syncthreads();
+            prefix = s_prefix;
+            need = s_need;
+        }
+    }
+    int above0 = 0, ties0 = 0;   // slots kept above the threshold, and threshold slots, so far
+    for (int j0 = 0; j0 < n; j0 += 4 * kSelThreads) {
+        const int j = j0 + 4 * tid;
+        uint32_t ab = 0, ti = 0;   // bits: slot j + i stays anyway, is at the threshold
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (j + i >= n) break;
+            if (j + i < lo || j + i >= hi) {
+                ab |= 1u << i;
+            } else if (some) {
+                const uint32_t key = j + i < cap ? keys[j + i] : weight_key(__ldg(w + j + i));
+                ab |= (key > prefix ? 1u : 0u) << i;
+                ti |= (key == prefix ? 1u : 0u) << i;
             }
         }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
-        __syncthreads();
-    }
-    // ordered pass: slot j stays if it is outside the middle, above the threshold,
-    // or at the threshold among the first `need`
-    const bool some = !all && m > p.sinks + p.recent;
-    int base = 0, ties = 0;   // kept slots and threshold slots so far
-    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const bool in = j < n, mid = in && j >= lo && j < hi;
-        const float x = in ? w[j] : 0.f;
-        const uint32_t key = mid ? weight_key(x) : 0u;
-        const bool tie = mid && some && key == prefix;
-        const unsigned tb = __ballot_sync(kFullMask, tie);
-        if (lane == 0) warp_sum[warp] = __popc(tb);
-        __syncthreads();
-        int tie_rank = ties + __popc(tb & ((1u << lane) - 1));
-        int tie_total = 0;
+        int2 c = make_int2(__popc(ab), __popc(ti));
+        const int2 own = c;
 #pragma unroll
-        for (int i = 0; i < kSelThreads / 32; ++i) {
-            if (i < warp) tie_rank += warp_sum[i];
-            tie_total += warp_sum[i];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFullMask, c.x, o), y = __shfl_up_sync(kFullMask, c.y, o);
+            if (lane >= o) {
+                c.x += x;
+                c.y += y;
+            }
         }
+        __syncthreads();   // the sums of the previous step have been read
+        if (lane == 31) warp_sum[warp] = c;
         __syncthreads();
-        const bool keep = in && (!mid || (some && (key > prefix || (tie && tie_rank < need))));
-        const unsigned kb = __ballot_sync(kFullMask, keep);
-        if (lane == 0) warp_sum[warp] = __popc(kb);
-        __syncthreads();
-        int at = base + __popc(kb & ((1u << lane) - 1)), total = 0;
+        int2 total = warp_sum[lane];   // (32 warps) prefix over the warps by every warp
+        const int2 mine = total;
 #pragma unroll
-        for (int i = 0; i < kSelThreads / 32; ++i) {
-            if (i < warp) at += warp_sum[i];
-            total += warp_sum[i];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFullMask, total.x, o), y = __shfl_up_sync(kFullMask, total.y, o);
+            if (lane >= o) {
+                total.x += x;
+                total.y += y;
+            }
         }
-        if (keep && at < m) {
-            kept[at] = j;
-            nw[at] = x;
+        int above = above0 + c.x - own.x + __shfl_sync(kFullMask, total.x - mine.x, warp);
+        int ties = ties0 + c.y - own.y + __shfl_sync(kFullMask, total.y - mine.y, warp);
+        above0 += __shfl_sync(kFullMask, total.x, 31);
+        ties0 += __shfl_sync(kFullMask, total.y, 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool a = (ab >> i) & 1u, e = (ti >> i) & 1u;
+            if (a || (e && ties < need)) {
+                const int at = above + min(ties, need);
+                if (at < m) {
+                    kept[at] = j + i;
+                    nw[at] = __ldg(w + j + i);
+                }
+            }
+            above += a;
+            ties += e;
         }
-        base += total;
-        ties += tie_total;
-        __syncthreads();
     }
     for (int i = m + tid; i < p.budget; i += kSelThreads) kept[i] = -1;
     for (long i = m + tid; i < p.new_stride; i += kSelThreads) nw[i] = 0.f;
 }
 
-// Two lanes copy one 32-byte row of codes; the first also its parameters.
-__global__ void __launch_bounds__(256) kv4_gather_kernel(Kv4EvictParams p) {
-    const int gk = p.c.d / kKv4Group, gv = p.c.dv / kKv4Group, per = gk + gv;
-    const long rows = (long)p.B * p.c.Hkv * p.budget * per;
-    const long step = (long)gridDim.x * blockDim.x / 2;
-    const int half = threadIdx.x & 1;
-    for (long i = ((long)blockIdx.x * blockDim.x + threadIdx.x) / 2; i < rows; i += step) {
-        // consecutive lane pairs: consecutive kept slots of one group
-        const long bhg = i / p.budget;
-        const int at = (int)(i - bhg * p.budget);
-        const int gi = (int)(bhg % per);
-        const long bh = bhg / per;
-        const int b = (int)(bh / p.c.Hkv), h = (int)(bh % p.c.Hkv);
-        const int j = p.kept[bh * p.budget + at];
-        if (j < 0) continue;
-        const int src = p.table[(long)b * p.width + j / kPage], dst = p.new_table[(long)b * p.new_width + at / kPage];
-        if (src < 0 || src >= p.c.n_pages || dst < 0 || dst >= p.c.n_pages) {
-            bad_page(p.status);
-            continue;
+// One CTA copies 64 kept tokens of one (sequence, head) to one new page: rows of
+// 32 bytes of codes, two lanes each, and their parameters.
+template <int GK, int GV>
+__global__ void __launch_bounds__(256) kv4_gather_kernel(Kv4EvictParams p, int tiles) {
+    __shared__ int src_page[kPage], src_slot[kPage];   // page -1: no such token
+    const int bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles;
+    const int b = bh / p.c.Hkv, h = bh - b * p.c.Hkv, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int dst = p.new_table[(long)b * p.new_width + tile];
+    if (tid < kPage) {
+        const int at = tile * kPage + tid;
+        const int j = at < p.budget ? p.kept[(long)bh * p.budget + at] : -1;
+        int src = -1;
+        if (j >= 0) {
+            src = p.table[(long)b * p.width + j / kPage];
+            if (src < 0 || src >= p.c.n_pages || dst < 0 || dst >= p.c.n_pages) {
+                src = -1;
+                bad_page(p.status);
+            }
         }
-        const bool is_v = gi >= gk;
-        const int g = is_v ? gi - gk : gi, groups = is_v ? gv : gk;
-        const long from = (((long)src * p.c.Hkv + h) * groups + g) * kPage + j % kPage;
-        const long to = (((long)dst * p.c.Hkv + h) * groups + g) * kPage + at % kPage;
-        uint4* codes = reinterpret_cast<uint4*>(is_v ? p.c.v_codes : p.c.k_codes);
+        src_page[tid] = src;
+        src_slot[tid] = j % kPage;
+    }
+    __syncthreads();
+    constexpr int kGroups = GK + GV;
+    // the codes: consecutive lane pairs take consecutive tokens of one group
+#pragma unroll
+    for (int i = tid; i < kGroups * kPage * 2; i += 256) {
+        const int g = i / (2 * kPage), x = (i / 2) % kPage, half = i & 1;
+        if (src_page[x] < 0) continue;
+        uint4* codes = reinterpret_cast<uint4*>(g >= GK ? p.c.v_codes : p.c.k_codes);
+        const int groups = g >= GK ? GV : GK, gi = g >= GK ? g - GK : g;
+        const long from = (((long)src_page[x] * p.c.Hkv + h) * groups + gi) * kPage + src_slot[x];
+        const long to = (((long)dst * p.c.Hkv + h) * groups + gi) * kPage + x;
         codes[to * 2 + half] = codes[from * 2 + half];
-        uint32_t* params = is_v ? p.c.v_params : p.c.k_params;
-        if (half == 0) params[to] = params[from];
+    }
+#pragma unroll
+    for (int i = tid; i < kGroups * kPage; i += 256) {
+        const int g = i / kPage, x = i % kPage;
+        if (src_page[x] < 0) continue;
+        uint32_t* params = g >= GK ? p.c.v_params : p.c.k_params;
+        const int groups = g >= GK ? GV : GK, gi = g >= GK ? g - GK : g;
+        params[(((long)dst * p.c.Hkv + h) * groups + gi) * kPage + x] =
+            params[(((long)src_page[x] * p.c.Hkv + h) * groups + gi) * kPage + src_slot[x]];
     }
 }
 
-int blocks_for(long threads, int block) {
-    const long n = (threads + block - 1) / block;
-    return (int)(n < 1 ? 1 : (n > 152 * 16 ? 152 * 16 : n));
+// Rows per warp: one while that gives fewer than 16 warps per SM, else four,
+// which look their places up together.
+int rows_per_warp(int total) { return total >= 152 * 16 ? 4 : 1; }
+
+template <int GK, int GV>
+cudaError_t append_dims(const Kv4Cache& c, const Kv4Batch& s, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                        long k_stride, long v_stride, int* status, cudaStream_t stream) {
+    const int rows = rows_per_warp(s.total), per_block = 4 * rows;
+    kv4_append_kernel<GK, GV><<<(s.total + per_block - 1) / per_block, 128, 0, stream>>>(c, s, k, v, k_stride, v_stride,
+                                                                                        rows, status);
+    return cudaGetLastError();
+}
+template <int GK, int GV>
+cudaError_t read_dims(const Kv4Cache& c, const Kv4Batch& s, __nv_bfloat16* k, __nv_bfloat16* v, int* status,
+                      cudaStream_t stream) {
+    const int rows = rows_per_warp(s.total), per_block = 4 * rows;
+    kv4_read_kernel<GK, GV><<<(s.total + per_block - 1) / per_block, 128, 0, stream>>>(c, s, k, v, rows, status);
+    return cudaGetLastError();
+}
+template <int GK, int GV>
+cudaError_t gather_dims(const Kv4EvictParams& p, cudaStream_t stream) {
+    const int tiles = (p.budget + kPage - 1) / kPage;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.B * p.c.Hkv * tiles));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_gather_kernel<GK, GV>, p, tiles);
+}
+
+// call(GK, GV) for the head dims of a cache
+template <class F>
+cudaError_t for_dims(const Kv4Cache& c, F call) {
+    if (c.d == 64 && c.dv == 64) return call(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    if (c.d == 128 && c.dv == 128) return call(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+    if (c.d == 192 && c.dv == 192) return call(std::integral_constant<int, 3>{}, std::integral_constant<int, 3>{});
+    if (c.d == 192 && c.dv == 128) return call(std::integral_constant<int, 3>{}, std::integral_constant<int, 2>{});
+    if (c.d == 256 && c.dv == 256) return call(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4Cache& c, const Kv4Batch& s, const __nv_bfloat16* k, const __nv_bfloat16* v,
                               long k_stride, long v_stride, int* status, cudaStream_t stream) {
-    const long threads = (long)s.total * c.Hkv * ((c.d + c.dv) / kKv4Group) * 8;
-    kv4_append_kernel<<<blocks_for(threads, 256), 256, 0, stream>>>(c, s, k, v, k_stride, v_stride, status);
-    return cudaGetLastError();
+    return for_dims(c, [&](auto gk, auto gv) {
+        return append_dims<gk.value, gv.value>(c, s, k, v, k_stride, v_stride, status, stream);
+    });
 }
 
 cudaError_t launch_kv4_read(const Kv4Cache& c, const Kv4Batch& s, __nv_bfloat16* k, __nv_bfloat16* v, int* status,
                             cudaStream_t stream) {
-    const long threads = (long)s.total * c.Hkv * ((c.d + c.dv) / kKv4Group) * 8;
-    kv4_read_kernel<<<blocks_for(threads, 256), 256, 0, stream>>>(c, s, k, v, status);
-    return cudaGetLastError();
+    return for_dims(c, [&](auto gk, auto gv) { return read_dims<gk.value, gv.value>(c, s, k, v, status, stream); });
 }
 
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream) {
-    kv4_select_kernel<<<p.B * p.c.Hkv, kSelThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const int cap = p.width * kPage < kSelKeys ? p.width * kPage : kSelKeys;
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = allow_smem(kv4_select_kernel, kSelKeys * 4, allowed);
     if (e != cudaSuccess) return e;
-    const long threads = (long)p.B * p.c.Hkv * p.budget * ((p.c.d + p.c.dv) / kKv4Group) * 2;
-    kv4_gather_kernel<<<blocks_for(threads, 256), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    kv4_select_kernel<<<p.B * p.c.Hkv, kSelThreads, cap * 4, stream>>>(p, cap);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return for_dims(p.c, [&](auto gk, auto gv) { return gather_dims<gk.value, gv.value>(p, stream); });
 }
 
 }  // namespace attn

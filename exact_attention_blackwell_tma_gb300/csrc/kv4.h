@@ -10,6 +10,8 @@
 //   params [pages][Hkv][groups][64][2]  bf16
 #pragma once
 
+#include <atomic>
+
 #include "kernels.h"
 #include "mask.cuh"
 
@@ -91,6 +93,21 @@ struct Kv4EvictParams {
     int* status;
 };
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream);
+
+// Allow a kernel `bytes` of dynamic shared memory, asked for once per device
+// (the attribute stays with the kernel; setting it on every call costs a
+// small call's launch a microsecond).
+template <class... Args>
+cudaError_t allow_smem(void (*kernel)(Args...), int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (bit & done.load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 #ifdef __CUDACC__
 // A sequence of a batch: rows [q0, q0 + nq) and lk cached tokens. Lengths out

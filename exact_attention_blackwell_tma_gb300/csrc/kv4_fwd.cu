@@ -114,7 +114,7 @@ struct Kv4Layout {
     static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
     static constexpr int smem(int B) { return kPrefixOff + (B + 1) * 4; }
     // accumulators take NR * DV / 4 registers of a thread
-    static constexpr int kRegCtas = NR * DV <= 128 ? 4 : (NR * DV <= 256 && DV < 256 ? 3 : 2);
+    static constexpr int kRegCtas = NR * DV <= 64 ? 4 : (NR * DV <= 256 && DV < 256 ? 3 : 2);
     static constexpr int kSmemCtas = 227 * 1024 / (smem(64) + 1024);   // (with up to 64 sequences)
     static constexpr int kCtas = kRegCtas < kSmemCtas ? kRegCtas : kSmemCtas;
     static_assert(kCtas >= 1 && smem(kKv4MaxBatch) <= 227 * 1024, "shared memory budget");
@@ -841,9 +841,11 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4Fwd
 template <int D, int DV, int NR>
 cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
     using Lay = Kv4Layout<D, DV, NR>;
-    auto kern = p.key_weights ? kv4_fwd_kernel<D, DV, NR, true> : kv4_fwd_kernel<D, DV, NR, false>;
+    static std::atomic<unsigned long long> allowed[2];
+    const bool scores = p.key_weights != nullptr;
+    auto kern = scores ? kv4_fwd_kernel<D, DV, NR, true> : kv4_fwd_kernel<D, DV, NR, false>;
     const int smem = Lay::smem(p.s.B);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(kern, Lay::smem(kKv4MaxBatch), allowed[scores]);
     if (e != cudaSuccess) return e;
     int grid = num_sms * Lay::kCtas;
     if (grid > kKv4MaxCtas) grid = kKv4MaxCtas;

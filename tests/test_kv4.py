@@ -644,7 +644,7 @@ def test_binding_refuses_tensors():
         binding.Kv4Cache(codes, params[:, :, :, :, :1], codes, params)
     with pytest.raises(ValueError):
         binding.Kv4Cache(codes, params, codes[:2], params[:2])
-    rows = lambda x, B=2, cu=None: binding._kv4_rows(x, 4, 64, B, cu, "q", torch.device("cpu"))  # noqa: E731
+    rows = lambda x, B=2, cu=None: binding._kv4_rows(x, 4, 64, B, cu is not None, "q", -1)  # noqa: E731
     x = torch.zeros(2, 5, 6, 64, dtype=torch.bfloat16)
     assert rows(x[:, :, 1:5]) == (5, 384) and rows(x[0, :, :4], 2, 1) == (5, 384)
     for bad in (x[:, :, :3], x.float()[:, :, :4], x[0, :, :4], x[:, ::2, :4][:, :, :, :32], x[:, :4, :4],
