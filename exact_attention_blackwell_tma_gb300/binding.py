@@ -57,6 +57,8 @@ def _declare(lib):
     lib.attn_fwd_sinks.restype = c_int
     lib.attn_fwd_sinks.argtypes = ([c_void_p] * 5 + [c_int] * 7 + [c_float, c_int, c_int, c_int, c_int, c_void_p,
                                                                      c_void_p, c_void_p])
+    lib.attn_bwd_sinks_workspace_size.restype = c_size_t
+    lib.attn_bwd_sinks_workspace_size.argtypes = [c_int] * 12
     lib.attn_bwd_sinks.restype = c_int
     lib.attn_bwd_sinks.argtypes = ([c_void_p] * 9 + [c_int] * 7 + [c_float, c_int, c_int, c_int, c_int, c_void_p,
                                                                      c_void_p, c_int, c_void_p, c_size_t, c_void_p])
@@ -214,6 +216,12 @@ def attn_fwd_sinks(q, k, v, o, lse, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, wi
     return load().attn_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, Lq, Lk, d, d_v, scale,
                                  int(causal), int(window_left), int(window_right), int(sinks), _ptr(cu_seqlens_q),
                                  _ptr(cu_seqlens_k), _stream(stream))
+
+
+def attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window_left, window_right, sinks,
+                                  deterministic) -> int:
+    return load().attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, int(causal), int(window_left),
+                                                int(window_right), int(sinks), int(deterministic))
 
 
 def attn_bwd_sinks(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left,
@@ -401,7 +409,11 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
     B, H, Lq, Lk, d, Hkv = _dims(q, k, cu_seqlens)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     d_v = v.shape[-1]
-    need = attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic)
+    if sinks:
+        need = attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window[0], window[1], sinks,
+                                             deterministic)
+    else:
+        need = attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     dq = torch.empty_like(q) if dq is None else dq

@@ -323,14 +323,16 @@ extern "C" int attn_fwd(const void* q, const void* k, const void* v, void* o, fl
 namespace {
 
 struct BwdWorkspace {
-    size_t dq_off, delta_off, part_off, sem_off, total;
+    size_t dq_off, delta_off, part_off, sink_off, sem_off, total;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// dQ accumulator | D terms | partial dK/dV slots (split grouped heads) |
-// semaphores | varlen map (placed by the launcher right after the semaphores)
-BwdWorkspace bwd_layout(int B, int H, int Hkv, int Lq, int Lk, int d, int dv, bool varlen) {
+// dQ accumulator | D terms | partial dK/dV slots (split grouped heads) | partials
+// of sink parts | semaphores | varlen map (placed by the launcher right after the
+// semaphores)
+BwdWorkspace bwd_layout(int B, int H, int Hkv, int Lq, int Lk, int d, int dv, bool varlen, int sink_parts = 1,
+                        int sink_blocks = 0) {
     BwdWorkspace w{};
     const size_t rows_q = varlen ? (size_t)Lq : (size_t)B * Lq;
     const long rows_k = varlen ? (long)Lk : (long)B * Lk;
@@ -339,7 +341,8 @@ BwdWorkspace bwd_layout(int B, int H, int Hkv, int Lq, int Lk, int d, int dv, bo
     w.dq_off = 0;
     w.delta_off = align256(rows_q * H * d * sizeof(float));
     w.part_off = w.delta_off + align256(rows_q * H * sizeof(float));
-    w.sem_off = w.part_off + align256(bwd_partial_bytes(split, rows_k, Hkv, d, dv));
+    w.sink_off = w.part_off + align256(bwd_partial_bytes(split, rows_k, Hkv, d, dv));
+    w.sem_off = w.sink_off + align256(sink_partial_bytes(sink_parts, split, B, sink_blocks, Hkv, d, dv));
     w.total = w.sem_off + align256(n_sem * sizeof(int)) + align256(sizeof(VarlenMap));
     return w;
 }
@@ -355,6 +358,19 @@ extern "C" size_t attn_bwd_ex_workspace_size(int B, int H, int Hkv, int Lq, int 
     // the varlen semaphore bound is the larger one, so take the maximum.
     BwdWorkspace a = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, false), b = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, true);
     return a.total > b.total ? a.total : b.total;
+}
+
+extern "C" size_t attn_bwd_sinks_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, int causal,
+                                                int window_left, int window_right, int sinks, int deterministic) {
+    (void)deterministic;
+    if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Lq < 0 || Lk < 0 || d <= 0 || d_v <= 0) return 0;
+    size_t most = 0;
+    for (int varlen = 0; varlen < 2; ++varlen) {   // (sized for both, as attn_bwd_ex_workspace_size)
+        const int parts = sink_part_count(B, Lq, varlen, window_left, causal ? 0 : window_right, sinks);
+        const size_t n = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, varlen, parts, sink_block_count(sinks, Lk)).total;
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 extern "C" size_t attn_bwd_gqa_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int causal,
@@ -394,14 +410,18 @@ int bwd_entry(const void* q, const void* k, const void* v, const void* o, const 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) ||
         !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
         return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
-    const size_t need = attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic);
+    const size_t need = sinks > 0 ? attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window_left,
+                                                                 window_right, sinks, deterministic)
+                                  : attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic);
     if (!workspace || ws_bytes < need)
         return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
     DevInfo di;
     if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
-    BwdWorkspace wl = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, varlen);
+    const int parts = sink_part_count(B, Lq, varlen, window_left, causal ? 0 : window_right, sinks);
+    const int sink_blocks = parts > 1 ? sink_block_count(sinks, Lk) : 0;
+    BwdWorkspace wl = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, varlen, parts, sink_blocks);
     char* ws = static_cast<char*>(workspace);
     BwdParams p{};
     p.g.B = B;
@@ -429,7 +449,10 @@ int bwd_entry(const void* q, const void* k, const void* v, const void* o, const 
     p.dk = static_cast<__nv_bfloat16*>(dk);
     p.dv = static_cast<__nv_bfloat16*>(dv);
     p.deterministic = deterministic ? 1 : 0;
-    p.nm = (Lk + 127) / 128;
+    p.sink_parts = parts;
+    p.sink_blocks = sink_blocks;
+    p.sink_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.sink_off) : nullptr;
+    p.nm = (Lk + 127) / 128 + sink_blocks * (parts - 1);
     p.nq = (Lq + 127) / 128;
     // a work tile is one key block of one key/value head; it streams Q and dO
     // of the query heads of the group (of its share of them when split)

@@ -106,6 +106,7 @@ struct BwdTile {
     const unsigned char* mcol;
     long mstride, mhead;
     int nheads;          // query heads the tile visits
+    int part;            // sinks: which part of a sink block's query range (-1: not one of several)
 };
 
 // The tile's query blocks in visiting order: every query head of its share of
@@ -164,7 +165,7 @@ __device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b :
 // that, with each dQ tile's contributions serialised from its highest key
 // block down, no work tile waits at its first dQ write (FlashAttention-4
 // paper, Section 3.2.4, SPT order).
-template <bool kGQA, bool kBand, bool kSparse, bool kSpt>
+template <bool kGQA, bool kBand, bool kSparse, bool kSpt, bool kSinks>
 __device__ __forceinline__ BwdTile bwd_tile(int t, const BwdParams& p, const VarlenMap* vm, int lane) {
     const Geometry& g = p.g;
     // the split tiles of one key block are neighbours in the walk, so they run
@@ -182,7 +183,8 @@ __device__ __forceinline__ BwdTile bwd_tile(int t, const BwdParams& p, const Var
     // the host by sched_sections_pay); the deterministic kernels keep one global
     // order too, shortest first (SPT), which their dQ turns need.
     const bool spt = kSpt && g.causal;
-    Tile ti = vm ? sched_varlen(*vm, t, g.B, g.Hkv, kBN, p.head_section, spt, true)
+    const int parts = kSinks ? p.sink_parts : 1;
+    Tile ti = vm ? sched_varlen(*vm, t, g.B, g.Hkv, kBN, p.head_section, spt, true, kSinks ? p.sink_blocks : 0, parts - 1)
                  : ((g.causal && (spt || !p.sections)) ? sched_dense_lpt(t, g.B, g.Hkv, p.nm, spt)
                                                         : sched_dense(t, g.Hkv, p.nm, p.head_section, false));
     BwdTile f;
@@ -200,12 +202,29 @@ __device__ __forceinline__ BwdTile bwd_tile(int t, const BwdParams& p, const Var
         f.q_row0 = ti.b * g.Lq;
         f.k_row0 = ti.b * g.Lk;
     }
+    f.part = -1;
+    if constexpr (kSinks) {   // the tiles of a sequence start with the parts of its sink blocks
+        if (parts > 1) {
+            const int nb = (f.lk + kBN - 1) / kBN, ns = nb < p.sink_blocks ? nb : p.sink_blocks;
+            if (f.n < ns * parts) {
+                f.part = f.n % parts;
+                f.n /= parts;
+            } else {
+                f.n -= ns * (parts - 1);
+            }
+        }
+    }
     // the query blocks whose rows see some key of this block (the mask band;
     // none: the tile writes zero dK/dV rows). No mask or the causal one: all
     // blocks, or those from the one holding row n*kBN - (lk - lq) on.
     if constexpr (kBand) {
-        band_query_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks), f.n * kBN,
+        band_query_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, kSinks ? p.mask.sinks : 0), f.n * kBN,
                           f.n * kBN + kBN - 1, kBM, &f.m_begin, &f.m_end);
+        if (kSinks && f.part >= 0) {
+            const int m0 = f.m_begin, len = f.m_end - m0;
+            f.m_begin = m0 + len * f.part / parts;
+            f.m_end = m0 + len * (f.part + 1) / parts;
+        }
     } else {
         f.m_end = (f.lq + kBM - 1) / kBM;
         f.m_begin = 0;
@@ -309,8 +328,42 @@ __global__ void bwd_prep(BwdParams p, VarlenMap* vm_out, long rows_q, long n_acc
         // longest-first map of the sequences (FlashAttention-4 paper, Section 3.3,
         // varlen LPT); work tiles are key blocks (or key-block pairs) of key/value heads
         sched_varlen_build(*vm_out, g.cu_seqlens, g.cu_seqlens_k, g.B, g.Hkv, keys_per_tile, true, threadIdx.x,
-                           blockDim.x);
+                           blockDim.x, p.sink_parts > 1 ? p.sink_blocks : 0, p.sink_parts - 1);
     }
+}
+
+// Sink blocks worked on in parts: dK (scaled) and dV of their key rows as the
+// sum of the parts' slots in order (part-major, then split), fp32 -> bf16, four
+// channels per thread.
+__global__ void bwd_sink_sum(BwdParams p) {
+    const Geometry& g = p.g;
+    const int c4 = (g.d + p.d_v) / 4;
+    const long slot_rows = (long)g.B * p.sink_blocks * kBN * g.Hkv;
+    const long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= slot_rows * c4) return;
+    const int c = (int)(i % c4);
+    const long at = i / c4;   // (b, key, head)
+    const int h = (int)(at % g.Hkv);
+    const long bk = at / g.Hkv;
+    const int b = (int)(bk / (p.sink_blocks * kBN)), key = (int)(bk % (p.sink_blocks * kBN));
+    const int k0 = g.cu_seqlens ? g.cu_seqlens_k[b] : b * g.Lk;
+    const int lk = g.cu_seqlens ? g.cu_seqlens_k[b + 1] - k0 : g.Lk;
+    if (key >= lk) return;
+    const bool is_v = c >= g.d / 4;
+    const int width = is_v ? p.d_v : g.d, col = (is_v ? c - g.d / 4 : c) * 4;
+    const int slots = p.sink_parts * p.split;
+    const float* src = p.sink_part + (is_v ? (long)slots * slot_rows * g.d : 0) + at * width + col;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < slots; ++s) {
+        const float4 x = *reinterpret_cast<const float4*>(src + (long)s * slot_rows * width);
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
+    }
+    const float mul = is_v ? 1.f : g.scale;
+    __nv_bfloat16* dst = (is_v ? p.dv : p.dk) + (((long)k0 + key) * g.Hkv + h) * width + col;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
 }
 
 // Split grouped heads: dK = scale * (sum of the dK slots), dV = sum of the dV
@@ -364,8 +417,9 @@ __global__ void bwd_convert(const float* __restrict__ acc, __nv_bfloat16* __rest
 // kernels for no mask and the causal mask keep their closed forms (a key's
 // query rows run from its diagonal, or from 0, to the sequence's end).
 // kSparse (with kBand only): a block mask is given, the walks skip the blocks
-// it drops.
-template <int HD, bool kDet, bool kGQA, bool kBand, bool kSparse>
+// it drops; kSinks (with kBand, without kSparse): the window has sinks, whose
+// key blocks are worked on in parts (BwdParams::sink_parts).
+template <int HD, bool kDet, bool kGQA, bool kBand, bool kSparse, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -438,7 +492,7 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         bool ok = true;
         float* stats = reinterpret_cast<float*>(smem + Lay::kStatOff);
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             if (kSparse ? f.nblk == 0 : f.m_begin >= f.m_end) continue;
             ok = warp_wait(bar(Lay::kKVEmpty), (tile_it & 1u) ^ 1u, w, lane);
             if (!ok) break;
@@ -570,7 +624,7 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         uint32_t tile_it = 0, qc = 0, pc = 0, dsc = 0, dqf = 0;
         bool ok = true;
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             if (kSparse ? f.nblk == 0 : f.m_begin >= f.m_end) continue;
             ok = warp_wait(bar(Lay::kKVFull), tile_it & 1u, w, lane);
             if (!ok) break;
@@ -766,16 +820,22 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         bool ok = true;
         uint32_t rr[32];
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             const int key = f.n * kBN + r;
             const bool key_ok = key < f.lk;
             const long krow = (long)f.k_row0 + key;
             // this thread's dK/dV row: bf16 outputs, or (split tiles) fp32 partial
             // slots, dK slot f.s and dV slot split + f.s; computed where used, so
             // that no pointer stays live through the query-block loop
-            const bool partial = kGQA && p.split > 1;
+            const bool partial = (kGQA && p.split > 1) || (kSinks && f.part >= 0);
             auto kv_off = [&]() { return (krow * g.Hkv + f.h) * HD + wg * (HD / 2); };
             auto part_slot = [&](int which) {   // 0: dV, 1: dK
+                if (kSinks && f.part >= 0) {   // a part of a sink block
+                    const long rows = (long)g.B * p.sink_blocks * kBN * g.Hkv;   // of a slot
+                    const long at = (((long)f.b * p.sink_blocks + f.n) * kBN + r) * g.Hkv + f.h;
+                    const long sl = (long)f.part * p.split + f.s + (which ? 0 : (long)p.sink_parts * p.split);
+                    return p.sink_part + (sl * rows + at) * HD + wg * (HD / 2);
+                }
                 const long slot = (varlen ? (long)g.Lk : (long)g.B * g.Lk) * g.Hkv * HD;
                 return p.dkv_part + (which ? f.s : p.split + f.s) * slot + kv_off();
             };
@@ -803,7 +863,7 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             // query q is allowed for this key iff q_lo <= q < q_hi (the mask band)
             int q_lo, q_hi;
             if constexpr (kBand) {
-                const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks);
+                const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right, kSinks ? p.mask.sinks : 0);
                 q_lo = key_ok ? band_query_lo(mb, key) : 0;
                 q_hi = key_ok ? band_query_hi(mb, key) : 0;   // (key_ok false: lo = 64 below)
             } else {
@@ -970,7 +1030,7 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             return go && !*abort_flag;
         };
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const BwdTile f = bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             QWalk qw = qwalk_start<kSparse>(f, lane);
             for (int u = 0; u < f.nblk; ++u, qwalk_step<kGQA, kSparse>(qw, f, lane)) {
                 const int m = qw.m;
@@ -1038,9 +1098,11 @@ bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
 // The instantiation for a mask: none or causal; a general band; a band with a block mask.
 template <int HD, bool kDet, bool kGQA>
-auto bwd_kernel_for(bool band, bool sparse) {
-    return sparse ? bwd_kernel<HD, kDet, kGQA, true, true>
-                  : (band ? bwd_kernel<HD, kDet, kGQA, true, false> : bwd_kernel<HD, kDet, kGQA, false, false>);
+auto bwd_kernel_for(bool band, bool sparse, bool sinks) {
+    return sparse ? bwd_kernel<HD, kDet, kGQA, true, true, false>
+                  : (sinks ? bwd_kernel<HD, kDet, kGQA, true, false, true>
+                           : (band ? bwd_kernel<HD, kDet, kGQA, true, false, false>
+                                   : bwd_kernel<HD, kDet, kGQA, false, false, false>));
 }
 
 template <int HD>
@@ -1081,10 +1143,11 @@ cudaError_t launch_bwd_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CU
         using Lay = BwdLayout<HD>;
         const bool gqa = g.group > 1, sparse = p.mask.ptr != nullptr;
         const bool band = sparse || g.win_left >= 0 || g.win_right > 0;
-        auto kern = p.deterministic ? (gqa ? bwd_kernel_for<HD, true, true>(band, sparse)
-                                           : bwd_kernel_for<HD, true, false>(band, sparse))
-                                    : (gqa ? bwd_kernel_for<HD, false, true>(band, sparse)
-                                           : bwd_kernel_for<HD, false, false>(band, sparse));
+        const bool sinks = !sparse && p.mask.sinks > 0;
+        auto kern = p.deterministic ? (gqa ? bwd_kernel_for<HD, true, true>(band, sparse, sinks)
+                                           : bwd_kernel_for<HD, true, false>(band, sparse, sinks))
+                                    : (gqa ? bwd_kernel_for<HD, false, true>(band, sparse, sinks)
+                                           : bwd_kernel_for<HD, false, false>(band, sparse, sinks));
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
         if (e != cudaSuccess) return e;
         cudaFuncAttributes fa;
@@ -1108,6 +1171,12 @@ cudaError_t launch_bwd_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CU
         if (blocks > 8 * num_sms) blocks = 8 * num_sms;
         if (blocks < 1) blocks = 1;
         bwd_dkv_sum<<<blocks, 256, 0, stream>>>(p.dkv_part, p.dk, p.dv, n4k, n4v, p.split, g.scale);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (p.sink_parts > 1) {   // after the split sum, which writes every key row
+        const long n = (long)g.B * p.sink_blocks * kBN * g.Hkv * ((HD + p.d_v) / 4);
+        bwd_sink_sum<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

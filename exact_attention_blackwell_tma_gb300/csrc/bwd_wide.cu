@@ -96,6 +96,7 @@ struct WideBwdTile {
     const unsigned char* mcol;
     long mstride, mhead;
     int nheads;          // query heads the tile visits
+    int part;            // sinks: which part of a sink block's query range (-1: not one of several)
 };
 
 // The tile's query blocks in visiting order: every query head of the tile's
@@ -154,13 +155,14 @@ __device__ __forceinline__ int floor_div_w(int a, int b) { return a >= 0 ? a / b
 // that, with each dQ tile's contributions serialised from its highest key
 // block down, no work tile waits at its first dQ write (FlashAttention-4
 // paper, Section 3.2.4, SPT order).
-template <bool kGQA, bool kBand, bool kSparse, bool kSpt>
+template <bool kGQA, bool kBand, bool kSparse, bool kSpt, bool kSinks>
 __device__ __forceinline__ WideBwdTile wide_bwd_tile(int t, const BwdParams& p, const VarlenMap* vm, int lane) {
     const Geometry& g = p.g;
     const int sp = kGQA ? (t >> 1) % p.split : 0;
     const int u = kGQA ? (t >> 1) / p.split : t >> 1;
     const bool spt = kSpt && g.causal;
-    Tile ti = vm ? sched_varlen(*vm, u, g.B, g.Hkv, kBN, p.head_section, spt, true)
+    const int parts = kSinks ? p.sink_parts : 1;
+    Tile ti = vm ? sched_varlen(*vm, u, g.B, g.Hkv, kBN, p.head_section, spt, true, kSinks ? p.sink_blocks : 0, parts - 1)
                  : (g.causal ? sched_dense_lpt(u, g.B, g.Hkv, p.nm, spt)
                              : sched_dense(u, g.Hkv, p.nm, p.head_section, false));
     WideBwdTile f;
@@ -179,12 +181,29 @@ __device__ __forceinline__ WideBwdTile wide_bwd_tile(int t, const BwdParams& p, 
         f.q_row0 = ti.b * g.Lq;
         f.k_row0 = ti.b * g.Lk;
     }
+    f.part = -1;
+    if constexpr (kSinks) {   // the tiles of a sequence start with the parts of its sink blocks
+        if (parts > 1) {
+            const int nb = (f.lk + kBN - 1) / kBN, ns = nb < p.sink_blocks ? nb : p.sink_blocks;
+            if (f.n < ns * parts) {
+                f.part = f.n % parts;
+                f.n /= parts;
+            } else {
+                f.n -= ns * (parts - 1);
+            }
+        }
+    }
     // the query blocks whose rows see some key of this block (the mask band;
     // none: the tile writes zero dK/dV rows). No mask or the causal one: all
     // blocks, or those from the one holding row n*kBN - (lk - lq) on.
     if constexpr (kBand) {
-        band_query_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks), f.n * kBN,
+        band_query_blocks(mask_band(f.lq, f.lk, g.win_left, g.win_right, kSinks ? p.mask.sinks : 0), f.n * kBN,
                           f.n * kBN + kBN - 1, kBM, &f.m_begin, &f.m_end);
+        if (kSinks && f.part >= 0) {
+            const int m0 = f.m_begin, len = f.m_end - m0;
+            f.m_begin = m0 + len * f.part / parts;
+            f.m_end = m0 + len * (f.part + 1) / parts;
+        }
     } else {
         f.m_end = (f.lq + kBM - 1) / kBM;
         f.m_begin = 0;
@@ -227,7 +246,7 @@ __device__ __forceinline__ WideBwdTile wide_bwd_tile(int t, const BwdParams& p, 
 // kDet: deterministic dQ accumulation (a separate instantiation keeps the
 // other path's code out of each kernel); kGQA: grouped heads; kBand: the mask
 // has a left bound (as in bwd.cu)
-template <int HD, int DV, bool kDet, bool kGQA, bool kBand, bool kSparse>
+template <int HD, int DV, bool kDet, bool kGQA, bool kBand, bool kSparse, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -298,7 +317,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         float* stats = reinterpret_cast<float*>(smem + Lay::kStatOff);
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             if (kSparse ? f.nblk == 0 : f.m_begin >= f.m_end) continue;
             ok = warp_wait(bar(Lay::kKVEmpty), (tile_it & 1u) ^ 1u, w, lane);
             if (!ok) break;
@@ -431,7 +450,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
         };
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             if (kSparse ? f.nblk == 0 : f.m_begin >= f.m_end) continue;
             const int pc = f.c, po = 1 - f.c;
             const bool narrow = chunk_width<HD>(f.c) == 64;
@@ -551,7 +570,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         uint32_t rr[32];
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             const int cw = chunk_width<HD>(f.c);
             const int key = f.n * kBN + r;
             const bool key_ok = key < f.lk;
@@ -559,7 +578,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             // this thread's dK/dV chunk row: bf16 outputs, or (split tiles) fp32
             // partial slots, dK slot f.s and dV slot split + f.s; computed where
             // used, so that no pointer stays live through the query-block loop
-            const bool partial = kGQA && p.split > 1;
+            const bool partial = (kGQA && p.split > 1) || (kSinks && f.part >= 0);
             // columns of the chunk: cw of dK; of dV cw too, or with DV < HD all DV
             // columns in chunk 0 and none in chunk 1
             const int cwv = DV == HD ? cw : (f.c == 0 ? DV : 0);
@@ -568,6 +587,14 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                              : (krow * g.Hkv + f.h) * DV + 128 * f.c + wg * (cwv / 2);
             };
             auto part_slot = [&](int which) {   // dK slots (HD wide) first, then the dV slots (DV wide)
+                if (kSinks && f.part >= 0) {   // a part of a sink block
+                    const long srows = (long)g.B * p.sink_blocks * kBN * g.Hkv;   // of a slot
+                    const long at = (((long)f.b * p.sink_blocks + f.n) * kBN + r) * g.Hkv + f.h;
+                    const long sl = (long)f.part * p.split + f.s;
+                    return which ? p.sink_part + (sl * srows + at) * HD + 128 * f.c + wg * (cw / 2)
+                                 : p.sink_part + (long)p.sink_parts * p.split * srows * HD + (sl * srows + at) * DV +
+                                       128 * f.c + wg * (cwv / 2);
+                }
                 const long rows = (varlen ? (long)g.Lk : (long)g.B * g.Lk) * g.Hkv;
                 return p.dkv_part + (which ? f.s * rows * HD : (p.split * HD + f.s * DV) * rows) + kv_off(which);
             };
@@ -589,7 +616,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             // query q is allowed for this key iff q_lo <= q < q_hi (the mask band)
             int q_lo, q_hi;
             if constexpr (kBand) {
-                const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right, p.mask.sinks);
+                const MaskBand mb = mask_band(f.lq, f.lk, g.win_left, g.win_right, kSinks ? p.mask.sinks : 0);
                 q_lo = key_ok ? band_query_lo(mb, key) : 0;
                 q_hi = key_ok ? band_query_hi(mb, key) : 0;   // (key_ok false: lo = 64 below)
             } else {
@@ -726,7 +753,7 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = true;
         uint32_t rr[32];
         for (int k = 0, t = blockIdx.x; t < n_tiles && ok; t = snake_tile(blockIdx.x, ++k, gridDim.x)) {
-            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet>(t, p, vmp, lane);
+            const WideBwdTile f = wide_bwd_tile<kGQA, kBand, kSparse, kDet, kSinks>(t, p, vmp, lane);
             const int cw = chunk_width<HD>(f.c);
             const int rounds = cw / 64;
             WideQWalk qw = qwalk_start<kSparse>(f, lane);
@@ -798,10 +825,11 @@ bwd_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
 // The instantiation for a mask: none or causal; a general band; a band with a block mask.
 template <int HD, int DV, bool kDet, bool kGQA>
-auto wide_kernel_for(bool band, bool sparse) {
-    return sparse ? bwd_wide_kernel<HD, DV, kDet, kGQA, true, true>
-                  : (band ? bwd_wide_kernel<HD, DV, kDet, kGQA, true, false>
-                          : bwd_wide_kernel<HD, DV, kDet, kGQA, false, false>);
+auto wide_kernel_for(bool band, bool sparse, bool sinks) {
+    return sparse ? bwd_wide_kernel<HD, DV, kDet, kGQA, true, true, false>
+                  : (sinks ? bwd_wide_kernel<HD, DV, kDet, kGQA, true, false, true>
+                           : (band ? bwd_wide_kernel<HD, DV, kDet, kGQA, true, false, false>
+                                   : bwd_wide_kernel<HD, DV, kDet, kGQA, false, false, false>));
 }
 
 template <int HD, int DV>
@@ -811,10 +839,11 @@ cudaError_t launch_wide_hd(const CUtensorMap& tq, const CUtensorMap& tk, const C
     using Lay = WideBwdLayout<HD, DV>;
     const bool gqa = p.g.group > 1, sparse = p.mask.ptr != nullptr;
     const bool band = sparse || p.g.win_left >= 0 || p.g.win_right > 0;
-    auto kern = p.deterministic ? (gqa ? wide_kernel_for<HD, DV, true, true>(band, sparse)
-                                       : wide_kernel_for<HD, DV, true, false>(band, sparse))
-                                : (gqa ? wide_kernel_for<HD, DV, false, true>(band, sparse)
-                                       : wide_kernel_for<HD, DV, false, false>(band, sparse));
+    const bool sinks = !sparse && p.mask.sinks > 0;   // (kSinks: as in bwd.cu)
+    auto kern = p.deterministic ? (gqa ? wide_kernel_for<HD, DV, true, true>(band, sparse, sinks)
+                                       : wide_kernel_for<HD, DV, true, false>(band, sparse, sinks))
+                                : (gqa ? wide_kernel_for<HD, DV, false, true>(band, sparse, sinks)
+                                       : wide_kernel_for<HD, DV, false, false>(band, sparse, sinks));
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;

@@ -73,8 +73,13 @@ struct BwdParams {
     int split;                // tiles per key block of a key/value head (divides g.group)
     int d_v;                  // head dim of v, o, dO, dv (g.d, or 128 with g.d = 192)
     int deterministic;
-    int n_tiles;              // dense: exact count, split included
-    int nm;                   // dense: 128-row K/V blocks per (b, h)
+    // sinks of a local window: the first sink_blocks key blocks of a sequence are
+    // seen to its last row, so each is worked on in sink_parts tiles of their own
+    // query ranges; sink_parts > 1: they leave fp32 partials in sink_part
+    int sink_blocks, sink_parts;
+    float* sink_part;
+    int n_tiles;              // dense: exact count, split and sink parts included
+    int nm;                   // dense: 128-row K/V blocks per (b, h), and with sink parts their tiles
     int nq;                   // dense: 128-row Q blocks per (b, h)
     int head_section;
     int sections;             // causal dense, default mode: walk heads in sections (sched_sections_pay)
@@ -112,6 +117,25 @@ inline int bwd_head_split(int B, int Hkv, int group, int Lk, bool varlen) {
 // Bytes of the partial dK/dV slots for a split (0 when split == 1); dv: head dim of v.
 inline size_t bwd_partial_bytes(int split, long rows_k, int Hkv, int d, int dv) {
     return split > 1 ? (size_t)split * rows_k * Hkv * (d + dv) * sizeof(float) : 0;
+}
+
+// Parts of a sink block: a tile of the window visits about (left + right) / 128
+// + 2 query blocks, a block with sinks all of a sequence's, so it is cut into
+// parts of that length (at most 32). Without parts the longest tile sets the time
+// (B2 H16 L8192 d128, window 1024: a sink block visits 64 query blocks, the
+// others 9; see the backward's launcher for the times).
+constexpr int kMaxSinkParts = 32;
+inline int sink_block_count(int sinks, int Lk) { return ((sinks < Lk ? sinks : Lk) + 127) / 128; }
+inline int sink_part_count(int B, int Lq, bool varlen, int win_left, int win_right, int sinks) {
+    if (sinks <= 0 || win_left < 0 || win_right < 0 || B <= 0) return 1;
+    const long nq = ((varlen ? (long)Lq / B : (long)Lq) + 127) / 128, window = ((long)win_left + win_right + 127) / 128 + 2;
+    const long parts = nq / window;
+    return parts < 1 ? 1 : (parts > kMaxSinkParts ? kMaxSinkParts : (int)parts);
+}
+// Bytes of their partials: dK slots (part-major, then split), then dV slots, of
+// [B][sink_blocks * 128][Hkv] rows.
+inline size_t sink_partial_bytes(int parts, int split, int B, int blocks, int Hkv, int d, int dv) {
+    return parts > 1 ? (size_t)parts * split * B * blocks * 128 * Hkv * (d + dv) * sizeof(float) : 0;
 }
 
 // Launchers (return cudaSuccess or the launch error).

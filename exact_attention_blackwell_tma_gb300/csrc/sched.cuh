@@ -133,10 +133,11 @@ __host__ __device__ __forceinline__ int vm_lk(const VarlenMap& vm, int b) { retu
 // cover query rows (forward), a sequence has heads * ceil(Lq / rows_per_block)
 // of them and sorts by Lk; over_keys = true: tiles cover keys (backward),
 // heads * ceil(Lk / rows_per_block), sorted by Lq. Ties: the other length,
-// then the sequence index.
+// then the sequence index. Each of a sequence's first `long_blocks` blocks counts
+// 1 + extra tiles (the backward's sink parts).
 __device__ __forceinline__ void sched_varlen_build(VarlenMap& vm, const int* cu, const int* cu_k, int B,
                                                    int heads, int rows_per_block, bool over_keys, int tid,
-                                                   int nthreads) {
+                                                   int nthreads, int long_blocks = 0, int extra = 0) {
     for (int i = tid; i <= B; i += nthreads) {
         vm.start[i] = cu[i];
         vm.start_k[i] = cu_k[i];
@@ -158,7 +159,8 @@ __device__ __forceinline__ void sched_varlen_build(VarlenMap& vm, const int* cu,
             vm.pre[k] = acc;
             const int b = vm.order[k];
             const int L = over_keys ? vm_lk(vm, b) : vm_lq(vm, b);
-            acc += heads * ((L + rows_per_block - 1) / rows_per_block);
+            const int nb = (L + rows_per_block - 1) / rows_per_block;
+            acc += heads * (nb + (nb < long_blocks ? nb : long_blocks) * extra);
         }
         vm.pre[B] = acc;
     }
@@ -167,7 +169,8 @@ __device__ __forceinline__ void sched_varlen_build(VarlenMap& vm, const int* cu,
 
 // over_keys as in sched_varlen_build: the tile's row blocks split Lk, else Lq.
 __host__ __device__ __forceinline__ Tile sched_varlen(const VarlenMap& vm, int t, int B, int H, int rows_per_block,
-                                             int hs, bool reverse, bool over_keys) {
+                                             int hs, bool reverse, bool over_keys, int long_blocks = 0,
+                                             int extra = 0) {
     int lo = 0, hi = B - 1;   // largest k with pre[k] <= t
     while (lo < hi) {
         int mid = (lo + hi + 1) >> 1;
@@ -177,7 +180,8 @@ __host__ __device__ __forceinline__ Tile sched_varlen(const VarlenMap& vm, int t
     Tile ti;
     ti.b = vm.order[lo];
     const int L = over_keys ? vm_lk(vm, ti.b) : vm_lq(vm, ti.b);
-    const int nm = (L + rows_per_block - 1) / rows_per_block;
+    const int nb = (L + rows_per_block - 1) / rows_per_block;
+    const int nm = nb + (nb < long_blocks ? nb : long_blocks) * extra;
     sched_within_batch(t - vm.pre[lo], nm, H, hs, reverse, ti.h, ti.m);
     return ti;
 }

@@ -209,9 +209,13 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
  * as there. A work tile visits the key blocks that hold sinks and then the
  * blocks of its rows' window; in the backward a block that holds a sink visits
  * every query row from its diagonal on. Key and value rows of every visited
- * 128-key block must be finite, as for the other masks. workspace:
- * attn_bwd_ex_workspace_size(...) bytes.
+ * 128-key block must be finite, as for the other masks. In the backward a block
+ * that holds sinks may be cut into parts of its query rows, whose fp32 partial
+ * dK and dV a last kernel sums in order (no atomics; the same bits on every run
+ * with deterministic != 0). workspace: attn_bwd_sinks_workspace_size(...) bytes.
  */
+size_t attn_bwd_sinks_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, int causal,
+                                     int window_left, int window_right, int sinks, int deterministic);
 int attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
                    int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, float scale, int causal,
                    int window_left, int window_right, int sinks,

@@ -91,6 +91,22 @@ def test_packed_sequences(d, deterministic):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (192, 128), (256, 256)])
+def test_sink_blocks_in_many_parts(d, dv, deterministic):
+    """A short window over a long sequence: each sink block's queries are worked on in several parts, dense and
+    grouped, and packed with sequences that have fewer key blocks than sinks."""
+    t = inputs.small(B=1, H=4, L=2500, d=d, dv=dv, seed=182, Hkv=2)
+    check(t, True, (20, 0), 200, f"parts d={d} det={deterministic}", deterministic=deterministic)
+    lens = [1900, 0, 90, 1300]
+    cu = inputs.cu_seqlens(lens)
+    g = torch.Generator("cpu").manual_seed(183)
+    r = lambda h, w: torch.randn(int(cu[-1]), h, w, generator=g).to(torch.bfloat16)  # noqa: E731
+    t = {"q": r(2, d), "k": r(2, d), "v": r(2, dv), "do": r(2, dv)}
+    check(t, True, (30, 0), 150, f"packed parts d={d} det={deterministic}", cu=cu, deterministic=deterministic)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_deterministic_backward_repeats(d):
     t = {n: x.cuda() for n, x in inputs.small(B=1, H=4, L=2048, d=d, seed=176).items()}
@@ -150,7 +166,7 @@ def test_captured_forward_and_backward_replay():
     ref = binding.backward(t["q"], t["k"], t["v"], o, lse, t["do"], deterministic=True, **kw)
     out, l2 = torch.empty_like(o), torch.empty_like(lse)
     grads = [torch.empty_like(x) for x in ref]
-    ws = torch.empty(binding.attn_bwd_ex_workspace_size(1, 4, 2, 500, 500, 128, 128, 1, 1), dtype=torch.uint8,
+    ws = torch.empty(binding.attn_bwd_sinks_workspace_size(1, 4, 2, 500, 500, 128, 128, 1, 90, 0, 6, 1), dtype=torch.uint8,
                      device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -179,7 +195,7 @@ def test_refusals():
     assert fwd(4, d=96) == binding.ATTN_ERR_ARG
     assert fwd(4, p=x + 2) == binding.ATTN_ERR_ALIGN
     assert fwd(4, p=None) == binding.ATTN_ERR_ARG
-    need = lib.attn_bwd_ex_workspace_size(1, 2, 1, 64, 64, 64, 64, 1, 0)
+    need = lib.attn_bwd_sinks_workspace_size(1, 2, 1, 64, 64, 64, 64, 1, 5, -1, 4, 0)
     bwd = lambda sinks, ws: lib.attn_bwd_sinks(*([x] * 9), 1, 2, 1, 64, 64, 64, 64, 0.1, 1, 5, -1, sinks,  # noqa: E731
                                                None, None, 0, x, ws, None)
     assert bwd(-3, need) == binding.ATTN_ERR_ARG
