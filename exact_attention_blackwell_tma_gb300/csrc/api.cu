@@ -634,7 +634,7 @@ struct Kv4Workspace {
     size_t ml, part, scores, total;
 };
 Kv4Workspace kv4_layout(int B, int H, int Hkv, long total, int width, int d, int dv, bool weights) {
-    const int nr = kv4_row_tiles(H / Hkv, B, (int)total, d, dv);
+    const int nr = kv4_row_tiles(H / Hkv, B, (int)total);
     Kv4Workspace w{};
     w.ml = align256(kv4_prefix_bytes());
     w.part = w.ml + align256(kv4_ml_bytes(nr));
@@ -706,7 +706,7 @@ extern "C" int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_ca
         return fail(ATTN_ERR_ARG, "key weights need a row length >= 1 and a decay in [0, 1]");
     if (B == 0 || (p.s.total == 0 && !key_weights)) return ok();
     const int group = H / p.c.Hkv;
-    const int nr = kv4_row_tiles(group, B, p.s.total, p.c.d, p.c.dv);
+    const int nr = kv4_row_tiles(group, B, p.s.total);
     // the work list counts pages of row blocks in an int
     const double units = ((double)p.s.total * group / (8 * nr) + B) * table_width * p.c.Hkv;
     if ((double)p.s.total * H >= 2.0e9) return fail(ATTN_ERR_ARG, "too many rows");

@@ -61,12 +61,13 @@ struct Kv4FwdParams {
 };
 
 // Row blocks: a CTA holds 8 * kv4_row_tiles(...) (query, head-of-the-group) rows
-// of one key/value head at once.
-inline int kv4_row_tiles(int group, int B, int total, int d, int dv) {
-    const long rows = B > 0 ? (long)group * ((total + B - 1) / B) : group;   // an average sequence's
-    const int most = d > 128 || dv > 128 ? 2 : 4;
-    const int nr = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-    return nr < most ? nr : most;
+// of one key/value head at once. Blocks of 16 rows when an average sequence has
+// more than 8; larger ones lose more to the registers they take from the number
+// of warps than they save by reading the codes less often (32 sequences, group 4,
+// 1 to 16 tokens each, d = 128: 8 rows at once 160 us, 16: 146, 32: 191).
+inline int kv4_row_tiles(int group, int B, int total) {
+    const long rows = B > 0 ? (long)group * ((total + B - 1) / B) : group;
+    return rows <= 8 ? 1 : 2;
 }
 constexpr int kKv4MaxCtas = 640;
 // Workspace parts in bytes.

@@ -107,11 +107,13 @@ struct Kv4Layout {
                          kSlot = kVpOff + GV * kParams;
     static constexpr int kSlots = D + DV <= 128 ? 3 : 2;          // per warp
     static constexpr int kQOff = kWarps * kSlots * kSlot;         // q fragments [NR][GK][2][32 lanes] x 16 bytes
-    static constexpr int kSumOff = kQOff + NR * GK * 1024;        // O rows of the block, summed warp by warp
-    static constexpr int kMlOff = kSumOff + kRows * DV * 4;       // (max, sum) per warp and row
+    static constexpr int kQSumOff = kQOff + NR * GK * 1024;       // q's sums [rows][GK], each warp's largest |q|
+    static constexpr int kMlOff = kQSumOff + (kRows * GK + kWarps) * 4 + (kRows * GK & 1) * 4;   // (max, sum) per warp and row
     static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
     static constexpr int kAbortOff = kBarOff + kWarps * kSlots * 8;
     static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
+    // at the end of a row block each warp's O rows go where its slots were
+    static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
     static constexpr int smem(int B) { return kPrefixOff + (B + 1) * 4; }
     // accumulators take NR * DV / 4 registers of a thread
     static constexpr int kRegCtas = NR * DV <= 64 ? 4 : (NR * DV <= 256 && DV < 256 ? 3 : 2);
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     float acc[GV * 4][NR][4];
     float qsum[NR][2][GK], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
     int klo[NR][2], khi[NR][2];
-    float* sums = reinterpret_cast<float*>(smem + Lay::kSumOff);
+    float* qsums = reinterpret_cast<float*>(smem + Lay::kQSumOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
     uint32_t got = 0, sent = 0, live = 0;   // slots waited for and issued so far; bit n % 32: the page of issue n is in range
     const long row_len = (long)p.s.width * kPage;
@@ -285,63 +287,69 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
         float qs;
         {
-            uint4 raw[NR][GK][2];
+            // (n, g) = 8 rows x 64 channels each, dealt to the warps; a lane takes row g8's channels 16 t4 ..
+            constexpr int kTasks = (NR * GK + kWarps - 1) / kWarps;
+            uint4 raw[kTasks][2];
             float top = 0.f;
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const int r = t.rb * kRows + n * 8 + g8;   // this lane loads row r's channels 16 t4 .. of each group
-                const bool in = r < w.rows;
-                const __nv_bfloat16* src = p.q + (long)(w.s.q0 + (in ? r / p.group : 0)) * p.q_stride +
-                                           (long)(t.h * p.group + (in ? r % p.group : 0)) * D + 16 * t4;
+            for (int y = 0; y < kTasks; ++y) {
+                const int task = y * kWarps + warp, n = task / GK, g = task % GK;
+                const int r = t.rb * kRows + n * 8 + g8;
+                raw[y][0] = raw[y][1] = make_uint4(0, 0, 0, 0);
+                if (task < NR * GK && r < w.rows) {
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (long)(w.s.q0 + r / p.group) * p.q_stride +
+                                                                      (long)(t.h * p.group + r % p.group) * D + g * kKv4Group + 16 * t4);
+                    raw[y][0] = src[0];
+                    raw[y][1] = src[1];
+                }
+            }
 #pragma unroll
-                for (int g = 0; g < GK; ++g)
+            for (int y = 0; y < kTasks; ++y) {
+                const int task = y * kWarps + warp, n = task / GK, g = task % GK;
+                const uint32_t ws[8] = {raw[y][0].x, raw[y][0].y, raw[y][0].z, raw[y][0].w,
+                                        raw[y][1].x, raw[y][1].y, raw[y][1].z, raw[y][1].w};
+                float part = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        raw[n][g][x] = in ? *reinterpret_cast<const uint4*>(src + g * kKv4Group + 8 * x) : make_uint4(0, 0, 0, 0);
-                        const uint32_t ws[4] = {raw[n][g][x].x, raw[n][g][x].y, raw[n][g][x].z, raw[n][g][x].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(ws[i])), fabsf(hi_bf16(ws[i]))));
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const float a = lo_bf16(ws[i]), b = hi_bf16(ws[i]);
+                    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+                    part += a;
+                    part += b;
+                }
+                part += __shfl_xor_sync(kFullMask, part, 1);
+                part += __shfl_xor_sync(kFullMask, part, 2);
+                if (t4 == 0 && task < NR * GK) qsums[(n * 8 + g8) * GK + g] = part;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            if (lane == 0) qsums[kRows * GK + warp] = top;
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) top = fmaxf(top, qsums[kRows * GK + x]);
             // the block's rows times 2^e have their largest element in [2^14, 2^15) (both powers stay in the float range)
             const int e = top > 0.f && top < INFINITY ? min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 126) : 0;
-            const float f = pow2(e);
+            const float f = pow2(e), f16 = f * 0.0625f;
             qs = p.scale_log2 * pow2(24 - e);
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                float part[GK];
+            for (int y = 0; y < kTasks; ++y) {
+                const int task = y * kWarps + warp;
+                if (task >= NR * GK) break;
 #pragma unroll
-                for (int g = 0; g < GK; ++g) {
-                    part[g] = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t ws[4] = {raw[n][g][x].x, raw[n][g][x].y, raw[n][g][x].z, raw[n][g][x].w};
-                        float c[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            c[2 * i] = lo_bf16(ws[i]);
-                            c[2 * i + 1] = hi_bf16(ws[i]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) part[g] += c[i];
-                        // word x holds channels 8 x .. 8 x + 7; step 2 x takes (0, 4) and (1, 5), step 2 x + 1 (2, 6) and (3, 7);
-                        // odd nibbles read 16 times too large
-                        if (warp == n % kWarps)   // one warp writes the fragments that all read
-                            *reinterpret_cast<uint4*>(smem + Lay::kQOff + (((n * GK + g) * 2 + x) * 32 + lane) * 16) =
-                                make_uint4(pack_f16x2(c[0] * f, c[4] * f), pack_f16x2(c[1] * f * 0.0625f, c[5] * f * 0.0625f),
-                                           pack_f16x2(c[2] * f, c[6] * f), pack_f16x2(c[3] * f * 0.0625f, c[7] * f * 0.0625f));
-                    }
-                    part[g] += __shfl_xor_sync(kFullMask, part[g], 1);
-                    part[g] += __shfl_xor_sync(kFullMask, part[g], 2);
+                for (int x = 0; x < 2; ++x) {
+                    // word x holds channels 8 x .. 8 x + 7; step 2 x takes (0, 4) and (1, 5), step 2 x + 1 (2, 6) and (3, 7);
+                    // odd nibbles read 16 times too large
+                    const uint4 v = raw[y][x];
+                    *reinterpret_cast<uint4*>(smem + Lay::kQOff + ((task * 2 + x) * 32 + lane) * 16) =
+                        make_uint4(pack_f16x2(lo_bf16(v.x) * f, lo_bf16(v.z) * f), pack_f16x2(hi_bf16(v.x) * f16, hi_bf16(v.z) * f16),
+                                   pack_f16x2(lo_bf16(v.y) * f, lo_bf16(v.w) * f), pack_f16x2(hi_bf16(v.y) * f16, hi_bf16(v.w) * f16));
                 }
-                // accumulator columns 2 t4, 2 t4 + 1 are rows 8 n + 2 t4 (+ 1): their sums live in lanes 4 (2 t4 (+ 1))
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int g = 0; g < GK; ++g)
-                        qsum[n][c][g] = p.scale_log2 * __shfl_sync(kFullMask, part[g], 4 * (2 * t4 + c));
+                    for (int g = 0; g < GK; ++g) qsum[n][c][g] = p.scale_log2 * qsums[(n * 8 + 2 * t4 + c) * GK + g];
                     const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
                     const int i = row / p.group;
                     klo[n][c] = row < w.rows ? band_key_lo(mb, i) : 0;
@@ -351,7 +359,6 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 #pragma unroll
                     for (int g = 0; g < GV; ++g) zb[n][c][g] = 0.f;
                 }
-            }
         }
         // keys that the block's first and last rows (hence all) see
         const int full_lo = band_key_lo(mb, (min(w.rows, t.rb * kRows + kRows) - 1) / p.group);
@@ -609,7 +616,12 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             if (ok && i + S < i1) issue(i + S);
         }
         // ------------------------------------------------ the four warps' rows become one
+        // (every copy into the slots has landed and been read: each warp's O rows go there)
         const bool ends = i1 == w.units, starts = i0 == 0;
+        if (!ok && lane == 0)   // (or is waited for here, after a wait that ran out)
+            for (; got < sent; ++got) drain_wait(bars + 8 * (got % S), (got / S) & 1u, p.wait_budget_ns);
+        got = __shfl_sync(kFullMask, got, 0);
+        float* mine = reinterpret_cast<float*>(smem + warp * S * Lay::kSlot);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -618,69 +630,57 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 l += __shfl_xor_sync(kFullMask, l, 4);
                 l += __shfl_xor_sync(kFullMask, l, 8);
                 l += __shfl_xor_sync(kFullMask, l, 16);
-                if (g8 == 0) ml[warp * kRows + n * 8 + 2 * t4 + c] = make_float2(m_run[n][c], l);
+                const int row = n * 8 + 2 * t4 + c;
+                if (g8 == 0) ml[warp * kRows + row] = make_float2(m_run[n][c], l);
+#pragma unroll
+                for (int g = 0; g < GV; ++g) {
+                    float z = zb[n][c][g];
+                    z += __shfl_xor_sync(kFullMask, z, 4);
+                    z += __shfl_xor_sync(kFullMask, z, 8);
+                    z += __shfl_xor_sync(kFullMask, z, 16);
+                    const float inv = wsc[g] == INFINITY ? 1.f : 1.f / wsc[g];   // (a power of two)
+                    float4* at = reinterpret_cast<float4*>(mine + row * DV + g * kKv4Group + 8 * g8);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        at[j] = make_float4(fmaf(acc[4 * g + 2 * j][n][c], inv * 16777216.f, z),
+                                            fmaf(acc[4 * g + 2 * j][n][2 + c], inv * 1048576.f, z),
+                                            fmaf(acc[4 * g + 2 * j + 1][n][c], inv * 16777216.f, z),
+                                            fmaf(acc[4 * g + 2 * j + 1][n][2 + c], inv * 1048576.f, z));
+                }
             }
         __syncthreads();
-        float f[NR][2];   // this warp's rows relative to the common maximum
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float m = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) m = fmaxf(m, ml[x * kRows + n * 8 + 2 * t4 + c].x);
-                f[n][c] = m_run[n][c] == -INFINITY ? 0.f : ex2_mufu(m_run[n][c] - m);
-            }
-        for (int x = 0; x < kWarps; ++x) {   // in warp order: the same sum on every run
-            if (warp == x) {
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int g = 0; g < GV; ++g) {
-                            float z = zb[n][c][g];
-                            z += __shfl_xor_sync(kFullMask, z, 4);
-                            z += __shfl_xor_sync(kFullMask, z, 8);
-                            z += __shfl_xor_sync(kFullMask, z, 16);
-                            const float inv = wsc[g] == INFINITY ? 1.f : 1.f / wsc[g];   // (a power of two)
-                            float2* at = reinterpret_cast<float2*>(sums + (n * 8 + 2 * t4 + c) * DV + g * kKv4Group + 8 * g8);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float2 o = x ? at[j] : make_float2(0.f, 0.f);
-                                if (f[n][c] != 0.f) {
-                                    o.x = fmaf(f[n][c], fmaf(acc[4 * g + j][n][c], inv * 16777216.f, z), o.x);
-                                    o.y = fmaf(f[n][c], fmaf(acc[4 * g + j][n][2 + c], inv * 1048576.f, z), o.y);
-                                }
-                                at[j] = o;
-                            }
-                        }
-            }
-            __syncthreads();
-        }
         const int part = 2 * blockIdx.x + (starts ? 1 : 0);
-        for (int x = tid; x < kRows * (DV / 4); x += kKv4Threads) {
+        const int n_rows = min(kRows, w.rows - t.rb * kRows);
+        for (int x = tid; x < n_rows * (DV / 4); x += kKv4Threads) {
             const int row = x / (DV / 4), c4 = x % (DV / 4);
-            const int r = t.rb * kRows + row;
-            if (r >= w.rows) continue;
+            float2 v[kWarps];
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int y = 0; y < kWarps; ++y) m = fmaxf(m, ml[y * kRows + row].x);
-#pragma unroll
             for (int y = 0; y < kWarps; ++y) {
-                const float2 v = ml[y * kRows + row];
-                l += v.y * (v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m));
+                v[y] = ml[y * kRows + row];
+                m = fmaxf(m, v[y].x);
             }
-            const float4 o = *reinterpret_cast<const float4*>(sums + row * DV + 4 * c4);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) {   // in warp order: the same sum on every run
+                const float f = v[y].x == -INFINITY ? 0.f : ex2_mufu(v[y].x - m);
+                l += v[y].y * f;
+                if (f != 0.f) {
+                    const float4 z = *reinterpret_cast<const float4*>(smem + y * S * Lay::kSlot + (row * DV + 4 * c4) * 4);
+                    o.x = fmaf(f, z.x, o.x);
+                    o.y = fmaf(f, z.y, o.y);
+                    o.z = fmaf(f, z.z, o.z);
+                    o.w = fmaf(f, z.w, o.w);
+                }
+            }
             if (starts && ends) {
+                const int r = t.rb * kRows + row, i = r / p.group, head = t.h * p.group + r % p.group;
                 const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (NaN stays)
-                const long tok = w.s.q0 + r / p.group;
-                const int head = t.h * p.group + r % p.group;
+                const long tok = w.s.q0 + i;
                 *reinterpret_cast<uint2*>(p.o + (tok * p.H + head) * DV + 4 * c4) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
                 if (c4 == 0) {
-                    float* dst = p.s.cu ? p.lse + (long)head * p.s.total + tok
-                                        : p.lse + ((long)t.b * p.H + head) * p.s.rows + r / p.group;
+                    float* dst = p.s.cu ? p.lse + (long)head * p.s.total + tok : p.lse + ((long)t.b * p.H + head) * p.s.rows + i;
                     *dst = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
             } else {
@@ -688,10 +688,9 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)part * kRows + row) * 2) = make_float2(m, l);
             }
         }
+        fence_proxy_async_smem();   // the next row block's copies come after these reads and writes
         __syncthreads();
     }
-    if (!ok && lane == 0)   // issued copies land before the CTA can exit
-        for (uint32_t n = got; n < sent; ++n) drain_wait(bars + 8 * (n % S), (n / S) & 1u, p.wait_budget_ns);
 }
 
 // ---------------------------------------------------------------- finish
@@ -868,13 +867,8 @@ cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) 
 
 template <int D, int DV>
 cudaError_t launch_dims(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) {
-    switch (kv4_row_tiles(p.group, p.s.B, p.s.total, D, DV)) {
-        case 1: return launch_one<D, DV, 1>(p, num_sms, stream);
-        case 2: return launch_one<D, DV, 2>(p, num_sms, stream);
-        default:
-            if constexpr (D <= 128 && DV <= 128) return launch_one<D, DV, 4>(p, num_sms, stream);
-            return cudaErrorInvalidValue;
-    }
+    return kv4_row_tiles(p.group, p.s.B, p.s.total) == 1 ? launch_one<D, DV, 1>(p, num_sms, stream)
+                                                         : launch_one<D, DV, 2>(p, num_sms, stream);
 }
 
 }  // namespace
