@@ -60,6 +60,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the first step of a sum: no accumulator to clear
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -89,6 +97,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 __device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // Every lane waits for the phase itself, so that each sees the data it guards.
 __device__ __forceinline__ bool lanes_wait(uint32_t bar, uint32_t parity, const WaitCtx& w) {
     return __all_sync(kFullMask, mbar_wait(bar, parity, w));
@@ -233,7 +246,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     int klo[NR][2], khi[NR][2];
     float* qsums = reinterpret_cast<float*>(smem + Lay::kQSumOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
-    uint32_t got = 0, sent = 0, live = 0;   // slots waited for and issued so far; bit n % 32: the page of issue n is in range
+    uint32_t got = 0, sent = 0;   // slots waited for and issued so far
     const long row_len = (long)p.s.width * kPage;
     bool ok = true;
     for (int u = u0; u < u1;) {
@@ -242,7 +255,8 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         const Unit t = unit_at(p, prefix, u, kRows, &w);
         const int i0 = t.i, i1 = min(w.units, i0 + u1 - u);
         u += i1 - i0;
-        // this warp's pages: index 2 i + warp / 2; each lane holds one of the next 32 ids
+        // this warp's pages: index 2 i + warp / 2; lane l holds the id of the unit l % 16 of the current
+        // sixteen, and of the next sixteen
         const int* table = p.s.table + (long)t.b * p.s.width;
         auto page_id = [&](int i) {
             const int x = 2 * i + (warp >> 1);
@@ -252,34 +266,36 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             atomicCAS(p.status, kStatusOk, kStatusBadPage);
             return -1;
         };
-        int ids = page_id(i0 + lane), ids_next = -2;
+        int ids = 0, ids_next = page_id(i0 + (lane & 15));
+        uint32_t live = 0;   // bit (i - i0) % 32: unit i's page is in range
         // copy `lane` of a slot: the codes of a group, or its parameters
         const bool cp_params = lane >= GK + GV, cp_v = (cp_params ? lane - GK - GV : lane) >= GK;
         const int cp_g = (cp_params ? lane - GK - GV : lane) - (cp_v ? GK : 0);
-        const uint8_t* cp_src = cp_params ? reinterpret_cast<const uint8_t*>(cp_v ? p.c.v_params : p.c.k_params)
-                                          : (cp_v ? p.c.v_codes : p.c.k_codes);
         const uint32_t cp_bytes = cp_params ? Lay::kParams : Lay::kCodes;
-        const uint32_t cp_dst = cp_params ? (cp_v ? Lay::kVpOff : Lay::kKpOff) + cp_g * Lay::kParams
-                                          : (cp_v ? Lay::kVOff : 0) + cp_g * Lay::kCodes;
+        const uint32_t cp_page = (uint32_t)p.c.Hkv * (cp_v ? GV : GK) * 2 * cp_bytes;   // bytes of a page (below 2^32: Hkv < 2^16)
+        const uint8_t* cp_src = (cp_params ? reinterpret_cast<const uint8_t*>(cp_v ? p.c.v_params : p.c.k_params)
+                                           : (cp_v ? p.c.v_codes : p.c.k_codes)) +
+                                (size_t)((t.h * (cp_v ? GV : GK) + cp_g) * 2 + half) * cp_bytes;
+        const uint32_t cp_dst = ring + (cp_params ? (cp_v ? Lay::kVpOff : Lay::kKpOff) + cp_g * Lay::kParams
+                                                  : (cp_v ? Lay::kVOff : 0) + cp_g * Lay::kCodes);
         auto issue = [&](int i) {   // the loads of unit i into the next slot (i - i0 = 0, 1, 2, ...)
             const int n = i - i0;
-            if ((n & 31) == 16) ids_next = page_id(i + 16 + lane);
-            if ((n & 31) == 0 && n > 0) ids = ids_next;
-            const int id = __shfl_sync(kFullMask, ids, n & 31);
-            const uint32_t s = sent % S;
-            live = (live & ~(1u << (sent & 31))) | ((id >= 0 ? 1u : 0u) << (sent & 31));
+            if ((n & 15) == 0) {
+                ids = ids_next;
+                ids_next = page_id(i + 16 + (lane & 15));
+                const uint32_t in = __ballot_sync(kFullMask, ids >= 0) & 0xffffu;
+                live = (live & (0xffff0000u >> (n & 16))) | in << (n & 16);
+            }
+            const int id = __shfl_sync(kFullMask, ids, n & 15);
+            const uint32_t s = sent % S, bar = bars + 8 * s;
             ++sent;
             if (id >= 0) {
-                if (lane == 0) mbar_expect_tx(bars + 8 * s, Lay::kSlot);
+                if (lane == 0) mbar_expect_tx(bar, Lay::kSlot);
                 __syncwarp();
-                if (lane < 2 * (GK + GV)) {
-                    const long at = ((long)id * p.c.Hkv + t.h) * (cp_v ? GV : GK) + cp_g;   // group of the cache
-                    bulk_load(ring + s * Lay::kSlot + cp_dst, cp_src + (at * 2 + half) * cp_bytes, cp_bytes, bars + 8 * s);
-                }
+                if (lane < 2 * (GK + GV)) bulk_load(cp_dst + s * Lay::kSlot, cp_src + (size_t)id * cp_page, cp_bytes, bar);
             } else if (lane == 0) {
-                mbar_arrive(bars + 8 * s);
+                mbar_arrive(bar);
             }
-            __syncwarp();
         };
         if (ok)
             for (int i = i0; i < i1 && i < i0 + S; ++i) issue(i);
@@ -384,6 +400,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 
         // One half page of 32 keys from slot `st`, its first key key0. kWhole: every row sees all of
         // them (the common case, kept free of masks and branches).
+        bool force = true;   // some row has yet to see its first key
         auto half_page = [&](auto whole_tag, const uint32_t st, const int key0) {
             constexpr bool kWhole = decltype(whole_tag)::value;
             float sc[2][NR][4];   // s - mu: per chunk [key g8, g8 + 8][row 2 t4, 2 t4 + 1] at 2 * key + row
@@ -404,17 +421,14 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     const uint32_t pa = lds32(par), pb = lds32(par + 32);
                     float d[NR][4];
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) d[n][x] = 0.f;
-#pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t xa = (k & 1) ? wa[k >> 1] >> 8 : wa[k >> 1], xb = (k & 1) ? wb[k >> 1] >> 8 : wb[k >> 1];
                         const uint32_t a0 = xa & 0x000f000fu, a1 = xb & 0x000f000fu, a2 = xa & 0x00f000f0u, a3 = xb & 0x00f000f0u;
 #pragma unroll
                         for (int n = 0; n < NR; ++n) {
                             const uint4 q4 = qf[n][k >> 1];
-                            mma_f16(d[n], a0, a1, a2, a3, (k & 1) ? q4.z : q4.x, (k & 1) ? q4.w : q4.y);
+                            if (k == 0) mma_f16_first(d[n], a0, a1, a2, a3, q4.x, q4.y);
+                            else mma_f16(d[n], a0, a1, a2, a3, (k & 1) ? q4.z : q4.x, (k & 1) ? q4.w : q4.y);
                         }
                     }
                     const float aa = lo_bf16(pa) * qs, ba = hi_bf16(pa), ab = lo_bf16(pb) * qs, bb = hi_bf16(pb);
@@ -456,10 +470,9 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             }
             // ---------------------------------------- V's parameters; does a maximum or a scale have to move?
             uint32_t vp[2][GV][2];
-            bool move = false;
+            bool move = force;
 #pragma unroll
             for (int g = 0; g < GV; ++g) {
-                float top = 0.f;
 #pragma unroll
                 for (int ck = 0; ck < 2; ++ck)
 #pragma unroll
@@ -471,18 +484,19 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                             for (int n = 0; n < NR; ++n) seen |= sc[ck][n][2 * x] != -INFINITY || sc[ck][n][2 * x + 1] != -INFINITY;
                             if (!seen) vp[ck][g][x] = 0u;
                         }
-                        top = fmaxf(top, fabsf(lo_bf16(vp[ck][g][x])));
                     }
+                const float top = max3(fmaxf(fabsf(lo_bf16(vp[0][g][0])), fabsf(lo_bf16(vp[0][g][1]))),
+                                       fabsf(lo_bf16(vp[1][g][0])), fabsf(lo_bf16(vp[1][g][1])));
                 move |= !(top * wsc[g] <= kWMost);
             }
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
-                    move |= mx > (m_run[n][c] == -INFINITY ? -INFINITY : kKv4Tau);
+                    move |= max3(fmaxf(sc[0][n][c], sc[0][n][2 + c]), sc[1][n][c], sc[1][n][2 + c]) > kKv4Tau;
                 }
             if (__any_sync(kFullMask, move)) {
+                bool unset = false;
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     float al[2];
@@ -500,6 +514,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                             sc[ck][n][c] += mu[n][c] - mu_new;
                             sc[ck][n][2 + c] += mu[n][c] - mu_new;
                         }
+                        unset |= m_new == -INFINITY && khi[n][c] > 0;
                         m_run[n][c] = m_new;
                         mu[n][c] = mu_new;
                         l_run[n][c] *= al[c];
@@ -511,6 +526,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 #pragma unroll
                         for (int x = 0; x < 4; ++x) acc[j][n][x] *= al[x & 1];
                 }
+                force = __any_sync(kFullMask, unset);
 #pragma unroll
                 for (int g = 0; g < GV; ++g) {
                     // a new power of two for the group's a'; infinities and NaN do not set it
@@ -598,7 +614,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             // barriers that the other warps wait at)
             const uint32_t s = got % S;
             if (ok) ok = lanes_wait(bars + 8 * s, (got / S) & 1u, wc);
-            const bool valid = ok && ((live >> (got & 31)) & 1u);
+            const bool valid = ok && ((live >> ((i - i0) & 31)) & 1u);
             if (ok) ++got;
             const int key0 = page_of(w, 2 * i + (warp >> 1)) * kPage + 32 * half;
             if (valid) {
@@ -723,17 +739,17 @@ __device__ __forceinline__ long lse_at(const Kv4FwdParams& p, const SeqWork& w, 
 }
 
 constexpr int kFinishThreads = 128;
-constexpr int kFinishKeys = 4 * kFinishThreads;   // keys of a weights block
+constexpr int kFinishTiles = 4, kFinishKeys = kFinishTiles * 4 * kFinishThreads;   // keys of a weights block
 constexpr int kFinishRows = 64;                   // rows whose LSE it holds at a time
 
 // Blocks [0, row_blocks): one warp per (token, head) whose row block several CTAs
 // shared joins their partial rows in CTA order (the same sum on every run); rows
 // that no key reaches get O = 0, LSE = -inf. The other blocks update key weights:
 //   key_weights[b][h][j] = decay * key_weights + sum over rows of exp(s - LSE),
-// four keys per thread, rows in order. Scores of pages that no row block visited
+// four times four keys per thread, rows in order. Scores of pages that no row block visited
 // were not written and count as nothing. Launched while the attention kernel
 // runs (programmatic dependent launch); what it left is read after the wait.
-__global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4FwdParams p, int rows_per_block,
+__global__ void __launch_bounds__(kFinishThreads, 7) kv4_finish_kernel(const Kv4FwdParams p, int rows_per_block,
                                                                     int row_blocks, int key_blocks) {
     __shared__ float lse2[kFinishRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -757,11 +773,11 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4Fwd
         if (s.c0 == s.c1) return;
         const float2 ml = join_ml(p, s, lane);
         float4 o[2] = {};
-        for (int c = s.c0; c <= s.c1; c += 8) {   // eight shares' loads in flight
-            float f[8];
-            float4 y[8][2];
+        for (int c = s.c0; c <= s.c1; c += 4) {   // four shares' loads in flight
+            float f[4];
+            float4 y[4][2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const bool in = c + k <= s.c1;
                 const long at = s.at(in ? c + k : s.c1);
                 const float mk = p.part_ml[2 * at];
@@ -771,7 +787,7 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4Fwd
                     if (x * 128 + lane * 4 < dv) y[k][x] = *reinterpret_cast<const float4*>(p.part_o + at * dv + x * 128 + lane * 4);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 4; ++k)
                 if (f[k] != 0.f)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -795,16 +811,20 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4Fwd
     const int id = blockIdx.x - row_blocks;
     const int bh = id / key_blocks, b = bh / p.c.Hkv, h = bh % p.c.Hkv;
     const SeqWork w = seq_work(p, b, rows_per_block);
-    const int j = (id % key_blocks) * kFinishKeys + 4 * threadIdx.x;
+    const int j0 = (id % key_blocks) * kFinishKeys + 4 * threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (j == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
+    if (j0 == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
     const int keys = (int)min((long)w.s.lk, p.weight_stride);
     if (w.s.bad || (id % key_blocks) * kFinishKeys >= keys) return;
-    const int page = j / kPage;
-    const bool seen = j < keys && (page < w.n_sink || (page >= w.first && page < w.first + w.pages - w.n_sink));
-    float sum[4] = {};
+    bool seen[kFinishTiles];
+    float sum[kFinishTiles][4] = {};
+#pragma unroll
+    for (int x = 0; x < kFinishTiles; ++x) {
+        const int j = j0 + x * 4 * kFinishThreads, page = j / kPage;
+        seen[x] = j < keys && (page < w.n_sink || (page >= w.first && page < w.first + w.pages - w.n_sink));
+    }
     const long row_len = (long)p.s.width * kPage;
-    const float* src = p.scores + ((long)h * p.s.total * p.group + (long)w.s.q0 * p.group) * row_len + j;
+    const float* src = p.scores + ((long)h * p.s.total * p.group + (long)w.s.q0 * p.group) * row_len + j0;
     for (int r0 = 0; r0 < w.rows && w.pages > 0; r0 += kFinishRows) {
         const int nr = min(kFinishRows, w.rows - r0);
         __syncthreads();
@@ -820,21 +840,31 @@ __global__ void __launch_bounds__(kFinishThreads) kv4_finish_kernel(const Kv4Fwd
             if (lane == 0) lse2[r] = v;
         }
         __syncthreads();
-        if (!seen) continue;
-#pragma unroll 4
         for (int r = 0; r < nr; ++r) {
-            const float4 s = __ldcs(reinterpret_cast<const float4*>(src + (r0 + r) * row_len));
+            const float* row = src + (r0 + r) * row_len;
             const float e = lse2[r];
-            sum[0] += s.x == -INFINITY ? 0.f : ex2_mufu(s.x - e);
-            sum[1] += s.y == -INFINITY ? 0.f : ex2_mufu(s.y - e);
-            sum[2] += s.z == -INFINITY ? 0.f : ex2_mufu(s.z - e);
-            sum[3] += s.w == -INFINITY ? 0.f : ex2_mufu(s.w - e);
+            float4 s[kFinishTiles];
+#pragma unroll
+            for (int x = 0; x < kFinishTiles; ++x)
+                if (seen[x]) s[x] = __ldcs(reinterpret_cast<const float4*>(row + x * 4 * kFinishThreads));
+#pragma unroll
+            for (int x = 0; x < kFinishTiles; ++x) {
+                if (!seen[x]) continue;
+                sum[x][0] += s[x].x == -INFINITY ? 0.f : ex2_mufu(s[x].x - e);
+                sum[x][1] += s[x].y == -INFINITY ? 0.f : ex2_mufu(s[x].y - e);
+                sum[x][2] += s[x].z == -INFINITY ? 0.f : ex2_mufu(s[x].z - e);
+                sum[x][3] += s[x].w == -INFINITY ? 0.f : ex2_mufu(s[x].w - e);
+            }
         }
     }
-    float* dst = p.key_weights + ((long)b * p.c.Hkv + h) * p.weight_stride + j;
+    float* dst = p.key_weights + ((long)b * p.c.Hkv + h) * p.weight_stride + j0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-        if (j + x < keys) dst[x] = p.weight_decay == 0.f ? sum[x] : fmaf(p.weight_decay, dst[x], sum[x]);
+    for (int x = 0; x < kFinishTiles; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int k = x * 4 * kFinishThreads + y;
+            if (j0 + k < keys) dst[k] = p.weight_decay == 0.f ? sum[x][y] : fmaf(p.weight_decay, dst[k], sum[x][y]);
+        }
 }
 
 template <int D, int DV, int NR>
