@@ -127,7 +127,7 @@ struct Kv4Layout {
     static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
     // at the end of a row block each warp's O rows go where its slots were
     static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
-    static constexpr int smem(int B) { return kPrefixOff + (B + 1) * 4; }
+    static constexpr int smem(int B) { return kPrefixOff + (2 * B + 1) * 4; }   // the work prefix, row blocks per sequence
     // accumulators take NR * DV / 4 registers of a thread
     static constexpr int kRegCtas = NR * DV <= 64 ? 4 : (NR * DV <= 256 && DV < 256 ? 3 : 2);
     static constexpr int kSmemCtas = 227 * 1024 / (smem(64) + 1024);   // (with up to 64 sequences)
@@ -159,40 +159,87 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4FwdParams& p, int b, int ro
 }
 __device__ __forceinline__ int page_of(const SeqWork& w, int i) { return i < w.n_sink ? i : w.first + i - w.n_sink; }
 
+// How the work list is cut: `per` units per CTA. aligned: every row block's units
+// are rounded up to a multiple of `per`, so that no CTA works on two row blocks.
+struct Cut {
+    int per, aligned;
+    __device__ __forceinline__ int span(int units) const { return aligned ? (units + per - 1) / per * per : units; }
+};
+// With few units per CTA a second row block costs as much as the units do (its
+// queries, its first loads, its epilogue), so the aligned cut is taken when it
+// needs at most this many units per CTA and fits the grid (16 windows of 4096
+// keys at d = 256, 33 units each, in twos: 16.7 us unaligned, 13.3 aligned). Longer ranges balance better uncut.
+constexpr int kAlignedMost = 8;
+// A unit takes a CTA about 1.5 us and joining a row's shares about 1 us per 8, so
+// a row block of U units is not cut into more than U / per with 12 per^2 >= U: the
+// sum of the two is least there (4 heads over 16000 keys, d = 64, 125 units each:
+// 23.4 us in ones, 15.3 in fours).
+__device__ __forceinline__ int least_per(int units) {
+    int per = 1;
+    while (12 * per * per < units) ++per;
+    return per;
+}
+
 // The units of all sequences as a prefix sum in shared memory (every thread of
-// the CTA calls); returns the units of one CTA.
+// the CTA calls); `times` (B more ints) is scratch.
 template <int kThreads>
-__device__ __forceinline__ int build_prefix(const Kv4FwdParams& p, int* prefix, int rows_per_block, int ctas) {
+__device__ __forceinline__ Cut build_prefix(const Kv4FwdParams& p, int* prefix, int* times, int rows_per_block, int ctas) {
     for (int b = threadIdx.x; b < p.s.B; b += kThreads) {
         const SeqWork w = seq_work(p, b, rows_per_block);
         if (w.s.bad && blockIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusBadPage);
-        prefix[b + 1] = p.c.Hkv * w.blocks * w.units;
+        prefix[b + 1] = w.units;
+        times[b] = p.c.Hkv * w.blocks;
     }
-    if (threadIdx.x == 0) prefix[0] = 0;
+    __shared__ Cut s_cut;
     __syncthreads();
     if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        auto total = [&](const Cut& c) {   // units of the list (below 2^31: checked on the host)
+            int x = 0;
+            for (int b = lane; b < p.s.B; b += 32) x += times[b] * c.span(prefix[b + 1]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
+            return x;
+        };
+        int longest = 0;
+        for (int b = lane; b < p.s.B; b += 32) longest = max(longest, times[b] > 0 ? prefix[b + 1] : 0);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(kFullMask, longest, o));
+        Cut cut{0, 0};
+        cut.per = max((total(cut) + ctas - 1) / ctas, longest > 0 ? least_per(longest) : 0);
+        for (int per = cut.per; per > 0 && per <= kAlignedMost; ++per)
+            if (total(Cut{per, 1}) <= per * ctas) {
+                cut = Cut{per, 1};
+                break;
+            }
         int carry = 0;
         for (int b0 = 0; b0 < p.s.B; b0 += 32) {
-            const int b = b0 + threadIdx.x;
-            int x = b < p.s.B ? prefix[b + 1] : 0;
+            const int b = b0 + lane;
+            int x = b < p.s.B ? times[b] * cut.span(prefix[b + 1]) : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFullMask, x, o);
-                if ((int)threadIdx.x >= o) x += y;
+                if (lane >= o) x += y;
             }
+            __syncwarp();
             if (b < p.s.B) prefix[b + 1] = carry + x;
             carry += __shfl_sync(kFullMask, x, 31);
         }
+        if (lane == 0) {
+            prefix[0] = 0;
+            s_cut = cut;
+        }
     }
     __syncthreads();
-    return (prefix[p.s.B] + ctas - 1) / ctas;
+    return s_cut;
 }
 
 // Unit u: sequence, head, row block and unit index within the row block.
 struct Unit {
     int b, h, rb, i;
 };
-__device__ __forceinline__ Unit unit_at(const Kv4FwdParams& p, const int* prefix, int u, int rows_per_block, SeqWork* w) {
+__device__ __forceinline__ Unit unit_at(const Kv4FwdParams& p, const int* prefix, const Cut& cut, int u, int rows_per_block,
+                                        SeqWork* w) {
     int lo = 0, hi = p.s.B - 1;   // the last b with prefix[b] <= u (and units of its own)
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -202,11 +249,11 @@ __device__ __forceinline__ Unit unit_at(const Kv4FwdParams& p, const int* prefix
     *w = seq_work(p, lo, rows_per_block);
     Unit r;
     r.b = lo;
-    const int rem = u - prefix[lo], per_head = w->blocks * w->units;
+    const int span = cut.span(w->units), rem = u - prefix[lo], per_head = w->blocks * span;
     r.h = rem / per_head;
     const int x = rem - r.h * per_head;
-    r.rb = x / w->units;
-    r.i = x - r.rb * w->units;
+    r.rb = x / span;
+    r.i = x - r.rb * span;   // (>= units: the padding behind an aligned row block)
     return r;
 }
 
@@ -227,11 +274,15 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         *abort_flag = 0;
         fence_barrier_init();
     }
-    const int per = build_prefix<kKv4Threads>(p, prefix, kRows, gridDim.x);   // (ends with __syncthreads)
+    const Cut cut = build_prefix<kKv4Threads>(p, prefix, prefix + p.s.B + 1, kRows, gridDim.x);   // (ends with __syncthreads)
+    const int per = cut.per;
     const int total = prefix[p.s.B];
     if (blockIdx.x == 0) {   // for the kernel that follows
         for (int i = tid; i <= p.s.B; i += kKv4Threads) p.prefix[i] = prefix[i];
-        if (tid == 0) p.prefix[kKv4MaxBatch + 1] = per;
+        if (tid == 0) {
+            p.prefix[kKv4MaxBatch + 1] = per;
+            p.prefix[kKv4MaxBatch + 2] = cut.aligned;
+        }
     }
     const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
     const WaitCtx wc{abort_flag, p.status, p.wait_budget_ns};
@@ -252,9 +303,9 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     for (int u = u0; u < u1;) {
         // ------------------------------------------------ a row block (this CTA's share of it): units i0 .. i1 - 1
         SeqWork w;
-        const Unit t = unit_at(p, prefix, u, kRows, &w);
+        const Unit t = unit_at(p, prefix, cut, u, kRows, &w);
         const int i0 = t.i, i1 = min(w.units, i0 + u1 - u);
-        u += i1 - i0;
+        u += min(cut.span(w.units) - i0, u1 - u);   // (with its padding)
         // this warp's pages: index 2 i + warp / 2; lane l holds the id of the unit l % 16 of the current
         // sixteen, and of the next sixteen
         const int* table = p.s.table + (long)t.b * p.s.width;
@@ -716,8 +767,9 @@ struct Shares {
     __device__ __forceinline__ long at(int c) const { return (long)(2 * c + (c == c0 ? 1 : 0)) * rows_per_block + in_block; }
 };
 __device__ __forceinline__ Shares shares_of(const Kv4FwdParams& p, const SeqWork& w, int b, int h, int r, int rows_per_block) {
-    const int per = p.prefix[kKv4MaxBatch + 1];
-    const int u = p.prefix[b] + (h * w.blocks + r / rows_per_block) * w.units;
+    const Cut cut{p.prefix[kKv4MaxBatch + 1], p.prefix[kKv4MaxBatch + 2]};
+    const int per = cut.per;
+    const int u = p.prefix[b] + (h * w.blocks + r / rows_per_block) * cut.span(w.units);
     return Shares{u / per, (u + w.units - 1) / per, r % rows_per_block, rows_per_block};
 }
 // (max, sum) of all shares of a row: every lane of the warp calls and gets both.
