@@ -441,6 +441,9 @@ int bwd_entry(const void* q, const void* k, const void* v, const void* o, const 
     p.mask.sinks = window_left < 0 ? 0 : (sinks < Lk ? sinks : Lk);   // (no left bound: nothing to keep visible)
     p.o = static_cast<const __nv_bfloat16*>(o);
     p.dout = static_cast<const __nv_bfloat16*>(dout);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
     p.lse = lse;
     p.dq_acc = reinterpret_cast<float*>(ws + wl.dq_off);
     p.delta = reinterpret_cast<float*>(ws + wl.delta_off);

@@ -61,6 +61,9 @@ struct BwdParams {
     Geometry g;
     const __nv_bfloat16* o;
     const __nv_bfloat16* dout;
+    const __nv_bfloat16* q;   // (the preprocess kernel's few-key rows read q, k and v; the main kernels their maps)
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
     const float* lse;         // natural-log LSE from the forward, layout as FwdParams::lse
     float* dq_acc;            // fp32 accumulator, layout of q
     float* delta;             // D_i = rowsum(dO * O), layout of lse
