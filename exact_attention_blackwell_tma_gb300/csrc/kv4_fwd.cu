@@ -34,9 +34,9 @@
 // caches balance, one long cache uses every SM). A row block that lies in one
 // CTA's range is finished there; others leave (max, sum, O) in the workspace
 // for the finishing kernel. Within a CTA each of four warps takes 32 of a unit's
-// 128 tokens, with softmax statistics and a ring of bulk copies of its own (one
-// lane per copy), so that nothing synchronises the warps until they add their
-// rows up at the end of a row block.
+// 128 tokens, with softmax statistics and a ring of asynchronous copies of its
+// own, so that nothing synchronises the warps until they add their rows up at the
+// end of a row block.
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -90,10 +90,16 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ void lds64(uint32_t a, uint32_t& x, uint32_t& y) {
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+// 16 bytes per lane from global to shared memory, past L1. (Bulk copies want
+// their operands in uniform registers: eight of them per half page, with sources
+// of their own, cost a loop of about 100 instructions.)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 __device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
@@ -101,10 +107,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
-}
-// Every lane waits for the phase itself, so that each sees the data it guards.
-__device__ __forceinline__ bool lanes_wait(uint32_t bar, uint32_t parity, const WaitCtx& w) {
-    return __all_sync(kFullMask, mbar_wait(bar, parity, w));
 }
 // 2^e for an unbiased exponent in the normal range
 __device__ __forceinline__ float pow2(int e) {
@@ -118,13 +120,11 @@ struct Kv4Layout {
     static constexpr int kCodes = 32 * 32, kParams = 32 * 4;   // of one group
     static constexpr int kVOff = GK * kCodes, kKpOff = kVOff + GV * kCodes, kVpOff = kKpOff + GK * kParams,
                          kSlot = kVpOff + GV * kParams;
-    static constexpr int kSlots = D + DV <= 128 ? 3 : 2;          // per warp
+    static constexpr int kSlots = D + DV <= 128 ? 4 : (D + DV <= 256 ? 3 : 2);   // per warp
     static constexpr int kQOff = kWarps * kSlots * kSlot;         // q fragments [NR][GK][2][32 lanes] x 16 bytes
     static constexpr int kQSumOff = kQOff + NR * GK * 1024;       // q's sums [rows][GK], each warp's largest |q|
     static constexpr int kMlOff = kQSumOff + (kRows * GK + kWarps) * 4 + (kRows * GK & 1) * 4;   // (max, sum) per warp and row
-    static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
-    static constexpr int kAbortOff = kBarOff + kWarps * kSlots * 8;
-    static constexpr int kPrefixOff = (kAbortOff + 4 + 15) / 16 * 16;
+    static constexpr int kPrefixOff = (kMlOff + kWarps * kRows * 8 + 15) / 16 * 16;
     // at the end of a row block each warp's O rows go where its slots were
     static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
     static constexpr int smem(int B) { return kPrefixOff + (2 * B + 1) * 4; }   // the work prefix, row blocks per sequence
@@ -262,18 +262,12 @@ template <int D, int DV, int NR, bool kScores>
 __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_fwd_kernel(const Kv4FwdParams p) {
     using Lay = Kv4Layout<D, DV, NR>;
     constexpr int GK = Lay::GK, GV = Lay::GV, S = Lay::kSlots, kRows = Lay::kRows;
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int* prefix = reinterpret_cast<int*>(smem + Lay::kPrefixOff);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbortOff);
-    const uint32_t ring = base + warp * S * Lay::kSlot, bars = base + Lay::kBarOff + warp * S * 8;
+    const uint32_t ring = base + warp * S * Lay::kSlot;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the finishing kernel waits for this grid's end)
-    if (tid == 0) {
-        for (int s = 0; s < kWarps * S; ++s) mbar_init(base + Lay::kBarOff + 8 * s, 1);
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
     const Cut cut = build_prefix<kKv4Threads>(p, prefix, prefix + p.s.B + 1, kRows, gridDim.x);   // (ends with __syncthreads)
     const int per = cut.per;
     const int total = prefix[p.s.B];
@@ -285,7 +279,6 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         }
     }
     const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
-    const WaitCtx wc{abort_flag, p.status, p.wait_budget_ns};
 
     const int g8 = lane >> 2, t4 = lane & 3;
     // This warp's 32 tokens of a unit (half warp % 2 of page warp / 2), in two chunks of 16. S^T
@@ -297,9 +290,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     int klo[NR][2], khi[NR][2];
     float* qsums = reinterpret_cast<float*>(smem + Lay::kQSumOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
-    uint32_t got = 0, sent = 0;   // slots waited for and issued so far
     const long row_len = (long)p.s.width * kPage;
-    bool ok = true;
     for (int u = u0; u < u1;) {
         // ------------------------------------------------ a row block (this CTA's share of it): units i0 .. i1 - 1
         SeqWork w;
@@ -319,37 +310,54 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         };
         int ids = 0, ids_next = page_id(i0 + (lane & 15));
         uint32_t live = 0;   // bit (i - i0) % 32: unit i's page is in range
-        // copy `lane` of a slot: the codes of a group, or its parameters
-        const bool cp_params = lane >= GK + GV, cp_v = (cp_params ? lane - GK - GV : lane) >= GK;
-        const int cp_g = (cp_params ? lane - GK - GV : lane) - (cp_v ? GK : 0);
-        const uint32_t cp_bytes = cp_params ? Lay::kParams : Lay::kCodes;
-        const uint32_t cp_page = (uint32_t)p.c.Hkv * (cp_v ? GV : GK) * 2 * cp_bytes;   // bytes of a page (below 2^32: Hkv < 2^16)
-        const uint8_t* cp_src = (cp_params ? reinterpret_cast<const uint8_t*>(cp_v ? p.c.v_params : p.c.k_params)
-                                           : (cp_v ? p.c.v_codes : p.c.k_codes)) +
-                                (size_t)((t.h * (cp_v ? GV : GK) + cp_g) * 2 + half) * cp_bytes;
-        const uint32_t cp_dst = ring + (cp_params ? (cp_v ? Lay::kVpOff : Lay::kKpOff) + cp_g * Lay::kParams
-                                                  : (cp_v ? Lay::kVOff : 0) + cp_g * Lay::kCodes);
-        auto issue = [&](int i) {   // the loads of unit i into the next slot (i - i0 = 0, 1, 2, ...)
+        // A lane's 16-byte pieces of a slot: piece `lane` and `lane` + 32 of every group's codes, and
+        // of the 8 (GK + GV) pieces of parameters number `lane`.
+        constexpr uint32_t kGroupCodes = kPage * 32, kGroupParams = kPage * 4;   // of a page
+        const uint32_t kc_page = (uint32_t)p.c.Hkv * GK * kGroupCodes, vc_page = (uint32_t)p.c.Hkv * GV * kGroupCodes;
+        const uint8_t* kc = p.c.k_codes + (size_t)t.h * GK * kGroupCodes + half * Lay::kCodes + lane * 16;
+        const uint8_t* vc = p.c.v_codes + (size_t)t.h * GV * kGroupCodes + half * Lay::kCodes + lane * 16;
+        const bool par = lane < 8 * (GK + GV), par_v = lane >= 8 * GK;
+        const int par_g = lane / 8 - (par_v ? GK : 0);
+        const uint32_t par_page = (uint32_t)p.c.Hkv * (par_v ? GV : GK) * kGroupParams;
+        const uint8_t* par_src = reinterpret_cast<const uint8_t*>(par_v ? p.c.v_params : p.c.k_params) +
+                                 (size_t)(t.h * (par_v ? GV : GK) + par_g) * kGroupParams + half * Lay::kParams + (lane & 7) * 16;
+        const uint32_t code_dst = ring + lane * 16, par_dst = ring + Lay::kKpOff + lane * 16;   // (V's parameters follow K's)
+        uint32_t slot_in = 0, slot_out = 0;   // slots written to and read from next, as byte offsets
+        auto issue = [&](int i) {   // the loads of unit i into the next slot (i - i0 = 0, 1, 2, ...), one group of copies
             const int n = i - i0;
-            if ((n & 15) == 0) {
-                ids = ids_next;
-                ids_next = page_id(i + 16 + (lane & 15));
-                const uint32_t in = __ballot_sync(kFullMask, ids >= 0) & 0xffffu;
-                live = (live & (0xffff0000u >> (n & 16))) | in << (n & 16);
+            if (i < i1) {
+                if ((n & 15) == 0) {
+                    ids = ids_next;
+                    ids_next = page_id(i + 16 + (lane & 15));
+                    const uint32_t in = __ballot_sync(kFullMask, ids >= 0) & 0xffffu;
+                    live = (live & (0xffff0000u >> (n & 16))) | in << (n & 16);
+                }
+                const int id = __shfl_sync(kFullMask, ids, n & 15);
+                if (id >= 0) {
+                    const uint8_t *k = kc + (size_t)id * kc_page, *v = vc + (size_t)id * vc_page;
+#pragma unroll
+                    for (int x = 0; x < 2 * GK; ++x)
+                        copy16(code_dst + slot_in + x * 512, k + (x >> 1) * kGroupCodes + (x & 1) * 512);
+#pragma unroll
+                    for (int x = 0; x < 2 * GV; ++x)
+                        copy16(code_dst + slot_in + Lay::kVOff + x * 512, v + (x >> 1) * kGroupCodes + (x & 1) * 512);
+                    if (par) copy16(par_dst + slot_in, par_src + (size_t)id * par_page);
+                    if constexpr (GK + GV > 4) {   // the parameters past the first 32 pieces
+                        constexpr int kRest = 8 * (GK + GV) - 32;   // all of V's last groups
+                        if (lane < kRest) {
+                            const int g = GV - kRest / 8 + lane / 8;
+                            copy16(par_dst + slot_in + 512, reinterpret_cast<const uint8_t*>(p.c.v_params) +
+                                                                ((size_t)id * p.c.Hkv + t.h) * GV * kGroupParams + g * kGroupParams +
+                                                                half * Lay::kParams + (lane & 7) * 16);
+                        }
+                    }
+                }
+                slot_in = slot_in == (S - 1) * Lay::kSlot ? 0 : slot_in + Lay::kSlot;
             }
-            const int id = __shfl_sync(kFullMask, ids, n & 15);
-            const uint32_t s = sent % S, bar = bars + 8 * s;
-            ++sent;
-            if (id >= 0) {
-                if (lane == 0) mbar_expect_tx(bar, Lay::kSlot);
-                __syncwarp();
-                if (lane < 2 * (GK + GV)) bulk_load(cp_dst + s * Lay::kSlot, cp_src + (size_t)id * cp_page, cp_bytes, bar);
-            } else if (lane == 0) {
-                mbar_arrive(bar);
-            }
+            copy_commit();
         };
-        if (ok)
-            for (int i = i0; i < i1 && i < i0 + S; ++i) issue(i);
+#pragma unroll
+        for (int x = 0; x < S - 1; ++x) issue(i0 + x);
         // ------------------------------------------------ its queries
         const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
         float qs;
@@ -661,16 +669,16 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 
         for (int i = i0; i < i1; ++i) {
             // -------------------------------------------- this warp's half page of unit i
-            // (after a wait that ran out no more is loaded or counted, and the warp goes on to the
-            // barriers that the other warps wait at)
-            const uint32_t s = got % S;
-            if (ok) ok = lanes_wait(bars + 8 * s, (got / S) & 1u, wc);
-            const bool valid = ok && ((live >> ((i - i0) & 31)) & 1u);
-            if (ok) ++got;
+            copy_wait<S - 2>();
+            __syncwarp();   // the slot is full, and every lane has read the one before
+            issue(i + S - 1);
+            const bool valid = (live >> ((i - i0) & 31)) & 1u;
+            const uint32_t st = ring + slot_out;
+            slot_out = slot_out == (S - 1) * Lay::kSlot ? 0 : slot_out + Lay::kSlot;
             const int key0 = page_of(w, 2 * i + (warp >> 1)) * kPage + 32 * half;
             if (valid) {
-                if (key0 >= full_lo && key0 + 32 <= full_hi) half_page(std::true_type{}, ring + s * Lay::kSlot, key0);
-                else half_page(std::false_type{}, ring + s * Lay::kSlot, key0);
+                if (key0 >= full_lo && key0 + 32 <= full_hi) half_page(std::true_type{}, st, key0);
+                else half_page(std::false_type{}, st, key0);
             } else if (kScores && 2 * i + (warp >> 1) < w.pages) {   // no key of a page that is out of range counts
                 float* dst = score_at + key0;
                 for (int n = 0; n < 2 * NR; ++n) {
@@ -679,15 +687,11 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     dst += n & 1 ? 7 * row_len : row_len;
                 }
             }
-            __syncwarp();   // every lane has read the slot
-            if (ok && i + S < i1) issue(i + S);
         }
         // ------------------------------------------------ the four warps' rows become one
         // (every copy into the slots has landed and been read: each warp's O rows go there)
         const bool ends = i1 == w.units, starts = i0 == 0;
-        if (!ok && lane == 0)   // (or is waited for here, after a wait that ran out)
-            for (; got < sent; ++got) drain_wait(bars + 8 * (got % S), (got / S) & 1u, p.wait_budget_ns);
-        got = __shfl_sync(kFullMask, got, 0);
+        __syncwarp();
         float* mine = reinterpret_cast<float*>(smem + warp * S * Lay::kSlot);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -755,8 +759,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)part * kRows + row) * 2) = make_float2(m, l);
             }
         }
-        fence_proxy_async_smem();   // the next row block's copies come after these reads and writes
-        __syncthreads();
+        __syncthreads();   // the next row block's copies come after these reads
     }
 }
 
