@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams 
             for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
             __syncthreads();
             const uint32_t mask = d == 0 ? 0u : 0xffffffffu << kShift[d - 1], digit = (1u << kBits[d]) - 1;
-#pragma unroll 4
+#pragma unroll 8
             for (int j = lo + tid; j < hi; j += kSelThreads) {
                 uint32_t key;
                 if (d == 0) {

@@ -521,6 +521,29 @@ def test_evict_reports_bad_pages():
         binding.check_status()
 
 
+@pytest.mark.gpu
+def test_pages_past_32_bit_offsets():
+    """A cache of more than 4 GB per tensor: its last pages work like its first ones."""
+    n_pages, Hkv, d = 70000, 8, 256
+    cache = binding.Kv4Cache.empty(n_pages, Hkv, d)
+    assert cache.k_codes.numel() > 2 ** 32
+    g = np.random.default_rng(27)
+    k, v, q = (bf16(g, 300, h, d).cuda() for h in (Hkv, Hkv, 16))
+    lens, cu = torch.tensor([300], dtype=torch.int32).cuda(), offsets([300]).cuda()
+    got = []
+    for first in (0, n_pages - 12):
+        table = torch.arange(first, first + 5, dtype=torch.int32).cuda()[None]
+        new = torch.arange(first + 6, first + 9, dtype=torch.int32).cuda()[None]
+        binding.kv4_append(cache, k, v, table, lens, cu_seqlens=cu)
+        w = torch.zeros(1, Hkv, 320, device="cuda")
+        o, lse = binding.kv4_forward(q[-2:], cache, table, lens, cu_seqlens=offsets([2]).cuda(), key_weights=w)
+        new_lens, kept, _ = binding.kv4_evict(cache, table, lens, w, new, budget=150, sinks=4, recent=30)
+        rk, rv = binding.kv4_read(cache, new, new_lens, 150, cu_seqlens=offsets([150]).cuda())
+        got.append((o, lse, w, kept, rk, rv))
+    binding.check_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and (got[0][0] != 0).any()
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.gpu
