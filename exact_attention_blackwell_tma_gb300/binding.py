@@ -456,7 +456,7 @@ class Kv4Cache:
     k_codes uint8 [pages, Hkv, d // 64, 64, 32], k_params bf16 [pages, Hkv, d // 64, 64, 2],
     v_codes and v_params the same with v's head dim."""
 
-    __slots__ = ("k_codes", "k_params", "v_codes", "v_params", "n_pages", "Hkv", "d", "dv", "_struct")
+    __slots__ = ("k_codes", "k_params", "v_codes", "v_params", "n_pages", "Hkv", "d", "dv", "device", "_struct")
 
     def __init__(self, k_codes, k_params, v_codes, v_params):
         pages, heads, groups = k_codes.shape[:3]
@@ -472,6 +472,7 @@ class Kv4Cache:
         _check_tensors(k_codes, k_params, v_codes, v_params)
         self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
         self.n_pages, self.Hkv, self.d, self.dv = pages, heads, groups * KV4_GROUP, v_groups * KV4_GROUP
+        self.device = device   # its index
         self._struct = _Kv4Struct(k_codes.data_ptr(), k_params.data_ptr(), v_codes.data_ptr(), v_params.data_ptr(),
                                   self.n_pages, self.Hkv, self.d, self.dv)
 
@@ -489,20 +490,26 @@ class Kv4Cache:
         return cls(codes(d), params(d), codes(dv), params(dv))
 
 
+def _kv4_int(name, t, dims, rows, device):
+    if t.dtype != torch.int32 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on cuda:{device}")
+    shape = t.shape
+    if len(shape) != dims or shape[0] != rows:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {dims} dimensions of {rows} rows")
+
+
 def _kv4_ints(cache, page_table, cache_lens, cu_seqlens, new_table=None):
     """Checks the int32 tensors of a call, which live on the cache's device, the current one; returns (B, device index)."""
-    device = cache.k_codes.get_device()
+    device = cache.device
     if device != torch.cuda.current_device():
         raise ValueError(f"the cache is on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
-    B = cache_lens.shape[0] if cache_lens.dim() == 1 else -1
-    for name, t, shape in (("cache_lens", cache_lens, 0), ("page_table", page_table, 2), ("cu_seqlens", cu_seqlens, 1),
-                           ("new_table", new_table, 2)):
-        if t is None and shape and name != "page_table":
-            continue
-        if t.dtype != torch.int32 or t.get_device() != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on cuda:{device}")
-        if t.dim() != max(shape, 1) or t.shape[0] != (B + 1 if shape == 1 else B):
-            raise ValueError(f"{name} has shape {tuple(t.shape)} for {B} sequences")
+    B = len(cache_lens)
+    _kv4_int("cache_lens", cache_lens, 1, B, device)
+    _kv4_int("page_table", page_table, 2, B, device)
+    if cu_seqlens is not None:
+        _kv4_int("cu_seqlens", cu_seqlens, 1, B + 1, device)
+    if new_table is not None:
+        _kv4_int("new_table", new_table, 2, B, device)
     return B, device
 
 
@@ -530,11 +537,12 @@ def _kv4_weights(key_weights, B, cache, device):
         raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on cuda:{device}")
 
 
-def _kv4_out(t, shape, dtype, device, name):
+def _kv4_out(t, shape, dtype, like, name):
+    """An output tensor: the caller's, checked, or a new one on the device of `like`."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+        return like.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {like.device}")
     return t
 
 
@@ -557,20 +565,21 @@ def kv4_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=None
     Lv, v_stride = _kv4_rows(v, cache.Hkv, cache.dv, B, cu_seqlens is not None, "v", device)
     if L != Lv:
         raise ValueError(f"k has {L} rows, v {Lv}")
-    _check(attn_kv4_append(k, v, k_stride, v_stride, cache._struct, page_table, page_table.shape[1], cache_lens,
-                           cu_seqlens, B, L, stream))
+    _check(load().attn_kv4_append(k.data_ptr(), v.data_ptr(), k_stride, v_stride, cache._struct, page_table.data_ptr(),
+                                  page_table.shape[1], cache_lens.data_ptr(), _ptr(cu_seqlens), B, L, _stream(stream)))
 
 
 def kv4_read(cache, page_table, cache_lens, rows, cu_seqlens=None, k=None, v=None, stream=None):
     """K, V in bf16 as the cache stands for them: the last rows of every sequence, packed ([rows, Hkv, d], rows =
     cu_seqlens[-1]) or dense (rows per sequence; [B, rows, Hkv, d], zero before a sequence's first token)."""
     B, _ = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
-    device = cache.k_codes.device
-    lead = (rows,) if cu_seqlens is not None else (B, rows)
+    like, heads = cache.k_params, cache.Hkv
+    packed = cu_seqlens is not None
     with _on(stream):
-        k = _kv4_out(k, lead + (cache.Hkv, cache.d), torch.bfloat16, device, "k")
-        v = _kv4_out(v, lead + (cache.Hkv, cache.dv), torch.bfloat16, device, "v")
-    _check(attn_kv4_read(k, v, cache._struct, page_table, page_table.shape[1], cache_lens, cu_seqlens, B, rows, stream))
+        k = _kv4_out(k, (rows, heads, cache.d) if packed else (B, rows, heads, cache.d), torch.bfloat16, like, "k")
+        v = _kv4_out(v, (rows, heads, cache.dv) if packed else (B, rows, heads, cache.dv), torch.bfloat16, like, "v")
+    _check(load().attn_kv4_read(k.data_ptr(), v.data_ptr(), cache._struct, page_table.data_ptr(), page_table.shape[1],
+                                cache_lens.data_ptr(), _ptr(cu_seqlens), B, rows, _stream(stream)))
     return k, v
 
 
@@ -581,7 +590,7 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     their keys have been appended. window and sinks as in forward(). key_weights (fp32 [B, Hkv, >= longest cache]):
     updated in place to weight_decay * key_weights + the attention weight each key got from the call's rows."""
     B, index = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
-    H, packed, device = q.shape[-2], cu_seqlens is not None, cache.k_codes.device
+    H, packed = q.shape[-2], cu_seqlens is not None
     L, q_stride = _kv4_rows(q, H, cache.d, B, packed, "q", index)
     if H % cache.Hkv != 0 or H == 0:
         raise ValueError(f"{H} query heads over {cache.Hkv} key/value heads")
@@ -591,14 +600,16 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     width = page_table.shape[1]
     need = _kv4_workspace(B, H, cache.Hkv, L, packed, width, cache.d, cache.dv, key_weights is not None)
     with _on(stream):
-        out = _kv4_out(out, q.shape[:-1] + (cache.dv,), torch.bfloat16, device, "out")
-        lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, device, "lse")
+        out = _kv4_out(out, (L, H, cache.dv) if packed else (B, L, H, cache.dv), torch.bfloat16, q, "out")
+        lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, q, "lse")
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    _check(attn_kv4_fwd(q, q_stride, cache._struct, page_table, width, cache_lens, cu_seqlens, out, lse, B, H, L, scale,
-                        causal, window[0], window[1], sinks, key_weights,
-                        0 if key_weights is None else key_weights.shape[2], weight_decay, workspace,
-                        workspace.numel() * workspace.element_size(), stream))
+            workspace, size = cache.k_codes.new_empty(max(need, 1)), need
+        else:
+            size = workspace.numel() * workspace.element_size()
+    _check(load().attn_kv4_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), width, cache_lens.data_ptr(),
+                               _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr(), B, H, L, scale, int(causal), window[0],
+                               window[1], sinks, _ptr(key_weights), 0 if key_weights is None else key_weights.shape[2],
+                               weight_decay, workspace.data_ptr(), size, _stream(stream)))
     return out, lse
 
 
@@ -609,14 +620,14 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
     are not in page_table). Returns new_lens int32 [B], kept int32 [B, Hkv, budget] (old token of each new one, -1 past
     the new length) and the kept key weights fp32 [B, Hkv, budget] (or as wide as new_key_weights is)."""
     B, index = _kv4_ints(cache, page_table, cache_lens, None, new_table)
-    device = cache.k_codes.device
     _kv4_weights(key_weights, B, cache, index)
     columns = budget if new_key_weights is None else new_key_weights.shape[-1]
     with _on(stream):
-        new_lens = _kv4_out(new_lens, (B,), torch.int32, device, "new_lens")
-        kept = _kv4_out(kept, (B, cache.Hkv, budget), torch.int32, device, "kept")
-        new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, device, "new_key_weights")
-    _check(attn_kv4_evict(cache._struct, page_table, page_table.shape[1], cache_lens, key_weights, key_weights.shape[2],
-                          new_table, new_table.shape[1], B, budget, sinks, recent, new_lens, kept, new_key_weights,
-                          columns, stream))
+        new_lens = _kv4_out(new_lens, (B,), torch.int32, cache_lens, "new_lens")
+        kept = _kv4_out(kept, (B, cache.Hkv, budget), torch.int32, cache_lens, "kept")
+        new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, key_weights, "new_key_weights")
+    _check(load().attn_kv4_evict(cache._struct, page_table.data_ptr(), page_table.shape[1], cache_lens.data_ptr(),
+                                 key_weights.data_ptr(), key_weights.shape[2], new_table.data_ptr(), new_table.shape[1],
+                                 B, budget, sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
+                                 new_key_weights.data_ptr(), columns, _stream(stream)))
     return new_lens, kept, new_key_weights
