@@ -537,12 +537,12 @@ def _kv4_weights(key_weights, B, cache, device):
         raise ValueError(f"key_weights must be a contiguous fp32 tensor [{B}, {cache.Hkv}, keys] on cuda:{device}")
 
 
-def _kv4_out(t, shape, dtype, like, name):
-    """An output tensor: the caller's, checked, or a new one on the device of `like`."""
+def _kv4_out(t, shape, dtype, device, name):
+    """An output tensor: the caller's, checked, or a new one."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
-    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {like.device}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
     return t
 
 
@@ -573,11 +573,11 @@ def kv4_read(cache, page_table, cache_lens, rows, cu_seqlens=None, k=None, v=Non
     """K, V in bf16 as the cache stands for them: the last rows of every sequence, packed ([rows, Hkv, d], rows =
     cu_seqlens[-1]) or dense (rows per sequence; [B, rows, Hkv, d], zero before a sequence's first token)."""
     B, _ = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
-    like, heads = cache.k_params, cache.Hkv
+    device, heads = cache.k_codes.device, cache.Hkv
     packed = cu_seqlens is not None
     with _on(stream):
-        k = _kv4_out(k, (rows, heads, cache.d) if packed else (B, rows, heads, cache.d), torch.bfloat16, like, "k")
-        v = _kv4_out(v, (rows, heads, cache.dv) if packed else (B, rows, heads, cache.dv), torch.bfloat16, like, "v")
+        k = _kv4_out(k, (rows, heads, cache.d) if packed else (B, rows, heads, cache.d), torch.bfloat16, device, "k")
+        v = _kv4_out(v, (rows, heads, cache.dv) if packed else (B, rows, heads, cache.dv), torch.bfloat16, device, "v")
     _check(load().attn_kv4_read(k.data_ptr(), v.data_ptr(), cache._struct, page_table.data_ptr(), page_table.shape[1],
                                 cache_lens.data_ptr(), _ptr(cu_seqlens), B, rows, _stream(stream)))
     return k, v
@@ -590,7 +590,7 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     their keys have been appended. window and sinks as in forward(). key_weights (fp32 [B, Hkv, >= longest cache]):
     updated in place to weight_decay * key_weights + the attention weight each key got from the call's rows."""
     B, index = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
-    H, packed = q.shape[-2], cu_seqlens is not None
+    H, packed, device = q.shape[-2], cu_seqlens is not None, q.device
     L, q_stride = _kv4_rows(q, H, cache.d, B, packed, "q", index)
     if H % cache.Hkv != 0 or H == 0:
         raise ValueError(f"{H} query heads over {cache.Hkv} key/value heads")
@@ -600,10 +600,10 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     width = page_table.shape[1]
     need = _kv4_workspace(B, H, cache.Hkv, L, packed, width, cache.d, cache.dv, key_weights is not None)
     with _on(stream):
-        out = _kv4_out(out, (L, H, cache.dv) if packed else (B, L, H, cache.dv), torch.bfloat16, q, "out")
-        lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, q, "lse")
+        out = _kv4_out(out, (L, H, cache.dv) if packed else (B, L, H, cache.dv), torch.bfloat16, device, "out")
+        lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, device, "lse")
         if workspace is None:
-            workspace, size = cache.k_codes.new_empty(max(need, 1)), need
+            workspace, size = torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
         else:
             size = workspace.numel() * workspace.element_size()
     _check(load().attn_kv4_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), width, cache_lens.data_ptr(),
@@ -621,11 +621,12 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
     the new length) and the kept key weights fp32 [B, Hkv, budget] (or as wide as new_key_weights is)."""
     B, index = _kv4_ints(cache, page_table, cache_lens, None, new_table)
     _kv4_weights(key_weights, B, cache, index)
+    device = cache_lens.device
     columns = budget if new_key_weights is None else new_key_weights.shape[-1]
     with _on(stream):
-        new_lens = _kv4_out(new_lens, (B,), torch.int32, cache_lens, "new_lens")
-        kept = _kv4_out(kept, (B, cache.Hkv, budget), torch.int32, cache_lens, "kept")
-        new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, key_weights, "new_key_weights")
+        new_lens = _kv4_out(new_lens, (B,), torch.int32, device, "new_lens")
+        kept = _kv4_out(kept, (B, cache.Hkv, budget), torch.int32, device, "kept")
+        new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, device, "new_key_weights")
     _check(load().attn_kv4_evict(cache._struct, page_table.data_ptr(), page_table.shape[1], cache_lens.data_ptr(),
                                  key_weights.data_ptr(), key_weights.shape[2], new_table.data_ptr(), new_table.shape[1],
                                  B, budget, sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
