@@ -122,8 +122,8 @@ struct Kv4Layout {
                          kSlot = kVpOff + GV * kParams;
     static constexpr int kSlots = D + DV <= 128 ? 4 : (D + DV <= 256 ? 3 : 2);   // per warp
     static constexpr int kQOff = kWarps * kSlots * kSlot;         // q fragments [NR][GK][2][32 lanes] x 16 bytes
-    static constexpr int kQSumOff = kQOff + NR * GK * 1024;       // q's sums [rows][GK], each warp's largest |q|
-    static constexpr int kMlOff = kQSumOff + (kRows * GK + kWarps) * 4 + (kRows * GK & 1) * 4;   // (max, sum) per warp and row
+    static constexpr int kQSumOff = kQOff + NR * GK * 1024;       // q's (sum, largest |q|) per row and group
+    static constexpr int kMlOff = kQSumOff + kRows * GK * 8;      // (max, sum) per warp and row
     static constexpr int kPrefixOff = (kMlOff + kWarps * kRows * 8 + 15) / 16 * 16;
     // at the end of a row block each warp's O rows go where its slots were
     static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
@@ -286,9 +286,9 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     // 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of P^T) lie 4 tokens apart and a warp's 32-bit loads hit 32 banks.
     const int half = warp & 1, tok0 = (g8 >> 1) + 4 * (g8 & 1);   // keys tok0, + 8 (chunk 0), + 16, + 24
     float acc[GV * 4][NR][4];
-    float qsum[NR][2][GK], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
+    float qsum[NR][2][GK], qscale[NR][2], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
     int klo[NR][2], khi[NR][2];
-    float* qsums = reinterpret_cast<float*>(smem + Lay::kQSumOff);
+    float2* qstat = reinterpret_cast<float2*>(smem + Lay::kQSumOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
     const long row_len = (long)p.s.width * kPage;
     for (int u = u0; u < u1;) {
@@ -360,12 +360,10 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         for (int x = 0; x < S - 1; ++x) issue(i0 + x);
         // ------------------------------------------------ its queries
         const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
-        float qs;
         {
             // (n, g) = 8 rows x 64 channels each, dealt to the warps; a lane takes row g8's channels 16 t4 ..
             constexpr int kTasks = (NR * GK + kWarps - 1) / kWarps;
             uint4 raw[kTasks][2];
-            float top = 0.f;
 #pragma unroll
             for (int y = 0; y < kTasks; ++y) {
                 const int task = y * kWarps + warp, n = task / GK, g = task % GK;
@@ -383,7 +381,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                 const int task = y * kWarps + warp, n = task / GK, g = task % GK;
                 const uint32_t ws[8] = {raw[y][0].x, raw[y][0].y, raw[y][0].z, raw[y][0].w,
                                         raw[y][1].x, raw[y][1].y, raw[y][1].z, raw[y][1].w};
-                float part = 0.f;
+                float part = 0.f, top = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float a = lo_bf16(ws[i]), b = hi_bf16(ws[i]);
@@ -391,24 +389,27 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     part += a;
                     part += b;
                 }
-                part += __shfl_xor_sync(kFullMask, part, 1);
-                part += __shfl_xor_sync(kFullMask, part, 2);
-                if (t4 == 0 && task < NR * GK) qsums[(n * 8 + g8) * GK + g] = part;
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    part += __shfl_xor_sync(kFullMask, part, o);
+                    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+                }
+                if (t4 == 0 && task < NR * GK) qstat[(n * 8 + g8) * GK + g] = make_float2(part, top);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-            if (lane == 0) qsums[kRows * GK + warp] = top;
             __syncthreads();
+            // row r times 2^e has its largest element in [2^14, 2^15) (both powers stay in the float range;
+            // a row of its own exponent, so that whatever an unused row of a padded batch holds stays there)
+            auto row_exponent = [&](int r) {
+                float top = 0.f;
 #pragma unroll
-            for (int x = 0; x < kWarps; ++x) top = fmaxf(top, qsums[kRows * GK + x]);
-            // the block's rows times 2^e have their largest element in [2^14, 2^15) (both powers stay in the float range)
-            const int e = top > 0.f && top < INFINITY ? min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 126) : 0;
-            const float f = pow2(e), f16 = f * 0.0625f;
-            qs = p.scale_log2 * pow2(24 - e);
+                for (int g = 0; g < GK; ++g) top = fmaxf(top, qstat[r * GK + g].y);
+                return top > 0.f && top < INFINITY ? min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 126) : 0;
+            };
 #pragma unroll
             for (int y = 0; y < kTasks; ++y) {
                 const int task = y * kWarps + warp;
                 if (task >= NR * GK) break;
+                const float f = pow2(row_exponent(task / GK * 8 + g8)), f16 = f * 0.0625f;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     // word x holds channels 8 x .. 8 x + 7; step 2 x takes (0, 4) and (1, 5), step 2 x + 1 (2, 6) and (3, 7);
@@ -424,7 +425,8 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int g = 0; g < GK; ++g) qsum[n][c][g] = p.scale_log2 * qsums[(n * 8 + 2 * t4 + c) * GK + g];
+                    for (int g = 0; g < GK; ++g) qsum[n][c][g] = p.scale_log2 * qstat[(n * 8 + 2 * t4 + c) * GK + g].x;
+                    qscale[n][c] = p.scale_log2 * pow2(24 - row_exponent(n * 8 + 2 * t4 + c));
                     const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
                     const int i = row / p.group;
                     klo[n][c] = row < w.rows ? band_key_lo(mb, i) : 0;
@@ -490,13 +492,13 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                             else mma_f16(d[n], a0, a1, a2, a3, (k & 1) ? q4.z : q4.x, (k & 1) ? q4.w : q4.y);
                         }
                     }
-                    const float aa = lo_bf16(pa) * qs, ba = hi_bf16(pa), ab = lo_bf16(pb) * qs, bb = hi_bf16(pb);
+                    const float aa = lo_bf16(pa), ba = hi_bf16(pa), ab = lo_bf16(pb), bb = hi_bf16(pb);
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            sc[ck][n][c] = fmaf(d[n][c], aa, fmaf(qsum[n][c][g], ba, g ? sc[ck][n][c] : -mu[n][c]));
-                            sc[ck][n][2 + c] = fmaf(d[n][2 + c], ab, fmaf(qsum[n][c][g], bb, g ? sc[ck][n][2 + c] : -mu[n][c]));
+                            sc[ck][n][c] = fmaf(d[n][c] * qscale[n][c], aa, fmaf(qsum[n][c][g], ba, g ? sc[ck][n][c] : -mu[n][c]));
+                            sc[ck][n][2 + c] = fmaf(d[n][2 + c] * qscale[n][c], ab, fmaf(qsum[n][c][g], bb, g ? sc[ck][n][2 + c] : -mu[n][c]));
                         }
                 }
             }

@@ -351,6 +351,27 @@ def test_forward_query_sizes(size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("junk", [3e38, 1e10, math.inf, math.nan, 0.0])
+def test_forward_unused_rows_hold_anything(junk):
+    """A padded dense batch: rows before a short sequence's tokens see no key, and neither they nor a neighbour's
+    bad row reach the rows beside them."""
+    pool = Pool([2, 100], 2, 128, seed=28)
+    q = bf16(pool.g, 2, 4, 4, 128)
+    q[0, :2] = junk   # sequence 0 has two tokens, its first two rows are padding
+    q[1, 1, 2] = junk
+    o, lse = binding.kv4_forward(q.cuda(), pool.cache, pool.table, pool.lens_t)
+    assert (o[0, :2] == 0).all() and torch.isneginf(lse[0, :, :2]).all()
+    clean = q.clone()
+    clean[0, :2] = 1
+    clean[1, 1, 2] = 1
+    o2, lse2 = binding.kv4_forward(clean.cuda(), pool.cache, pool.table, pool.lens_t)
+    keep = torch.ones(2, 4, 4, dtype=torch.bool)
+    keep[1, 1, 2] = False
+    assert torch.equal(o.cpu()[keep], o2.cpu()[keep]) and torch.equal(lse.cpu().transpose(1, 2)[keep], lse2.cpu().transpose(1, 2)[keep])
+    binding.check_status()
+
+
+@pytest.mark.gpu
 def test_forward_a_maximum_that_climbs():
     """Scores that grow along the cache move the running maximum again and again."""
     pool = Pool([2000], 1, 64, seed=18)
