@@ -123,7 +123,8 @@ struct Kv4Layout {
     static constexpr int kSlots = D + DV <= 128 ? 4 : (D + DV <= 256 ? 3 : 2);   // per warp
     static constexpr int kQOff = kWarps * kSlots * kSlot;         // q fragments [NR][GK][2][32 lanes] x 16 bytes
     static constexpr int kQSumOff = kQOff + NR * GK * 1024;       // q's (sum, largest |q|) per row and group
-    static constexpr int kMlOff = kQSumOff + kRows * GK * 8;      // (max, sum) per warp and row
+    static constexpr int kKeysOff = kQSumOff + kRows * GK * 8;    // the keys [lo, hi) of each row's window
+    static constexpr int kMlOff = kKeysOff + kRows * 8;           // (max, sum) per warp and row
     static constexpr int kPrefixOff = (kMlOff + kWarps * kRows * 8 + 15) / 16 * 16;
     // at the end of a row block each warp's O rows go where its slots were
     static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
     const int half = warp & 1, tok0 = (g8 >> 1) + 4 * (g8 & 1);   // keys tok0, + 8 (chunk 0), + 16, + 24
     float acc[GV * 4][NR][4];
     float qsum[NR][2][GK], qscale[NR][2], m_run[NR][2], mu[NR][2], l_run[NR][2], zb[NR][2][GV], wsc[GV];
-    int klo[NR][2], khi[NR][2];
+    int2* row_keys = reinterpret_cast<int2*>(smem + Lay::kKeysOff);
     float2* qstat = reinterpret_cast<float2*>(smem + Lay::kQSumOff);
     float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
     const long row_len = (long)p.s.width * kPage;
@@ -360,6 +361,10 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
         for (int x = 0; x < S - 1; ++x) issue(i0 + x);
         // ------------------------------------------------ its queries
         const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
+        if (tid < kRows) {
+            const int row = t.rb * kRows + tid, i = row / p.group;
+            row_keys[tid] = row < w.rows ? make_int2(band_key_lo(mb, i), band_key_hi(mb, i)) : make_int2(0, 0);
+        }
         {
             // (n, g) = 8 rows x 64 channels each, dealt to the warps; a lane takes row g8's channels 16 t4 ..
             constexpr int kTasks = (NR * GK + kWarps - 1) / kWarps;
@@ -427,10 +432,6 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 #pragma unroll
                     for (int g = 0; g < GK; ++g) qsum[n][c][g] = p.scale_log2 * qstat[(n * 8 + 2 * t4 + c) * GK + g].x;
                     qscale[n][c] = p.scale_log2 * pow2(24 - row_exponent(n * 8 + 2 * t4 + c));
-                    const int row = t.rb * kRows + n * 8 + 2 * t4 + c;
-                    const int i = row / p.group;
-                    klo[n][c] = row < w.rows ? band_key_lo(mb, i) : 0;
-                    khi[n][c] = row < w.rows ? band_key_hi(mb, i) : 0;
                     m_run[n][c] = -INFINITY;
                     mu[n][c] = l_run[n][c] = 0.f;
 #pragma unroll
@@ -504,14 +505,16 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
             }
             if constexpr (!kWhole) {
 #pragma unroll
-                for (int ck = 0; ck < 2; ++ck)
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
+                    for (int c = 0; c < 2; ++c) {
+                        const int2 k = row_keys[n * 8 + 2 * t4 + c];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int j = key0 + tok0 + 16 * ck + 8 * (x >> 1);
-                            if (!(j < khi[n][x & 1] && (j >= klo[n][x & 1] || j < p.sinks))) sc[ck][n][x] = -INFINITY;
+                            const int j = key0 + tok0 + 8 * x;
+                            if (!(j < k.y && (j >= k.x || j < p.sinks))) sc[x >> 1][n][2 * (x & 1) + c] = -INFINITY;
                         }
+                    }
             }
             if constexpr (kScores) {
                 float* dst = score_at + key0;
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                             sc[ck][n][c] += mu[n][c] - mu_new;
                             sc[ck][n][2 + c] += mu[n][c] - mu_new;
                         }
-                        unset |= m_new == -INFINITY && khi[n][c] > 0;
+                        unset |= m_new == -INFINITY && row_keys[n * 8 + 2 * t4 + c].y > 0;
                         m_run[n][c] = m_new;
                         mu[n][c] = mu_new;
                         l_run[n][c] *= al[c];
