@@ -295,9 +295,11 @@ __device__ __forceinline__ float dot8(const uint4* a, const uint4* b, int pieces
 }
 
 // Where such rows weigh: a short window with its sinks gives few keys to every
-// row, a short sequence to a good part of them. (Looking for them costs the
-// preprocess kernel half its time again: B2 H16 L8192 d128 38 -> 56 us; over long
-// sequences a handful of first rows does not show in the gradients.)
+// row, and of a short sequence's rows a good part see few. Beyond, the first rows
+// under a causal mask still would, but looking for them costs the preprocess kernel
+// half its time again (B2 H16 L8192 d128 38 -> 56 us; one head pair of 300 rows: the
+// step 36 -> 43 us) for a few percent of the error (2.7e-3 -> 2.6e-3 there), the rest
+// of which is the rounding of dS itself.
 inline bool few_key_rows(const BwdParams& p) {
     const Geometry& g = p.g;
     if (p.mask.sinks <= 0 || p.mask.ptr || g.B <= 0) return false;
@@ -331,23 +333,26 @@ __device__ __noinline__ float few_keys_D(const BwdParams& p, float otherwise, bo
     if (!__any_sync(0xffffffffu, few)) return otherwise;
     const float lse2 = few ? p.lse[li] * kLog2e : 0.f;
     const long i = row * g.H + h;
-    float D = 0.f;
+    float s[kFewKeys], dp[kFewKeys];   // (the keys' loads go out together, the shuffles follow)
+#pragma unroll
     for (int x = 0; x < kFewKeys; ++x) {
-        const bool in = few && x < n;
-        float s = 0.f, dp = 0.f;
-        if (in) {
-            const long key = (k0 + (x < n_sink ? x : lo + x - n_sink)) * g.Hkv + h / g.group;
-            s = dot8(reinterpret_cast<const uint4*>(p.q + i * g.d), reinterpret_cast<const uint4*>(p.k + key * g.d),
-                     g.d / 64, l8);
-            dp = dot8(reinterpret_cast<const uint4*>(p.dout + i * p.d_v), reinterpret_cast<const uint4*>(p.v + key * p.d_v),
-                      p.d_v / 64, l8);
-        }
+        s[x] = dp[x] = 0.f;
+        if (!few || x >= n) continue;
+        const long key = (k0 + (x < n_sink ? x : lo + x - n_sink)) * g.Hkv + h / g.group;
+        s[x] = dot8(reinterpret_cast<const uint4*>(p.q + i * g.d), reinterpret_cast<const uint4*>(p.k + key * g.d),
+                    g.d / 64, l8);
+        dp[x] = dot8(reinterpret_cast<const uint4*>(p.dout + i * p.d_v), reinterpret_cast<const uint4*>(p.v + key * p.d_v),
+                     p.d_v / 64, l8);
+    }
+    float D = 0.f;
+#pragma unroll
+    for (int x = 0; x < kFewKeys; ++x) {
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            dp += __shfl_xor_sync(0xffffffffu, dp, o);
+            s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
+            dp[x] += __shfl_xor_sync(0xffffffffu, dp[x], o);
         }
-        if (in) D = fmaf(exp2f(fmaf(s, g.scale_log2, -lse2)), dp, D);
+        if (few && x < n) D = fmaf(exp2f(fmaf(s[x], g.scale_log2, -lse2)), dp[x], D);
     }
     return few ? D : otherwise;
 }

@@ -62,9 +62,9 @@ struct Kv4FwdParams {
 
 // Row blocks: a CTA holds 8 * kv4_row_tiles(...) (query, head-of-the-group) rows
 // of one key/value head at once. Blocks of 16 rows when an average sequence has
-// more than 8; larger ones lose more to the registers they take from the number
-// of warps than they save by reading the codes less often (32 sequences, group 4,
-// 1 to 16 tokens each, d = 128: 8 rows at once 160 us, 16: 146, 32: 191).
+// more than 8 (32 sequences, group 4, 1 to 16 tokens each, d = 128: 111 us, 123 with
+// 8 rows at once); blocks of 32 took so many registers from the number of warps
+// that they lost more than they saved by reading the codes less often.
 inline int kv4_row_tiles(int group, int B, int total) {
     const long rows = B > 0 ? (long)group * ((total + B - 1) / B) : group;
     return rows <= 8 ? 1 : 2;
