@@ -83,41 +83,41 @@ def kinds_of(w):
 # is checked at run time and the field is reported as null after any change.
 NCU_TRAFFIC = {
     ("b1h32l32768d128", "bwd", False): {
-        "bytes": 8728.203e6 + 4564.870e6,
+        "bytes": 8721.897e6 + 4562.903e6,
         "profile": "profiles/bwd_kernel_b1h32l32768d128_traffic.md",
         "sources": {
             "exact_attention_blackwell_tma_gb300/csrc/bwd.cu":
-                "60bc2511e502cc06be6d193c1279504a2fdce162ce618fc40e08004425c032ba",
+                "e82505a11c245679ee26dccb7d3040eb64e9dbb84adee13eaaf3c58aef32a56e",
             "exact_attention_blackwell_tma_gb300/csrc/ptx.cuh":
-                "3c0283284f2342dd722773b9195bbfdc67274aa16994dbb143983c848529bf9c",
+                "641795ebbb9bb4db85c45ff90508640a49b30853717bfc035d19782c6042499a",
             "exact_attention_blackwell_tma_gb300/csrc/sched.cuh":
-                "0328db7053351282b31375c9f4ccf44236a648824c9e57efab5f143fdd22abd6",
+                "1bf2728d0ebfb0c5e8443d8ad2a7d35d6695a44d7680a85ab013340ae3d5dc72",
             "exact_attention_blackwell_tma_gb300/csrc/kernels.h":
-                "5affc1850bc7073eafc4f405d84928b0a015bd41fe555c117e9c97cdf3d90f72",
+                "cfd62a1654d6de06e28134109898fea0340c2c7eb402228477cba3fc3ed48ed0",
             "exact_attention_blackwell_tma_gb300/csrc/mask.cuh":
-                "a8db3e42b70e326e0df86ce85e11cf81134dc7f609b7d0006d9f1a409692beee",
+                "3a36f66481eeaa601a81dc1e2c9802d77209c7b9b1f652cde28e47ce91c864b7",
             "exact_attention_blackwell_tma_gb300/csrc/dq_order.cuh":
-                "d3268cfe95ac87277ec035e806c4ac4c57c17361d3c6b4c9c26b3e80fa94ac40",
+                "845908a7abb4fb1f6f9cd931394d8f1af9716a1617deaf0499d7364b4dccaac4",
             "exact_attention_blackwell_tma_gb300/csrc/dq_reduce.cuh":
                 "7ddedbe18fcca40f3a3e932502abeb8096da330d02b5731aeb6314e8dafeb072",
         },
     },
     ("b1h32l32768d128", "bwd", True): {
-        "bytes": 6605.666e6 + 3768.216e6,
+        "bytes": 6230.453e6 + 3538.929e6,
         "profile": "profiles/bwd_kernel_b1h32l32768d128_traffic.md",
         "sources": {
             "exact_attention_blackwell_tma_gb300/csrc/bwd.cu":
-                "60bc2511e502cc06be6d193c1279504a2fdce162ce618fc40e08004425c032ba",
+                "e82505a11c245679ee26dccb7d3040eb64e9dbb84adee13eaaf3c58aef32a56e",
             "exact_attention_blackwell_tma_gb300/csrc/ptx.cuh":
-                "3c0283284f2342dd722773b9195bbfdc67274aa16994dbb143983c848529bf9c",
+                "641795ebbb9bb4db85c45ff90508640a49b30853717bfc035d19782c6042499a",
             "exact_attention_blackwell_tma_gb300/csrc/sched.cuh":
-                "0328db7053351282b31375c9f4ccf44236a648824c9e57efab5f143fdd22abd6",
+                "1bf2728d0ebfb0c5e8443d8ad2a7d35d6695a44d7680a85ab013340ae3d5dc72",
             "exact_attention_blackwell_tma_gb300/csrc/kernels.h":
-                "5affc1850bc7073eafc4f405d84928b0a015bd41fe555c117e9c97cdf3d90f72",
+                "cfd62a1654d6de06e28134109898fea0340c2c7eb402228477cba3fc3ed48ed0",
             "exact_attention_blackwell_tma_gb300/csrc/mask.cuh":
-                "a8db3e42b70e326e0df86ce85e11cf81134dc7f609b7d0006d9f1a409692beee",
+                "3a36f66481eeaa601a81dc1e2c9802d77209c7b9b1f652cde28e47ce91c864b7",
             "exact_attention_blackwell_tma_gb300/csrc/dq_order.cuh":
-                "d3268cfe95ac87277ec035e806c4ac4c57c17361d3c6b4c9c26b3e80fa94ac40",
+                "845908a7abb4fb1f6f9cd931394d8f1af9716a1617deaf0499d7364b4dccaac4",
             "exact_attention_blackwell_tma_gb300/csrc/dq_reduce.cuh":
                 "7ddedbe18fcca40f3a3e932502abeb8096da330d02b5731aeb6314e8dafeb072",
         },

@@ -346,6 +346,9 @@ def _mask_heads(block_mask, H, Lq, Lk):
     return 1 if len(shape) == 2 else shape[0]
 
 
+_sinks_workspace = functools.lru_cache(maxsize=4096)(attn_bwd_sinks_workspace_size)   # a function of the sizes alone
+
+
 def _no_block_mask(block_mask):
     if block_mask is not None:
         raise ValueError("sinks are not combined with a block mask")
@@ -380,8 +383,9 @@ def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, 
         lse = torch.empty((B, H, Lq) if cu_seqlens is None else (H, Lq), dtype=torch.float32, device=q.device)
     if sinks:
         _no_block_mask(block_mask)
-        _check(attn_fwd_sinks(q, k, v, out, lse, B, H, Hkv, Lq, Lk, d, dv, scale, causal, window[0], window[1], sinks,
-                              cu_seqlens, cu_seqlens_k, stream))
+        _check(load().attn_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv,
+                                     Lq, Lk, d, dv, scale, int(causal), window[0], window[1], sinks, _ptr(cu_seqlens),
+                                     _ptr(cu_seqlens_k), _stream(stream)))
     elif tuple(window) != (-1, -1) or block_mask is not None:
         mh = _mask_heads(block_mask, H, Lq, Lk)
         _check_tensors(block_mask)
@@ -410,8 +414,7 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     d_v = v.shape[-1]
     if sinks:
-        need = attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window[0], window[1], sinks,
-                                             deterministic)
+        need = _sinks_workspace(B, H, Hkv, Lq, Lk, d, d_v, causal, window[0], window[1], sinks, deterministic)
     else:
         need = attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
@@ -422,8 +425,11 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
     ws_bytes = workspace.numel() * workspace.element_size()
     if sinks:
         _no_block_mask(block_mask)
-        _check(attn_bwd_sinks(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window[0],
-                              window[1], sinks, cu_seqlens, cu_seqlens_k, deterministic, workspace, ws_bytes, stream))
+        _check(load().attn_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                     dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Lq, Lk, d,
+                                     d_v, scale, int(causal), window[0], window[1], sinks, _ptr(cu_seqlens),
+                                     _ptr(cu_seqlens_k), int(deterministic), workspace.data_ptr(), ws_bytes,
+                                     _stream(stream)))
     elif d_v != d or tuple(window) != (-1, -1) or block_mask is not None:
         mh = _mask_heads(block_mask, H, Lq, Lk)
         _check_tensors(block_mask)

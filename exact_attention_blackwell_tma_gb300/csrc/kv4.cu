@@ -10,14 +10,9 @@ namespace {
 
 __device__ __forceinline__ void bad_page(int* status) { atomicCAS(status, kStatusOk, kStatusBadPage); }
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {   // of two bf16 each
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -154,17 +149,14 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4Cache c, Kv4Batch s,
                     f[2 * j] = __uint_as_float(w[j] << 16);
                     f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
                 }
-                float lo = f[0], hi = f[0];
+                // (min, -max) of the group as one bf16 pair: the shuffles carry both, NaN wins
+                uint32_t mn = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
+                uint32_t mx = min2_nan(min2_nan(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u),
+                                       min2_nan(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
+                uint32_t m = min2_nan(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
 #pragma unroll
-                for (int j = 1; j < 8; ++j) {
-                    lo = min_nan(lo, f[j]);
-                    hi = max_nan(hi, f[j]);
-                }
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) {
-                    lo = min_nan(lo, __shfl_xor_sync(kFullMask, lo, o));
-                    hi = max_nan(hi, __shfl_xor_sync(kFullMask, hi, o));
-                }
+                for (int o = 1; o < 8; o <<= 1) m = min2_nan(m, __shfl_xor_sync(kFullMask, m, o));
+                const float lo = __uint_as_float(m << 16), hi = -__uint_as_float(m & 0xffff0000u);
                 if (ch >= chunks) continue;
                 const float sc = scale_of(lo, hi);
                 const uint32_t codes = codes_of(f, lo, hi, sc);
