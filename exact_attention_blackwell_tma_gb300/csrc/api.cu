@@ -613,9 +613,10 @@ int check_kv4(const attn_kv4_cache* c, int B, int L, const int* table, int width
     if (c->d_v != c->d && !(c->d == 192 && c->d_v == 128))
         return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (d_v = d, or d = 192 with d_v = 128)", c->d,
                     c->d_v);
-    if ((long)width * kPage >= (1L << 31)) return fail(ATTN_ERR_ARG, "kv4: table width %d too large", width);
+    // (tokens and rows below 2^30: a row's position plus a window bound stays an int)
+    if ((long)width * kPage >= (1L << 30)) return fail(ATTN_ERR_ARG, "kv4: table width %d too large", width);
     const long total = cu ? (long)L : (long)B * L;
-    if (total >= (1L << 31)) return fail(ATTN_ERR_ARG, "too many rows");
+    if (total >= (1L << 30)) return fail(ATTN_ERR_ARG, "too many rows");
     if (B > 0 && (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params || !table || !lens))
         return fail(ATTN_ERR_ARG, "null tensor pointer");
     if (!aligned16(c->k_codes) || !aligned16(c->k_params) || !aligned16(c->v_codes) || !aligned16(c->v_params))
@@ -690,7 +691,7 @@ extern "C" size_t attn_kv4_fwd_workspace_size(int B, int H, int Hkv, int L, int 
                                               int key_weights) {
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || table_width < 1 || d <= 0 || d_v <= 0) return 0;
     const long total = packed ? (long)L : (long)B * L;
-    if (total >= (1L << 31)) return 0;
+    if (total >= (1L << 30)) return 0;
     return kv4_layout(B, H, Hkv, total, table_width, d, d_v, key_weights != 0).total;
 }
 
@@ -746,7 +747,6 @@ extern "C" int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_ca
     p.part_o = reinterpret_cast<float*>(ws + wl.part);
     p.scores = key_weights ? reinterpret_cast<float*>(ws + wl.scores) : nullptr;
     p.status = di.status;
-    p.wait_budget_ns = wait_budget_ns();
     const cudaError_t e = launch_kv4_fwd(p, di.sms, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 forward launch failed: %s", cudaGetErrorString(e));
     return ok();

@@ -57,7 +57,6 @@ struct Kv4FwdParams {
     float* part_o;             // workspace: partial rows
     float* scores;             // workspace: [total * H][width * 64] log2-unit scores (key weights only)
     int* status;
-    uint64_t wait_budget_ns;
 };
 
 // Row blocks: a CTA holds 8 * kv4_row_tiles(...) (query, head-of-the-group) rows

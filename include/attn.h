@@ -360,7 +360,7 @@ int attn_kv4_read(void* k, void* v, const attn_kv4_cache* cache, const int* page
  * for. Masks as in attn_fwd_sinks, aligned at the end of the cache; a row that
  * sees no key gets O = 0, LSE = -inf. Meant for one to a few dozen rows of a
  * group per sequence (decode, speculative tokens, short chunks): the cache is
- * read once per 8, 16 or 32 (query, head of the group) rows. For long chunks
+ * read once per 8 or 16 (query, head of the group) rows. For long chunks
  * use attn_kv4_read and attn_fwd_ex. P times a value's scale is rounded to fp16
  * relative to the largest scale that the same 64 channels of any visible key
  * have: scales more than 2^19 below it lose bits.

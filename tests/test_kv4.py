@@ -648,7 +648,7 @@ def test_refuses_arguments(lib):
     ap = lambda k=X, ks=128, vs=128, table=X, width=3, lens=X, B=1, L=1: lib.attn_kv4_append(  # noqa: E731
         k, X, ks, vs, c, table, width, lens, None, B, L, None)
     for kw in (dict(k=None), dict(ks=120), dict(vs=132), dict(table=None), dict(width=0), dict(lens=None), dict(B=-1),
-               dict(B=1025), dict(L=-1), dict(B=1000, L=2 ** 31 - 1), dict(width=2 ** 31 - 1)):
+               dict(B=1025), dict(L=-1), dict(B=1000, L=2 ** 31 - 1), dict(width=2 ** 31 - 1), dict(width=2 ** 24), dict(L=2 ** 30)):
         assert ap(**kw) == binding.ATTN_ERR_ARG, kw
     assert ap(k=X + 2) == binding.ATTN_ERR_ALIGN
     assert ap(B=0) == 0 and ap(L=0) == 0
