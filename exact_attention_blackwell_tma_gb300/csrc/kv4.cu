@@ -227,10 +227,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kSelThreads = 1024, kSelBins = 2048;
 constexpr int kSelKeys = 49152;   // keys of a row that stay in shared memory; those behind are read again
 
-// One CTA per (sequence, head): the slots it keeps, ascending. The weights are
-// read once into shared memory; the need-th largest key of the middle is found
-// digit by digit (11, 11 and 10 bits, a histogram each); then one ordered pass
-// writes the kept slots. Of the keys equal to the threshold the first `need`
+// One CTA per (sequence, head): the slots it keeps, ascending. The need-th
+// largest key of the middle is found digit by digit (11, 11 and 10 bits, a
+// histogram each; the first leaves the keys in shared memory for the others);
+// then one ordered pass, its weights loaded a step ahead (128 rows of up to
+// 32768 weights: 31 -> 28 us), writes the kept slots. Of the keys equal to the threshold the first `need`
 // stay, so a slot's place is (slots kept above the threshold before it) +
 // min(threshold slots before it, need): one scan of two counts.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams p, int cap) {
@@ -290,7 +291,14 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams 
             if (lane == 31) warp_sum[warp].x = before;
             before -= c0 + c1;
             __syncthreads();
-            for (int i = 0; i < warp; ++i) before += warp_sum[i].x;
+            int sum = warp_sum[lane].x;   // (32 warps) the sums of the warps before this one, by every warp
+            const int own = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(kFullMask, sum, o);
+                if (lane >= o) sum += x;
+            }
+            before += __shfl_sync(kFullMask, sum - own, warp);
             if (before < need && need <= before + c0) {
                 s_prefix = prefix | (uint32_t)top << kShift[d];
                 s_need = need - before;
@@ -304,8 +312,16 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams 
         }
     }
     int above0 = 0, ties0 = 0;   // slots kept above the threshold, and threshold slots, so far
+    float next[4];               // the weights of the next step
+    auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = j + i < n ? __ldg(w + j + i) : 0.f;
+    };
+    fetch(4 * tid);
     for (int j0 = 0; j0 < n; j0 += 4 * kSelThreads) {
         const int j = j0 + 4 * tid;
+        const float at_j[4] = {next[0], next[1], next[2], next[3]};
+        fetch(j + 4 * kSelThreads);
         uint32_t ab = 0, ti = 0;   // bits: slot j + i stays anyway, is at the threshold
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams 
             if (j + i < lo || j + i >= hi) {
                 ab |= 1u << i;
             } else if (some) {
-                const uint32_t key = j + i < cap ? keys[j + i] : weight_key(__ldg(w + j + i));
+                const uint32_t key = weight_key(at_j[i]);
                 ab |= (key > prefix ? 1u : 0u) << i;
                 ti |= (key == prefix ? 1u : 0u) << i;
             }
@@ -352,7 +368,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(Kv4EvictParams 
                 const int at = above + min(ties, need);
                 if (at < m) {
                     kept[at] = j + i;
-                    nw[at] = __ldg(w + j + i);
+                    nw[at] = at_j[i];
                 }
             }
             above += a;
