@@ -83,7 +83,7 @@ def kinds_of(w):
 # is checked at run time and the field is reported as null after any change.
 NCU_TRAFFIC = {
     ("b1h32l32768d128", "bwd", False): {
-        "bytes": 8721.897e6 + 4562.903e6,
+        "bytes": 8.73e9 + 4.57e9,
         "profile": "profiles/bwd_kernel_b1h32l32768d128_traffic.md",
         "sources": {
             "exact_attention_blackwell_tma_gb300/csrc/bwd.cu":
@@ -103,7 +103,7 @@ NCU_TRAFFIC = {
         },
     },
     ("b1h32l32768d128", "bwd", True): {
-        "bytes": 6230.453e6 + 3538.929e6,
+        "bytes": 6.24e9 + 3.53e9,
         "profile": "profiles/bwd_kernel_b1h32l32768d128_traffic.md",
         "sources": {
             "exact_attention_blackwell_tma_gb300/csrc/bwd.cu":
