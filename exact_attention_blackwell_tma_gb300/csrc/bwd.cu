@@ -276,23 +276,31 @@ __device__ __forceinline__ BwdTile bwd_tile(int t, const BwdParams& p, const Var
 // dS = P (dP - D) cancels, and the rounding of O to bf16 in <dO, O> shows: the
 // relative L2 error of dQ was 4.1e-3 with two keys per row and 5.8e-3 over
 // sequences of three, against 2.4e-3 in general.
-constexpr int kFewKeys = 8;
+constexpr int kFewKeys = 8, kFewChunk = 32;
 
-// sum over the eight lanes of a row of a . b, both `pieces` x 64 bf16, lane l8 16-byte pieces l8, l8 + 8, ..
-__device__ __forceinline__ float dot8(const uint4* a, const uint4* b, int pieces, int l8) {
-    float acc = 0.f;
-    for (int j = 0; j < pieces; ++j) {
-        const uint4 x = a[j * 8 + l8], y = b[j * 8 + l8];
-        const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162*>(&x), *y2 = reinterpret_cast<const __nv_bfloat162*>(&y);
+// A row's 16-byte pieces l8, l8 + 8, .. of `pieces` x 64 bf16 per lane, and one lane's part of a dot product.
+struct RowPieces {
+    uint4 x[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, int pieces, int l8, bool valid) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 fx = __bfloat1622float2(x2[e]), fy = __bfloat1622float2(y2[e]);
-            acc = fmaf(fx.x, fy.x, acc);
-            acc = fmaf(fx.y, fy.y, acc);
-        }
+        for (int j = 0; j < 4; ++j) x[j] = valid && j < pieces ? __ldg(reinterpret_cast<const uint4*>(row) + j * 8 + l8) : make_uint4(0, 0, 0, 0);
     }
-    return acc;
-}
+    __device__ __forceinline__ float dot(const RowPieces& y, int pieces) const {
+        float acc = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j >= pieces) break;
+            const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162*>(&x[j]), *y2 = reinterpret_cast<const __nv_bfloat162*>(&y.x[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 fx = __bfloat1622float2(x2[e]), fy = __bfloat1622float2(y2[e]);
+                acc = fmaf(fx.x, fy.x, acc);
+                acc = fmaf(fx.y, fy.y, acc);
+            }
+        }
+        return acc;
+    }
+};
 
 // Where such rows weigh: a short window with its sinks gives few keys to every
 // row, and of a short sequence's rows a good part see few. Beyond, the first rows
@@ -307,9 +315,12 @@ inline bool few_key_rows(const BwdParams& p) {
 }
 
 // D of a row that sees few keys, else `otherwise`; the four rows of a warp call
-// together. row: packed row, h: query head, (b, r): dense sequence and row in it.
-__device__ __noinline__ float few_keys_D(const BwdParams& p, float otherwise, bool valid, long row, int h, long b, int r,
-                                         int l8) {
+// together. row: packed row, h: query head, (b, r): dense sequence and row in it,
+// dout: the row's dO. q and dO stay in registers over the keys, and a block takes
+// 32 rows of a head, whose keys are mostly the same, so L1 serves them (B3 H32
+// L2329 d192, 7 keys per row: 755 -> 201 us for the preprocess kernel).
+__device__ __forceinline__ float few_keys_D(const BwdParams& p, float otherwise, bool valid, long row, int h, long b, int r,
+                                            const RowPieces& dout, int l8) {
     const Geometry& g = p.g;
     int lq = g.Lq, lk = g.Lk;
     long k0 = b * g.Lk, li = (b * g.H + h) * g.Lq + r;
@@ -332,27 +343,23 @@ __device__ __noinline__ float few_keys_D(const BwdParams& p, float otherwise, bo
     const bool few = valid && r >= 0 && r < lq && n > 0 && n <= kFewKeys;
     if (!__any_sync(0xffffffffu, few)) return otherwise;
     const float lse2 = few ? p.lse[li] * kLog2e : 0.f;
-    const long i = row * g.H + h;
-    float s[kFewKeys], dp[kFewKeys];   // (the keys' loads go out together, the shuffles follow)
-#pragma unroll
-    for (int x = 0; x < kFewKeys; ++x) {
-        s[x] = dp[x] = 0.f;
-        if (!few || x >= n) continue;
-        const long key = (k0 + (x < n_sink ? x : lo + x - n_sink)) * g.Hkv + h / g.group;
-        s[x] = dot8(reinterpret_cast<const uint4*>(p.q + i * g.d), reinterpret_cast<const uint4*>(p.k + key * g.d),
-                    g.d / 64, l8);
-        dp[x] = dot8(reinterpret_cast<const uint4*>(p.dout + i * p.d_v), reinterpret_cast<const uint4*>(p.v + key * p.d_v),
-                     p.d_v / 64, l8);
-    }
+    RowPieces q;
+    q.load(p.q + (row * g.H + h) * g.d, g.d / 64, l8, few);
+    const int most = __reduce_max_sync(0xffffffffu, few ? n : 0);
     float D = 0.f;
-#pragma unroll
-    for (int x = 0; x < kFewKeys; ++x) {
+    for (int x = 0; x < most; ++x) {
+        const bool in = few && x < n;
+        const long key = (k0 + (x < n_sink ? x : lo + x - n_sink)) * g.Hkv + h / g.group;
+        RowPieces k, v;
+        k.load(p.k + key * g.d, g.d / 64, l8, in);
+        v.load(p.v + key * p.d_v, p.d_v / 64, l8, in);
+        float s = q.dot(k, g.d / 64), dp = dout.dot(v, p.d_v / 64);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
-            s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
-            dp[x] += __shfl_xor_sync(0xffffffffu, dp[x], o);
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            dp += __shfl_xor_sync(0xffffffffu, dp, o);
         }
-        if (few && x < n) D = fmaf(exp2f(fmaf(s[x], g.scale_log2, -lse2)), dp[x], D);
+        if (in) D = fmaf(exp2f(fmaf(s, g.scale_log2, -lse2)), dp, D);
     }
     return few ? D : otherwise;
 }
@@ -365,55 +372,35 @@ __global__ void bwd_prep(BwdParams p, VarlenMap* vm_out, long rows_q, long n_acc
     const int dv = p.d_v;   // O and dO have the head dim of v: 64 .. 256, 4 pieces of 8 lanes at most
     const int pieces = dv / 64;
     const int lane = threadIdx.x & 31, l8 = lane & 7;
-    const long n_rows = rows_q * g.H;
+    // (row, head) pairs in order; with few keys 32 rows of a head, then the next
+    // head: neighbours share their keys in L1
+    constexpr int kChunk = kFewChunk;
+    const long n_rows = (kFew ? (rows_q + kChunk - 1) / kChunk * kChunk : rows_q) * g.H;
     const long warps = stride / 32;
     for (long r0 = tid / 32 * 4; r0 < n_rows; r0 += warps * 4) {
-        const long i = r0 + (lane >> 3);   // (row, head) of this lane's group
-        const bool valid = i < n_rows;
-        const uint4* o4 = reinterpret_cast<const uint4*>(p.o + (valid ? i : 0) * dv);
-        const uint4* d4 = reinterpret_cast<const uint4*>(p.dout + (valid ? i : 0) * dv);
-        uint4 a[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (valid && j < pieces) {
-                a[j] = o4[j * 8 + l8];
-                b[j] = d4[j * 8 + l8];
-            }
-        float acc = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!valid || j >= pieces) continue;
-            const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a[j]);
-            const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 fa = __bfloat1622float2(a2[e]), fb = __bfloat1622float2(b2[e]);
-                acc = fmaf(fa.x, fb.x, acc);
-                acc = fmaf(fa.y, fb.y, acc);
-            }
+        const long x = r0 + (lane >> 3);   // this lane's group's
+        long row, h;
+        if constexpr (kFew) {
+            const long y = x / kChunk, chunk = y / g.H;
+            h = y - chunk * g.H;
+            row = chunk * kChunk + (x - y * kChunk);
+        } else {
+            row = x / g.H;
+            h = x - row * g.H;
         }
+        const bool valid = x < n_rows && row < rows_q;
+        const long i = valid ? row * g.H + h : 0;
+        RowPieces a, b;
+        a.load(p.o + i * dv, pieces, l8, valid);
+        b.load(p.dout + i * dv, pieces, l8, valid);
+        float acc = a.dot(b, pieces);
         acc += __shfl_xor_sync(0xffffffffu, acc, 4);
         acc += __shfl_xor_sync(0xffffffffu, acc, 2);
         acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-        if constexpr (kFew) {
-            const long row = (valid ? i : 0) / g.H;
-            const int h = (int)((valid ? i : 0) - row * g.H);
-            const long b = g.cu_seqlens || g.Lq == 0 ? 0 : row / g.Lq;
-            const int r = (int)(row - b * g.Lq);
-            acc = few_keys_D(p, acc, valid, row, h, b, r, l8);
-            if (valid && l8 == 0) p.delta[g.cu_seqlens ? (long)h * g.Lq + row : (b * g.H + h) * g.Lq + r] = acc;
-        } else if (valid && l8 == 0) {
-            const long row = i / g.H;
-            const int h = (int)(i - row * g.H);
-            long di;
-            if (g.cu_seqlens) {
-                di = (long)h * g.Lq + row;
-            } else {
-                const long b = row / g.Lq, r = row - b * g.Lq;
-                di = (b * g.H + h) * g.Lq + r;
-            }
-            p.delta[di] = acc;
-        }
+        if (!valid) row = h = 0;
+        const long bi = g.cu_seqlens || g.Lq == 0 ? 0 : row / g.Lq, r = row - bi * g.Lq;
+        if constexpr (kFew) acc = few_keys_D(p, acc, valid, row, (int)h, bi, (int)r, b, l8);
+        if (valid && l8 == 0) p.delta[g.cu_seqlens ? h * g.Lq + row : (bi * g.H + h) * g.Lq + r] = acc;
     }
     float4* acc4 = reinterpret_cast<float4*>(p.dq_acc);
     for (long i = tid; i < n_acc4; i += stride) acc4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1212,11 +1199,12 @@ cudaError_t launch_bwd_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CU
     VarlenMap* vm = reinterpret_cast<VarlenMap*>(
         reinterpret_cast<char*>(p.semaphores) + (((size_t)n_sem * sizeof(int) + 255) & ~(size_t)255));
     {
-        const long work = rows_q * g.H * 8;   // eight lanes per (row, head)
+        const bool few = few_key_rows(p);
+        const long work = (few ? (rows_q + kFewChunk - 1) / kFewChunk * kFewChunk : rows_q) * g.H * 8;   // eight lanes per (row, head)
         int blocks = (int)((work + 255) / 256);
         if (blocks > 8 * num_sms) blocks = 8 * num_sms;
         if (blocks < 1) blocks = 1;
-        auto prep = few_key_rows(p) ? bwd_prep<true> : bwd_prep<false>;
+        auto prep = few ? bwd_prep<true> : bwd_prep<false>;
         prep<<<blocks, 256, 0, stream>>>(p, vm, rows_q, n_acc4, n_sem, pair ? 2 * kBN : kBN);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
