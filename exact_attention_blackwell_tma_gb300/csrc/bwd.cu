@@ -305,8 +305,8 @@ struct RowPieces {
 // Where such rows weigh: a short window with its sinks gives few keys to every
 // row, and of a short sequence's rows a good part see few. Beyond, the first rows
 // under a causal mask still would, but looking for them costs the preprocess kernel
-// half its time again (B2 H16 L8192 d128 38 -> 56 us; one head pair of 300 rows: the
-// step 36 -> 43 us) for a few percent of the error (2.7e-3 -> 2.6e-3 there), the rest
+// half its time again (B2 H16 L8192 d128 38 -> 61 us; one head pair of 300 rows: the
+// step 35 -> 39 us) for a few percent of the error (2.7e-3 -> 2.6e-3 there), the rest
 // of which is the rounding of dS itself.
 inline bool few_key_rows(const BwdParams& p) {
     const Geometry& g = p.g;

@@ -780,18 +780,17 @@ __device__ __forceinline__ Shares shares_of(const Kv4FwdParams& p, const SeqWork
     const int u = p.prefix[b] + (h * w.blocks + r / rows_per_block) * cut.span(w.units);
     return Shares{u / per, (u + w.units - 1) / per, r % rows_per_block, rows_per_block};
 }
-// (max, sum) of all shares of a row: every lane of the warp calls and gets both.
-__device__ __forceinline__ float2 join_ml(const Kv4FwdParams& p, const Shares& s, int lane) {
+// (max, sum) of all shares of a row, taken by `lanes` (a power of two) neighbouring
+// lanes, of which this is `lane`: every lane of the warp calls and gets its row's.
+__device__ __forceinline__ float2 join_ml(const Kv4FwdParams& p, const Shares& s, int lane, int lanes) {
     float m = -INFINITY, l = 0.f;
-    for (int c = s.c0 + lane; c <= s.c1; c += 32) m = fmaxf(m, p.part_ml[2 * s.at(c)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-    for (int c = s.c0 + lane; c <= s.c1; c += 32) {
+    for (int c = s.c0 + lane; c <= s.c1; c += lanes) m = fmaxf(m, p.part_ml[2 * s.at(c)]);
+    for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+    for (int c = s.c0 + lane; c <= s.c1; c += lanes) {
         const float2 v = *reinterpret_cast<const float2*>(p.part_ml + 2 * s.at(c));
         l += v.y * (v.x == -INFINITY ? 0.f : ex2_mufu(v.x - m));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFullMask, l, o);
+    for (int o = lanes / 2; o > 0; o >>= 1) l += __shfl_xor_sync(kFullMask, l, o);
     return make_float2(m, l);
 }
 __device__ __forceinline__ long lse_at(const Kv4FwdParams& p, const SeqWork& w, int b, int i, int head) {
@@ -799,16 +798,21 @@ __device__ __forceinline__ long lse_at(const Kv4FwdParams& p, const SeqWork& w, 
 }
 
 constexpr int kFinishThreads = 128;
-constexpr int kFinishTiles = 4, kFinishKeys = kFinishTiles * 4 * kFinishThreads;   // keys of a weights block
+constexpr int kFinishKeys = 4 * kFinishThreads;   // keys of a tile
 constexpr int kFinishRows = 64;                   // rows whose LSE it holds at a time
 
 // Blocks [0, row_blocks): one warp per (token, head) whose row block several CTAs
 // shared joins their partial rows in CTA order (the same sum on every run); rows
 // that no key reaches get O = 0, LSE = -inf. The other blocks update key weights:
 //   key_weights[b][h][j] = decay * key_weights + sum over rows of exp(s - LSE),
-// four times four keys per thread, rows in order. Scores of pages that no row block visited
+// four keys per thread and tile, rows in order: four tiles of one row at a time, or,
+// when that makes too few blocks for the SMs, one tile of four rows; a block's rows
+// get their LSE all at once, several lanes each (4 caches of up to 2253 keys, 8 heads
+// of up to 88 rows, the wait for the attention kernel's 18 us included: 24 us, 66 with
+// four tiles and a warp per row). Scores of pages that no row block visited
 // were not written and count as nothing. Launched while the attention kernel
 // runs (programmatic dependent launch); what it left is read after the wait.
+template <int kTiles>
 __global__ void __launch_bounds__(kFinishThreads, 7) kv4_finish_kernel(const Kv4FwdParams p, int rows_per_block,
                                                                     int row_blocks, int key_blocks) {
     __shared__ float lse2[kFinishRows];
@@ -831,7 +835,7 @@ __global__ void __launch_bounds__(kFinishThreads, 7) kv4_finish_kernel(const Kv4
         }
         const Shares s = shares_of(p, w, b, head / p.group, i * p.group + head % p.group, rows_per_block);
         if (s.c0 == s.c1) return;
-        const float2 ml = join_ml(p, s, lane);
+        const float2 ml = join_ml(p, s, lane, 32);
         float4 o[2] = {};
         for (int c = s.c0; c <= s.c1; c += 4) {   // four shares' loads in flight
             float f[4];
@@ -871,58 +875,66 @@ __global__ void __launch_bounds__(kFinishThreads, 7) kv4_finish_kernel(const Kv4
     const int id = blockIdx.x - row_blocks;
     const int bh = id / key_blocks, b = bh / p.c.Hkv, h = bh % p.c.Hkv;
     const SeqWork w = seq_work(p, b, rows_per_block);
-    const int j0 = (id % key_blocks) * kFinishKeys + 4 * threadIdx.x;
+    const int j0 = (id % key_blocks) * kTiles * kFinishKeys + 4 * threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (j0 == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
     const int keys = (int)min((long)w.s.lk, p.weight_stride);
-    if (w.s.bad || (id % key_blocks) * kFinishKeys >= keys) return;
-    bool seen[kFinishTiles];
-    float sum[kFinishTiles][4] = {};
+    if (w.s.bad || (id % key_blocks) * kTiles * kFinishKeys >= keys) return;
+    bool seen[kTiles];
+    float sum[kTiles][4] = {};
 #pragma unroll
-    for (int x = 0; x < kFinishTiles; ++x) {
-        const int j = j0 + x * 4 * kFinishThreads, page = j / kPage;
+    for (int x = 0; x < kTiles; ++x) {
+        const int j = j0 + x * kFinishKeys, page = j / kPage;
         seen[x] = j < keys && (page < w.n_sink || (page >= w.first && page < w.first + w.pages - w.n_sink));
     }
     const long row_len = (long)p.s.width * kPage;
     const float* src = p.scores + ((long)h * p.s.total * p.group + (long)w.s.q0 * p.group) * row_len + j0;
     for (int r0 = 0; r0 < w.rows && w.pages > 0; r0 += kFinishRows) {
         const int nr = min(kFinishRows, w.rows - r0);
+        int lanes = 32;   // of a row
+        while (lanes > 1 && kFinishThreads / lanes < nr) lanes >>= 1;
         __syncthreads();
-        for (int r = warp; r < nr; r += kFinishThreads / 32) {
+        {
+            const int r = min((int)threadIdx.x / lanes, nr - 1);   // (at most 64 rows: two lanes or more)
             const Shares s = shares_of(p, w, b, h, r0 + r, rows_per_block);
-            float v;
-            if (s.c0 == s.c1) {
-                v = p.lse[lse_at(p, w, b, (r0 + r) / p.group, h * p.group + (r0 + r) % p.group)] * kLog2e;
-            } else {
-                const float2 ml = join_ml(p, s, lane);
-                v = ml.y == 0.f ? -INFINITY : ml.x + log2f(ml.y);
-            }
-            if (lane == 0) lse2[r] = v;
+            const float2 ml = join_ml(p, Shares{s.c0, s.c0 == s.c1 ? s.c0 - 1 : s.c1, s.in_block, s.rows_per_block},
+                                      lane & (lanes - 1), lanes);
+            const float v = s.c0 == s.c1 ? p.lse[lse_at(p, w, b, (r0 + r) / p.group, h * p.group + (r0 + r) % p.group)] * kLog2e
+                                         : (ml.y == 0.f ? -INFINITY : ml.x + log2f(ml.y));
+            if ((lane & (lanes - 1)) == 0) lse2[r] = v;
         }
         __syncthreads();
-        for (int r = 0; r < nr; ++r) {
-            const float* row = src + (r0 + r) * row_len;
-            const float e = lse2[r];
-            float4 s[kFinishTiles];
+        constexpr int kAhead = 4 / kTiles;
+        for (int r = 0; r < nr; r += kAhead) {
+            float4 s[kAhead][kTiles];
 #pragma unroll
-            for (int x = 0; x < kFinishTiles; ++x)
-                if (seen[x]) s[x] = __ldcs(reinterpret_cast<const float4*>(row + x * 4 * kFinishThreads));
+            for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-            for (int x = 0; x < kFinishTiles; ++x) {
-                if (!seen[x]) continue;
-                sum[x][0] += s[x].x == -INFINITY ? 0.f : ex2_mufu(s[x].x - e);
-                sum[x][1] += s[x].y == -INFINITY ? 0.f : ex2_mufu(s[x].y - e);
-                sum[x][2] += s[x].z == -INFINITY ? 0.f : ex2_mufu(s[x].z - e);
-                sum[x][3] += s[x].w == -INFINITY ? 0.f : ex2_mufu(s[x].w - e);
+                for (int x = 0; x < kTiles; ++x)
+                    if (seen[x] && (kAhead == 1 || r + k < nr))
+                        s[k][x] = __ldcs(reinterpret_cast<const float4*>(src + (r0 + r + k) * row_len + x * kFinishKeys));
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (kAhead > 1 && r + k >= nr) break;
+                const float e = lse2[r + k];
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x) {
+                    if (!seen[x]) continue;
+                    const float4 y = s[k][x];
+                    sum[x][0] += y.x == -INFINITY ? 0.f : ex2_mufu(y.x - e);
+                    sum[x][1] += y.y == -INFINITY ? 0.f : ex2_mufu(y.y - e);
+                    sum[x][2] += y.z == -INFINITY ? 0.f : ex2_mufu(y.z - e);
+                    sum[x][3] += y.w == -INFINITY ? 0.f : ex2_mufu(y.w - e);
+                }
             }
         }
     }
     float* dst = p.key_weights + ((long)b * p.c.Hkv + h) * p.weight_stride + j0;
 #pragma unroll
-    for (int x = 0; x < kFinishTiles; ++x)
+    for (int x = 0; x < kTiles; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const int k = x * 4 * kFinishThreads + y;
+            const int k = x * kFinishKeys + y;
             if (j0 + k < keys) dst[k] = p.weight_decay == 0.f ? sum[x][y] : fmaf(p.weight_decay, dst[k], sum[x][y]);
         }
 }
@@ -942,7 +954,9 @@ cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) 
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int row_blocks = (int)(((long)p.s.total * p.H + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
-    const int key_blocks = p.key_weights ? (p.s.width * kPage + kFinishKeys - 1) / kFinishKeys : 0;
+    const long key_tiles = p.key_weights ? ((long)p.s.width * kPage + kFinishKeys - 1) / kFinishKeys : 0;
+    const int tiles = (key_tiles + 3) / 4 * p.c.Hkv * p.s.B >= 7 * num_sms ? 4 : 1;
+    const int key_blocks = (int)((key_tiles + tiles - 1) / tiles);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(row_blocks + (long)key_blocks * p.c.Hkv * p.s.B));
     cfg.blockDim = dim3(kFinishThreads);
@@ -952,7 +966,7 @@ cudaError_t launch_one(const Kv4FwdParams& p, int num_sms, cudaStream_t stream) 
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_finish_kernel, p, Lay::kRows, row_blocks, key_blocks);
+    return cudaLaunchKernelEx(&cfg, tiles == 4 ? kv4_finish_kernel<4> : kv4_finish_kernel<1>, p, Lay::kRows, row_blocks, key_blocks);
 }
 
 template <int D, int DV>
