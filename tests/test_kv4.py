@@ -278,6 +278,15 @@ def test_forward_many_rows(d, n, H, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [((-1, -1), 0), ((300, -1), 4)])
+def test_key_weights_of_many_caches(window, sinks):
+    """Enough (sequence, head) pairs that a block takes four tiles of keys: their borders, and none at all."""
+    lens = [2100, 513, 0, 512, 1537, 2048, 2049] + [3 + i % 90 for i in range(133)]
+    new = [3, 1, 0, 2, 5, 1, 1] + [1] * 133
+    check_forward(Pool(lens, 8, 64, seed=23), new, 16, decay=0.5, window=window, sinks=sinks)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("L", [1, 4])
 def test_forward_dense_batch(L):
     check_forward(Pool([100, 250, 64, 4], 2, 128, seed=11), [L] * 4, 8, packed=False, decay=0.0)
