@@ -37,9 +37,10 @@ __device__ __forceinline__ float scale_of(float lo, float hi) {
 }
 
 // round((x - lo) / s) to 0 .. 15, ties to even, decided exactly: next to a
-// border (k + 1/2) s the sign of (x - lo) - (k + 1/2) s is taken as above.
-__device__ __forceinline__ uint32_t code_of(float x, float lo, float s, float inv) {
-    const float d = x - lo, q = d * inv;
+// border (k + 1/2) s the sign of (x - lo) - (k + 1/2) s is taken as above. It
+// divides: the reciprocal of a scale of 2^-128 or less is infinite.
+__device__ __forceinline__ uint32_t code_of(float x, float lo, float s) {
+    const float d = x - lo, q = __fdiv_rn(d, s);
     const float k = floorf(q), frac = q - k;
     float c = rintf(q);
     if (fabsf(frac - 0.5f) < 6.1e-5f) {
@@ -79,9 +80,8 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float lo, floa
     const bool sure = far < 0.5f - 6.1e-5f || tiny >= (hi - lo) * 1.2207e-4f;
     if (sure && s >= 1e-30f && s <= 1e30f) return (uint32_t)half[0] | (uint32_t)half[1] << 16;
     uint32_t codes = 0;
-    inv = __fdiv_rn(1.f, s);
 #pragma unroll 1
-    for (int j = 0; j < 8; ++j) codes |= code_of(x[j], lo, s, inv) << (4 * j);
+    for (int j = 0; j < 8; ++j) codes |= code_of(x[j], lo, s) << (4 * j);
     return codes;
 }
 
