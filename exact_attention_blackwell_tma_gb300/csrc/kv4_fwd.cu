@@ -50,7 +50,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kKv4Threads = 32 * kWarps;
 constexpr float kKv4Tau = 8.f;                   // a row's max moves when it grows by more (log2 units)
-constexpr float kWTarget = 32.f;                 // the largest a' of a group is scaled to [16, 32)
+constexpr int kWTargetLog = 5;                   // the largest a' of a group is scaled to [16, 32) = [2^4, 2^5)
 constexpr float kWMost = 128.f;                  // ... and rescaled past this: p a' <= 2^8 * 2^7 in fp16
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -605,7 +605,9 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
                     if (!(top * wsc[g] <= kWMost) && top > 0.f) {
-                        const float now = kWTarget * pow2(127 - (int)(__float_as_uint(top) >> 23) - 1);
+                        // (at most 2^127, as infinity means none yet: of scales below 2^-123 p a' is then off by up
+                        // to 2^-152, an eighth of the smallest fp32)
+                        const float now = pow2(kWTargetLog + 126 - (int)(__float_as_uint(top) >> 23));
                         const float r = wsc[g] == INFINITY ? 1.f : now / wsc[g];
                         wsc[g] = now;
 #pragma unroll

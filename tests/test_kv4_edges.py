@@ -1,10 +1,13 @@
 """The 4-bit cache at the ends of its types' ranges (bounds: test_kv4.py)."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from exact_attention_blackwell_tma_gb300 import binding
-from test_kv4 import Pool, check_appended, offsets
+from _plain import assert_within
+from test_kv4 import Pool, bf16, check_appended, offsets
 
 
 @pytest.mark.gpu
@@ -22,3 +25,32 @@ def test_append_codes_at_the_ends_of_the_range(step):
                        cu_seqlens=offsets([len(rows)]).cuda())
     binding.check_status()
     check_appended(pool, [len(rows)], x, x.flip(0), before)
+
+
+def check_values_of_size(size, d, n, lens, H):
+    """O for values around `size`; the floor is what fp32 and bf16 resolve at the bottom of their range."""
+    pool = Pool(lens, 1, d, seed=33)
+    pool.host[3] = (pool.host[3].double() * size).to(torch.bfloat16)
+    pool.upload()
+    q = bf16(pool.g, sum(n), H, d)
+    o, _ = binding.kv4_forward(q.cuda(), pool.cache, pool.table, pool.lens_t, scale=0.1, cu_seqlens=offsets(n).cuda())
+    binding.check_status()
+    o, at = o.double().cpu() / size, 0
+    for b, rows in enumerate(n):
+        k, (v, ac, spread) = pool.values(b, 0)[0], (x / size for x in pool.values(b, 1))
+        s = torch.einsum("ihd,jhd->hij", q[at:at + rows].double(), k.expand(-1, H, -1)) * 0.1
+        i, j = torch.arange(rows)[:, None], torch.arange(lens[b])[None]
+        p = torch.softmax(s.masked_fill(j > i + lens[b] - rows, -math.inf), -1)
+        ref, c, x = (torch.einsum("hij,jhd->ihd", p, y.expand(-1, H, -1)) for y in (v, ac, spread))
+        # 2^-134: half a step of the smallest bf16; sums of 2^-149-sized fp32 roundings stay far below another
+        assert_within(o[at:at + rows], ref, 2.0 ** -11 * c + 2.0 ** -13 * x + 2.0 ** -8 * ref.abs() + 2.0 ** -133 / size,
+                      f"size {size} sequence {b}", floor=0.0)
+        at += rows
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -120, 2.0 ** -122, 2.0 ** -124, 2.0 ** -126, 2.0 ** -128])
+@pytest.mark.parametrize("d", [64, 256])
+def test_forward_tiny_values(size, d):
+    """Value scales down to the subnormals keep the codes' share of O."""
+    check_values_of_size(size, d, [1, 3], [700, 33], 2)
