@@ -720,10 +720,10 @@ __global__ void __launch_bounds__(kKv4Threads, Kv4Layout<D, DV, NR>::kCtas) kv4_
                     float4* at = reinterpret_cast<float4*>(mine + row * DV + g * kKv4Group + 8 * g8);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        at[j] = make_float4(fmaf(acc[4 * g + 2 * j][n][c], inv * 16777216.f, z),
-                                            fmaf(acc[4 * g + 2 * j][n][2 + c], inv * 1048576.f, z),
-                                            fmaf(acc[4 * g + 2 * j + 1][n][c], inv * 16777216.f, z),
-                                            fmaf(acc[4 * g + 2 * j + 1][n][2 + c], inv * 1048576.f, z));
+                        at[j] = make_float4(fmaf(acc[4 * g + 2 * j][n][c] * 16777216.f, inv, z),   // (inv may be up to 2^123)
+                                            fmaf(acc[4 * g + 2 * j][n][2 + c] * 1048576.f, inv, z),
+                                            fmaf(acc[4 * g + 2 * j + 1][n][c] * 16777216.f, inv, z),
+                                            fmaf(acc[4 * g + 2 * j + 1][n][2 + c] * 1048576.f, inv, z));
                 }
             }
         __syncthreads();

@@ -54,3 +54,11 @@ def check_values_of_size(size, d, n, lens, H):
 def test_forward_tiny_values(size, d):
     """Value scales down to the subnormals keep the codes' share of O."""
     check_values_of_size(size, d, [1, 3], [700, 33], 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [2.0 ** 90, 2.0 ** 106, 2.0 ** 112])
+@pytest.mark.parametrize("d", [64, 256])
+def test_forward_huge_values(size, d):
+    """Value scales past 2^107, where 2^24 times the scale leaves the fp32 range."""
+    check_values_of_size(size, d, [1, 3], [700, 33], 2)
