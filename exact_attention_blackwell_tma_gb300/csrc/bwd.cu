@@ -274,10 +274,21 @@ __device__ __forceinline__ BwdTile bwd_tile(int t, const BwdParams& p, const Var
 // kFew (windows with sinks, which may leave a row very few keys): rows that see
 // at most kFewKeys keys get D_i = sum_j P_ij dP_ij from q, k and v instead. There
 // dS = P (dP - D) cancels, and the rounding of O to bf16 in <dO, O> shows: the
-// relative L2 error of dQ was 4.1e-3 with two keys per row and 5.8e-3 over
-// sequences of three, against 2.4e-3 in general.
+// relative L2 error of dQ over sequences of two and three tokens is 3.8e-3 and
+// 3.6e-3 that way, 2.4e-3 this way, as in general.
 constexpr int kFewKeys = 8, kFewChunk = 32;
 
+// acc + the dot product of two pieces of 8 bf16
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float acc) {
+    const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162*>(&x), *y2 = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 fx = __bfloat1622float2(x2[e]), fy = __bfloat1622float2(y2[e]);
+        acc = fmaf(fx.x, fy.x, acc);
+        acc = fmaf(fx.y, fy.y, acc);
+    }
+    return acc;
+}
 // A row's 16-byte pieces l8, l8 + 8, .. of `pieces` x 64 bf16 per lane, and one lane's part of a dot product.
 struct RowPieces {
     uint4 x[4];
@@ -290,35 +301,50 @@ struct RowPieces {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j >= pieces) break;
-            const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162*>(&x[j]), *y2 = reinterpret_cast<const __nv_bfloat162*>(&y.x[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 fx = __bfloat1622float2(x2[e]), fy = __bfloat1622float2(y2[e]);
-                acc = fmaf(fx.x, fy.x, acc);
-                acc = fmaf(fx.y, fy.y, acc);
-            }
+            acc = dot8(x[j], y.x[j], acc);
         }
         return acc;
     }
 };
+// The same of two rows in memory, piece by piece: few registers.
+__device__ __forceinline__ float dot_rows(const __nv_bfloat16* x, const __nv_bfloat16* y, int pieces, int l8, bool valid) {
+    float acc = 0.f;
+#pragma unroll 1
+    for (int j = 0; valid && j < pieces; ++j)
+        acc = dot8(__ldg(reinterpret_cast<const uint4*>(x) + j * 8 + l8), __ldg(reinterpret_cast<const uint4*>(y) + j * 8 + l8), acc);
+    return acc;
+}
 
 // Where such rows weigh: a short window with its sinks gives few keys to every
 // row, and of a short sequence's rows a good part see few. Beyond, the first rows
 // under a causal mask still would, but looking for them costs the preprocess kernel
 // half its time again (B2 H16 L8192 d128 38 -> 61 us; one head pair of 300 rows: the
 // step 35 -> 39 us) for a few percent of the error (2.7e-3 -> 2.6e-3 there), the rest
-// of which is the rounding of dS itself.
-inline bool few_key_rows(const BwdParams& p) {
+// of which is the rounding of dS itself. A sequence's own lengths decide, so its
+// gradients are as precise in a packed batch as alone.
+constexpr int kFewRows = 128;
+__host__ __device__ __forceinline__ bool few_key_sequence(int lq, int lk, int win_left, int sinks) {
+    return lq <= kFewRows || (win_left < lk ? win_left : lk) + 1L + (sinks < lk ? sinks : lk) <= kFewKeys;
+}
+// How the preprocess kernel looks for them: not at all; in every row; or (packed
+// sequences, whose lengths are on the device) in those of short sequences.
+enum FewKeys { kFewNone, kFewAll, kFewShort };
+inline FewKeys few_key_rows(const BwdParams& p) {
     const Geometry& g = p.g;
-    if (p.mask.sinks <= 0 || p.mask.ptr || g.B <= 0) return false;
-    return (long)g.win_left + 1 + p.mask.sinks <= kFewKeys || (g.cu_seqlens ? g.Lq / g.B : g.Lq) <= 128;
+    if (p.mask.sinks <= 0 || p.mask.ptr || g.B <= 0) return kFewNone;
+    if (few_key_sequence(g.cu_seqlens ? kFewRows + 1 : g.Lq, g.Lk, g.win_left, p.mask.sinks)) return kFewAll;
+    return g.cu_seqlens ? kFewShort : kFewNone;
 }
 
 // D of a row that sees few keys, else `otherwise`; the four rows of a warp call
 // together. row: packed row, h: query head, (b, r): dense sequence and row in it,
-// dout: the row's dO. q and dO stay in registers over the keys, and a block takes
-// 32 rows of a head, whose keys are mostly the same, so L1 serves them (B3 H32
-// L2329 d192, 7 keys per row: 755 -> 201 us for the preprocess kernel).
+// dout: the row's dO. kFewAll: q and dO stay in registers over the keys, and a block
+// takes 32 rows of a head, whose keys are mostly the same, so L1 serves them (B3 H32
+// L2329 d192, 7 keys per row: 755 -> 201 us for the preprocess kernel). kFewShort:
+// rows in memory order and few registers, as the rows of long sequences, which
+// only look their sequence up, want the memory bandwidth (64 packed sequences of 2048
+// rows, H32/8, d128: the backward 5.97 ms without looking, 6.08, and 6.39 the other way).
+template <FewKeys kFew>
 __device__ __forceinline__ float few_keys_D(const BwdParams& p, float otherwise, bool valid, long row, int h, long b, int r,
                                             const RowPieces& dout, int l8) {
     const Geometry& g = p.g;
@@ -338,22 +364,31 @@ __device__ __forceinline__ float few_keys_D(const BwdParams& p, float otherwise,
         li = (long)h * g.Lq + row;
     }
     const MaskBand mb = mask_band(lq, lk, g.win_left, g.win_right, p.mask.sinks);
+    valid = valid && few_key_sequence(lq, lk, mb.wl, mb.sinks);
     const int lo = band_key_lo(mb, r), hi = band_key_hi(mb, r);
     const int n_sink = hi > lo ? min(mb.sinks, lo) : 0, n = hi > lo ? hi - lo + n_sink : 0;
     const bool few = valid && r >= 0 && r < lq && n > 0 && n <= kFewKeys;
     if (!__any_sync(0xffffffffu, few)) return otherwise;
     const float lse2 = few ? p.lse[li] * kLog2e : 0.f;
     RowPieces q;
-    q.load(p.q + (row * g.H + h) * g.d, g.d / 64, l8, few);
+    const long at = row * g.H + h;
+    if constexpr (kFew == kFewAll) q.load(p.q + at * g.d, g.d / 64, l8, few);
     const int most = __reduce_max_sync(0xffffffffu, few ? n : 0);
     float D = 0.f;
     for (int x = 0; x < most; ++x) {
         const bool in = few && x < n;
         const long key = (k0 + (x < n_sink ? x : lo + x - n_sink)) * g.Hkv + h / g.group;
-        RowPieces k, v;
-        k.load(p.k + key * g.d, g.d / 64, l8, in);
-        v.load(p.v + key * p.d_v, p.d_v / 64, l8, in);
-        float s = q.dot(k, g.d / 64), dp = dout.dot(v, p.d_v / 64);
+        float s, dp;
+        if constexpr (kFew == kFewAll) {
+            RowPieces k, v;
+            k.load(p.k + key * g.d, g.d / 64, l8, in);
+            v.load(p.v + key * p.d_v, p.d_v / 64, l8, in);
+            s = q.dot(k, g.d / 64);
+            dp = dout.dot(v, p.d_v / 64);
+        } else {
+            s = dot_rows(p.q + at * g.d, p.k + key * g.d, g.d / 64, l8, in);
+            dp = dot_rows(p.dout + at * p.d_v, p.v + key * p.d_v, p.d_v / 64, l8, in);
+        }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
             s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -364,8 +399,9 @@ __device__ __forceinline__ float few_keys_D(const BwdParams& p, float otherwise,
     return few ? D : otherwise;
 }
 
-template <bool kFew>
-__global__ void bwd_prep(BwdParams p, VarlenMap* vm_out, long rows_q, long n_acc4, int n_sem, int keys_per_tile) {
+template <FewKeys kFew>
+__global__ void __launch_bounds__(256, kFew == kFewAll ? 2 : 5)
+bwd_prep(const __grid_constant__ BwdParams p, VarlenMap* vm_out, long rows_q, long n_acc4, int n_sem, int keys_per_tile) {
     const Geometry& g = p.g;
     const long stride = (long)gridDim.x * blockDim.x;
     const long tid = (long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -375,12 +411,12 @@ __global__ void bwd_prep(BwdParams p, VarlenMap* vm_out, long rows_q, long n_acc
     // (row, head) pairs in order; with few keys 32 rows of a head, then the next
     // head: neighbours share their keys in L1
     constexpr int kChunk = kFewChunk;
-    const long n_rows = (kFew ? (rows_q + kChunk - 1) / kChunk * kChunk : rows_q) * g.H;
+    const long n_rows = (kFew == kFewAll ? (rows_q + kChunk - 1) / kChunk * kChunk : rows_q) * g.H;
     const long warps = stride / 32;
     for (long r0 = tid / 32 * 4; r0 < n_rows; r0 += warps * 4) {
         const long x = r0 + (lane >> 3);   // this lane's group's
         long row, h;
-        if constexpr (kFew) {
+        if constexpr (kFew == kFewAll) {
             const long y = x / kChunk, chunk = y / g.H;
             h = y - chunk * g.H;
             row = chunk * kChunk + (x - y * kChunk);
@@ -399,7 +435,7 @@ __global__ void bwd_prep(BwdParams p, VarlenMap* vm_out, long rows_q, long n_acc
         acc += __shfl_xor_sync(0xffffffffu, acc, 1);
         if (!valid) row = h = 0;
         const long bi = g.cu_seqlens || g.Lq == 0 ? 0 : row / g.Lq, r = row - bi * g.Lq;
-        if constexpr (kFew) acc = few_keys_D(p, acc, valid, row, (int)h, bi, (int)r, b, l8);
+        if constexpr (kFew != kFewNone) acc = few_keys_D<kFew>(p, acc, valid, row, (int)h, bi, (int)r, b, l8);
         if (valid && l8 == 0) p.delta[g.cu_seqlens ? h * g.Lq + row : (bi * g.H + h) * g.Lq + r] = acc;
     }
     float4* acc4 = reinterpret_cast<float4*>(p.dq_acc);
@@ -1199,12 +1235,12 @@ cudaError_t launch_bwd_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CU
     VarlenMap* vm = reinterpret_cast<VarlenMap*>(
         reinterpret_cast<char*>(p.semaphores) + (((size_t)n_sem * sizeof(int) + 255) & ~(size_t)255));
     {
-        const bool few = few_key_rows(p);
-        const long work = (few ? (rows_q + kFewChunk - 1) / kFewChunk * kFewChunk : rows_q) * g.H * 8;   // eight lanes per (row, head)
+        const FewKeys few = few_key_rows(p);
+        const long work = (few == kFewAll ? (rows_q + kFewChunk - 1) / kFewChunk * kFewChunk : rows_q) * g.H * 8;   // eight lanes per (row, head)
         int blocks = (int)((work + 255) / 256);
         if (blocks > 8 * num_sms) blocks = 8 * num_sms;
         if (blocks < 1) blocks = 1;
-        auto prep = few ? bwd_prep<true> : bwd_prep<false>;
+        auto prep = few == kFewAll ? bwd_prep<kFewAll> : (few == kFewShort ? bwd_prep<kFewShort> : bwd_prep<kFewNone>);
         prep<<<blocks, 256, 0, stream>>>(p, vm, rows_q, n_acc4, n_sem, pair ? 2 * kBN : kBN);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

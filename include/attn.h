@@ -212,7 +212,12 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
  * 128-key block must be finite, as for the other masks. In the backward a block
  * that holds sinks may be cut into parts of its query rows, whose fp32 partial
  * dK and dV a last kernel sums in order (no atomics; the same bits on every run
- * with deterministic != 0). workspace: attn_bwd_sinks_workspace_size(...) bytes.
+ * with deterministic != 0). As in the other calls P is rounded to bf16 for its
+ * product with V, P and dS for dV, dQ and dK, and <dO_i, O_i> is taken from the
+ * bf16 O; but rows that see at most eight keys, of sequences of at most 128
+ * query rows or under a window that with its sinks holds at most eight keys, get
+ * it as sum_j P_ij <dO_i, v_j>, where the rounding of O would show in dS. The
+ * sequence's own lengths decide, dense or packed. workspace: attn_bwd_sinks_workspace_size(...) bytes.
  */
 size_t attn_bwd_sinks_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, int causal,
                                      int window_left, int window_right, int sinks, int deterministic);
