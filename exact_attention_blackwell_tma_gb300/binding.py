@@ -59,6 +59,8 @@ def _declare(lib):
                                                                      c_void_p, c_void_p])
     lib.attn_bwd_sinks_workspace_size.restype = c_size_t
     lib.attn_bwd_sinks_workspace_size.argtypes = [c_int] * 12
+    lib.attn_bwd_packed_workspace_size.restype = c_size_t
+    lib.attn_bwd_packed_workspace_size.argtypes = [c_int] * 12
     lib.attn_bwd_sinks.restype = c_int
     lib.attn_bwd_sinks.argtypes = ([c_void_p] * 9 + [c_int] * 7 + [c_float, c_int, c_int, c_int, c_int, c_void_p,
                                                                      c_void_p, c_int, c_void_p, c_size_t, c_void_p])
@@ -224,6 +226,12 @@ def attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window_left
                                                 int(window_right), int(sinks), int(deterministic))
 
 
+def attn_bwd_packed_workspace_size(B, H, Hkv, Tq, Tk, d, d_v, causal, window_left, window_right, sinks,
+                                   deterministic) -> int:
+    return load().attn_bwd_packed_workspace_size(B, H, Hkv, Tq, Tk, d, d_v, int(causal), int(window_left),
+                                                 int(window_right), int(sinks), int(deterministic))
+
+
 def attn_bwd_sinks(q, k, v, o, lse, dout, dq, dk, dv, B, H, Hkv, Lq, Lk, d, d_v, scale, causal, window_left,
                    window_right, sinks, cu_seqlens_q, cu_seqlens_k, deterministic, workspace, ws_bytes,
                    stream=None) -> int:
@@ -346,7 +354,9 @@ def _mask_heads(block_mask, H, Lq, Lk):
     return 1 if len(shape) == 2 else shape[0]
 
 
-_sinks_workspace = functools.lru_cache(maxsize=4096)(attn_bwd_sinks_workspace_size)   # a function of the sizes alone
+# functions of the sizes alone
+_sinks_workspace = functools.lru_cache(maxsize=4096)(attn_bwd_sinks_workspace_size)
+_packed_workspace = functools.lru_cache(maxsize=4096)(attn_bwd_packed_workspace_size)
 
 
 def _no_block_mask(block_mask):
@@ -413,7 +423,9 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
     B, H, Lq, Lk, d, Hkv = _dims(q, k, cu_seqlens)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     d_v = v.shape[-1]
-    if sinks:
+    if cu_seqlens is not None:
+        need = _packed_workspace(B, H, Hkv, Lq, Lk, d, d_v, causal, window[0], window[1], sinks, deterministic)
+    elif sinks:
         need = _sinks_workspace(B, H, Hkv, Lq, Lk, d, d_v, causal, window[0], window[1], sinks, deterministic)
     else:
         need = attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic)

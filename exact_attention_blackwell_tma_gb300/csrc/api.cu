@@ -354,8 +354,8 @@ extern "C" size_t attn_bwd_ex_workspace_size(int B, int H, int Hkv, int Lq, int 
     (void)causal;
     (void)deterministic;
     if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Lq < 0 || Lk < 0 || d <= 0 || d_v <= 0) return 0;
-    // varlen and dense share the formula when Lq and Lk are the packed count;
-    // the varlen semaphore bound is the larger one, so take the maximum.
+    // For either reading of the sizes: a dense problem's rows are B * Lq, a packed
+    // one's Lq, with a semaphore bound that may be the larger.
     BwdWorkspace a = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, false), b = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, true);
     return a.total > b.total ? a.total : b.total;
 }
@@ -371,6 +371,14 @@ extern "C" size_t attn_bwd_sinks_workspace_size(int B, int H, int Hkv, int Lq, i
         most = n > most ? n : most;
     }
     return most;
+}
+
+extern "C" size_t attn_bwd_packed_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int d_v, int causal,
+                                                 int window_left, int window_right, int sinks, int deterministic) {
+    (void)deterministic;
+    if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Tq < 0 || Tk < 0 || d <= 0 || d_v <= 0) return 0;
+    const int parts = sink_part_count(B, Tq, true, window_left, causal ? 0 : window_right, sinks);
+    return bwd_layout(B, H, Hkv, Tq, Tk, d, d_v, true, parts, sink_block_count(sinks, Tk)).total;
 }
 
 extern "C" size_t attn_bwd_gqa_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int causal,
@@ -410,9 +418,12 @@ int bwd_entry(const void* q, const void* k, const void* v, const void* o, const 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) ||
         !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
         return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
-    const size_t need = sinks > 0 ? attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window_left,
-                                                                 window_right, sinks, deterministic)
-                                  : attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic);
+    // (a dense problem's is the larger of the two readings of its sizes, which differ by a few semaphores)
+    const size_t need = cu_seqlens ? attn_bwd_packed_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window_left,
+                                                                    window_right, sinks, deterministic)
+                        : sinks > 0 ? attn_bwd_sinks_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, window_left,
+                                                                    window_right, sinks, deterministic)
+                                    : attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic);
     if (!workspace || ws_bytes < need)
         return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

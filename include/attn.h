@@ -183,7 +183,9 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
                 const int* cu_seqlens_q, const int* cu_seqlens_k, cudaStream_t stream);
 
 /*
- * Workspace for attn_bwd_ex (any of the arguments attn_bwd_ex accepts).
+ * Workspace for attn_bwd_ex (any of the arguments attn_bwd_ex accepts). For a
+ * packed batch this counts Lq = Tq rows for every sequence:
+ * attn_bwd_packed_workspace_size is what such a call needs, B times less.
  */
 size_t attn_bwd_ex_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, int causal,
                                   int deterministic);
@@ -217,7 +219,9 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
  * bf16 O; but rows that see at most eight keys, of sequences of at most 128
  * query rows or under a window that with its sinks holds at most eight keys, get
  * it as sum_j P_ij <dO_i, v_j>, where the rounding of O would show in dS. The
- * sequence's own lengths decide, dense or packed. workspace: attn_bwd_sinks_workspace_size(...) bytes.
+ * sequence's own lengths decide, dense or packed. workspace:
+ * attn_bwd_sinks_workspace_size(...) bytes, or for packed sequences
+ * attn_bwd_packed_workspace_size(...), which is smaller.
  */
 size_t attn_bwd_sinks_workspace_size(int B, int H, int Hkv, int Lq, int Lk, int d, int d_v, int causal,
                                      int window_left, int window_right, int sinks, int deterministic);
@@ -231,6 +235,15 @@ int attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, c
                    int window_left, int window_right, int sinks,
                    const int* cu_seqlens_q, const int* cu_seqlens_k, int deterministic,
                    void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * What the backward of a packed batch (Tq query rows and Tk key rows in all)
+ * needs, whichever of attn_bwd, attn_bwd_gqa, attn_bwd_varlen, attn_bwd_ex
+ * (sinks 0 for these) or attn_bwd_sinks is called: about Tq * H * d * 4 bytes.
+ * Returns 0 for invalid sizes.
+ */
+size_t attn_bwd_packed_workspace_size(int B, int H, int Hkv, int Tq, int Tk, int d, int d_v, int causal,
+                                      int window_left, int window_right, int sinks, int deterministic);
 
 /*
  * Workspace for attn_bwd_gqa: as attn_bwd_workspace_size, plus fp32 slots

@@ -1,4 +1,4 @@
-"""Windows with sinks in batches of very different sequences."""
+"""Windows with sinks in batches of very different sequences, and the workspace of the backward."""
 import math
 
 import pytest
@@ -32,3 +32,48 @@ def test_few_keys_beside_a_long_sequence(d, dv):
         got = torch.cat([got[s] for s in short]).double().cpu()
         rel = ((got - ref).norm() / ref.norm()).item()
         assert rel <= math.sqrt(2 / 3) * 2.0 ** -8, f"{n}: {rel:.2e}"
+
+
+@pytest.fixture(scope="module")
+def host_lib():
+    from exact_attention_blackwell_tma_gb300 import build
+    build.build()
+    return binding.load()
+
+
+@pytest.mark.parametrize("B,L,H,Hkv,d,dv,window,sinks", [(64, 2048, 32, 8, 128, 128, 512, 4), (16, 4096, 16, 16, 64, 64, 512, 4),
+                                                        (1024, 30, 8, 2, 192, 128, 50, 1), (64, 2048, 32, 8, 128, 128, -1, 0),
+                                                        (7, 333, 4, 4, 256, 256, 1000, 70)])
+def test_packed_workspace_goes_by_the_rows(host_lib, B, L, H, Hkv, d, dv, window, sinks):
+    """A packed batch of T rows needs the fp32 dQ of T rows, D, semaphores, the map and at most as much again in
+    partials, not B times that; the call asks for exactly this."""
+    T = B * L
+    need = host_lib.attn_bwd_packed_workspace_size(B, H, Hkv, T, T, d, dv, 1, window, 0, sinks, 0)
+    dq = 4 * T * H * d
+    assert dq <= need <= 2 * dq + (64 << 20)
+    x = 1 << 20   # never used: the workspace is refused first
+    rc = host_lib.attn_bwd_sinks(*([x] * 9), B, H, Hkv, T, T, d, dv, 0.1, 1, window, 0, sinks, x, None, 0, x, need - 1, None)
+    assert rc == binding.ATTN_ERR_WORKSPACE and f"{need} bytes needed" in binding.last_error()
+    assert host_lib.attn_bwd_packed_workspace_size(B, 3, 2, T, T, d, dv, 1, window, 0, sinks, 0) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [((60, 0), 200), ((-1, -1), 0)])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 4, 64), (4, 2, 192)])
+def test_packed_backward_stays_inside_its_workspace(H, Hkv, d, window, sinks):
+    """With exactly the bytes asked for, whatever they hold, the gradients are the same and the bytes behind stay."""
+    lens = [900, 1, 0, 300, 1500] + [40] * 30
+    cu = inputs.cu_seqlens(lens)
+    T = sum(lens)
+    g = torch.Generator("cpu").manual_seed(186)
+    q, k, v, do = (torch.randn(T, h, d, generator=g).to(torch.bfloat16).cuda() for h in (H, Hkv, Hkv, H))
+    kw = dict(causal=True, window=window, sinks=sinks, cu_seqlens=cu.cuda())
+    o, lse = binding.forward(q, k, v, **kw)
+    ref = binding.backward(q, k, v, o, lse, do, deterministic=True, **kw)
+    need = binding.attn_bwd_packed_workspace_size(len(lens), H, Hkv, T, T, d, d, 1, *window, sinks, 1)
+    for fill in (0, 255):
+        buf = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+        got = binding.backward(q, k, v, o, lse, do, deterministic=True, workspace=buf[:need], **kw)
+        binding.check_status()
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+        assert (buf[need:] == fill).all()
