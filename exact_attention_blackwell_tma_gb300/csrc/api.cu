@@ -346,6 +346,9 @@ BwdWorkspace bwd_layout(int B, int H, int Hkv, int Lq, int Lk, int d, int dv, bo
     w.total = w.sem_off + align256(n_sem * sizeof(int)) + align256(sizeof(VarlenMap));
     return w;
 }
+int sink_parts_of(int B, int H, int Hkv, int Lq, int Lk, bool varlen, int win_left, int win_right, int sinks) {
+    return sink_part_count(B, Hkv, bwd_head_split(B, Hkv, H / Hkv, Lk, varlen), Lq, Lk, varlen, win_left, win_right, sinks);
+}
 
 }  // namespace
 
@@ -366,7 +369,7 @@ extern "C" size_t attn_bwd_sinks_workspace_size(int B, int H, int Hkv, int Lq, i
     if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Lq < 0 || Lk < 0 || d <= 0 || d_v <= 0) return 0;
     size_t most = 0;
     for (int varlen = 0; varlen < 2; ++varlen) {   // (sized for both, as attn_bwd_ex_workspace_size)
-        const int parts = sink_part_count(B, Lq, varlen, window_left, causal ? 0 : window_right, sinks);
+        const int parts = sink_parts_of(B, H, Hkv, Lq, Lk, varlen, window_left, causal ? 0 : window_right, sinks);
         const size_t n = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, varlen, parts, sink_block_count(sinks, Lk)).total;
         most = n > most ? n : most;
     }
@@ -377,7 +380,7 @@ extern "C" size_t attn_bwd_packed_workspace_size(int B, int H, int Hkv, int Tq, 
                                                  int window_left, int window_right, int sinks, int deterministic) {
     (void)deterministic;
     if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Tq < 0 || Tk < 0 || d <= 0 || d_v <= 0) return 0;
-    const int parts = sink_part_count(B, Tq, true, window_left, causal ? 0 : window_right, sinks);
+    const int parts = sink_parts_of(B, H, Hkv, Tq, Tk, true, window_left, causal ? 0 : window_right, sinks);
     return bwd_layout(B, H, Hkv, Tq, Tk, d, d_v, true, parts, sink_block_count(sinks, Tk)).total;
 }
 
@@ -430,7 +433,7 @@ int bwd_entry(const void* q, const void* k, const void* v, const void* o, const 
         return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
     DevInfo di;
     if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
-    const int parts = sink_part_count(B, Lq, varlen, window_left, causal ? 0 : window_right, sinks);
+    const int parts = sink_parts_of(B, H, Hkv, Lq, Lk, varlen, window_left, causal ? 0 : window_right, sinks);
     const int sink_blocks = parts > 1 ? sink_block_count(sinks, Lk) : 0;
     BwdWorkspace wl = bwd_layout(B, H, Hkv, Lq, Lk, d, d_v, varlen, parts, sink_blocks);
     char* ws = static_cast<char*>(workspace);

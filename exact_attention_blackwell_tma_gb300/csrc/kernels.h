@@ -126,13 +126,21 @@ inline size_t bwd_partial_bytes(int split, long rows_k, int Hkv, int d, int dv) 
 // + 2 query blocks, a block with sinks all of a sequence's, so it is cut into
 // parts of that length (at most 32). Without parts the longest tile sets the time
 // (B2 H16 L8192 d128, window 1024: a sink block visits 64 query blocks, the
-// others 9; see the backward's launcher for the times).
+// others 9; see the backward's launcher for the times). Many sink blocks balance
+// by themselves: no more parts than it takes to make kSplitTargetTiles tiles of
+// them, which also bounds the partials to twice that many tiles (0.34 GB at
+// d = 256), however many keys are sinks (B2 H16 L8192 d128, window 100, every key a
+// sink: 5.25 ms in 21 parts, 1.62 in one; B8 H32 L4096, window 128, 200 sinks: 1.84
+// in 10, 1.52 in 2).
 constexpr int kMaxSinkParts = 32;
 inline int sink_block_count(int sinks, int Lk) { return ((sinks < Lk ? sinks : Lk) + 127) / 128; }
-inline int sink_part_count(int B, int Lq, bool varlen, int win_left, int win_right, int sinks) {
+inline int sink_part_count(int B, int Hkv, int split, int Lq, int Lk, bool varlen, int win_left, int win_right, int sinks) {
     if (sinks <= 0 || win_left < 0 || win_right < 0 || B <= 0) return 1;
     const long nq = ((varlen ? (long)Lq / B : (long)Lq) + 127) / 128, window = ((long)win_left + win_right + 127) / 128 + 2;
-    const long parts = nq / window;
+    const long tiles = (long)B * sink_block_count(sinks, Lk) * Hkv * split;   // (none if there are no keys)
+    const long wanted = tiles > 0 ? (kSplitTargetTiles + tiles - 1) / tiles : 1;
+    long parts = nq / window;
+    if (parts > wanted) parts = wanted;
     return parts < 1 ? 1 : (parts > kMaxSinkParts ? kMaxSinkParts : (int)parts);
 }
 // Bytes of their partials: dK slots (part-major, then split), then dV slots, of

@@ -77,3 +77,18 @@ def test_packed_backward_stays_inside_its_workspace(H, Hkv, d, window, sinks):
         binding.check_status()
         assert all(torch.equal(a, b) for a, b in zip(ref, got))
         assert (buf[need:] == fill).all()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("B,L,H,Hkv,d,window", [(1, 32768, 32, 32, 128, 128), (2, 8192, 16, 16, 128, 100), (8, 32768, 8, 8, 64, 128),
+                                                (1, 5001, 8, 2, 192, 64), (1, 100000, 1, 1, 256, 10), (64, 2048, 32, 8, 128, 0)])
+def test_sink_partials_are_bounded(host_lib, B, L, H, Hkv, d, window, packed):
+    """However many keys are sinks, their partial dK and dV take at most 2 x 640 tiles of 128 rows (kernels.h)."""
+    rows = B * L if packed else L
+    size = host_lib.attn_bwd_packed_workspace_size if packed else host_lib.attn_bwd_sinks_workspace_size
+    base = size(B, H, Hkv, rows, rows, d, d, 1, window, 0, 0, 0)
+    for sinks in (1, 4, 129, 1000, 5000, L, 2 ** 31 - 1):
+        more = size(B, H, Hkv, rows, rows, d, d, 1, window, 0, sinks, 0) - base
+        assert 0 <= more <= 2 * 640 * 128 * 2 * d * 4 + 256, (sinks, more)
+    if L // 128 > window // 128 + 2 and B * Hkv * H // Hkv < 320:   # few sinks of a long sequence: cut into parts
+        assert size(B, H, Hkv, rows, rows, d, d, 1, window, 0, 4, 0) > base
