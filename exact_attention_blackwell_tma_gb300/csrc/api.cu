@@ -728,7 +728,7 @@ extern "C" int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_ca
     // the work list counts pages of row blocks in an int
     const double units = ((double)p.s.total * group / (8 * nr) + B) * table_width * p.c.Hkv;
     if ((double)p.s.total * H >= 2.0e9) return fail(ATTN_ERR_ARG, "too many rows");
-    if (units >= 2.0e9) return fail(ATTN_ERR_ARG, "kv4: too many (row block, page) pairs");
+    if (units >= (double)kKv4MostUnits) return fail(ATTN_ERR_ARG, "kv4: too many (row block, page) pairs");
     if (p.s.total > 0 && (!q || !o || !lse)) return fail(ATTN_ERR_ARG, "null tensor pointer");
     if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(key_weights))
         return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");

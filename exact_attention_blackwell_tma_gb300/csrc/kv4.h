@@ -69,6 +69,10 @@ inline int kv4_row_tiles(int group, int B, int total) {
     return rows <= 8 ? 1 : 2;
 }
 constexpr int kKv4MaxCtas = 640;
+// The work list counts (row block, two pages) units in an int. A batch of rows
+// that follow one another stays below this (checked on the host); offsets that
+// run backwards can make sequences share rows and pass it: such a call does no work.
+constexpr long kKv4MostUnits = 2000000000;
 // Workspace parts in bytes.
 inline size_t kv4_prefix_bytes() { return (kKv4MaxBatch + 8) * sizeof(int); }
 inline size_t kv4_ml_bytes(int nr) { return (size_t)kKv4MaxCtas * 2 * nr * 8 * 2 * sizeof(float); }

@@ -195,21 +195,28 @@ __device__ __forceinline__ Cut build_prefix(const Kv4FwdParams& p, int* prefix, 
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        auto total = [&](const Cut& c) {   // units of the list (below 2^31: checked on the host)
-            int x = 0;
-            for (int b = lane; b < p.s.B; b += 32) x += times[b] * c.span(prefix[b + 1]);
+        auto total = [&](const Cut& c) {   // units of the list
+            long x = 0;
+            for (int b = lane; b < p.s.B; b += 32) x += (long)times[b] * c.span(prefix[b + 1]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
             return x;
         };
+        const long all = total(Cut{0, 0});
+        const bool fits = all <= kKv4MostUnits;
+        if (!fits) {   // (see kKv4MostUnits: an empty list, cut into nothing)
+            for (int b = lane; b < p.s.B; b += 32) times[b] = 0;
+            __syncwarp();
+            if (blockIdx.x == 0 && lane == 0) atomicCAS(p.status, kStatusOk, kStatusBadPage);
+        }
         int longest = 0;
         for (int b = lane; b < p.s.B; b += 32) longest = max(longest, times[b] > 0 ? prefix[b + 1] : 0);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(kFullMask, longest, o));
         Cut cut{0, 0};
-        cut.per = max((total(cut) + ctas - 1) / ctas, longest > 0 ? least_per(longest) : 0);
+        cut.per = fits ? max((int)((all + ctas - 1) / ctas), longest > 0 ? least_per(longest) : 0) : 0;
         for (int per = cut.per; per > 0 && per <= kAlignedMost; ++per)
-            if (total(Cut{per, 1}) <= per * ctas) {
+            if (total(Cut{per, 1}) <= (long)per * ctas) {
                 cut = Cut{per, 1};
                 break;
             }
@@ -835,6 +842,7 @@ __global__ void __launch_bounds__(kFinishThreads, 7) kv4_finish_kernel(const Kv4
             if (lane == 0) *lse = -INFINITY;
             return;
         }
+        if (p.prefix[kKv4MaxBatch + 1] == 0) return;   // (a list that did not fit: nothing to join)
         const Shares s = shares_of(p, w, b, head / p.group, i * p.group + head % p.group, rows_per_block);
         if (s.c0 == s.c1) return;
         const float2 ml = join_ml(p, s, lane, 32);
@@ -882,6 +890,7 @@ __global__ void __launch_bounds__(kFinishThreads, 7) kv4_finish_kernel(const Kv4
     if (j0 == 0 && w.s.lk > p.weight_stride) atomicCAS(p.status, kStatusOk, kStatusBadPage);
     const int keys = (int)min((long)w.s.lk, p.weight_stride);
     if (w.s.bad || (id % key_blocks) * kTiles * kFinishKeys >= keys) return;
+    if (w.units > 0 && w.rows > 0 && p.prefix[kKv4MaxBatch + 1] == 0) return;   // (a list that did not fit)
     bool seen[kTiles];
     float sum[kTiles][4] = {};
 #pragma unroll

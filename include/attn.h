@@ -337,9 +337,10 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  *               they are. A sequence may have no rows.
  * All on the device; pages may be shared by sequences as long as no call
  * writes them. A page id, length or offset out of range touches no memory
- * outside the cache: the keys of such a page do not count, and
- * attn_check_status reports ATTN_ERR_ARG. Calls are asynchronous, allocate
- * nothing and can be captured into a CUDA graph.
+ * outside the cache: the keys of such a page do not count, rows may be left
+ * unwritten where offsets do not ascend, and attn_check_status reports
+ * ATTN_ERR_ARG. Calls are asynchronous, allocate nothing and can be captured
+ * into a CUDA graph.
  */
 typedef struct attn_kv4_cache {
     void* k_codes;

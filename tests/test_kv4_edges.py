@@ -62,3 +62,26 @@ def test_forward_tiny_values(size, d):
 def test_forward_huge_values(size, d):
     """Value scales past 2^107, where 2^24 times the scale leaves the fp32 range."""
     check_values_of_size(size, d, [1, 3], [700, 33], 2)
+
+
+@pytest.mark.gpu
+def test_offsets_that_run_backwards_do_no_work():
+    """Offsets 0, T, 0, T, .. pass every sequence's own check but give 512 sequences the same rows, whose work list
+    (512 sequences x 16384 row blocks x 32768 units = 2^38) no int counts: reported, nothing written."""
+    T, H, width = 4096, 64, 1 << 16
+    pool = Pool([64], 1, 64, seed=34)
+    table = torch.full((1023, width), -1, dtype=torch.int32, device="cuda")
+    lens = torch.full((1023,), width * 64, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([T * (i % 2) for i in range(1024)], dtype=torch.int32).cuda()
+    q = torch.ones(T, H, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((T, H, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, T), 7.0, device="cuda")
+    binding.kv4_forward(q, pool.cache, table, lens, cu_seqlens=cu, out=out, lse=lse)
+    with pytest.raises(binding.AttnError):
+        binding.check_status()
+    assert (out == 7).all() and (lse == 7).all()
+    # the next call is not affected
+    q = bf16(pool.g, 1, 2, 64)
+    o, _ = binding.kv4_forward(q.cuda(), pool.cache, pool.table, pool.lens_t, cu_seqlens=offsets([1]).cuda())
+    binding.check_status()
+    assert torch.isfinite(o).all()
