@@ -372,6 +372,12 @@ def _check_tensors(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
+def _check_workspace(workspace, device):
+    """A caller's workspace goes to the kernels as it is: it has to lie on their device (an index)."""
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{device}, got one on {workspace.device}")
+
+
 def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, out=None, lse=None,
             stream=None, cu_seqlens_k=None, window=(-1, -1), block_mask=None, sinks=0):
     """O, LSE for bf16 q, k, v ([B, L, H, d], or [T, H, d] with int32 cu_seqlens).
@@ -431,6 +437,8 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
         need = attn_bwd_ex_workspace_size(B, H, Hkv, Lq, Lk, d, d_v, causal, deterministic)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(workspace, q.get_device())
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -623,6 +631,7 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
         if workspace is None:
             workspace, size = torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
         else:
+            _check_workspace(workspace, index)
             size = workspace.numel() * workspace.element_size()
     _check(load().attn_kv4_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), width, cache_lens.data_ptr(),
                                _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr(), B, H, L, scale, int(causal), window[0],

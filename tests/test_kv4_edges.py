@@ -85,3 +85,29 @@ def test_offsets_that_run_backwards_do_no_work():
     o, _ = binding.kv4_forward(q.cuda(), pool.cache, pool.table, pool.lens_t, cu_seqlens=offsets([1]).cuda())
     binding.check_status()
     assert torch.isfinite(o).all()
+
+
+@pytest.mark.gpu
+def test_refuses_a_workspace_that_is_not_on_the_device():
+    pool = Pool([100], 1, 64, seed=35)
+    q, cu = bf16(pool.g, 1, 2, 64).cuda(), offsets([1]).cuda()
+    args = (q, pool.cache, pool.table, pool.lens_t)
+    need = binding.attn_kv4_fwd_workspace_size(1, 2, 1, 1, 1, pool.width, 64, 64, 0)
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.uint8, pin_memory=True),
+                torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            binding.kv4_forward(*args, cu_seqlens=cu, workspace=bad)
+    o, lse = binding.kv4_forward(*args, cu_seqlens=cu)
+    o2, lse2 = binding.kv4_forward(*args, cu_seqlens=cu, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    x = torch.ones(1, 9, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = binding.forward(x, x, x, causal=True, window=(3, 0), sinks=1)
+    with pytest.raises(ValueError):
+        binding.backward(x, x, x, o, lse, x, causal=True, window=(3, 0), sinks=1,
+                         workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    binding.check_status()
+
+
+def test_workspace_check():
+    with pytest.raises(ValueError):
+        binding._check_workspace(torch.empty(8, dtype=torch.uint8), 0)
