@@ -679,7 +679,7 @@ extern "C" int attn_kv4_append(const void* k, const void* v, long long k_stride,
     if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
     const cudaError_t e = launch_kv4_append(c, s, static_cast<const __nv_bfloat16*>(k),
                                             static_cast<const __nv_bfloat16*>(v), (long)k_stride, (long)v_stride,
-                                            di.status, stream);
+                                            di.status, di.sms, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 append launch failed: %s", cudaGetErrorString(e));
     return ok();
 }
@@ -696,7 +696,7 @@ extern "C" int attn_kv4_read(void* k, void* v, const attn_kv4_cache* cache, cons
     DevInfo di;
     if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
     const cudaError_t e = launch_kv4_read(c, s, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v),
-                                          di.status, stream);
+                                          di.status, di.sms, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "kv4 read launch failed: %s", cudaGetErrorString(e));
     return ok();
 }

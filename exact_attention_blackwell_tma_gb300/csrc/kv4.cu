@@ -429,23 +429,23 @@ __global__ void __launch_bounds__(128) kv4_gather_kernel(Kv4EvictParams p, int t
 // Rows per warp: up to four, which look their places up together, as long as
 // that leaves 48 warps per SM (17000 rows of 8 heads, d = 128, append: 34 us with
 // four rows per warp, 30 with two).
-int rows_per_warp(int total) {
-    const int rows = total / (152 * 48);
+int rows_per_warp(int total, int num_sms) {
+    const int rows = total / (num_sms * 48);
     return rows < 1 ? 1 : (rows > 4 ? 4 : rows);
 }
 
 template <int GK, int GV>
 cudaError_t append_dims(const Kv4Cache& c, const Kv4Batch& s, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                        long k_stride, long v_stride, int* status, cudaStream_t stream) {
-    const int rows = rows_per_warp(s.total), per_block = 4 * rows;
+                        long k_stride, long v_stride, int* status, int num_sms, cudaStream_t stream) {
+    const int rows = rows_per_warp(s.total, num_sms), per_block = 4 * rows;
     kv4_append_kernel<GK, GV><<<(s.total + per_block - 1) / per_block, 128, 0, stream>>>(c, s, k, v, k_stride, v_stride,
                                                                                         rows, status);
     return cudaGetLastError();
 }
 template <int GK, int GV>
 cudaError_t read_dims(const Kv4Cache& c, const Kv4Batch& s, __nv_bfloat16* k, __nv_bfloat16* v, int* status,
-                      cudaStream_t stream) {
-    const int rows = rows_per_warp(s.total), per_block = 4 * rows;
+                      int num_sms, cudaStream_t stream) {
+    const int rows = rows_per_warp(s.total, num_sms), per_block = 4 * rows;
     kv4_read_kernel<GK, GV><<<(s.total + per_block - 1) / per_block, 128, 0, stream>>>(c, s, k, v, rows, status);
     return cudaGetLastError();
 }
@@ -478,15 +478,17 @@ cudaError_t for_dims(const Kv4Cache& c, F call) {
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4Cache& c, const Kv4Batch& s, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                              long k_stride, long v_stride, int* status, cudaStream_t stream) {
+                              long k_stride, long v_stride, int* status, int num_sms, cudaStream_t stream) {
     return for_dims(c, [&](auto gk, auto gv) {
-        return append_dims<gk.value, gv.value>(c, s, k, v, k_stride, v_stride, status, stream);
+        return append_dims<gk.value, gv.value>(c, s, k, v, k_stride, v_stride, status, num_sms, stream);
     });
 }
 
 cudaError_t launch_kv4_read(const Kv4Cache& c, const Kv4Batch& s, __nv_bfloat16* k, __nv_bfloat16* v, int* status,
-                            cudaStream_t stream) {
-    return for_dims(c, [&](auto gk, auto gv) { return read_dims<gk.value, gv.value>(c, s, k, v, status, stream); });
+                            int num_sms, cudaStream_t stream) {
+    return for_dims(c, [&](auto gk, auto gv) {
+        return read_dims<gk.value, gv.value>(c, s, k, v, status, num_sms, stream);
+    });
 }
 
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream) {

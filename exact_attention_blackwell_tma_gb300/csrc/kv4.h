@@ -80,9 +80,9 @@ inline size_t kv4_part_bytes(int nr, int dv) { return (size_t)kKv4MaxCtas * 2 * 
 
 cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_append(const Kv4Cache& c, const Kv4Batch& s, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                              long k_stride, long v_stride, int* status, cudaStream_t stream);
+                              long k_stride, long v_stride, int* status, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4Cache& c, const Kv4Batch& s, __nv_bfloat16* k, __nv_bfloat16* v, int* status,
-                            cudaStream_t stream);
+                            int num_sms, cudaStream_t stream);
 struct Kv4EvictParams {
     Kv4Cache c;
     const int* table;
