@@ -154,9 +154,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without building the Stream object (3 us); torch does not promise this name
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:   # the handle of torch.cuda.current_stream() without building the Stream object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return (torch.cuda.current_stream().cuda_stream if _raw_stream is None
+                else _raw_stream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
