@@ -405,8 +405,8 @@ def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, 
     if sinks:
         _no_block_mask(block_mask)
         _check(load().attn_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv,
-                                     Lq, Lk, d, dv, scale, int(causal), int(window[0]), int(window[1]), int(sinks),
-                                     _ptr(cu_seqlens), _ptr(cu_seqlens_k), _stream(stream)))
+                                     Lq, Lk, d, dv, scale, int(causal), window[0], window[1], sinks, _ptr(cu_seqlens),
+                                     _ptr(cu_seqlens_k), _stream(stream)))
     elif tuple(window) != (-1, -1) or block_mask is not None:
         mh = _mask_heads(block_mask, H, Lq, Lk)
         _check_tensors(block_mask)
@@ -452,7 +452,7 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
         _no_block_mask(block_mask)
         _check(load().attn_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                      dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Lq, Lk, d,
-                                     d_v, scale, int(causal), int(window[0]), int(window[1]), int(sinks), _ptr(cu_seqlens),
+                                     d_v, scale, int(causal), window[0], window[1], sinks, _ptr(cu_seqlens),
                                      _ptr(cu_seqlens_k), int(deterministic), workspace.data_ptr(), ws_bytes,
                                      _stream(stream)))
     elif d_v != d or tuple(window) != (-1, -1) or block_mask is not None:
@@ -640,7 +640,7 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
             size = workspace.numel() * workspace.element_size()
     _check(load().attn_kv4_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), width, cache_lens.data_ptr(),
                                _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr(), B, H, L, scale, int(causal),
-                               int(window[0]), int(window[1]), int(sinks), _ptr(key_weights),
+                               window[0], window[1], sinks, _ptr(key_weights),
                                0 if key_weights is None else key_weights.shape[2], weight_decay, workspace.data_ptr(), size, _stream(stream)))
     return out, lse
 
@@ -661,6 +661,6 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
         new_key_weights = _kv4_out(new_key_weights, (B, cache.Hkv, columns), torch.float32, device, "new_key_weights")
     _check(load().attn_kv4_evict(cache._struct, page_table.data_ptr(), page_table.shape[1], cache_lens.data_ptr(),
                                  key_weights.data_ptr(), key_weights.shape[2], new_table.data_ptr(), new_table.shape[1],
-                                 B, int(budget), int(sinks), int(recent), new_lens.data_ptr(), kept.data_ptr(),
+                                 B, budget, sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
                                  new_key_weights.data_ptr(), columns, _stream(stream)))
     return new_lens, kept, new_key_weights
