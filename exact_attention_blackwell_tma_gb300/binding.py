@@ -511,6 +511,8 @@ class Kv4Cache:
     def empty(cls, n_pages, Hkv, d, dv=None, device="cuda"):
         """A cache of n_pages zeroed pages."""
         dv = d if dv is None else dv
+        if d % KV4_GROUP or dv % KV4_GROUP:
+            raise ValueError(f"head dims {d}, {dv} of a 4-bit cache must be multiples of {KV4_GROUP}")
 
         def codes(width):
             return torch.zeros((n_pages, Hkv, width // KV4_GROUP, KV4_PAGE, KV4_GROUP // 2), dtype=torch.uint8,

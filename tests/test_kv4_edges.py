@@ -111,3 +111,9 @@ def test_refuses_a_workspace_that_is_not_on_the_device():
 def test_workspace_check():
     with pytest.raises(ValueError):
         binding._check_workspace(torch.empty(8, dtype=torch.uint8), 0)
+
+
+@pytest.mark.parametrize("d,dv", [(96, None), (100, 64), (128, 72), (32, 32)])
+def test_empty_cache_refuses_head_dims(d, dv):
+    with pytest.raises(ValueError, match="multiples of 64"):
+        binding.Kv4Cache.empty(3, 1, d, dv, device="cpu")
