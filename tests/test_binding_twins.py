@@ -81,3 +81,25 @@ def test_sinks_of_twins_and_other_integers():
     a = binding.kv4_forward(q[0, :1], *args, cu_seqlens=cu, window=(50, -1), sinks=4)
     b = binding.kv4_forward(q[0, :1], *args, cu_seqlens=cu, window=np.array([50, -1]), sinks=np.int64(4))
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1, 10 ** 20])
+def test_integers_that_do_not_fit_are_refused(big):
+    """Their low 32 bits would be another bound (2^32 sinks: none)."""
+    x = torch.ones(1, 200, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = binding.forward(x, x, x, causal=True, window=(5, 0), sinks=2)
+    pool = Pool([200], 2, 64, seed=44)
+    args, cu = (pool.cache, pool.table, pool.lens_t), offsets([1]).cuda()
+    w = torch.zeros(1, 2, 256, device="cuda")
+    for window, sinks in (((5, 0), big), ((big, 0), 2), ((5, big), 2)):
+        with pytest.raises(ValueError, match="fit"):
+            binding.forward(x, x, x, causal=True, window=window, sinks=sinks)
+        with pytest.raises(ValueError, match="fit"):
+            binding.backward(x, x, x, o, lse, x, causal=True, window=window, sinks=sinks)
+        with pytest.raises(ValueError, match="fit"):
+            binding.kv4_forward(x[0, :1], *args, cu_seqlens=cu, window=window, sinks=sinks)
+    for kw in (dict(budget=big), dict(budget=64, sinks=big), dict(budget=64, recent=big)):
+        with pytest.raises(ValueError, match="fit"):
+            binding.kv4_evict(*args, w, pool.table, **kw)
+    binding.check_status()
