@@ -340,7 +340,7 @@ inline FewKeys few_key_rows(const BwdParams& p) {
 // together. row: packed row, h: query head, (b, r): dense sequence and row in it,
 // dout: the row's dO. kFewAll: q and dO stay in registers over the keys, and a block
 // takes 32 rows of a head, whose keys are mostly the same, so L1 serves them (B3 H32
-// L2329 d192, 7 keys per row: 755 -> 201 us for the preprocess kernel). kFewShort:
+// L2329 d192, 7 keys per row: the preprocess kernel 211 us, 884 without). kFewShort:
 // rows in memory order and few registers, as the rows of long sequences, which
 // only look their sequence up, want the memory bandwidth (64 packed sequences of 2048
 // rows, H32/8, d128: the backward 5.97 ms without looking, 6.08, and 6.39 the other way).

@@ -169,12 +169,12 @@ struct Cut {
 // With few units per CTA a second row block costs as much as the units do (its
 // queries, its first loads, its epilogue), so the aligned cut is taken when it
 // needs at most this many units per CTA and fits the grid (16 windows of 4096
-// keys at d = 256, 33 units each, in twos: 16.7 us unaligned, 13.3 aligned). Longer ranges balance better uncut.
+// keys at d = 256, 33 units each, in twos: 16.2 us unaligned, 12.3 aligned). Longer ranges balance better uncut.
 constexpr int kAlignedMost = 8;
 // A unit takes a CTA about 1.5 us and joining a row's shares about 1 us per 8, so
 // a row block of U units is not cut into more than U / per with 12 per^2 >= U: the
 // sum of the two is least there (4 heads over 16000 keys, d = 64, 125 units each:
-// 23.4 us in ones, 15.3 in fours).
+// a pass of 23.8 us in ones, 14.6 in fours).
 __device__ __forceinline__ int least_per(int units) {
     int per = 1;
     while (12 * per * per < units) ++per;
@@ -817,8 +817,8 @@ constexpr int kFinishRows = 64;                   // rows whose LSE it holds at 
 // four keys per thread and tile, rows in order: four tiles of one row at a time, or,
 // when that makes too few blocks for the SMs, one tile of four rows; a block's rows
 // get their LSE all at once, several lanes each (4 caches of up to 2253 keys, 8 heads
-// of up to 88 rows, the wait for the attention kernel's 18 us included: 24 us, 66 with
-// four tiles and a warp per row). Scores of pages that no row block visited
+// of 88 rows, d = 128, the wait for the attention kernel's 25 us included: 38 us, 95
+// with four tiles and a warp per row). Scores of pages that no row block visited
 // were not written and count as nothing. Launched while the attention kernel
 // runs (programmatic dependent launch); what it left is read after the wait.
 template <int kTiles>
