@@ -382,13 +382,17 @@ int attn_kv4_read(void* k, void* v, const attn_kv4_cache* cache, const int* page
  * read once per 8 or 16 (query, head of the group) rows. For long chunks
  * use attn_kv4_read and attn_fwd_ex. P times a value's scale is rounded to fp16
  * relative to the largest scale that the same 64 channels of any visible key
- * have: scales more than 2^19 below it lose bits.
+ * have: scales more than 2^19 below it lose bits. Elements of q of 2^115 and
+ * more count as infinite.
  * key_weights (fp32 [B, Hkv, weight_stride], or NULL): for every cached key
  *   key_weights = weight_decay * key_weights + sum over the call's rows and the
  *   group's query heads of exp(s - LSE)
  * (weight_decay in [0, 1]; 1 accumulates, 0 ignores the old contents). Entries
  * past a sequence's length are left as they are; weight_stride must cover the
  * longest cache. Sums are taken in a fixed order: results repeat bit for bit.
+ * The workspace then holds rows x H x table_width x 64 fp32 scores (one token of 64
+ * sequences, H = 32, tables of 16384 tokens: 134 MB), so pass a table as wide as
+ * the longest cache.
  * workspace: attn_kv4_fwd_workspace_size(...) bytes, 256-byte aligned, used by
  * one call at a time (calls or captured graphs that may overlap need one each);
  * its contents need not be initialised.
