@@ -377,11 +377,11 @@ def _check_tensors(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
-def _check_ints(**bounds):
-    """ctypes keeps the low 32 bits of an integer without a word."""
-    for name, x in bounds.items():
+def _check_ints(*bounds):
+    """Window bounds, sinks and budgets: ctypes keeps the low 32 bits of an integer without a word."""
+    for x in bounds:
         if not -2 ** 31 <= x < 2 ** 31:
-            raise ValueError(f"{name} {x} does not fit an int")
+            raise ValueError(f"{x} (of {bounds}) does not fit an int")
 
 
 def _check_workspace(workspace, device):
@@ -411,7 +411,7 @@ def forward(q, k, v, causal: bool, scale: float | None = None, cu_seqlens=None, 
         lse = torch.empty((B, H, Lq) if cu_seqlens is None else (H, Lq), dtype=torch.float32, device=q.device)
     if sinks:
         _no_block_mask(block_mask)
-        _check_ints(window_left=window[0], window_right=window[1], sinks=sinks)
+        _check_ints(window[0], window[1], sinks)
         _check(load().attn_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv,
                                      Lq, Lk, d, dv, scale, int(causal), window[0], window[1], sinks, _ptr(cu_seqlens),
                                      _ptr(cu_seqlens_k), _stream(stream)))
@@ -443,7 +443,7 @@ def backward(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, cu
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     d_v = v.shape[-1]
     if sinks:
-        _check_ints(window_left=window[0], window_right=window[1], sinks=sinks)
+        _check_ints(window[0], window[1], sinks)
     if cu_seqlens is not None:
         need = _packed_workspace(B, H, Hkv, Lq, Lk, d, d_v, causal, window[0], window[1], sinks, deterministic)
     elif sinks:
@@ -633,7 +633,7 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     their keys have been appended. window and sinks as in forward(). key_weights (fp32 [B, Hkv, >= longest cache]):
     updated in place to weight_decay * key_weights + the attention weight each key got from the call's rows."""
     B, index = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
-    _check_ints(window_left=window[0], window_right=window[1], sinks=sinks)
+    _check_ints(window[0], window[1], sinks)
     H, packed, device = q.shape[-2], cu_seqlens is not None, q.device
     L, q_stride = _kv4_rows(q, H, cache.d, B, packed, "q", index)
     if H % cache.Hkv != 0 or H == 0:
@@ -666,7 +666,7 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
     the new length) and the kept key weights fp32 [B, Hkv, budget] (or as wide as new_key_weights is)."""
     B, index = _kv4_ints(cache, page_table, cache_lens, None, new_table)
     _kv4_weights(key_weights, B, cache, index)
-    _check_ints(budget=budget, sinks=sinks, recent=recent)
+    _check_ints(budget, sinks, recent)
     device = cache_lens.device
     columns = budget if new_key_weights is None else new_key_weights.shape[-1]
     with _on(stream):
