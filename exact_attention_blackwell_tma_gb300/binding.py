@@ -654,7 +654,8 @@ def kv4_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: fl
     _check(load().attn_kv4_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), width, cache_lens.data_ptr(),
                                _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr(), B, H, L, scale, int(causal),
                                window[0], window[1], sinks, _ptr(key_weights),
-                               0 if key_weights is None else key_weights.shape[2], weight_decay, workspace.data_ptr(), size, _stream(stream)))
+                               0 if key_weights is None else key_weights.shape[2], weight_decay, workspace.data_ptr(),
+                               size, _stream(stream)))
     return out, lse
 
 
