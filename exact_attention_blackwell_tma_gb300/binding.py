@@ -96,6 +96,16 @@ def _declare(lib):
     lib.attn_kv4_evict.restype = c_int
     lib.attn_kv4_evict.argtypes = ([kv4, c_void_p, c_int, c_void_p, c_void_p, i64, c_void_p] + [c_int] * 5
                                    + [c_void_p] * 3 + [i64, c_void_p])
+    lib.attn_linear_workspace_size.restype = c_size_t
+    lib.attn_linear_workspace_size.argtypes = [c_int] * 7
+    lib.attn_linear_fwd.restype = c_int
+    lib.attn_linear_fwd.argtypes = ([c_void_p] * 3 + [i64] * 3 + [c_void_p] * 4 + [c_int] * 6
+                                    + [c_float, c_void_p, c_void_p, c_size_t, c_void_p])
+    lib.attn_linear_bwd.restype = c_int
+    lib.attn_linear_bwd.argtypes = ([c_void_p] * 4 + [i64] * 4 + [c_void_p] * 7 + [c_int] * 6
+                                    + [c_float, c_void_p, c_void_p, c_size_t, c_void_p])
+    lib.attn_linear_step.restype = c_int
+    lib.attn_linear_step.argtypes = [c_void_p] * 3 + [i64] * 3 + [c_void_p] * 3 + [c_int] * 5 + [c_float, c_void_p]
     lib.attn_set_backward_cta_pairs.restype = c_int
     lib.attn_set_backward_cta_pairs.argtypes = [c_int]
     lib.attn_set_exp2_emulation.restype = c_int
@@ -314,6 +324,31 @@ def attn_kv4_evict(cache, page_table, table_width, cache_lens, key_weights, weig
     return load().attn_kv4_evict(cache, _ptr(page_table), table_width, _ptr(cache_lens), _ptr(key_weights),
                                  weight_stride, _ptr(new_table), new_width, B, budget, sinks, recent, _ptr(new_lens),
                                  _ptr(kept), _ptr(new_key_weights), new_weight_stride, _stream(stream))
+
+
+def attn_linear_workspace_size(B, H, Hkv, L, packed, d, d_v) -> int:
+    return load().attn_linear_workspace_size(B, H, Hkv, L, int(packed), d, d_v)
+
+
+def attn_linear_fwd(q, k, v, q_stride, k_stride, v_stride, log_decay, state, o, final_state, B, H, Hkv, L, d, d_v, scale,
+                    cu_seqlens, workspace, ws_bytes, stream=None) -> int:
+    return load().attn_linear_fwd(_ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, _ptr(log_decay), _ptr(state),
+                                  _ptr(o), _ptr(final_state), B, H, Hkv, L, d, d_v, scale, _ptr(cu_seqlens),
+                                  _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def attn_linear_bwd(q, k, v, dout, q_stride, k_stride, v_stride, dout_stride, log_decay, state, dfinal, dq, dk, dv, dstate,
+                    B, H, Hkv, L, d, d_v, scale, cu_seqlens, workspace, ws_bytes, stream=None) -> int:
+    return load().attn_linear_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dout), q_stride, k_stride, v_stride, dout_stride,
+                                  _ptr(log_decay), _ptr(state), _ptr(dfinal), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate),
+                                  B, H, Hkv, L, d, d_v, scale, _ptr(cu_seqlens), _ptr(workspace), ws_bytes,
+                                  _stream(stream))
+
+
+def attn_linear_step(q, k, v, q_stride, k_stride, v_stride, log_decay, state, o, B, H, Hkv, d, d_v, scale,
+                     stream=None) -> int:
+    return load().attn_linear_step(_ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, _ptr(log_decay), _ptr(state),
+                                   _ptr(o), B, H, Hkv, d, d_v, scale, _stream(stream))
 
 
 def attn_set_backward_cta_pairs(enable) -> int:
@@ -679,3 +714,119 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
                                  B, budget, sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
                                  new_key_weights.data_ptr(), columns, _stream(stream)))
     return new_lens, kept, new_key_weights
+
+
+# ---------------------------------------------------------------- linear attention with a decay per head
+
+_linear_workspace = functools.lru_cache(maxsize=4096)(attn_linear_workspace_size)   # a function of the sizes alone
+
+
+def _linear_float(name, t, shape, device):
+    if t.dtype != torch.float32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 tensor {tuple(shape)} on cuda:{device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _linear_inputs(q, k, v, log_decay, cu_seqlens, *states):
+    """Checks what the forward and the backward share: (B, H, Hkv, L, d, dv, strides, device index)."""
+    device, packed = q.get_device(), cu_seqlens is not None
+    if device != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if q.dim() != (3 if packed else 4) or k.dim() != q.dim() or v.dim() != q.dim():
+        raise ValueError(f"q, k and v must be [{'T' if packed else 'B, L'}, heads, channels], got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    if packed:
+        _kv4_int("cu_seqlens", cu_seqlens, 1, len(cu_seqlens), device)
+    B = len(cu_seqlens) - 1 if packed else q.shape[0]
+    H, d, Hkv, dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
+    L, q_stride = _kv4_rows(q, H, d, B, packed, "q", device)
+    Lk, k_stride = _kv4_rows(k, Hkv, d, B, packed, "k", device)
+    Lv, v_stride = _kv4_rows(v, Hkv, dv, B, packed, "v", device)
+    if Lk != L or Lv != L:
+        raise ValueError(f"q has {L} rows, k {Lk}, v {Lv}")
+    _linear_float("log_decay", log_decay, (Hkv,), device)
+    for name, t in states:
+        if t is not None:
+            _linear_float(name, t, (B, Hkv, d, dv), device)
+    return B, H, Hkv, L, d, dv, (q_stride, k_stride, v_stride), device
+
+
+def _linear_scratch(workspace, B, H, Hkv, L, packed, d, dv, device):
+    """(workspace or None, bytes) for a call; the caller's is checked."""
+    if workspace is not None:
+        _check_workspace(workspace, device)
+        return workspace, workspace.numel() * workspace.element_size()
+    need = _linear_workspace(B, H, Hkv, L, packed, d, dv)
+    return (torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}") if need else None), need
+
+
+def linear_forward(q, k, v, log_decay, scale: float | None = None, cu_seqlens=None, state=None, final_state=False,
+                   out=None, workspace=None, stream=None):
+    """Linear attention with a decay per key/value head (log_decay fp32 [Hkv], natural log): o_t = scale q_t^T S_t with
+    S_t = exp(log_decay) S_(t-1) + k_t v_t^T. bf16 q, k, v [B, L, heads, channels], or [T, heads, channels] with int32
+    cu_seqlens; rows may be strided (a slice of a fused projection), query heads grouped (head h reads h // (H // Hkv)).
+    state: fp32 [B, Hkv, d, dv] to start from (None: zeros). final_state: True for the state behind the last token, or
+    the tensor to write it to (state itself will do). Returns O and that state (or None)."""
+    packed = cu_seqlens is not None
+    final = final_state if isinstance(final_state, torch.Tensor) else None
+    B, H, Hkv, L, d, dv, strides, index = _linear_inputs(q, k, v, log_decay, cu_seqlens, ("state", state),
+                                                         ("final_state", final))
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(stream):
+        out = _kv4_out(out, q.shape[:-1] + (dv,), torch.bfloat16, q.device, "out")
+        if final is None and final_state:
+            final = torch.empty((B, Hkv, d, dv), dtype=torch.float32, device=q.device)
+        workspace, size = _linear_scratch(workspace, B, H, Hkv, L, packed, d, dv, index)
+    _check(load().attn_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, log_decay.data_ptr(), _ptr(state),
+                                  out.data_ptr(), _ptr(final), B, H, Hkv, L, d, dv, scale, _ptr(cu_seqlens),
+                                  _ptr(workspace), size, _stream(stream)))
+    return out, final
+
+
+def linear_backward(q, k, v, log_decay, dout, scale: float | None = None, cu_seqlens=None, state=None, dstate=None,
+                    workspace=None, dq=None, dk=None, dv=None, stream=None):
+    """dQ, dK, dV (bf16) and the gradient of `state` (fp32, None without one) of linear_forward for the gradients dout
+    of O and dstate of its final state (fp32 [B, Hkv, d, dv], None: zeros). The decay gets no gradient."""
+    packed = cu_seqlens is not None
+    B, H, Hkv, L, d, d_v, strides, index = _linear_inputs(q, k, v, log_decay, cu_seqlens, ("state", state),
+                                                          ("dstate", dstate))
+    Lo, dout_stride = _kv4_rows(dout, H, d_v, B, packed, "dout", index)
+    if Lo != L:
+        raise ValueError(f"q has {L} rows, dout {Lo}")
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(stream):
+        dq = _kv4_out(dq, q.shape, torch.bfloat16, q.device, "dq")
+        dk = _kv4_out(dk, k.shape, torch.bfloat16, q.device, "dk")
+        dv = _kv4_out(dv, v.shape, torch.bfloat16, q.device, "dv")
+        first = None if state is None else torch.empty_like(state)
+        workspace, size = _linear_scratch(workspace, B, H, Hkv, L, packed, d, d_v, index)
+    _check(load().attn_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), *strides, dout_stride,
+                                  log_decay.data_ptr(), _ptr(state), _ptr(dstate), dq.data_ptr(), dk.data_ptr(),
+                                  dv.data_ptr(), _ptr(first), B, H, Hkv, L, d, d_v, scale, _ptr(cu_seqlens),
+                                  _ptr(workspace), size, _stream(stream)))
+    return dq, dk, dv, first
+
+
+def linear_step(q, k, v, log_decay, state, scale: float | None = None, out=None, stream=None):
+    """linear_forward of one new token per sequence: q [B, H, d], k [B, Hkv, d], v [B, Hkv, dv] (rows may be strided).
+    state (fp32 [B, Hkv, d, dv]) is updated in place; returns O [B, H, dv]."""
+    device = q.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q, k and v must be [B, heads, channels], got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    (H, d), Hkv, dv = q.shape[1:], k.shape[1], v.shape[2]
+    B, q_stride = _kv4_rows(q, H, d, 1, True, "q", device)
+    Bk, k_stride = _kv4_rows(k, Hkv, d, 1, True, "k", device)
+    Bv, v_stride = _kv4_rows(v, Hkv, dv, 1, True, "v", device)
+    if Bk != B or Bv != B:
+        raise ValueError(f"q has {B} rows, k {Bk}, v {Bv}")
+    _linear_float("log_decay", log_decay, (Hkv,), device)
+    _linear_float("state", state, (B, Hkv, d, dv), device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(stream):
+        out = _kv4_out(out, (B, H, dv), torch.bfloat16, q.device, "out")
+    _check(load().attn_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
+                                   log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), B, H, Hkv, d, dv, scale,
+                                   _stream(stream)))
+    return out

@@ -15,6 +15,7 @@
 
 #include "kernels.h"
 #include "kv4.h"
+#include "linear.h"
 #include "ptx.cuh"
 #include "sched.cuh"
 
@@ -809,6 +810,166 @@ extern "C" int attn_kv4_evict(const attn_kv4_cache* cache, const int* page_table
     return ok();
 }
 
+// ---------------------------------------------------------------- linear attention
+namespace {
+
+int check_linear(int B, int H, int Hkv, int L, const int* cu, int d, int dv, float scale) {
+    if (B < 0 || L < 0) return fail(ATTN_ERR_ARG, "linear: bad sizes B=%d L=%d", B, L);
+    int rc = check_heads(H, Hkv);
+    if (rc) return rc;
+    if (d != 64 && d != 128 && d != 192 && d != 256)
+        return fail(ATTN_ERR_ARG, "head dim %d not supported (64, 128, 192, 256)", d);
+    if (dv != d && !(d == 192 && dv == 128))
+        return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (d_v = d, or d = 192 with d_v = 128)", d, dv);
+    if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_ARG, "scale must be finite and > 0");
+    if (cu && (B < 1 || B > kMaxVarlenBatch)) return fail(ATTN_ERR_ARG, "varlen: B must be in [1, %d]", kMaxVarlenBatch);
+    if ((cu ? (long)L : (long)B * L) >= (1L << 30)) return fail(ATTN_ERR_ARG, "too many rows");
+    return ATTN_OK;
+}
+
+// What the four products of linear attention share; the roles of the tensors come on top.
+int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, const float* log_decay, void* workspace,
+                  size_t ws_bytes, LinParams* p, bool* split) {
+    const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, d, dv);
+    if ((double)plan.segments * Hkv * ((d > dv ? d : dv) / 64) >= 2.0e9 || (double)B * Hkv * d * dv / 256 >= 2.0e9)
+        return fail(ATTN_ERR_ARG, "linear: too many sequences and heads");
+    const size_t need = plan.split ? (size_t)plan.segments * Hkv * d * dv * sizeof(float) : 0;
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    p->log_decay = log_decay;
+    p->states = static_cast<float*>(workspace);
+    p->cu = cu;
+    p->B = B;
+    p->rows = L;
+    p->total = cu ? L : B * L;
+    p->Hkv = Hkv;
+    p->per = H / Hkv;
+    p->seg_rows = plan.seg_rows;
+    p->segments = plan.segments;
+    p->init_mul = p->final_mul = 1.f;
+    p->status = di.status;
+    *split = plan.split;
+    return ATTN_OK;
+}
+
+const __nv_bfloat16* bf16(const void* x) { return static_cast<const __nv_bfloat16*>(x); }
+
+}  // namespace
+
+extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v) {
+    if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
+    if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
+    const LinPlan plan = lin_plan(B, Hkv, L, packed != 0, d, d_v);
+    return plan.split ? (size_t)plan.segments * Hkv * d * d_v * sizeof(float) : 0;
+}
+
+extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                               long long v_stride, const float* log_decay, const float* state, void* o, float* final_state,
+                               int B, int H, int Hkv, int L, int d, int d_v, float scale, const int* cu_seqlens,
+                               void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    int rc = check_linear(B, H, Hkv, L, cu_seqlens, d, d_v, scale);
+    if (rc) return rc;
+    const bool rows = (cu_seqlens ? (long)L : (long)B * L) > 0;
+    if (B == 0 || (!rows && !final_state)) return ok();
+    if (!log_decay || (rows && (!q || !k || !v || !o))) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state) || !aligned16(final_state))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if (rows && ((rc = check_stride("q", q_stride, (long long)H * d)) || (rc = check_stride("k", k_stride, (long long)Hkv * d)) ||
+                 (rc = check_stride("v", v_stride, (long long)Hkv * d_v))))
+        return rc;
+    LinParams p{};
+    bool split;
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, workspace, ws_bytes, &p, &split))) return rc;
+    p.a = bf16(q), p.b = bf16(k), p.c = bf16(v);
+    p.a_stride = (long)q_stride, p.b_stride = (long)k_stride, p.c_stride = (long)v_stride;
+    p.out = static_cast<__nv_bfloat16*>(o);
+    p.DK = d, p.DV = d_v;
+    p.init = state;
+    p.final = final_state;
+    p.out_mul = scale;
+    const cudaError_t e = launch_linear(p, split, false, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear forward launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, const void* dout, long long q_stride,
+                               long long k_stride, long long v_stride, long long dout_stride, const float* log_decay,
+                               const float* state, const float* dfinal, void* dq, void* dk, void* dv, float* dstate, int B,
+                               int H, int Hkv, int L, int d, int d_v, float scale, const int* cu_seqlens, void* workspace,
+                               size_t ws_bytes, cudaStream_t stream) {
+    int rc = check_linear(B, H, Hkv, L, cu_seqlens, d, d_v, scale);
+    if (rc) return rc;
+    const bool rows = (cu_seqlens ? (long)L : (long)B * L) > 0;
+    if (B == 0 || (!rows && !dstate)) return ok();
+    if (!log_decay || (rows && (!q || !k || !v || !dout || !dq || !dk || !dv))) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(dq) || !aligned16(dk) ||
+        !aligned16(dv) || !aligned16(state) || !aligned16(dfinal) || !aligned16(dstate))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if (rows && ((rc = check_stride("q", q_stride, (long long)H * d)) || (rc = check_stride("k", k_stride, (long long)Hkv * d)) ||
+                 (rc = check_stride("v", v_stride, (long long)Hkv * d_v)) ||
+                 (rc = check_stride("dout", dout_stride, (long long)H * d_v))))
+        return rc;
+    LinParams p{};
+    bool split;
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, workspace, ws_bytes, &p, &split))) return rc;
+    p.out_mul = scale;
+    cudaError_t e = cudaSuccess;
+    if (rows) {   // dq, forwards
+        p.a = bf16(dout), p.b = bf16(v), p.c = bf16(k);
+        p.a_stride = (long)dout_stride, p.b_stride = (long)v_stride, p.c_stride = (long)k_stride;
+        p.out = static_cast<__nv_bfloat16*>(dq);
+        p.DK = d_v, p.DV = d;
+        p.init = state;
+        p.init_trans = 1;
+        e = launch_linear(p, split, false, stream);
+    }
+    p.reverse = p.e = 1;
+    p.init = dfinal;
+    p.init_mul = 1.f / scale;
+    if (rows && e == cudaSuccess) {   // dk, backwards
+        p.a = bf16(v), p.b = bf16(dout), p.c = bf16(q);
+        p.a_stride = (long)v_stride, p.b_stride = (long)dout_stride, p.c_stride = (long)q_stride;
+        p.out = static_cast<__nv_bfloat16*>(dk);
+        e = launch_linear(p, split, true, stream);
+    }
+    if (e == cudaSuccess) {   // dv and the gradient of the first state (last: it may be dfinal's buffer)
+        p.a = bf16(k), p.b = bf16(q), p.c = bf16(dout);
+        p.a_stride = (long)k_stride, p.b_stride = (long)q_stride, p.c_stride = (long)dout_stride;
+        p.out = static_cast<__nv_bfloat16*>(dv);
+        p.DK = d, p.DV = d_v;
+        p.init_trans = 0;
+        p.final = dstate;
+        p.final_mul = scale;
+        e = launch_linear(p, split, true, stream);
+    }
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear backward launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int attn_linear_step(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                                long long v_stride, const float* log_decay, float* state, void* o, int B, int H, int Hkv,
+                                int d, int d_v, float scale, cudaStream_t stream) {
+    int rc = check_linear(B, H, Hkv, 1, nullptr, d, d_v, scale);
+    if (rc) return rc;
+    if (B == 0) return ok();
+    if ((double)B * Hkv * (d_v / 64) >= 2.0e9) return fail(ATTN_ERR_ARG, "linear: too many sequences and heads");
+    if (!q || !k || !v || !log_decay || !state || !o) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(o))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if ((rc = check_stride("q", q_stride, (long long)H * d)) || (rc = check_stride("k", k_stride, (long long)Hkv * d)) ||
+        (rc = check_stride("v", v_stride, (long long)Hkv * d_v)))
+        return rc;
+    const LinStepParams p{bf16(q), bf16(k), bf16(v), (long)q_stride, (long)k_stride, (long)v_stride, log_decay, state,
+                          static_cast<__nv_bfloat16*>(o), B, Hkv, H / Hkv, d, d_v, scale};
+    const cudaError_t e = launch_linear_step(p, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear step launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
 extern "C" int attn_set_backward_cta_pairs(int enable) { return g_bwd_pairs.exchange(enable ? 1 : 0); }
 
 extern "C" int attn_set_exp2_emulation(int d, int every) {
@@ -832,7 +993,7 @@ extern "C" int attn_check_status(cudaStream_t stream) {
         if (st == kStatusMisaligned)
             return fail(ATTN_ERR_LAUNCH, "dynamic shared memory was not 1024-byte aligned");
         if (st == kStatusBadPage)
-            return fail(ATTN_ERR_ARG, "4-bit cache: a page id, a cache length or a row offset was out of range");
+            return fail(ATTN_ERR_ARG, "a page id, a cache length or a row offset was out of range");
         return fail(ATTN_ERR_TIMEOUT, "a kernel gave up waiting (status %d)", st);
     }
     return ok();

@@ -427,6 +427,62 @@ int attn_kv4_evict(const attn_kv4_cache* cache, const int* page_table, int table
                    float* new_key_weights, long long new_weight_stride, cudaStream_t stream);
 
 /*
+ * Linear attention with a decay for each head. Per sequence and key/value head,
+ * with D = exp(log_decay) and a state S (d x d_v, fp32) in place of a cache:
+ *   S_t = D S_(t-1) + k_t v_t^T,   o_t = scale q_t^T S_t      (t = 1 .. n)
+ * that is o_t = scale (sum_{s <= t} D^(t-s) <q_t, k_s> v_s + D^t q_t^T S_0).
+ *   q, k, v   bf16 rows of H x d, Hkv x d and Hkv x d_v elements, their strides
+ *             (elements between rows, multiples of 8) of their own; o contiguous.
+ *             Head dims as in attn_fwd_ex (d_v = d, or 192 with 128). The H / Hkv
+ *             query heads of a group share a state and its decay.
+ *   rows      dense (cu_seqlens NULL: L rows for each of B sequences) or packed
+ *             (cu_seqlens int32 [B + 1] on the device, L rows in all, B <= 1024).
+ *             A sequence may have no rows: its state goes through as it is. Rows
+ *             past the last sequence are left as they are. Offsets out of range make an
+ *             empty sequence, and attn_check_status reports ATTN_ERR_ARG.
+ *   log_decay fp32 [Hkv] on the device, the natural logarithm; values above 0 count
+ *             as 0 (no decay), -infinity keeps the current token alone.
+ *   states    fp32 [B, Hkv, d, d_v]. state NULL: zeros. final_state NULL: not wanted; it
+ *             may be state's buffer.
+ * Within 64 tokens the products <q_t, k_s> D^(t-s), and the state before its product
+ * with q, are rounded to bf16; sums and states are fp32 to 2^-16. The rows of a
+ * sequence's 64-token chunks must be finite: an infinity or NaN in k or v spreads to
+ * all rows of its chunk, not only to the later ones.
+ * workspace: attn_linear_workspace_size(...) bytes (0: none needed, NULL will do),
+ * 256-byte aligned, used by one call at a time; its contents need not be
+ * initialised. The calls allocate nothing, use no atomics on data (results repeat bit for
+ * bit) and can be captured into a CUDA graph.
+ */
+size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v);
+int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride, long long v_stride,
+                    const float* log_decay, const float* state, void* o, float* final_state,
+                    int B, int H, int Hkv, int L, int d, int d_v, float scale, const int* cu_seqlens,
+                    void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Its backward for a loss whose gradients are dout (of o; bf16, rows of H x d_v,
+ * dout_stride apart) and dfinal (of the final state; fp32, NULL: zeros):
+ *   G_t = (D G_(t+1) or, for t = n, dfinal) + scale q_t dout_t^T,   dk_t = G_t v_t,
+ *   dv_t = G_t^T k_t,   dq_t = scale S_t dout_t,   dstate = D G_1
+ * (sums over the query heads of a group in G, dk, dv). Writes dq, dk, dv (bf16, contiguous) and
+ * dstate (fp32, the gradient of `state`; NULL: not wanted; it may be dfinal's or
+ * state's buffer). The decay is a constant of the model: it gets no gradient. Workspace as in the forward.
+ */
+int attn_linear_bwd(const void* q, const void* k, const void* v, const void* dout, long long q_stride, long long k_stride,
+                    long long v_stride, long long dout_stride, const float* log_decay, const float* state,
+                    const float* dfinal, void* dq, void* dk, void* dv, float* dstate,
+                    int B, int H, int Hkv, int L, int d, int d_v, float scale, const int* cu_seqlens,
+                    void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * One new token for each of B sequences: state is updated in place and o
+ * (bf16 [B, H, d_v]) written, all in fp32 up to o. q, k, v: one row per sequence.
+ */
+int attn_linear_step(const void* q, const void* k, const void* v, long long q_stride, long long k_stride, long long v_stride,
+                     const float* log_decay, float* state, void* o, int B, int H, int Hkv, int d, int d_v, float scale,
+                     cudaStream_t stream);
+
+/*
  * Partial emulation of the forward's exponentials (FlashAttention-4 paper,
  * Section 3.1.3, "partial emulation"; FA4 blog, "关键实现技术"): for head dim d
  * (64 or 128), `every` = 8 or 4 computes one score-column pair in every 8 or 4
