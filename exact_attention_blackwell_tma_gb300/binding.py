@@ -32,6 +32,12 @@ class _Kv4Struct(ctypes.Structure):
                 ("n_pages", c_int), ("Hkv", c_int), ("d", c_int), ("d_v", c_int)]
 
 
+class _PagedStruct(ctypes.Structure):
+    """attn_paged_cache of include/attn.h."""
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scales", c_void_p), ("v_scales", c_void_p),
+                ("n_pages", c_int), ("Hkv", c_int), ("d", c_int), ("d_v", c_int), ("bits", c_int)]
+
+
 class AttnError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"attn error {code}: {msg}")
@@ -96,6 +102,18 @@ def _declare(lib):
     lib.attn_kv4_evict.restype = c_int
     lib.attn_kv4_evict.argtypes = ([kv4, c_void_p, c_int, c_void_p, c_void_p, i64, c_void_p] + [c_int] * 5
                                    + [c_void_p] * 3 + [i64, c_void_p])
+    paged = ctypes.POINTER(_PagedStruct)
+    lib.attn_paged_append.restype = c_int
+    lib.attn_paged_append.argtypes = [c_void_p, c_void_p, i64, i64, paged, c_void_p, c_int, c_void_p, c_void_p, c_int,
+                                      c_int, c_void_p]
+    lib.attn_paged_read.restype = c_int
+    lib.attn_paged_read.argtypes = [c_void_p, c_void_p, paged, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                                    c_void_p]
+    lib.attn_paged_fwd_workspace_size.restype = c_size_t
+    lib.attn_paged_fwd_workspace_size.argtypes = [c_int] * 7
+    lib.attn_paged_fwd.restype = c_int
+    lib.attn_paged_fwd.argtypes = ([c_void_p, i64, paged, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p]
+                                   + [c_int] * 3 + [c_float] + [c_int] * 4 + [c_void_p, c_size_t, c_void_p])
     lib.attn_linear_workspace_size.restype = c_size_t
     lib.attn_linear_workspace_size.argtypes = [c_int] * 7
     lib.attn_linear_fwd.restype = c_int
@@ -324,6 +342,28 @@ def attn_kv4_evict(cache, page_table, table_width, cache_lens, key_weights, weig
     return load().attn_kv4_evict(cache, _ptr(page_table), table_width, _ptr(cache_lens), _ptr(key_weights),
                                  weight_stride, _ptr(new_table), new_width, B, budget, sinks, recent, _ptr(new_lens),
                                  _ptr(kept), _ptr(new_key_weights), new_weight_stride, _stream(stream))
+
+
+def attn_paged_append(k, v, k_stride, v_stride, cache, page_table, table_width, cache_lens, cu_seqlens, B, L,
+                      stream=None) -> int:
+    return load().attn_paged_append(_ptr(k), _ptr(v), k_stride, v_stride, cache, _ptr(page_table), table_width,
+                                    _ptr(cache_lens), _ptr(cu_seqlens), B, L, _stream(stream))
+
+
+def attn_paged_read(k, v, cache, page_table, table_width, cache_lens, cu_seqlens, B, L, stream=None) -> int:
+    return load().attn_paged_read(_ptr(k), _ptr(v), cache, _ptr(page_table), table_width, _ptr(cache_lens),
+                                  _ptr(cu_seqlens), B, L, _stream(stream))
+
+
+def attn_paged_fwd_workspace_size(B, H, Hkv, L, packed, d, d_v) -> int:
+    return load().attn_paged_fwd_workspace_size(B, H, Hkv, L, int(packed), d, d_v)
+
+
+def attn_paged_fwd(q, q_stride, cache, page_table, table_width, cache_lens, cu_seqlens, o, lse, B, H, L, scale, causal,
+                   window_left, window_right, sinks, workspace, ws_bytes, stream=None) -> int:
+    return load().attn_paged_fwd(_ptr(q), q_stride, cache, _ptr(page_table), table_width, _ptr(cache_lens),
+                                 _ptr(cu_seqlens), _ptr(o), _ptr(lse), B, H, L, scale, int(causal), int(window_left),
+                                 int(window_right), int(sinks), _ptr(workspace), ws_bytes, _stream(stream))
 
 
 def attn_linear_workspace_size(B, H, Hkv, L, packed, d, d_v) -> int:
@@ -714,6 +754,104 @@ def kv4_evict(cache, page_table, cache_lens, key_weights, new_table, budget: int
                                  B, budget, sinks, recent, new_lens.data_ptr(), kept.data_ptr(),
                                  new_key_weights.data_ptr(), columns, _stream(stream)))
     return new_lens, kept, new_key_weights
+
+
+# ---------------------------------------------------------------- the paged cache in bf16 or 8 bits
+
+PAGED_PAGE = 64   # tokens of a page
+
+
+class PagedCache:
+    """A paged key/value cache: k [pages, Hkv, 64, d] and v [pages, Hkv, 64, dv] in bf16, or in float8_e4m3fn with
+    uint8 exponents k_scales and v_scales [pages, Hkv, 64] (include/attn.h, attn_paged_cache)."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "n_pages", "Hkv", "d", "dv", "device", "_struct")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        shape, device, codes = k.shape, k.get_device(), k.dtype == torch.float8_e4m3fn
+        if (len(shape) != 4 or shape[2] != PAGED_PAGE or v.dim() != 4 or v.shape[:3] != shape[:3] or v.dtype != k.dtype
+                or not (codes or k.dtype == torch.bfloat16) or v.get_device() != device):
+            raise ValueError(f"a paged cache needs k and v [pages, heads, {PAGED_PAGE}, channels] in bf16 or float8_e4m3fn on "
+                             f"one device, got {k.dtype} {tuple(shape)} and {v.dtype} {tuple(v.shape)}")
+        scales = (k_scales, v_scales)
+        if codes:
+            for t in scales:
+                if t is None or t.dtype != torch.uint8 or t.shape != shape[:3] or t.get_device() != device:
+                    raise ValueError(f"an 8-bit cache needs uint8 k_scales and v_scales {tuple(shape[:3])} on its device")
+        elif scales != (None, None):
+            raise ValueError("a bf16 cache has no scales")
+        _check_tensors(k, v, k_scales, v_scales)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.n_pages, self.Hkv, self.d, self.dv = shape[0], shape[1], shape[3], v.shape[3]
+        self.device = device   # its index
+        self._struct = _PagedStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scales), _ptr(v_scales), self.n_pages, self.Hkv,
+                                    self.d, self.dv, 8 if codes else 16)
+
+    @classmethod
+    def empty(cls, n_pages, Hkv, d, dv=None, dtype=torch.bfloat16, device="cuda"):
+        """A cache of n_pages zeroed pages in bf16 or float8_e4m3fn."""
+        def rows(width):
+            return torch.zeros((n_pages, Hkv, PAGED_PAGE, width), dtype=dtype, device=device)
+
+        def scales():
+            if dtype != torch.float8_e4m3fn:
+                return None
+            return torch.ones((n_pages, Hkv, PAGED_PAGE), dtype=torch.uint8, device=device)
+        return cls(rows(d), rows(d if dv is None else dv), scales(), scales())
+
+
+_paged_workspace = functools.lru_cache(maxsize=4096)(attn_paged_fwd_workspace_size)   # a function of the sizes alone
+
+
+def paged_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=None):
+    """Write new keys and values (bf16 [T, Hkv, d] with int32 cu_seqlens, or [B, L, Hkv, d]) into the pages of their
+    sequences, quantised if the cache is in 8 bits. Lengths and strides as in kv4_append()."""
+    B, device = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    L, k_stride = _kv4_rows(k, cache.Hkv, cache.d, B, cu_seqlens is not None, "k", device)
+    Lv, v_stride = _kv4_rows(v, cache.Hkv, cache.dv, B, cu_seqlens is not None, "v", device)
+    if L != Lv:
+        raise ValueError(f"k has {L} rows, v {Lv}")
+    _check(load().attn_paged_append(k.data_ptr(), v.data_ptr(), k_stride, v_stride, cache._struct, page_table.data_ptr(),
+                                    page_table.shape[1], cache_lens.data_ptr(), _ptr(cu_seqlens), B, L, _stream(stream)))
+
+
+def paged_read(cache, page_table, cache_lens, rows, cu_seqlens=None, k=None, v=None, stream=None):
+    """K, V in bf16 as the cache stands for them: the last rows of every sequence, as kv4_read() gives them."""
+    B, _ = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    device, heads = cache.k.device, cache.Hkv
+    packed = cu_seqlens is not None
+    with _on(stream):
+        k = _kv4_out(k, (rows, heads, cache.d) if packed else (B, rows, heads, cache.d), torch.bfloat16, device, "k")
+        v = _kv4_out(v, (rows, heads, cache.dv) if packed else (B, rows, heads, cache.dv), torch.bfloat16, device, "v")
+    _check(load().attn_paged_read(k.data_ptr(), v.data_ptr(), cache._struct, page_table.data_ptr(), page_table.shape[1],
+                                  cache_lens.data_ptr(), _ptr(cu_seqlens), B, rows, _stream(stream)))
+    return k, v
+
+
+def paged_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: float | None = None, cu_seqlens=None,
+                  window=(-1, -1), sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """O, LSE of new tokens q (bf16 [T, H, d] with cu_seqlens, or [B, L, H, d]) over their sequence's cache, to which
+    their keys have been appended. window and sinks as in forward()."""
+    B, index = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    _check_ints(window[0], window[1], sinks)
+    H, packed, device = q.shape[-2], cu_seqlens is not None, q.device
+    L, q_stride = _kv4_rows(q, H, cache.d, B, packed, "q", index)
+    if H % cache.Hkv != 0 or H == 0:
+        raise ValueError(f"{H} query heads over {cache.Hkv} key/value heads")
+    scale = 1.0 / math.sqrt(cache.d) if scale is None else scale
+    need = _paged_workspace(B, H, cache.Hkv, L, packed, cache.d, cache.dv)
+    with _on(stream):
+        out = _kv4_out(out, (L, H, cache.dv) if packed else (B, L, H, cache.dv), torch.bfloat16, device, "out")
+        lse = _kv4_out(lse, (H, L) if packed else (B, H, L), torch.float32, device, "lse")
+        if workspace is None:
+            workspace, size = torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
+        else:
+            _check_workspace(workspace, index)
+            size = workspace.numel() * workspace.element_size()
+    _check(load().attn_paged_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), page_table.shape[1],
+                                 cache_lens.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr(), B, H, L, scale,
+                                 int(causal), window[0], window[1], sinks, workspace.data_ptr(), size, _stream(stream)))
+    return out, lse
 
 
 # ---------------------------------------------------------------- linear attention with a decay per head

@@ -20,10 +20,12 @@ BUILD = os.path.join(PKG, "_build")
 
 LIBS = {
     "libattn.so": ["api.cu", "fwd.cu", "fwd_wide.cu", "bwd.cu", "bwd_wide.cu", "bwd_pair.cu",
-                   "kv4.cu", "kv4_fwd.cu", "linear.cu"],
+                   "kv4.cu", "kv4_fwd.cu", "linear.cu",
+                   "paged.cu", "paged_fwd.cu"],
     "libattn_selftest.so": ["selftest.cu"],
 }
-HEADERS = ["ptx.cuh", "sched.cuh", "kernels.h", "mask.cuh", "dq_order.cuh", "dq_reduce.cuh", "kv4.h", "linear.h"]
+HEADERS = ["ptx.cuh", "sched.cuh", "kernels.h", "mask.cuh", "dq_order.cuh", "dq_reduce.cuh", "kv4.h", "linear.h", "paged.h",
+           "paged_work.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

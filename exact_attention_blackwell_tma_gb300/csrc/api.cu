@@ -16,6 +16,7 @@
 #include "kernels.h"
 #include "kv4.h"
 #include "linear.h"
+#include "paged.h"
 #include "ptx.cuh"
 #include "sched.cuh"
 
@@ -616,30 +617,37 @@ extern "C" int attn_bwd_noalloc(const void* q, const void* k, const void* v, con
 // ---------------------------------------------------------------- the 4-bit key/value cache
 namespace {
 
+// The sizes of a call on a paged cache; what its cache holds is checked by the caller.
+int check_pages(const char* what, int n_pages, int Hkv, int d, int dv, int B, int L, const int* table, int width,
+                const int* lens, const int* cu, Kv4Batch* batch) {
+    if (B < 0 || L < 0 || Hkv < 1 || Hkv > 65535 || n_pages < 1 || width < 1)
+        return fail(ATTN_ERR_ARG, "%s: bad sizes B=%d L=%d Hkv=%d pages=%d table width=%d", what, B, L, Hkv, n_pages, width);
+    if (B > kKv4MaxBatch) return fail(ATTN_ERR_ARG, "%s: B must be in [0, %d]", what, kKv4MaxBatch);
+    if (d != 64 && d != 128 && d != 192 && d != 256)
+        return fail(ATTN_ERR_ARG, "head dim %d not supported (64, 128, 192, 256)", d);
+    if (dv != d && !(d == 192 && dv == 128))
+        return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (d_v = d, or d = 192 with d_v = 128)", d, dv);
+    // (tokens and rows below 2^30: a row's position plus a window bound stays an int)
+    if ((long)width * kPage >= (1L << 30)) return fail(ATTN_ERR_ARG, "%s: table width %d too large", what, width);
+    const long total = cu ? (long)L : (long)B * L;
+    if (total >= (1L << 30)) return fail(ATTN_ERR_ARG, "too many rows");
+    if (B > 0 && (!table || !lens)) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    *batch = Kv4Batch{table, lens, cu, B, width, L, (int)total};
+    return ATTN_OK;
+}
+
 int check_kv4(const attn_kv4_cache* c, int B, int L, const int* table, int width, const int* lens, const int* cu,
               Kv4Cache* cache, Kv4Batch* batch) {
     if (!c) return fail(ATTN_ERR_ARG, "kv4: null cache");
-    if (B < 0 || L < 0 || c->Hkv < 1 || c->Hkv > 65535 || c->n_pages < 1 || width < 1)
-        return fail(ATTN_ERR_ARG, "kv4: bad sizes B=%d L=%d Hkv=%d pages=%d table width=%d", B, L, c->Hkv, c->n_pages,
-                    width);
-    if (B > kKv4MaxBatch) return fail(ATTN_ERR_ARG, "kv4: B must be in [0, %d]", kKv4MaxBatch);
-    if (c->d != 64 && c->d != 128 && c->d != 192 && c->d != 256)
-        return fail(ATTN_ERR_ARG, "head dim %d not supported (64, 128, 192, 256)", c->d);
-    if (c->d_v != c->d && !(c->d == 192 && c->d_v == 128))
-        return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (d_v = d, or d = 192 with d_v = 128)", c->d,
-                    c->d_v);
-    // (tokens and rows below 2^30: a row's position plus a window bound stays an int)
-    if ((long)width * kPage >= (1L << 30)) return fail(ATTN_ERR_ARG, "kv4: table width %d too large", width);
-    const long total = cu ? (long)L : (long)B * L;
-    if (total >= (1L << 30)) return fail(ATTN_ERR_ARG, "too many rows");
-    if (B > 0 && (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params || !table || !lens))
+    int rc = check_pages("kv4", c->n_pages, c->Hkv, c->d, c->d_v, B, L, table, width, lens, cu, batch);
+    if (rc) return rc;
+    if (B > 0 && (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params))
         return fail(ATTN_ERR_ARG, "null tensor pointer");
     if (!aligned16(c->k_codes) || !aligned16(c->k_params) || !aligned16(c->v_codes) || !aligned16(c->v_params))
         return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
     *cache = Kv4Cache{static_cast<unsigned char*>(c->k_codes), static_cast<unsigned*>(c->k_params),
                       static_cast<unsigned char*>(c->v_codes), static_cast<unsigned*>(c->v_params),
                       c->n_pages, c->Hkv, c->d, c->d_v};
-    *batch = Kv4Batch{table, lens, cu, B, width, L, (int)total};
     return ATTN_OK;
 }
 
@@ -967,6 +975,121 @@ extern "C" int attn_linear_step(const void* q, const void* k, const void* v, lon
                           static_cast<__nv_bfloat16*>(o), B, Hkv, H / Hkv, d, d_v, scale};
     const cudaError_t e = launch_linear_step(p, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear step launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+// ---------------------------------------------------------------- the paged cache in bf16 or 8 bits
+namespace {
+
+int check_paged(const attn_paged_cache* c, int B, int L, const int* table, int width, const int* lens, const int* cu,
+                PagedCache* cache, Kv4Batch* batch) {
+    if (!c) return fail(ATTN_ERR_ARG, "paged: null cache");
+    if (c->bits != 16 && c->bits != 8) return fail(ATTN_ERR_ARG, "paged: %d bits not supported (16: bf16, 8: e4m3)", c->bits);
+    int rc = check_pages("paged", c->n_pages, c->Hkv, c->d, c->d_v, B, L, table, width, lens, cu, batch);
+    if (rc) return rc;
+    if (B > 0 && (!c->k || !c->v || (c->bits == 8 && (!c->k_scales || !c->v_scales))))
+        return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(c->k) || !aligned16(c->v) || (c->bits == 8 && (!aligned16(c->k_scales) || !aligned16(c->v_scales))))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    *cache = PagedCache{static_cast<unsigned char*>(c->k), static_cast<unsigned char*>(c->v),
+                        static_cast<unsigned char*>(c->k_scales), static_cast<unsigned char*>(c->v_scales),
+                        c->n_pages, c->Hkv, c->d, c->d_v};
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int attn_paged_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                                 const attn_paged_cache* cache, const int* page_table, int table_width,
+                                 const int* cache_lens, const int* cu_seqlens, int B, int L, cudaStream_t stream) {
+    PagedCache c;
+    Kv4Batch s;
+    int rc = check_paged(cache, B, L, page_table, table_width, cache_lens, cu_seqlens, &c, &s);
+    if (rc) return rc;
+    if (B == 0 || s.total == 0) return ok();
+    if (!k || !v) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if ((rc = check_stride("k", k_stride, (long long)c.Hkv * c.d))) return rc;
+    if ((rc = check_stride("v", v_stride, (long long)c.Hkv * c.dv))) return rc;
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    const cudaError_t e = launch_paged_append(c, cache->bits == 8, s, bf16(k), bf16(v), (long)k_stride, (long)v_stride,
+                                              di.status, di.sms, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "paged append launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int attn_paged_read(void* k, void* v, const attn_paged_cache* cache, const int* page_table, int table_width,
+                               const int* cache_lens, const int* cu_seqlens, int B, int L, cudaStream_t stream) {
+    PagedCache c;
+    Kv4Batch s;
+    int rc = check_paged(cache, B, L, page_table, table_width, cache_lens, cu_seqlens, &c, &s);
+    if (rc) return rc;
+    if (B == 0 || s.total == 0) return ok();
+    if (!k || !v) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    const cudaError_t e = launch_paged_read(c, cache->bits == 8, s, static_cast<__nv_bfloat16*>(k),
+                                            static_cast<__nv_bfloat16*>(v), di.status, di.sms, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "paged read launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" size_t attn_paged_fwd_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v) {
+    if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d <= 0 || d_v <= 0) return 0;
+    const long total = packed ? (long)L : (long)B * L;
+    if (total >= (1L << 30)) return 0;
+    return kv4_layout(B, H, Hkv, total, 1, d, d_v, false).total;
+}
+
+extern "C" int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* cache, const int* page_table,
+                              int table_width, const int* cache_lens, const int* cu_seqlens, void* o, float* lse, int B,
+                              int H, int L, float scale, int causal, int window_left, int window_right, int sinks,
+                              void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    PagedFwdParams p{};
+    int rc = check_paged(cache, B, L, page_table, table_width, cache_lens, cu_seqlens, &p.c, &p.s);
+    if (rc) return rc;
+    if ((rc = check_heads(H, p.c.Hkv))) return rc;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_ARG, "scale must be finite and > 0");
+    if ((rc = check_window(window_left, window_right, sinks))) return rc;
+    if (B == 0 || p.s.total == 0) return ok();
+    const int group = H / p.c.Hkv;
+    const int nr = kv4_row_tiles(group, B, p.s.total);
+    // the work list counts pages of row blocks in an int
+    const double units = ((double)p.s.total * group / (8 * nr) + B) * table_width * p.c.Hkv;
+    if ((double)p.s.total * H >= 2.0e9) return fail(ATTN_ERR_ARG, "too many rows");
+    if (units >= (double)kKv4MostUnits) return fail(ATTN_ERR_ARG, "paged: too many (row block, page) pairs");
+    if (!q || !o || !lse) return fail(ATTN_ERR_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse))
+        return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+    if ((rc = check_stride("q", q_stride, (long long)H * p.c.d))) return rc;
+    const Kv4Workspace wl = kv4_layout(B, H, p.c.Hkv, p.s.total, 1, p.c.d, p.c.dv, false);
+    if (!workspace || ws_bytes < wl.total)
+        return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total, ws_bytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    char* ws = static_cast<char*>(workspace);
+    p.q = bf16(q);
+    p.q_stride = (long)q_stride;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.H = H;
+    p.group = group;
+    // (bounds past any cache change nothing; clamped so the index arithmetic cannot overflow)
+    const int most = table_width * kPage > p.s.total ? table_width * kPage : p.s.total;
+    p.win_left = window_left < most ? window_left : most;
+    p.win_right = causal ? 0 : (window_right < most ? window_right : most);
+    p.sinks = window_left < 0 ? 0 : (sinks < most ? sinks : most);
+    p.scale_log2 = scale * kLog2e;
+    p.prefix = reinterpret_cast<int*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + wl.ml);
+    p.part_o = reinterpret_cast<float*>(ws + wl.part);
+    p.status = di.status;
+    const cudaError_t e = launch_paged_fwd(p, cache->bits == 8, di.sms, stream);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "paged forward launch failed: %s", cudaGetErrorString(e));
     return ok();
 }
 

@@ -8,8 +8,6 @@
 namespace attn {
 namespace {
 
-__device__ __forceinline__ void bad_page(int* status) { atomicCAS(status, kStatusOk, kStatusBadPage); }
-
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {   // of two bf16 each
     uint32_t r;
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -85,30 +83,6 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float lo, floa
     return codes;
 }
 
-// Where a packed row lives: its page and slot, or page -1: nowhere (out of
-// range, reported), -2: no such row (past the last sequence), -3: before the
-// sequence's first token (a padded dense batch).
-struct RowPlace {
-    int page, slot;
-};
-__device__ __forceinline__ RowPlace place_of(const Kv4Cache& c, const Kv4Batch& s, int t, int* status) {
-    RowPlace r{-2, 0};
-    if (t >= s.total) return r;
-    const int b = kv4_seq_of_row(s, t);
-    if (b < 0) return r;
-    const Kv4Seq q = kv4_seq(s, b);
-    const int slot = q.lk - q.nq + t - q.q0;
-    r.page = -1;
-    if (!q.bad && slot < 0) r.page = -3;
-    if (!q.bad && slot >= 0) {
-        r.slot = slot % kPage;
-        r.page = s.table[(long)b * s.width + slot / kPage];
-        if (r.page < 0 || r.page >= c.n_pages) r.page = -1;
-    }
-    if (r.page == -1) bad_page(status);
-    return r;
-}
-
 // A warp takes `rows` (1 to 4) consecutive rows, whose places its first lanes
 // look up together, and walks their groups of 64 channels four at a time, eight
 // lanes per group: 16 bytes of bf16 and 4 bytes of codes per lane, the extremes
@@ -121,7 +95,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4Cache c, Kv4Batch s,
     const int t0 = (blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * rows;
     RowPlace mine{-2, 0};
     if (lane < rows) {
-        mine = place_of(c, s, t0 + lane, status);
+        mine = place_of(c.n_pages, s, t0 + lane, status);
         if (mine.page == -3) bad_page(status);   // more new rows than the cache holds tokens
     }
     const int chunks = c.Hkv * (GK + GV);
@@ -178,7 +152,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Cache c, Kv4Batch s, _
     const int lane = threadIdx.x & 31, l8 = lane & 7;
     const int t0 = (blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * rows;
     RowPlace mine{-2, 0};
-    if (lane < rows) mine = place_of(c, s, t0 + lane, status);
+    if (lane < rows) mine = place_of(c.n_pages, s, t0 + lane, status);
     const int chunks = c.Hkv * (GK + GV);
     for (int x = 0; x < rows; ++x) {
         const int page = __shfl_sync(kFullMask, mine.page, x), slot = __shfl_sync(kFullMask, mine.slot, x);

@@ -14,6 +14,7 @@
 
 #include "kernels.h"
 #include "mask.cuh"
+#include "ptx.cuh"
 
 namespace attn {
 
@@ -147,6 +148,31 @@ __device__ __forceinline__ int kv4_seq_of_row(const Kv4Batch& s, int t) {
         else hi = mid - 1;
     }
     return t < s.cu[lo + 1] ? lo : -1;   // (offsets that do not ascend: no sequence)
+}
+__device__ __forceinline__ void bad_page(int* status) { atomicCAS(status, kStatusOk, kStatusBadPage); }
+
+// Where a packed row lives: its page and slot, or page -1: nowhere (out of
+// range, reported), -2: no such row (past the last sequence), -3: before the
+// sequence's first token (a padded dense batch).
+struct RowPlace {
+    int page, slot;
+};
+__device__ __forceinline__ RowPlace place_of(int n_pages, const Kv4Batch& s, int t, int* status) {
+    RowPlace r{-2, 0};
+    if (t >= s.total) return r;
+    const int b = kv4_seq_of_row(s, t);
+    if (b < 0) return r;
+    const Kv4Seq q = kv4_seq(s, b);
+    const int slot = q.lk - q.nq + t - q.q0;
+    r.page = -1;
+    if (!q.bad && slot < 0) r.page = -3;
+    if (!q.bad && slot >= 0) {
+        r.slot = slot % kPage;
+        r.page = s.table[(long)b * s.width + slot / kPage];
+        if (r.page < 0 || r.page >= n_pages) r.page = -1;
+    }
+    if (r.page == -1) bad_page(status);
+    return r;
 }
 #endif
 

@@ -1,0 +1,46 @@
+// The paged key/value cache in bf16 or 8 bits: its layout and the launchers of its kernels.
+//
+// Pages of 64 tokens, [pages][Hkv][64][channels] for K (d) and V (dv), in bf16 or in
+// e4m3. With e4m3, bytes e [pages][Hkv][64] give each token and head a scale of
+// 2^(e - 127) for its codes, e from 1 up (255: the row held an infinity or a NaN,
+// its codes are 0). A power of two costs a code that has an exponent of its own
+// nothing, and makes quantising exact up to the one rounding of the code.
+// Batches (tables, lengths, rows) are those of the 4-bit cache.
+#pragma once
+
+#include "kv4.h"
+
+namespace attn {
+
+struct PagedCache {
+    unsigned char* k;          // bf16 or e4m3 rows, by `bits`
+    unsigned char* v;
+    unsigned char* k_scales;   // (8 bits)
+    unsigned char* v_scales;
+    int n_pages, Hkv, d, dv;
+};
+
+struct PagedFwdParams {
+    PagedCache c;
+    Kv4Batch s;
+    const __nv_bfloat16* q;
+    long q_stride;             // elements between tokens of q
+    __nv_bfloat16* o;
+    float* lse;
+    int H, group;
+    int win_left, win_right, sinks;
+    float scale_log2;
+    int* prefix;               // workspace: as in Kv4FwdParams
+    float* part_ml;
+    float* part_o;
+    int* status;
+};
+
+cudaError_t launch_paged_append(const PagedCache& c, bool codes, const Kv4Batch& s, const __nv_bfloat16* k,
+                                const __nv_bfloat16* v, long k_stride, long v_stride, int* status, int num_sms,
+                                cudaStream_t stream);
+cudaError_t launch_paged_read(const PagedCache& c, bool codes, const Kv4Batch& s, __nv_bfloat16* k, __nv_bfloat16* v,
+                              int* status, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_fwd(const PagedFwdParams& p, bool codes, int num_sms, cudaStream_t stream);
+
+}  // namespace attn

@@ -1,0 +1,612 @@
+// Attention of a few new tokens per sequence over the paged cache in bf16 or 8 bits.
+//
+// Mathematics. s_ij = scale <q_i, k_j>, O_i = sum_j p_ij v_j with p = exp(s - LSE), in one
+// pass over the keys: a running maximum (moved when a row's grows by more than
+// 2^kPagedTau) and sum per row, in fp32, as are all accumulators. With 8 bits k_j = 2^e c_j
+// with codes c_j: the power enters the score in fp32, and that of v_j enters p
+// before p's rounding to bf16, which it does not change (bf16 has fp32's exponents).
+//
+// What bounds it: the cache is read once. As in the 4-bit kernel, keys (channels for PV)
+// take the M side of mma.sync m16n8k16 and the query rows the N side,
+//   S^T[key, row] = K[key, ch] q^T[ch, row],   O^T[ch, row] += V^T[ch, key] P^T[key, row],
+// which pads a handful of rows to 8 (a tcgen05 tile: to 64 or 128 on its M side, and on
+// its N side it would write S to tensor memory and read it back for every 128 keys).
+// bf16 operands come by ldmatrix. Codes: a byte seeeemmm in the upper half of a 16-bit
+// lane, its exponent and mantissa moved down by four, is the bf16 c 2^-120, subnormal codes
+// included (the bf16 is subnormal too): a shift and two logic operations per pair, no
+// conversions, which have a fraction of the rate. K's 2^120 goes into q and the score; V's
+// is one multiplication per pair, as p 2^(e - 120) could leave the range.
+//
+// Work: paged_work.cuh. Each of four warps takes 32 of a unit's 128 tokens in steps of
+// kTok, with statistics and a ring of asynchronous copies of its own.
+#include <type_traits>
+
+#include "paged.h"
+#include "paged_work.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4, kPagedThreads = 32 * kWarps;
+constexpr float kPagedTau = 8.f;   // a row's max moves when it grows by more (log2 units)
+// p is held 2^16 times smaller than exp(s - max), so that sums of p v stay finite for any N
+// keys with N max|v| below 2^136; at the other end p times V's scale is a normal bf16 for
+// scales from 2^-102 up (and p within 2^-8 of its row's largest).
+constexpr float kPagedShift = 16.f;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint16_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 ldsm4(uint32_t a) {
+    uint4 r;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 ldsm4t(uint32_t a) {
+    uint4 r;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    return r;
+}
+// 16 bytes to shared memory past L1, the first `bytes` of them from memory, zeros behind
+__device__ __forceinline__ void copy16n(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+// codes in the upper bytes of both halves: the bf16 pair c 2^-120
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) { return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u); }
+__device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+    return r;
+}
+
+// Rows of `bytes` in shared memory, kTok tokens: panels of 128 bytes a row (and one of 64
+// behind them where they do not divide), their 16-byte pieces permuted by the token so
+// that neither eight tokens of one piece (ldmatrix) nor a warp's reads of codes (tokens t and
+// t + 4 together in QK; tokens t, two pieces each, in PV) meet in a bank.
+template <int kBytes, int kTok>
+__device__ __forceinline__ uint32_t row_piece(uint32_t base, int tok, int piece) {
+    constexpr int kFull = kBytes / 128;
+    if (kBytes % 128 == 0 || piece < 8 * kFull) {
+        const int sw = ((tok & 3) << 1) ^ ((tok & 4) ? 5 : 0);
+        return base + (piece >> 3) * (kTok * 128) + tok * 128 + (((piece & 7) ^ sw) << 4);
+    }
+    const int slot = ((tok >> 2) & 1) * 4 + (piece & 3), line = (tok & 3) + 4 * (tok >> 3);
+    return base + kFull * (kTok * 128) + line * 128 + ((slot ^ ((tok & 3) << 1)) << 4);
+}
+
+template <bool kCodes, int D, int DV, int NR>
+struct PagedLayout {
+    static constexpr int kRows = 8 * NR, kElt = kCodes ? 1 : 2;
+    static constexpr int kKRow = D * kElt, kVRow = DV * kElt;
+    // a slot: kTok tokens, about 8 KB, so that a warp's copies in flight cover the latency
+    static constexpr int kTok = 32 * (kKRow + kVRow) <= 8192 ? 32 : 16, kSteps = 32 / kTok;   // steps per unit
+    static constexpr int kVOff = kTok * kKRow, kKsOff = kVOff + kTok * kVRow, kVsOff = kKsOff + kTok;
+    static constexpr int kSlot = kVOff + kTok * kVRow + (kCodes ? 128 : 0);   // (scales padded to a line)
+    static constexpr int kSlots = 3;
+    static constexpr int kQOff = kWarps * kSlots * kSlot;          // q fragments [NR][D / 32][32 lanes] x 16 bytes
+    static constexpr int kQExpOff = kQOff + NR * (D / 32) * 512;   // row exponents of q
+    static constexpr int kKeysOff = kQExpOff + kRows * 4;
+    static constexpr int kMlOff = kKeysOff + kRows * 8;
+    static constexpr int kPrefixOff = (kMlOff + kWarps * kRows * 8 + 15) / 16 * 16;
+    static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
+    static constexpr int smem(int B) { return kPrefixOff + (2 * B + 1) * 4; }
+    static constexpr int kRegCtas = NR * DV <= 128 ? 4 : (NR * DV <= 256 ? 3 : 2);
+    static constexpr int kSmemCtas = 227 * 1024 / (smem(64) + 1024);
+    static constexpr int kCtas = kRegCtas < kSmemCtas ? kRegCtas : kSmemCtas;
+    static_assert(kCtas >= 1 && smem(kKv4MaxBatch) <= 227 * 1024, "shared memory budget");
+};
+
+template <bool kCodes, int D, int DV, int NR>
+__global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>::kCtas) paged_fwd_kernel(const PagedFwdParams p) {
+    using Lay = PagedLayout<kCodes, D, DV, NR>;
+    constexpr int S = Lay::kSlots, kRows = Lay::kRows, kTok = Lay::kTok, CK = kTok / 16, kSteps = Lay::kSteps;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* prefix = reinterpret_cast<int*>(smem + Lay::kPrefixOff);
+    const uint32_t ring = base + warp * S * Lay::kSlot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the finishing kernel waits for this grid's end)
+    const Cut cut = build_prefix<kPagedThreads>(p, prefix, prefix + p.s.B + 1, kRows, gridDim.x);   // (ends with __syncthreads)
+    const int per = cut.per;
+    const int total = prefix[p.s.B];
+    if (blockIdx.x == 0) {   // for the kernel that follows
+        for (int i = tid; i <= p.s.B; i += kPagedThreads) p.prefix[i] = prefix[i];
+        if (tid == 0) {
+            p.prefix[kKv4MaxBatch + 1] = per;
+            p.prefix[kKv4MaxBatch + 2] = cut.aligned;
+        }
+    }
+    const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
+    const int g8 = lane >> 2, t4 = lane & 3, half = warp & 1;
+    // the tokens of S^T's rows g8 and g8 + 8 of a chunk: with codes, row 2 t + e + 8 h is token t + 4 e + 8 h
+    const int tok0 = kCodes ? (g8 >> 1) + 4 * (g8 & 1) : g8;
+    float acc[DV / 16][NR][4];
+    float qscale[NR][2], m_run[NR][2], mu[NR][2], l_run[NR][2];   // m_run: the max plus the shift; mu: it, or 0
+    int2* row_keys = reinterpret_cast<int2*>(smem + Lay::kKeysOff);
+    int* q_exp = reinterpret_cast<int*>(smem + Lay::kQExpOff);
+    float2* ml = reinterpret_cast<float2*>(smem + Lay::kMlOff);
+    for (int u = u0; u < u1;) {
+        // ------------------------------------------------ a row block (this CTA's share of it): units i0 .. i1 - 1
+        SeqWork w;
+        const Unit t = unit_at(p, prefix, cut, u, kRows, &w);
+        const int i0 = t.i, i1 = min(w.units, i0 + u1 - u);
+        u += min(cut.span(w.units) - i0, u1 - u);   // (with its padding)
+        // this warp's pages: index 2 i + warp / 2; lane l holds the id of the unit l % 16 of the current
+        // sixteen, and of the next sixteen
+        const int* table = p.s.table + (long)t.b * p.s.width;
+        auto page_id = [&](int i) {
+            const int x = 2 * i + (warp >> 1);
+            if (i >= i1 || x >= w.pages) return -2;   // no such page
+            const int id = table[page_of(w, x)];
+            if (id >= 0 && id < p.c.n_pages) return id;
+            atomicCAS(p.status, kStatusOk, kStatusBadPage);
+            return -1;
+        };
+        int ids = 0, ids_next = page_id(i0 + (lane & 15));
+        uint32_t live = 0;   // bit (i - i0) % 32: unit i's page is in range
+        uint32_t slot_in = 0, slot_out = 0;
+        auto issue = [&](int n) {   // the copies of step n (0, 1, 2, ...) of this share into the next slot
+            const int x = n / kSteps, i = i0 + x, part = n % kSteps;
+            if (i < i1) {
+                if (part == 0 && (x & 15) == 0) {
+                    ids = ids_next;
+                    ids_next = page_id(i + 16 + (lane & 15));
+                    const uint32_t in = __ballot_sync(kFullMask, ids >= 0) & 0xffffu;
+                    live = (live & (0xffff0000u >> (x & 16))) | in << (x & 16);
+                }
+                const int id = __shfl_sync(kFullMask, ids, x & 15);
+                if (id >= 0) {
+                    const int tok = 32 * half + part * kTok;   // of the page
+                    const int left = w.s.lk - page_of(w, 2 * i + (warp >> 1)) * kPage - tok;   // tokens that exist: what
+                    const long row0 = ((long)id * p.c.Hkv + t.h) * kPage + tok;                // lies behind may be anything
+                    const unsigned char *k = p.c.k + row0 * Lay::kKRow, *v = p.c.v + row0 * Lay::kVRow;
+                    const uint32_t st = ring + slot_in;
+                    constexpr int kKP = Lay::kKRow / 16, kVP = Lay::kVRow / 16;   // pieces of a row
+#pragma unroll
+                    for (int y = 0; y < kTok * kKP / 32; ++y) {
+                        const int z = y * 32 + lane, r = z / kKP, c = z % kKP;
+                        copy16n(row_piece<Lay::kKRow, kTok>(st, r, c), k + z * 16, r < left ? 16 : 0);
+                    }
+#pragma unroll
+                    for (int y = 0; y < kTok * kVP / 32; ++y) {
+                        const int z = y * 32 + lane, r = z / kVP, c = z % kVP;
+                        copy16n(row_piece<Lay::kVRow, kTok>(st + Lay::kVOff, r, c), v + z * 16, r < left ? 16 : 0);
+                    }
+                    if (kCodes && lane < 2 * CK) {
+                        const int c = lane % CK;
+                        copy16n(st + (lane < CK ? Lay::kKsOff : Lay::kVsOff) + c * 16,
+                                (lane < CK ? p.c.k_scales : p.c.v_scales) + row0 + c * 16, min(max(left - c * 16, 0), 16));
+                    }
+                }
+                slot_in = slot_in == (S - 1) * Lay::kSlot ? 0 : slot_in + Lay::kSlot;
+            }
+            copy_commit();
+        };
+#pragma unroll
+        for (int x = 0; x < S - 1; ++x) issue(x);
+        // ------------------------------------------------ its queries
+        const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
+        if (tid < kRows) {
+            const int row = t.rb * kRows + tid, i = row / p.group;
+            row_keys[tid] = row < w.rows ? make_int2(band_key_lo(mb, i), band_key_hi(mb, i)) : make_int2(0, 0);
+        }
+        auto q_row = [&](int r) {   // row r of the block, or null
+            r += t.rb * kRows;
+            return r < w.rows ? p.q + (long)(w.s.q0 + r / p.group) * p.q_stride + (long)(t.h * p.group + r % p.group) * D : nullptr;
+        };
+        if constexpr (kCodes) {   // row r times 2^e has its largest element in [2^60, 2^61) (its own exponent per row)
+            for (int r = warp; r < kRows; r += kWarps) {
+                const __nv_bfloat16* src = q_row(r);
+                uint32_t m = 0;
+                if (src) {
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) m = __vmaxu2(m, reinterpret_cast<const uint32_t*>(src)[x * 32 + lane] & 0x7fff7fffu);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, o));
+                const int top = (int)(max(m & 0xffffu, m >> 16) >> 7);   // (biased; 255: an infinity or a NaN)
+                if (lane == 0) q_exp[r] = top == 255 ? 0 : min(max(60 - (top - 127), -6), 120);
+            }
+            __syncthreads();
+        }
+        for (int task = warp; task < NR * (D / 32); task += kWarps) {   // 8 rows x 32 channels
+            const int n = task / (D / 32), kk = task % (D / 32), r = n * 8 + g8;
+            const __nv_bfloat16* src = q_row(r);
+            uint32_t f[4] = {0u, 0u, 0u, 0u};
+            if (src) {
+                if constexpr (kCodes) {
+                    // channels 64 G + 16 t4 + 8 (kk % 2) .. + 7; word i of a code row's piece serves k step i:
+                    // its bytes (0, 2) and (1, 3) are the two pairs of a step
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + (kk >> 1) * 64 + 16 * t4 + 8 * (kk & 1));
+                    const float e = pow2(q_exp[r]);
+                    auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+                    auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
+                    f[0] = pack_bf16x2(lo(v.x) * e, lo(v.y) * e);
+                    f[1] = pack_bf16x2(hi(v.x) * e, hi(v.y) * e);
+                    f[2] = pack_bf16x2(lo(v.z) * e, lo(v.w) * e);
+                    f[3] = pack_bf16x2(hi(v.z) * e, hi(v.w) * e);
+                } else {
+                    const uint32_t* x = reinterpret_cast<const uint32_t*>(src + kk * 32) + t4;
+                    f[0] = x[0], f[1] = x[4], f[2] = x[8], f[3] = x[12];
+                }
+            }
+            *reinterpret_cast<uint4*>(smem + Lay::kQOff + (task * 32 + lane) * 16) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                qscale[n][c] = kCodes ? p.scale_log2 * pow2(120 - q_exp[n * 8 + 2 * t4 + c]) : p.scale_log2;
+                m_run[n][c] = -INFINITY;
+                mu[n][c] = l_run[n][c] = 0.f;
+            }
+        // keys that the block's first and last rows (hence all) see
+        const int full_lo = band_key_lo(mb, (min(w.rows, t.rb * kRows + kRows) - 1) / p.group);
+        const int full_hi = band_key_hi(mb, t.rb * kRows / p.group);
+        // ... and that some row sees, sinks aside
+        const int some_lo = band_key_lo(mb, t.rb * kRows / p.group);
+        const int some_hi = band_key_hi(mb, (min(w.rows, t.rb * kRows + kRows) - 1) / p.group);
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[j][n][x] = 0.f;
+        __syncthreads();   // the q fragments are in place
+        const uint32_t qfrag = base + Lay::kQOff + lane * 16;
+
+        // kTok keys from slot `st`, the first key0. kWhole: every row sees all of them.
+        bool force = true;   // some row has yet to see its first key
+        auto step = [&](auto whole_tag, const uint32_t st, const int key0) {
+            constexpr bool kWhole = decltype(whole_tag)::value;
+            float sc[CK][NR][4];   // s - mu: per chunk [key tok0, tok0 + 8][row 2 t4, 2 t4 + 1] at 2 * key + row
+#pragma unroll
+            for (int ck = 0; ck < CK; ++ck)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sc[ck][n][x] = 0.f;
+            if constexpr (kCodes) {
+#pragma unroll
+                for (int G = 0; G < D / 64; ++G) {
+                    uint4 q0[NR], q1[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        q0[n] = lds128(qfrag + (n * (D / 32) + 2 * G) * 512);
+                        q1[n] = lds128(qfrag + (n * (D / 32) + 2 * G + 1) * 512);
+                    }
+#pragma unroll
+                    for (int ck = 0; ck < CK; ++ck) {
+                        const uint4 a = lds128(row_piece<Lay::kKRow, kTok>(st, tok0 + 16 * ck, 4 * G + t4));
+                        const uint4 b = lds128(row_piece<Lay::kKRow, kTok>(st, tok0 + 16 * ck + 8, 4 * G + t4));
+                        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = codes_bf16(wa[i] << 8), a1 = codes_bf16(wb[i] << 8), a2 = codes_bf16(wa[i]),
+                                           a3 = codes_bf16(wb[i]);
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) {
+                                const uint4 q = i < 2 ? q0[n] : q1[n];
+                                mma_bf16(sc[ck][n], a0, a1, a2, a3, (i & 1) ? q.z : q.x, (i & 1) ? q.w : q.y);
+                            }
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk) {
+                    uint4 q[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) q[n] = lds128(qfrag + (n * (D / 32) + kk) * 512);
+#pragma unroll
+                    for (int ck = 0; ck < CK; ++ck)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint4 a = ldsm4(row_piece<Lay::kKRow, kTok>(st, ck * 16 + (lane & 15), kk * 4 + y * 2 + (lane >> 4)));
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) mma_bf16(sc[ck][n], a.x, a.y, a.z, a.w, y ? q[n].z : q[n].x, y ? q[n].w : q[n].y);
+                        }
+                }
+            }
+            float vs[CK][2];
+#pragma unroll
+            for (int ck = 0; ck < CK; ++ck) {
+                float ks[2] = {1.f, 1.f};
+                if constexpr (kCodes) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        ks[x] = __uint_as_float(lds8(st + Lay::kKsOff + ck * 16 + tok0 + 8 * x) << 23);
+                        vs[ck][x] = __uint_as_float(lds8(st + Lay::kVsOff + ck * 16 + tok0 + 8 * x) << 23);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float s = sc[ck][n][x] * qscale[n][x & 1];
+                        sc[ck][n][x] = kCodes ? fmaf(s, ks[x >> 1], -mu[n][x & 1]) : s - mu[n][x & 1];
+                    }
+            }
+            if constexpr (!kWhole) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int2 k = row_keys[n * 8 + 2 * t4 + c];
+#pragma unroll
+                        for (int x = 0; x < 2 * CK; ++x) {
+                            const int j = key0 + tok0 + 8 * x;
+                            if (!(j < k.y && (j >= k.x || j < p.sinks))) sc[x >> 1][n][2 * (x & 1) + c] = -INFINITY;
+                        }
+                    }
+            }
+            bool move = force;
+#pragma unroll
+            for (int ck = 0; ck < CK; ++ck)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) move |= sc[ck][n][x] > kPagedTau - kPagedShift;
+            if (__any_sync(kFullMask, move)) {
+                bool unset = false;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    float al[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int ck = 0; ck < CK; ++ck) mx = fmaxf(mx, fmaxf(sc[ck][n][c], sc[ck][n][2 + c]));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
+                        // (a row whose own maximum has not moved stays as it is, whatever its neighbours do)
+                        const bool moves = mx > kPagedTau - kPagedShift || m_run[n][c] == -INFINITY;
+                        const float m_new = moves ? fmaxf(m_run[n][c], mx + mu[n][c] + kPagedShift) : m_run[n][c];
+                        al[c] = m_new == -INFINITY ? 1.f : ex2_mufu(m_run[n][c] - m_new);
+                        const float mu_new = m_new == -INFINITY ? 0.f : m_new;
+#pragma unroll
+                        for (int ck = 0; ck < CK; ++ck) {
+                            sc[ck][n][c] += mu[n][c] - mu_new;
+                            sc[ck][n][2 + c] += mu[n][c] - mu_new;
+                        }
+                        unset |= m_new == -INFINITY && row_keys[n * 8 + 2 * t4 + c].y > 0;
+                        m_run[n][c] = m_new;
+                        mu[n][c] = mu_new;
+                        l_run[n][c] *= al[c];
+                    }
+#pragma unroll
+                    for (int j = 0; j < DV / 16; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) acc[j][n][x] *= al[x & 1];
+                }
+                force = __any_sync(kFullMask, unset);
+            }
+            uint32_t b0[CK][NR], b1[CK][NR];
+#pragma unroll
+            for (int ck = 0; ck < CK; ++ck)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    float x[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float e = ex2_mufu(sc[ck][n][y]);
+                        l_run[n][y & 1] += e;
+                        x[y] = kCodes ? e * vs[ck][y >> 1] : e;
+                        if (kCodes && !kWhole && e == 0.f) x[y] = 0.f;   // (times the infinite scale of a masked key)
+                    }
+                    b0[ck][n] = transpose8x8(pack_bf16x2(x[0], x[1]));
+                    b1[ck][n] = transpose8x8(pack_bf16x2(x[2], x[3]));
+                }
+            // ---------------------------------------- values
+            const uint32_t sv = st + Lay::kVOff;
+#pragma unroll
+            for (int ck = 0; ck < CK; ++ck) {
+                if constexpr (kCodes) {
+#pragma unroll
+                    for (int x = 0; x < DV / 32; ++x) {   // channels 32 x + 4 g8 .. + 3
+                        const int piece = 2 * x + (g8 >> 2), at = (g8 & 3) * 4;
+                        uint32_t wv[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) wv[y] = lds32(row_piece<Lay::kVRow, kTok>(sv, ck * 16 + t4 + 4 * y, piece) + at);
+                        uint32_t f[4][2];   // channel c: tokens (t, t + 4), (t + 8, t + 12)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                f[c][y] = times_2_120(codes_bf16(__byte_perm(wv[2 * y], wv[2 * y + 1], (4 + c) << 12 | c << 4)));
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            mma_bf16(acc[2 * x][n], f[0][0], f[1][0], f[0][1], f[1][1], b0[ck][n], b1[ck][n]);
+                            mma_bf16(acc[2 * x + 1][n], f[2][0], f[3][0], f[2][1], f[3][1], b0[ck][n], b1[ck][n]);
+                        }
+                    }
+                } else {
+                    uint32_t in[2] = {~0u, ~0u};   // values that no row sees may hold anything: they read as zero
+                    if constexpr (!kWhole) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int j = key0 + ck * 16 + 8 * (y >> 1) + 2 * t4 + (y & 1);
+                            if (!(j < some_hi && (j >= some_lo || j < p.sinks))) in[y >> 1] &= (y & 1) ? 0x0000ffffu : 0xffff0000u;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < DV / 16; ++j) {
+                        uint4 a = ldsm4t(row_piece<Lay::kVRow, kTok>(sv, ck * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                                                           2 * j + ((lane >> 3) & 1)));
+                        if constexpr (!kWhole) a = make_uint4(a.x & in[0], a.y & in[0], a.z & in[1], a.w & in[1]);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma_bf16(acc[j][n], a.x, a.y, a.z, a.w, b0[ck][n], b1[ck][n]);
+                    }
+                }
+            }
+        };
+
+        const int steps = (i1 - i0) * kSteps;
+        for (int n = 0; n < steps; ++n) {
+            copy_wait<S - 2>();
+            __syncwarp();   // the slot is full, and every lane has read the one before
+            issue(n + S - 1);
+            const int x = n / kSteps, i = i0 + x;
+            const bool valid = (live >> (x & 31)) & 1u;
+            const uint32_t st = ring + slot_out;
+            slot_out = slot_out == (S - 1) * Lay::kSlot ? 0 : slot_out + Lay::kSlot;
+            const int key0 = page_of(w, 2 * i + (warp >> 1)) * kPage + 32 * half + n % kSteps * kTok;
+            if (valid && key0 < w.s.lk) {
+                if (key0 >= full_lo && key0 + kTok <= full_hi) step(std::true_type{}, st, key0);
+                else step(std::false_type{}, st, key0);
+            }
+        }
+        // ------------------------------------------------ the four warps' rows become one
+        // (every copy into the slots has landed and been read: each warp's O rows go there)
+        const bool ends = i1 == w.units, starts = i0 == 0;
+        copy_wait<0>();
+        __syncwarp();
+        float* mine = reinterpret_cast<float*>(smem + warp * S * Lay::kSlot);
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[n][c];
+                l += __shfl_xor_sync(kFullMask, l, 4);
+                l += __shfl_xor_sync(kFullMask, l, 8);
+                l += __shfl_xor_sync(kFullMask, l, 16);
+                const int row = n * 8 + 2 * t4 + c;
+                if (g8 == 0) ml[warp * kRows + row] = make_float2(m_run[n][c], l);
+                if constexpr (kCodes) {
+#pragma unroll
+                    for (int x = 0; x < DV / 32; ++x)
+                        *reinterpret_cast<float4*>(mine + row * DV + 32 * x + 4 * g8) =
+                            make_float4(acc[2 * x][n][c], acc[2 * x][n][2 + c], acc[2 * x + 1][n][c], acc[2 * x + 1][n][2 + c]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < DV / 16; ++j) {
+                        mine[row * DV + j * 16 + g8] = acc[j][n][c];
+                        mine[row * DV + j * 16 + g8 + 8] = acc[j][n][2 + c];
+                    }
+                }
+            }
+        __syncthreads();
+        const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+        const int n_rows = min(kRows, w.rows - t.rb * kRows);
+        for (int x = tid; x < n_rows * (DV / 4); x += kPagedThreads) {
+            const int row = x / (DV / 4), c4 = x % (DV / 4);
+            float2 v[kWarps];
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) {
+                v[y] = ml[y * kRows + row];
+                m = fmaxf(m, v[y].x);
+            }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) {   // in warp order: the same sum on every run
+                const float f = v[y].x == -INFINITY ? 0.f : ex2_mufu(v[y].x - m);
+                l += v[y].y * f;
+                if (f != 0.f) {
+                    const float4 z = *reinterpret_cast<const float4*>(smem + y * S * Lay::kSlot + (row * DV + 4 * c4) * 4);
+                    o.x = fmaf(f, z.x, o.x);
+                    o.y = fmaf(f, z.y, o.y);
+                    o.z = fmaf(f, z.z, o.z);
+                    o.w = fmaf(f, z.w, o.w);
+                }
+            }
+            if (starts && ends) {
+                const int r = t.rb * kRows + row, i = r / p.group, head = t.h * p.group + r % p.group;
+                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (NaN stays)
+                *reinterpret_cast<uint2*>(p.o + ((long)(w.s.q0 + i) * p.H + head) * DV + 4 * c4) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (c4 == 0) p.lse[lse_at(p, w, t.b, i, head)] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            } else {
+                *reinterpret_cast<float4*>(p.part_o + ((long)part * kRows + row) * DV + 4 * c4) = o;
+                if (c4 == 0) *reinterpret_cast<float2*>(p.part_ml + ((long)part * kRows + row) * 2) = make_float2(m, l);
+            }
+        }
+        __syncthreads();   // the next row block's copies come after these reads
+    }
+}
+
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) paged_finish_kernel(const PagedFwdParams p, int rows_per_block) {
+    finish_row(p, (long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), rows_per_block);
+}
+
+template <bool kCodes, int D, int DV, int NR>
+cudaError_t launch_one(const PagedFwdParams& p, int num_sms, cudaStream_t stream) {
+    using Lay = PagedLayout<kCodes, D, DV, NR>;
+    static std::atomic<unsigned long long> allowed;
+    auto kern = paged_fwd_kernel<kCodes, D, DV, NR>;
+    cudaError_t e = allow_smem(kern, Lay::smem(kKv4MaxBatch), allowed);
+    if (e != cudaSuccess) return e;
+    int grid = num_sms * Lay::kCtas;
+    if (grid > kKv4MaxCtas) grid = kKv4MaxCtas;
+    kern<<<grid, kPagedThreads, Lay::smem(p.s.B), stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long)p.s.total * p.H + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_finish_kernel, p, Lay::kRows);
+}
+
+template <bool kCodes, int D, int DV>
+cudaError_t launch_dims(const PagedFwdParams& p, int num_sms, cudaStream_t stream) {
+    return kv4_row_tiles(p.group, p.s.B, p.s.total) == 1 ? launch_one<kCodes, D, DV, 1>(p, num_sms, stream)
+                                                         : launch_one<kCodes, D, DV, 2>(p, num_sms, stream);
+}
+template <bool kCodes>
+cudaError_t launch_form(const PagedFwdParams& p, int num_sms, cudaStream_t stream) {
+    const int d = p.c.d, dv = p.c.dv;
+    if (d == 64 && dv == 64) return launch_dims<kCodes, 64, 64>(p, num_sms, stream);
+    if (d == 128 && dv == 128) return launch_dims<kCodes, 128, 128>(p, num_sms, stream);
+    if (d == 192 && dv == 192) return launch_dims<kCodes, 192, 192>(p, num_sms, stream);
+    if (d == 192 && dv == 128) return launch_dims<kCodes, 192, 128>(p, num_sms, stream);
+    if (d == 256 && dv == 256) return launch_dims<kCodes, 256, 256>(p, num_sms, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_fwd(const PagedFwdParams& p, bool codes, int num_sms, cudaStream_t stream) {
+    return codes ? launch_form<true>(p, num_sms, stream) : launch_form<false>(p, num_sms, stream);
+}
+
+}  // namespace attn

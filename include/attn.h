@@ -427,6 +427,53 @@ int attn_kv4_evict(const attn_kv4_cache* cache, const int* page_table, int table
                    float* new_key_weights, long long new_weight_stride, cudaStream_t stream);
 
 /*
+ * A paged key/value cache in bf16 or in 8 bits, for serving: append, read back,
+ * attend. Batches, page tables, lengths and errors as for the 4-bit cache above.
+ *   bits 16: k bf16 [n_pages, Hkv, 64, d], v bf16 [n_pages, Hkv, 64, d_v];
+ *            k_scales and v_scales are not used (may be NULL).
+ *   bits 8:  k, v e4m3 codes of the same shapes, k_scales and v_scales bytes
+ *            [n_pages, Hkv, 64]: a code c of a row whose byte is e stands for
+ *            c 2^(e - 127), 1 <= e <= 247; e = 255 marks a row of NaN.
+ */
+typedef struct attn_paged_cache {
+    void* k;
+    void* v;
+    void* k_scales;
+    void* v_scales;
+    int n_pages, Hkv, d, d_v;
+    int bits;
+} attn_paged_cache;
+
+/*
+ * Write the rows of k and v (bf16, k_stride and v_stride elements between rows,
+ * multiples of 8) into the cache; to 8 bits: per row and head e - 127 is the least
+ * exponent from -126 up with max |x| <= 448 2^(e - 127), code = x 2^(127 - e) rounded to
+ * e4m3, ties to even. A row with a NaN or an infinity reads back as NaN throughout.
+ */
+int attn_paged_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                      const attn_paged_cache* cache, const int* page_table, int table_width, const int* cache_lens,
+                      const int* cu_seqlens, int B, int L, cudaStream_t stream);
+
+/* The inverse, as attn_kv4_read: the last rows of every sequence's cache in bf16. */
+int attn_paged_read(void* k, void* v, const attn_paged_cache* cache, const int* page_table, int table_width,
+                    const int* cache_lens, const int* cu_seqlens, int B, int L, cudaStream_t stream);
+
+/*
+ * Attention of the rows of q over their sequence's cache, as attn_kv4_fwd without
+ * key weights. P is rounded to bf16 for its product with V. What a cache holds
+ * behind a sequence's last token or left of every window counts as nothing, whatever
+ * it is. An infinity or NaN in a cached bf16 value also reaches rows of the call
+ * that do not see it, when others of their head and sequence do (in 8 bits it
+ * stays with the rows that see it). With 8 bits elements of q of 2^67 and more may
+ * count as infinite. Results repeat bit for bit.
+ */
+size_t attn_paged_fwd_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v);
+int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* cache, const int* page_table,
+                   int table_width, const int* cache_lens, const int* cu_seqlens, void* o, float* lse,
+                   int B, int H, int L, float scale, int causal, int window_left, int window_right, int sinks,
+                   void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Linear attention with a decay for each head. Per sequence and key/value head,
  * with D = exp(log_decay) and a state S (d x d_v, fp32) in place of a cache:
  *   S_t = D S_(t-1) + k_t v_t^T,   o_t = scale q_t^T S_t      (t = 1 .. n)
