@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 
 LIBS = {
     "libattn.so": ["api.cu", "fwd.cu", "fwd_wide.cu", "bwd.cu", "bwd_wide.cu", "bwd_pair.cu",
-                   "kv4.cu", "kv4_fwd.cu", "linear.cu",
+                   "kv4.cu", "kv4_fwd.cu", "linear.cu", "linear_tc.cu",
                    "paged.cu", "paged_fwd.cu"],
     "libattn_selftest.so": ["selftest.cu"],
 }

@@ -835,19 +835,41 @@ int check_linear(int B, int H, int Hkv, int L, const int* cu, int d, int dv, flo
     return ATTN_OK;
 }
 
+// [rows, H, d] bf16 with `stride` elements between rows, in boxes of 128 rows x 64 columns of one head
+bool make_map_rows(CUtensorMap* m, const void* ptr, long rows, int H, int d, long stride) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64u, 1, 128u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+struct LinTensor {
+    const void* x;
+    long long stride;
+    int heads, width;
+    CUtensorMap map;
+};
+
+size_t linear_bytes(const LinPlan& plan, int Hkv, int d, int dv) { return (size_t)plan.segments * Hkv * d * dv * sizeof(float); }
+
 // What the four products of linear attention share; the roles of the tensors come on top.
-int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, const float* log_decay, void* workspace,
-                  size_t ws_bytes, LinParams* p, bool* split) {
+int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, const float* log_decay, bool final,
+                  void* workspace, size_t ws_bytes, LinTensor* const* tensors, int n_tensors, LinParams* p, DevInfo* di) {
     const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, d, dv);
     if ((double)plan.segments * Hkv * ((d > dv ? d : dv) / 64) >= 2.0e9 || (double)B * Hkv * d * dv / 256 >= 2.0e9)
         return fail(ATTN_ERR_ARG, "linear: too many sequences and heads");
-    const size_t need = plan.split ? (size_t)plan.segments * Hkv * d * dv * sizeof(float) : 0;
+    const size_t need = plan.split || final ? linear_bytes(plan, Hkv, d, dv) : 0;
     if (need > 0 && (!workspace || ws_bytes < need))
         return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
-    DevInfo di;
-    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    if (!device_info(di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
     p->log_decay = log_decay;
     p->states = static_cast<float*>(workspace);
     p->cu = cu;
@@ -858,21 +880,36 @@ int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, co
     p->per = H / Hkv;
     p->seg_rows = plan.seg_rows;
     p->segments = plan.segments;
+    p->plan_split = plan.split;
     p->init_mul = p->final_mul = 1.f;
-    p->status = di.status;
-    *split = plan.split;
+    p->status = di->status;
+    p->wait_budget_ns = wait_budget_ns();
+    if (lin_on_tc(d, dv) && p->total > 0)
+        for (int i = 0; i < n_tensors; ++i) {
+            LinTensor& t = *tensors[i];
+            if (!make_map_rows(&t.map, t.x, p->total, t.heads, t.width, (long)t.stride))
+                return fail(ATTN_ERR_LAUNCH, "cuTensorMapEncodeTiled failed");
+        }
     return ATTN_OK;
 }
 
 const __nv_bfloat16* bf16(const void* x) { return static_cast<const __nv_bfloat16*>(x); }
+
+// The roles of a product (linear.h)
+LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const LinTensor& c, void* out) {
+    p->a = bf16(a.x), p->b = bf16(b.x), p->c = bf16(c.x);
+    p->a_stride = (long)a.stride, p->b_stride = (long)b.stride, p->c_stride = (long)c.stride;
+    p->out = static_cast<__nv_bfloat16*>(out);
+    p->DK = a.width, p->DV = c.width;
+    return LinMaps{a.map, b.map, c.map};
+}
 
 }  // namespace
 
 extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v) {
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
     if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
-    const LinPlan plan = lin_plan(B, Hkv, L, packed != 0, d, d_v);
-    return plan.split ? (size_t)plan.segments * Hkv * d * d_v * sizeof(float) : 0;
+    return linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v), Hkv, d, d_v);
 }
 
 extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -889,17 +926,18 @@ extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long
     if (rows && ((rc = check_stride("q", q_stride, (long long)H * d)) || (rc = check_stride("k", k_stride, (long long)Hkv * d)) ||
                  (rc = check_stride("v", v_stride, (long long)Hkv * d_v))))
         return rc;
+    LinTensor tq{q, q_stride, H, d, {}}, tk{k, k_stride, Hkv, d, {}}, tv{v, v_stride, Hkv, d_v, {}};
+    LinTensor* const all[] = {&tq, &tk, &tv};
     LinParams p{};
-    bool split;
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, workspace, ws_bytes, &p, &split))) return rc;
-    p.a = bf16(q), p.b = bf16(k), p.c = bf16(v);
-    p.a_stride = (long)q_stride, p.b_stride = (long)k_stride, p.c_stride = (long)v_stride;
-    p.out = static_cast<__nv_bfloat16*>(o);
-    p.DK = d, p.DV = d_v;
+    DevInfo di;
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, final_state != nullptr, workspace, ws_bytes, all, 3, &p, &di)))
+        return rc;
+    const LinMaps maps = linear_roles(&p, tq, tk, tv, o);
     p.init = state;
     p.final = final_state;
     p.out_mul = scale;
-    const cudaError_t e = launch_linear(p, split, false, stream);
+    cudaError_t e = launch_linear_states(p, maps, false, di.sms, stream);
+    if (e == cudaSuccess) e = launch_linear_out(p, maps, false, di.sms, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear forward launch failed: %s", cudaGetErrorString(e));
     return ok();
 }
@@ -921,38 +959,36 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
                  (rc = check_stride("v", v_stride, (long long)Hkv * d_v)) ||
                  (rc = check_stride("dout", dout_stride, (long long)H * d_v))))
         return rc;
+    LinTensor tq{q, q_stride, H, d, {}}, tk{k, k_stride, Hkv, d, {}}, tv{v, v_stride, Hkv, d_v, {}},
+        tdo{dout, dout_stride, H, d_v, {}};
+    LinTensor* const all[] = {&tq, &tk, &tv, &tdo};
     LinParams p{};
-    bool split;
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, workspace, ws_bytes, &p, &split))) return rc;
+    DevInfo di;
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, dstate != nullptr, workspace, ws_bytes, all, 4, &p, &di)))
+        return rc;
     p.out_mul = scale;
     cudaError_t e = cudaSuccess;
     if (rows) {   // dq, forwards
-        p.a = bf16(dout), p.b = bf16(v), p.c = bf16(k);
-        p.a_stride = (long)dout_stride, p.b_stride = (long)v_stride, p.c_stride = (long)k_stride;
-        p.out = static_cast<__nv_bfloat16*>(dq);
-        p.DK = d_v, p.DV = d;
+        const LinMaps maps = linear_roles(&p, tdo, tv, tk, dq);
         p.init = state;
         p.init_trans = 1;
-        e = launch_linear(p, split, false, stream);
+        e = launch_linear_states(p, maps, false, di.sms, stream);
+        if (e == cudaSuccess) e = launch_linear_out(p, maps, false, di.sms, stream);
     }
-    p.reverse = p.e = 1;
+    // dv and the gradient of the first state, and dk, backwards: its states are those of dv, transposed
+    // (dstate, which may be dfinal's buffer, is written where the states are made: nothing reads dfinal behind)
     p.init = dfinal;
     p.init_mul = 1.f / scale;
-    if (rows && e == cudaSuccess) {   // dk, backwards
-        p.a = bf16(v), p.b = bf16(dout), p.c = bf16(q);
-        p.a_stride = (long)v_stride, p.b_stride = (long)dout_stride, p.c_stride = (long)q_stride;
-        p.out = static_cast<__nv_bfloat16*>(dk);
-        e = launch_linear(p, split, true, stream);
-    }
-    if (e == cudaSuccess) {   // dv and the gradient of the first state (last: it may be dfinal's buffer)
-        p.a = bf16(k), p.b = bf16(q), p.c = bf16(dout);
-        p.a_stride = (long)k_stride, p.b_stride = (long)q_stride, p.c_stride = (long)dout_stride;
-        p.out = static_cast<__nv_bfloat16*>(dv);
-        p.DK = d, p.DV = d_v;
-        p.init_trans = 0;
-        p.final = dstate;
-        p.final_mul = scale;
-        e = launch_linear(p, split, true, stream);
+    p.init_trans = 0;
+    p.final = dstate;
+    p.final_mul = scale;
+    const LinMaps maps = linear_roles(&p, tk, tq, tdo, dv);
+    if (e == cudaSuccess) e = launch_linear_states(p, maps, true, di.sms, stream);
+    if (rows && e == cudaSuccess) e = launch_linear_out(p, maps, true, di.sms, stream);
+    if (rows && e == cudaSuccess) {
+        const LinMaps maps_k = linear_roles(&p, tv, tdo, tq, dk);
+        p.init_trans = p.states_trans = 1;
+        e = launch_linear_out(p, maps_k, true, di.sms, stream);
     }
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear backward launch failed: %s", cudaGetErrorString(e));
     return ok();

@@ -1,17 +1,15 @@
-// Linear attention with a decay per head: prompts and training in chunks of 64
-// tokens, single tokens by the recurrence. linear.h gives the one form that the
-// forward and the gradients share.
+// Linear attention with a decay per head: the plan of its segments, the scan over them, the
+// kernels on mma.sync for the head dims that linear_tc.cu does not take, and the single
+// token by the recurrence. linear.h gives the one form that the forward and the gradients share.
 //
-// Mathematics. Within a chunk the pairs are taken as in attention, P_ij =
-// decay^(i-j) <a_i, b_j> for j <= i and out += P c; what lies before the chunk
-// enters through the state X, out += decay^(i+1-e) a X. No factor is larger than
-// 1, so nothing overflows for fast decays. Sums, states and decays are fp32.
-// Roundings to bf16, the type of the tensor cores' operands: P before its product
-// with c and X before its product with a (both like P in the exact attention:
-// they reach outputs that are bf16 themselves). A state's sum takes its weighted
-// operand as two bf16 terms (16 bits): the state leaves the call in fp32, where a
-// rounding of 2^-9 per token would show. Each chunk's share of the state is summed
-// on its own and added in fp32, which rounds once per 64 tokens.
+// Mathematics. Within a chunk of 64 tokens the pairs are taken as in attention, P_ij =
+// D^|i-j| <a_i, b_j> and out += P c; what lies before the chunk enters through the state
+// X, out += D^(..) a X. No factor is larger than 1, so nothing overflows for fast decays.
+// Sums, states and decays are fp32. Roundings to bf16, the type of the tensor cores'
+// operands: P, X before its product with a, and the weighted b in the state's update within
+// a segment (like P in the exact attention: they reach outputs that are bf16 themselves).
+// The segments' shares, which the states that leave a call are made of, take the weighted b
+// as three bf16 terms, all 24 bits of it.
 #include <atomic>
 
 #include "kv4.h"
@@ -21,7 +19,7 @@
 namespace attn {
 namespace {
 
-constexpr int kLinThreads = 256, kC = kLinChunk;
+constexpr int kLinThreads = 256, kC = 64;
 constexpr int kPanel = kC * 128;   // bytes of 64 rows x 64 columns
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -52,61 +50,21 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int col, int
     return base + (col >> 6) * (rows * 128) + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
 }
 
-// A segment of a sequence: positions [r0, r1) of its n, q0 its first row.
-struct Segment {
-    int b, q0, n, r0, r1;
-    bool first, last, live;
-};
-__device__ __forceinline__ int seg_start(const LinParams& p, int b) {
-    return p.cu ? p.cu[b] / p.seg_rows + b : b * max(1, (p.rows + p.seg_rows - 1) / p.seg_rows);
-}
-// Offsets out of range make an empty sequence (reported); a start that is off only moves
-// segments that are then not live or reads another one's state.
-__device__ __forceinline__ Segment segment_at(const LinParams& p, int s) {
-    Segment g;
-    int lo = 0, hi = p.B - 1;   // the last b that starts at s or before
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (seg_start(p, mid) <= s) lo = mid;
-        else hi = mid - 1;
-    }
-    g.b = lo;
-    g.q0 = p.cu ? p.cu[lo] : lo * p.rows;
-    g.n = p.cu ? p.cu[lo + 1] - g.q0 : p.rows;
-    if (g.q0 < 0 || g.n < 0 || g.q0 > p.total - g.n) {
-        if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusBadPage);
-        g.q0 = g.n = 0;
-    }
-    const int i = s - seg_start(p, lo), count = max(1, (g.n + p.seg_rows - 1) / p.seg_rows);
-    g.live = i >= 0 && i < count;
-    g.first = i == 0;
-    g.last = i == count - 1;
-    g.r0 = g.live ? i * p.seg_rows : 0;
-    g.r1 = min(g.n, g.r0 + p.seg_rows);
-    return g;
-}
-
-__device__ __forceinline__ float log2_decay(const LinParams& p, int h) {
-    const float l = p.log_decay[h] * kLog2e;
-    return l > 0.f ? 0.f : l;   // (a decay above 1 counts as 1; NaN stays)
-}
-__device__ __forceinline__ float decay_pow(float l2, int n) { return n == 0 ? 1.f : exp2f(l2 * (float)n); }   // (0^0 = 1)
-
-// 64 positions from r0 on (zeros past the sequence's end), `width` columns
-__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, long stride, int width, const LinParams& p,
-                                          const Segment& g, int r0) {
+// 64 tokens from row r0 of a sequence on (zeros past its end), `width` columns
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, long stride, int width, const Segment& g,
+                                          int r0) {
     const int pieces = width >> 3, shift = 31 - __clz(pieces);
     for (int x = threadIdx.x; x < kC * pieces; x += kLinThreads) {
         const int row = (pieces & (pieces - 1)) == 0 ? x >> shift : x / pieces, col = (x - row * pieces) * 8, r = r0 + row;
         const bool in = r < g.n;
-        const long t = g.q0 + (p.reverse ? g.n - 1 - r : r);
-        copy16z(tile_at(dst, row, col), in ? src + t * stride + col : src, in);
+        copy16z(tile_at(dst, row, col), in ? src + (long)(g.q0 + r) * stride + col : src, in);
     }
 }
 
 // X = decay X + (weights b)^T c over a chunk. Warp w owns rows 16 MT (w % 4) .. of
 // X and columns 32 (w / 4) ..; w_tab[j] is token j's weight.
-template <int MT>
+// kTerms bf16 terms of the weighted b.
+template <int MT, int kTerms>
 __device__ __forceinline__ void update_state(float (&X)[MT][4][4], uint32_t b_tile, uint32_t c_tile, const float* w_tab,
                                              float decay) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t4 = lane & 3;
@@ -121,19 +79,28 @@ __device__ __forceinline__ void update_state(float (&X)[MT][4][4], uint32_t b_ti
         float acc[4][4] = {};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            uint32_t raw[4], hi[4], lo[4];
+            uint32_t raw[4];
+            float f[4][2];
             ldsm4t(tile_at(b_tile, ks * 16 + (lane & 7) + ((lane >> 4) << 3), m0 + mt * 16 + ((lane >> 3) & 1) * 8), raw);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {   // raw[x]: tokens 16 ks + 2 t4 + 8 (x / 2), + 1
                 const int j = ks * 16 + 2 * t4 + 8 * (x >> 1);
-                const float f0 = __uint_as_float(raw[x] << 16) * w_tab[j], f1 = __uint_as_float(raw[x] & 0xffff0000u) * w_tab[j + 1];
-                hi[x] = pack_bf16x2(f0, f1);
-                lo[x] = pack_bf16x2(f0 - __uint_as_float(hi[x] << 16), f1 - __uint_as_float(hi[x] & 0xffff0000u));
+                f[x][0] = __uint_as_float(raw[x] << 16) * w_tab[j];
+                f[x][1] = __uint_as_float(raw[x] & 0xffff0000u) * w_tab[j + 1];
             }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                mma_bf16(acc[n], hi, cf[ks][n >> 1][(n & 1) * 2], cf[ks][n >> 1][(n & 1) * 2 + 1]);
-                mma_bf16(acc[n], lo, cf[ks][n >> 1][(n & 1) * 2], cf[ks][n >> 1][(n & 1) * 2 + 1]);
+            for (int term = 0; term < kTerms; ++term) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    w[x] = pack_bf16x2(f[x][0], f[x][1]);
+                    if (term + 1 < kTerms) {
+                        f[x][0] -= __uint_as_float(w[x] << 16);
+                        f[x][1] -= __uint_as_float(w[x] & 0xffff0000u);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) mma_bf16(acc[n], w, cf[ks][n >> 1][(n & 1) * 2], cf[ks][n >> 1][(n & 1) * 2 + 1]);
             }
         }
 #pragma unroll
@@ -156,30 +123,31 @@ __device__ __forceinline__ void each_pair(float (&X)[MT][4][4], F f) {
             for (int x = 0; x < 2; ++x) f(m0 + mt * 16 + 8 * x, n0 + n * 8, X[mt][n][2 * x], X[mt][n][2 * x + 1]);
 }
 
+// Powers of the decay for a chunk whose tokens i < n (all 64, but for a sequence's last)
+// exist. Token i's weight in the state: in order D^(n - 1 - i), backwards D^(i + 1).
 struct Tables {
-    float w[2 * kC];       // decay^(63 - x + e), zero from x = 64 on: the last n tokens' weights from w[64 - n]
-    float into[kC];        // decay^(i + 1 - e)
-    float pow[kC];         // decay^n
+    float w[2 * kC];       // in order: D^(63 - x), zero from x = 64 on (read from x = 64 - n); backwards: D^(x + 1)
+    float pow[kC + 1];     // D^x
 };
-__device__ __forceinline__ void fill_tables(Tables* t, float l2, int e) {
+template <bool kBack>
+__device__ __forceinline__ void fill_tables(Tables* t, float l2) {
     for (int x = threadIdx.x; x < 2 * kC; x += kLinThreads) {
-        t->w[x] = x < kC ? decay_pow(l2, kC - 1 - x + e) : 0.f;
-        if (x < kC) {
-            t->into[x] = decay_pow(l2, x + 1 - e);
-            t->pow[x] = decay_pow(l2, x);
-        }
+        t->w[x] = x < kC ? decay_pow(l2, kBack ? x + 1 : kC - 1 - x) : 0.f;
+        if (x <= kC) t->pow[x] = decay_pow(l2, x);
     }
 }
+template <bool kBack>
+__device__ __forceinline__ const float* weights(const Tables* t, int n) { return kBack ? t->w : t->w + kC - n; }
 
 template <int DK>
 struct StateSmem {
     static constexpr int kB = kC * DK * 2, kStage = kB + kPanel, kTables = 2 * kStage, kBytes = kTables + (int)sizeof(Tables);
 };
 
-// What each segment but a sequence's last adds to the state (carried in: nothing);
-// per: b and c per state.
-template <int DK>
-__global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_state_kernel(const LinParams p, const int per) {
+// What each segment adds to the state (carried in: nothing); without a final state to
+// return, the segment that a walk visits last is not needed.
+template <int DK, bool kBack>
+__global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_state_kernel(const LinParams p) {
     using Lay = StateSmem<DK>;
     constexpr int MT = DK / 64;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -187,61 +155,74 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_state_kern
     Tables* tab = reinterpret_cast<Tables*>(smem + Lay::kTables);
     const int nt = p.DV >> 6, tile = blockIdx.x % nt, h = blockIdx.x / nt % p.Hkv, s = blockIdx.x / nt / p.Hkv;
     const Segment g = segment_at(p, s);
-    if (!g.live || g.last) return;
+    if (!g.live || (!p.final && (kBack ? g.first : g.last))) return;
     const float l2 = log2_decay(p, h);
-    fill_tables(tab, l2, p.e);
-    const int items = (g.r1 - g.r0) / kC * per;   // (a segment that is not the last is whole)
+    fill_tables<kBack>(tab, l2);
+    const int per = kBack ? p.per : 1, chunks = (g.r1 - g.r0 + kC - 1) / kC, items = chunks * per;
+    auto row_of = [&](int it) { return g.r0 + (kBack ? chunks - 1 - it / per : it / per) * kC; };
     auto issue = [&](int it) {
         if (it < items) {
-            const int r = g.r0 + it / per * kC, head = h * per + it % per;
+            const int r = row_of(it), head = h * per + it % per;
             const uint32_t at = base + (it & 1) * Lay::kStage;
-            load_tile(at, p.b + head * DK, p.b_stride, DK, p, g, r);
-            load_tile(at + Lay::kB, p.c + (long)head * p.DV + tile * 64, p.c_stride, 64, p, g, r);
+            load_tile(at, p.b + (long)head * DK, p.b_stride, DK, g, r);
+            load_tile(at + Lay::kB, p.c + (long)head * p.DV + tile * 64, p.c_stride, 64, g, r);
         }
         copy_commit();
     };
     float X[MT][4][4] = {};
     issue(0);
-    const float decay = decay_pow(l2, kC);
     for (int it = 0; it < items; ++it) {
         copy_wait0();
         __syncthreads();
         issue(it + 1);
         const uint32_t at = base + (it & 1) * Lay::kStage;
-        update_state<MT>(X, at, at + Lay::kB, tab->w, it % per == 0 ? decay : 1.f);
+        const int n = min(kC, g.r1 - row_of(it));
+        update_state<MT, 3>(X, at, at + Lay::kB, weights<kBack>(tab, n), it % per == 0 ? tab->pow[n] : 1.f);
     }
+    copy_wait0();
     float* dst = p.states + ((long)s * p.Hkv + h) * DK * p.DV + tile * 64;
     each_pair<MT>(X, [&](int row, int col, float x0, float x1) {
         *reinterpret_cast<float2*>(dst + (long)row * p.DV + col) = make_float2(x0, x1);
     });
 }
 
-// Turns the segments' shares into the state that each of them starts from: X_0 =
-// init, X_(s+1) = decay^rows X_s + share_s. A thread takes one element.
+// Turns the segments' shares into the state that each of them starts from, in the
+// order of the walk: X = init, then X = D^rows X + share; and writes the last one. A
+// thread takes one element.
+template <bool kBack>
 __global__ void __launch_bounds__(kLinThreads) lin_scan_kernel(const LinParams p) {
-    const int size = p.DK * p.DV, blocks = (size + kLinThreads - 1) / kLinThreads;
+    const int size = p.DK * p.DV, blocks = size / kLinThreads;
     const int bh = blockIdx.x / blocks, b = bh / p.Hkv, h = bh % p.Hkv, x = blockIdx.x % blocks * kLinThreads + threadIdx.x;
-    const int s0 = seg_start(p, b);
+    const int s0 = lin_seg_start(p, b);
     if (s0 < 0 || s0 >= p.segments) return;
     const Segment g = segment_at(p, s0);
+    if (g.b != b) return;   // (offsets that do not ascend)
     const int count = min(max(1, (g.n + p.seg_rows - 1) / p.seg_rows), p.segments - s0);
-    if (g.b != b || count < 2 || x >= size) return;   // (one segment starts from init itself)
     float X = 0.f;
     if (p.init) X = p.init_mul * p.init[(long)bh * size + (p.init_trans ? x % p.DV * p.DK + x / p.DV : x)];
-    const float over = decay_pow(log2_decay(p, h), p.seg_rows);   // (every segment but the last is whole)
+    const float l2 = log2_decay(p, h), whole = decay_pow(l2, p.seg_rows);
+    const int rest = g.n - (count - 1) * p.seg_rows;   // rows of the segment that ends the sequence
+    const float part = decay_pow(l2, rest);
     float* at = p.states + ((long)s0 * p.Hkv + h) * size + x;
     const long step = (long)p.Hkv * size;
     constexpr int kAhead = 8;
-    for (int s = 0; s < count; s += kAhead) {
+    for (int i = 0; i < count; i += kAhead) {   // (step i of the walk)
         float y[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) y[k] = s + k < count - 1 ? at[(s + k) * step] : 0.f;
+        for (int k = 0; k < kAhead; ++k) {
+            const int s = kBack ? count - 1 - i - k : i + k;
+            const bool in = i + k < count && (p.final || i + k < count - 1) && g.n > 0;
+            y[k] = in ? at[s * step] : 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            if (s + k < count) at[(s + k) * step] = X;
-            X = fmaf(X, over, y[k]);
+            if (i + k >= count) break;
+            const int s = kBack ? count - 1 - i - k : i + k;
+            at[s * step] = X;
+            X = fmaf(X, s == count - 1 ? part : whole, y[k]);
         }
     }
+    if (p.final) p.final[(long)bh * size + x] = X * p.final_mul;
 }
 
 template <int DK>
@@ -251,11 +232,11 @@ struct OutSmem {
                          kBytes = kTables + (int)sizeof(Tables);
 };
 
-// The outputs of a segment: 64 positions at a time, 64 of the DV columns per CTA.
-// kSum: one a and out for the group, b and c per query head; else the reverse.
+// The outputs of a segment: 64 tokens at a time, 64 of the DV columns per CTA.
+// kBack: one a and out for the group, b and c per query head; else the reverse.
 // Warps: P and out in tiles of 16 rows (warp % 4) x 32 columns (warp / 4), the
 // state as in update_state.
-template <int DK, bool kSum>
+template <int DK, bool kBack>
 __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel(const LinParams p) {
     using Lay = OutSmem<DK>;
     constexpr int MT = DK / 64;
@@ -264,52 +245,51 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel
     Tables* tab = reinterpret_cast<Tables*>(smem + Lay::kTables);
     const int nt = p.DV >> 6, tile = blockIdx.x % nt, h = blockIdx.x / nt % p.Hkv, s = blockIdx.x / nt / p.Hkv;
     const Segment g = segment_at(p, s);
-    if (!g.live) return;
+    if (!g.live || g.r0 == g.r1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
     const int per = p.per, chunks = (g.r1 - g.r0 + kC - 1) / kC, items = chunks * per;
     const int i0 = (warp & 3) * 16, j0 = (warp >> 2) * 32;   // this warp's rows and columns
+    auto row_of = [&](int chunk) { return g.r0 + (kBack ? chunks - 1 - chunk : chunk) * kC; };
     auto issue = [&](int it) {
         if (it < items) {
-            const int chunk = it / per, x = it - chunk * per, r = g.r0 + chunk * kC, head = h * per + x;
-            const uint32_t a_at = base + ((kSum ? chunk : it) & 1) * Lay::kA;
-            const uint32_t b_at = base + Lay::kBCOff + ((kSum ? it : chunk) & 1) * Lay::kBC;
-            if (!kSum || x == 0) load_tile(a_at, p.a + (long)(kSum ? h : head) * DK, p.a_stride, DK, p, g, r);
-            if (kSum || x == 0) {
-                const long hb = kSum ? head : h;
-                load_tile(b_at, p.b + hb * DK, p.b_stride, DK, p, g, r);
-                load_tile(b_at + Lay::kA, p.c + hb * p.DV + tile * 64, p.c_stride, 64, p, g, r);
+            const int chunk = it / per, x = it - chunk * per, r = row_of(chunk), head = h * per + x;
+            const uint32_t a_at = base + ((kBack ? chunk : it) & 1) * Lay::kA;
+            const uint32_t b_at = base + Lay::kBCOff + ((kBack ? it : chunk) & 1) * Lay::kBC;
+            if (!kBack || x == 0) load_tile(a_at, p.a + (long)(kBack ? h : head) * DK, p.a_stride, DK, g, r);
+            if (kBack || x == 0) {
+                const long hb = kBack ? head : h;
+                load_tile(b_at, p.b + hb * DK, p.b_stride, DK, g, r);
+                load_tile(b_at + Lay::kA, p.c + hb * p.DV + tile * 64, p.c_stride, 64, g, r);
             }
         }
         copy_commit();
     };
     issue(0);
-    const float l2 = log2_decay(p, h);
-    fill_tables(tab, l2, p.e);
+    fill_tables<kBack>(tab, log2_decay(p, h));
     float X[MT][4][4];
     {
-        const long size = (long)DK * p.DV;
-        const bool more = !(g.first && g.last);   // (of several segments, each starts from the workspace)
-        const float* src = more ? p.states + ((long)s * p.Hkv + h) * size : p.init ? p.init + ((long)g.b * p.Hkv + h) * size : nullptr;
+        const float* src = lin_state_src(p, s, g.b, h);
+        const bool trans = p.split() ? p.states_trans : p.init_trans;
+        const float mul = p.split() ? 1.f : p.init_mul;
         each_pair<MT>(X, [&](int row, int col, float& x0, float& x1) {
             col += tile * 64;
             if (!src) {
                 x0 = x1 = 0.f;
-            } else if (!more && p.init_trans) {
-                x0 = p.init_mul * src[(long)col * DK + row];
-                x1 = p.init_mul * src[(long)(col + 1) * DK + row];
+            } else if (trans) {
+                x0 = mul * src[(long)col * DK + row];
+                x1 = mul * src[(long)(col + 1) * DK + row];
             } else {
                 const float2 y = *reinterpret_cast<const float2*>(src + (long)row * p.DV + col);
-                x0 = more ? y.x : p.init_mul * y.x;
-                x1 = more ? y.y : p.init_mul * y.y;
+                x0 = mul * y.x;
+                x1 = mul * y.y;
             }
         });
     }
-    const float whole = decay_pow(l2, kC);
     float acc[4][4];
     for (int it = 0; it < items; ++it) {
-        const int chunk = it / per, x = it - chunk * per, r0 = g.r0 + chunk * kC, n = min(kC, g.r1 - r0);
-        const uint32_t a_at = base + ((kSum ? chunk : it) & 1) * Lay::kA;
-        const uint32_t b_at = base + Lay::kBCOff + ((kSum ? it : chunk) & 1) * Lay::kBC, c_at = b_at + Lay::kA;
+        const int chunk = it / per, x = it - chunk * per, r0 = row_of(chunk), n = min(kC, g.r1 - r0);
+        const uint32_t a_at = base + ((kBack ? chunk : it) & 1) * Lay::kA;
+        const uint32_t b_at = base + Lay::kBCOff + ((kBack ? it : chunk) & 1) * Lay::kBC, c_at = b_at + Lay::kA;
         const uint32_t x_at = base + Lay::kX, p_at = base + Lay::kP;
         copy_wait0();
         __syncthreads();   // this item's tiles are there; everyone is done with the one before
@@ -319,9 +299,9 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel
                 *reinterpret_cast<uint32_t*>(smem + Lay::kX + row * 128 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2) =
                     pack_bf16x2(x0, x1);
             });
-        {   // P: rows i0 .. + 15, columns j0 .. + 31 (nothing above the diagonal)
+        {   // P: rows i0 .. + 15, columns j0 .. + 31 (nothing on the far side of the diagonal)
             float P[4][4] = {};
-            if (j0 <= i0 + 15) {
+            if (kBack ? j0 + 31 >= i0 : j0 <= i0 + 15) {
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     uint32_t af[4];
@@ -340,14 +320,15 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int i = i0 + g8 + 8 * z, j = j0 + y * 8 + 2 * t4;
-                    const float p0 = i >= j ? P[y][2 * z] * tab->pow[i - j] : 0.f;
-                    const float p1 = i >= j + 1 ? P[y][2 * z + 1] * tab->pow[i - j - 1] : 0.f;
+                    const int gap = kBack ? j - i : i - j, next = kBack ? gap + 1 : gap - 1;   // of columns j and j + 1
+                    const float p0 = gap >= 0 ? P[y][2 * z] * tab->pow[gap] : 0.f;
+                    const float p1 = next >= 0 ? P[y][2 * z + 1] * tab->pow[next] : 0.f;
                     *reinterpret_cast<uint32_t*>(smem + Lay::kP + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2) =
                         pack_bf16x2(p0, p1);
                 }
         }
         __syncthreads();
-        if (!kSum || x == 0) {   // what the state gives: a X
+        if (!kBack || x == 0) {   // what the state gives: a X
 #pragma unroll
             for (int y = 0; y < 4; ++y)
 #pragma unroll
@@ -364,7 +345,8 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel
                     mma_bf16(acc[2 * y + 1], af, bf[2], bf[3]);
                 }
             }
-            const float f0 = tab->into[i0 + g8], f1 = tab->into[i0 + g8 + 8];
+            const int i = i0 + g8;
+            const float f0 = tab->pow[kBack ? max(n - 1 - i, 0) : i + 1], f1 = tab->pow[kBack ? max(n - 9 - i, 0) : i + 9];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 acc[y][0] *= f0;
@@ -374,8 +356,8 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel
             }
         }
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {   // P c, tokens up to the rows' own
-            if (ks * 16 > i0) break;
+        for (int ks = 0; ks < 4; ++ks) {   // P c, tokens up to (backwards: from) the rows' own
+            if (kBack ? ks * 16 + 15 < i0 : ks * 16 > i0) continue;
             uint32_t af[4];
             ldsm4(tile_at(p_at, i0 + (lane & 15), ks * 16 + (lane >> 4) * 8), af);
 #pragma unroll
@@ -386,50 +368,47 @@ __global__ void __launch_bounds__(kLinThreads, DK <= 128 ? 2 : 1) lin_out_kernel
                 mma_bf16(acc[2 * y + 1], af, bf[2], bf[3]);
             }
         }
-        if (!kSum || x == per - 1) {
-            const long heads = kSum ? p.Hkv : (long)p.Hkv * per;
-            __nv_bfloat16* out = p.out + (kSum ? h : (long)h * per + x) * p.DV + tile * 64 + j0 + 2 * t4;
+        if (!kBack || x == per - 1) {
+            const long heads = kBack ? p.Hkv : (long)p.Hkv * per;
+            __nv_bfloat16* out = p.out + (kBack ? h : (long)h * per + x) * p.DV + tile * 64 + j0 + 2 * t4;
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-                const int i = i0 + g8 + 8 * z, r = r0 + i;
+                const int i = i0 + g8 + 8 * z;
                 if (i >= n) continue;
-                const long t = g.q0 + (p.reverse ? g.n - 1 - r : r);
+                const long t = g.q0 + r0 + i;
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                     *reinterpret_cast<uint32_t*>(out + t * heads * p.DV + y * 8) =
                         pack_bf16x2(acc[y][2 * z] * p.out_mul, acc[y][2 * z + 1] * p.out_mul);
             }
         }
-        const bool wanted = chunk < chunks - 1 || (g.last && p.final);   // (another segment's start is in the workspace)
-        if (wanted && (kSum || x == per - 1))
-            update_state<MT>(X, b_at, c_at, tab->w + kC - n, kSum && x > 0 ? 1.f : n == kC ? whole : decay_pow(l2, n));
+        if (chunk < chunks - 1 && (kBack || x == per - 1))
+            update_state<MT, 1>(X, b_at, c_at, weights<kBack>(tab, n), kBack && x > 0 ? 1.f : tab->pow[n]);
     }
     copy_wait0();
-    if (g.last && p.final) {
-        float* dst = p.final + ((long)g.b * p.Hkv + h) * DK * p.DV + tile * 64;
-        each_pair<MT>(X, [&](int row, int col, float x0, float x1) {
-            *reinterpret_cast<float2*>(dst + (long)row * p.DV + col) = make_float2(x0 * p.final_mul, x1 * p.final_mul);
-        });
-    }
 }
 
-template <int DK>
-cudaError_t launch_dk(const LinParams& p, bool split, bool sum, cudaStream_t stream) {
-    static std::atomic<unsigned long long> allowed[3];
+template <int DK, bool kBack>
+cudaError_t launch_dk(const LinParams& p, bool state, cudaStream_t stream) {
+    static std::atomic<unsigned long long> allowed[2];
     const unsigned ctas = (unsigned)((long)p.segments * p.Hkv * (p.DV / 64));
     cudaError_t e;
-    if (split) {
-        if ((e = allow_smem(lin_state_kernel<DK>, StateSmem<DK>::kBytes, allowed[0])) != cudaSuccess) return e;
-        lin_state_kernel<DK><<<ctas, kLinThreads, StateSmem<DK>::kBytes, stream>>>(p, sum ? p.per : 1);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const unsigned blocks = (unsigned)(((long)p.DK * p.DV + kLinThreads - 1) / kLinThreads * p.B * p.Hkv);
-        lin_scan_kernel<<<blocks, kLinThreads, 0, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (state) {
+        if ((e = allow_smem(lin_state_kernel<DK, kBack>, StateSmem<DK>::kBytes, allowed[0])) != cudaSuccess) return e;
+        lin_state_kernel<DK, kBack><<<ctas, kLinThreads, StateSmem<DK>::kBytes, stream>>>(p);
+    } else {
+        if ((e = allow_smem(lin_out_kernel<DK, kBack>, OutSmem<DK>::kBytes, allowed[1])) != cudaSuccess) return e;
+        lin_out_kernel<DK, kBack><<<ctas, kLinThreads, OutSmem<DK>::kBytes, stream>>>(p);
     }
-    auto kern = sum ? lin_out_kernel<DK, true> : lin_out_kernel<DK, false>;
-    if ((e = allow_smem(kern, OutSmem<DK>::kBytes, allowed[sum ? 1 : 2])) != cudaSuccess) return e;
-    kern<<<ctas, kLinThreads, OutSmem<DK>::kBytes, stream>>>(p);
     return cudaGetLastError();
+}
+template <bool kBack>
+cudaError_t launch_sync(const LinParams& p, bool state, cudaStream_t stream) {
+    if (p.DK == 64) return launch_dk<64, kBack>(p, state, stream);
+    if (p.DK == 128) return launch_dk<128, kBack>(p, state, stream);
+    if (p.DK == 192) return launch_dk<192, kBack>(p, state, stream);
+    if (p.DK == 256) return launch_dk<256, kBack>(p, state, stream);
+    return cudaErrorInvalidValue;
 }
 
 // ---------------------------------------------------------------- one token
@@ -497,27 +476,39 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const LinStepPar
 }  // namespace
 
 LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv) {
-    const long chunks = packed ? (long)L / kC + 1 : (long)B * ((L + kC - 1) / kC);
+    constexpr int kUnit = 128;   // a chunk of the tcgen05 kernels, two of the others
+    const long units = packed ? (long)L / kUnit + 1 : (long)B * ((L + kUnit - 1) / kUnit);
     const long tiles = (long)Hkv * ((d < dv ? d : dv) / 64);
-    const long longest = (L + kC - 1) / kC;   // chunks that a sequence can have
-    long seg = (chunks * tiles + 1215) / 1216;
-    if (seg < 4) seg = 4;
+    const long longest = (L + kUnit - 1) / kUnit;   // units that a sequence can have
+    long seg = (units * tiles + 1215) / 1216;
+    if (seg < 2) seg = 2;
     if (!packed && (long)B * tiles >= 304) seg = longest;
     if (seg > longest) seg = longest;
     if (seg < 1) seg = 1;
     LinPlan r;
     r.split = seg < longest;
-    r.seg_rows = (int)(seg * kC);
+    r.seg_rows = (int)(seg * kUnit);
     r.segments = packed ? L / r.seg_rows + B : B * (int)(L > 0 ? ((long)L + r.seg_rows - 1) / r.seg_rows : 1);
     return r;
 }
 
-cudaError_t launch_linear(const LinParams& p, bool split, bool sum, cudaStream_t stream) {
-    if (p.DK == 64) return launch_dk<64>(p, split, sum, stream);
-    if (p.DK == 128) return launch_dk<128>(p, split, sum, stream);
-    if (p.DK == 192) return launch_dk<192>(p, split, sum, stream);
-    if (p.DK == 256) return launch_dk<256>(p, split, sum, stream);
-    return cudaErrorInvalidValue;
+cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
+    if (!p.split()) return cudaSuccess;
+    cudaError_t e = cudaSuccess;
+    if (p.total > 0)
+        e = lin_on_tc(p.DK, p.DV) ? launch_linear_state_tc(p, maps, back, num_sms, stream)
+                                  : back ? launch_sync<true>(p, true, stream) : launch_sync<false>(p, true, stream);
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = (unsigned)((long)p.DK * p.DV / kLinThreads * p.B * p.Hkv);
+    if (back) lin_scan_kernel<true><<<blocks, kLinThreads, 0, stream>>>(p);
+    else lin_scan_kernel<false><<<blocks, kLinThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
+    if (p.total == 0) return cudaSuccess;
+    return lin_on_tc(p.DK, p.DV) ? launch_linear_out_tc(p, maps, back, num_sms, stream)
+                                 : back ? launch_sync<true>(p, false, stream) : launch_sync<false>(p, false, stream);
 }
 
 cudaError_t launch_linear_step(const LinStepParams& p, cudaStream_t stream) {

@@ -1,9 +1,10 @@
 """Linear attention with a decay per head against its definition in float64: forward, backward, single tokens.
 
-Bounds. Within chunks of 64 positions the kernels round P_ij = decay^(i-j) <a_i, b_j> and the state X that is
-carried in to bf16 (U = 2^-8 of each, half a step) before their products; the output is rounded once. Sums are
-fp32 and a state's weighted operand has 16 bits: F = 2^-15 of the sums of absolute values covers both (256
-products of 2^-24 each in a score, 2^-17 of the operand, 2^-24 per chunk added to a state, over fewer than 100).
+Bounds. Within chunks of 64 positions (128 where both head dims are 128) the kernels round P_ij = decay^(i-j) <a_i, b_j>
+and the state X that is carried in to bf16 (U = 2^-8 of each, half a step) before their products; what a chunk adds to X on
+the way to the next ones takes its weighted operand in bf16 (U of every term w_j b_j c_j, however they cancel). The output is
+rounded once. The states that leave a call take that operand in 24 bits. Sums are fp32: F = 2^-15 of the sums of absolute
+values covers them (256 products of 2^-24 each in a score, 2^-24 per chunk added to a state, over fewer than 100).
 """
 import math
 
@@ -14,7 +15,7 @@ from exact_attention_blackwell_tma_gb300 import binding
 
 gpu = pytest.mark.gpu
 
-U, F, CHUNK = 2.0 ** -8, 2.0 ** -15, 64
+U, F = 2.0 ** -8, 2.0 ** -15
 
 
 def definition(q, k, v, l, S0, scale):
@@ -41,21 +42,23 @@ def bounds(a, b, c, l, X0, e):
     """Error bounds of sum_(j<=i) D^(i-j) <a_i, b_j> c_j + D^(i+1-e) a_i X of one state head, [m][n, width] lists over
     its members (a: one per output, or one; b and c: one pair, or one per query head), and of the final state."""
     n, X = a[0].shape[0], X0
-    absX = X0.abs()
+    absX, absY = X0.abs(), torch.zeros_like(X0)   # with the state carried in, and without
+    chunk = 128 if X0.shape == (128, 128) else 64
     outs = [torch.zeros((n, c[0].shape[1]), dtype=torch.float64, device=a[0].device) for _ in a]
 
     def power(m):
         return torch.where(m > 0, torch.exp(l * m.clamp(min=1)), 1.0)
 
-    for s in range(0, n, CHUNK):
-        t = min(n, s + CHUNK)
+    # chunks are counted from the sequence's first token: a walk from its last (e = 1) meets the short one first
+    starts = [0, *range((n - 1) % chunk + 1 if e else chunk, n, chunk)] if n else []
+    for s, t in zip(starts, [*starts[1:], n]):
         i = torch.arange(t - s, device=a[0].device, dtype=torch.float64)
         gap = i[:, None] - i[None, :]
         D = torch.where(gap >= 0, power(gap), 0.0)
         into = power(i + 1 - e)[:, None]
         for m, x in enumerate(a):
             x = x[s:t]
-            bound = into * (U * (x.abs() @ X.abs()) + F * (x.abs() @ absX))
+            bound = into * (U * (x.abs() @ X.abs()) + U * (1 + U) * (x.abs() @ absY) + F * (x.abs() @ absX))
             for y, z in zip(b, c):
                 y, z = y[s:t], z[s:t]
                 bound = bound + U * ((x @ y.T * D).abs() @ z.abs()) + F * ((x.abs() @ y.abs().T * D) @ z.abs())
@@ -63,7 +66,8 @@ def bounds(a, b, c, l, X0, e):
         w = power(t - s - 1 - i + e)[:, None]
         over = power(torch.tensor(float(t - s), dtype=torch.float64, device=a[0].device))
         X = over * X + sum((w * y[s:t]).T @ z[s:t] for y, z in zip(b, c))
-        absX = over * absX + sum((w * y[s:t]).abs().T @ z[s:t].abs() for y, z in zip(b, c))
+        new = sum((w * y[s:t]).abs().T @ z[s:t].abs() for y, z in zip(b, c))
+        absX, absY = over * absX + new, over * absY + new
     return outs, F * absX
 
 
@@ -455,7 +459,9 @@ def test_refuses_sizes_and_workspaces(built):
     assert _codes(L=4096, ws=4112, n=need)[:2] == (binding.ATTN_ERR_ALIGN,) * 2
     assert _codes(B=0) == (binding.ATTN_OK,) * 3
     assert binding.attn_linear_workspace_size(1, 3, 2, 4096, False, 64, 64) == 0
-    assert binding.attn_linear_workspace_size(1, 2, 2, 64, False, 64, 64) == 0   # one segment: none needed
+    # one segment: for a final state alone
+    assert _codes(L=64, F=4096)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
+    assert binding.attn_linear_workspace_size(1, 2, 2, 64, False, 64, 64) == 2 * 64 * 64 * 4
 
 
 @gpu
