@@ -884,7 +884,7 @@ int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, co
     p->init_mul = p->final_mul = 1.f;
     p->status = di->status;
     p->wait_budget_ns = wait_budget_ns();
-    if (lin_on_tc(d, dv) && p->total > 0)
+    if (p->total > 0)
         for (int i = 0; i < n_tensors; ++i) {
             LinTensor& t = *tensors[i];
             if (!make_map_rows(&t.map, t.x, p->total, t.heads, t.width, (long)t.stride))
@@ -897,8 +897,6 @@ const __nv_bfloat16* bf16(const void* x) { return static_cast<const __nv_bfloat1
 
 // The roles of a product (linear.h)
 LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const LinTensor& c, void* out) {
-    p->a = bf16(a.x), p->b = bf16(b.x), p->c = bf16(c.x);
-    p->a_stride = (long)a.stride, p->b_stride = (long)b.stride, p->c_stride = (long)c.stride;
     p->out = static_cast<__nv_bfloat16*>(out);
     p->DK = a.width, p->DV = c.width;
     return LinMaps{a.map, b.map, c.map};

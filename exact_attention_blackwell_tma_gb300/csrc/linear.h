@@ -27,8 +27,6 @@
 namespace attn {
 
 struct LinParams {
-    const __nv_bfloat16 *a, *b, *c;
-    long a_stride, b_stride, c_stride;   // elements between tokens
     __nv_bfloat16* out;                  // tokens of heads x DV, contiguous
     const float* log_decay;              // [Hkv], natural log
     const float* init;                   // [B][Hkv][DK][DV] ([DV][DK] with init_trans), or null
@@ -56,18 +54,16 @@ struct LinPlan {
 };
 LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv);
 
-// Tensor maps of a, b and c for the tcgen05 kernels: 128 tokens x 64 channels
+// Tensor maps of a, b and c: 128 tokens x 64 channels of a head
 struct LinMaps {
     CUtensorMap a, b, c;
 };
-// Whether the tcgen05 kernels take these head dims (else those on mma.sync do)
-inline bool lin_on_tc(int DK, int DV) { return DK == 128 && DV == 128; }
 
 // The states that the segments start from, and the last one (nothing to do without several segments or `final`); the outputs
 cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
 cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
-cudaError_t launch_linear_state_tc(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
-cudaError_t launch_linear_out_tc(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
+// (the first half of the states: what each segment adds)
+cudaError_t launch_linear_shares(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
 
 struct LinStepParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -89,8 +85,21 @@ struct Segment {
 __device__ __forceinline__ int lin_seg_start(const LinParams& p, int b) {
     return p.cu ? __ldg(p.cu + b) / p.seg_rows + b : b * max(1, (p.rows + p.seg_rows - 1) / p.seg_rows);
 }
-// Offsets out of range make an empty sequence (reported); a start that is off only moves
-// segments that are then not live or read another one's state.
+// Rows [q0, q0 + n) of sequence b. Offsets out of range make an empty sequence (reported).
+__device__ __forceinline__ void lin_sequence(const LinParams& p, int b, int* q0, int* n) {
+    if (!p.cu) {
+        *q0 = b * p.rows;
+        *n = p.rows;
+        return;
+    }
+    *q0 = __ldg(p.cu + b);
+    *n = __ldg(p.cu + b + 1) - *q0;
+    if (*q0 < 0 || *n < 0 || *q0 > p.total - *n) {
+        atomicCAS(p.status, kStatusOk, kStatusBadPage);
+        *q0 = *n = 0;
+    }
+}
+// (A start that is off for bad offsets only moves segments, which are then not live or read another one's state.)
 __device__ __forceinline__ Segment segment_at(const LinParams& p, int s) {
     Segment g;
     if (p.cu) {
@@ -101,17 +110,10 @@ __device__ __forceinline__ Segment segment_at(const LinParams& p, int s) {
             else hi = mid - 1;
         }
         g.b = lo;
-        g.q0 = __ldg(p.cu + lo);
-        g.n = __ldg(p.cu + lo + 1) - g.q0;
-        if (g.q0 < 0 || g.n < 0 || g.q0 > p.total - g.n) {
-            atomicCAS(p.status, kStatusOk, kStatusBadPage);
-            g.q0 = g.n = 0;
-        }
     } else {
         g.b = s / max(1, (p.rows + p.seg_rows - 1) / p.seg_rows);
-        g.q0 = g.b * p.rows;
-        g.n = p.rows;
     }
+    lin_sequence(p, g.b, &g.q0, &g.n);
     const int i = s - lin_seg_start(p, g.b), count = max(1, (g.n + p.seg_rows - 1) / p.seg_rows);
     g.live = i >= 0 && i < count;
     g.first = i == 0;

@@ -1,21 +1,27 @@
-// Linear attention with a decay per head on tcgen05: head dims 128, 128 tokens a chunk.
-// linear.h gives the form (a, b, c, the state X) that the forward and the gradients share,
-// linear.cu the scan between the two kernels and the roundings.
+// Linear attention with a decay per head on tcgen05, 128 tokens a chunk. linear.h gives the form
+// (a, b, c, the state X) that the forward and the gradients share, linear.cu the scan between
+// the two kernels and the roundings.
 //
-// What bounds it: each chunk of a head brings 96 KB (32 KB each of a, b and c) and takes 32 KB
-// of output; at HBM speed an SM gets that in about 5600 cycles, of which the four products of
-// 128 x 128 x 128 take 2100 on the tensor cores (mma.sync, at a quarter of the rate and with its
-// operands through registers, set the time). So one CTA per SM walks segments, with the
-// next chunk's tiles in flight, and the roles
-//   warps 0-3  P: scores from tensor memory, times the decays, back as bf16 (the next
-//              product's A operand, over the scores' columns); b times the state's weights, in
-//              place in shared memory, once the scores have been taken from it
-//   warps 4-7  the state: X = D^n X + (the chunk's share), in registers in fp32, written to shared
-//              memory in bf16 for the next chunk; and the outputs, P c + D^(..) a X
-//   warp 8     tile loads (TMA), two stages
-//   warp 9     the products:  P = a b^T;  O2 = a X;  O1 = P c;  KV = (w b)^T c
-// Tensor memory: P (128 columns), O1, O2, KV: all 512. The tensor pipe executes in issue order,
-// so the next chunk's scores may be issued behind the product that reads P. Every wait is bounded.
+// What bounds it: for head dims of 128 a chunk of a head brings 96 KB (32 KB each of a, b and c)
+// and takes 32 KB of output, which is 5600 cycles of an SM's share of HBM's rate; its products take 2600
+// on the tensor cores (mma.sync, at a quarter of the rate and with its operands through
+// registers, set the time there). What costs is the chain through the chunks: scores, decays, product,
+// state, and the next chunk's product with it. So one CTA per SM walks segments with the
+// next tiles in flight, in roles that each take less than the loads do:
+//   warps 0-7    the state, X = D^n X + (the chunk's share), in registers in fp32, written to shared
+//                memory in bf16 for the next chunk; and the outputs, P c + D^(..) a X
+//   warps 8-15   P: scores from tensor memory, times the decays, back as bf16 over their columns (the
+//                next product's A operand); then b times the state's weights, in two bf16 terms,
+//                the first in place once the scores are taken
+//   warp 16      tile loads (TMA): a alone, b and c in a ring
+//   warp 17      the products, each issued by an elected lane of the converged warp:
+//                P = a b^T;  O2 = a X;  O1 = P c;  KV = (w b)^T c
+// The tensor pipe executes in issue order, so the next scores may be issued behind the product
+// that reads P. Every wait is bounded.
+//
+// DT of the output's columns per CTA: all 128 of them for head dims of 128, else 64, which is what
+// tensor memory (P 128 columns, O1, O2 and KV's two tiles of 128 channels) and shared memory hold at
+// 192 and 256; a and b are then read again, from L2, for the next columns.
 #include <atomic>
 
 #include "kv4.h"
@@ -27,91 +33,209 @@ namespace {
 
 constexpr int kCh = 128;                 // tokens of a chunk
 constexpr int kBox = 16384;              // 128 rows x 64 columns
-constexpr int kTile = 2 * kBox;          // 128 x 128
-constexpr uint32_t kTmemCols = 512, kTmP = 0, kTmO1 = 128, kTmO2 = 256, kTmKV = 384;
+constexpr int kHalf = kBox / 2;          // 64 rows
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// Two loads of 16 columns and one wait
+__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&r)[16], uint32_t (&s)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(s[0]), "=r"(s[1]),
+          "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7]), "=r"(s[8]), "=r"(s[9]), "=r"(s[10]),
+          "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15])
+        : "r"(t0), "r"(t1)
         : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// 32 bytes to memory: a whole sector per lane (16 at a time, a chunk's outputs kept the load/store unit busy for 2000 cycles)
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// tc_commit by the lane that the mma_.._w calls elect
+__device__ __forceinline__ void commit_w(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+// A bounded wait of the whole warp. All lanes poll (one access for the warp, no branch around it), and the clock is
+// read only after some polls: reading it first delays the warp's resumption.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const WaitCtx& w) {
+    uint64_t deadline = 0;
+    bool ok = true;
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if ((it & 63u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (deadline == 0) {
+                deadline = now + w.budget_ns;
+            } else if (*w.abort_flag || now > deadline) {
+                *w.abort_flag = 1;
+                atomicCAS(w.status, kStatusOk, kStatusWaitTimeout);
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(kFullMask, ok);
+}
+// Whether the phase has completed, without waiting
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return __shfl_sync(kFullMask, ok, 0) != 0;
 }
 __device__ __forceinline__ float lo16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-// 16 bytes of a tile: row, piece of eight columns (128-byte swizzle, boxes of 64 columns)
+// 16 bytes of a tile of boxes of `rows` rows x 64 columns (128-byte swizzle): row, piece of eight columns
+template <int kBoxBytes = kBox>
 __device__ __forceinline__ uint4* piece_at(uint8_t* tile, int row, int piece) {
-    return reinterpret_cast<uint4*>(tile + (piece >> 3) * kBox + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+    return reinterpret_cast<uint4*>(tile + (piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// The walk over the CTA's (segment, head) pairs, the same for every warp.
-struct Walk {
-    int s, h, chunks, items, per;
-    Segment g;
+// The CTA's (segment, head, tile of columns) triples. One warp finds them (a search over the offsets)
+// and hands them to the others through a ring in shared memory: the search in each role's loop made the code
+// several times as long, and warps that resume from a wait missed the instruction cache.
+struct Triple {
+    int s, b, h, tile, row0, rows;   // rows row0 .. of the tensors; rows = 0: the end
 };
-template <bool kBack>
-__device__ __forceinline__ bool next_pair(const LinParams& p, int& k, Walk& w, bool all) {
-    for (; k < p.segments * p.Hkv; k += gridDim.x) {
-        w.s = k / p.Hkv;
-        w.h = k - w.s * p.Hkv;
-        w.g = segment_at(p, w.s);
-        if (!w.g.live || w.g.r0 == w.g.r1) continue;
-        if (!all && (kBack ? w.g.first : w.g.last)) continue;
-        w.chunks = (w.g.r1 - w.g.r0 + kCh - 1) / kCh;
-        k += gridDim.x;
-        return true;
+constexpr int kTriples = 4;   // entries of the ring
+struct TripleRing {
+    Triple at[kTriples];
+};
+template <int DT, bool kBack>
+__device__ __forceinline__ void find_triples(const LinParams& p, TripleRing* ring, uint32_t full, uint32_t empty, const WaitCtx& w,
+                                             int lane, bool all) {
+    const int nt = p.DV / DT, n = p.segments * p.Hkv * nt;
+    uint32_t i = 0;
+    for (int k = blockIdx.x;; k += gridDim.x) {
+        Triple t{};
+        if (k < n) {
+            const int sh = k / nt;
+            t.tile = k - sh * nt;
+            t.s = sh / p.Hkv;
+            t.h = sh - t.s * p.Hkv;
+            const Segment g = segment_at(p, t.s);
+            if (!g.live || g.r0 == g.r1 || (!all && (kBack ? g.first : g.last))) continue;
+            t.b = g.b;
+            t.row0 = g.q0 + g.r0;
+            t.rows = g.r1 - g.r0;
+        }
+        if (!wait_all(empty + 8 * (i % kTriples), ((i / kTriples) & 1u) ^ 1u, w)) return;
+        if (lane == 0) {
+            ring->at[i % kTriples] = t;
+            mbar_arrive(full + 8 * (i % kTriples));
+        }
+        __syncwarp();
+        ++i;
+        if (k >= n) return;
     }
-    return false;
+}
+// A role's place in the walk. An item is a chunk (the outputs forwards, shares backwards: of one query head, x).
+struct Walk {
+    Triple t;
+    int chunks, chunk, x, per;
+    uint32_t taken;
+    bool live;
+};
+__device__ __forceinline__ bool next_triple(Walk& i, const TripleRing* ring, uint32_t full, uint32_t empty, const WaitCtx& w,
+                                            int lane) {
+    const uint32_t slot = i.taken % kTriples;
+    if (!wait_all(full + 8 * slot, (i.taken / kTriples) & 1u, w)) return false;
+    i.t = ring->at[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + 8 * slot);
+    ++i.taken;
+    i.chunks = (i.t.rows + kCh - 1) / kCh;
+    i.chunk = i.x = 0;
+    i.live = i.t.rows > 0;
+    return true;
 }
 template <bool kBack>
-__device__ __forceinline__ int chunk_row(const Walk& w, int chunk) {   // of the sequence
-    return w.g.r0 + (kBack ? w.chunks - 1 - chunk : chunk) * kCh;
+__device__ __forceinline__ int chunk_row(const Walk& i) {   // of the segment
+    return (kBack ? i.chunks - 1 - i.chunk : i.chunk) * kCh;
 }
+
+// Rows of (w b)^T c, the state's channels, come in tiles of 128. At 192 the second tile starts 64 early (its first
+// 64 rows are the first tile's), at 64 the tile's other rows are of whatever lies behind b (kTailPad: within the
+// buffers); neither are looked at.
+template <int DK>
+__host__ __device__ constexpr int tile_channel(int mt) { return DK > 128 && 128 * mt + 128 > DK ? DK - 128 : 128 * mt; }
+template <int DK>
+__device__ __forceinline__ bool tile_row(int mt, int row) { return tile_channel<DK>(mt) + row >= 128 * mt && tile_channel<DK>(mt) + row < DK; }
+template <int DK>
+__device__ __forceinline__ SmemDesc weighted_desc(uint32_t base, int mt, int box_bytes) {
+    return sdesc_sw128_split(base + tile_channel<DK>(mt) / 64 * box_bytes, box_bytes, 1024);
+}
+template <int DK>
+constexpr int kTailPad = DK == 64 ? kHalf : 0;
 
 // ---------------------------------------------------------------- outputs
+template <int DK, int DT>
 struct OutLay {
-    static constexpr int kStage = 3 * kTile, kXOff = 2 * kStage, kBarOff = kXOff + kTile;
-    static constexpr int kFull = 0, kEmpty = 2, kPFull = 4, kPReady = 5, kOFull = 6, kOFree = 7, kXReady = 8, kDrain = 9, kNumBars = 10;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8, kPowOff = kMiscOff + 16;   // D^0 .. D^31, per warp
-    static constexpr int kBytes = kPowOff + 4 * 32 * 4 + 1024;
+    static constexpr int MT = (DK + 127) / 128, kB = DK / 64 * kBox, kC = DT / 64 * kBox, kX = DT / 64 * DK * 128;
+    static constexpr int kRing = DK <= 192 ? 2 : 1;                       // stages of b and c
+    static constexpr int kTerm = DK / 64 * kHalf, kTerms = DK <= 128 ? 2 : 1;   // buffers of 64 tokens for the second term
+    static constexpr int kStage = kB + kC, kAOff = kRing * kStage, kXOff = kAOff + kB, kTermOff = kXOff + kX;
+    static constexpr int kBarOff = kTermOff + kTerms * kTerm + kTailPad<DK>;
+    static constexpr int kAFull = 0, kAFree = 1, kBFull = 2, kBFree = 4, kPFull = 6, kPReady = 7, kWReady = 8, kTFree = 10,
+                         kOFull = 12, kOFree = 13, kXReady = 14, kDrain = 15, kRFull = 16, kREmpty = kRFull + kTriples,
+                         kNumBars = kREmpty + kTriples;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8, kRingOff = kMiscOff + 16;
+    static constexpr int kPowOff = kRingOff + (int)sizeof(TripleRing), kBytes = kPowOff + 8 * 64 * 4;   // 64 floats for each of warps 8-15
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
+    static constexpr uint32_t kTmP = 0, kTmO1 = 128, kTmO2 = 128 + DT, kTmKV = 128 + 2 * DT;
+    static_assert(kTmKV + MT * DT <= 512, "tensor memory budget");
 };
-constexpr int kOutThreads = 320;
+constexpr int kOutThreads = 640;
+// registers per thread: at launch, and as the roles share them (their sum over the five warpgroups is the launch's)
+constexpr int kOutRegs = 96, kOutRegsX = 120, kOutRegsP = 88, kOutRegsRest = 64;
+static_assert(2 * kOutRegsX + 2 * kOutRegsP + kOutRegsRest <= 5 * kOutRegs, "registers of the launch");
 
-template <bool kBack>
+template <int DK, int DT, bool kBack>
 __global__ void __launch_bounds__(kOutThreads, 1)
 lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
-    using Lay = OutLay;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t* smem = smem_raw + (base - raw);
+    using Lay = OutLay<DK, DT>;
+    constexpr int MT = Lay::MT, HC = DT / 2;   // HC: columns of a warp of the states and outputs
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMiscOff + 4);
+    TripleRing* ring = reinterpret_cast<TripleRing*>(smem + Lay::kRingOff);
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(Lay::kFull + s), 1);
-            mbar_init(bar(Lay::kEmpty + s), 1);
+        for (int i = 0; i < Lay::kNumBars; ++i) {
+            const bool by_256 = i == Lay::kPReady || i == Lay::kWReady || i == Lay::kWReady + 1 || i == Lay::kOFree || i == Lay::kXReady;
+            mbar_init(bar(i), by_256 ? 256 : i >= Lay::kREmpty ? 18 : 1);
         }
-        mbar_init(bar(Lay::kPFull), 1);
-        mbar_init(bar(Lay::kPReady), 128);
-        mbar_init(bar(Lay::kOFull), 1);
-        mbar_init(bar(Lay::kOFree), 128);
-        mbar_init(bar(Lay::kXReady), 128);
-        mbar_init(bar(Lay::kDrain), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 16 && lane == 0) {
         tma_prefetch_desc(&maps.a);
         tma_prefetch_desc(&maps.b);
         tma_prefetch_desc(&maps.c);
     }
-    if (warp == 9) {
-        tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+    if (warp == 17) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -121,306 +245,438 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
     const int per = p.per;
     Walk at;
-    int k = blockIdx.x;
+    at.per = per;
+    at.taken = 0;
+    bool ok = true;
+    auto take = [&] { return next_triple(at, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane); };
+    auto advance = [&] {   // to the next item; true where a new triple is due
+        if (++at.x < at.per) return false;
+        at.x = 0;
+        return ++at.chunk == at.chunks;
+    };
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ loads
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && next_pair<kBack>(p, k, at, true)) {
-            for (int i = 0; i < at.chunks * per && ok; ++i, ++it) {
-                const int chunk = i / per, x = i - chunk * per, row = at.g.q0 + chunk_row<kBack>(at, chunk);
-                const int ha = kBack ? at.h : at.h * per + x, hb = kBack ? at.h * per + x : at.h;
-                const uint32_t st = it & 1u;
-                ok = warp_wait(bar(Lay::kEmpty + st), ((it >> 1) & 1u) ^ 1u, w, lane);
-                if (ok && lane == 0) {
-                    const uint32_t to = base + st * Lay::kStage, full = bar(Lay::kFull + st);
-                    mbar_expect_tx(full, 3 * kTile);
+    if (warp >= 16) {
+        setmaxnreg_dec<kOutRegsRest>();
+        if (warp == 18) {
+            find_triples<DT, kBack>(p, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, true);
+        } else if (warp == 16) {
+            // ------------------------------------------------------------ loads
+            uint32_t na = 0, nb = 0;
+            for (bool fresh = true;; fresh = advance()) {
+                if (fresh && !(ok = take())) break;
+                if (!at.live) break;
+                const int row = at.t.row0 + chunk_row<kBack>(at);
+                const int ha = kBack ? at.t.h : at.t.h * per + at.x, hb = kBack ? at.t.h * per + at.x : at.t.h;
+                if (kBack || at.x == 0) {
+                    const uint32_t st = nb % Lay::kRing, full = bar(Lay::kBFull + st), to = base + st * Lay::kStage;
+                    if (!(ok = wait_all(bar(Lay::kBFree + st), ((nb / Lay::kRing) & 1u) ^ 1u, w))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(full, Lay::kStage);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        tma_load_3d(to + y * kBox, &maps.a, full, y * 64, ha, row);
-                        tma_load_3d(to + kTile + y * kBox, &maps.b, full, y * 64, hb, row);
-                        tma_load_3d(to + 2 * kTile + y * kBox, &maps.c, full, y * 64, hb, row);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        if (lane == 0)   // (a pending load must land before the CTA gives up its memory)
-            for (uint32_t i = 0; i < 2 && i < it; ++i) {
-                const uint32_t n = it - 1 - i;
-                if (ok || i > 0) drain_wait(bar(Lay::kFull + (n & 1u)), (n >> 1) & 1u, p.wait_budget_ns);
-            }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ products
-        constexpr uint32_t kIdP = idesc_bf16_f32(128, 128, false, false);    // a, b: rows of channels
-        constexpr uint32_t kIdN = idesc_bf16_f32(128, 128, false, true);     // B (X, c): rows along the sum
-        constexpr uint32_t kIdKV = idesc_bf16_f32(128, 128, true, true);     // (w b)^T, c: rows of tokens
-        const SmemDesc a_km = sdesc_sw128_split(base, 16, 1024), b_km = sdesc_sw128_split(base + kTile, 16, 1024);
-        const SmemDesc b_mn = sdesc_sw128_split(base + kTile, kBox, 1024), c_mn = sdesc_sw128_split(base + 2 * kTile, kBox, 1024);
-        const SmemDesc x_mn = sdesc_sw128_split(base + Lay::kXOff, kBox, 1024);
-        uint32_t it = 0, outs = 0, xs = 0;   // items, rounds of the outputs' columns, states
-        bool ok = true;
-        while (ok && next_pair<kBack>(p, k, at, true)) {
-            for (int i = 0; i < at.chunks * per; ++i, ++it) {
-                const int x = i % per;
-                const uint32_t st = it & 1u, off = desc_step(st * Lay::kStage);
-                const bool head = !kBack || x == 0, tail = !kBack || x == per - 1;   // of a round of the outputs
-                const bool shares = kBack || x == per - 1;                          // this item adds to the state
-                if (!(ok = warp_wait(bar(Lay::kFull + st), (it >> 1) & 1u, w, lane))) break;
-                tc_fence_after_sync();
-                if (lane == 0) {
+                        for (int y = 0; y < DK / 64; ++y) tma_load_3d(to + y * kBox, &maps.b, full, y * 64, hb, row);
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const uint32_t step = desc_step((y >> 2) * kBox + (y & 3) * 32);
-                        mma_ss(tmem + kTmP, a_km, off + step, b_km, off + step, kIdP, y > 0);
+                        for (int y = 0; y < DT / 64; ++y)
+                            tma_load_3d(to + Lay::kB + y * kBox, &maps.c, full, at.t.tile * DT + y * 64, hb, row);
                     }
-                    tc_commit(bar(Lay::kPFull));
-                }
-                __syncwarp();
-                if (head) {
-                    if (x == 0) {
-                        if (!(ok = warp_wait(bar(Lay::kXReady), xs & 1u, w, lane))) break;
-                        ++xs;
-                    }
-                    if (!(ok = warp_wait(bar(Lay::kOFree), (outs & 1u) ^ 1u, w, lane))) break;
-                    tc_fence_after_sync();
-                    if (lane == 0)
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            mma_ss(tmem + kTmO2, a_km, off + desc_step((y >> 2) * kBox + (y & 3) * 32), x_mn, desc_step(y * 2048),
-                                   kIdN, y > 0);
                     __syncwarp();
+                    ++nb;
                 }
-                if (!(ok = warp_wait(bar(Lay::kPReady), it & 1u, w, lane))) break;
-                tc_fence_after_sync();
-                if (lane == 0) {
+                if (!kBack || at.x == 0) {
+                    if (!(ok = wait_all(bar(Lay::kAFree), (na & 1u) ^ 1u, w))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(bar(Lay::kAFull), Lay::kB);
+#pragma unroll
+                        for (int y = 0; y < DK / 64; ++y)
+                            tma_load_3d(base + Lay::kAOff + y * kBox, &maps.a, bar(Lay::kAFull), y * 64, ha, row);
+                    }
+                    __syncwarp();
+                    ++na;
+                }
+            }
+            if (lane == 0) {   // (a pending load must land before the CTA gives up its memory)
+                if (na > 0) drain_wait(bar(Lay::kAFull), (na - 1) & 1u, p.wait_budget_ns);
+                for (uint32_t i = nb > Lay::kRing ? nb - Lay::kRing : 0; i < nb; ++i)
+                    drain_wait(bar(Lay::kBFull + i % Lay::kRing), (i / Lay::kRing) & 1u, p.wait_budget_ns);
+            }
+            __syncwarp();
+        } else if (warp == 17) {
+            // ------------------------------------------------------------ products
+            constexpr uint32_t kIdP = idesc_bf16_f32(128, 128, false, false);    // a, b: rows of channels
+            constexpr uint32_t kIdN = idesc_bf16_f32(128, DT, false, true);      // B (X, c): rows along the sum
+            constexpr uint32_t kIdKV = idesc_bf16_f32(128, DT, true, true);      // (w b)^T, c: rows of tokens
+            const SmemDesc a_km = sdesc_sw128_split(base + Lay::kAOff, 16, 1024), b_km = sdesc_sw128_split(base, 16, 1024);
+            const SmemDesc c_mn = sdesc_sw128_split(base + Lay::kB, kBox, 1024);
+            const SmemDesc x_mn = sdesc_sw128_split(base + Lay::kXOff, DK * 128, 1024);
+            uint32_t na = 0, nb = 0, it = 0, outs = 0, xs = 0, shared = 0;   // loads taken, items, rounds of O, states, shares
+            // `at` is an item ahead: what is finished here is the one before, if any
+            bool some = false, shares = false, last_x = false;
+            int x = 0;
+            uint32_t st = 0;
+            for (bool fresh = true;; fresh = advance()) {
+                const uint32_t off = desc_step(st * Lay::kStage);
+                const bool head = !kBack || x == 0, tail = !kBack || last_x;   // of a round of the outputs
+                if (some) {
+                    if (head) {
+                        if (x == 0) {
+                            if (!(ok = wait_all(bar(Lay::kXReady), xs & 1u, w))) break;
+                            ++xs;
+                        }
+                        if (!(ok = wait_all(bar(Lay::kOFree), (outs & 1u) ^ 1u, w))) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int y = 0; y < DK / 16; ++y)
+                            mma_ss_w(tmem + Lay::kTmO2, a_km, desc_step((y >> 2) * kBox + (y & 3) * 32), x_mn, desc_step(y * 2048),
+                                     kIdN, y > 0);
+                        if (!kBack || per == 1) commit_w(bar(Lay::kAFree));
+                    }
+                    if (!(ok = wait_all(bar(Lay::kPReady), it & 1u, w))) break;
+                    tc_fence_after_sync();
 #pragma unroll
                     for (int y = 0; y < 8; ++y)
-                        mma_ts(tmem + kTmO1, tmem + kTmP + y * 8, c_mn, off + desc_step(y * 2048), kIdN, !head || y > 0);
-                    if (shares)
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            mma_ss(tmem + kTmKV, b_mn, off + desc_step(y * 2048), c_mn, off + desc_step(y * 2048), kIdKV,
-                                   (kBack && x > 0) || y > 0);
-                    tc_commit(bar(Lay::kEmpty + st));
-                    if (tail) tc_commit(bar(Lay::kOFull));
+                        mma_ts_w(tmem + Lay::kTmO1, tmem + Lay::kTmP + (y >> 1) * 32 + (y & 1) * 8, c_mn, off + desc_step(y * 2048),
+                                 kIdN, !head || y > 0);
+                    ++it;
                 }
-                __syncwarp();
-                if (tail) ++outs;
-            }
-        }
-        if (lane == 0) {
-            tc_commit(bar(Lay::kDrain));
-            drain_wait(bar(Lay::kDrain), 0, p.wait_budget_ns);
-        }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ------------------------------------------------------------ P, and the weights on b
-        const uint32_t t_p = tmem + ((uint32_t)(warp * 32) << 16) + kTmP;
-        float* pow = reinterpret_cast<float*>(smem + Lay::kPowOff) + warp * 32;
-        uint32_t it = 0;
-        bool ok = true;
-        float l2 = 0.f;
-        int head_of = -1;
-        while (ok && next_pair<kBack>(p, k, at, true)) {
-            if (at.h != head_of) {
-                l2 = log2_decay(p, at.h);
-                head_of = at.h;
-                __syncwarp();
-                pow[lane] = decay_pow(l2, lane);
-                __syncwarp();
-            }
-            const int row = warp * 32 + lane;
-            // to columns of a block of 32 on the near side: the distance to the block's nearer end, then pow[]
-            float far[4];
+                if (fresh && !(ok = take())) break;
+                const bool new_a = !kBack || at.x == 0, new_b = kBack || at.x == 0;
+                const uint32_t b_full = bar(Lay::kBFull + nb % Lay::kRing), b_parity = (nb / Lay::kRing) & 1u;
+                // the next scores come first if their tiles have come: they have the longer way to go
+                const bool early = some && at.live && (!new_a || warp_test(bar(Lay::kAFull), na & 1u)) &&
+                                   (!new_b || warp_test(b_full, b_parity));
+#pragma unroll 1
+                for (int turn = 0; turn < 2 && ok; ++turn) {
+                    if ((turn == 0) == early) {
+                        if (!at.live) continue;
+                        if (new_a && !(ok = wait_all(bar(Lay::kAFull), na & 1u, w))) break;
+                        if (new_b && !(ok = wait_all(b_full, b_parity, w))) break;
+                        na += new_a;
+                        nb += new_b;
+                        tc_fence_after_sync();
+                        const uint32_t next = desc_step((nb - 1) % Lay::kRing * Lay::kStage);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int d = kBack ? 32 * b - row : row - 32 * b - 31;
-                far[b] = d >= 0 ? decay_pow(l2, d) : 0.f;
-            }
-            for (int i = 0; i < at.chunks * per; ++i, ++it) {
-                const int chunk = i / per, x = i - chunk * per;
-                const int n = min(kCh, at.g.r1 - chunk_row<kBack>(at, chunk));
-                const bool shares = kBack || x == per - 1;
-                const float weight = row < n ? decay_pow(l2, kBack ? row + 1 : n - 1 - row) : 0.f;
-                uint8_t* tiles = smem + (it & 1u) * Lay::kStage;
-                if (!(ok = warp_wait(bar(Lay::kPFull), it & 1u, w, lane))) break;
-                tc_fence_after_sync();
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t out[32];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int b = 2 * half + y;   // columns 32 b .. + 31
-                        const bool near = kBack ? b > warp : b < warp;
-                        if (near || b == warp) {
-                            uint32_t r[32];
-                            tmem_ld32(t_p + 32 * b, r);
-                            if (near) {
-                                const float f = far[b];
-                                const int end = n - 32 * b;   // (backwards: the columns that exist)
-#pragma unroll
-                                for (int c = 0; c < 32; c += 4) {
-                                    const float4 t = *reinterpret_cast<const float4*>(pow + (kBack ? c : 28 - c));
-                                    const float q[4] = {kBack ? t.x : t.w, kBack ? t.y : t.z, kBack ? t.z : t.y, kBack ? t.w : t.x};
-                                    float v[4];
-#pragma unroll
-                                    for (int z = 0; z < 4; ++z)
-                                        v[z] = kBack && c + z >= end ? 0.f : __uint_as_float(r[c + z]) * (f * q[z]);
-                                    out[16 * y + c / 2] = pack_bf16x2(v[0], v[1]);
-                                    out[16 * y + c / 2 + 1] = pack_bf16x2(v[2], v[3]);
+                        for (int y = 0; y < DK / 16; ++y) {
+                            const uint32_t step = desc_step((y >> 2) * kBox + (y & 3) * 32);
+                            mma_ss_w(tmem + Lay::kTmP, a_km, step, b_km, next + step, kIdP, y > 0);
+                        }
+                        commit_w(bar(Lay::kPFull));
+                        if (kBack && per > 1 && at.x == per - 1) commit_w(bar(Lay::kAFree));   // (a X came with x = 0)
+                    } else if (some) {
+                        if (shares) {
+#pragma unroll 1
+                            for (int half = 0; half < 2; ++half) {
+                                if (half < 3 - Lay::kTerms) {   // (one pass over all rows, or two over 64)
+                                    if (!(ok = wait_all(bar(Lay::kWReady + half), shared & 1u, w))) break;
+                                    tc_fence_after_sync();
                                 }
-                            } else {
+                                const uint32_t rows = off + desc_step(half * kHalf), buf = Lay::kTerms == 2 ? half : 0;
+                                const uint32_t more = (kBack && x > 0) || half > 0;
+#pragma unroll 1
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    const SmemDesc b_mn = weighted_desc<DK>(base, mt, kBox);
+                                    const SmemDesc t_mn = weighted_desc<DK>(base + Lay::kTermOff + buf * Lay::kTerm, mt, kHalf);
+                                    const uint32_t kv = tmem + Lay::kTmKV + mt * DT;
 #pragma unroll
-                                for (int c = 0; c < 32; c += 2) {
-                                    const int d0 = kBack ? c - lane : lane - c, d1 = kBack ? d0 + 1 : d0 - 1;
-                                    const float v0 = d0 >= 0 && (!kBack || 32 * b + c < n) ? __uint_as_float(r[c]) * pow[d0] : 0.f;
-                                    const float v1 = d1 >= 0 && (!kBack || 32 * b + c + 1 < n) ? __uint_as_float(r[c + 1]) * pow[d1] : 0.f;
-                                    out[16 * y + c / 2] = pack_bf16x2(v0, v1);
+                                    for (int y = 0; y < 4; ++y)
+                                        mma_ss_w(kv, b_mn, rows + desc_step(y * 2048), c_mn, rows + desc_step(y * 2048), kIdKV,
+                                                 y > 0 ? 1u : more);
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y)
+                                        mma_ss_w(kv, t_mn, desc_step(y * 2048), c_mn, rows + desc_step(y * 2048), kIdKV, 1);
                                 }
+                                if (half >= Lay::kTerms - 1) commit_w(bar(Lay::kTFree + Lay::kTerms - 1));
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) out[16 * y + c] = 0u;
+                            if (!ok) break;
+                            ++shared;
+                        }
+                        if (kBack || last_x) commit_w(bar(Lay::kBFree + st));
+                        if (tail) {
+                            commit_w(bar(Lay::kOFull));
+                            ++outs;
                         }
                     }
-                    tmem_st32(t_p + 32 * half, out);
                 }
-                if (n < kCh && row >= n) {   // c's rows past the sequence's end, whatever they hold
+                if (!ok || !at.live) break;
+                some = true;
+                x = at.x;
+                last_x = x == per - 1;
+                shares = (kBack || last_x) && at.chunk + 1 < at.chunks;   // the item adds to the state
+                st = (nb - 1) % Lay::kRing;
+            }
+            commit_w(bar(Lay::kDrain));
+            if (lane == 0) drain_wait(bar(Lay::kDrain), 0, p.wait_budget_ns);
+            __syncwarp();
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ P, and the weights on b
+        setmaxnreg_dec<kOutRegsP>();
+        const int q4 = warp & 3, hf = (warp - 8) >> 2, t = tid - 256, row = q4 * 32 + lane;
+        const uint32_t t_p = tmem + ((uint32_t)(q4 * 32) << 16) + Lay::kTmP;
+        // Decays of at least 2^-4 keep the factor 2^(31 * 4) that a row's own block needs in range; the others look each power up
+        constexpr float kSlowest = -4.f;
+        // pw[c]: forwards D^(31 - c), zeros from 32 on; backwards D^(c - 32), zeros up to there
+        float* pw = reinterpret_cast<float*>(smem + Lay::kPowOff) + (warp - 8) * 64;
+        const float* near_pw = pw + (kBack ? 32 : 0);
+        const float* own_pw = pw + (kBack ? 32 - lane : 31 - lane);
+        uint32_t it = 0, nb = 0, shared = 0;
+        float l2 = 0.f, far0 = 0.f, far1 = 0.f, diag = 0.f;
+        for (bool fresh = true;; fresh = advance(), ++it) {
+            if (fresh) {
+                if (!(ok = take()) || !at.live) break;
+                l2 = log2_decay(p, at.t.h);
+                __syncwarp();
+                pw[lane] = kBack ? 0.f : decay_pow(l2, 31 - lane);
+                pw[32 + lane] = kBack ? decay_pow(l2, lane) : 0.f;
+                __syncwarp();
+                // to a block of 32 columns on the near side: the distance to its nearer end, then near_pw
+                const int d0 = kBack ? 32 * hf - row : row - 32 * hf - 31, d1 = kBack ? d0 + 64 : d0 - 64;
+                far0 = d0 >= 0 ? decay_pow(l2, d0) : 0.f;
+                far1 = d1 >= 0 ? decay_pow(l2, d1) : 0.f;
+                diag = exp2f(l2 * (kBack ? -lane : lane - 31));   // (the same, to the block that holds the row: not below 1)
+            }
+            const int n = min(kCh, at.t.rows - chunk_row<kBack>(at));
+            const bool shares = (kBack || at.x == per - 1) && at.chunk + 1 < at.chunks;
+            if (kBack || at.x == 0) ++nb;
+            uint8_t* tiles = smem + (nb - 1) % Lay::kRing * Lay::kStage;
+            if (!(ok = wait_all(bar(Lay::kPFull), it & 1u, w))) break;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int b = hf; b < 4; b += 2) {   // columns 32 b .. + 31; P goes to the first 16 of them
+                uint32_t out[16];
+                if (b == q4 || (kBack ? b > q4 : b < q4)) {
+                    uint32_t r[32];
+                    tmem_ld32(t_p + 32 * b, r);
+                    if (kBack && n < 32 * b + 32) {   // columns past the sequence's end, whatever they hold
+                        const int end = n - 32 * b;
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) *piece_at(tiles + 2 * kTile, row, c) = make_uint4(0, 0, 0, 0);
+                        for (int c = 0; c < 32; ++c)
+                            if (c >= end) r[c] = 0u;
+                    }
+                    if (b != q4 || l2 >= kSlowest) {
+                        const float far = b == q4 ? diag : b == hf ? far0 : far1;
+                        const uint64_t f = f32x2(far, far);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(near_pw + c);
+                            float v[4];
+                            f32x2_split(fmul2(f32x2(u2f(r[c]), u2f(r[c + 1])), fmul2(f, g.x)), v[0], v[1]);
+                            f32x2_split(fmul2(f32x2(u2f(r[c + 2]), u2f(r[c + 3])), fmul2(f, g.y)), v[2], v[3]);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                if (b == q4 && (kBack ? c + z < lane : c + z > lane)) v[z] = 0.f;
+                            out[c / 2] = pack_bf16x2(v[0], v[1]);
+                            out[c / 2 + 1] = pack_bf16x2(v[2], v[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float v0 = (kBack ? c >= lane : c <= lane) ? u2f(r[c]) * own_pw[c] : 0.f;
+                            const float v1 = (kBack ? c + 1 >= lane : c + 1 <= lane) ? u2f(r[c + 1]) * own_pw[c + 1] : 0.f;
+                            out[c / 2] = pack_bf16x2(v0, v1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) out[c] = 0u;
                 }
-                if (shares) {   // (the scores have been taken: b may change)
+                tmem_st16(t_p + 32 * b, out);
+            }
+            if (n < kCh && (kBack || at.x == 0)) {   // c's rows past the sequence's end, whatever they hold
+                const int r = t & 127;
+                if (r >= n)
+                    for (int c = t >> 7; c < DT / 8; c += 2) *piece_at(tiles + Lay::kB, r, c) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before_sync();
+            mbar_arrive(bar(Lay::kPReady));
+            if (!shares) continue;
+            // as many rows at a time as there are buffers for; a thread takes every kLanes-th piece of its row, so that
+            // eight neighbouring rows lie in eight banks
+            constexpr int kRows = 64 * Lay::kTerms, kLanes = 256 / kRows, kPieces = DK / 8 / kLanes, kAtOnce = kPieces % 3 == 0 ? 3 : 4;
+#pragma unroll 1
+            for (int r0 = 0; r0 < kCh; r0 += kRows) {
+                const int r = r0 + (t & (kRows - 1)), p0 = t / kRows;
+                const uint32_t use = r0 == 0 ? 0 : 1, round = Lay::kTerms == 2 ? shared : 2 * shared + use;
+                const float weight = r < n ? decay_pow(l2, kBack ? r + 1 : n - 1 - r) : 0.f;
+                uint8_t* second = smem + Lay::kTermOff + (Lay::kTerms == 2 ? (r >> 6) * Lay::kTerm : 0);
+                if (!(ok = wait_all(bar(Lay::kTFree + Lay::kTerms - 1), (round & 1u) ^ 1u, w))) break;
+#pragma unroll 1
+                for (int y0 = 0; y0 < kPieces; y0 += kAtOnce) {
+                    uint4 v[kAtOnce];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        uint4* at16 = piece_at(tiles + kTile, row, c);
-                        const uint4 v = *at16;
-                        auto scaled = [&](uint32_t u) { return pack_bf16x2(lo16(u) * weight, hi16(u) * weight); };
-                        *at16 = row < n ? make_uint4(scaled(v.x), scaled(v.y), scaled(v.z), scaled(v.w)) : make_uint4(0, 0, 0, 0);
+                    for (int y = 0; y < kAtOnce; ++y) v[y] = *piece_at(tiles, r, p0 + kLanes * (y0 + y));
+#pragma unroll
+                    for (int y = 0; y < kAtOnce; ++y) {
+                        const uint32_t u[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float f0 = lo16(u[z]) * weight, f1 = hi16(u[z]) * weight;
+                            hi[z] = pack_bf16x2(f0, f1);
+                            lo[z] = pack_bf16x2(f0 - lo16(hi[z]), f1 - hi16(hi[z]));
+                        }
+                        if (kBack && r >= n) hi[0] = hi[1] = hi[2] = hi[3] = lo[0] = lo[1] = lo[2] = lo[3] = 0u;
+                        const int c = p0 + kLanes * (y0 + y);
+                        *piece_at(tiles, r, c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *piece_at<kHalf>(second, r & 63, c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 fence_proxy_async_smem();
-                tmem_st_wait();
-                tc_fence_before_sync();
-                mbar_arrive(bar(Lay::kPReady));
+                mbar_arrive(bar(Lay::kWReady + use));
             }
+            if (!ok) break;
+            ++shared;
         }
     } else {
         // ------------------------------------------------------------ the state and the outputs
-        const int row = (warp & 3) * 32 + lane;   // of X (a channel) and of the outputs (a token)
-        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        uint8_t* xs = smem + Lay::kXOff;
+        setmaxnreg_inc<kOutRegsX>();
+        const int q4 = warp & 3, col0 = (warp >> 2) * HC, row = q4 * 32 + lane;   // of X (a tile's) and of the outputs
+        const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16) + col0;
+        at.per = kBack ? 1 : per;   // (backwards one round of outputs for all query heads)
         uint32_t outs = 0;
-        bool ok = true;
-        float X[128];
-        auto store_x = [&] {
+        float X[MT][HC];
+        float l2 = 0.f, into = 0.f, over = 0.f;
+        const bool whole_sectors = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;   // (rows are multiples of 128 bytes)
+        __nv_bfloat16* out = nullptr;   // null: this thread's token does not exist
+        // `at` is an item ahead: the outputs are those of the one before, if any; `last`: of a segment
+        bool some = false, moves = false, last = true;
+        for (bool fresh = true;; fresh = advance()) {
+            if (fresh && !(ok = take())) break;
+            if (last && at.live) {   // (X is in shared memory: the registers take the next segment's)
+                l2 = log2_decay(p, at.t.h);
+                const float* src = lin_state_src(p, at.t.s, at.t.b, at.t.h);
+                const float mul = p.split() ? 1.f : p.init_mul;
+                const bool trans = p.split() ? p.states_trans : p.init_trans;
+                const int c0 = at.t.tile * DT + col0;
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                *piece_at(xs, row, c) = make_uint4(pack_bf16x2(X[8 * c], X[8 * c + 1]), pack_bf16x2(X[8 * c + 2], X[8 * c + 3]),
-                                                   pack_bf16x2(X[8 * c + 4], X[8 * c + 5]), pack_bf16x2(X[8 * c + 6], X[8 * c + 7]));
-            fence_proxy_async_smem();
-            mbar_arrive(bar(Lay::kXReady));
-        };
-        while (ok && next_pair<kBack>(p, k, at, true)) {
-            const float l2 = log2_decay(p, at.h);
-            const float* src = lin_state_src(p, at.s, at.g.b, at.h);
-            const float mul = p.split() ? 1.f : p.init_mul;
-            if (!src) {
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int r = tile_channel<DK>(mt) + row;
+                    if (!src || !tile_row<DK>(mt, row)) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c) X[c] = 0.f;
-            } else if (p.split() ? p.states_trans : p.init_trans) {
+                        for (int c = 0; c < HC; ++c) X[mt][c] = 0.f;
+                    } else if (trans) {
+                        const float* from = src + (long)c0 * DK + r;
 #pragma unroll
-                for (int c = 0; c < 128; ++c) X[c] = mul * src[c * 128 + row];
-            } else {
+                        for (int c = 0; c < HC; ++c) X[mt][c] = mul * from[c * DK];
+                    } else {
+                        const float* from = src + (long)r * p.DV + c0;
 #pragma unroll
-                for (int c = 0; c < 128; c += 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(src + row * 128 + c);
-                    X[c] = mul * y.x, X[c + 1] = mul * y.y, X[c + 2] = mul * y.z, X[c + 3] = mul * y.w;
-                }
-            }
-            store_x();   // (the products that read the last pair's are done: its last round of outputs was waited for)
-            for (int chunk = 0; chunk < at.chunks && ok; ++chunk) {
-                const int r0 = chunk_row<kBack>(at, chunk), n = min(kCh, at.g.r1 - r0);
-                const float into = row < n ? decay_pow(l2, kBack ? n - 1 - row : row + 1) : 0.f;
-                for (int x = 0; x < (kBack ? 1 : per); ++x, ++outs) {
-                    if (!(ok = warp_wait(bar(Lay::kOFull), outs & 1u, w, lane))) break;
-                    tc_fence_after_sync();
-                    if ((kBack || x == per - 1) && chunk + 1 < at.chunks) {
-                        const float over = decay_pow(l2, n);
-#pragma unroll
-                        for (int c = 0; c < 128; c += 16) {
-                            uint32_t r[16];
-                            tmem_ld16(t_row + kTmKV + c, r);
-#pragma unroll
-                            for (int z = 0; z < 16; ++z) X[c + z] = fmaf(X[c + z], over, __uint_as_float(r[z]));
-                        }
-                        store_x();
-                    }
-                    __nv_bfloat16* out = p.out + ((long)(at.g.q0 + r0 + row) * (kBack ? p.Hkv : p.Hkv * per) + (kBack ? at.h : at.h * per + x)) * 128;
-#pragma unroll
-                    for (int c = 0; c < 128; c += 16) {
-                        uint32_t o1[16], o2[16], o[8];
-                        tmem_ld16(t_row + kTmO1 + c, o1);
-                        tmem_ld16(t_row + kTmO2 + c, o2);
-#pragma unroll
-                        for (int z = 0; z < 8; ++z)
-                            o[z] = pack_bf16x2(p.out_mul * fmaf(into, __uint_as_float(o2[2 * z]), __uint_as_float(o1[2 * z])),
-                                               p.out_mul * fmaf(into, __uint_as_float(o2[2 * z + 1]), __uint_as_float(o1[2 * z + 1])));
-                        if (row < n) {
-                            *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        for (int c = 0; c < HC; c += 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(from + c);
+                            X[mt][c] = mul * y.x, X[mt][c + 1] = mul * y.y, X[mt][c + 2] = mul * y.z, X[mt][c + 3] = mul * y.w;
                         }
                     }
-                    tc_fence_before_sync();
-                    mbar_arrive(bar(Lay::kOFree));
                 }
             }
+            if (some) {
+                if (!(ok = wait_all(bar(Lay::kOFull), outs & 1u, w))) break;
+                tc_fence_after_sync();
+                if (moves && !last) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int c = 0; c < HC; c += 32) {
+                            uint32_t r[32];
+                            tmem_ld32(t_row + Lay::kTmKV + mt * DT + c, r);
+#pragma unroll
+                            for (int z = 0; z < 32; ++z) X[mt][c + z] = fmaf(X[mt][c + z], over, u2f(r[z]));
+                        }
+                }
+            }
+            // (the products with the last X are done: the outputs that use it are here)
+            if (last ? at.live : moves) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    if (tile_row<DK>(mt, row)) {
+#pragma unroll
+                        for (int c = 0; c < HC; c += 8)
+                            *piece_at<DK * 128>(smem + Lay::kXOff, tile_channel<DK>(mt) + row, (col0 + c) >> 3) =
+                                make_uint4(pack_bf16x2(X[mt][c], X[mt][c + 1]), pack_bf16x2(X[mt][c + 2], X[mt][c + 3]),
+                                           pack_bf16x2(X[mt][c + 4], X[mt][c + 5]), pack_bf16x2(X[mt][c + 6], X[mt][c + 7]));
+                    }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(Lay::kXReady));
+            }
+            if (some) {
+#pragma unroll 1
+                for (int c = 0; c < HC; c += 16) {
+                    uint32_t o1[16], o2[16], o[8];
+                    tmem_ld16x2(t_row + Lay::kTmO1 + c, t_row + Lay::kTmO2 + c, o1, o2);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z)
+                        o[z] = pack_bf16x2(fmaf(into, u2f(o2[2 * z]), p.out_mul * u2f(o1[2 * z])),
+                                           fmaf(into, u2f(o2[2 * z + 1]), p.out_mul * u2f(o1[2 * z + 1])));
+                    if (out && whole_sectors) {
+                        store32(out + c, o);
+                    } else if (out) {
+                        *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(bar(Lay::kOFree));
+                ++outs;
+            }
+            if (!at.live) break;
+            some = true;
+            const int r0 = chunk_row<kBack>(at), n = min(kCh, at.t.rows - r0);
+            moves = at.x == at.per - 1;
+            last = moves && at.chunk + 1 == at.chunks;
+            into = p.out_mul * (row < n ? decay_pow(l2, kBack ? n - 1 - row : row + 1) : 0.f);
+            over = decay_pow(l2, n);
+            out = row < n ? p.out + ((long)(at.t.row0 + r0 + row) * (kBack ? p.Hkv : p.Hkv * per) + (kBack ? at.t.h : at.t.h * per + at.x)) * p.DV +
+                                at.t.tile * DT + col0
+                          : nullptr;
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, 512);
     }
 }
 
 // ---------------------------------------------------------------- segments' shares
 // X' of a segment for X = 0: one sum over its tokens in tensor memory, each weighted by the
 // decay up to the segment's end (backwards: its start), b times that weight in three bf16 terms
-// (all of its 24 bits): the first in place, the others in buffers of 64 tokens, two of each.
+// (all of its 24 bits): the first in place, the others in buffers of 64 tokens.
+template <int DK, int DT>
 struct StateLay {
-    static constexpr int kStage = 2 * kTile, kTermOff = 2 * kStage, kTerm = kTile / 2;   // [buffer][term] of 64 x 128
-    static constexpr int kBarOff = kTermOff + 4 * kTerm;
-    static constexpr int kFull = 0, kEmpty = 2, kWReady = 4, kWFree = 6, kSFull = 8, kSFree = 10, kDrain = 12, kNumBars = 13;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8, kBytes = kMiscOff + 16 + 1024;
+    static constexpr int MT = (DK + 127) / 128, kB = DK / 64 * kBox, kC = DT / 64 * kBox, kStage = kB + kC;
+    static constexpr int kTerm = DK / 64 * kHalf, kSets = DK <= 192 ? 2 : 1;   // sets of buffers
+    static constexpr int kTermOff = 2 * kStage, kBarOff = kTermOff + kSets * 2 * kTerm + kTailPad<DK>;
+    static constexpr int kFull = 0, kEmpty = 2, kWReady = 4, kWFree = 6, kSFull = 8, kSFree = 10, kDrain = 12, kRFull = 13,
+                         kREmpty = kRFull + kTriples, kNumBars = kREmpty + kTriples;
+    static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16, kRingOff = kMiscOff + 16;
+    static constexpr int kBytes = kRingOff + (int)sizeof(TripleRing);
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
+    static constexpr uint32_t kAcc = MT * DT, kCols = 2 * kAcc <= 128 ? 128 : 256;
+    static_assert(2 * kAcc <= kCols, "tensor memory budget");
 };
-constexpr int kStateThreads = 448;   // warps 0-7: weights, 8-11: results, 12: loads, 13: products
+constexpr int kStateThreads = 480;   // warps 0-7: weights, 8-11: results, 12: loads, 13: products, 14: triples
 
-template <bool kBack>
+template <int DK, int DT, bool kBack>
 __global__ void __launch_bounds__(kStateThreads, 1)
 lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
-    using Lay = StateLay;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t* smem = smem_raw + (base - raw);
+    using Lay = StateLay<DK, DT>;
+    constexpr int MT = Lay::MT;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMiscOff + 4);
+    TripleRing* ring = reinterpret_cast<TripleRing*>(smem + Lay::kRingOff);
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(Lay::kFull + s), 1);
-            mbar_init(bar(Lay::kEmpty + s), 1);
-            mbar_init(bar(Lay::kWReady + s), 256);
-            mbar_init(bar(Lay::kWFree + s), 1);
-            mbar_init(bar(Lay::kSFull + s), 1);
-            mbar_init(bar(Lay::kSFree + s), 128);
+        for (int i = 0; i < Lay::kNumBars; ++i) {
+            const bool by_256 = i == Lay::kWReady || i == Lay::kWReady + 1, by_128 = i == Lay::kSFree || i == Lay::kSFree + 1;
+            mbar_init(bar(i), by_256 ? 256 : by_128 ? 128 : i >= Lay::kREmpty ? 14 : 1);
         }
-        mbar_init(bar(Lay::kDrain), 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -429,7 +685,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         tma_prefetch_desc(&maps.c);
     }
     if (warp == 13) {
-        tmem_alloc(smem_addr(tmem_slot), 256);
+        tmem_alloc(smem_addr(tmem_slot), Lay::kCols);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -437,103 +693,113 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
-    const int per = kBack ? p.per : 1;
-    const bool all = p.final != nullptr;
     Walk at;
-    int k = blockIdx.x;
+    at.per = kBack ? p.per : 1;
+    at.taken = 0;
+    bool ok = true;
+    auto take = [&] { return next_triple(at, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane); };
+    auto advance = [&] {   // to the next item; true where a new triple is due
+        if (++at.x < at.per) return false;
+        at.x = 0;
+        return ++at.chunk == at.chunks;
+    };
+    uint32_t it = 0;
 
-    if (warp == 12) {
+    if (warp == 14) {
+        // (without a final state the segment that a walk visits last is not needed)
+        find_triples<DT, kBack>(p, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, p.final != nullptr);
+    } else if (warp == 12) {
         // ------------------------------------------------------------ loads
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && next_pair<kBack>(p, k, at, all)) {
-            for (int i = 0; i < at.chunks * per && ok; ++i, ++it) {
-                const int chunk = i / per, x = i - chunk * per, row = at.g.q0 + chunk_row<kBack>(at, chunk);
-                const int hb = at.h * per + x;
-                const uint32_t st = it & 1u;
-                ok = warp_wait(bar(Lay::kEmpty + st), ((it >> 1) & 1u) ^ 1u, w, lane);
-                if (ok && lane == 0) {
-                    const uint32_t to = base + st * Lay::kStage, full = bar(Lay::kFull + st);
-                    mbar_expect_tx(full, 2 * kTile);
+        for (bool fresh = true;; fresh = advance(), ++it) {
+            if (fresh && !(ok = take())) break;
+            if (!at.live) break;
+            const int row = at.t.row0 + chunk_row<kBack>(at), hb = at.t.h * at.per + at.x;
+            const uint32_t st = it & 1u;
+            if (!(ok = wait_all(bar(Lay::kEmpty + st), ((it >> 1) & 1u) ^ 1u, w))) break;
+            if (lane == 0) {
+                const uint32_t to = base + st * Lay::kStage, full = bar(Lay::kFull + st);
+                mbar_expect_tx(full, Lay::kStage);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        tma_load_3d(to + y * kBox, &maps.b, full, y * 64, hb, row);
-                        tma_load_3d(to + kTile + y * kBox, &maps.c, full, y * 64, hb, row);
-                    }
-                }
-                __syncwarp();
+                for (int y = 0; y < DK / 64; ++y) tma_load_3d(to + y * kBox, &maps.b, full, y * 64, hb, row);
+#pragma unroll
+                for (int y = 0; y < DT / 64; ++y)
+                    tma_load_3d(to + Lay::kB + y * kBox, &maps.c, full, at.t.tile * DT + y * 64, hb, row);
             }
+            __syncwarp();
         }
         if (lane == 0)
-            for (uint32_t i = 0; i < 2 && i < it; ++i) {
-                const uint32_t n = it - 1 - i;
-                if (ok || i > 0) drain_wait(bar(Lay::kFull + (n & 1u)), (n >> 1) & 1u, p.wait_budget_ns);
-            }
+            for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i)
+                drain_wait(bar(Lay::kFull + (i & 1u)), (i >> 1) & 1u, p.wait_budget_ns);
         __syncwarp();
     } else if (warp == 13) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t kIdKV = idesc_bf16_f32(128, 128, true, true);
-        const SmemDesc b_mn = sdesc_sw128_split(base, kBox, 1024), c_mn = sdesc_sw128_split(base + kTile, kBox, 1024);
-        const SmemDesc t_mn = sdesc_sw128_split(base + Lay::kTermOff, Lay::kTerm / 2, 1024);   // (boxes of 64 rows)
-        uint32_t it = 0, pairs = 0;
-        bool ok = true;
-        while (ok && next_pair<kBack>(p, k, at, all)) {
-            const uint32_t acc = tmem + (pairs & 1u) * 128;
-            if (!(ok = warp_wait(bar(Lay::kSFree + (pairs & 1u)), ((pairs >> 1) & 1u) ^ 1u, w, lane))) break;
-            for (int i = 0; i < at.chunks * per && ok; ++i, ++it) {
-                const uint32_t st = it & 1u, off = desc_step(st * Lay::kStage);
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = warp_wait(bar(Lay::kWReady + half), it & 1u, w, lane))) break;
-                    tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint32_t c0 = off + desc_step(half * 8192);
+        constexpr uint32_t kIdKV = idesc_bf16_f32(128, DT, true, true);
+        const SmemDesc c_mn = sdesc_sw128_split(base + Lay::kB, kBox, 1024);
+        uint32_t sums = 0;
+        for (bool fresh = true;; ++it) {
+            if (fresh && !(ok = take())) break;
+            if (!at.live) break;
+            const uint32_t acc = tmem + (sums & 1u) * Lay::kAcc, st = it & 1u, off = desc_step(st * Lay::kStage);
+            if (fresh && !(ok = wait_all(bar(Lay::kSFree + (sums & 1u)), ((sums >> 1) & 1u) ^ 1u, w))) break;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = wait_all(bar(Lay::kWReady + half), it & 1u, w))) break;
+                tc_fence_after_sync();
+                const uint32_t c0 = off + desc_step(half * kHalf), set = Lay::kSets == 2 ? half : 0, more = !fresh || half > 0;
+#pragma unroll 1
+                for (int mt = 0; mt < MT; ++mt) {
+                    const SmemDesc b_mn = weighted_desc<DK>(base, mt, kBox);
+                    const SmemDesc t_mn = weighted_desc<DK>(base + Lay::kTermOff + 2 * set * Lay::kTerm, mt, kHalf);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            mma_ss(acc, b_mn, c0 + desc_step(y * 2048), c_mn, c0 + desc_step(y * 2048), kIdKV, i > 0 || half > 0 || y > 0);
+                    for (int y = 0; y < 4; ++y)
+                        mma_ss_w(acc + mt * DT, b_mn, c0 + desc_step(y * 2048), c_mn, c0 + desc_step(y * 2048), kIdKV, y > 0 ? 1u : more);
 #pragma unroll
-                        for (int term = 0; term < 2; ++term)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                mma_ss(acc, t_mn, desc_step((2 * half + term) * Lay::kTerm + y * 2048), c_mn, c0 + desc_step(y * 2048), kIdKV, 1);
-                        tc_commit(bar(Lay::kWFree + half));
-                        if (half == 1) tc_commit(bar(Lay::kEmpty + st));
-                        if (half == 1 && i + 1 == at.chunks * per) tc_commit(bar(Lay::kSFull + (pairs & 1u)));
-                    }
-                    __syncwarp();
+                    for (int y = 0; y < 8; ++y)
+                        mma_ss_w(acc + mt * DT, t_mn, desc_step((y >> 2) * Lay::kTerm + (y & 3) * 2048), c_mn,
+                                 c0 + desc_step((y & 3) * 2048), kIdKV, 1);
                 }
+                commit_w(bar(Lay::kWFree + set));
             }
-            ++pairs;
+            if (!ok) break;
+            commit_w(bar(Lay::kEmpty + st));
+            fresh = advance();
+            if (fresh) commit_w(bar(Lay::kSFull + (sums++ & 1u)));
         }
-        if (lane == 0) {
-            tc_commit(bar(Lay::kDrain));
-            drain_wait(bar(Lay::kDrain), 0, p.wait_budget_ns);
-        }
+        commit_w(bar(Lay::kDrain));
+        if (lane == 0) drain_wait(bar(Lay::kDrain), 0, p.wait_budget_ns);
         __syncwarp();
     } else if (warp < 8) {
         // ------------------------------------------------------------ weights
         // a thread takes pieces x, x + 4, .. of a row, so that eight neighbouring rows lie in eight banks
         const int r64 = tid & 63, p0 = tid >> 6;
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && next_pair<kBack>(p, k, at, all)) {
-            const float l2 = log2_decay(p, at.h);
-            for (int i = 0; i < at.chunks * per && ok; ++i, ++it) {
-                const int r0 = chunk_row<kBack>(at, i / per);
-                const uint32_t st = it & 1u;
-                uint8_t* tiles = smem + st * Lay::kStage;
-                if (!(ok = warp_wait(bar(Lay::kFull + st), (it >> 1) & 1u, w, lane))) break;
-                for (int half = 0; half < 2; ++half) {
-                    const int row = half * 64 + r64, r = r0 + row;
-                    const bool in = r < at.g.r1;
-                    const float weight = in ? decay_pow(l2, kBack ? r - at.g.r0 + 1 : at.g.r1 - 1 - r) : 0.f;
-                    uint8_t* terms = smem + Lay::kTermOff + 2 * half * Lay::kTerm;
-                    if (!(ok = warp_wait(bar(Lay::kWFree + half), (it & 1u) ^ 1u, w, lane))) break;
+        float l2 = 0.f;
+        for (bool fresh = true;; fresh = advance(), ++it) {
+            if (fresh) {
+                if (!(ok = take()) || !at.live) break;
+                l2 = log2_decay(p, at.t.h);
+            }
+            const int r0 = chunk_row<kBack>(at);
+            const uint32_t st = it & 1u;
+            uint8_t* tiles = smem + st * Lay::kStage;
+            if (!(ok = wait_all(bar(Lay::kFull + st), (it >> 1) & 1u, w))) break;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int row = half * 64 + r64, r = r0 + row;
+                const uint32_t use = 2 * it + half, set = use % Lay::kSets;
+                const bool in = r < at.t.rows;
+                const float weight = in ? decay_pow(l2, kBack ? r + 1 : at.t.rows - 1 - r) : 0.f;
+                uint8_t* buf = smem + Lay::kTermOff + 2 * set * Lay::kTerm;
+                if (!(ok = wait_all(bar(Lay::kWFree + set), ((use / Lay::kSets) & 1u) ^ 1u, w))) break;
+                constexpr int kPieces = DK / 32, kAtOnce = kPieces % 3 == 0 ? 3 : 2;
+#pragma unroll 1
+                for (int y0 = 0; y0 < kPieces; y0 += kAtOnce) {
+                    uint4 v[kAtOnce];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int c = p0 + 4 * y;
-                        uint4* at16 = piece_at(tiles, row, c);
-                        const uint4 v = *at16;
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    for (int y = 0; y < kAtOnce; ++y) v[y] = *piece_at(tiles, row, p0 + 4 * (y0 + y));
+#pragma unroll
+                    for (int y = 0; y < kAtOnce; ++y) {
+                        const uint32_t u[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+                        const int c = p0 + 4 * (y0 + y);
                         uint32_t o[3][4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
@@ -545,70 +811,105 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                                 f1 -= hi16(o[term][z]);
                             }
                         }
-                        *at16 = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+                        *piece_at(tiles, row, c) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
 #pragma unroll
                         for (int term = 1; term < 3; ++term)
-                            *reinterpret_cast<uint4*>(terms + (term - 1) * Lay::kTerm + (c >> 3) * (Lay::kTerm / 2) + r64 * 128 +
-                                                      (((c & 7) ^ (r64 & 7)) << 4)) =
+                            *piece_at<kHalf>(buf + (term - 1) * Lay::kTerm, r64, c) =
                                 make_uint4(o[term][0], o[term][1], o[term][2], o[term][3]);
-                        if (!in) *piece_at(tiles + kTile, row, c) = make_uint4(0, 0, 0, 0);
                     }
-                    fence_proxy_async_smem();
-                    mbar_arrive(bar(Lay::kWReady + half));
                 }
+                if (!in)
+                    for (int c = p0; c < DT / 8; c += 4) *piece_at(tiles + Lay::kB, row, c) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                mbar_arrive(bar(Lay::kWReady + half));
             }
+            if (!ok) break;
         }
     } else {
         // ------------------------------------------------------------ results
         const int row = (warp & 3) * 32 + lane;
-        uint32_t pairs = 0;
-        bool ok = true;
-        while (ok && next_pair<kBack>(p, k, at, all)) {
-            if (!(ok = warp_wait(bar(Lay::kSFull + (pairs & 1u)), (pairs >> 1) & 1u, w, lane))) break;
+        for (uint32_t sums = 0;; ++sums) {
+            if (!(ok = take()) || !at.live) break;
+            if (!(ok = wait_all(bar(Lay::kSFull + (sums & 1u)), (sums >> 1) & 1u, w))) break;
             tc_fence_after_sync();
-            float* dst = p.states + (((long)at.s * p.Hkv + at.h) * 128 + row) * 128;
-            const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (pairs & 1u) * 128;
+            const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (sums & 1u) * Lay::kAcc;
+#pragma unroll 1
+            for (int mt = 0; mt < MT; ++mt) {
+                float* dst = p.states + (((long)at.t.s * p.Hkv + at.t.h) * DK + tile_channel<DK>(mt) + row) * p.DV + at.t.tile * DT;
+#pragma unroll 1
+                for (int c = 0; c < DT; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(t_row + mt * DT + c, r);
+                    if (tile_row<DK>(mt, row)) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(t_row + c, r);
-#pragma unroll
-                for (int z = 0; z < 16; z += 4) *reinterpret_cast<uint4*>(dst + c + z) = make_uint4(r[z], r[z + 1], r[z + 2], r[z + 3]);
+                        for (int z = 0; z < 32; z += 8)   // (the workspace is 256-byte aligned)
+                            store32(dst + c + z, {r[z], r[z + 1], r[z + 2], r[z + 3], r[z + 4], r[z + 5], r[z + 6], r[z + 7]});
+                    }
+                }
             }
             tc_fence_before_sync();
-            mbar_arrive(bar(Lay::kSFree + (pairs & 1u)));
-            ++pairs;
+            mbar_arrive(bar(Lay::kSFree + (sums & 1u)));
         }
     }
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 13) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, Lay::kCols);
     }
 }
 
 template <class Kernel>
-cudaError_t launch_tc(Kernel kern, int threads, int bytes, std::atomic<unsigned long long>& allowed, const LinParams& p,
-                      const LinMaps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tc(Kernel kern, int threads, int bytes, long triples, std::atomic<unsigned long long>& allowed,
+                      const LinParams& p, const LinMaps& maps, int num_sms, cudaStream_t stream) {
     cudaError_t e = allow_smem(kern, bytes, allowed);
     if (e != cudaSuccess) return e;
-    const long pairs = (long)p.segments * p.Hkv;
-    kern<<<(unsigned)(pairs < num_sms ? pairs : num_sms), threads, bytes, stream>>>(maps, p);
+    kern<<<(unsigned)(triples < num_sms ? triples : num_sms), threads, bytes, stream>>>(maps, p);
     return cudaGetLastError();
+}
+// The registers that the roles share out must be those of the launch (asked once per kernel and device set)
+template <class Kernel>
+cudaError_t check_regs(Kernel kern, std::atomic<int>& done) {
+    if (done.load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kOutRegs) return cudaErrorInvalidConfiguration;
+    done.store(1, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+template <int DK, int DT, bool kBack>
+cudaError_t launch_one(bool outputs, const LinParams& p, const LinMaps& maps, int num_sms, cudaStream_t stream) {
+    static std::atomic<unsigned long long> allowed[2];
+    static std::atomic<int> regs;
+    const long triples = (long)p.segments * p.Hkv * (p.DV / DT);
+    if (!outputs)
+        return launch_tc(lin_state_tc_kernel<DK, DT, kBack>, kStateThreads, StateLay<DK, DT>::kBytes, triples, allowed[0], p, maps,
+                         num_sms, stream);
+    const cudaError_t e = check_regs(lin_out_tc_kernel<DK, DT, kBack>, regs);
+    if (e != cudaSuccess) return e;
+    return launch_tc(lin_out_tc_kernel<DK, DT, kBack>, kOutThreads, OutLay<DK, DT>::kBytes, triples, allowed[1], p, maps, num_sms,
+                     stream);
+}
+template <bool kBack>
+cudaError_t launch_dims(bool outputs, const LinParams& p, const LinMaps& maps, int num_sms, cudaStream_t stream) {
+    if (p.DK == 64) return launch_one<64, 64, kBack>(outputs, p, maps, num_sms, stream);
+    if (p.DK == 128 && p.DV == 128) return launch_one<128, 128, kBack>(outputs, p, maps, num_sms, stream);
+    if (p.DK == 128) return launch_one<128, 64, kBack>(outputs, p, maps, num_sms, stream);
+    if (p.DK == 192) return launch_one<192, 64, kBack>(outputs, p, maps, num_sms, stream);
+    if (p.DK == 256) return launch_one<256, 64, kBack>(outputs, p, maps, num_sms, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_linear_state_tc(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
-    static std::atomic<unsigned long long> allowed[2];
-    return launch_tc(back ? lin_state_tc_kernel<true> : lin_state_tc_kernel<false>, kStateThreads, StateLay::kBytes, allowed[back],
-                     p, maps, num_sms, stream);
+cudaError_t launch_linear_shares(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
+    return back ? launch_dims<true>(false, p, maps, num_sms, stream) : launch_dims<false>(false, p, maps, num_sms, stream);
 }
-cudaError_t launch_linear_out_tc(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
-    static std::atomic<unsigned long long> allowed[2];
-    return launch_tc(back ? lin_out_tc_kernel<true> : lin_out_tc_kernel<false>, kOutThreads, OutLay::kBytes, allowed[back], p, maps,
-                     num_sms, stream);
+cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
+    if (p.total == 0) return cudaSuccess;
+    return back ? launch_dims<true>(true, p, maps, num_sms, stream) : launch_dims<false>(true, p, maps, num_sms, stream);
 }
 
 }  // namespace attn
