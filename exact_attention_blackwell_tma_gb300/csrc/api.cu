@@ -835,13 +835,13 @@ int check_linear(int B, int H, int Hkv, int L, const int* cu, int d, int dv, flo
     return ATTN_OK;
 }
 
-// [rows, H, d] bf16 with `stride` elements between rows, in boxes of 128 rows x 64 columns of one head
-bool make_map_rows(CUtensorMap* m, const void* ptr, long rows, int H, int d, long stride) {
+// [rows, H, d] bf16 with `stride` elements between rows, in boxes of box_rows rows x 64 columns of one head
+bool make_map_rows(CUtensorMap* m, const void* ptr, long rows, int H, int d, long stride, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[3] = {64u, 1, 128u};
+    cuuint32_t box[3] = {64u, 1, (cuuint32_t)box_rows};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -853,15 +853,17 @@ struct LinTensor {
     const void* x;
     long long stride;
     int heads, width;
-    CUtensorMap map;
+    int box_rows = 128;
+    CUtensorMap map = {};
 };
+LinTensor lin_output(void* x, int heads, int width) { return LinTensor{x, (long long)heads * width, heads, width, 32}; }
 
 size_t linear_bytes(const LinPlan& plan, int Hkv, int d, int dv) { return (size_t)plan.segments * Hkv * d * dv * sizeof(float); }
 
 // What the four products of linear attention share; the roles of the tensors come on top.
 int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, const float* log_decay, bool final,
                   void* workspace, size_t ws_bytes, LinTensor* const* tensors, int n_tensors, LinParams* p, DevInfo* di) {
-    const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, d, dv);
+    const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, d, dv, final);
     if ((double)plan.segments * Hkv * ((d > dv ? d : dv) / 64) >= 2.0e9 || (double)B * Hkv * d * dv / 256 >= 2.0e9)
         return fail(ATTN_ERR_ARG, "linear: too many sequences and heads");
     const size_t need = plan.split || final ? linear_bytes(plan, Hkv, d, dv) : 0;
@@ -887,7 +889,7 @@ int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, co
     if (p->total > 0)
         for (int i = 0; i < n_tensors; ++i) {
             LinTensor& t = *tensors[i];
-            if (!make_map_rows(&t.map, t.x, p->total, t.heads, t.width, (long)t.stride))
+            if (!make_map_rows(&t.map, t.x, p->total, t.heads, t.width, (long)t.stride, t.box_rows))
                 return fail(ATTN_ERR_LAUNCH, "cuTensorMapEncodeTiled failed");
         }
     return ATTN_OK;
@@ -896,10 +898,10 @@ int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, co
 const __nv_bfloat16* bf16(const void* x) { return static_cast<const __nv_bfloat16*>(x); }
 
 // The roles of a product (linear.h)
-LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const LinTensor& c, void* out) {
-    p->out = static_cast<__nv_bfloat16*>(out);
+LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const LinTensor& c, const LinTensor& out) {
+    p->out = static_cast<__nv_bfloat16*>(const_cast<void*>(out.x));
     p->DK = a.width, p->DV = c.width;
-    return LinMaps{a.map, b.map, c.map};
+    return LinMaps{a.map, b.map, c.map, out.map};
 }
 
 }  // namespace
@@ -907,7 +909,9 @@ LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const
 extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v) {
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
     if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
-    return linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v), Hkv, d, d_v);
+    const size_t with = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, true), Hkv, d, d_v);
+    const size_t without = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, false), Hkv, d, d_v);
+    return with > without ? with : without;
 }
 
 extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -924,13 +928,13 @@ extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long
     if (rows && ((rc = check_stride("q", q_stride, (long long)H * d)) || (rc = check_stride("k", k_stride, (long long)Hkv * d)) ||
                  (rc = check_stride("v", v_stride, (long long)Hkv * d_v))))
         return rc;
-    LinTensor tq{q, q_stride, H, d, {}}, tk{k, k_stride, Hkv, d, {}}, tv{v, v_stride, Hkv, d_v, {}};
-    LinTensor* const all[] = {&tq, &tk, &tv};
+    LinTensor tq{q, q_stride, H, d}, tk{k, k_stride, Hkv, d}, tv{v, v_stride, Hkv, d_v}, to = lin_output(o, H, d_v);
+    LinTensor* const all[] = {&tq, &tk, &tv, &to};
     LinParams p{};
     DevInfo di;
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, final_state != nullptr, workspace, ws_bytes, all, 3, &p, &di)))
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, final_state != nullptr, workspace, ws_bytes, all, 4, &p, &di)))
         return rc;
-    const LinMaps maps = linear_roles(&p, tq, tk, tv, o);
+    const LinMaps maps = linear_roles(&p, tq, tk, tv, to);
     p.init = state;
     p.final = final_state;
     p.out_mul = scale;
@@ -957,17 +961,17 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
                  (rc = check_stride("v", v_stride, (long long)Hkv * d_v)) ||
                  (rc = check_stride("dout", dout_stride, (long long)H * d_v))))
         return rc;
-    LinTensor tq{q, q_stride, H, d, {}}, tk{k, k_stride, Hkv, d, {}}, tv{v, v_stride, Hkv, d_v, {}},
-        tdo{dout, dout_stride, H, d_v, {}};
-    LinTensor* const all[] = {&tq, &tk, &tv, &tdo};
+    LinTensor tq{q, q_stride, H, d}, tk{k, k_stride, Hkv, d}, tv{v, v_stride, Hkv, d_v}, tdo{dout, dout_stride, H, d_v};
+    LinTensor tdq = lin_output(dq, H, d), tdk = lin_output(dk, Hkv, d), tdv = lin_output(dv, Hkv, d_v);
+    LinTensor* const all[] = {&tq, &tk, &tv, &tdo, &tdq, &tdk, &tdv};
     LinParams p{};
     DevInfo di;
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, dstate != nullptr, workspace, ws_bytes, all, 4, &p, &di)))
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, dstate != nullptr, workspace, ws_bytes, all, 7, &p, &di)))
         return rc;
     p.out_mul = scale;
     cudaError_t e = cudaSuccess;
     if (rows) {   // dq, forwards
-        const LinMaps maps = linear_roles(&p, tdo, tv, tk, dq);
+        const LinMaps maps = linear_roles(&p, tdo, tv, tk, tdq);
         p.init = state;
         p.init_trans = 1;
         e = launch_linear_states(p, maps, false, di.sms, stream);
@@ -980,11 +984,11 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
     p.init_trans = 0;
     p.final = dstate;
     p.final_mul = scale;
-    const LinMaps maps = linear_roles(&p, tk, tq, tdo, dv);
+    const LinMaps maps = linear_roles(&p, tk, tq, tdo, tdv);
     if (e == cudaSuccess) e = launch_linear_states(p, maps, true, di.sms, stream);
     if (rows && e == cudaSuccess) e = launch_linear_out(p, maps, true, di.sms, stream);
     if (rows && e == cudaSuccess) {
-        const LinMaps maps_k = linear_roles(&p, tv, tdo, tq, dk);
+        const LinMaps maps_k = linear_roles(&p, tv, tdo, tq, tdk);
         p.init_trans = p.states_trans = 1;
         e = launch_linear_out(p, maps_k, true, di.sms, stream);
     }

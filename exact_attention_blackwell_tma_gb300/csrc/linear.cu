@@ -131,19 +131,20 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const LinStepPar
 
 }  // namespace
 
-LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv) {
+LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv, bool final) {
     constexpr int kUnit = 128, kSms = 152;   // tokens of a chunk; CTAs of a wave on a GB300
     const long longest = ((long)L + kUnit - 1) / kUnit;   // chunks that a sequence can have
     const long units = packed ? (long)L / kUnit + B : B * longest;
     const long tiles = (long)Hkv * (d == 128 && dv == 128 ? 1 : d / 64);
     // Chunks of a segment: those that take the least time, counted in chunks of the outputs' kernel. A CTA's
     // segments one after the other; a split call also needs the shares (half as long), and each segment costs its
-    // states' way through memory and a start of the walk.
+    // states' way through memory (64 KB four times, of two chunks' traffic) and a start of the walk.
     long seg = longest;
-    double least = packed && B > 1 ? 1e30 : (double)((B * tiles + kSms - 1) / kSms) * longest;   // (one long sequence may be most of a batch)
+    double least = (double)((B * tiles + kSms - 1) / kSms) * longest * (final ? 1.5 : 1.0) + (final ? 4 : 0);
+    if (packed && B > 1) least = 1e30;   // (one long sequence may be most of a batch)
     for (long x = 1; x < longest && x <= 64; ++x) {
         const long segments = packed ? units / x + B / 2 : B * ((longest + x - 1) / x);
-        const double cost = (double)((segments * tiles + kSms - 1) / kSms) * (1.5 * x + 1.5) + 4;
+        const double cost = (double)((segments * tiles + kSms - 1) / kSms) * (1.5 * x + 2) + 4;
         if (cost < least) {
             least = cost;
             seg = x;

@@ -52,11 +52,11 @@ struct LinPlan {
     int seg_rows, segments;
     bool split;   // some sequence may have more than one segment
 };
-LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv);
+LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv, bool final);   // final: the last states are wanted
 
-// Tensor maps of a, b and c: 128 tokens x 64 channels of a head
+// Tensor maps, boxes of 64 channels of a head: a, b and c by 128 tokens, out by 32
 struct LinMaps {
-    CUtensorMap a, b, c;
+    CUtensorMap a, b, c, out;
 };
 
 // The states that the segments start from, and the last one (nothing to do without several segments or `final`); the outputs

@@ -8,14 +8,15 @@
 // registers, set the time there). What costs is the chain through the chunks: scores, decays, product,
 // state, and the next chunk's product with it. So one CTA per SM walks segments with the
 // next tiles in flight, in roles that each take less than the loads do:
-//   warps 0-7    the state, X = D^n X + (the chunk's share), in registers in fp32, written to shared
-//                memory in bf16 for the next chunk; and the outputs, P c + D^(..) a X
+//   warps 0-7    the outputs, P c + D^(..) a X, and the state, X = D^n X + (the chunk's share), in registers in
+//                fp32, written to shared memory in bf16 for the next chunk
 //   warps 8-15   P: scores from tensor memory, times the decays, back as bf16 over their columns (the
 //                next product's A operand); then b times the state's weights, in two bf16 terms,
 //                the first in place once the scores are taken
-//   warp 16      tile loads (TMA): a alone, b and c in a ring
+//   warp 16      tile loads (TMA), a ring for each of a, b and c
 //   warp 17      the products, each issued by an elected lane of the converged warp:
 //                P = a b^T;  O2 = a X;  O1 = P c;  KV = (w b)^T c
+//   warp 18      which segments and heads come next
 // The tensor pipe executes in issue order, so the next scores may be issued behind the product
 // that reads P. Every wait is bounded.
 //
@@ -61,6 +62,13 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// A box of shared memory to the tensor of the map, tracked by this thread's bulk groups
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
 // tc_commit by the lane that the mma_.._w calls elect
 __device__ __forceinline__ void commit_w(uint32_t bar) {
     asm volatile(
@@ -68,6 +76,9 @@ __device__ __forceinline__ void commit_w(uint32_t bar) {
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
+// A value that all lanes have, from an instruction whose result the compiler knows to be one for the warp: what
+// follows from it (loops, stages, descriptors) then stays in uniform registers, which the products take their operands from.
+__device__ __forceinline__ int uniform(int x) { return (int)__reduce_or_sync(kFullMask, (unsigned)x); }
 // A bounded wait of the whole warp. All lanes poll (one access for the warp, no branch around it), and the clock is
 // read only after some polls: reading it first delays the warp's resumption.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const WaitCtx& w) {
@@ -88,15 +99,19 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Wa
     }
     return __all_sync(kFullMask, ok);
 }
-// Whether the phase has completed, without waiting
-__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+// Whether the phase has completed, without waiting. (Tests of several barriers ahead of their waits overlap: under
+// the other warps' shared-memory traffic each takes some 250 cycles.)
+__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return __shfl_sync(kFullMask, ok, 0) != 0;
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_unless(bool done, uint32_t bar, uint32_t parity, const WaitCtx& w) {
+    return __all_sync(kFullMask, done) || wait_all(bar, parity, w);
 }
 __device__ __forceinline__ float lo16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
@@ -155,7 +170,8 @@ __device__ __forceinline__ bool next_triple(Walk& i, const TripleRing* ring, uin
                                             int lane) {
     const uint32_t slot = i.taken % kTriples;
     if (!wait_all(full + 8 * slot, (i.taken / kTriples) & 1u, w)) return false;
-    i.t = ring->at[slot];
+    const Triple& t = ring->at[slot];
+    i.t = Triple{uniform(t.s), uniform(t.b), uniform(t.h), uniform(t.tile), uniform(t.row0), uniform(t.rows)};
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + 8 * slot);
     ++i.taken;
@@ -187,16 +203,26 @@ constexpr int kTailPad = DK == 64 ? kHalf : 0;
 template <int DK, int DT>
 struct OutLay {
     static constexpr int MT = (DK + 127) / 128, kB = DK / 64 * kBox, kC = DT / 64 * kBox, kX = DT / 64 * DK * 128;
-    static constexpr int kRing = DK <= 192 ? 2 : 1;                       // stages of b and c
-    static constexpr int kTerm = DK / 64 * kHalf, kTerms = DK <= 128 ? 2 : 1;   // buffers of 64 tokens for the second term
-    static constexpr int kStage = kB + kC, kAOff = kRing * kStage, kXOff = kAOff + kB, kTermOff = kXOff + kX;
-    static constexpr int kBarOff = kTermOff + kTerms * kTerm + kTailPad<DK>;
-    static constexpr int kAFull = 0, kAFree = 1, kBFull = 2, kBFree = 4, kPFull = 6, kPReady = 7, kWReady = 8, kTFree = 10,
-                         kOFull = 12, kOFree = 13, kXReady = 14, kDrain = 15, kRFull = 16, kREmpty = kRFull + kTriples,
-                         kNumBars = kREmpty + kTriples;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8, kRingOff = kMiscOff + 16;
+    // Stages of a, b and c: two where the 227 KB allow it (a load takes 2000 to 3500 cycles under load). The second
+    // term has buffers of 64 tokens or, where all of a, b and c have two stages of 32 KB (kShareA), goes where a
+    // was once a X is done.
+    static constexpr bool kShareA = DK == 128 && DT == 128;
+    static constexpr int kRingA = DK <= 128 ? 2 : 1, kRingB = DK <= 192 ? 2 : 1, kRingC = 2;
+    static constexpr int kTerm = DK / 64 * kHalf, kTerms = DK <= 128 ? 2 : 1;
+    static constexpr int kAOff = kRingB * kB, kCOff = kAOff + kRingA * kB, kXOff = kCOff + kRingC * kC, kTermOff = kXOff + kX;
+    // a chunk's outputs pass through X's place on their way to memory, which no product needs then (at 64 it is too small)
+    static constexpr int kOutOff = DK == 64 ? kTermOff + kTerms * kTerm + kTailPad<DK> : kXOff, kOutBox = DK == 64 ? kBox : DK * 128;
+    static constexpr int kBarOff = DK == 64 ? kOutOff + kBox : kTermOff + (kShareA ? 0 : kTerms * kTerm);
+    // warps 0-3 and 4-7 share the columns, or the tiles of X's channels, or have work for the first four alone
+    static constexpr int kWarpsX = DT == 128 || MT == 2 ? 8 : 4, kWarpsO = DT == 128 ? 8 : 4;
+    static constexpr int kAFull = 0, kAFree = 2, kBFull = 4, kBFree = 6, kCFull = 8, kCFree = 10, kPFull = 12, kPReady = 13,
+                         kWReady = 14, kTFree = 16, kOFull = 18, kOFree = 19, kXReady = 20, kKVFull = 21, kDrain = 22,
+                         kRFull = 23,
+                         kREmpty = kRFull + kTriples, kNumBars = kREmpty + kTriples;
+    static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16, kRingOff = kMiscOff + 16;
     static constexpr int kPowOff = kRingOff + (int)sizeof(TripleRing), kBytes = kPowOff + 8 * 64 * 4;   // 64 floats for each of warps 8-15
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
+    static_assert(kXOff % 1024 == 0 && kTermOff % 1024 == 0 && kBarOff % 16 == 0 && kPowOff % 16 == 0, "alignment of tiles and tables");
     static constexpr uint32_t kTmP = 0, kTmO1 = 128, kTmO2 = 128 + DT, kTmKV = 128 + 2 * DT;
     static_assert(kTmKV + MT * DT <= 512, "tensor memory budget");
 };
@@ -209,27 +235,30 @@ template <int DK, int DT, bool kBack>
 __global__ void __launch_bounds__(kOutThreads, 1)
 lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     using Lay = OutLay<DK, DT>;
-    constexpr int MT = Lay::MT, HC = DT / 2;   // HC: columns of a warp of the states and outputs
+    constexpr int MT = Lay::MT;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     if (base & 1023u) {
         if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMiscOff + 4);
     TripleRing* ring = reinterpret_cast<TripleRing*>(smem + Lay::kRingOff);
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < Lay::kNumBars; ++i) {
-            const bool by_256 = i == Lay::kPReady || i == Lay::kWReady || i == Lay::kWReady + 1 || i == Lay::kOFree || i == Lay::kXReady;
-            mbar_init(bar(i), by_256 ? 256 : i >= Lay::kREmpty ? 18 : 1);
+            const bool by_p = i == Lay::kPReady || i == Lay::kWReady || i == Lay::kWReady + 1;
+            mbar_init(bar(i), by_p ? 256 : i == Lay::kOFree ? 32 * Lay::kWarpsO : i == Lay::kXReady ? 32 * Lay::kWarpsX
+                              : i >= Lay::kREmpty ? 10 + Lay::kWarpsX : 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 16 && lane == 0) {
+        tma_prefetch_desc(&maps.out);
         tma_prefetch_desc(&maps.a);
         tma_prefetch_desc(&maps.b);
         tma_prefetch_desc(&maps.c);
@@ -254,6 +283,11 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         at.x = 0;
         return ++at.chunk == at.chunks;
     };
+    constexpr uint32_t RB = Lay::kRingB, RC = Lay::kRingC;
+    // where the second term goes: backwards with several query heads a is read for each of them, so that it keeps to
+    // the first stage and the term to the second; else the term follows a X in its stage
+    const bool follows = Lay::kShareA && !(kBack && per > 1);
+    const uint32_t RA = Lay::kShareA && !follows ? 1 : Lay::kRingA;
 
     if (warp >= 16) {
         setmaxnreg_dec<kOutRegsRest>();
@@ -261,42 +295,53 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             find_triples<DT, kBack>(p, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, true);
         } else if (warp == 16) {
             // ------------------------------------------------------------ loads
-            uint32_t na = 0, nb = 0;
+            uint32_t na = 0, nb = 0, sent_b = 0;   // tiles of a, of b and c
             for (bool fresh = true;; fresh = advance()) {
                 if (fresh && !(ok = take())) break;
                 if (!at.live) break;
                 const int row = at.t.row0 + chunk_row<kBack>(at);
                 const int ha = kBack ? at.t.h : at.t.h * per + at.x, hb = kBack ? at.t.h * per + at.x : at.t.h;
-                if (kBack || at.x == 0) {
-                    const uint32_t st = nb % Lay::kRing, full = bar(Lay::kBFull + st), to = base + st * Lay::kStage;
-                    if (!(ok = wait_all(bar(Lay::kBFree + st), ((nb / Lay::kRing) & 1u) ^ 1u, w))) break;
+                const bool new_a = !kBack || at.x == 0, new_b = kBack || at.x == 0;
+                if (new_b) {
+                    const uint32_t st = nb % RB, full = bar(Lay::kBFull + st), to = base + st * Lay::kB;
+                    if (!(ok = wait_all(bar(Lay::kBFree + st), ((nb / RB) & 1u) ^ 1u, w))) break;
                     if (lane == 0) {
-                        mbar_expect_tx(full, Lay::kStage);
+                        mbar_expect_tx(full, Lay::kB);
 #pragma unroll
                         for (int y = 0; y < DK / 64; ++y) tma_load_3d(to + y * kBox, &maps.b, full, y * 64, hb, row);
-#pragma unroll
-                        for (int y = 0; y < DT / 64; ++y)
-                            tma_load_3d(to + Lay::kB + y * kBox, &maps.c, full, at.t.tile * DT + y * 64, hb, row);
+                        ++sent_b;
                     }
                     __syncwarp();
-                    ++nb;
                 }
-                if (!kBack || at.x == 0) {
-                    if (!(ok = wait_all(bar(Lay::kAFree), (na & 1u) ^ 1u, w))) break;
+                if (new_a) {
+                    const uint32_t st = na % RA, full = bar(Lay::kAFull + st), to = base + Lay::kAOff + st * Lay::kB;
+                    if (!(ok = wait_all(bar(Lay::kAFree + st), ((na / RA) & 1u) ^ 1u, w))) break;
                     if (lane == 0) {
-                        mbar_expect_tx(bar(Lay::kAFull), Lay::kB);
+                        mbar_expect_tx(full, Lay::kB);
 #pragma unroll
-                        for (int y = 0; y < DK / 64; ++y)
-                            tma_load_3d(base + Lay::kAOff + y * kBox, &maps.a, bar(Lay::kAFull), y * 64, ha, row);
+                        for (int y = 0; y < DK / 64; ++y) tma_load_3d(to + y * kBox, &maps.a, full, y * 64, ha, row);
                     }
                     __syncwarp();
                     ++na;
                 }
+                if (new_b) {
+                    const uint32_t st = nb % RC, full = bar(Lay::kCFull + st), to = base + Lay::kCOff + st * Lay::kC;
+                    if (!(ok = wait_all(bar(Lay::kCFree + st), ((nb / RC) & 1u) ^ 1u, w))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(full, Lay::kC);
+#pragma unroll
+                        for (int y = 0; y < DT / 64; ++y)
+                            tma_load_3d(to + y * kBox, &maps.c, full, at.t.tile * DT + y * 64, hb, row);
+                    }
+                    __syncwarp();
+                    ++nb;
+                }
             }
             if (lane == 0) {   // (a pending load must land before the CTA gives up its memory)
-                if (na > 0) drain_wait(bar(Lay::kAFull), (na - 1) & 1u, p.wait_budget_ns);
-                for (uint32_t i = nb > Lay::kRing ? nb - Lay::kRing : 0; i < nb; ++i)
-                    drain_wait(bar(Lay::kBFull + i % Lay::kRing), (i / Lay::kRing) & 1u, p.wait_budget_ns);
+                for (uint32_t i = na > RA ? na - RA : 0; i < na; ++i) drain_wait(bar(Lay::kAFull + i % RA), (i / RA) & 1u, p.wait_budget_ns);
+                for (uint32_t i = sent_b > RB ? sent_b - RB : 0; i < sent_b; ++i)
+                    drain_wait(bar(Lay::kBFull + i % RB), (i / RB) & 1u, p.wait_budget_ns);
+                for (uint32_t i = nb > RC ? nb - RC : 0; i < nb; ++i) drain_wait(bar(Lay::kCFull + i % RC), (i / RC) & 1u, p.wait_budget_ns);
             }
             __syncwarp();
         } else if (warp == 17) {
@@ -305,93 +350,113 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             constexpr uint32_t kIdN = idesc_bf16_f32(128, DT, false, true);      // B (X, c): rows along the sum
             constexpr uint32_t kIdKV = idesc_bf16_f32(128, DT, true, true);      // (w b)^T, c: rows of tokens
             const SmemDesc a_km = sdesc_sw128_split(base + Lay::kAOff, 16, 1024), b_km = sdesc_sw128_split(base, 16, 1024);
-            const SmemDesc c_mn = sdesc_sw128_split(base + Lay::kB, kBox, 1024);
+            const SmemDesc c_mn = sdesc_sw128_split(base + Lay::kCOff, kBox, 1024);
             const SmemDesc x_mn = sdesc_sw128_split(base + Lay::kXOff, DK * 128, 1024);
-            uint32_t na = 0, nb = 0, it = 0, outs = 0, xs = 0, shared = 0;   // loads taken, items, rounds of O, states, shares
-            // `at` is an item ahead: what is finished here is the one before, if any
+            uint32_t na = 0, nb = 0, nc = 0, it = 0, outs = 0, xs = 0, shared = 0;   // tiles taken, items, rounds of O, states, shares
+            // `at` is an item ahead: what is finished here is the one before, if any, with its tiles in a_st and b_st
             bool some = false, shares = false, last_x = false;
             int x = 0;
-            uint32_t st = 0;
+            uint32_t a_st = 0, b_st = 0;
             for (bool fresh = true;; fresh = advance()) {
-                const uint32_t off = desc_step(st * Lay::kStage);
+                const uint32_t a_off = desc_step(a_st * Lay::kB), c_st = (nc - 1 + (kBack || x == 0)) % RC,
+                               c_off = desc_step(c_st * Lay::kC);
                 const bool head = !kBack || x == 0, tail = !kBack || last_x;   // of a round of the outputs
                 if (some) {
+                    const bool new_c = kBack || x == 0;
+                    const uint32_t c_full = bar(Lay::kCFull + nc % RC), c_parity = (nc / RC) & 1u;
+                    const bool x_done = test_phase(bar(Lay::kXReady), xs & 1u), o_done = test_phase(bar(Lay::kOFree), (outs & 1u) ^ 1u),
+                               c_done = test_phase(c_full, c_parity), p_done = test_phase(bar(Lay::kPReady), it & 1u);
                     if (head) {
-                        if (x == 0) {
-                            if (!(ok = wait_all(bar(Lay::kXReady), xs & 1u, w))) break;
-                            ++xs;
-                        }
-                        if (!(ok = wait_all(bar(Lay::kOFree), (outs & 1u) ^ 1u, w))) break;
+                        if (!(ok = wait_unless(x_done, bar(Lay::kXReady), xs & 1u, w))) break;
+                        ++xs;
+                        if (!(ok = wait_unless(o_done, bar(Lay::kOFree), (outs & 1u) ^ 1u, w))) break;
                         tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                         for (int y = 0; y < DK / 16; ++y)
-                            mma_ss_w(tmem + Lay::kTmO2, a_km, desc_step((y >> 2) * kBox + (y & 3) * 32), x_mn, desc_step(y * 2048),
-                                     kIdN, y > 0);
-                        if (!kBack || per == 1) commit_w(bar(Lay::kAFree));
+                            mma_ss_w(tmem + Lay::kTmO2, a_km, a_off + desc_step((y >> 2) * kBox + (y & 3) * 32), x_mn,
+                                     desc_step(y * 2048), kIdN, y > 0);
+                        if (follows && shares) commit_w(bar(Lay::kTFree + 1));
+                        else if (!kBack || per == 1) commit_w(bar(Lay::kAFree + a_st));
                     }
-                    if (!(ok = wait_all(bar(Lay::kPReady), it & 1u, w))) break;
+                    if (new_c) {
+                        if (!(ok = wait_unless(c_done, c_full, c_parity, w))) break;
+                        ++nc;
+                    }
+                    if (!(ok = wait_unless(p_done, bar(Lay::kPReady), it & 1u, w))) break;
                     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int y = 0; y < 8; ++y)
-                        mma_ts_w(tmem + Lay::kTmO1, tmem + Lay::kTmP + (y >> 1) * 32 + (y & 1) * 8, c_mn, off + desc_step(y * 2048),
+                        mma_ts_w(tmem + Lay::kTmO1, tmem + Lay::kTmP + (y >> 1) * 32 + (y & 1) * 8, c_mn, c_off + desc_step(y * 2048),
                                  kIdN, !head || y > 0);
                     ++it;
+                    if (tail) {
+                        commit_w(bar(Lay::kOFull));
+                        ++outs;
+                    }
                 }
                 if (fresh && !(ok = take())) break;
                 const bool new_a = !kBack || at.x == 0, new_b = kBack || at.x == 0;
-                const uint32_t b_full = bar(Lay::kBFull + nb % Lay::kRing), b_parity = (nb / Lay::kRing) & 1u;
-                // the next scores come first if their tiles have come: they have the longer way to go
-                const bool early = some && at.live && (!new_a || warp_test(bar(Lay::kAFull), na & 1u)) &&
-                                   (!new_b || warp_test(b_full, b_parity));
+                const uint32_t a_full = bar(Lay::kAFull + na % RA), a_parity = (na / RA) & 1u;
+                const uint32_t b_full = bar(Lay::kBFull + nb % RB), b_parity = (nb / RB) & 1u;
+                const uint32_t a_was = a_st, b_was = b_st, rows0 = desc_step(b_st * Lay::kB);
+                // the next scores come now if their tiles have come: they have the longer way to go
+                const bool a_done = test_phase(a_full, a_parity), b_done = test_phase(b_full, b_parity),
+                           w_done = test_phase(bar(Lay::kWReady), shared & 1u);
+                const bool early = __all_sync(kFullMask, some && at.live && (!new_a || a_done) && (!new_b || b_done));
 #pragma unroll 1
                 for (int turn = 0; turn < 2 && ok; ++turn) {
                     if ((turn == 0) == early) {
                         if (!at.live) continue;
-                        if (new_a && !(ok = wait_all(bar(Lay::kAFull), na & 1u, w))) break;
-                        if (new_b && !(ok = wait_all(b_full, b_parity, w))) break;
+                        if (new_a && !(ok = wait_unless(early, a_full, a_parity, w))) break;
+                        if (new_b && !(ok = wait_unless(early, b_full, b_parity, w))) break;
                         na += new_a;
                         nb += new_b;
+                        a_st = (na - 1) % RA;
+                        b_st = (nb - 1) % RB;
                         tc_fence_after_sync();
-                        const uint32_t next = desc_step((nb - 1) % Lay::kRing * Lay::kStage);
-#pragma unroll
+                        const uint32_t next_a = desc_step(a_st * Lay::kB), next_b = desc_step(b_st * Lay::kB);
+#pragma unroll 1
                         for (int y = 0; y < DK / 16; ++y) {
                             const uint32_t step = desc_step((y >> 2) * kBox + (y & 3) * 32);
-                            mma_ss_w(tmem + Lay::kTmP, a_km, step, b_km, next + step, kIdP, y > 0);
+                            mma_ss_w(tmem + Lay::kTmP, a_km, next_a + step, b_km, next_b + step, kIdP, y > 0);
                         }
                         commit_w(bar(Lay::kPFull));
-                        if (kBack && per > 1 && at.x == per - 1) commit_w(bar(Lay::kAFree));   // (a X came with x = 0)
+                        if (kBack && per > 1 && at.x == per - 1) commit_w(bar(Lay::kAFree + a_st));   // (a X came with x = 0)
                     } else if (some) {
                         if (shares) {
 #pragma unroll 1
                             for (int half = 0; half < 2; ++half) {
                                 if (half < 3 - Lay::kTerms) {   // (one pass over all rows, or two over 64)
-                                    if (!(ok = wait_all(bar(Lay::kWReady + half), shared & 1u, w))) break;
+                                    if (!(ok = wait_unless(half == 0 && w_done, bar(Lay::kWReady + half), shared & 1u, w))) break;
                                     tc_fence_after_sync();
                                 }
-                                const uint32_t rows = off + desc_step(half * kHalf), buf = Lay::kTerms == 2 ? half : 0;
+                                const uint32_t rows = desc_step(half * kHalf), buf = Lay::kTerms == 2 ? half : 0;
                                 const uint32_t more = (kBack && x > 0) || half > 0;
 #pragma unroll 1
                                 for (int mt = 0; mt < MT; ++mt) {
                                     const SmemDesc b_mn = weighted_desc<DK>(base, mt, kBox);
-                                    const SmemDesc t_mn = weighted_desc<DK>(base + Lay::kTermOff + buf * Lay::kTerm, mt, kHalf);
+                                    const uint32_t t_at = Lay::kShareA ? base + Lay::kAOff + (follows ? a_was : 1) * Lay::kB + half * kHalf
+                                                                       : base + Lay::kTermOff + buf * Lay::kTerm;
+                                    const SmemDesc t_mn = weighted_desc<DK>(t_at, mt, Lay::kShareA ? kBox : kHalf);
                                     const uint32_t kv = tmem + Lay::kTmKV + mt * DT;
-#pragma unroll
+#pragma unroll 1
                                     for (int y = 0; y < 4; ++y)
-                                        mma_ss_w(kv, b_mn, rows + desc_step(y * 2048), c_mn, rows + desc_step(y * 2048), kIdKV,
-                                                 y > 0 ? 1u : more);
-#pragma unroll
+                                        mma_ss_w(kv, b_mn, rows0 + rows + desc_step(y * 2048), c_mn, c_off + rows + desc_step(y * 2048),
+                                                 kIdKV, y > 0 ? 1u : more);
+#pragma unroll 1
                                     for (int y = 0; y < 4; ++y)
-                                        mma_ss_w(kv, t_mn, desc_step(y * 2048), c_mn, rows + desc_step(y * 2048), kIdKV, 1);
+                                        mma_ss_w(kv, t_mn, desc_step(y * 2048), c_mn, c_off + rows + desc_step(y * 2048), kIdKV, 1);
                                 }
-                                if (half >= Lay::kTerms - 1) commit_w(bar(Lay::kTFree + Lay::kTerms - 1));
+                                if (!follows && half >= Lay::kTerms - 1) commit_w(bar(Lay::kTFree + Lay::kTerms - 1));
                             }
+                            if (follows) commit_w(bar(Lay::kAFree + a_was));
                             if (!ok) break;
                             ++shared;
+                            if (tail) commit_w(bar(Lay::kKVFull));
                         }
-                        if (kBack || last_x) commit_w(bar(Lay::kBFree + st));
-                        if (tail) {
-                            commit_w(bar(Lay::kOFull));
-                            ++outs;
+                        if (kBack || last_x) {
+                            commit_w(bar(Lay::kBFree + b_was));
+                            commit_w(bar(Lay::kCFree + c_st));
                         }
                     }
                 }
@@ -400,7 +465,6 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 x = at.x;
                 last_x = x == per - 1;
                 shares = (kBack || last_x) && at.chunk + 1 < at.chunks;   // the item adds to the state
-                st = (nb - 1) % Lay::kRing;
             }
             commit_w(bar(Lay::kDrain));
             if (lane == 0) drain_wait(bar(Lay::kDrain), 0, p.wait_budget_ns);
@@ -417,7 +481,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         float* pw = reinterpret_cast<float*>(smem + Lay::kPowOff) + (warp - 8) * 64;
         const float* near_pw = pw + (kBack ? 32 : 0);
         const float* own_pw = pw + (kBack ? 32 - lane : 31 - lane);
-        uint32_t it = 0, nb = 0, shared = 0;
+        uint32_t it = 0, na = 0, nb = 0, shared = 0;
         float l2 = 0.f, far0 = 0.f, far1 = 0.f, diag = 0.f;
         for (bool fresh = true;; fresh = advance(), ++it) {
             if (fresh) {
@@ -436,7 +500,8 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const int n = min(kCh, at.t.rows - chunk_row<kBack>(at));
             const bool shares = (kBack || at.x == per - 1) && at.chunk + 1 < at.chunks;
             if (kBack || at.x == 0) ++nb;
-            uint8_t* tiles = smem + (nb - 1) % Lay::kRing * Lay::kStage;
+            if (!kBack || at.x == 0) ++na;
+            uint8_t* b_tile = smem + (nb - 1) % RB * Lay::kB;
             if (!(ok = wait_all(bar(Lay::kPFull), it & 1u, w))) break;
             tc_fence_after_sync();
 #pragma unroll 1
@@ -482,8 +547,10 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             }
             if (n < kCh && (kBack || at.x == 0)) {   // c's rows past the sequence's end, whatever they hold
                 const int r = t & 127;
+                if (!(ok = wait_all(bar(Lay::kCFull + (nb - 1) % RC), ((nb - 1) / RC) & 1u, w))) break;
                 if (r >= n)
-                    for (int c = t >> 7; c < DT / 8; c += 2) *piece_at(tiles + Lay::kB, r, c) = make_uint4(0, 0, 0, 0);
+                    for (int c = t >> 7; c < DT / 8; c += 2)
+                        *piece_at(smem + Lay::kCOff + (nb - 1) % RC * Lay::kC, r, c) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
             tmem_st_wait();
@@ -498,28 +565,35 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 const int r = r0 + (t & (kRows - 1)), p0 = t / kRows;
                 const uint32_t use = r0 == 0 ? 0 : 1, round = Lay::kTerms == 2 ? shared : 2 * shared + use;
                 const float weight = r < n ? decay_pow(l2, kBack ? r + 1 : n - 1 - r) : 0.f;
-                uint8_t* second = smem + Lay::kTermOff + (Lay::kTerms == 2 ? (r >> 6) * Lay::kTerm : 0);
-                if (!(ok = wait_all(bar(Lay::kTFree + Lay::kTerms - 1), (round & 1u) ^ 1u, w))) break;
-#pragma unroll 1
+                uint4 lo[kPieces];
+#pragma unroll
                 for (int y0 = 0; y0 < kPieces; y0 += kAtOnce) {
                     uint4 v[kAtOnce];
 #pragma unroll
-                    for (int y = 0; y < kAtOnce; ++y) v[y] = *piece_at(tiles, r, p0 + kLanes * (y0 + y));
+                    for (int y = 0; y < kAtOnce; ++y) v[y] = *piece_at(b_tile, r, p0 + kLanes * (y0 + y));
 #pragma unroll
                     for (int y = 0; y < kAtOnce; ++y) {
                         const uint32_t u[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-                        uint32_t hi[4], lo[4];
+                        uint32_t h[4], l[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const float f0 = lo16(u[z]) * weight, f1 = hi16(u[z]) * weight;
-                            hi[z] = pack_bf16x2(f0, f1);
-                            lo[z] = pack_bf16x2(f0 - lo16(hi[z]), f1 - hi16(hi[z]));
+                            h[z] = pack_bf16x2(f0, f1);
+                            l[z] = pack_bf16x2(f0 - lo16(h[z]), f1 - hi16(h[z]));
                         }
-                        if (kBack && r >= n) hi[0] = hi[1] = hi[2] = hi[3] = lo[0] = lo[1] = lo[2] = lo[3] = 0u;
-                        const int c = p0 + kLanes * (y0 + y);
-                        *piece_at(tiles, r, c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *piece_at<kHalf>(second, r & 63, c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (kBack && r >= n) h[0] = h[1] = h[2] = h[3] = l[0] = l[1] = l[2] = l[3] = 0u;
+                        *piece_at(b_tile, r, p0 + kLanes * (y0 + y)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        lo[y0 + y] = make_uint4(l[0], l[1], l[2], l[3]);
                     }
+                }
+                // the second term, once its place is free
+                if (!(ok = wait_all(bar(Lay::kTFree + Lay::kTerms - 1), (round & 1u) ^ (follows ? 0u : 1u), w))) break;
+                uint8_t* second = Lay::kShareA ? smem + Lay::kAOff + (follows ? (na - 1) % RA : 1) * Lay::kB
+                                               : smem + Lay::kTermOff + (Lay::kTerms == 2 ? (r >> 6) * Lay::kTerm : 0);
+#pragma unroll
+                for (int y = 0; y < kPieces; ++y) {
+                    const int c = p0 + kLanes * y;
+                    *(Lay::kShareA ? piece_at(second, r, c) : piece_at<kHalf>(second, r & 63, c)) = lo[y];
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(Lay::kWReady + use));
@@ -528,19 +602,23 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             ++shared;
         }
     } else {
-        // ------------------------------------------------------------ the state and the outputs
+        // ------------------------------------------------------------ the outputs and the state
         setmaxnreg_inc<kOutRegsX>();
-        const int q4 = warp & 3, col0 = (warp >> 2) * HC, row = q4 * 32 + lane;   // of X (a tile's) and of the outputs
+        const int q4 = warp & 3, group = warp >> 2, row = q4 * 32 + lane;   // of X (a tile's) and of the outputs
+        const int col0 = DT == 128 ? 64 * group : 0, mt = DT == 128 ? 0 : group;
+        const bool has_x = tile_row<DK>(mt, row);
+        const int channel = tile_channel<DK>(mt) + row;
         const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16) + col0;
+        // (32 rows of 128 bytes that are this warp's alone, as X's rows and then as those of the outputs)
+        uint8_t* staged = smem + Lay::kOutOff + (col0 >> 6) * Lay::kOutBox + q4 * 4096;
         at.per = kBack ? 1 : per;   // (backwards one round of outputs for all query heads)
-        uint32_t outs = 0;
-        float X[MT][HC];
+        uint32_t outs = 0, moved = 0;
+        float X[64];
         float l2 = 0.f, into = 0.f, over = 0.f;
-        const bool whole_sectors = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;   // (rows are multiples of 128 bytes)
-        __nv_bfloat16* out = nullptr;   // null: this thread's token does not exist
         // `at` is an item ahead: the outputs are those of the one before, if any; `last`: of a segment
+        int n = 0, token0 = 0, head = 0, column = 0;   // its tokens, where the outputs go
         bool some = false, moves = false, last = true;
-        for (bool fresh = true;; fresh = advance()) {
+        for (bool fresh = true; warp < Lay::kWarpsX; fresh = advance()) {
             if (fresh && !(ok = take())) break;
             if (last && at.live) {   // (X is in shared memory: the registers take the next segment's)
                 l2 = log2_decay(p, at.t.h);
@@ -548,86 +626,97 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 const float mul = p.split() ? 1.f : p.init_mul;
                 const bool trans = p.split() ? p.states_trans : p.init_trans;
                 const int c0 = at.t.tile * DT + col0;
+                if (!src || !has_x) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const int r = tile_channel<DK>(mt) + row;
-                    if (!src || !tile_row<DK>(mt, row)) {
+                    for (int c = 0; c < 64; ++c) X[c] = 0.f;
+                } else if (trans) {
+                    const float* from = src + (long)c0 * DK + channel;
 #pragma unroll
-                        for (int c = 0; c < HC; ++c) X[mt][c] = 0.f;
-                    } else if (trans) {
-                        const float* from = src + (long)c0 * DK + r;
+                    for (int c = 0; c < 64; ++c) X[c] = mul * from[c * DK];
+                } else {
+                    const float* from = src + (long)channel * p.DV + c0;
 #pragma unroll
-                        for (int c = 0; c < HC; ++c) X[mt][c] = mul * from[c * DK];
-                    } else {
-                        const float* from = src + (long)r * p.DV + c0;
-#pragma unroll
-                        for (int c = 0; c < HC; c += 4) {
-                            const float4 y = *reinterpret_cast<const float4*>(from + c);
-                            X[mt][c] = mul * y.x, X[mt][c + 1] = mul * y.y, X[mt][c + 2] = mul * y.z, X[mt][c + 3] = mul * y.w;
-                        }
+                    for (int c = 0; c < 64; c += 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(from + c);
+                        X[c] = mul * y.x, X[c + 1] = mul * y.y, X[c + 2] = mul * y.z, X[c + 3] = mul * y.w;
                     }
                 }
             }
             if (some) {
                 if (!(ok = wait_all(bar(Lay::kOFull), outs & 1u, w))) break;
                 tc_fence_after_sync();
-                if (moves && !last) {
+                if (warp < Lay::kWarpsO) {
+                    // all 32 rows by one copy from shared memory (row by row from registers the stores alone took a third
+                    // of the shared memory's time); at a sequence's end those that exist, one by one
+                    const bool whole = q4 * 32 + 32 <= n;
+                    uint8_t* direct = reinterpret_cast<uint8_t*>(
+                        p.out + ((long)(token0 + row) * (kBack ? p.Hkv : p.Hkv * per) + head) * p.DV + column);
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t o1[16], o2[16], o[8];
+                        tmem_ld16x2(t_row + Lay::kTmO1 + c, t_row + Lay::kTmO2 + c, o1, o2);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                        for (int z = 0; z < 8; ++z)
+                            o[z] = pack_bf16x2(fmaf(into, u2f(o2[2 * z]), p.out_mul * u2f(o1[2 * z])),
+                                               fmaf(into, u2f(o2[2 * z + 1]), p.out_mul * u2f(o1[2 * z + 1])));
 #pragma unroll
-                        for (int c = 0; c < HC; c += 32) {
-                            uint32_t r[32];
-                            tmem_ld32(t_row + Lay::kTmKV + mt * DT + c, r);
-#pragma unroll
-                            for (int z = 0; z < 32; ++z) X[mt][c + z] = fmaf(X[mt][c + z], over, u2f(r[z]));
+                        for (int z = 0; z < 2; ++z) {
+                            uint8_t* to = whole ? staged + lane * 128 + ((((c >> 3) + z) ^ (lane & 7)) << 4) : direct + 2 * c + 16 * z;
+                            if (row < n) *reinterpret_cast<uint4*>(to) = make_uint4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
                         }
-                }
-            }
-            // (the products with the last X are done: the outputs that use it are here)
-            if (last ? at.live : moves) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    if (tile_row<DK>(mt, row)) {
-#pragma unroll
-                        for (int c = 0; c < HC; c += 8)
-                            *piece_at<DK * 128>(smem + Lay::kXOff, tile_channel<DK>(mt) + row, (col0 + c) >> 3) =
-                                make_uint4(pack_bf16x2(X[mt][c], X[mt][c + 1]), pack_bf16x2(X[mt][c + 2], X[mt][c + 3]),
-                                           pack_bf16x2(X[mt][c + 4], X[mt][c + 5]), pack_bf16x2(X[mt][c + 6], X[mt][c + 7]));
                     }
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(Lay::kOFree));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (whole && lane == 0) {
+                        tma_store_3d(&maps.out, smem_addr(staged), column, head, token0 + q4 * 32);
+                        bulk_commit_group();
+                    }
+                }
+                ++outs;
+                if (moves && !last) {
+                    if (!(ok = wait_all(bar(Lay::kKVFull), moved & 1u, w))) break;
+                    ++moved;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld32(t_row + Lay::kTmKV + mt * DT + c, r);
+#pragma unroll
+                        for (int z = 0; z < 32; ++z) X[c + z] = fmaf(X[c + z], over, u2f(r[z]));
+                    }
+                    tc_fence_before_sync();
+                }
+                if (lane == 0) bulk_wait_group_read0();
+                __syncwarp();
+            }
+            // (the products with the last X are done: the outputs that use it have been here)
+            if (!last || at.live) {
+                if (has_x) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 8)
+                        *piece_at<DK * 128>(smem + Lay::kXOff, channel, (col0 + c) >> 3) =
+                            make_uint4(pack_bf16x2(X[c], X[c + 1]), pack_bf16x2(X[c + 2], X[c + 3]), pack_bf16x2(X[c + 4], X[c + 5]),
+                                       pack_bf16x2(X[c + 6], X[c + 7]));
+                }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(Lay::kXReady));
             }
-            if (some) {
-#pragma unroll 1
-                for (int c = 0; c < HC; c += 16) {
-                    uint32_t o1[16], o2[16], o[8];
-                    tmem_ld16x2(t_row + Lay::kTmO1 + c, t_row + Lay::kTmO2 + c, o1, o2);
-#pragma unroll
-                    for (int z = 0; z < 8; ++z)
-                        o[z] = pack_bf16x2(fmaf(into, u2f(o2[2 * z]), p.out_mul * u2f(o1[2 * z])),
-                                           fmaf(into, u2f(o2[2 * z + 1]), p.out_mul * u2f(o1[2 * z + 1])));
-                    if (out && whole_sectors) {
-                        store32(out + c, o);
-                    } else if (out) {
-                        *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                }
-                tc_fence_before_sync();
-                mbar_arrive(bar(Lay::kOFree));
-                ++outs;
-            }
             if (!at.live) break;
             some = true;
-            const int r0 = chunk_row<kBack>(at), n = min(kCh, at.t.rows - r0);
+            const int r0 = chunk_row<kBack>(at);
+            n = min(kCh, at.t.rows - r0);
             moves = at.x == at.per - 1;
             last = moves && at.chunk + 1 == at.chunks;
             into = p.out_mul * (row < n ? decay_pow(l2, kBack ? n - 1 - row : row + 1) : 0.f);
             over = decay_pow(l2, n);
-            out = row < n ? p.out + ((long)(at.t.row0 + r0 + row) * (kBack ? p.Hkv : p.Hkv * per) + (kBack ? at.t.h : at.t.h * per + at.x)) * p.DV +
-                                at.t.tile * DT + col0
-                          : nullptr;
+            token0 = at.t.row0 + r0;
+            head = kBack ? at.t.h : at.t.h * per + at.x;
+            column = at.t.tile * DT + col0;
         }
+        if (lane == 0) bulk_wait_group0();
+        __syncwarp();
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -639,8 +728,9 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 
 // ---------------------------------------------------------------- segments' shares
 // X' of a segment for X = 0: one sum over its tokens in tensor memory, each weighted by the
-// decay up to the segment's end (backwards: its start), b times that weight in three bf16 terms
-// (all of its 24 bits): the first in place, the others in buffers of 64 tokens.
+// decay up to the segment's end (backwards: its start), b times that weight in bf16 terms: the first in
+// place, the others in buffers of 64 tokens. Three terms (all 24 bits) where a state leaves the call, else two
+// (the states are rounded to 8 bits by the products that use them).
 template <int DK, int DT>
 struct StateLay {
     static constexpr int MT = (DK + 127) / 128, kB = DK / 64 * kBox, kC = DT / 64 * kBox, kStage = kB + kC;
@@ -651,6 +741,7 @@ struct StateLay {
     static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16, kRingOff = kMiscOff + 16;
     static constexpr int kBytes = kRingOff + (int)sizeof(TripleRing);
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
+    static_assert(kTermOff % 1024 == 0 && kBarOff % 16 == 0 && kRingOff % 8 == 0, "alignment of tiles and tables");
     static constexpr uint32_t kAcc = MT * DT, kCols = 2 * kAcc <= 128 ? 128 : 256;
     static_assert(2 * kAcc <= kCols, "tensor memory budget");
 };
@@ -667,12 +758,13 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMiscOff + 4);
     TripleRing* ring = reinterpret_cast<TripleRing*>(smem + Lay::kRingOff);
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < Lay::kNumBars; ++i) {
             const bool by_256 = i == Lay::kWReady || i == Lay::kWReady + 1, by_128 = i == Lay::kSFree || i == Lay::kSFree + 1;
             mbar_init(bar(i), by_256 ? 256 : by_128 ? 128 : i >= Lay::kREmpty ? 14 : 1);
@@ -703,6 +795,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         at.x = 0;
         return ++at.chunk == at.chunks;
     };
+    const int terms = p.final ? 3 : 2;   // of the weighted b
     uint32_t it = 0;
 
     if (warp == 14) {
@@ -750,11 +843,11 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 for (int mt = 0; mt < MT; ++mt) {
                     const SmemDesc b_mn = weighted_desc<DK>(base, mt, kBox);
                     const SmemDesc t_mn = weighted_desc<DK>(base + Lay::kTermOff + 2 * set * Lay::kTerm, mt, kHalf);
-#pragma unroll
+#pragma unroll 1
                     for (int y = 0; y < 4; ++y)
                         mma_ss_w(acc + mt * DT, b_mn, c0 + desc_step(y * 2048), c_mn, c0 + desc_step(y * 2048), kIdKV, y > 0 ? 1u : more);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y)
+#pragma unroll 1
+                    for (int y = 0; y < 4 * (terms - 1); ++y)
                         mma_ss_w(acc + mt * DT, t_mn, desc_step((y >> 2) * Lay::kTerm + (y & 3) * 2048), c_mn,
                                  c0 + desc_step((y & 3) * 2048), kIdKV, 1);
                 }
@@ -814,7 +907,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         *piece_at(tiles, row, c) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
 #pragma unroll
                         for (int term = 1; term < 3; ++term)
-                            *piece_at<kHalf>(buf + (term - 1) * Lay::kTerm, r64, c) =
+                            if (term < terms) *piece_at<kHalf>(buf + (term - 1) * Lay::kTerm, r64, c) =
                                 make_uint4(o[term][0], o[term][1], o[term][2], o[term][3]);
                     }
                 }

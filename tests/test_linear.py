@@ -390,10 +390,14 @@ def test_unwanted_outputs_change_nothing():
     p = Problem([500, 77], 2, 2, 64, 64, seed=16)
     o, final = p.forward(final_state=True)
     o2, none = p.forward()
-    assert none is None and torch.equal(o, o2)
+    assert none is None
+    p.check_forward(o, final)   # (each within its bounds: a wanted state is summed in more bits, which o may show in its last)
+    p.check_forward(o2, None)
     ws = torch.empty(binding.attn_linear_workspace_size(2, 2, 2, 577, True, 64, 64), dtype=torch.uint8, device="cuda")
     o3, _ = p.forward(workspace=ws.fill_(255))   # whatever the workspace holds
-    assert torch.equal(o, o3)
+    assert torch.equal(o2, o3)
+    o4, final4 = p.forward(final_state=True, workspace=ws.fill_(255))
+    assert torch.equal(o, o4) and torch.equal(final, final4)
 
 
 @gpu
