@@ -858,20 +858,23 @@ struct LinTensor {
 };
 LinTensor lin_output(void* x, int heads, int width) { return LinTensor{x, (long long)heads * width, heads, width, 32}; }
 
-size_t linear_bytes(const LinPlan& plan, int Hkv, int d, int dv) { return (size_t)plan.segments * Hkv * d * dv * sizeof(float); }
+size_t linear_bytes(const LinPlan& plan, int d, int dv) { return (size_t)plan.slots * d * dv * sizeof(float); }
 
 // What the four products of linear attention share; the roles of the tensors come on top.
 int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, const float* log_decay, bool final,
-                  void* workspace, size_t ws_bytes, LinTensor* const* tensors, int n_tensors, LinParams* p, DevInfo* di) {
+                  void* workspace, size_t ws_bytes, LinTensor* const* tensors, int n_tensors, LinParams* p) {
     const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, d, dv, final);
-    if ((double)plan.segments * Hkv * ((d > dv ? d : dv) / 64) >= 2.0e9 || (double)B * Hkv * d * dv / 256 >= 2.0e9)
+    // (runs, units and the scan's blocks are counted in ints)
+    const double chunks = cu ? (double)L / kLinChunk + B : (double)B * (L / kLinChunk + 1);
+    if (chunks * Hkv >= 1.0e9 || (double)B * Hkv * d * dv / 512 >= 2.0e9)
         return fail(ATTN_ERR_ARG, "linear: too many sequences and heads");
-    const size_t need = plan.split || final ? linear_bytes(plan, Hkv, d, dv) : 0;
+    const size_t need = linear_bytes(plan, d, dv);
     if (need > 0 && (!workspace || ws_bytes < need))
         return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return fail(ATTN_ERR_ALIGN, "workspace must be 256-byte aligned");
-    if (!device_info(di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
+    DevInfo di;
+    if (!device_info(&di)) return fail(ATTN_ERR_LAUNCH, "cannot query the current device");
     p->log_decay = log_decay;
     p->states = static_cast<float*>(workspace);
     p->cu = cu;
@@ -880,11 +883,10 @@ int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, co
     p->total = cu ? L : B * L;
     p->Hkv = Hkv;
     p->per = H / Hkv;
-    p->seg_rows = plan.seg_rows;
-    p->segments = plan.segments;
-    p->plan_split = plan.split;
+    p->ranges = plan.ranges;
+    p->whole = plan.whole;
     p->init_mul = p->final_mul = 1.f;
-    p->status = di->status;
+    p->status = di.status;
     p->wait_budget_ns = wait_budget_ns();
     if (p->total > 0)
         for (int i = 0; i < n_tensors; ++i) {
@@ -909,8 +911,8 @@ LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const
 extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v) {
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
     if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
-    const size_t with = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, true), Hkv, d, d_v);
-    const size_t without = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, false), Hkv, d, d_v);
+    const size_t with = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, true), d, d_v);
+    const size_t without = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, false), d, d_v);
     return with > without ? with : without;
 }
 
@@ -931,15 +933,14 @@ extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long
     LinTensor tq{q, q_stride, H, d}, tk{k, k_stride, Hkv, d}, tv{v, v_stride, Hkv, d_v}, to = lin_output(o, H, d_v);
     LinTensor* const all[] = {&tq, &tk, &tv, &to};
     LinParams p{};
-    DevInfo di;
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, final_state != nullptr, workspace, ws_bytes, all, 4, &p, &di)))
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, final_state != nullptr, workspace, ws_bytes, all, 4, &p)))
         return rc;
     const LinMaps maps = linear_roles(&p, tq, tk, tv, to);
     p.init = state;
     p.final = final_state;
     p.out_mul = scale;
-    cudaError_t e = launch_linear_states(p, maps, false, di.sms, stream);
-    if (e == cudaSuccess) e = launch_linear_out(p, maps, false, di.sms, stream);
+    cudaError_t e = launch_linear_states(p, maps, false, stream);
+    if (e == cudaSuccess) e = launch_linear_out(p, maps, false, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear forward launch failed: %s", cudaGetErrorString(e));
     return ok();
 }
@@ -965,8 +966,7 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
     LinTensor tdq = lin_output(dq, H, d), tdk = lin_output(dk, Hkv, d), tdv = lin_output(dv, Hkv, d_v);
     LinTensor* const all[] = {&tq, &tk, &tv, &tdo, &tdq, &tdk, &tdv};
     LinParams p{};
-    DevInfo di;
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, dstate != nullptr, workspace, ws_bytes, all, 7, &p, &di)))
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, dstate != nullptr, workspace, ws_bytes, all, 7, &p)))
         return rc;
     p.out_mul = scale;
     cudaError_t e = cudaSuccess;
@@ -974,8 +974,8 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
         const LinMaps maps = linear_roles(&p, tdo, tv, tk, tdq);
         p.init = state;
         p.init_trans = 1;
-        e = launch_linear_states(p, maps, false, di.sms, stream);
-        if (e == cudaSuccess) e = launch_linear_out(p, maps, false, di.sms, stream);
+        e = launch_linear_states(p, maps, false, stream);
+        if (e == cudaSuccess) e = launch_linear_out(p, maps, false, stream);
     }
     // dv and the gradient of the first state, and dk, backwards: its states are those of dv, transposed
     // (dstate, which may be dfinal's buffer, is written where the states are made: nothing reads dfinal behind)
@@ -985,12 +985,12 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
     p.final = dstate;
     p.final_mul = scale;
     const LinMaps maps = linear_roles(&p, tk, tq, tdo, tdv);
-    if (e == cudaSuccess) e = launch_linear_states(p, maps, true, di.sms, stream);
-    if (rows && e == cudaSuccess) e = launch_linear_out(p, maps, true, di.sms, stream);
+    if (e == cudaSuccess) e = launch_linear_states(p, maps, true, stream);
+    if (rows && e == cudaSuccess) e = launch_linear_out(p, maps, true, stream);
     if (rows && e == cudaSuccess) {
         const LinMaps maps_k = linear_roles(&p, tv, tdo, tq, tdk);
         p.init_trans = p.states_trans = 1;
-        e = launch_linear_out(p, maps_k, true, di.sms, stream);
+        e = launch_linear_out(p, maps_k, true, stream);
     }
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear backward launch failed: %s", cudaGetErrorString(e));
     return ok();

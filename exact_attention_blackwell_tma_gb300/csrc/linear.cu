@@ -18,53 +18,80 @@ namespace {
 
 constexpr int kScanThreads = 128;
 
-// Turns the segments' shares into the state that each of them starts from, in the
-// order of the walk: X = init, then X = D^rows X + share; and writes the last one. A
-// thread takes four neighbouring elements.
+// Turns the segments' shares into the states that their neighbours start from, in the order of the walk:
+// X = init, then X = D^rows X + share; and writes the last one. A thread takes four neighbouring elements.
 template <bool kBack>
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinParams p) {
+    __shared__ int s_before, s_all;
     const int size = p.DK * p.DV, blocks = size / (4 * kScanThreads);
-    const int bh = blockIdx.x / blocks, b = bh / p.Hkv, h = bh % p.Hkv, x = (blockIdx.x % blocks * kScanThreads + threadIdx.x) * 4;
-    int q0, n;
-    lin_sequence(p, b, &q0, &n);
-    const int s0 = lin_seg_start(p, b), count = max(1, (n + p.seg_rows - 1) / p.seg_rows);
-    if (s0 < 0 || s0 + count > p.segments) return;   // (bad offsets, reported)
+    const int run = blockIdx.x / blocks, b = run / p.Hkv, h = run - b * p.Hkv;
+    const int x = ((blockIdx.x - run * blocks) * kScanThreads + threadIdx.x) * 4;
     float4 X = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.init) {
-        const float* src = p.init + (long)bh * size;
+    if (p.init) {   // (loaded before the offsets are looked at: their latencies overlap)
+        const float* src = p.init + (long)run * size;
         if (p.init_trans) {
             const float* t = src + x % p.DV * p.DK + x / p.DV;
             X = make_float4(t[0], t[p.DK], t[2 * p.DK], t[3 * p.DK]);
         } else {
             X = *reinterpret_cast<const float4*>(src + x);
         }
-        X = make_float4(p.init_mul * X.x, p.init_mul * X.y, p.init_mul * X.z, p.init_mul * X.w);
     }
-    const float l2 = log2_decay(p, h), whole = decay_pow(l2, p.seg_rows);
-    const float part = decay_pow(l2, n - (count - 1) * p.seg_rows);   // over the rows of the segment that ends the sequence
-    float4* at = reinterpret_cast<float4*>(p.states + ((long)s0 * p.Hkv + h) * size + x);
-    const long step = (long)p.Hkv * size / 4;
-    constexpr int kAhead = 8;
-    for (int i = 0; i < count; i += kAhead) {   // (step i of the walk)
+    const float l2 = log2_decay(p, h);
+    int q0, n;
+    lin_sequence(p, b, &q0, &n);
+    // its units: unit0 .. unit0 + chunks - 1, in ranges first .. last
+    const int chunks = lin_chunks(n);
+    int first = 0, last = 0, each = 1;
+    long unit0 = 0;
+    if (!p.whole) {
+        if (threadIdx.x < 32) {
+            int before, all;
+            lin_chunks_before(p, b, threadIdx.x, &before, &all);
+            if (threadIdx.x == 0) {
+                s_before = before;
+                s_all = all;
+            }
+        }
+        __syncthreads();
+        each = lin_range_units(p, lin_units(p, s_all));
+        unit0 = (long)s_before * p.Hkv + (long)h * chunks;
+        first = (int)min(unit0 / each, (long)p.ranges - 1);
+        last = chunks > 0 ? (int)min((unit0 + chunks - 1) / each, (long)p.ranges - 1) : first;
+    }
+    X = make_float4(p.init_mul * X.x, p.init_mul * X.y, p.init_mul * X.z, p.init_mul * X.w);
+    const float4 start = X;
+    // rows of the run in range i (all of them, if it is not cut)
+    auto rows_in = [&](int i) {
+        if (first == last) return n;
+        const long lo = max(unit0, (long)i * each) - unit0, hi = min(unit0 + chunks, (long)(i + 1) * each) - unit0;
+        return (int)(min((long)n, hi * kLinChunk) - lo * kLinChunk);
+    };
+    float4* slots = reinterpret_cast<float4*>(p.states + x);
+    auto move = [&](float f, const float4& y) {
+        X = make_float4(fmaf(X.x, f, y.x), fmaf(X.y, f, y.y), fmaf(X.z, f, y.z), fmaf(X.w, f, y.w));
+    };
+    const int cuts = last - first;
+    constexpr int kAhead = 4;
+    for (int i = 0; i < cuts; i += kAhead) {   // (step i of the walk)
         float4 y[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int s = kBack ? count - 1 - i - k : i + k;
-            const bool in = i + k < count && (p.final || i + k < count - 1) && n > 0;
-            y[k] = in ? at[s * step] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k < cuts) y[k] = slots[(long)(kBack ? last - i - k : first + i + k) * (size / 4)];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            if (i + k >= count) break;
-            const int s = kBack ? count - 1 - i - k : i + k;
-            at[s * step] = X;
-            const float f = s == count - 1 ? part : whole;
-            X = make_float4(fmaf(X.x, f, y[k].x), fmaf(X.y, f, y[k].y), fmaf(X.z, f, y[k].z), fmaf(X.w, f, y[k].w));
+            if (i + k >= cuts) break;
+            const int r = kBack ? last - i - k : first + i + k;
+            move(decay_pow(l2, rows_in(r)), y[k]);
+            slots[(long)r * (size / 4)] = X;
         }
     }
-    if (p.final)
-        *reinterpret_cast<float4*>(p.final + (long)bh * size + x) =
+    if (p.final) {
+        float4* at = slots + ((long)p.cut_slots() + run) * (size / 4);
+        if (n > 0) move(decay_pow(l2, rows_in(kBack ? first : last)), *at);
+        *at = start;
+        *reinterpret_cast<float4*>(p.final + (long)run * size + x) =
             make_float4(X.x * p.final_mul, X.y * p.final_mul, X.z * p.final_mul, X.w * p.final_mul);
+    }
 }
 
 // ---------------------------------------------------------------- one token
@@ -132,36 +159,26 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const LinStepPar
 }  // namespace
 
 LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv, bool final) {
-    constexpr int kUnit = 128, kSms = 152;   // tokens of a chunk; CTAs of a wave on a GB300
-    const long longest = ((long)L + kUnit - 1) / kUnit;   // chunks that a sequence can have
-    const long units = packed ? (long)L / kUnit + B : B * longest;
-    const long tiles = (long)Hkv * (d == 128 && dv == 128 ? 1 : d / 64);
-    // Chunks of a segment: those that take the least time, counted in chunks of the outputs' kernel. A CTA's
-    // segments one after the other; a split call also needs the shares (half as long), and each segment costs its
-    // states' way through memory (64 KB four times, of two chunks' traffic) and a start of the walk.
-    long seg = longest;
-    double least = (double)((B * tiles + kSms - 1) / kSms) * longest * (final ? 1.5 : 1.0) + (final ? 4 : 0);
-    if (packed && B > 1) least = 1e30;   // (one long sequence may be most of a batch)
-    for (long x = 1; x < longest && x <= 64; ++x) {
-        const long segments = packed ? units / x + B / 2 : B * ((longest + x - 1) / x);
-        const double cost = (double)((segments * tiles + kSms - 1) / kSms) * (1.5 * x + 2) + 4;
-        if (cost < least) {
-            least = cost;
-            seg = x;
-        }
-    }
-    if (seg < 1) seg = 1;
+    constexpr int kSms = 152;   // CTAs of a wave on a GB300, one per SM
+    const int tiles = d == 128 && dv == 128 ? 1 : (d > dv ? d : dv) / 64;   // CTAs of a range (the transposed product's count if more)
+    const long most = kSms / tiles, runs = (long)B * Hkv, longest = ((long)L + kLinChunk - 1) / kLinChunk;
+    const long units = (packed ? (long)L / kLinChunk + B : B * longest) * Hkv;   // (packed: at most)
+    // Whole runs or ranges of units, whichever takes less time, counted in chunks of the outputs' kernel (4 us): where
+    // states are to be made it takes half as long again, and the two launches 24 us.
+    const double whole = (double)((runs + most - 1) / most) * longest * (final ? 1.5 : 1.0) + (final ? 6 : 0);
+    const double cut = (double)((units + most - 1) / most) * 1.5 + 6;
     LinPlan r;
-    r.split = seg < longest;
-    r.seg_rows = (int)(seg * kUnit);
-    r.segments = packed ? L / r.seg_rows + B : B * (int)(L > 0 ? ((long)L + r.seg_rows - 1) / r.seg_rows : 1);
+    r.whole = whole <= cut;
+    const long count = r.whole ? runs : units;
+    r.ranges = (int)(count < most ? (count < 1 ? 1 : count) : most);
+    r.slots = (r.whole ? 0 : r.ranges) + (final ? runs : 0);
     return r;
 }
 
-cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
+cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool back, cudaStream_t stream) {
     if (!p.split()) return cudaSuccess;
     if (p.total > 0) {
-        const cudaError_t e = launch_linear_shares(p, maps, back, num_sms, stream);
+        const cudaError_t e = launch_linear_shares(p, maps, back, stream);
         if (e != cudaSuccess) return e;
     }
     const unsigned blocks = (unsigned)((long)p.DK * p.DV / (4 * kScanThreads) * p.B * p.Hkv);

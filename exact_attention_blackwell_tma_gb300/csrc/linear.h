@@ -15,10 +15,13 @@
 // query heads share a state. o and dq have an output for each (a differs), dk and
 // dv sum over them (b and c differ): `back` says that, too.
 //
-// Sequences are cut into segments, numbered and chunked from their first token in
-// either direction; three kernels: what each segment adds to the state, the scan that
-// turns this into the state each segment starts from, the outputs. A call whose
-// sequences have one segment each, and that wants no state back, is the last one alone.
+// Segments. A run is a sequence's key/value head; it has a unit for every chunk of kLinChunk tokens, counted from
+// the first token in either direction. The runs' units lie in a row, sequence by sequence and head by head, and are cut
+// into `ranges` of the same length, so that every CTA has as much to do as the others (the chunks of 32 runs of 8192
+// tokens on 152 SMs: 13.5 each; whole segments of one length gave 16 to some). A segment is what a range has of
+// a run. Three kernels: what each segment that others follow adds to the state, the scan that turns this into the
+// state behind it, the outputs. A call whose runs are not cut (`whole`: range i has runs i, i + ranges, ..) and
+// that wants no state back is the last one alone.
 #pragma once
 
 #include "kernels.h"
@@ -31,26 +34,25 @@ struct LinParams {
     const float* log_decay;              // [Hkv], natural log
     const float* init;                   // [B][Hkv][DK][DV] ([DV][DK] with init_trans), or null
     float* final;                        // [B][Hkv][DK][DV], or null
-    float* states;                       // workspace: [segments][Hkv][DK][DV]
+    float* states;                       // workspace: [ranges if cut, and B Hkv with `final`][DK][DV] (see lin_share_slot)
     const int* cu;                       // row offsets, or null (dense)
     int B, rows, total;                  // rows per sequence (dense), rows in all
     int Hkv, per, DK, DV;
-    int seg_rows;                        // rows of a segment, a multiple of a chunk's
-    int segments;                        // upper bound of the segments of all sequences
-    int plan_split;                      // some sequence may have more than one
-    int init_trans, states_trans;        // (states_trans: [segments][Hkv][DV][DK], the states of the transposed product)
+    int ranges, whole;
+    int init_trans, states_trans;        // (states_trans: [..][DV][DK], the states of the transposed product)
     float out_mul, init_mul, final_mul;
     int* status;
     uint64_t wait_budget_ns;
-    // whether the states go through the workspace (with `final`, whose buffer may be init's, they do)
-    __host__ __device__ bool split() const { return plan_split || final; }
+    // whether there are states to make
+    __host__ __device__ bool split() const { return !whole || final; }
+    __host__ __device__ int cut_slots() const { return whole ? 0 : ranges; }
 };
 
-// Segments. A sequence of n rows has ceil(n / seg_rows), at least one, numbered
-// from lin_seg_start on: that leaves gaps but needs no scan over the lengths.
+constexpr int kLinChunk = 128;
+
 struct LinPlan {
-    int seg_rows, segments;
-    bool split;   // some sequence may have more than one segment
+    int ranges, whole;
+    long slots;   // states of the workspace
 };
 LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv, bool final);   // final: the last states are wanted
 
@@ -60,10 +62,10 @@ struct LinMaps {
 };
 
 // The states that the segments start from, and the last one (nothing to do without several segments or `final`); the outputs
-cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
-cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool back, cudaStream_t stream);
+cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, cudaStream_t stream);
 // (the first half of the states: what each segment adds)
-cudaError_t launch_linear_shares(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_shares(const LinParams& p, const LinMaps& maps, bool back, cudaStream_t stream);
 
 struct LinStepParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -77,14 +79,23 @@ struct LinStepParams {
 cudaError_t launch_linear_step(const LinStepParams& p, cudaStream_t stream);
 
 #ifdef __CUDACC__
-// A segment of a sequence: rows [r0, r1) of its n, q0 its first row.
-struct Segment {
-    int b, q0, n, r0, r1;
-    bool first, last, live;
+struct LinSegment {
+    int run, h, row0, rows;        // rows row0 .. of the tensors; rows = 0: no more
+    int after_start, before_end;   // whether the run has units in front of it, and behind it
 };
-__device__ __forceinline__ int lin_seg_start(const LinParams& p, int b) {
-    return p.cu ? __ldg(p.cu + b) / p.seg_rows + b : b * max(1, (p.rows + p.seg_rows - 1) / p.seg_rows);
+// Where a segment's share goes, and the state it starts from (-1: the call's initial state). Slot i < cut_slots is range
+// i's: what its last segment (backwards: its first), cut off by the range's end, adds, and then, by the scan, the
+// state that its neighbour starts from. Slot cut_slots + run: the share of the segment that ends a walk and, by
+// the scan, the run's initial state (whose own buffer may be `final`, which is written before the outputs are).
+__device__ __forceinline__ int lin_share_slot(const LinParams& p, const LinSegment& g, int range, bool back) {
+    return (back ? g.after_start : g.before_end) ? range : p.cut_slots() + g.run;
 }
+__device__ __forceinline__ int lin_start_slot(const LinParams& p, const LinSegment& g, int range, bool back) {
+    // (within the slots whatever the offsets)
+    if (back ? g.before_end : g.after_start) return back ? min(range + 1, p.ranges - 1) : max(range - 1, 0);
+    return p.final ? p.cut_slots() + g.run : -1;
+}
+
 // Rows [q0, q0 + n) of sequence b. Offsets out of range make an empty sequence (reported).
 __device__ __forceinline__ void lin_sequence(const LinParams& p, int b, int* q0, int* n) {
     if (!p.cu) {
@@ -99,35 +110,110 @@ __device__ __forceinline__ void lin_sequence(const LinParams& p, int b, int* q0,
         *q0 = *n = 0;
     }
 }
-// (A start that is off for bad offsets only moves segments, which are then not live or read another one's state.)
-__device__ __forceinline__ Segment segment_at(const LinParams& p, int s) {
-    Segment g;
-    if (p.cu) {
-        int lo = 0, hi = p.B - 1;   // the last b that starts at s or before
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (lin_seg_start(p, mid) <= s) lo = mid;
-            else hi = mid - 1;
-        }
-        g.b = lo;
-    } else {
-        g.b = s / max(1, (p.rows + p.seg_rows - 1) / p.seg_rows);
+__device__ __forceinline__ int lin_chunks(int n) { return (n + kLinChunk - 1) / kLinChunk; }
+// Chunks of the sequences in front of b, and of all (a warp's work; units are Hkv times as many, below 2^30: rows are)
+__device__ __forceinline__ void lin_chunks_before(const LinParams& p, int b, int lane, int* before, int* all) {
+    if (!p.cu) {
+        *before = b * lin_chunks(p.rows);
+        *all = p.B * lin_chunks(p.rows);
+        return;
     }
-    lin_sequence(p, g.b, &g.q0, &g.n);
-    const int i = s - lin_seg_start(p, g.b), count = max(1, (g.n + p.seg_rows - 1) / p.seg_rows);
-    g.live = i >= 0 && i < count;
-    g.first = i == 0;
-    g.last = i == count - 1;
-    g.r0 = g.live ? i * p.seg_rows : 0;
-    g.r1 = g.live ? min(g.n, g.r0 + p.seg_rows) : 0;
-    return g;
+    constexpr int kMost = 1 << 25;   // (more than there are for offsets that ascend; the sums stay ints)
+    int x = 0, y = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        int q0, n;
+        lin_sequence(p, i, &q0, &n);
+        y = min(y + lin_chunks(n), kMost);
+        if (i < b) x = min(x + lin_chunks(n), kMost);
+    }
+    *before = (int)__reduce_add_sync(0xffffffffu, (unsigned)x);
+    *all = (int)__reduce_add_sync(0xffffffffu, (unsigned)y);
 }
+// Units of a range. Bad offsets can overlap, which may make more units than rows: a product that leaves int is capped,
+// the units behind it are not worked on.
+__device__ __forceinline__ int lin_units(const LinParams& p, int chunks) {
+    const long u = (long)chunks * p.Hkv;
+    return u < (1L << 30) ? (int)u : 1 << 30;
+}
+__device__ __forceinline__ int lin_range_units(const LinParams& p, int units) { return max(1, (units + p.ranges - 1) / p.ranges); }
 
-// The state that segment s (of sequence b) starts from, or null (zeros)
-__device__ __forceinline__ const float* lin_state_src(const LinParams& p, int s, int b, int h) {
-    const long size = (long)p.DK * p.DV;
-    return p.split() ? p.states + ((long)s * p.Hkv + h) * size : p.init ? p.init + ((long)b * p.Hkv + h) * size : nullptr;
-}
+// Yields a range's segments in the order of the units (for one warp, all lanes alike).
+struct LinFinder {
+    int u, end, b, h, q0, n, c0, step;   // the next unit, that of sequence b and head h at chunk c0
+    __device__ __forceinline__ LinFinder(const LinParams& p, int range, int lane) {
+        step = p.whole ? p.ranges : 1;
+        if (p.whole) {   // u and end count runs
+            u = range;
+            end = p.B * p.Hkv;
+            if (u < end) at_run(p, u);
+            return;
+        }
+        int skip, chunks;
+        lin_chunks_before(p, 0, lane, &skip, &chunks);
+        const int units = lin_units(p, chunks), each = lin_range_units(p, units);
+        u = (int)min((long)range * each, (long)units);
+        end = min(units, u + each);
+        if (u >= end) return;
+        // the sequence that holds unit u, and the units in front of it
+        long before = 0;
+        if (!p.cu) {
+            b = u / p.Hkv / lin_chunks(p.rows);
+            before = (long)b * lin_chunks(p.rows) * p.Hkv;
+        } else {
+            for (int b0 = 0;; b0 += 32) {
+                int c = 0;
+                if (b0 + lane < p.B) {
+                    lin_sequence(p, b0 + lane, &q0, &n);
+                    c = lin_chunks(n);
+                }
+                int sum = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, before + (long)sum * p.Hkv > u);
+                if (past || b0 + 32 >= p.B) {
+                    const int at = past ? __ffs(past) - 1 : 31;
+                    before += (long)__shfl_sync(0xffffffffu, sum - c, at) * p.Hkv;
+                    b = min(b0 + at, p.B - 1);
+                    break;
+                }
+                before += (long)__shfl_sync(0xffffffffu, sum, 31) * p.Hkv;
+            }
+        }
+        lin_sequence(p, b, &q0, &n);
+        const int c = max(1, lin_chunks(n));
+        h = min((int)((u - before) / c), p.Hkv - 1);
+        c0 = (int)(u - before) - h * c;
+    }
+    __device__ __forceinline__ void at_run(const LinParams& p, int run) {
+        b = run / p.Hkv;
+        h = run - b * p.Hkv;
+        lin_sequence(p, b, &q0, &n);
+        c0 = 0;
+    }
+    __device__ __forceinline__ LinSegment next(const LinParams& p) {
+        while (u < end && b < p.B) {
+            const int c = lin_chunks(n), c1 = p.whole ? c : min(c, c0 + end - u);
+            const LinSegment g{b * p.Hkv + h, h, q0 + c0 * kLinChunk, min(n, c1 * kLinChunk) - c0 * kLinChunk, c0 > 0, c1 < c};
+            if (p.whole) {
+                u += step;
+                if (u < end) at_run(p, u);
+            } else {
+                u += c1 - c0;
+                c0 = 0;
+                if (u < end && ++h == p.Hkv) {
+                    h = 0;
+                    if (++b < p.B) lin_sequence(p, b, &q0, &n);
+                }
+            }
+            if (g.rows > 0) return g;
+        }
+        return LinSegment{0, 0, 0, 0, 0, 0};
+    }
+};
+
 __device__ __forceinline__ float log2_decay(const LinParams& p, int h) {
     const float l = p.log_decay[h] * kLog2e;
     return l > 0.f ? 0.f : l;   // (a decay above 1 counts as 1; NaN stays)

@@ -16,7 +16,7 @@
 //   warp 16      tile loads (TMA), a ring for each of a, b and c
 //   warp 17      the products, each issued by an elected lane of the converged warp:
 //                P = a b^T;  O2 = a X;  O1 = P c;  KV = (w b)^T c
-//   warp 18      which segments and heads come next
+//   warp 18      which segments come next
 // The tensor pipe executes in issue order, so the next scores may be issued behind the product
 // that reads P. Every wait is bounded.
 //
@@ -121,57 +121,44 @@ __device__ __forceinline__ uint4* piece_at(uint8_t* tile, int row, int piece) {
     return reinterpret_cast<uint4*>(tile + (piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// The CTA's (segment, head, tile of columns) triples. One warp finds them (a search over the offsets)
-// and hands them to the others through a ring in shared memory: the search in each role's loop made the code
-// several times as long, and warps that resume from a wait missed the instruction cache.
-struct Triple {
-    int s, b, h, tile, row0, rows;   // rows row0 .. of the tensors; rows = 0: the end
+// The CTA's segments. One warp finds them (LinFinder searches the offsets) and hands them to the others through a
+// ring in shared memory: the search in each role's loop made the code several times as long, and warps that resume from
+// a wait missed the instruction cache.
+constexpr int kSegments = 4;   // entries of the ring
+struct SegmentRing {
+    LinSegment at[kSegments];
 };
-constexpr int kTriples = 4;   // entries of the ring
-struct TripleRing {
-    Triple at[kTriples];
-};
-template <int DT, bool kBack>
-__device__ __forceinline__ void find_triples(const LinParams& p, TripleRing* ring, uint32_t full, uint32_t empty, const WaitCtx& w,
-                                             int lane, bool all) {
-    const int nt = p.DV / DT, n = p.segments * p.Hkv * nt;
-    uint32_t i = 0;
-    for (int k = blockIdx.x;; k += gridDim.x) {
-        Triple t{};
-        if (k < n) {
-            const int sh = k / nt;
-            t.tile = k - sh * nt;
-            t.s = sh / p.Hkv;
-            t.h = sh - t.s * p.Hkv;
-            const Segment g = segment_at(p, t.s);
-            if (!g.live || g.r0 == g.r1 || (!all && (kBack ? g.first : g.last))) continue;
-            t.b = g.b;
-            t.row0 = g.q0 + g.r0;
-            t.rows = g.r1 - g.r0;
-        }
-        if (!wait_all(empty + 8 * (i % kTriples), ((i / kTriples) & 1u) ^ 1u, w)) return;
+template <bool kBack>
+__device__ __forceinline__ void find_segments(const LinParams& p, int range, SegmentRing* ring, uint32_t full, uint32_t empty,
+                                              const WaitCtx& w, int lane, bool shares) {
+    LinFinder finder(p, range, lane);
+    LinSegment g;
+    for (uint32_t i = 0;; ++i) {
+        // (only those whose share somebody wants: the next segment, or who wants the last state)
+        do g = finder.next(p);
+        while (shares && g.rows > 0 && !(kBack ? g.after_start : g.before_end) && !p.final);
+        if (!wait_all(empty + 8 * (i % kSegments), ((i / kSegments) & 1u) ^ 1u, w)) return;
         if (lane == 0) {
-            ring->at[i % kTriples] = t;
-            mbar_arrive(full + 8 * (i % kTriples));
+            ring->at[i % kSegments] = g;
+            mbar_arrive(full + 8 * (i % kSegments));
         }
         __syncwarp();
-        ++i;
-        if (k >= n) return;
+        if (g.rows == 0) return;
     }
 }
 // A role's place in the walk. An item is a chunk (the outputs forwards, shares backwards: of one query head, x).
 struct Walk {
-    Triple t;
+    LinSegment t;
     int chunks, chunk, x, per;
     uint32_t taken;
     bool live;
 };
-__device__ __forceinline__ bool next_triple(Walk& i, const TripleRing* ring, uint32_t full, uint32_t empty, const WaitCtx& w,
-                                            int lane) {
-    const uint32_t slot = i.taken % kTriples;
-    if (!wait_all(full + 8 * slot, (i.taken / kTriples) & 1u, w)) return false;
-    const Triple& t = ring->at[slot];
-    i.t = Triple{uniform(t.s), uniform(t.b), uniform(t.h), uniform(t.tile), uniform(t.row0), uniform(t.rows)};
+__device__ __forceinline__ bool next_segment(Walk& i, const SegmentRing* ring, uint32_t full, uint32_t empty, const WaitCtx& w,
+                                             int lane) {
+    const uint32_t slot = i.taken % kSegments;
+    if (!wait_all(full + 8 * slot, (i.taken / kSegments) & 1u, w)) return false;
+    const LinSegment& t = ring->at[slot];
+    i.t = LinSegment{uniform(t.run), uniform(t.h), uniform(t.row0), uniform(t.rows), uniform(t.after_start), uniform(t.before_end)};
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + 8 * slot);
     ++i.taken;
@@ -218,9 +205,9 @@ struct OutLay {
     static constexpr int kAFull = 0, kAFree = 2, kBFull = 4, kBFree = 6, kCFull = 8, kCFree = 10, kPFull = 12, kPReady = 13,
                          kWReady = 14, kTFree = 16, kOFull = 18, kOFree = 19, kXReady = 20, kKVFull = 21, kDrain = 22,
                          kRFull = 23,
-                         kREmpty = kRFull + kTriples, kNumBars = kREmpty + kTriples;
+                         kREmpty = kRFull + kSegments, kNumBars = kREmpty + kSegments;
     static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16, kRingOff = kMiscOff + 16;
-    static constexpr int kPowOff = kRingOff + (int)sizeof(TripleRing), kBytes = kPowOff + 8 * 64 * 4;   // 64 floats for each of warps 8-15
+    static constexpr int kPowOff = kRingOff + (int)sizeof(SegmentRing), kBytes = kPowOff + 8 * 64 * 4;   // 64 floats for each of warps 8-15
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
     static_assert(kXOff % 1024 == 0 && kTermOff % 1024 == 0 && kBarOff % 16 == 0 && kPowOff % 16 == 0, "alignment of tiles and tables");
     static constexpr uint32_t kTmP = 0, kTmO1 = 128, kTmO2 = 128 + DT, kTmKV = 128 + 2 * DT;
@@ -246,7 +233,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMiscOff + 4);
-    TripleRing* ring = reinterpret_cast<TripleRing*>(smem + Lay::kRingOff);
+    SegmentRing* ring = reinterpret_cast<SegmentRing*>(smem + Lay::kRingOff);
     if (tid == 0) {
 #pragma unroll 1
         for (int i = 0; i < Lay::kNumBars; ++i) {
@@ -273,12 +260,13 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     const uint32_t tmem = *tmem_slot;
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
     const int per = p.per;
+    const int nt = p.DV / DT, range = blockIdx.x / nt, tile = blockIdx.x - range * nt;
     Walk at;
     at.per = per;
     at.taken = 0;
     bool ok = true;
-    auto take = [&] { return next_triple(at, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane); };
-    auto advance = [&] {   // to the next item; true where a new triple is due
+    auto take = [&] { return next_segment(at, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane); };
+    auto advance = [&] {   // to the next item; true where a new segment is due
         if (++at.x < at.per) return false;
         at.x = 0;
         return ++at.chunk == at.chunks;
@@ -292,7 +280,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (warp >= 16) {
         setmaxnreg_dec<kOutRegsRest>();
         if (warp == 18) {
-            find_triples<DT, kBack>(p, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, true);
+            find_segments<kBack>(p, range, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, false);
         } else if (warp == 16) {
             // ------------------------------------------------------------ loads
             uint32_t na = 0, nb = 0, sent_b = 0;   // tiles of a, of b and c
@@ -331,7 +319,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         mbar_expect_tx(full, Lay::kC);
 #pragma unroll
                         for (int y = 0; y < DT / 64; ++y)
-                            tma_load_3d(to + y * kBox, &maps.c, full, at.t.tile * DT + y * 64, hb, row);
+                            tma_load_3d(to + y * kBox, &maps.c, full, tile * DT + y * 64, hb, row);
                     }
                     __syncwarp();
                     ++nb;
@@ -371,7 +359,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         ++xs;
                         if (!(ok = wait_unless(o_done, bar(Lay::kOFree), (outs & 1u) ^ 1u, w))) break;
                         tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll
                         for (int y = 0; y < DK / 16; ++y)
                             mma_ss_w(tmem + Lay::kTmO2, a_km, a_off + desc_step((y >> 2) * kBox + (y & 3) * 32), x_mn,
                                      desc_step(y * 2048), kIdN, y > 0);
@@ -384,7 +372,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                     }
                     if (!(ok = wait_unless(p_done, bar(Lay::kPReady), it & 1u, w))) break;
                     tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll
                     for (int y = 0; y < 8; ++y)
                         mma_ts_w(tmem + Lay::kTmO1, tmem + Lay::kTmP + (y >> 1) * 32 + (y & 1) * 8, c_mn, c_off + desc_step(y * 2048),
                                  kIdN, !head || y > 0);
@@ -415,7 +403,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         b_st = (nb - 1) % RB;
                         tc_fence_after_sync();
                         const uint32_t next_a = desc_step(a_st * Lay::kB), next_b = desc_step(b_st * Lay::kB);
-#pragma unroll 1
+#pragma unroll
                         for (int y = 0; y < DK / 16; ++y) {
                             const uint32_t step = desc_step((y >> 2) * kBox + (y & 3) * 32);
                             mma_ss_w(tmem + Lay::kTmP, a_km, next_a + step, b_km, next_b + step, kIdP, y > 0);
@@ -439,11 +427,11 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                                                                        : base + Lay::kTermOff + buf * Lay::kTerm;
                                     const SmemDesc t_mn = weighted_desc<DK>(t_at, mt, Lay::kShareA ? kBox : kHalf);
                                     const uint32_t kv = tmem + Lay::kTmKV + mt * DT;
-#pragma unroll 1
+#pragma unroll
                                     for (int y = 0; y < 4; ++y)
                                         mma_ss_w(kv, b_mn, rows0 + rows + desc_step(y * 2048), c_mn, c_off + rows + desc_step(y * 2048),
                                                  kIdKV, y > 0 ? 1u : more);
-#pragma unroll 1
+#pragma unroll
                                     for (int y = 0; y < 4; ++y)
                                         mma_ss_w(kv, t_mn, desc_step(y * 2048), c_mn, c_off + rows + desc_step(y * 2048), kIdKV, 1);
                                 }
@@ -622,10 +610,13 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             if (fresh && !(ok = take())) break;
             if (last && at.live) {   // (X is in shared memory: the registers take the next segment's)
                 l2 = log2_decay(p, at.t.h);
-                const float* src = lin_state_src(p, at.t.s, at.t.b, at.t.h);
-                const float mul = p.split() ? 1.f : p.init_mul;
-                const bool trans = p.split() ? p.states_trans : p.init_trans;
-                const int c0 = at.t.tile * DT + col0;
+                // forwards it starts behind the range before's last segment, backwards in front of the one after's first
+                const int slot = lin_start_slot(p, at.t, range, kBack);
+                const bool trans = slot >= 0 ? p.states_trans : p.init_trans;
+                const float mul = slot >= 0 ? 1.f : p.init_mul;
+                const long size = (long)DK * p.DV;
+                const float* src = slot >= 0 ? p.states + slot * size : p.init ? p.init + at.t.run * size : nullptr;
+                const int c0 = tile * DT + col0;
                 if (!src || !has_x) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) X[c] = 0.f;
@@ -713,7 +704,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             over = decay_pow(l2, n);
             token0 = at.t.row0 + r0;
             head = kBack ? at.t.h : at.t.h * per + at.x;
-            column = at.t.tile * DT + col0;
+            column = tile * DT + col0;
         }
         if (lane == 0) bulk_wait_group0();
         __syncwarp();
@@ -737,9 +728,9 @@ struct StateLay {
     static constexpr int kTerm = DK / 64 * kHalf, kSets = DK <= 192 ? 2 : 1;   // sets of buffers
     static constexpr int kTermOff = 2 * kStage, kBarOff = kTermOff + kSets * 2 * kTerm + kTailPad<DK>;
     static constexpr int kFull = 0, kEmpty = 2, kWReady = 4, kWFree = 6, kSFull = 8, kSFree = 10, kDrain = 12, kRFull = 13,
-                         kREmpty = kRFull + kTriples, kNumBars = kREmpty + kTriples;
+                         kREmpty = kRFull + kSegments, kNumBars = kREmpty + kSegments;
     static constexpr int kMiscOff = kBarOff + (kNumBars + 1) / 2 * 16, kRingOff = kMiscOff + 16;
-    static constexpr int kBytes = kRingOff + (int)sizeof(TripleRing);
+    static constexpr int kBytes = kRingOff + (int)sizeof(SegmentRing);
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
     static_assert(kTermOff % 1024 == 0 && kBarOff % 16 == 0 && kRingOff % 8 == 0, "alignment of tiles and tables");
     static constexpr uint32_t kAcc = MT * DT, kCols = 2 * kAcc <= 128 ? 128 : 256;
@@ -762,7 +753,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kMiscOff + 4);
-    TripleRing* ring = reinterpret_cast<TripleRing*>(smem + Lay::kRingOff);
+    SegmentRing* ring = reinterpret_cast<SegmentRing*>(smem + Lay::kRingOff);
     if (tid == 0) {
 #pragma unroll 1
         for (int i = 0; i < Lay::kNumBars; ++i) {
@@ -785,12 +776,13 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
+    const int nt = p.DV / DT, range = blockIdx.x / nt, tile = blockIdx.x - range * nt;
     Walk at;
     at.per = kBack ? p.per : 1;
     at.taken = 0;
     bool ok = true;
-    auto take = [&] { return next_triple(at, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane); };
-    auto advance = [&] {   // to the next item; true where a new triple is due
+    auto take = [&] { return next_segment(at, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane); };
+    auto advance = [&] {   // to the next item; true where a new segment is due
         if (++at.x < at.per) return false;
         at.x = 0;
         return ++at.chunk == at.chunks;
@@ -799,8 +791,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     uint32_t it = 0;
 
     if (warp == 14) {
-        // (without a final state the segment that a walk visits last is not needed)
-        find_triples<DT, kBack>(p, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, p.final != nullptr);
+        find_segments<kBack>(p, range, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, true);
     } else if (warp == 12) {
         // ------------------------------------------------------------ loads
         for (bool fresh = true;; fresh = advance(), ++it) {
@@ -816,7 +807,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 for (int y = 0; y < DK / 64; ++y) tma_load_3d(to + y * kBox, &maps.b, full, y * 64, hb, row);
 #pragma unroll
                 for (int y = 0; y < DT / 64; ++y)
-                    tma_load_3d(to + Lay::kB + y * kBox, &maps.c, full, at.t.tile * DT + y * 64, hb, row);
+                    tma_load_3d(to + Lay::kB + y * kBox, &maps.c, full, tile * DT + y * 64, hb, row);
             }
             __syncwarp();
         }
@@ -843,12 +834,13 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 for (int mt = 0; mt < MT; ++mt) {
                     const SmemDesc b_mn = weighted_desc<DK>(base, mt, kBox);
                     const SmemDesc t_mn = weighted_desc<DK>(base + Lay::kTermOff + 2 * set * Lay::kTerm, mt, kHalf);
-#pragma unroll 1
+#pragma unroll
                     for (int y = 0; y < 4; ++y)
                         mma_ss_w(acc + mt * DT, b_mn, c0 + desc_step(y * 2048), c_mn, c0 + desc_step(y * 2048), kIdKV, y > 0 ? 1u : more);
-#pragma unroll 1
-                    for (int y = 0; y < 4 * (terms - 1); ++y)
-                        mma_ss_w(acc + mt * DT, t_mn, desc_step((y >> 2) * Lay::kTerm + (y & 3) * 2048), c_mn,
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        if (y < 4 * (terms - 1))
+                            mma_ss_w(acc + mt * DT, t_mn, desc_step((y >> 2) * Lay::kTerm + (y & 3) * 2048), c_mn,
                                  c0 + desc_step((y & 3) * 2048), kIdKV, 1);
                 }
                 commit_w(bar(Lay::kWFree + set));
@@ -928,7 +920,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (sums & 1u) * Lay::kAcc;
 #pragma unroll 1
             for (int mt = 0; mt < MT; ++mt) {
-                float* dst = p.states + (((long)at.t.s * p.Hkv + at.t.h) * DK + tile_channel<DK>(mt) + row) * p.DV + at.t.tile * DT;
+                float* dst = p.states + ((long)lin_share_slot(p, at.t, range, kBack) * DK + tile_channel<DK>(mt) + row) * p.DV + tile * DT;
 #pragma unroll 1
                 for (int c = 0; c < DT; c += 32) {
                     uint32_t r[32];
@@ -953,11 +945,11 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 }
 
 template <class Kernel>
-cudaError_t launch_tc(Kernel kern, int threads, int bytes, long triples, std::atomic<unsigned long long>& allowed,
-                      const LinParams& p, const LinMaps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tc(Kernel kern, int threads, int bytes, int tiles, std::atomic<unsigned long long>& allowed,
+                      const LinParams& p, const LinMaps& maps, cudaStream_t stream) {
     cudaError_t e = allow_smem(kern, bytes, allowed);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(triples < num_sms ? triples : num_sms), threads, bytes, stream>>>(maps, p);
+    kern<<<(unsigned)(p.ranges * tiles), threads, bytes, stream>>>(maps, p);
     return cudaGetLastError();
 }
 // The registers that the roles share out must be those of the launch (asked once per kernel and device set)
@@ -973,36 +965,34 @@ cudaError_t check_regs(Kernel kern, std::atomic<int>& done) {
 }
 
 template <int DK, int DT, bool kBack>
-cudaError_t launch_one(bool outputs, const LinParams& p, const LinMaps& maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch_one(bool outputs, const LinParams& p, const LinMaps& maps, cudaStream_t stream) {
     static std::atomic<unsigned long long> allowed[2];
     static std::atomic<int> regs;
-    const long triples = (long)p.segments * p.Hkv * (p.DV / DT);
+    const int tiles = p.DV / DT;
     if (!outputs)
-        return launch_tc(lin_state_tc_kernel<DK, DT, kBack>, kStateThreads, StateLay<DK, DT>::kBytes, triples, allowed[0], p, maps,
-                         num_sms, stream);
+        return launch_tc(lin_state_tc_kernel<DK, DT, kBack>, kStateThreads, StateLay<DK, DT>::kBytes, tiles, allowed[0], p, maps, stream);
     const cudaError_t e = check_regs(lin_out_tc_kernel<DK, DT, kBack>, regs);
     if (e != cudaSuccess) return e;
-    return launch_tc(lin_out_tc_kernel<DK, DT, kBack>, kOutThreads, OutLay<DK, DT>::kBytes, triples, allowed[1], p, maps, num_sms,
-                     stream);
+    return launch_tc(lin_out_tc_kernel<DK, DT, kBack>, kOutThreads, OutLay<DK, DT>::kBytes, tiles, allowed[1], p, maps, stream);
 }
 template <bool kBack>
-cudaError_t launch_dims(bool outputs, const LinParams& p, const LinMaps& maps, int num_sms, cudaStream_t stream) {
-    if (p.DK == 64) return launch_one<64, 64, kBack>(outputs, p, maps, num_sms, stream);
-    if (p.DK == 128 && p.DV == 128) return launch_one<128, 128, kBack>(outputs, p, maps, num_sms, stream);
-    if (p.DK == 128) return launch_one<128, 64, kBack>(outputs, p, maps, num_sms, stream);
-    if (p.DK == 192) return launch_one<192, 64, kBack>(outputs, p, maps, num_sms, stream);
-    if (p.DK == 256) return launch_one<256, 64, kBack>(outputs, p, maps, num_sms, stream);
+cudaError_t launch_dims(bool outputs, const LinParams& p, const LinMaps& maps, cudaStream_t stream) {
+    if (p.DK == 64) return launch_one<64, 64, kBack>(outputs, p, maps, stream);
+    if (p.DK == 128 && p.DV == 128) return launch_one<128, 128, kBack>(outputs, p, maps, stream);
+    if (p.DK == 128) return launch_one<128, 64, kBack>(outputs, p, maps, stream);
+    if (p.DK == 192) return launch_one<192, 64, kBack>(outputs, p, maps, stream);
+    if (p.DK == 256) return launch_one<256, 64, kBack>(outputs, p, maps, stream);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_linear_shares(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
-    return back ? launch_dims<true>(false, p, maps, num_sms, stream) : launch_dims<false>(false, p, maps, num_sms, stream);
+cudaError_t launch_linear_shares(const LinParams& p, const LinMaps& maps, bool back, cudaStream_t stream) {
+    return back ? launch_dims<true>(false, p, maps, stream) : launch_dims<false>(false, p, maps, stream);
 }
-cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, int num_sms, cudaStream_t stream) {
+cudaError_t launch_linear_out(const LinParams& p, const LinMaps& maps, bool back, cudaStream_t stream) {
     if (p.total == 0) return cudaSuccess;
-    return back ? launch_dims<true>(true, p, maps, num_sms, stream) : launch_dims<false>(true, p, maps, num_sms, stream);
+    return back ? launch_dims<true>(true, p, maps, stream) : launch_dims<false>(true, p, maps, stream);
 }
 
 }  // namespace attn
