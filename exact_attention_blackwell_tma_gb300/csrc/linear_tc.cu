@@ -36,6 +36,15 @@ constexpr int kCh = 128;                 // tokens of a chunk
 constexpr int kBox = 16384;              // 128 rows x 64 columns
 constexpr int kHalf = kBox / 2;          // 64 rows
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 // Two loads of 16 columns and one wait
 __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&r)[16], uint32_t (&s)[16]) {
     asm volatile(
@@ -718,9 +727,10 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 }
 
 // ---------------------------------------------------------------- segments' shares
-// X' of a segment for X = 0: one sum over its tokens in tensor memory, each weighted by the
-// decay up to the segment's end (backwards: its start), b times that weight in bf16 terms: the first in
-// place, the others in buffers of 64 tokens. Three terms (all 24 bits) where a state leaves the call, else two
+// X' of a segment for X = 0. An item's sum is made in tensor memory, its tokens weighted by the decay up to the
+// chunk's end (backwards: its start), and added to the segment's in registers: the tensor cores' sums are cut off rather
+// than rounded, which over 5000 tokens of four query heads in one sum made 4e-6 of a state. b times the weight is in
+// bf16 terms: the first in place, the others in buffers of 64 tokens. Three terms (all 24 bits) where a state leaves the call, else two
 // (the states are rounded to 8 bits by the products that use them).
 template <int DK, int DT>
 struct StateLay {
@@ -733,10 +743,11 @@ struct StateLay {
     static constexpr int kBytes = kRingOff + (int)sizeof(SegmentRing);
     static_assert(kBytes <= 227 * 1024, "shared memory budget");
     static_assert(kTermOff % 1024 == 0 && kBarOff % 16 == 0 && kRingOff % 8 == 0, "alignment of tiles and tables");
+    static constexpr int kWarpsR = DT == 128 || MT == 2 ? 8 : 4;   // as in OutLay
     static constexpr uint32_t kAcc = MT * DT, kCols = 2 * kAcc <= 128 ? 128 : 256;
     static_assert(2 * kAcc <= kCols, "tensor memory budget");
 };
-constexpr int kStateThreads = 480;   // warps 0-7: weights, 8-11: results, 12: loads, 13: products, 14: triples
+constexpr int kStateThreads = 608;   // warps 0-7: weights, 8-15: the segment's sum, 16: loads, 17: products, 18: segments
 
 template <int DK, int DT, bool kBack>
 __global__ void __launch_bounds__(kStateThreads, 1)
@@ -757,17 +768,17 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (tid == 0) {
 #pragma unroll 1
         for (int i = 0; i < Lay::kNumBars; ++i) {
-            const bool by_256 = i == Lay::kWReady || i == Lay::kWReady + 1, by_128 = i == Lay::kSFree || i == Lay::kSFree + 1;
-            mbar_init(bar(i), by_256 ? 256 : by_128 ? 128 : i >= Lay::kREmpty ? 14 : 1);
+            const bool by_w = i == Lay::kWReady || i == Lay::kWReady + 1, by_r = i == Lay::kSFree || i == Lay::kSFree + 1;
+            mbar_init(bar(i), by_w ? 256 : by_r ? 32 * Lay::kWarpsR : i >= Lay::kREmpty ? 10 + Lay::kWarpsR : 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 12 && lane == 0) {
+    if (warp == 16 && lane == 0) {
         tma_prefetch_desc(&maps.b);
         tma_prefetch_desc(&maps.c);
     }
-    if (warp == 13) {
+    if (warp == 17) {
         tmem_alloc(smem_addr(tmem_slot), Lay::kCols);
         tmem_relinquish();
     }
@@ -790,9 +801,9 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     const int terms = p.final ? 3 : 2;   // of the weighted b
     uint32_t it = 0;
 
-    if (warp == 14) {
+    if (warp == 18) {
         find_segments<kBack>(p, range, ring, bar(Lay::kRFull), bar(Lay::kREmpty), w, lane, true);
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         // ------------------------------------------------------------ loads
         for (bool fresh = true;; fresh = advance(), ++it) {
             if (fresh && !(ok = take())) break;
@@ -815,21 +826,20 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i)
                 drain_wait(bar(Lay::kFull + (i & 1u)), (i >> 1) & 1u, p.wait_budget_ns);
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 17) {
         // ------------------------------------------------------------ products
         constexpr uint32_t kIdKV = idesc_bf16_f32(128, DT, true, true);
         const SmemDesc c_mn = sdesc_sw128_split(base + Lay::kB, kBox, 1024);
-        uint32_t sums = 0;
-        for (bool fresh = true;; ++it) {
+        for (bool fresh = true;; fresh = advance(), ++it) {
             if (fresh && !(ok = take())) break;
             if (!at.live) break;
-            const uint32_t acc = tmem + (sums & 1u) * Lay::kAcc, st = it & 1u, off = desc_step(st * Lay::kStage);
-            if (fresh && !(ok = wait_all(bar(Lay::kSFree + (sums & 1u)), ((sums >> 1) & 1u) ^ 1u, w))) break;
+            const uint32_t st = it & 1u, acc = tmem + st * Lay::kAcc, off = desc_step(st * Lay::kStage);
+            if (!(ok = wait_all(bar(Lay::kSFree + st), ((it >> 1) & 1u) ^ 1u, w))) break;
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 if (!(ok = wait_all(bar(Lay::kWReady + half), it & 1u, w))) break;
                 tc_fence_after_sync();
-                const uint32_t c0 = off + desc_step(half * kHalf), set = Lay::kSets == 2 ? half : 0, more = !fresh || half > 0;
+                const uint32_t c0 = off + desc_step(half * kHalf), set = Lay::kSets == 2 ? half : 0, more = half > 0;
 #pragma unroll 1
                 for (int mt = 0; mt < MT; ++mt) {
                     const SmemDesc b_mn = weighted_desc<DK>(base, mt, kBox);
@@ -847,8 +857,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             }
             if (!ok) break;
             commit_w(bar(Lay::kEmpty + st));
-            fresh = advance();
-            if (fresh) commit_w(bar(Lay::kSFull + (sums++ & 1u)));
+            commit_w(bar(Lay::kSFull + st));
         }
         commit_w(bar(Lay::kDrain));
         if (lane == 0) drain_wait(bar(Lay::kDrain), 0, p.wait_budget_ns);
@@ -863,16 +872,16 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 if (!(ok = take()) || !at.live) break;
                 l2 = log2_decay(p, at.t.h);
             }
-            const int r0 = chunk_row<kBack>(at);
+            const int n = min(kCh, at.t.rows - chunk_row<kBack>(at));
             const uint32_t st = it & 1u;
             uint8_t* tiles = smem + st * Lay::kStage;
             if (!(ok = wait_all(bar(Lay::kFull + st), (it >> 1) & 1u, w))) break;
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                const int row = half * 64 + r64, r = r0 + row;
+                const int row = half * 64 + r64;
                 const uint32_t use = 2 * it + half, set = use % Lay::kSets;
-                const bool in = r < at.t.rows;
-                const float weight = in ? decay_pow(l2, kBack ? r + 1 : at.t.rows - 1 - r) : 0.f;
+                const bool in = row < n;
+                const float weight = in ? decay_pow(l2, kBack ? row + 1 : n - 1 - row) : 0.f;
                 uint8_t* buf = smem + Lay::kTermOff + 2 * set * Lay::kTerm;
                 if (!(ok = wait_all(bar(Lay::kWFree + set), ((use / Lay::kSets) & 1u) ^ 1u, w))) break;
                 constexpr int kPieces = DK / 32, kAtOnce = kPieces % 3 == 0 ? 3 : 2;
@@ -911,34 +920,44 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             if (!ok) break;
         }
     } else {
-        // ------------------------------------------------------------ results
-        const int row = (warp & 3) * 32 + lane;
-        for (uint32_t sums = 0;; ++sums) {
-            if (!(ok = take()) || !at.live) break;
-            if (!(ok = wait_all(bar(Lay::kSFull + (sums & 1u)), (sums >> 1) & 1u, w))) break;
-            tc_fence_after_sync();
-            const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (sums & 1u) * Lay::kAcc;
-#pragma unroll 1
-            for (int mt = 0; mt < MT; ++mt) {
-                float* dst = p.states + ((long)lin_share_slot(p, at.t, range, kBack) * DK + tile_channel<DK>(mt) + row) * p.DV + tile * DT;
-#pragma unroll 1
-                for (int c = 0; c < DT; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(t_row + mt * DT + c, r);
-                    if (tile_row<DK>(mt, row)) {
+        // ------------------------------------------------------------ the segment's sum
+        const int q4 = warp & 3, group = (warp - 8) >> 2, row = q4 * 32 + lane;
+        const int col0 = DT == 128 ? 64 * group : 0, mt = DT == 128 ? 0 : group;
+        const uint32_t t_row = tmem + ((uint32_t)(q4 * 32) << 16) + mt * DT + col0;
+        float X[64];
+        float l2 = 0.f;
+        for (bool fresh = true; warp < 8 + Lay::kWarpsR; ++it) {
+            if (fresh) {
+                if (!(ok = take()) || !at.live) break;
+                l2 = log2_decay(p, at.t.h);
 #pragma unroll
-                        for (int z = 0; z < 32; z += 8)   // (the workspace is 256-byte aligned)
-                            store32(dst + c + z, {r[z], r[z + 1], r[z + 2], r[z + 3], r[z + 4], r[z + 5], r[z + 6], r[z + 7]});
-                    }
-                }
+                for (int c = 0; c < 64; ++c) X[c] = 0.f;
+            }
+            const float over = at.x == 0 ? decay_pow(l2, min(kCh, at.t.rows - chunk_row<kBack>(at))) : 1.f;
+            const uint32_t st = it & 1u;
+            if (!(ok = wait_all(bar(Lay::kSFull + st), (it >> 1) & 1u, w))) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(t_row + st * Lay::kAcc + c, r);
+#pragma unroll
+                for (int z = 0; z < 16; ++z) X[c + z] = fmaf(X[c + z], over, u2f(r[z]));
             }
             tc_fence_before_sync();
-            mbar_arrive(bar(Lay::kSFree + (sums & 1u)));
+            mbar_arrive(bar(Lay::kSFree + st));
+            const int slot = lin_share_slot(p, at.t, range, kBack);
+            if (!(fresh = advance()) || !tile_row<DK>(mt, row)) continue;
+            float* dst = p.states + ((long)slot * DK + tile_channel<DK>(mt) + row) * p.DV + tile * DT + col0;
+#pragma unroll
+            for (int c = 0; c < 64; c += 8)   // (the workspace is 256-byte aligned)
+                store32(dst + c, {f2u(X[c]), f2u(X[c + 1]), f2u(X[c + 2]), f2u(X[c + 3]), f2u(X[c + 4]), f2u(X[c + 5]), f2u(X[c + 6]),
+                                  f2u(X[c + 7])});
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 17) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, Lay::kCols);
     }
