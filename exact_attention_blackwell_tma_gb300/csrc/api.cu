@@ -660,8 +660,7 @@ int check_stride(const char* what, long long stride, long long least) {
 struct Kv4Workspace {
     size_t ml, part, scores, total;
 };
-Kv4Workspace kv4_layout(int B, int H, int Hkv, long total, int width, int d, int dv, bool weights) {
-    const int nr = kv4_row_tiles(H / Hkv, B, (int)total);
+Kv4Workspace kv4_layout(int nr, int H, long total, int width, int dv, bool weights) {   // nr: tiles of 8 rows of a block
     Kv4Workspace w{};
     w.ml = align256(kv4_prefix_bytes());
     w.part = w.ml + align256(kv4_ml_bytes(nr));
@@ -715,7 +714,7 @@ extern "C" size_t attn_kv4_fwd_workspace_size(int B, int H, int Hkv, int L, int 
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || table_width < 1 || d <= 0 || d_v <= 0) return 0;
     const long total = packed ? (long)L : (long)B * L;
     if (total >= (1L << 30)) return 0;
-    return kv4_layout(B, H, Hkv, total, table_width, d, d_v, key_weights != 0).total;
+    return kv4_layout(kv4_row_tiles(H / Hkv, B, (int)total), H, total, table_width, d_v, key_weights != 0).total;
 }
 
 extern "C" int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_cache* cache, const int* page_table,
@@ -742,7 +741,7 @@ extern "C" int attn_kv4_fwd(const void* q, long long q_stride, const attn_kv4_ca
     if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(key_weights))
         return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
     if ((rc = check_stride("q", q_stride, (long long)H * p.c.d))) return rc;
-    const Kv4Workspace wl = kv4_layout(B, H, p.c.Hkv, p.s.total, table_width, p.c.d, p.c.dv, key_weights != nullptr);
+    const Kv4Workspace wl = kv4_layout(nr, H, p.s.total, table_width, p.c.dv, key_weights != nullptr);
     if (!workspace || ws_bytes < wl.total)
         return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total, ws_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -1078,7 +1077,7 @@ extern "C" size_t attn_paged_fwd_workspace_size(int B, int H, int Hkv, int L, in
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d <= 0 || d_v <= 0) return 0;
     const long total = packed ? (long)L : (long)B * L;
     if (total >= (1L << 30)) return 0;
-    return kv4_layout(B, H, Hkv, total, 1, d, d_v, false).total;
+    return kv4_layout(paged_row_tiles(H / Hkv, B, (int)total), H, total, 1, d_v, false).total;
 }
 
 extern "C" int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* cache, const int* page_table,
@@ -1093,7 +1092,7 @@ extern "C" int attn_paged_fwd(const void* q, long long q_stride, const attn_page
     if ((rc = check_window(window_left, window_right, sinks))) return rc;
     if (B == 0 || p.s.total == 0) return ok();
     const int group = H / p.c.Hkv;
-    const int nr = kv4_row_tiles(group, B, p.s.total);
+    const int nr = paged_row_tiles(group, B, p.s.total);
     // the work list counts pages of row blocks in an int
     const double units = ((double)p.s.total * group / (8 * nr) + B) * table_width * p.c.Hkv;
     if ((double)p.s.total * H >= 2.0e9) return fail(ATTN_ERR_ARG, "too many rows");
@@ -1102,7 +1101,7 @@ extern "C" int attn_paged_fwd(const void* q, long long q_stride, const attn_page
     if (!aligned16(q) || !aligned16(o) || !aligned16(lse))
         return fail(ATTN_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
     if ((rc = check_stride("q", q_stride, (long long)H * p.c.d))) return rc;
-    const Kv4Workspace wl = kv4_layout(B, H, p.c.Hkv, p.s.total, 1, p.c.d, p.c.dv, false);
+    const Kv4Workspace wl = kv4_layout(nr, H, p.s.total, 1, p.c.dv, false);
     if (!workspace || ws_bytes < wl.total)
         return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total, ws_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

@@ -17,8 +17,10 @@
 // conversions, which have a fraction of the rate. K's 2^120 goes into q and the score; V's
 // is one multiplication per pair, as p 2^(e - 120) could leave the range.
 //
-// Work: paged_work.cuh. Each of four warps takes 32 of a unit's 128 tokens in steps of
-// kTok, with statistics and a ring of asynchronous copies of its own.
+// Work: paged_work.cuh. Each of four warps loads 32 of a unit's 128 tokens in steps of
+// kTok, through a ring of asynchronous copies of its own. A block of up to 8 NR rows is every warp's,
+// for its own tokens, with statistics of its own; in a larger one (16 to 32 rows) the two warps of a page
+// take half of the rows each, for the tokens of both, so that the cache is read once for twice the rows.
 #include <type_traits>
 
 #include "paged.h"
@@ -108,19 +110,19 @@ __device__ __forceinline__ uint32_t row_piece(uint32_t base, int tok, int piece)
 
 template <bool kCodes, int D, int DV, int NR>
 struct PagedLayout {
-    static constexpr int kRows = 8 * NR, kElt = kCodes ? 1 : 2;
+    static constexpr int kGroups = NR == 1 ? 1 : 2, kWarpRows = 8 * NR, kRows = kWarpRows * kGroups, kElt = kCodes ? 1 : 2;
     static constexpr int kKRow = D * kElt, kVRow = DV * kElt;
     // a slot: kTok tokens, about 8 KB, so that a warp's copies in flight cover the latency
     static constexpr int kTok = 32 * (kKRow + kVRow) <= 8192 ? 32 : 16, kSteps = 32 / kTok;   // steps per unit
     static constexpr int kVOff = kTok * kKRow, kKsOff = kVOff + kTok * kVRow, kVsOff = kKsOff + kTok;
     static constexpr int kSlot = kVOff + kTok * kVRow + (kCodes ? 128 : 0);   // (scales padded to a line)
     static constexpr int kSlots = 3;
-    static constexpr int kQOff = kWarps * kSlots * kSlot;          // q fragments [NR][D / 32][32 lanes] x 16 bytes
-    static constexpr int kQExpOff = kQOff + NR * (D / 32) * 512;   // row exponents of q
+    static constexpr int kQOff = kWarps * kSlots * kSlot;          // q fragments [kGroups NR][D / 32][32 lanes] x 16 bytes
+    static constexpr int kQExpOff = kQOff + kGroups * NR * (D / 32) * 512;   // row exponents of q
     static constexpr int kKeysOff = kQExpOff + kRows * 4;
     static constexpr int kMlOff = kKeysOff + kRows * 8;
-    static constexpr int kPrefixOff = (kMlOff + kWarps * kRows * 8 + 15) / 16 * 16;
-    static_assert(kRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
+    static constexpr int kPrefixOff = (kMlOff + kWarps * kWarpRows * 8 + 15) / 16 * 16;
+    static_assert(kWarpRows * DV * 4 <= kSlots * kSlot, "O rows of a warp");
     static constexpr int smem(int B) { return kPrefixOff + (2 * B + 1) * 4; }
     static constexpr int kRegCtas = NR * DV <= 128 ? 4 : (NR * DV <= 256 ? 3 : 2);
     static constexpr int kSmemCtas = 227 * 1024 / (smem(64) + 1024);
@@ -131,7 +133,7 @@ struct PagedLayout {
 template <bool kCodes, int D, int DV, int NR>
 __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>::kCtas) paged_fwd_kernel(const PagedFwdParams p) {
     using Lay = PagedLayout<kCodes, D, DV, NR>;
-    constexpr int S = Lay::kSlots, kRows = Lay::kRows, kTok = Lay::kTok, CK = kTok / 16, kSteps = Lay::kSteps;
+    constexpr int S = Lay::kSlots, kRows = Lay::kRows, kWarpRows = Lay::kWarpRows, kTok = Lay::kTok, CK = kTok / 16, kSteps = Lay::kSteps;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -217,6 +219,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
 #pragma unroll
         for (int x = 0; x < S - 1; ++x) issue(x);
         // ------------------------------------------------ its queries
+        const int n_rows = min(kRows, w.rows - t.rb * kRows);
+        const bool pairs = Lay::kGroups > 1 && n_rows > kWarpRows;   // rows by the warps of a page
+        const int row0 = pairs ? (warp & 1) * kWarpRows : 0;         // this warp's first row of the block
+        const int row_end = min(n_rows, row0 + kWarpRows);
+        auto sync_page = [&] {   // the warps that read each other's slots
+            if (pairs) asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+            else __syncwarp();
+        };
         const MaskBand mb = mask_band(w.s.nq, w.s.lk, p.win_left, p.win_right, p.sinks);
         if (tid < kRows) {
             const int row = t.rb * kRows + tid, i = row / p.group;
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
             }
             __syncthreads();
         }
-        for (int task = warp; task < NR * (D / 32); task += kWarps) {   // 8 rows x 32 channels
+        for (int task = warp; task < (pairs ? Lay::kGroups : 1) * NR * (D / 32); task += kWarps) {   // 8 rows x 32 channels
             const int n = task / (D / 32), kk = task % (D / 32), r = n * 8 + g8;
             const __nv_bfloat16* src = q_row(r);
             uint32_t f[4] = {0u, 0u, 0u, 0u};
@@ -268,16 +278,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
         for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                qscale[n][c] = kCodes ? p.scale_log2 * pow2(120 - q_exp[n * 8 + 2 * t4 + c]) : p.scale_log2;
+                qscale[n][c] = kCodes ? p.scale_log2 * pow2(120 - q_exp[row0 + n * 8 + 2 * t4 + c]) : p.scale_log2;
                 m_run[n][c] = -INFINITY;
                 mu[n][c] = l_run[n][c] = 0.f;
             }
-        // keys that the block's first and last rows (hence all) see
-        const int full_lo = band_key_lo(mb, (min(w.rows, t.rb * kRows + kRows) - 1) / p.group);
-        const int full_hi = band_key_hi(mb, t.rb * kRows / p.group);
+        // keys that this warp's first and last rows (hence all) see
+        const int q_first = (t.rb * kRows + row0) / p.group, q_last = (t.rb * kRows + row_end - 1) / p.group;
+        const int full_lo = band_key_lo(mb, q_last), full_hi = band_key_hi(mb, q_first);
         // ... and that some row sees, sinks aside
-        const int some_lo = band_key_lo(mb, t.rb * kRows / p.group);
-        const int some_hi = band_key_hi(mb, (min(w.rows, t.rb * kRows + kRows) - 1) / p.group);
+        const int some_lo = band_key_lo(mb, q_first), some_hi = band_key_hi(mb, q_last);
 #pragma unroll
         for (int j = 0; j < DV / 16; ++j)
 #pragma unroll
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
 #pragma unroll
                 for (int x = 0; x < 4; ++x) acc[j][n][x] = 0.f;
         __syncthreads();   // the q fragments are in place
-        const uint32_t qfrag = base + Lay::kQOff + lane * 16;
+        const uint32_t qfrag = base + Lay::kQOff + row0 / 8 * (D / 32) * 512 + lane * 16;
 
         // kTok keys from slot `st`, the first key0. kWhole: every row sees all of them.
         bool force = true;   // some row has yet to see its first key
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int2 k = row_keys[n * 8 + 2 * t4 + c];
+                        const int2 k = row_keys[row0 + n * 8 + 2 * t4 + c];
 #pragma unroll
                         for (int x = 0; x < 2 * CK; ++x) {
                             const int j = key0 + tok0 + 8 * x;
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                             sc[ck][n][c] += mu[n][c] - mu_new;
                             sc[ck][n][2 + c] += mu[n][c] - mu_new;
                         }
-                        unset |= m_new == -INFINITY && row_keys[n * 8 + 2 * t4 + c].y > 0;
+                        unset |= m_new == -INFINITY && row_keys[row0 + n * 8 + 2 * t4 + c].y > 0;
                         m_run[n][c] = m_new;
                         mu[n][c] = mu_new;
                         l_run[n][c] *= al[c];
@@ -477,23 +486,28 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
         const int steps = (i1 - i0) * kSteps;
         for (int n = 0; n < steps; ++n) {
             copy_wait<S - 2>();
-            __syncwarp();   // the slot is full, and every lane has read the one before
+            sync_page();   // the slot is full, and whoever reads it has read the one before
             issue(n + S - 1);
             const int x = n / kSteps, i = i0 + x;
             const bool valid = (live >> (x & 31)) & 1u;
-            const uint32_t st = ring + slot_out;
+            const uint32_t slot = slot_out;
             slot_out = slot_out == (S - 1) * Lay::kSlot ? 0 : slot_out + Lay::kSlot;
-            const int key0 = page_of(w, 2 * i + (warp >> 1)) * kPage + 32 * half + n % kSteps * kTok;
-            if (valid && key0 < w.s.lk) {
-                if (key0 >= full_lo && key0 + kTok <= full_hi) step(std::true_type{}, st, key0);
-                else step(std::false_type{}, st, key0);
+            const int page0 = page_of(w, 2 * i + (warp >> 1)) * kPage + n % kSteps * kTok;
+#pragma unroll 1
+            for (int x0 = pairs ? 0 : half, x1 = pairs ? 2 : half + 1; x0 < x1; ++x0) {   // (half a page each)
+                const uint32_t st = base + ((warp & 2) + x0) * S * Lay::kSlot + slot;
+                const int key0 = page0 + 32 * x0;
+                if (valid && key0 < w.s.lk) {
+                    if (key0 >= full_lo && key0 + kTok <= full_hi) step(std::true_type{}, st, key0);
+                    else step(std::false_type{}, st, key0);
+                }
             }
         }
         // ------------------------------------------------ the four warps' rows become one
         // (every copy into the slots has landed and been read: each warp's O rows go there)
         const bool ends = i1 == w.units, starts = i0 == 0;
         copy_wait<0>();
-        __syncwarp();
+        sync_page();
         float* mine = reinterpret_cast<float*>(smem + warp * S * Lay::kSlot);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -504,7 +518,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                 l += __shfl_xor_sync(kFullMask, l, 8);
                 l += __shfl_xor_sync(kFullMask, l, 16);
                 const int row = n * 8 + 2 * t4 + c;
-                if (g8 == 0) ml[warp * kRows + row] = make_float2(m_run[n][c], l);
+                if (g8 == 0) ml[warp * kWarpRows + row] = make_float2(m_run[n][c], l);
                 if constexpr (kCodes) {
 #pragma unroll
                     for (int x = 0; x < DV / 32; ++x)
@@ -520,14 +534,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
             }
         __syncthreads();
         const int part = 2 * blockIdx.x + (starts ? 1 : 0);
-        const int n_rows = min(kRows, w.rows - t.rb * kRows);
         for (int x = tid; x < n_rows * (DV / 4); x += kPagedThreads) {
-            const int row = x / (DV / 4), c4 = x % (DV / 4);
+            const int row = x / (DV / 4), c4 = x % (DV / 4), at = pairs ? row % kWarpRows : row;
             float2 v[kWarps];
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int y = 0; y < kWarps; ++y) {
-                v[y] = ml[y * kRows + row];
+            for (int y = 0; y < kWarps; ++y) {   // (a warp without this row has no share)
+                v[y] = pairs && (y & 1) != row / kWarpRows ? make_float2(-INFINITY, 0.f) : ml[y * kWarpRows + at];
                 m = fmaxf(m, v[y].x);
             }
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -536,7 +549,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                 const float f = v[y].x == -INFINITY ? 0.f : ex2_mufu(v[y].x - m);
                 l += v[y].y * f;
                 if (f != 0.f) {
-                    const float4 z = *reinterpret_cast<const float4*>(smem + y * S * Lay::kSlot + (row * DV + 4 * c4) * 4);
+                    const float4 z = *reinterpret_cast<const float4*>(smem + y * S * Lay::kSlot + (at * DV + 4 * c4) * 4);
                     o.x = fmaf(f, z.x, o.x);
                     o.y = fmaf(f, z.y, o.y);
                     o.z = fmaf(f, z.z, o.z);
@@ -589,8 +602,8 @@ cudaError_t launch_one(const PagedFwdParams& p, int num_sms, cudaStream_t stream
 
 template <bool kCodes, int D, int DV>
 cudaError_t launch_dims(const PagedFwdParams& p, int num_sms, cudaStream_t stream) {
-    return kv4_row_tiles(p.group, p.s.B, p.s.total) == 1 ? launch_one<kCodes, D, DV, 1>(p, num_sms, stream)
-                                                         : launch_one<kCodes, D, DV, 2>(p, num_sms, stream);
+    return paged_row_tiles(p.group, p.s.B, p.s.total) == 1 ? launch_one<kCodes, D, DV, 1>(p, num_sms, stream)
+                                                           : launch_one<kCodes, D, DV, 2>(p, num_sms, stream);
 }
 template <bool kCodes>
 cudaError_t launch_form(const PagedFwdParams& p, int num_sms, cudaStream_t stream) {
