@@ -1,6 +1,6 @@
 // The paged cache in bf16 or 8 bits: append (quantise) and read. Bound by memory:
 // each value is touched once. A warp takes a few consecutive tokens, whose places
-// its first lanes look up together, and walks their heads, kAhead of them with
+// its first lanes look up together. An append walks their heads, kAhead of them with
 // their loads in flight; a lane holds d / 32 neighbouring channels of a head.
 #include <type_traits>
 
@@ -43,19 +43,6 @@ __device__ __forceinline__ void store_words(void* p, const Words<W>& r) {
     }
 }
 // W pairs of codes, 2 W bytes
-template <int W>
-__device__ __forceinline__ void load_codes(const unsigned char* p, uint16_t (&c)[W]) {
-    if constexpr (W == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        c[0] = v.x & 0xffff, c[1] = v.x >> 16, c[2] = v.y & 0xffff, c[3] = v.y >> 16;
-    } else if constexpr (W == 2) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p));
-        c[0] = v & 0xffff, c[1] = v >> 16;
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) c[i] = __ldg(reinterpret_cast<const uint16_t*>(p) + i);
-    }
-}
 template <int W>
 __device__ __forceinline__ void store_codes(unsigned char* p, const uint16_t (&c)[W]) {
     if constexpr (W == 4)
@@ -117,40 +104,46 @@ __device__ __forceinline__ void append_row(const __nv_bfloat16* src, unsigned ch
         }
     }
 }
-template <bool kCodes, int D>
-__device__ __forceinline__ void read_row(__nv_bfloat16* dst, const unsigned char* rows, const unsigned char* scales, int Hkv,
-                                         long page, int slot, int lane) {
-    constexpr int W = D / 64;
-    for (int h0 = 0; h0 < Hkv; h0 += kAhead) {
-        Words<W> r[kAhead];
-        uint16_t c[kAhead][W];
-        uint32_t e[kAhead];
+// One token's K and V rows, all heads, in pieces of eight channels (16 bytes of output): a lane's pieces
+// lie 32 apart, kPieces of them with their loads in flight (two: 112 us; four 119, eight 135, see tokens_per_warp).
+template <bool kCodes, int D, int DV>
+__device__ __forceinline__ void read_token(__nv_bfloat16* k, __nv_bfloat16* v, const PagedCache& c, long page, int slot, int lane) {
+    constexpr int PK = D / 8, PV = DV / 8, kPieces = 2;
+    const int of_k = c.Hkv * PK, all = of_k + c.Hkv * PV;
+    for (int p0 = lane; p0 < all; p0 += 32 * kPieces) {
+        uint4 x[kPieces];
+        uint32_t e[kPieces];
 #pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            const long at = (max(page, 0l) * Hkv + min(h0 + y, Hkv - 1)) * kPage + slot;
+        for (int y = 0; y < kPieces; ++y) {
+            const int p = min(p0 + 32 * y, all - 1), q = p < of_k ? p : p - of_k, h = p < of_k ? q / PK : q / PV;
+            const long row = (max(page, 0l) * c.Hkv + h) * kPage + slot;
+            const long at = p < of_k ? row * D + (q - h * PK) * 8 : row * DV + (q - h * PV) * 8;   // channels
+            const unsigned char* src = p < of_k ? c.k : c.v;
             if constexpr (kCodes) {
-                load_codes<W>(rows + at * D + lane * 2 * W, c[y]);
-                e[y] = __ldg(scales + at);
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + at));
+                x[y].x = w.x, x[y].y = w.y;
+                e[y] = __ldg((p < of_k ? c.k_scales : c.v_scales) + row);
             } else {
-                r[y] = load_words<W>(rows + (at * D + lane * 2 * W) * 2);
+                x[y] = __ldg(reinterpret_cast<const uint4*>(src + 2 * at));
             }
         }
 #pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            if (h0 + y >= Hkv) break;
+        for (int y = 0; y < kPieces; ++y) {
+            const int p = p0 + 32 * y;
+            if (p >= all) break;
             if constexpr (kCodes) {
                 const float f = __uint_as_float(e[y] << 23);   // (255: infinity, times codes of 0: NaN)
+                const uint32_t w[2] = {x[y].x, x[y].y};
+                uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const float2 x = e4m3_values(c[y][i]);
-                    r[y].x[i] = pack_bf16x2(x.x * f, x.y * f);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 z = e4m3_values((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+                    o[i] = pack_bf16x2(z.x * f, z.y * f);
                 }
+                x[y] = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (page < 0) {   // (a row that lies nowhere reads as zero)
-#pragma unroll
-                for (int i = 0; i < W; ++i) r[y].x[i] = 0u;
-            }
-            store_words<W>(dst + (long)(h0 + y) * D + lane * 2 * W, r[y]);
+            if (page < 0) x[y] = make_uint4(0, 0, 0, 0);   // (a row that lies nowhere reads as zero)
+            *reinterpret_cast<uint4*>(p < of_k ? k + p * 8 : v + (p - of_k) * 8) = x[y];
         }
     }
 }
@@ -184,15 +177,16 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(PagedCache c,
     for (int x = 0; x < rows; ++x) {
         const int page = __shfl_sync(0xffffffffu, mine.page, x), slot = __shfl_sync(0xffffffffu, mine.slot, x);
         if (page == -2) continue;
-        read_row<kCodes, D>(k + (long)(t0 + x) * c.Hkv * D, c.k, c.k_scales, c.Hkv, page, slot, lane);
-        read_row<kCodes, DV>(v + (long)(t0 + x) * c.Hkv * DV, c.v, c.v_scales, c.Hkv, page, slot, lane);
+        read_token<kCodes, D, DV>(k + (long)(t0 + x) * c.Hkv * D, v + (long)(t0 + x) * c.Hkv * DV, c, page, slot, lane);
     }
 }
 
-// Tokens per warp: up to four, as long as that leaves 48 warps per SM
+// Tokens per warp: two where that leaves 48 warps per SM (a chunked prefill of 12000 tokens and the 70000 of its prefix
+// read back, 8 heads, 8 bits: 112 us; 119 with four, 153 with all in one wave: neighbouring tokens of a page should be
+// read together)
 int tokens_per_warp(int total, int num_sms) {
     const int rows = total / (num_sms * 48);
-    return rows < 1 ? 1 : (rows > 4 ? 4 : rows);
+    return rows < 1 ? 1 : (rows > 2 ? 2 : rows);
 }
 
 // call(D, DV) for the head dims of a cache
