@@ -206,6 +206,96 @@ def test_many_segments(packed, d, dv, H, Hkv):
 
 
 @gpu
+@pytest.mark.parametrize("n", [127, 128, 129, 191, 192, 257])
+def test_lengths_around_a_chunk(n):
+    Problem([n], 3, 1, 128, 128, seed=n).check()
+    Problem([n, n], 2, 2, 128, 128, packed=False, states=False, seed=n).check()
+
+
+@gpu
+@pytest.mark.parametrize("d,dv,H,Hkv", [(64, 64, 6, 3), (128, 128, 2, 2), (192, 128, 3, 3)])
+def test_more_runs_than_thread_blocks(d, dv, H, Hkv):
+    """Ranges of units that span many short sequences and heads, empty sequences among them."""
+    g = torch.Generator().manual_seed(d)
+    lens = torch.randint(0, 41, (70,), generator=g).tolist() + [700] + [0, 0] + torch.randint(0, 300, (9,), generator=g).tolist()
+    Problem(lens, H, Hkv, d, dv, seed=d).check()
+
+
+@gpu
+@pytest.mark.parametrize("packed", [True, False])
+def test_runs_that_several_ranges_cut(packed):
+    lens = [3000, 5, 0, 5200] if packed else [4100, 4100]
+    Problem(lens, 2, 2, 128, 128, packed=packed, seed=3, states=packed).check()
+
+
+@gpu
+def test_offsets_that_change_between_replays():
+    """A captured call reads the offsets when it runs; its segments follow them."""
+    p = Problem([700, 41, 300, 1], 4, 2, 64, 64, seed=18)
+    for _ in range(2):
+        p.forward(final_state=True), p.backward()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, final = p.forward(final_state=True)
+        grads = p.backward()
+    for lens in ([700, 41, 300, 1], [0, 1, 2, 1039], [260, 261, 260, 261], [1042, 0, 0, 0]):
+        p.lens = lens
+        p.cu.copy_(torch.tensor([sum(lens[:b]) for b in range(5)], dtype=torch.int32))
+        graph.replay()
+        binding.check_status()
+        p.check_forward(o, final, f"{lens}")
+        p.check_backward(*grads, f"{lens}")
+
+
+@gpu
+@pytest.mark.parametrize("n", [90, 900])
+def test_states_in_place(n):
+    """The final state in state's buffer, and its gradient in dfinal's or in state's."""
+    p = Problem([n, 33], 4, 2, 128, 128, seed=19)
+    o, final = p.forward(final_state=True)
+    *_, want = p.backward()
+    state = p.state.clone()
+    o2, same = binding.linear_forward(p.q, p.k, p.v, p.log_decay, cu_seqlens=p.cu, state=state, final_state=state)
+    assert torch.equal(o, o2) and torch.equal(final, same)
+    ws = torch.empty(binding.attn_linear_workspace_size(2, 4, 2, n + 33, True, 128, 128), dtype=torch.uint8, device="cuda")
+    for where in ("dfinal", "state"):
+        state, dfinal = p.state.clone(), p.dstate.clone()
+        into = dfinal if where == "dfinal" else state
+        dq, dk, dv = torch.empty_like(p.q), torch.empty_like(p.k), torch.empty_like(p.v)
+        rc = binding.attn_linear_bwd(p.q, p.k, p.v, p.do, 512, 256, 256, 512, p.log_decay, state, dfinal, dq, dk, dv, into, 2, 4, 2,
+                                     n + 33, 128, 128, p.scale, p.cu, ws, ws.numel())
+        assert rc == binding.ATTN_OK
+        binding.check_status()
+        p.check_backward(dq, dk, dv, into, where)
+        assert torch.equal(into, want)
+
+
+@gpu
+def test_outputs_at_any_16_byte_boundary():
+    """Outputs that start 16 bytes into an allocation, next to bytes that stay as they are."""
+    p = Problem([200], 2, 2, 128, 128, seed=20)
+    flat = torch.full((200 * 2 * 128 + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:-8].view(200, 2, 128)
+    o, _ = p.forward(out=out)
+    assert o.data_ptr() == out.data_ptr() and torch.equal(o, p.forward()[0])
+    assert (flat[:8] == 7).all() and (flat[-8:] == 7).all()
+
+
+@gpu
+def test_two_calls_at_once():
+    """Calls on two streams at the same time, each with a workspace of its own."""
+    a, b = Problem([3000, 700], 4, 2, 128, 128, seed=21), Problem([2500], 4, 4, 64, 64, seed=22)
+    want = [[*x.forward(final_state=True), *x.backward()] for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [[*x.forward(final_state=True, stream=s), *x.backward(stream=s)] for x, s in zip((a, b), streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for g, w in zip(got, want) for x, y in zip(g, w))
+    binding.check_status()
+
+
+@gpu
 @pytest.mark.parametrize("packed", [True, False])
 def test_decays(packed):
     """None at all, slow, fast, far below the smallest float, only the current token; above 1 counts as none."""

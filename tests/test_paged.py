@@ -279,6 +279,16 @@ def test_forward_many_rows(bits, d, n, H, Hkv):
 
 @gpu
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_forward_row_blocks(bits, d):
+    """Numbers of rows around those that a warp, and a thread block, holds at once."""
+    new = [7, 8, 9, 15, 16, 17, 24, 31, 32, 33, 48, 63, 64, 65]
+    check_forward(Pool(bits, [n + 100 + 13 * n for n in new], 1, d, seed=16), new, 1, window=(90, -1), sinks=3)
+    check_forward(Pool(bits, [150] * 9, 1, d, seed=17), [1, 2, 3, 4, 5, 6, 7, 8, 9], 4)
+
+
+@gpu
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("L", [1, 4])
 def test_forward_dense_batch(bits, L):
     check_forward(Pool(bits, [100, 250, 64, 4], 2, 128, seed=11), [L] * 4, 8, packed=False)
