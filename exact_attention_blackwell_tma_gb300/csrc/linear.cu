@@ -23,6 +23,8 @@ constexpr int kScanThreads = 128;
 template <bool kBack>
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinParams p) {
     __shared__ int s_before, s_all;
+    launch_next();
+    wait_for_last();
     const int size = p.DK * p.DV, blocks = size / (4 * kScanThreads);
     const int run = blockIdx.x / blocks, b = run / p.Hkv, h = run - b * p.Hkv;
     const int x = ((blockIdx.x - run * blocks) * kScanThreads + threadIdx.x) * 4;
@@ -182,9 +184,7 @@ cudaError_t launch_linear_states(const LinParams& p, const LinMaps& maps, bool b
         if (e != cudaSuccess) return e;
     }
     const unsigned blocks = (unsigned)((long)p.DK * p.DV / (4 * kScanThreads) * p.B * p.Hkv);
-    if (back) lin_scan_kernel<true><<<blocks, kScanThreads, 0, stream>>>(p);
-    else lin_scan_kernel<false><<<blocks, kScanThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(back ? lin_scan_kernel<true> : lin_scan_kernel<false>, blocks, kScanThreads, 0, stream, p);
 }
 
 cudaError_t launch_linear_step(const LinStepParams& p, cudaStream_t stream) {

@@ -238,6 +238,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
         return;
     }
+    launch_next();
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
@@ -267,6 +268,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    wait_for_last();
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
     const int per = p.per;
     const int nt = p.DV / DT, range = blockIdx.x / nt, tile = blockIdx.x - range * nt;
@@ -760,6 +762,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
         return;
     }
+    launch_next();
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
@@ -786,6 +789,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    wait_for_last();
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
     const int nt = p.DV / DT, range = blockIdx.x / nt, tile = blockIdx.x - range * nt;
     Walk at;
@@ -968,8 +972,7 @@ cudaError_t launch_tc(Kernel kern, int threads, int bytes, int tiles, std::atomi
                       const LinParams& p, const LinMaps& maps, cudaStream_t stream) {
     cudaError_t e = allow_smem(kern, bytes, allowed);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(p.ranges * tiles), threads, bytes, stream>>>(maps, p);
-    return cudaGetLastError();
+    return launch_early(kern, (unsigned)(p.ranges * tiles), threads, bytes, stream, maps, p);
 }
 // The registers that the roles share out must be those of the launch (asked once per kernel and device set)
 template <class Kernel>

@@ -549,7 +549,7 @@ def test_refuses_sizes_and_workspaces(built):
     need = binding.attn_linear_workspace_size(1, 2, 2, 4096, False, 64, 64)
     assert need > 0
     assert _codes(L=4096)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
-    assert _codes(L=4096, ws=4096, n=need - 1)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
+    assert _codes(L=4096, F=4096, ws=4096, n=need - 1)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
     assert _codes(L=4096, ws=4112, n=need)[:2] == (binding.ATTN_ERR_ALIGN,) * 2
     assert _codes(B=0) == (binding.ATTN_OK,) * 3
     assert binding.attn_linear_workspace_size(1, 3, 2, 4096, False, 64, 64) == 0
