@@ -115,7 +115,7 @@ def _declare(lib):
     lib.attn_paged_fwd.argtypes = ([c_void_p, i64, paged, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p]
                                    + [c_int] * 3 + [c_float] + [c_int] * 4 + [c_void_p, c_size_t, c_void_p])
     lib.attn_linear_workspace_size.restype = c_size_t
-    lib.attn_linear_workspace_size.argtypes = [c_int] * 7
+    lib.attn_linear_workspace_size.argtypes = [c_int] * 8
     lib.attn_linear_fwd.restype = c_int
     lib.attn_linear_fwd.argtypes = ([c_void_p] * 3 + [i64] * 3 + [c_void_p] * 4 + [c_int] * 6
                                     + [c_float, c_void_p, c_void_p, c_size_t, c_void_p])
@@ -184,6 +184,15 @@ def _ptr(t):
 
 # The current stream's handle without building the Stream object (3 us); torch does not promise this name
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# The current device's index without the check that CUDA is initialised, which it is where a CUDA tensor has been seen
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_on(stream, device):
+    """_stream() for a call on the current device, whose index the caller has."""
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _stream(stream):
@@ -366,8 +375,8 @@ def attn_paged_fwd(q, q_stride, cache, page_table, table_width, cache_lens, cu_s
                                  int(window_right), int(sinks), _ptr(workspace), ws_bytes, _stream(stream))
 
 
-def attn_linear_workspace_size(B, H, Hkv, L, packed, d, d_v) -> int:
-    return load().attn_linear_workspace_size(B, H, Hkv, L, int(packed), d, d_v)
+def attn_linear_workspace_size(B, H, Hkv, L, packed, d, d_v, final_state) -> int:
+    return load().attn_linear_workspace_size(B, H, Hkv, L, int(packed), d, d_v, int(final_state))
 
 
 def attn_linear_fwd(q, k, v, q_stride, k_stride, v_stride, log_decay, state, o, final_state, B, H, Hkv, L, d, d_v, scale,
@@ -619,7 +628,7 @@ def _kv4_int(name, t, dims, rows, device):
 def _kv4_ints(cache, page_table, cache_lens, cu_seqlens, new_table=None):
     """Checks the int32 tensors of a call, which live on the cache's device, the current one; returns (B, device index)."""
     device = cache.device
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         raise ValueError(f"the cache is on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
     B = len(cache_lens)
     _kv4_int("cache_lens", cache_lens, 1, B, device)
@@ -667,11 +676,16 @@ def _kv4_out(t, shape, dtype, device, name):
 _kv4_workspace = functools.lru_cache(maxsize=4096)(attn_kv4_fwd_workspace_size)   # a function of the sizes alone
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocations inside belong to the stream that the call runs on."""
+    if stream is None:
+        return _HERE
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def kv4_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=None):
@@ -812,19 +826,19 @@ def paged_append(cache, k, v, page_table, cache_lens, cu_seqlens=None, stream=No
     if L != Lv:
         raise ValueError(f"k has {L} rows, v {Lv}")
     _check(load().attn_paged_append(k.data_ptr(), v.data_ptr(), k_stride, v_stride, cache._struct, page_table.data_ptr(),
-                                    page_table.shape[1], cache_lens.data_ptr(), _ptr(cu_seqlens), B, L, _stream(stream)))
+                                    page_table.shape[1], cache_lens.data_ptr(), _ptr(cu_seqlens), B, L, _stream_on(stream, device)))
 
 
 def paged_read(cache, page_table, cache_lens, rows, cu_seqlens=None, k=None, v=None, stream=None):
     """K, V in bf16 as the cache stands for them: the last rows of every sequence, as kv4_read() gives them."""
-    B, _ = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
+    B, index = _kv4_ints(cache, page_table, cache_lens, cu_seqlens)
     device, heads = cache.k.device, cache.Hkv
     packed = cu_seqlens is not None
     with _on(stream):
         k = _kv4_out(k, (rows, heads, cache.d) if packed else (B, rows, heads, cache.d), torch.bfloat16, device, "k")
         v = _kv4_out(v, (rows, heads, cache.dv) if packed else (B, rows, heads, cache.dv), torch.bfloat16, device, "v")
     _check(load().attn_paged_read(k.data_ptr(), v.data_ptr(), cache._struct, page_table.data_ptr(), page_table.shape[1],
-                                  cache_lens.data_ptr(), _ptr(cu_seqlens), B, rows, _stream(stream)))
+                                  cache_lens.data_ptr(), _ptr(cu_seqlens), B, rows, _stream_on(stream, index)))
     return k, v
 
 
@@ -850,7 +864,7 @@ def paged_forward(q, cache, page_table, cache_lens, causal: bool = True, scale: 
             size = workspace.numel() * workspace.element_size()
     _check(load().attn_paged_fwd(q.data_ptr(), q_stride, cache._struct, page_table.data_ptr(), page_table.shape[1],
                                  cache_lens.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr(), B, H, L, scale,
-                                 int(causal), window[0], window[1], sinks, workspace.data_ptr(), size, _stream(stream)))
+                                 int(causal), window[0], window[1], sinks, workspace.data_ptr(), size, _stream_on(stream, index)))
     return out, lse
 
 
@@ -868,7 +882,7 @@ def _linear_float(name, t, shape, device):
 def _linear_inputs(q, k, v, log_decay, cu_seqlens, *states):
     """Checks what the forward and the backward share: (B, H, Hkv, L, d, dv, strides, device index)."""
     device, packed = q.get_device(), cu_seqlens is not None
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         raise ValueError(f"q is on {q.device}, the current device is cuda:{torch.cuda.current_device()}")
     if q.dim() != (3 if packed else 4) or k.dim() != q.dim() or v.dim() != q.dim():
         raise ValueError(f"q, k and v must be [{'T' if packed else 'B, L'}, heads, channels], got {tuple(q.shape)}, "
@@ -889,12 +903,12 @@ def _linear_inputs(q, k, v, log_decay, cu_seqlens, *states):
     return B, H, Hkv, L, d, dv, (q_stride, k_stride, v_stride), device
 
 
-def _linear_scratch(workspace, B, H, Hkv, L, packed, d, dv, device):
+def _linear_scratch(workspace, B, H, Hkv, L, packed, d, dv, final, device):
     """(workspace or None, bytes) for a call; the caller's is checked."""
     if workspace is not None:
         _check_workspace(workspace, device)
         return workspace, workspace.numel() * workspace.element_size()
-    need = _linear_workspace(B, H, Hkv, L, packed, d, dv)
+    need = _linear_workspace(B, H, Hkv, L, packed, d, dv, final)
     return (torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}") if need else None), need
 
 
@@ -914,10 +928,10 @@ def linear_forward(q, k, v, log_decay, scale: float | None = None, cu_seqlens=No
         out = _kv4_out(out, q.shape[:-1] + (dv,), torch.bfloat16, q.device, "out")
         if final is None and final_state:
             final = torch.empty((B, Hkv, d, dv), dtype=torch.float32, device=q.device)
-        workspace, size = _linear_scratch(workspace, B, H, Hkv, L, packed, d, dv, index)
+        workspace, size = _linear_scratch(workspace, B, H, Hkv, L, packed, d, dv, final is not None, index)
     _check(load().attn_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, log_decay.data_ptr(), _ptr(state),
                                   out.data_ptr(), _ptr(final), B, H, Hkv, L, d, dv, scale, _ptr(cu_seqlens),
-                                  _ptr(workspace), size, _stream(stream)))
+                                  _ptr(workspace), size, _stream_on(stream, index)))
     return out, final
 
 
@@ -937,11 +951,11 @@ def linear_backward(q, k, v, log_decay, dout, scale: float | None = None, cu_seq
         dk = _kv4_out(dk, k.shape, torch.bfloat16, q.device, "dk")
         dv = _kv4_out(dv, v.shape, torch.bfloat16, q.device, "dv")
         first = None if state is None else torch.empty_like(state)
-        workspace, size = _linear_scratch(workspace, B, H, Hkv, L, packed, d, d_v, index)
+        workspace, size = _linear_scratch(workspace, B, H, Hkv, L, packed, d, d_v, first is not None, index)
     _check(load().attn_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), *strides, dout_stride,
                                   log_decay.data_ptr(), _ptr(state), _ptr(dstate), dq.data_ptr(), dk.data_ptr(),
                                   dv.data_ptr(), _ptr(first), B, H, Hkv, L, d, d_v, scale, _ptr(cu_seqlens),
-                                  _ptr(workspace), size, _stream(stream)))
+                                  _ptr(workspace), size, _stream_on(stream, index)))
     return dq, dk, dv, first
 
 
@@ -949,7 +963,7 @@ def linear_step(q, k, v, log_decay, state, scale: float | None = None, out=None,
     """linear_forward of one new token per sequence: q [B, H, d], k [B, Hkv, d], v [B, Hkv, dv] (rows may be strided).
     state (fp32 [B, Hkv, d, dv]) is updated in place; returns O [B, H, dv]."""
     device = q.get_device()
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         raise ValueError(f"q is on {q.device}, the current device is cuda:{torch.cuda.current_device()}")
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError(f"q, k and v must be [B, heads, channels], got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
@@ -966,5 +980,5 @@ def linear_step(q, k, v, log_decay, state, scale: float | None = None, out=None,
         out = _kv4_out(out, (B, H, dv), torch.bfloat16, q.device, "out")
     _check(load().attn_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
                                    log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), B, H, Hkv, d, dv, scale,
-                                   _stream(stream)))
+                                   _stream_on(stream, device)))
     return out

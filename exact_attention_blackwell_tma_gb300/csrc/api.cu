@@ -907,12 +907,10 @@ LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const
 
 }  // namespace
 
-extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v) {
+extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v, int final_state) {
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
     if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
-    const size_t with = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, true), d, d_v);
-    const size_t without = linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, false), d, d_v);
-    return with > without ? with : without;
+    return linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, final_state != 0), d, d_v);
 }
 
 extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,

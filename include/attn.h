@@ -491,16 +491,17 @@ int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* ca
  *             as 0 (no decay), -infinity keeps the current token alone.
  *   states    fp32 [B, Hkv, d, d_v]. state NULL: zeros. final_state NULL: not wanted; it
  *             may be state's buffer.
- * Within 64 tokens the products <q_t, k_s> D^(t-s), and the state before its product
- * with q, are rounded to bf16; sums and states are fp32 to 2^-16. The rows of a
- * sequence's 64-token chunks must be finite: an infinity or NaN in k or v spreads to
- * all rows of its chunk, not only to the later ones.
- * workspace: attn_linear_workspace_size(...) bytes (0: none needed, NULL will do),
- * 256-byte aligned, used by one call at a time; its contents need not be
- * initialised. The calls allocate nothing, use no atomics on data (results repeat bit for
- * bit) and can be captured into a CUDA graph.
+ * Within 128 tokens (a chunk, counted from a sequence's first) the products <q_t, k_s> D^(t-s),
+ * and the state before its product with q, are rounded to bf16; sums and the states that
+ * leave a call are fp32 (1e-6). The rows of a chunk must be finite: an infinity or NaN in k or
+ * v spreads to all rows of its chunk, not only to the later ones.
+ * workspace: attn_linear_workspace_size(...) bytes (0: none needed, NULL will do; final_state != 0:
+ * the call has one, in the backward dstate), 256-byte aligned, used by one call at a time; its
+ * contents need not be initialised. The calls allocate nothing, use no atomics on data (results
+ * repeat bit for bit; whether a final state is asked for may change the last bit of o) and can be
+ * captured into a CUDA graph, which reads the offsets when it runs.
  */
-size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v);
+size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v, int final_state);
 int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride, long long v_stride,
                     const float* log_decay, const float* state, void* o, float* final_state,
                     int B, int H, int Hkv, int L, int d, int d_v, float scale, const int* cu_seqlens,

@@ -201,7 +201,7 @@ def test_dense_lengths(n):
 def test_many_segments(packed, d, dv, H, Hkv):
     """Sequences that several thread blocks walk, a segment each."""
     lens = [1500, 3, 2049] if packed else [1601, 1601]
-    assert binding.attn_linear_workspace_size(len(lens), H, Hkv, sum(lens) if packed else lens[0], packed, d, dv) > 0
+    assert binding.attn_linear_workspace_size(len(lens), H, Hkv, sum(lens) if packed else lens[0], packed, d, dv, False) > 0
     Problem(lens, H, Hkv, d, dv, packed=packed, seed=d + packed).check()
 
 
@@ -257,7 +257,7 @@ def test_states_in_place(n):
     state = p.state.clone()
     o2, same = binding.linear_forward(p.q, p.k, p.v, p.log_decay, cu_seqlens=p.cu, state=state, final_state=state)
     assert torch.equal(o, o2) and torch.equal(final, same)
-    ws = torch.empty(binding.attn_linear_workspace_size(2, 4, 2, n + 33, True, 128, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(binding.attn_linear_workspace_size(2, 4, 2, n + 33, True, 128, 128, True), dtype=torch.uint8, device="cuda")
     for where in ("dfinal", "state"):
         state, dfinal = p.state.clone(), p.dstate.clone()
         into = dfinal if where == "dfinal" else state
@@ -483,7 +483,7 @@ def test_unwanted_outputs_change_nothing():
     assert none is None
     p.check_forward(o, final)   # (each within its bounds: a wanted state is summed in more bits, which o may show in its last)
     p.check_forward(o2, None)
-    ws = torch.empty(binding.attn_linear_workspace_size(2, 2, 2, 577, True, 64, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(binding.attn_linear_workspace_size(2, 2, 2, 577, True, 64, 64, True), dtype=torch.uint8, device="cuda")
     o3, _ = p.forward(workspace=ws.fill_(255))   # whatever the workspace holds
     assert torch.equal(o2, o3)
     o4, final4 = p.forward(final_state=True, workspace=ws.fill_(255))
@@ -546,16 +546,17 @@ def test_refuses_sizes_and_workspaces(built):
     assert _codes(cu=4096, B=0)[:2] == (binding.ATTN_ERR_ARG,) * 2
     assert _codes(q=4104) == (binding.ATTN_ERR_ALIGN,) * 3
     assert _codes(S=4100) == (binding.ATTN_ERR_ALIGN,) * 3
-    need = binding.attn_linear_workspace_size(1, 2, 2, 4096, False, 64, 64)
+    need = binding.attn_linear_workspace_size(1, 2, 2, 4096, False, 64, 64, False)
     assert need > 0
     assert _codes(L=4096)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
-    assert _codes(L=4096, F=4096, ws=4096, n=need - 1)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
+    assert _codes(L=4096, ws=4096, n=need - 1)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
     assert _codes(L=4096, ws=4112, n=need)[:2] == (binding.ATTN_ERR_ALIGN,) * 2
     assert _codes(B=0) == (binding.ATTN_OK,) * 3
-    assert binding.attn_linear_workspace_size(1, 3, 2, 4096, False, 64, 64) == 0
+    assert binding.attn_linear_workspace_size(1, 3, 2, 4096, False, 64, 64, True) == 0
     # one segment: for a final state alone
     assert _codes(L=64, F=4096)[:2] == (binding.ATTN_ERR_WORKSPACE,) * 2
-    assert binding.attn_linear_workspace_size(1, 2, 2, 64, False, 64, 64) == 2 * 64 * 64 * 4
+    assert binding.attn_linear_workspace_size(1, 2, 2, 64, False, 64, 64, True) == 2 * 64 * 64 * 4
+    assert binding.attn_linear_workspace_size(1, 2, 2, 64, False, 64, 64, False) == 0
 
 
 @gpu
