@@ -857,12 +857,13 @@ struct LinTensor {
 };
 LinTensor lin_output(void* x, int heads, int width) { return LinTensor{x, (long long)heads * width, heads, width, 32}; }
 
+int linear_bwd_tiles(int d, int dv) { return lin_tiles(d, dv) > lin_tiles(dv, d) ? lin_tiles(d, dv) : lin_tiles(dv, d); }
 size_t linear_bytes(const LinPlan& plan, int d, int dv) { return (size_t)plan.slots * d * dv * sizeof(float); }
 
 // What the four products of linear attention share; the roles of the tensors come on top.
-int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, const float* log_decay, bool final,
+int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, int tiles, const float* log_decay, bool final,
                   void* workspace, size_t ws_bytes, LinTensor* const* tensors, int n_tensors, LinParams* p) {
-    const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, d, dv, final);
+    const LinPlan plan = lin_plan(B, Hkv, L, cu != nullptr, tiles, final);
     // (runs, units and the scan's blocks are counted in ints)
     const double chunks = cu ? (double)L / kLinChunk + B : (double)B * (L / kLinChunk + 1);
     if (chunks * Hkv >= 1.0e9 || (double)B * Hkv * d * dv / 512 >= 2.0e9)
@@ -910,7 +911,9 @@ LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const
 extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v, int final_state) {
     if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
     if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
-    return linear_bytes(lin_plan(B, Hkv, L, packed != 0, d, d_v, final_state != 0), d, d_v);
+    const LinPlan fwd = lin_plan(B, Hkv, L, packed != 0, lin_tiles(d, d_v), final_state != 0);
+    const LinPlan bwd = lin_plan(B, Hkv, L, packed != 0, linear_bwd_tiles(d, d_v), final_state != 0);
+    return linear_bytes(fwd.slots > bwd.slots ? fwd : bwd, d, d_v);
 }
 
 extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -930,7 +933,8 @@ extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long
     LinTensor tq{q, q_stride, H, d}, tk{k, k_stride, Hkv, d}, tv{v, v_stride, Hkv, d_v}, to = lin_output(o, H, d_v);
     LinTensor* const all[] = {&tq, &tk, &tv, &to};
     LinParams p{};
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, final_state != nullptr, workspace, ws_bytes, all, 4, &p)))
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, lin_tiles(d, d_v), log_decay, final_state != nullptr, workspace,
+                            ws_bytes, all, 4, &p)))
         return rc;
     const LinMaps maps = linear_roles(&p, tq, tk, tv, to);
     p.init = state;
@@ -963,7 +967,8 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
     LinTensor tdq = lin_output(dq, H, d), tdk = lin_output(dk, Hkv, d), tdv = lin_output(dv, Hkv, d_v);
     LinTensor* const all[] = {&tq, &tk, &tv, &tdo, &tdq, &tdk, &tdv};
     LinParams p{};
-    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, log_decay, dstate != nullptr, workspace, ws_bytes, all, 7, &p)))
+    if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, linear_bwd_tiles(d, d_v), log_decay, dstate != nullptr, workspace,
+                            ws_bytes, all, 7, &p)))
         return rc;
     p.out_mul = scale;
     cudaError_t e = cudaSuccess;

@@ -160,9 +160,8 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const LinStepPar
 
 }  // namespace
 
-LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv, bool final) {
+LinPlan lin_plan(int B, int Hkv, int L, bool packed, int tiles, bool final) {
     constexpr int kSms = 152;   // CTAs of a wave on a GB300, one per SM
-    const int tiles = d == 128 && dv == 128 ? 1 : (d > dv ? d : dv) / 64;   // CTAs of a range (the transposed product's count if more)
     const long most = kSms / tiles, runs = (long)B * Hkv, longest = ((long)L + kLinChunk - 1) / kLinChunk;
     const long units = (packed ? (long)L / kLinChunk + B : B * longest) * Hkv;   // (packed: at most)
     // Whole runs or ranges of units, whichever takes less time, counted in chunks of the outputs' kernel (4 us): where

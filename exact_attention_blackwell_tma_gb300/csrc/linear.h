@@ -54,7 +54,9 @@ struct LinPlan {
     int ranges, whole;
     long slots;   // states of the workspace
 };
-LinPlan lin_plan(int B, int Hkv, int L, bool packed, int d, int dv, bool final);   // final: the last states are wanted
+// final: the last states are wanted; tiles: the most CTAs that a range has in any of the call's products
+LinPlan lin_plan(int B, int Hkv, int L, bool packed, int tiles, bool final);
+inline int lin_tiles(int DK, int DV) { return DK == 128 && DV == 128 ? 1 : DV / 64; }
 
 // Tensor maps, boxes of 64 channels of a head: a, b and c by 128 tokens, out by 32
 struct LinMaps {
