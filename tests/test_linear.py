@@ -1,10 +1,11 @@
 """Linear attention with a decay per head against its definition in float64: forward, backward, single tokens.
 
-Bounds. Within chunks of 64 positions (128 where both head dims are 128) the kernels round P_ij = decay^(i-j) <a_i, b_j>
-and the state X that is carried in to bf16 (U = 2^-8 of each, half a step) before their products; what a chunk adds to X on
-the way to the next ones takes its weighted operand in bf16 (U of every term w_j b_j c_j, however they cancel). The output is
-rounded once. The states that leave a call take that operand in 24 bits. Sums are fp32: F = 2^-15 of the sums of absolute
-values covers them (256 products of 2^-24 each in a score, 2^-24 per chunk added to a state, over fewer than 100).
+Bounds. Within chunks of 128 positions the kernels round P_ij = decay^(i-j) <a_i, b_j> and the state X that is
+carried in to bf16 (U = 2^-8 of each, half a step) before their products; the output is rounded once. Sums are
+fp32, and what a chunk adds to X on the way to the next ones takes its weighted operand in 16 bits (24 in the states that
+leave a call): F = 2^-15 of the sums of absolute values covers both (256 products of 2^-24 each in a score, 2^-17 of the
+operand, 2^-22 for each of the 24 sums of a chunk's share that the tensor cores cut off, 2^-24 per chunk added to a state,
+over fewer than 100).
 """
 import math
 
@@ -15,7 +16,7 @@ from exact_attention_blackwell_tma_gb300 import binding
 
 gpu = pytest.mark.gpu
 
-U, F = 2.0 ** -8, 2.0 ** -15
+U, F, CHUNK = 2.0 ** -8, 2.0 ** -15, 128
 
 
 def definition(q, k, v, l, S0, scale):
@@ -42,15 +43,14 @@ def bounds(a, b, c, l, X0, e):
     """Error bounds of sum_(j<=i) D^(i-j) <a_i, b_j> c_j + D^(i+1-e) a_i X of one state head, [m][n, width] lists over
     its members (a: one per output, or one; b and c: one pair, or one per query head), and of the final state."""
     n, X = a[0].shape[0], X0
-    absX, absY = X0.abs(), torch.zeros_like(X0)   # with the state carried in, and without
-    chunk = 128 if X0.shape == (128, 128) else 64
+    absX = X0.abs()
     outs = [torch.zeros((n, c[0].shape[1]), dtype=torch.float64, device=a[0].device) for _ in a]
 
     def power(m):
         return torch.where(m > 0, torch.exp(l * m.clamp(min=1)), 1.0)
 
     # chunks are counted from the sequence's first token: a walk from its last (e = 1) meets the short one first
-    starts = [0, *range((n - 1) % chunk + 1 if e else chunk, n, chunk)] if n else []
+    starts = [0, *range((n - 1) % CHUNK + 1 if e else CHUNK, n, CHUNK)] if n else []
     for s, t in zip(starts, [*starts[1:], n]):
         i = torch.arange(t - s, device=a[0].device, dtype=torch.float64)
         gap = i[:, None] - i[None, :]
@@ -58,7 +58,7 @@ def bounds(a, b, c, l, X0, e):
         into = power(i + 1 - e)[:, None]
         for m, x in enumerate(a):
             x = x[s:t]
-            bound = into * (U * (x.abs() @ X.abs()) + U * (1 + U) * (x.abs() @ absY) + F * (x.abs() @ absX))
+            bound = into * (U * (x.abs() @ X.abs()) + F * (x.abs() @ absX))
             for y, z in zip(b, c):
                 y, z = y[s:t], z[s:t]
                 bound = bound + U * ((x @ y.T * D).abs() @ z.abs()) + F * ((x.abs() @ y.abs().T * D) @ z.abs())
@@ -66,8 +66,7 @@ def bounds(a, b, c, l, X0, e):
         w = power(t - s - 1 - i + e)[:, None]
         over = power(torch.tensor(float(t - s), dtype=torch.float64, device=a[0].device))
         X = over * X + sum((w * y[s:t]).T @ z[s:t] for y, z in zip(b, c))
-        new = sum((w * y[s:t]).abs().T @ z[s:t].abs() for y, z in zip(b, c))
-        absX, absY = over * absX + new, over * absY + new
+        absX = over * absX + sum((w * y[s:t]).abs().T @ z[s:t].abs() for y, z in zip(b, c))
     return outs, F * absX
 
 
