@@ -71,6 +71,14 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// 32 bytes from memory. A row per lane by 16 bytes fetched each sector twice (shared memory leaves L1 little room), which
+// held up the SM's other loads and barriers for 15 000 cycles wherever a segment began.
+__device__ __forceinline__ void load32(const float* src, float* v) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(src)
+                 : "memory");
+}
 // A box of shared memory to the tensor of the map, tracked by this thread's bulk groups
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -637,10 +645,19 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                     for (int c = 0; c < 64; ++c) X[c] = mul * from[c * DK];
                 } else {
                     const float* from = src + (long)channel * p.DV + c0;
+                    if ((reinterpret_cast<uintptr_t>(src) & 31u) == 0) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const float4 y = *reinterpret_cast<const float4*>(from + c);
-                        X[c] = mul * y.x, X[c + 1] = mul * y.y, X[c + 2] = mul * y.z, X[c + 3] = mul * y.w;
+                        for (int c = 0; c < 64; c += 8) load32(from + c, X + c);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(from + c);
+                            X[c] = y.x, X[c + 1] = y.y, X[c + 2] = y.z, X[c + 3] = y.w;
+                        }
+                    }
+                    if (mul != 1.f) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) X[c] *= mul;
                     }
                 }
             }
