@@ -782,21 +782,26 @@ class PagedCache:
     __slots__ = ("k", "v", "k_scales", "v_scales", "n_pages", "Hkv", "d", "dv", "device", "_struct")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
-        shape, device, codes = k.shape, k.get_device(), k.dtype == torch.float8_e4m3fn
-        if (len(shape) != 4 or shape[2] != PAGED_PAGE or v.dim() != 4 or v.shape[:3] != shape[:3] or v.dtype != k.dtype
-                or not (codes or k.dtype == torch.bfloat16) or v.get_device() != device):
+        shape, v_shape, device, kind = k.shape, v.shape, k.get_device(), k.dtype
+        codes = kind == torch.float8_e4m3fn
+        if (len(shape) != 4 or len(v_shape) != 4 or shape[2] != PAGED_PAGE or v_shape[:3] != shape[:3] or v.dtype != kind
+                or not (codes or kind == torch.bfloat16) or v.get_device() != device):
             raise ValueError(f"a paged cache needs k and v [pages, heads, {PAGED_PAGE}, channels] in bf16 or float8_e4m3fn on "
-                             f"one device, got {k.dtype} {tuple(shape)} and {v.dtype} {tuple(v.shape)}")
-        scales = (k_scales, v_scales)
+                             f"one device, got {kind} {tuple(shape)} and {v.dtype} {tuple(v_shape)}")
+        contiguous = k.is_contiguous() and v.is_contiguous()
         if codes:
-            for t in scales:
-                if t is None or t.dtype != torch.uint8 or t.shape != shape[:3] or t.get_device() != device:
-                    raise ValueError(f"an 8-bit cache needs uint8 k_scales and v_scales {tuple(shape[:3])} on its device")
-        elif scales != (None, None):
+            lead = shape[:3]
+            for t in (k_scales, v_scales):
+                if t is None or t.dtype != torch.uint8 or t.shape != lead or t.get_device() != device:
+                    raise ValueError(f"an 8-bit cache needs uint8 k_scales and v_scales {tuple(lead)} on its device")
+                contiguous = contiguous and t.is_contiguous()
+        elif k_scales is not None or v_scales is not None:
             raise ValueError("a bf16 cache has no scales")
-        _check_tensors(k, v, k_scales, v_scales)
+        if device < 0 or not contiguous:
+            raise ValueError("tensors must be contiguous CUDA tensors")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.n_pages, self.Hkv, self.d, self.dv = shape[0], shape[1], shape[3], v.shape[3]
+        self.n_pages, self.Hkv, _, self.d = shape
+        self.dv = v_shape[3]
         self.device = device   # its index
         self._struct = _PagedStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scales), _ptr(v_scales), self.n_pages, self.Hkv,
                                     self.d, self.dv, 8 if codes else 16)
