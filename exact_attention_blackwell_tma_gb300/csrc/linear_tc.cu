@@ -32,7 +32,8 @@
 namespace attn {
 namespace {
 
-constexpr int kCh = 128;                 // tokens of a chunk
+constexpr int kCh = kLinChunk;           // tokens of a chunk (the tiles below are for 128)
+static_assert(kCh == 128, "tiles of 128 tokens");
 constexpr int kBox = 16384;              // 128 rows x 64 columns
 constexpr int kHalf = kBox / 2;          // 64 rows
 
