@@ -11,11 +11,17 @@
 //   S^T[key, row] = K[key, ch] q^T[ch, row],   O^T[ch, row] += V^T[ch, key] P^T[key, row],
 // which pads a handful of rows to 8 (a tcgen05 tile: to 64 or 128 on its M side, and on
 // its N side it would write S to tensor memory and read it back for every 128 keys).
-// bf16 operands come by ldmatrix. Codes: a byte seeeemmm in the upper half of a 16-bit
+// bf16 operands come by ldmatrix. K's codes are converted to f16, two at a time and exactly, NaN
+// included, and q too, by a power of two of each row's own: 8 bits keep all of themselves
+// down to 2^-31 of the row's largest, and what is lost below is under 2^-39 of it.
+// V's go to bf16, as p needs its exponents: a byte seeeemmm in the upper half of a 16-bit
 // lane, its exponent and mantissa moved down by four, is the bf16 c 2^-120, subnormal codes
-// included (the bf16 is subnormal too): a shift and two logic operations per pair, no
-// conversions, which have a fraction of the rate. K's 2^120 goes into q and the score; V's
-// is one multiplication per pair, as p 2^(e - 120) could leave the range.
+// included (the bf16 is subnormal too): a shift and two logic operations per pair, then
+// one multiplication, as p 2^(e - 120) could leave the range. The codes 7f and ff, which
+// are NaN and would count as 480 so, are looked for in every word of V, two operations for four
+// codes; a step that has some makes the channels they stand in NaN for the rows that see
+// their keys. (64 caches of 4096 to 16384, H32/8, d = 128: K by shifts as well and nothing
+// looked for 222 us, with both looked for 251, K in f16 and V looked through 212.)
 //
 // Work: paged_work.cuh. Each of four warps loads 32 of a unit's 128 tokens in steps of
 // kTok, through a ring of asynchronous copies of its own. A block of up to 8 NR rows is every warp's,
@@ -40,6 +46,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                                          uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -85,8 +97,23 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
-// codes in the upper bytes of both halves: the bf16 pair c 2^-120
+// codes in the upper bytes of both halves: the bf16 pair c 2^-120 (NaN: 480 2^-120)
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t x) { return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u); }
+// Bits 80808080 of the words' `or` tell whether a code is NaN: adding one to a byte changes its eighth bit if the seven below
+// are set. (Only whether there are any: the carry out of an ff reaches the bytes above it.)
+__device__ __forceinline__ uint32_t changed(uint32_t codes) { return codes ^ (codes + 0x01010101u); }
+// Exactly: 80 in each byte whose code is NaN, 0 in the others
+__device__ __forceinline__ uint32_t nan_codes(uint32_t codes) { return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t codes_f16(uint16_t x) {   // two codes, exactly; NaN stays
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
@@ -236,7 +263,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
             r += t.rb * kRows;
             return r < w.rows ? p.q + (long)(w.s.q0 + r / p.group) * p.q_stride + (long)(t.h * p.group + r % p.group) * D : nullptr;
         };
-        if constexpr (kCodes) {   // row r times 2^e has its largest element in [2^60, 2^61) (its own exponent per row)
+        if constexpr (kCodes) {   // row r times 2^e has its largest element in [2^14, 2^15) (its own exponent per row)
             for (int r = warp; r < kRows; r += kWarps) {
                 const __nv_bfloat16* src = q_row(r);
                 uint32_t m = 0;
@@ -246,8 +273,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, o));
-                const int top = (int)(max(m & 0xffffu, m >> 16) >> 7);   // (biased; 255: an infinity or a NaN)
-                if (lane == 0) q_exp[r] = top == 255 ? 0 : min(max(60 - (top - 127), -6), 120);
+                const int top = (int)(max(m & 0xffffu, m >> 16) >> 7);   // (biased; 255, an infinity or a NaN: as the largest number's)
+                if (lane == 0) q_exp[r] = min(max(14 - (top - 127), -113), 126);
             }
             __syncthreads();
         }
@@ -258,15 +285,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
             if (src) {
                 if constexpr (kCodes) {
                     // channels 64 G + 16 t4 + 8 (kk % 2) .. + 7; word i of a code row's piece serves k step i:
-                    // its bytes (0, 2) and (1, 3) are the two pairs of a step
+                    // its bytes (0, 1) and (2, 3) are the two pairs of a step
                     const uint4 v = *reinterpret_cast<const uint4*>(src + (kk >> 1) * 64 + 16 * t4 + 8 * (kk & 1));
                     const float e = pow2(q_exp[r]);
                     auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
                     auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
-                    f[0] = pack_bf16x2(lo(v.x) * e, lo(v.y) * e);
-                    f[1] = pack_bf16x2(hi(v.x) * e, hi(v.y) * e);
-                    f[2] = pack_bf16x2(lo(v.z) * e, lo(v.w) * e);
-                    f[3] = pack_bf16x2(hi(v.z) * e, hi(v.w) * e);
+                    f[0] = pack_f16x2(lo(v.x) * e, hi(v.x) * e);
+                    f[1] = pack_f16x2(lo(v.y) * e, hi(v.y) * e);
+                    f[2] = pack_f16x2(lo(v.z) * e, hi(v.z) * e);
+                    f[3] = pack_f16x2(lo(v.w) * e, hi(v.w) * e);
                 } else {
                     const uint32_t* x = reinterpret_cast<const uint32_t*>(src + kk * 32) + t4;
                     f[0] = x[0], f[1] = x[4], f[2] = x[8], f[3] = x[12];
@@ -278,7 +305,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
         for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                qscale[n][c] = kCodes ? p.scale_log2 * pow2(120 - q_exp[row0 + n * 8 + 2 * t4 + c]) : p.scale_log2;
+                qscale[n][c] = kCodes ? p.scale_log2 * pow2(-q_exp[row0 + n * 8 + 2 * t4 + c]) : p.scale_log2;
                 m_run[n][c] = -INFINITY;
                 mu[n][c] = l_run[n][c] = 0.f;
             }
@@ -323,12 +350,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t a0 = codes_bf16(wa[i] << 8), a1 = codes_bf16(wb[i] << 8), a2 = codes_bf16(wa[i]),
-                                           a3 = codes_bf16(wb[i]);
+                            const uint32_t a0 = codes_f16((uint16_t)wa[i]), a1 = codes_f16((uint16_t)wb[i]),
+                                           a2 = codes_f16((uint16_t)(wa[i] >> 16)), a3 = codes_f16((uint16_t)(wb[i] >> 16));
 #pragma unroll
                             for (int n = 0; n < NR; ++n) {
                                 const uint4 q = i < 2 ? q0[n] : q1[n];
-                                mma_bf16(sc[ck][n], a0, a1, a2, a3, (i & 1) ? q.z : q.x, (i & 1) ? q.w : q.y);
+                                mma_f16(sc[ck][n], a0, a1, a2, a3, (i & 1) ? q.z : q.x, (i & 1) ? q.w : q.y);
                             }
                         }
                     }
@@ -441,6 +468,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                 }
             // ---------------------------------------- values
             const uint32_t sv = st + Lay::kVOff;
+            uint32_t nans = 0;
 #pragma unroll
             for (int ck = 0; ck < CK; ++ck) {
                 if constexpr (kCodes) {
@@ -450,6 +478,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         uint32_t wv[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) wv[y] = lds32(row_piece<Lay::kVRow, kTok>(sv, ck * 16 + t4 + 4 * y, piece) + at);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) nans |= changed(wv[y]);
                         uint32_t f[4][2];   // channel c: tokens (t, t + 4), (t + 8, t + 12)
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
@@ -478,6 +508,50 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         if constexpr (!kWhole) a = make_uint4(a.x & in[0], a.y & in[0], a.z & in[1], a.w & in[1]);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) mma_bf16(acc[j][n], a.x, a.y, a.z, a.w, b0[ck][n], b1[ck][n]);
+                    }
+                }
+            }
+            if constexpr (kCodes) {
+                if (__any_sync(kFullMask, (nans & 0x80808080u) != 0)) {
+                    // the same products, of 1 for a NaN code with 1 for a row that sees the key (with p the rows that do not
+                    // would get 0 times NaN)
+#pragma unroll 1
+                    for (int ck = 0; ck < CK; ++ck) {
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int2 k = row_keys[row0 + n * 8 + 2 * t4 + (y & 1)];
+                                const int j = key0 + ck * 16 + tok0 + 8 * (y >> 1);
+                                x[y] = kWhole || (j < k.y && (j >= k.x || j < p.sinks)) ? 0x3f80u : 0u;
+                            }
+                            b0[0][n] = transpose8x8(x[0] | x[1] << 16);
+                            b1[0][n] = transpose8x8(x[2] | x[3] << 16);
+                        }
+#pragma unroll
+                        for (int x = 0; x < DV / 32; ++x) {
+                            const int piece = 2 * x + (g8 >> 2), at = (g8 & 3) * 4;
+                            uint32_t wv[4], f[4][2];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                wv[y] = nan_codes(lds32(row_piece<Lay::kVRow, kTok>(sv, ck * 16 + t4 + 4 * y, piece) + at));
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)   // (1 in bf16 for a NaN code)
+                                    f[c][y] = (__byte_perm(wv[2 * y], wv[2 * y + 1], (4 + c) << 12 | c << 4) >> 15 & 0x00010001u) * 0x3f80u;
+#pragma unroll
+                            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    float hits[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_bf16(hits, f[2 * y][0], f[2 * y + 1][0], f[2 * y][1], f[2 * y + 1][1], b0[0][n], b1[0][n]);
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z)
+                                        if (hits[z] > 0.f) acc[2 * x + y][n][z] = __uint_as_float(0x7fc00000u);
+                                }
+                        }
                     }
                 }
             }

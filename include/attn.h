@@ -464,8 +464,8 @@ int attn_paged_read(void* k, void* v, const attn_paged_cache* cache, const int* 
  * behind a sequence's last token or left of every window counts as nothing, whatever
  * it is. An infinity or NaN in a cached bf16 value also reaches rows of the call
  * that do not see it, when others of their head and sequence do (in 8 bits it
- * stays with the rows that see it). With 8 bits elements of q of 2^67 and more may
- * count as infinite. Results repeat bit for bit.
+ * stays with the rows that see it; the codes 7f and ff are NaN, as attn_paged_read
+ * has them). Results repeat bit for bit.
  */
 size_t attn_paged_fwd_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v);
 int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* cache, const int* page_table,

@@ -1,0 +1,131 @@
+"""The paged cache in bf16 and 8 bits where its contents are at the ends of their types (bounds: test_paged.py)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from exact_attention_blackwell_tma_gb300 import binding
+from _plain import SLACK, U, visible
+from test_paged import BITS, DIMS, PAGE, Pool, bf16, offsets
+
+gpu = pytest.mark.gpu
+
+
+def put_byte(pool, b, which, j, head, byte, channel=None, scale=False):
+    """A code (of every channel, or of one) or the scale of token j's row of a head."""
+    at = (int(pool.table_host[b][j // PAGE]), head, j % PAGE)
+    if scale:
+        pool.host[2 * which + 1][at] = byte
+    elif channel is None:
+        pool.host[2 * which][at] = byte
+    else:
+        pool.host[2 * which][at][channel] = byte
+
+
+def check_as_read(pool, new, H, q=None, window=(-1, -1), sinks=0, scale=None):
+    """O and LSE are those of what paged_read gives, row by row over the keys a row sees: NaN in the same places, the
+    rest within the bounds. Returns O and the mask of its NaN."""
+    T, r, at, where = sum(new), H // pool.Hkv, 0, []
+    q = bf16(pool.g, T, H, pool.d) if q is None else q
+    scale = 1 / math.sqrt(pool.d) if scale is None else scale
+    o, lse = binding.paged_forward(q.cuda(), pool.cache, pool.table, pool.lens_t, scale=scale, cu_seqlens=offsets(new).cuda(),
+                                   window=window, sinks=sinks)
+    read = binding.paged_read(pool.cache, pool.table, pool.lens_t, sum(pool.lens), cu_seqlens=offsets(pool.lens).cuda())
+    binding.check_status()
+    got, got_lse, key0 = o.double().cpu(), lse.double().cpu(), 0
+    for b, n in enumerate(new):
+        k, v = (x[key0:key0 + pool.lens[b]].double().cpu().repeat_interleave(r, 1) for x in read)
+        ok = visible(n, pool.lens[b], True, window, sinks)
+        for i in range(n):
+            ks, vs = k[ok[i]], v[ok[i]]
+            s = torch.einsum("hd,jhd->hj", q[at + i].double(), ks) * scale
+            p = torch.softmax(s, -1)
+            ref = torch.einsum("hj,jhd->hd", p, vs)
+            spread = torch.einsum("hj,jhd->hd", p, vs.abs())
+            bad = torch.isnan(ref)
+            where.append(bad)
+            assert torch.equal(torch.isnan(got[at + i]), bad), f"sequence {b} row {i}: NaN in other places"
+            over = (got[at + i] - ref).abs() - (U + SLACK) * spread - U * ref.abs() - 1e-6
+            assert over[~bad].numel() == 0 or over[~bad].max() <= 0, f"sequence {b} row {i}: {over[~bad].max():.3e} past the bound"
+            assert torch.equal(torch.isnan(got_lse[:, at + i]), torch.isnan(s).any(-1)), f"sequence {b} row {i}: LSE"
+        at += n
+        key0 += pool.lens[b]
+    return o, torch.stack(where)
+
+
+# ------------------------------------------------------------------ codes that are NaN
+
+@gpu
+@pytest.mark.parametrize("d,dv", DIMS)
+@pytest.mark.parametrize("new", [[1, 1], [3, 5], [40, 17]])
+def test_nan_codes_are_nan(d, dv, new):
+    """The codes 7f and ff, as paged_read has them: in K they make the rows that see the key, in V the channel they stand
+    in of the rows that see it. Row blocks of one token, of a warp's rows and of two warps'; pages seen whole and in part."""
+    pool = Pool(8, [330, 100], 3, d, dv, seed=40 + d + dv + new[0])
+    for b, n in enumerate(pool.lens):
+        for _ in range(20):   # V of head 0: anywhere
+            put_byte(pool, b, 1, int(pool.g.integers(n)), 0, int(pool.g.choice([127, 255])), int(pool.g.integers(dv)))
+        # K of head 1: keys that the last rows alone see; head 2 is clean
+        for j in (n - 1, n - max(1, new[b] // 2)):
+            put_byte(pool, b, 0, j, 1, int(pool.g.choice([127, 255])), int(pool.g.integers(d)))
+    pool.upload()
+    _, bad = check_as_read(pool, new, 6)
+    assert bad[:, :2].any() and not bad[:, :2].all() and bad[-1, 2:4].all() and not bad[:, 4:].any()
+    if new[0] > 1:
+        assert not bad[0, 2:4].any()
+
+
+@gpu
+@pytest.mark.parametrize("which", [0, 1])
+def test_every_place_of_a_nan_code(which):
+    """One code at a time, in every token of a tile and every channel of a head."""
+    lens = [33] * 64
+    pool = Pool(8, lens, 1, 64, seed=41)
+    for turn in range(33):
+        pool.host[2 * which] &= 0x7f
+        pool.host[2 * which][pool.host[2 * which] == 0x7f] = 0
+        for b in range(64):
+            put_byte(pool, b, which, (turn + b) % 33, 0, 127 + 128 * (b & 1), b)
+        pool.upload()
+        q = bf16(pool.g, 64, 1, 64).cuda()
+        o, _ = binding.paged_forward(q, pool.cache, pool.table, pool.lens_t, cu_seqlens=offsets([1] * 64).cuda())
+        want = torch.eye(64, dtype=torch.bool) if which else torch.ones(64, 64, dtype=torch.bool)
+        assert torch.equal(torch.isnan(o[:, 0]).cpu(), want), turn
+    binding.check_status()
+
+
+@gpu
+@pytest.mark.parametrize("window,sinks", [((50, -1), 4), ((0, -1), 0), ((200, -1), 70)])
+def test_nan_codes_and_windows(window, sinks):
+    """Between the sinks and the windows they count as nothing, within either as NaN."""
+    pool = Pool(8, [500, 129], 2, 128, seed=42)
+    for b, n in enumerate(pool.lens):
+        for j in (2, 60, 69, 75, n // 2, n - 60, n - 40, n - 2):
+            put_byte(pool, b, 1, j, 0, 127, int(pool.g.integers(128)))
+        for j in (60, 75, n // 2, n - 3):
+            put_byte(pool, b, 0, j, 1, 255, int(pool.g.integers(128)))
+    pool.upload()
+    check_as_read(pool, [9, 2], 4, window=window, sinks=sinks)
+
+
+@gpu
+def test_nan_codes_in_a_cache_of_many_blocks():
+    """Shares of several thread blocks are joined with them."""
+    pool = Pool(8, [30000, 70], 1, 128, seed=43)
+    for j in (3, 17000, 29990):
+        put_byte(pool, 0, 1, j, 0, 255, j % 128)
+    pool.upload()
+    _, bad = check_as_read(pool, [2, 1], 4)
+    assert bad[0].sum() == 4 * 3 and not bad[2].any()
+
+
+@gpu
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** 70, 2.0 ** 110])
+@pytest.mark.parametrize("bits", BITS)
+def test_query_sizes_at_the_ends(bits, size):
+    """Rows of very different size in one block; the scale undoes the size."""
+    pool = Pool(bits, [300], 1, 64, seed=47)
+    q = (bf16(pool.g, 4, 3, 64).float() * size * 2.0 ** torch.arange(-4, 8).reshape(4, 3, 1)).to(torch.bfloat16)
+    _, bad = check_as_read(pool, [4], 3, q=q, scale=2.0 ** -9 / size)
+    assert not bad.any()
