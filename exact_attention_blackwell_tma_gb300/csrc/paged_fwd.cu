@@ -3,8 +3,9 @@
 // Mathematics. s_ij = scale <q_i, k_j>, O_i = sum_j p_ij v_j with p = exp(s - LSE), in one
 // pass over the keys: a running maximum (moved when a row's grows by more than
 // 2^kPagedTau) and sum per row, in fp32, as are all accumulators. With 8 bits k_j = 2^e c_j
-// with codes c_j: the power enters the score in fp32, and that of v_j enters p
-// before p's rounding to bf16, which it does not change (bf16 has fp32's exponents).
+// with codes c_j: the power enters the score in fp32, and that of v_j the bf16 operands of the
+// product, v up to 2^7 and p beyond it, whose rounding it does not change. (All of it in p, whose
+// weights are 2^-16 and less, would take scales below 2^-102 out of bf16's normal numbers.)
 //
 // What bounds it: the cache is read once. As in the 4-bit kernel, keys (channels for PV)
 // take the M side of mma.sync m16n8k16 and the query rows the N side,
@@ -17,7 +18,7 @@
 // V's go to bf16, as p needs its exponents: a byte seeeemmm in the upper half of a 16-bit
 // lane, its exponent and mantissa moved down by four, is the bf16 c 2^-120, subnormal codes
 // included (the bf16 is subnormal too): a shift and two logic operations per pair, then
-// one multiplication, as p 2^(e - 120) could leave the range. The codes 7f and ff, which
+// one multiplication by the tokens' scales times 2^120. The codes 7f and ff, which
 // are NaN and would count as 480 so, are looked for in every word of V, two operations for four
 // codes; a step that has some makes the channels they stand in NaN for the rows that see
 // their keys. (64 caches of 4096 to 16384, H32/8, d = 128: K by shifts as well and nothing
@@ -38,8 +39,7 @@ namespace {
 constexpr int kWarps = 4, kPagedThreads = 32 * kWarps;
 constexpr float kPagedTau = 8.f;   // a row's max moves when it grows by more (log2 units)
 // p is held 2^16 times smaller than exp(s - max), so that sums of p v stay finite for any N
-// keys with N max|v| below 2^136; at the other end p times V's scale is a normal bf16 for
-// scales from 2^-102 up (and p within 2^-8 of its row's largest).
+// keys with N max|v| below 2^136; at the other end a sum holds its fp32's 2^-149, which is 2^-133 of O.
 constexpr float kPagedShift = 16.f;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -114,11 +114,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {   // bf16 pairs
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
+// V's scale is split: 2^(min(e, kInV) - 127) goes to v, the rest to p, which is 1 for rows of values below 448 2^7
+constexpr uint32_t kInV = 134;
+__device__ __forceinline__ float scale_of_p(uint32_t e) { return fmaxf(__uint_as_float(e << 23) * 0x1p-7f, 1.f); }
+// Byte t of a and of b, in the halves of a word; such a pair's scales of v times 2^120, in bf16; bits 01000100: past kInV
+__device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int t) { return __byte_perm(a, b, (4 + t) << 8 | t) & 0x00ff00ffu; }
+__device__ __forceinline__ uint32_t scales_of_v(uint32_t e) { return __vminu2(e, kInV * 0x10001u) * 128u + 120u * 128u * 0x10001u; }
+__device__ __forceinline__ uint32_t past_v(uint32_t e) { return e + (255u - kInV) * 0x10001u; }
 
 // Rows of `bytes` in shared memory, kTok tokens: panels of 128 bytes a row (and one of 64
 // behind them where they do not divide), their 16-byte pieces permuted by the token so
@@ -376,16 +383,19 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         }
                 }
             }
-            float vs[CK][2];
+            uint32_t v_scales[CK][2], past = 0;   // of tokens t4 and t4 + 4, t4 + 8 and t4 + 12
 #pragma unroll
             for (int ck = 0; ck < CK; ++ck) {
+                if constexpr (kCodes) {
+                    const uint4 e = lds128(st + Lay::kVsOff + ck * 16);
+                    const uint32_t e0 = byte_pair(e.x, e.y, t4), e1 = byte_pair(e.z, e.w, t4);
+                    v_scales[ck][0] = scales_of_v(e0), v_scales[ck][1] = scales_of_v(e1);
+                    past |= past_v(e0) | past_v(e1);
+                }
                 float ks[2] = {1.f, 1.f};
                 if constexpr (kCodes) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        ks[x] = __uint_as_float(lds8(st + Lay::kKsOff + ck * 16 + tok0 + 8 * x) << 23);
-                        vs[ck][x] = __uint_as_float(lds8(st + Lay::kVsOff + ck * 16 + tok0 + 8 * x) << 23);
-                    }
+                    for (int x = 0; x < 2; ++x) ks[x] = __uint_as_float(lds8(st + Lay::kKsOff + ck * 16 + tok0 + 8 * x) << 23);
                 }
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
@@ -408,7 +418,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         }
                     }
             }
-            bool move = force;
+            const bool some_past = kCodes && (past & 0x01000100u) != 0;
+            bool move = force || some_past, scale_p = false;
 #pragma unroll
             for (int ck = 0; ck < CK; ++ck)
 #pragma unroll
@@ -449,23 +460,34 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         for (int x = 0; x < 4; ++x) acc[j][n][x] *= al[x & 1];
                 }
                 force = __any_sync(kFullMask, unset);
+                scale_p = kCodes && __any_sync(kFullMask, some_past);   // (rows whose maximum stays have changed nothing)
             }
             uint32_t b0[CK][NR], b1[CK][NR];
+            auto weights = [&](auto scaled_tag) {
 #pragma unroll
-            for (int ck = 0; ck < CK; ++ck)
+                for (int ck = 0; ck < CK; ++ck)
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float x[4];
+                    for (int n = 0; n < NR; ++n) {
+                        float x[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float e = ex2_mufu(sc[ck][n][y]);
-                        l_run[n][y & 1] += e;
-                        x[y] = kCodes ? e * vs[ck][y >> 1] : e;
-                        if (kCodes && !kWhole && e == 0.f) x[y] = 0.f;   // (times the infinite scale of a masked key)
+                        for (int y = 0; y < 4; ++y) {
+                            const float e = ex2_mufu(sc[ck][n][y]);
+                            l_run[n][y & 1] += e;
+                            x[y] = e;
+                            if constexpr (decltype(scaled_tag)::value) {   // (0 for a masked key, whose scale may be infinite)
+                                const float f = scale_of_p(lds8(st + Lay::kVsOff + ck * 16 + tok0 + 8 * (y >> 1)));
+                                if (kWhole || e != 0.f) x[y] = e * f;
+                            }
+                        }
+                        b0[ck][n] = transpose8x8(pack_bf16x2(x[0], x[1]));
+                        b1[ck][n] = transpose8x8(pack_bf16x2(x[2], x[3]));
                     }
-                    b0[ck][n] = transpose8x8(pack_bf16x2(x[0], x[1]));
-                    b1[ck][n] = transpose8x8(pack_bf16x2(x[2], x[3]));
-                }
+            };
+            if (scale_p) {
+                if constexpr (kCodes) weights(std::true_type{});
+            } else {
+                weights(std::false_type{});
+            }
             // ---------------------------------------- values
             const uint32_t sv = st + Lay::kVOff;
             uint32_t nans = 0;
@@ -485,7 +507,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int y = 0; y < 2; ++y)
-                                f[c][y] = times_2_120(codes_bf16(__byte_perm(wv[2 * y], wv[2 * y + 1], (4 + c) << 12 | c << 4)));
+                                f[c][y] = times(codes_bf16(__byte_perm(wv[2 * y], wv[2 * y + 1], (4 + c) << 12 | c << 4)), v_scales[ck][y]);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) {
                             mma_bf16(acc[2 * x][n], f[0][0], f[1][0], f[0][1], f[1][1], b0[ck][n], b1[ck][n]);

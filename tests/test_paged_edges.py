@@ -129,3 +129,28 @@ def test_query_sizes_at_the_ends(bits, size):
     q = (bf16(pool.g, 4, 3, 64).float() * size * 2.0 ** torch.arange(-4, 8).reshape(4, 3, 1)).to(torch.bfloat16)
     _, bad = check_as_read(pool, [4], 3, q=q, scale=2.0 ** -9 / size)
     assert not bad.any()
+
+
+# ------------------------------------------------------------------ small values
+
+@gpu
+@pytest.mark.parametrize("e", [1, 4, 8, 16, 25, 40, 60])
+@pytest.mark.parametrize("d,N", [(64, 100), (128, 700), (256, 100)])
+def test_small_value_scales(e, d, N):
+    """V's scales from the least one (2^-126) up: O to its own rounding and P's, as for any other size. What is added is half
+    a step of the smallest bf16 (2^-134) for a value's and for O's rounding each, and for the sums, whose weights are 2^-16
+    and more and which cannot hold less than 2^-149: 2^-150 / 2^-16 for each of a row's N products."""
+    pool = Pool(8, [N], 1, d, seed=46 + e)
+    pool.host[3] = torch.tensor(pool.g.integers(e, e + 8, pool.host[3].shape).astype(np.uint8))
+    pool.upload()
+    q = bf16(pool.g, 2, 4, d)
+    o, _ = binding.paged_forward(q.cuda(), pool.cache, pool.table, pool.lens_t, cu_seqlens=offsets([2]).cuda())
+    binding.check_status()
+    k, v = (pool.values(0, which).repeat_interleave(4, 1) for which in (0, 1))
+    s = torch.einsum("ihd,jhd->hij", q.double(), k) / math.sqrt(d)
+    p = torch.softmax(s.masked_fill(~visible(2, N, True, (-1, -1), 0), -math.inf), -1)
+    ref, spread = torch.einsum("hij,jhd->ihd", p, v), torch.einsum("hij,jhd->ihd", p, v.abs())
+    bound = (U + SLACK) * spread + U * ref.abs() + 2.0 ** -133 + N * 2.0 ** -134
+    size = v.abs().max()
+    over = ((o.double().cpu() - ref).abs() - bound) / size
+    assert torch.isfinite(o).all() and over.max() <= 0, f"{over.max():.3e} of the largest value past the bound"
