@@ -132,7 +132,7 @@ __device__ __forceinline__ void read_token(__nv_bfloat16* k, __nv_bfloat16* v, c
             const int p = p0 + 32 * y;
             if (p >= all) break;
             if constexpr (kCodes) {
-                const float f = __uint_as_float(e[y] << 23);   // (255: infinity, times codes of 0: NaN)
+                const float f = paged_scale(e[y]);
                 const uint32_t w[2] = {x[y].x, x[y].y};
                 uint32_t o[4];
 #pragma unroll

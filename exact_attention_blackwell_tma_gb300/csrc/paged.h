@@ -2,8 +2,8 @@
 //
 // Pages of 64 tokens, [pages][Hkv][64][channels] for K (d) and V (dv), in bf16 or in
 // e4m3. With e4m3, bytes e [pages][Hkv][64] give each token and head a scale of
-// 2^(e - 127) for its codes, e from 1 up (255: the row held an infinity or a NaN,
-// its codes are 0). A power of two costs a code that has an exponent of its own
+// 2^(e - 127) for its codes, e from 1 up (255: the row held an infinity or a NaN and is
+// NaN throughout, whatever its codes are; an append makes them 0). A power of two costs a code that has an exponent of its own
 // nothing, and makes quantising exact up to the one rounding of the code.
 // Batches (tables, lengths, rows) are those of the 4-bit cache.
 #pragma once
@@ -39,6 +39,10 @@ struct PagedFwdParams {
 // Tiles of 8 (query, head-of-the-group) rows that a CTA holds at once: four when an average sequence has more than 8 rows
 // (32 sequences, group 4, 1 to 16 tokens, bf16, d = 128: 188 us in blocks of two tiles, 143 of four).
 inline int paged_row_tiles(int group, int B, int total) { return kv4_row_tiles(group, B, total) == 1 ? 1 : 4; }
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float paged_scale(uint32_t e) { return __uint_as_float(e == 255 ? 0x7fc00000u : e << 23); }
+#endif
 
 cudaError_t launch_paged_append(const PagedCache& c, bool codes, const Kv4Batch& s, const __nv_bfloat16* k,
                                 const __nv_bfloat16* v, long k_stride, long v_stride, int* status, int num_sms,

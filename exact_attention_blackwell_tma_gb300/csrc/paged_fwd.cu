@@ -121,7 +121,7 @@ __device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {   // bf16 pa
 }
 // V's scale is split: 2^(min(e, kInV) - 127) goes to v, the rest to p, which is 1 for rows of values below 448 2^7
 constexpr uint32_t kInV = 134;
-__device__ __forceinline__ float scale_of_p(uint32_t e) { return fmaxf(__uint_as_float(e << 23) * 0x1p-7f, 1.f); }
+__device__ __forceinline__ float scale_of_p(uint32_t e) { return e == 255 ? NAN : fmaxf(__uint_as_float(e << 23) * 0x1p-7f, 1.f); }
 // Byte t of a and of b, in the halves of a word; such a pair's scales of v times 2^120, in bf16; bits 01000100: past kInV
 __device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int t) { return __byte_perm(a, b, (4 + t) << 8 | t) & 0x00ff00ffu; }
 __device__ __forceinline__ uint32_t scales_of_v(uint32_t e) { return __vminu2(e, kInV * 0x10001u) * 128u + 120u * 128u * 0x10001u; }
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                 float ks[2] = {1.f, 1.f};
                 if constexpr (kCodes) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) ks[x] = __uint_as_float(lds8(st + Lay::kKsOff + ck * 16 + tok0 + 8 * x) << 23);
+                    for (int x = 0; x < 2; ++x) ks[x] = paged_scale(lds8(st + Lay::kKsOff + ck * 16 + tok0 + 8 * x));
                 }
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                             const float e = ex2_mufu(sc[ck][n][y]);
                             l_run[n][y & 1] += e;
                             x[y] = e;
-                            if constexpr (decltype(scaled_tag)::value) {   // (0 for a masked key, whose scale may be infinite)
+                            if constexpr (decltype(scaled_tag)::value) {   // (0 for a masked key, whose scale may be NaN)
                                 const float f = scale_of_p(lds8(st + Lay::kVsOff + ck * 16 + tok0 + 8 * (y >> 1)));
                                 if (kWhole || e != 0.f) x[y] = e * f;
                             }

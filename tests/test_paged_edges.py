@@ -154,3 +154,22 @@ def test_small_value_scales(e, d, N):
     size = v.abs().max()
     over = ((o.double().cpu() - ref).abs() - bound) / size
     assert torch.isfinite(o).all() and over.max() <= 0, f"{over.max():.3e} of the largest value past the bound"
+
+
+# ------------------------------------------------------------------ rows marked as NaN
+
+@gpu
+@pytest.mark.parametrize("d,dv", DIMS)
+def test_rows_marked_nan_hold_any_codes(d, dv):
+    """A scale of 255 makes a row NaN, whatever its codes are: read back, as keys and as values."""
+    pool = Pool(8, [200, 70], 2, d, dv, seed=45)
+    for b, n in enumerate(pool.lens):
+        for j in (0, n - 1):   # (their codes stay as they are: neither 0 nor NaN)
+            put_byte(pool, b, 1, j, 0, 255, scale=True)
+        put_byte(pool, b, 0, n - 2, 1, 255, scale=True)
+    pool.upload()
+    k, v = binding.paged_read(pool.cache, pool.table, pool.lens_t, 270, cu_seqlens=offsets([200, 70]).cuda())
+    assert torch.isnan(v[[0, 199, 200, 269], 0]).all() and torch.isnan(k[[198, 268], 1]).all()
+    assert torch.isnan(v).sum() == 4 * dv and torch.isnan(k).sum() == 2 * d
+    _, bad = check_as_read(pool, [4, 3], 4)
+    assert bad[:, :2].all() and not bad[0, 2:].any() and bad[3, 2:].all()
