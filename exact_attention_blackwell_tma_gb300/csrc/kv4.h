@@ -41,6 +41,7 @@ struct Kv4Batch {
 };
 
 struct Kv4FwdParams {
+    static constexpr bool kKeepsNan = false;   // paged_work.cuh
     Kv4Cache c;
     Kv4Batch s;
     const __nv_bfloat16* q;

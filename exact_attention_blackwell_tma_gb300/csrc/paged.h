@@ -21,6 +21,7 @@ struct PagedCache {
 };
 
 struct PagedFwdParams {
+    static constexpr bool kKeepsNan = true;   // paged_work.cuh
     PagedCache c;
     Kv4Batch s;
     const __nv_bfloat16* q;

@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
                             x[y] = e;
                             if constexpr (decltype(scaled_tag)::value) {   // (0 for a masked key, whose scale may be NaN)
                                 const float f = scale_of_p(lds8(st + Lay::kVsOff + ck * 16 + tok0 + 8 * (y >> 1)));
-                                if (kWhole || e != 0.f) x[y] = e * f;
+                                if (kWhole || sc[ck][n][y] != -INFINITY) x[y] = e * f;
                             }
                         }
                         b0[ck][n] = transpose8x8(pack_bf16x2(x[0], x[1]));
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<kCodes, D, DV, NR>:
             for (int y = 0; y < kWarps; ++y) {   // in warp order: the same sum on every run
                 const float f = v[y].x == -INFINITY ? 0.f : ex2_mufu(v[y].x - m);
                 l += v[y].y * f;
-                if (f != 0.f) {
+                if (v[y].x != -INFINITY) {   // (a factor of 0 leaves a NaN)
                     const float4 z = *reinterpret_cast<const float4*>(smem + y * S * Lay::kSlot + (at * DV + 4 * c4) * 4);
                     o.x = fmaf(f, z.x, o.x);
                     o.y = fmaf(f, z.y, o.y);

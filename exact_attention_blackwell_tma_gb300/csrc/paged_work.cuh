@@ -2,7 +2,8 @@
 // (sequence, key/value head, row block, two pages) units, its cut into ranges for
 // the CTAs, and the joining of row blocks that several CTAs had a share of. P: the
 // kernel's parameters, with the fields s (Kv4Batch), c.Hkv, c.dv, H, group,
-// win_left, win_right, sinks, prefix, part_ml, part_o, o, lse, status.
+// win_left, win_right, sinks, prefix, part_ml, part_o, o, lse, status, and kKeepsNan:
+// shares whose weight is nothing in fp32 are multiplied by 0 (NaN stays) instead of left out.
 #pragma once
 
 #include "kv4.h"
@@ -200,20 +201,23 @@ __device__ __forceinline__ void finish_row(const P& p, long row, int rows_per_bl
     float4 o[2] = {};
     for (int c = s.c0; c <= s.c1; c += 4) {   // four shares' loads in flight
         float f[4];
+        bool live[4];
         float4 y[4][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const bool in = c + k <= s.c1;
             const long at = s.at(in ? c + k : s.c1);
             const float mk = p.part_ml[2 * at];
-            f[k] = !in || mk == -INFINITY ? 0.f : ex2_mufu(mk - ml.x);
+            live[k] = in && mk != -INFINITY;
+            f[k] = live[k] ? ex2_mufu(mk - ml.x) : 0.f;
+            if (!P::kKeepsNan) live[k] = f[k] != 0.f;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (x * 128 + lane * 4 < dv) y[k][x] = *reinterpret_cast<const float4*>(p.part_o + at * dv + x * 128 + lane * 4);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (f[k] != 0.f)
+            if (live[k])
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     o[x].x = fmaf(f[k], y[k][x].x, o[x].x);

@@ -173,3 +173,43 @@ def test_rows_marked_nan_hold_any_codes(d, dv):
     assert torch.isnan(v).sum() == 4 * dv and torch.isnan(k).sum() == 2 * d
     _, bad = check_as_read(pool, [4, 3], 4)
     assert bad[:, :2].all() and not bad[0, 2:].any() and bad[3, 2:].all()
+
+
+# ------------------------------------------------------------------ keys whose weight is nothing in fp32
+
+@gpu
+@pytest.mark.parametrize("bits,how", [(16, "value"), (8, "code"), (8, "scale")])
+@pytest.mark.parametrize("N,new,window,light,j", [
+    (9000, 1, -1, (0, 4500), 5), (9000, 1, -1, (0, 4500), 4400), (128, 1, -1, (64, 128), 70), (128, 20, -1, (0, 64), 33),
+    (9000, 6, 4000, (4990, 8000), 4998), (9000, 6, 4000, (4990, 8000), 6000)])
+def test_nan_of_a_key_without_weight(bits, how, N, new, window, light, j):
+    """The NaN value of a key whose weight is below 2^-149 reaches the rows that see it, whichever warp or thread block
+    the key falls to: 0 times NaN, wherever the sum over the keys is cut."""
+    pool = Pool(bits, [N], 1, 64, seed=44)
+    tokens = np.arange(N)
+    page, slot = pool.table_host[0][tokens // PAGE].astype(np.int64), tokens % PAGE
+    few = torch.tensor((tokens >= light[0]) & (tokens < light[1]))[:, None]
+    # the light keys score 256 less than the others (b8 is the code of -1)
+    pool.host[0][page, 0, slot] = torch.where(few, -32.0, 0.0).to(torch.bfloat16) if bits == 16 else few.to(torch.uint8) * 0xb8
+    if bits == 8:
+        pool.host[1][:] = 127 + 5
+    if how == "value":
+        pool.host[2][int(page[j]), 0, j % PAGE, 9] = math.nan
+    elif how == "code":
+        put_byte(pool, 0, 1, j, 0, 127, 9)
+    else:
+        put_byte(pool, 0, 1, j, 0, 0)
+        put_byte(pool, 0, 1, j, 0, 255, scale=True)
+    pool.upload()
+    q = torch.ones(new, 2, 64, dtype=torch.bfloat16)
+    o, lse = binding.paged_forward(q.cuda(), pool.cache, pool.table, pool.lens_t, scale=1 / 8, cu_seqlens=offsets([new]).cuda(),
+                                   window=(window, -1))
+    binding.check_status()
+    sees = visible(new, N, True, (window, -1), 0)[:, j].cuda()
+    assert torch.isnan(o[sees][..., 9]).all() and torch.isfinite(lse).all()
+    if bits == 8:   # (a NaN in bf16 reaches the rows beside them, too)
+        assert torch.isfinite(o[~sees]).all()
+    if how == "scale":
+        assert torch.isnan(o[sees]).all()
+    elif bits == 8:
+        assert torch.isfinite(o[..., :9]).all() and torch.isfinite(o[..., 10:]).all()
