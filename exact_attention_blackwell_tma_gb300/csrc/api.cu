@@ -885,7 +885,6 @@ int linear_common(int B, int H, int Hkv, int L, const int* cu, int d, int dv, in
     p->per = H / Hkv;
     p->ranges = plan.ranges;
     p->whole = plan.whole;
-    p->init_mul = p->final_mul = 1.f;
     p->status = di.status;
     p->wait_budget_ns = wait_budget_ns();
     if (p->total > 0)
@@ -939,7 +938,7 @@ extern "C" int attn_linear_fwd(const void* q, const void* k, const void* v, long
     const LinMaps maps = linear_roles(&p, tq, tk, tv, to);
     p.init = state;
     p.final = final_state;
-    p.out_mul = scale;
+    p.scale = scale;
     cudaError_t e = launch_linear_states(p, maps, false, stream);
     if (e == cudaSuccess) e = launch_linear_out(p, maps, false, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "linear forward launch failed: %s", cudaGetErrorString(e));
@@ -970,7 +969,7 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
     if ((rc = linear_common(B, H, Hkv, L, cu_seqlens, d, d_v, linear_bwd_tiles(d, d_v), log_decay, dstate != nullptr, workspace,
                             ws_bytes, all, 7, &p)))
         return rc;
-    p.out_mul = scale;
+    p.scale = scale;
     cudaError_t e = cudaSuccess;
     if (rows) {   // dq, forwards
         const LinMaps maps = linear_roles(&p, tdo, tv, tk, tdq);
@@ -982,10 +981,8 @@ extern "C" int attn_linear_bwd(const void* q, const void* k, const void* v, cons
     // dv and the gradient of the first state, and dk, backwards: its states are those of dv, transposed
     // (dstate, which may be dfinal's buffer, is written where the states are made: nothing reads dfinal behind)
     p.init = dfinal;
-    p.init_mul = 1.f / scale;
     p.init_trans = 0;
     p.final = dstate;
-    p.final_mul = scale;
     const LinMaps maps = linear_roles(&p, tk, tq, tdo, tdv);
     if (e == cudaSuccess) e = launch_linear_states(p, maps, true, stream);
     if (rows && e == cudaSuccess) e = launch_linear_out(p, maps, true, stream);

@@ -60,7 +60,6 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinParams 
         first = (int)min(unit0 / each, (long)p.ranges - 1);
         last = chunks > 0 ? (int)min((unit0 + chunks - 1) / each, (long)p.ranges - 1) : first;
     }
-    X = make_float4(p.init_mul * X.x, p.init_mul * X.y, p.init_mul * X.z, p.init_mul * X.w);
     const float4 start = X;
     // rows of the run in range i (all of them, if it is not cut)
     auto rows_in = [&](int i) {
@@ -91,8 +90,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const LinParams 
         float4* at = slots + ((long)p.cut_slots() + run) * (size / 4);
         if (n > 0) move(decay_pow(l2, rows_in(kBack ? first : last)), *at);
         *at = start;
-        *reinterpret_cast<float4*>(p.final + (long)run * size + x) =
-            make_float4(X.x * p.final_mul, X.y * p.final_mul, X.z * p.final_mul, X.w * p.final_mul);
+        *reinterpret_cast<float4*>(p.final + (long)run * size + x) = X;
     }
 }
 

@@ -3,13 +3,14 @@
 // One form serves the forward and the three gradients. With the tokens of a sequence
 // taken in order (o, dq) or from the last to the first (dk, dv: `back`), token i's
 // position r, and D the decay,
-//   out_i = out_mul (sum_{j at or before i} D^|r_i - r_j| <a_i, b_j> c_j + D^(r_i + 1 - back) a_i^T X)
-//   X'    = D^n X + sum_j D^(n - 1 - r_j + back) b_j c_j^T
-// where X is the state carried in (times init_mul) and X' the one carried out:
-//   o   a = q,  b = k,  c = v,  X = S_0                    X' = S_n
+//   out_i = scale sum_{j at or before i} D^|r_i - r_j| <a_i, b_j> c_j + x D^(r_i + 1 - back) a_i^T X
+//   X'    = D^n X + y sum_j D^(n - 1 - r_j + back) b_j c_j^T
+// where X is the state carried in and X' the one carried out, x = scale and y = 1 forwards, x = 1 and y = scale
+// backwards (dS arrives at its own size: divided by a small scale it might leave the range):
+//   o   a = q,  b = k,  c = v,  X = S_0          X' = S_n
 //   dq  a = dO, b = v,  c = k,  X = S_0^T
-//   dk  a = v,  b = dO, c = q,  X = dS_n^T / scale
-//   dv  a = k,  b = q,  c = dO, X = dS_n / scale           X' = dS_0 / scale
+//   dk  a = v,  b = dO, c = q,  X = dS_n^T
+//   dv  a = k,  b = q,  c = dO, X = dS_n         X' = dS_0
 // (dS is the gradient of the state behind a token; that of the state in front of
 // it has one more factor of D, hence `back` in the exponents.) Grouped heads: `per`
 // query heads share a state. o and dq have an output for each (a differs), dk and
@@ -40,7 +41,7 @@ struct LinParams {
     int Hkv, per, DK, DV;
     int ranges, whole;
     int init_trans, states_trans;        // (states_trans: [..][DV][DK], the states of the transposed product)
-    float out_mul, init_mul, final_mul;
+    float scale;
     int* status;
     uint64_t wait_budget_ns;
     // whether there are states to make

@@ -633,7 +633,6 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 // forwards it starts behind the range before's last segment, backwards in front of the one after's first
                 const int slot = lin_start_slot(p, at.t, range, kBack);
                 const bool trans = slot >= 0 ? p.states_trans : p.init_trans;
-                const float mul = slot >= 0 ? 1.f : p.init_mul;
                 const long size = (long)DK * p.DV;
                 const float* src = slot >= 0 ? p.states + slot * size : p.init ? p.init + at.t.run * size : nullptr;
                 const int c0 = tile * DT + col0;
@@ -643,7 +642,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 } else if (trans) {
                     const float* from = src + (long)c0 * DK + channel;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) X[c] = mul * from[c * DK];
+                    for (int c = 0; c < 64; ++c) X[c] = from[c * DK];
                 } else {
                     const float* from = src + (long)channel * p.DV + c0;
                     if ((reinterpret_cast<uintptr_t>(src) & 31u) == 0) {
@@ -655,10 +654,6 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                             const float4 y = *reinterpret_cast<const float4*>(from + c);
                             X[c] = y.x, X[c + 1] = y.y, X[c + 2] = y.z, X[c + 3] = y.w;
                         }
-                    }
-                    if (mul != 1.f) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) X[c] *= mul;
                     }
                 }
             }
@@ -677,8 +672,8 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         tmem_ld16x2(t_row + Lay::kTmO1 + c, t_row + Lay::kTmO2 + c, o1, o2);
 #pragma unroll
                         for (int z = 0; z < 8; ++z)
-                            o[z] = pack_bf16x2(fmaf(into, u2f(o2[2 * z]), p.out_mul * u2f(o1[2 * z])),
-                                               fmaf(into, u2f(o2[2 * z + 1]), p.out_mul * u2f(o1[2 * z + 1])));
+                            o[z] = pack_bf16x2(fmaf(into, u2f(o2[2 * z]), p.scale * u2f(o1[2 * z])),
+                                               fmaf(into, u2f(o2[2 * z + 1]), p.scale * u2f(o1[2 * z + 1])));
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             uint8_t* to = whole ? staged + lane * 128 + ((((c >> 3) + z) ^ (lane & 7)) << 4) : direct + 2 * c + 16 * z;
@@ -704,7 +699,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         uint32_t r[32];
                         tmem_ld32(t_row + Lay::kTmKV + mt * DT + c, r);
 #pragma unroll
-                        for (int z = 0; z < 32; ++z) X[c + z] = fmaf(X[c + z], over, u2f(r[z]));
+                        for (int z = 0; z < 32; ++z) X[c + z] = fmaf(X[c + z], over, kBack ? p.scale * u2f(r[z]) : u2f(r[z]));
                     }
                     tc_fence_before_sync();
                 }
@@ -729,7 +724,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             n = min(kCh, at.t.rows - r0);
             moves = at.x == at.per - 1;
             last = moves && at.chunk + 1 == at.chunks;
-            into = p.out_mul * (row < n ? decay_pow(l2, kBack ? n - 1 - row : row + 1) : 0.f);
+            into = (kBack ? 1.f : p.scale) * (row < n ? decay_pow(l2, kBack ? n - 1 - row : row + 1) : 0.f);
             over = decay_pow(l2, n);
             token0 = at.t.row0 + r0;
             head = kBack ? at.t.h : at.t.h * per + at.x;
@@ -970,6 +965,10 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             mbar_arrive(bar(Lay::kSFree + st));
             const int slot = lin_share_slot(p, at.t, range, kBack);
             if (!(fresh = advance()) || !tile_row<DK>(mt, row)) continue;
+            if (kBack) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) X[c] *= p.scale;
+            }
             float* dst = p.states + ((long)slot * DK + tile_channel<DK>(mt) + row) * p.DV + tile * DT + col0;
 #pragma unroll
             for (int c = 0; c < 64; c += 8)   // (the workspace is 256-byte aligned)
