@@ -820,14 +820,16 @@ extern "C" int attn_kv4_evict(const attn_kv4_cache* cache, const int* page_table
 // ---------------------------------------------------------------- linear attention
 namespace {
 
+bool linear_dims(int d, int dv) {
+    return (d == 64 || d == 128 || d == 192 || d == 256) && (dv == d || (d == 192 && dv == 128));
+}
+
 int check_linear(int B, int H, int Hkv, int L, const int* cu, int d, int dv, float scale) {
     if (B < 0 || L < 0) return fail(ATTN_ERR_ARG, "linear: bad sizes B=%d L=%d", B, L);
     int rc = check_heads(H, Hkv);
     if (rc) return rc;
-    if (d != 64 && d != 128 && d != 192 && d != 256)
-        return fail(ATTN_ERR_ARG, "head dim %d not supported (64, 128, 192, 256)", d);
-    if (dv != d && !(d == 192 && dv == 128))
-        return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (d_v = d, or d = 192 with d_v = 128)", d, dv);
+    if (!linear_dims(d, dv))
+        return fail(ATTN_ERR_ARG, "head dims d=%d, d_v=%d not supported (64, 128, 192 or 256, d_v = d, or d = 192 with d_v = 128)", d, dv);
     if (!std::isfinite(scale) || !(scale > 0.f)) return fail(ATTN_ERR_ARG, "scale must be finite and > 0");
     if (cu && (B < 1 || B > kMaxVarlenBatch)) return fail(ATTN_ERR_ARG, "varlen: B must be in [1, %d]", kMaxVarlenBatch);
     if ((cu ? (long)L : (long)B * L) >= (1L << 30)) return fail(ATTN_ERR_ARG, "too many rows");
@@ -908,7 +910,7 @@ LinMaps linear_roles(LinParams* p, const LinTensor& a, const LinTensor& b, const
 }  // namespace
 
 extern "C" size_t attn_linear_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v, int final_state) {
-    if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || d < 64 || d_v < 64) return 0;
+    if (B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || L < 0 || !linear_dims(d, d_v)) return 0;
     if ((packed ? (long)L : (long)B * L) >= (1L << 30)) return 0;
     const LinPlan fwd = lin_plan(B, Hkv, L, packed != 0, lin_tiles(d, d_v), final_state != 0);
     const LinPlan bwd = lin_plan(B, Hkv, L, packed != 0, linear_bwd_tiles(d, d_v), final_state != 0);

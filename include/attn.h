@@ -496,7 +496,8 @@ int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* ca
  * and the state before its product with q, are rounded to bf16; sums and the states that
  * leave a call are fp32 (1e-6). The rows of a chunk must be finite: an infinity or NaN in k or
  * v spreads to all rows of its chunk, not only to the later ones.
- * workspace: attn_linear_workspace_size(...) bytes (0: none needed, NULL will do; final_state != 0:
+ * workspace: attn_linear_workspace_size(...) bytes (0: none needed, NULL will do, or sizes and head dims that the
+ * calls refuse; final_state != 0:
  * the call has one, in the backward dstate), 256-byte aligned, used by one call at a time; its
  * contents need not be initialised. The calls allocate nothing, use no atomics on data (results
  * repeat bit for bit; whether a final state is asked for may change the last bit of o) and can be

@@ -1,9 +1,12 @@
 """Linear attention at the ends of what it takes, and how exact the states are that leave it (definitions: test_linear.py)."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from exact_attention_blackwell_tma_gb300 import binding
-from test_linear import U, Problem, bounds, within
+from test_linear import DIMS, U, Problem, bounds, within
 
 gpu = pytest.mark.gpu
 
@@ -51,3 +54,38 @@ def test_gradient_of_a_sequence_without_tokens():
     *_, dS = p.backward()
     assert torch.equal(dS[0], p.dstate[0]) and torch.equal(dS[2], p.dstate[2]) and not torch.equal(dS[1], p.dstate[1])
     binding.check_status()
+
+
+# ------------------------------------------------------------------ sizes of the workspace
+
+@pytest.fixture(scope="module")
+def built():
+    from exact_attention_blackwell_tma_gb300 import build
+    return build.build()
+
+
+def test_size_of_refused_head_dims(built):
+    """Head dims that the calls refuse have no size; the query returns (asked in a process of its own)."""
+    dims = [(96, 96), (9792, 9792), (64, 9792), (1 << 20, 1 << 20), (128, 64), (128, 192), (320, 320), (0, 64), (-64, -64),
+            (2 ** 31 - 1, 2 ** 31 - 1)]
+    code = ("from exact_attention_blackwell_tma_gb300 import binding as b\n"
+            f"for d, e in {dims}:\n"
+            "    print([b.attn_linear_workspace_size(1, 1, 1, 128, p, d, e, f) for p in (0, 1) for f in (0, 1)], flush=True)")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, f"ended with {run.returncode} after {run.stdout!r}"
+    assert run.stdout.split("\n")[:-1] == ["[0, 0, 0, 0]"] * len(dims)
+
+
+def test_size_of_supported_head_dims(built):
+    for d, d_v in DIMS:
+        assert binding.attn_linear_workspace_size(1, 1, 1, 128, False, d, d_v, True) == d * d_v * 4
+
+
+@gpu
+@pytest.mark.parametrize("d", [96, 9792])
+def test_tensors_of_refused_head_dims(d):
+    x, l = torch.zeros((1, 2, 1, d), dtype=torch.bfloat16, device="cuda"), torch.zeros(1, device="cuda")
+    for call in (lambda: binding.linear_forward(x, x, x, l), lambda: binding.linear_backward(x, x, x, l, x)):
+        with pytest.raises(binding.AttnError) as err:
+            call()
+        assert err.value.code == binding.ATTN_ERR_ARG
