@@ -89,3 +89,67 @@ def test_tensors_of_refused_head_dims(d):
         with pytest.raises(binding.AttnError) as err:
             call()
         assert err.value.code == binding.ATTN_ERR_ARG
+
+
+# ------------------------------------------------------------------ the states that leave a call, in fp32
+
+def state_of(k, v, l, S0):
+    """S_n of one head from its definition in float64, and the sum of the absolute values of its terms."""
+    n = k.shape[0]
+    place = torch.arange(n, device=k.device, dtype=torch.float64)
+    w = torch.exp(l * (n - 1 - place))[:, None]
+    over = torch.exp(l * n)
+    return (w * k).T @ v + over * S0, (w * k.abs()).T @ v.abs() + over * S0.abs()
+
+
+@gpu
+@pytest.mark.parametrize("d,dv", DIMS)
+@pytest.mark.parametrize("n", [2, 7, 16])
+def test_states_of_few_tokens(d, dv, n):
+    """Element by element. A product k_s v_s takes its decay as exp2 (2 units of 2^-23) of an exponent of at most 11.6, which is
+    rounded twice (2 11.6 ln 2 2^-24), and in fp32 (2^-24); its three bf16 terms hold all of it, and 16 tokens are one sum of
+    the tensor cores for each, cut off at most 2^-22 below: 2^-22 + 16.1 2^-24 + 2^-24 + 3 2^-22, below 2^-18.9 of the terms.
+    Two terms leave up to 2^-17 of a product."""
+    p = Problem([n], 2, 2, d, dv, logs=[-0.3, -0.5], states=False, seed=61 + n)
+    _, final = p.forward(final_state=True)
+    p.state, scale = torch.zeros_like(final), 1.0
+    dq, dk, dv_, dS = p.backward(scale=scale)
+    binding.check_status()
+    zero = torch.zeros_like(final[0, 0], dtype=torch.float64)
+    for h in range(2):
+        l = p.logs()[h]
+        for name, got, (ref, size) in (
+                ("S", final[0, h], state_of(p.k[:, h].double(), p.v[:, h].double(), l, zero)),
+                # dS_0 = D (q_1 dO_1^T + D q_2 dO_2^T ..): a walk from the last token on, with one more factor of D
+                ("dS", dS[0, h], [torch.exp(l) * x for x in state_of(p.q[:, h].flip(0).double(), p.do[:, h].flip(0).double(), l, zero)])):
+            within(got, ref, 2.0 ** -18.9 * size, f"{name} {h}", floor=1e-30)
+
+
+@gpu
+@pytest.mark.parametrize("d,dv,H,Hkv,lens,packed", [
+    (64, 64, 2, 2, [5000], True), (128, 128, 8, 2, [3000, 700, 2100], True), (128, 128, 4, 4, [6000, 6000], False),
+    (192, 128, 4, 1, [4000, 90], True), (256, 256, 2, 1, [2500], True), (64, 64, 12, 1, [130, 1, 900], True)])
+def test_states_of_many_tokens(d, dv, H, Hkv, lens, packed):
+    """Relative error of a state as a whole, |got - ref|_2 / |ref|_2. A chunk's share is 24 sums of the tensor cores, each cut
+    off by half a unit on average, at most 2^-24 of it: 24 2^-24 = 1.43e-6. The decay over a chunk is off by 2^-22 = 0.24e-6, and
+    the slowest head here remembers two chunks. Two bf16 terms instead of three are off by 2.4e-6 (the same in a simulation of
+    a million products)."""
+    p = Problem(lens, H, Hkv, d, dv, packed=packed, seed=71)
+    scale = 1.0
+    _, final = p.forward(final_state=True)
+    *_, dS = p.backward(scale=scale)
+    binding.check_status()
+    per, flat = H // Hkv, [x.flatten(0, -3).double() for x in (p.q, p.k, p.v, p.do)]
+    at = 0
+    for b, n in enumerate(lens):
+        q, k, v, do = (x[at:at + n] for x in flat)
+        at += n
+        for h in range(Hkv):
+            l = p.logs()[h]
+            ref, _ = state_of(k[:, h], v[:, h], l, p.state[b, h].double())
+            back = torch.exp(l * n) * p.dstate[b, h].double()
+            for x in range(h * per, (h + 1) * per):
+                back = back + torch.exp(l) * state_of(q[:, x].flip(0), do[:, x].flip(0), l, torch.zeros_like(ref))[0]
+            for name, got, want in (("S", final[b, h], ref), ("dS", dS[b, h], back)):
+                err = ((got.double() - want).norm() / want.norm()).item()
+                assert err <= 1.7e-6, f"{name} of sequence {b}, head {h}: {err:.3e}"
