@@ -84,7 +84,8 @@ cudaError_t launch_linear_step(const LinStepParams& p, cudaStream_t stream);
 #ifdef __CUDACC__
 // The kernels of a call start before the one in front of them has ended (its last CTAs, the launch and the first
 // instructions of the next overlap: 349 -> 332 us for a training step of ten kernels) and wait for it before they
-// touch global memory.
+// touch global memory. A kernel lets the next one start once it has its tensor memory: the next one's CTA, should it find
+// room on the same SM, could else take the columns first and hold them while it waits for the CTA that needs them.
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <class... P, class... A>

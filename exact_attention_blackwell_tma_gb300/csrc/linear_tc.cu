@@ -247,7 +247,6 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
         return;
     }
-    launch_next();
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
@@ -277,6 +276,7 @@ lin_out_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    launch_next();   // (see launch_early)
     wait_for_last();
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
     const int per = p.per;
@@ -775,7 +775,6 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, kStatusMisaligned);
         return;
     }
-    launch_next();
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return base + Lay::kBarOff + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kMiscOff);
@@ -802,6 +801,7 @@ lin_state_tc_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    launch_next();
     wait_for_last();
     const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
     const int nt = p.DV / DT, range = blockIdx.x / nt, tile = blockIdx.x - range * nt;
