@@ -777,7 +777,8 @@ PAGED_PAGE = 64   # tokens of a page
 
 class PagedCache:
     """A paged key/value cache: k [pages, Hkv, 64, d] and v [pages, Hkv, 64, dv] in bf16, or in float8_e4m3fn with
-    uint8 exponents k_scales and v_scales [pages, Hkv, 64] (include/attn.h, attn_paged_cache)."""
+    uint8 exponents k_scales and v_scales [pages, Hkv, 64] (include/attn.h, attn_paged_cache). A cache quantised elsewhere
+    will do: its NaN codes are NaN in paged_read and paged_forward alike."""
 
     __slots__ = ("k", "v", "k_scales", "v_scales", "n_pages", "Hkv", "d", "dv", "device", "_struct")
 

@@ -8,8 +8,8 @@
 // Sums, states and decays are fp32. Roundings to bf16, the type of the tensor cores'
 // operands: P and X before their products (like P in the exact attention: they reach outputs
 // that are bf16 themselves). The weighted b in the state's update is as good as its sum must be:
-// two bf16 terms (16 bits) on the way from chunk to chunk, where X is rounded to 8 bits next, and three (all
-// 24) in the segments' shares, which the states that leave a call are made of.
+// two bf16 terms (16 bits) on the way from chunk to chunk, where X is rounded to 8 bits next, and in the shares of a
+// call that wants no last state; three (all 24) in the shares that a state which leaves the call is made of.
 #include "linear.h"
 #include "ptx.cuh"
 

@@ -66,7 +66,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// 32 bytes to memory: a whole sector per lane (16 at a time, a chunk's outputs kept the load/store unit busy for 2000 cycles)
+// 32 bytes to memory, a whole sector per lane (the segments' shares: a row of a state per lane)
 __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])

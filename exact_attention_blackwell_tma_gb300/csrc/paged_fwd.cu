@@ -22,7 +22,7 @@
 // are NaN and would count as 480 so, are looked for in every word of V, two operations for four
 // codes; a step that has some makes the channels they stand in NaN for the rows that see
 // their keys. (64 caches of 4096 to 16384, H32/8, d = 128: K by shifts as well and nothing
-// looked for 222 us, with both looked for 251, K in f16 and V looked through 212.)
+// looked for 222 us, with both looked for 251, as it is 218.)
 //
 // Work: paged_work.cuh. Each of four warps loads 32 of a unit's 128 tokens in steps of
 // kTok, through a ring of asynchronous copies of its own. A block of up to 8 NR rows is every warp's,

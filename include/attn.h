@@ -466,7 +466,8 @@ int attn_paged_read(void* k, void* v, const attn_paged_cache* cache, const int* 
  * that do not see it, when others of their head and sequence do (in 8 bits it
  * stays with the rows that see it; the codes 7f and ff are NaN, as attn_paged_read
  * has them). Sums of values are held down to 2^-133 per 16 keys, the smallest bf16
- * number. Results repeat bit for bit.
+ * number. With 8 bits scale <q, codes of k> has to be an fp32 number, as the score itself
+ * has. Results repeat bit for bit.
  */
 size_t attn_paged_fwd_workspace_size(int B, int H, int Hkv, int L, int packed, int d, int d_v);
 int attn_paged_fwd(const void* q, long long q_stride, const attn_paged_cache* cache, const int* page_table,
